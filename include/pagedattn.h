@@ -63,6 +63,7 @@ enum pa_dtype { PA_DTYPE_F16 = 0, PA_DTYPE_BF16 = 1 };
 #define PA_DEVERR_TIMEOUT      0x10u /* a bounded wait on a copy expired */
 #define PA_DEVERR_APPEND_SLOT  0x20u /* decode_append: slot is not the last position's */
 #define PA_DEVERR_QUERY_RANGE  0x40u /* prefill: chunk < 0, > seq_len or > max_query_len */
+#define PA_DEVERR_POSITION_RANGE 0x80u /* rotation: position >= max_position */
 
 /* PAGEDATTN_VERSION of the loaded library. */
 int pa_version(void);
@@ -322,6 +323,64 @@ int pa_reshape_and_cache(const void *k_new, const void *v_new,
                          const int64_t *slot_mapping, int num_tokens,
                          int num_kv_heads, int head_dim, int block_size,
                          int num_blocks, int dtype, void *stream);
+
+/*
+ * New tokens made ready for attention in one pass: queries and keys normalised
+ * per head (optional) and rotated by their positions, and the keys and values
+ * written into their pool slots.  The pages describe the pool write alone
+ * (pa_reshape_and_cache); normalising and rotating before it are what models
+ * do between their projections and the attention.
+ *
+ * Per token and per segment x of d = head_dim / num_maps channels (a head, or
+ * each of its num_maps equal parts: differential attention keeps two keys in
+ * a head, see pa_diff_decode):
+ *     y_c = x_c * w_c / sqrt(mean_c x_c^2 + eps)    w = q_norm (k_norm); no norm if NULL
+ *     y'_a = y_a cos - y_b sin,  y'_b = y_b cos + y_a sin    for each pair (a, b)
+ * with pairs (i, i + rotary_dim/2), or (2i, 2i + 1) if interleaved is
+ * non-zero, i < rotary_dim / 2; channels past rotary_dim are not rotated.
+ * cos and sin are cos_sin[position][i] and cos_sin[position][rotary_dim/2 + i].
+ * Everything is computed in fp32 and rounded to dtype once.  Then
+ *     q_out[t] = q',  k_cache[slot / 16][h][slot % 16] = k',  v_cache[...] = v
+ * (v as raw bits).
+ *
+ *   q         [num_tokens][num_heads][head_dim]     dtype; tokens q_stride elements apart
+ *   k_new, v_new [num_tokens][num_kv_heads][head_dim] dtype; k_stride, v_stride
+ *             (so all three may be slices of one projection's output).  A stride is
+ *             a multiple of 8 and at least the row's size; with one token any is taken
+ *   q_out     [num_tokens][num_heads][head_dim], q_out_stride; may be q itself (the
+ *             same pointer and stride), no other overlap
+ *   cos_sin   [max_position][rotary_dim] fp32
+ *   positions [num_tokens] int32; slot_mapping [num_tokens] int64
+ *   q_norm, k_norm [head_dim / num_maps] dtype, or NULL
+ *   num_maps  1 or 2; rotary_dim a multiple of 16, 16..head_dim / num_maps
+ *   eps       finite, >= 0
+ * A token with a negative slot or position is padding: nothing of it is read
+ * or written, its q_out row stays as it was.  A position >= max_position sets
+ * PA_DEVERR_POSITION_RANGE, a slot >= num_blocks*16 PA_DEVERR_SLOT_RANGE; both
+ * skip the token whole.  Two tokens naming the same slot race.  The kernel is
+ * a programmatic dependent launch, as the decode's are.
+ */
+int pa_rope_and_cache(void *q_out, const void *q, const void *k_new, const void *v_new,
+                      void *k_cache, void *v_cache, const int64_t *slot_mapping,
+                      const int32_t *positions, const float *cos_sin, const void *q_norm,
+                      const void *k_norm, int num_tokens, int num_heads, int num_kv_heads,
+                      int head_dim, int num_maps, int block_size, int num_blocks,
+                      int max_position, int rotary_dim, int interleaved, float eps,
+                      int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                      int64_t q_out_stride, int dtype, void *stream);
+
+/*
+ * The same normalisation and rotation without the pool: q_out = q', k_out = k',
+ * for the entry points that append the new tokens themselves
+ * (pa_decode_append, pa_decode_shared_prefix).  k_out may be k itself, as q_out
+ * may be q.  Arguments as pa_rope_and_cache; a negative position marks padding.
+ */
+int pa_qk_norm_rope(void *q_out, void *k_out, const void *q, const void *k,
+                    const int32_t *positions, const float *cos_sin, const void *q_norm,
+                    const void *k_norm, int num_tokens, int num_heads, int num_kv_heads,
+                    int head_dim, int num_maps, int max_position, int rotary_dim,
+                    int interleaved, float eps, int64_t q_stride, int64_t k_stride,
+                    int64_t q_out_stride, int64_t k_out_stride, int dtype, void *stream);
 
 /*
  * Copy-on-write of shared blocks: for every pair i,

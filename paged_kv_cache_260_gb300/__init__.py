@@ -1,5 +1,6 @@
-"""GB300 (sm_103a) paged KV cache: decode attention, chunked prefill,
-reshape_and_cache, copy_blocks, swap_blocks.
+"""GB300 (sm_103a) paged KV cache: decode attention, chunked prefill, both
+also as differential attention, reshape_and_cache, rope_and_cache,
+copy_blocks, swap_blocks.
 
 A thin ctypes binding over ``libpagedattn.so`` (the C ABI in
 ``include/pagedattn.h``).  Functions take torch CUDA tensors, pass their data
@@ -20,8 +21,8 @@ __all__ = [
     "PagedAttnError", "load", "version", "decode", "decode_workspace_size", "workspace_for",
     "decode_noalloc", "decode_append", "decode_shared_prefix",
     "decode_shared_prefix_workspace_size", "prefill", "prefill_workspace_size",
-    "reshape_and_cache", "copy_blocks", "swap_blocks", "gather_kv", "validate_tables",
-    "selftest_bounded_wait", "get_device_error",
+    "reshape_and_cache", "rope_and_cache", "qk_norm_rope", "copy_blocks", "swap_blocks", "gather_kv",
+    "validate_tables", "selftest_bounded_wait", "get_device_error",
     "PA_DTYPE_F16", "PA_DTYPE_BF16", "DEVERR", "STATUS",
 ]
 
@@ -31,7 +32,8 @@ BLOCK_SIZE = 16
 STATUS = {0: "PA_OK", 1: "PA_ERR_INVALID_ARG", 2: "PA_ERR_UNSUPPORTED", 3: "PA_ERR_WORKSPACE",
           4: "PA_ERR_CUDA", 5: "PA_ERR_DEVICE"}
 DEVERR = {"SLOT_RANGE": 0x1, "BLOCK_RANGE": 0x2, "TABLE_RANGE": 0x4, "SEQLEN_RANGE": 0x8,
-          "TIMEOUT": 0x10, "APPEND_SLOT": 0x20, "QUERY_RANGE": 0x40}
+          "TIMEOUT": 0x10, "APPEND_SLOT": 0x20, "QUERY_RANGE": 0x40,
+          "POSITION_RANGE": 0x80}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpagedattn.so")
@@ -80,6 +82,11 @@ def load(path: str = LIB_PATH):
         L.pa_decode_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, f, i, vp]
         L.pa_reshape_and_cache.restype = i
         L.pa_reshape_and_cache.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, vp]
+        i64 = C.c_int64
+        L.pa_rope_and_cache.restype = i
+        L.pa_rope_and_cache.argtypes = [vp] * 11 + [i] * 10 + [f] + [i64] * 4 + [i, vp]
+        L.pa_qk_norm_rope.restype = i
+        L.pa_qk_norm_rope.argtypes = [vp] * 8 + [i] * 8 + [f] + [i64] * 4 + [i, vp]
         L.pa_copy_blocks.restype = i
         L.pa_copy_blocks.argtypes = [vp, vp, vp, i, i, i, i, i, i, vp]
         L.pa_swap_blocks.restype = i
@@ -337,6 +344,90 @@ def reshape_and_cache(k_new, v_new, k_cache, v_cache, slot_mapping, stream=None)
                                      _ptr(slot_mapping), nt, hkv, d, bs, nb, _dtype_code(k_cache),
                                      _stream(stream))
     _check("pa_reshape_and_cache", rc)
+
+
+def _rows(t, dtype, device):
+    """Elements between the tokens of [tokens, heads, head_dim] rows whose heads lie
+    one after the other (any distance between tokens: slices of a projection's output)."""
+    n, h, d = t.shape
+    st, sh, se = t.stride()
+    _require(t.dtype == dtype and t.get_device() == device, "rows: dtype or device")
+    _require((se == 1 or d == 1) and (sh == d or h == 1), "rows: a token's heads must be contiguous")
+    return st if n > 1 else h * d
+
+
+def _rope_args(q_out, q, k, positions, cos_sin, q_norm, k_norm, num_maps):
+    """Checks what rope_and_cache and qk_norm_rope share; (device, dtype)."""
+    torch = _torch()
+    n, hq, d = q.shape
+    dt, dev = q.dtype, q.get_device()
+    _require(dev >= 0 and dev == torch.cuda.current_device(),
+             "tensors must be on the current CUDA device")
+    _require(k.dim() == 3 and k.shape[0] == n and k.shape[2] == d and q_out.shape == q.shape,
+             "shapes")
+    _require(positions.shape == (n,) and positions.dtype == torch.int32, "positions: int32 [tokens]")
+    _require(cos_sin.dim() == 2 and cos_sin.dtype == torch.float32, "cos_sin: float32 [positions, "
+             "rotary_dim]")
+    for t in (positions, cos_sin):
+        _require(t.get_device() == dev and t.is_contiguous(),
+                 "tensors must be contiguous, on the current CUDA device")
+    for w in (q_norm, k_norm):
+        if w is not None:
+            _require(w.numel() * num_maps == d and w.dtype == dt and w.is_contiguous() and
+                     w.get_device() == dev, "norm weights: [head_dim / num_maps] of q's dtype")
+    return dev, dt
+
+
+def rope_and_cache(q_out, q, k_new, v_new, k_cache, v_cache, slot_mapping, positions, cos_sin,
+                   q_norm=None, k_norm=None, eps=1e-6, interleaved=False, num_maps=1, stream=None):
+    """pa_rope_and_cache: q and k normalised per head (with q_norm, k_norm) and rotated
+    by their positions; q goes to q_out, k and v into pool slot slot_mapping[i].
+
+    q, q_out [tokens, heads, head_dim]; k_new, v_new [tokens, kv_heads, head_dim];
+    tokens may lie any distance apart (slices of one projection's output), and
+    q_out may be q.  slot_mapping int64 and positions int32 [tokens], negative for
+    padding; cos_sin float32 [max_position, rotary_dim], each row the cosines, then
+    the sines, of its position's rotary_dim / 2 angles, for example
+        a = torch.arange(max_position).double()[:, None] * inv_freq[None]
+        cos_sin = torch.cat([a.cos(), a.sin()], 1).float()
+    num_maps=2 treats a head as two keys of half its size (differential attention).
+    """
+    n, hq, d = q.shape
+    nb, hkv, bs, d2 = k_cache.shape
+    dev, dt = _rope_args(q_out, q, k_new, positions, cos_sin, q_norm, k_norm, num_maps)
+    _require(d2 == d and v_cache.shape == k_cache.shape and k_new.shape[1] == hkv and
+             v_new.shape == k_new.shape, "shapes")
+    _require(slot_mapping.shape == (n,) and slot_mapping.dtype == _torch().int64,
+             "slot_mapping: int64 [tokens]")
+    for t in (k_cache, v_cache, slot_mapping):
+        _require(t.get_device() == dev and t.is_contiguous(),
+                 "tensors must be contiguous, on the current CUDA device")
+    _require(k_cache.dtype == dt and v_cache.dtype == dt, "pools: q's dtype")
+    rc = load().pa_rope_and_cache(
+        _ptr(q_out), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
+        _ptr(slot_mapping), _ptr(positions), _ptr(cos_sin), _ptr(q_norm), _ptr(k_norm), n, hq, hkv,
+        d, int(num_maps), bs, nb, cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0,
+        float(eps), _rows(q, dt, dev), _rows(k_new, dt, dev), _rows(v_new, dt, dev),
+        _rows(q_out, dt, dev), _dtype_code(q), _stream(stream))
+    _check("pa_rope_and_cache", rc)
+    return q_out
+
+
+def qk_norm_rope(q_out, k_out, q, k, positions, cos_sin, q_norm=None, k_norm=None, eps=1e-6,
+                 interleaved=False, num_maps=1, stream=None):
+    """pa_qk_norm_rope: rope_and_cache's normalisation and rotation without the pool, for
+    decode_append and decode_shared_prefix, which write the new tokens themselves.
+    q_out may be q and k_out may be k."""
+    n, hq, d = q.shape
+    dev, dt = _rope_args(q_out, q, k, positions, cos_sin, q_norm, k_norm, num_maps)
+    _require(k_out.shape == k.shape, "shapes")
+    rc = load().pa_qk_norm_rope(
+        _ptr(q_out), _ptr(k_out), _ptr(q), _ptr(k), _ptr(positions), _ptr(cos_sin), _ptr(q_norm),
+        _ptr(k_norm), n, hq, k.shape[1], d, int(num_maps), cos_sin.shape[0], cos_sin.shape[1],
+        1 if interleaved else 0, float(eps), _rows(q, dt, dev), _rows(k, dt, dev),
+        _rows(q_out, dt, dev), _rows(k_out, dt, dev), _dtype_code(q), _stream(stream))
+    _check("pa_qk_norm_rope", rc)
+    return q_out, k_out
 
 
 def copy_blocks(k_cache, v_cache, block_mapping, stream=None):

@@ -11,6 +11,7 @@
 #include "pa_cache.h"
 #include "pa_internal.h"
 #include "pa_prefill_abi.h"
+#include "pa_rope.h"
 #include "pa_schedule.cuh"
 #include "pa_shared.h"
 #include "pagedattn.h"
@@ -994,6 +995,135 @@ int pa_reshape_and_cache(const void *k_new, const void *v_new, void *k_cache, vo
                                                 num_tokens, num_kv_heads, head_dim, num_blocks,
                                                 ds->err, ds->num_sms,
                                                 static_cast<cudaStream_t>(stream)));
+}
+
+// Checks and launch shared by pa_rope_and_cache (pool non-null) and
+// pa_qk_norm_rope; the caller has filled in p's pointers, strides and counts.
+static int rope_impl(RopeParams &p, bool pool, int num_heads, int head_dim, int interleaved,
+                     int dtype, void *stream)
+{
+    const int hkv = p.num_kv_heads;
+    if (num_heads <= 0 || num_heads % hkv || p.num_tokens < 0 || p.max_position <= 0 ||
+        !isfinite(p.eps) || p.eps < 0.f)
+        return PA_ERR_INVALID_ARG;
+    if (p.num_maps != 1 && p.num_maps != 2)
+        return PA_ERR_UNSUPPORTED;
+    const int seg = head_dim / p.num_maps;
+    if (p.rotary_dim <= 0 || p.rotary_dim > seg)
+        return PA_ERR_INVALID_ARG;
+    if (p.rotary_dim % 16)
+        return PA_ERR_UNSUPPORTED;
+    if (p.num_tokens == 0)
+        return PA_OK;
+    if (!p.q_out || !p.q || !p.k || !p.positions || !p.cos_sin ||
+        (pool ? !p.v || !p.k_cache || !p.v_cache || !p.slots : !p.k_out))
+        return PA_ERR_INVALID_ARG;
+    for (const void *x : {p.q, p.k, p.v, (const void *)p.q_out, (const void *)p.k_out,
+                          (const void *)p.k_cache, (const void *)p.v_cache,
+                          (const void *)p.cos_sin, p.q_norm, p.k_norm})
+        if (!aligned(x, 16))
+            return PA_ERR_INVALID_ARG;
+    if (!aligned(p.positions, 4) || !aligned(p.slots, 8))
+        return PA_ERR_INVALID_ARG;
+    if (p.num_tokens > 1) {
+        const long long qrow = (long long)num_heads * head_dim, krow = (long long)hkv * head_dim;
+        auto bad = [](long long stride, long long row) { return stride < row || stride % 8; };
+        if (bad(p.q_stride, qrow) || bad(p.q_out_stride, qrow) || bad(p.k_stride, krow) ||
+            bad(pool ? p.v_stride : p.k_out_stride, krow))
+            return PA_ERR_INVALID_ARG;
+    }
+    // an output row may replace its own input row, nothing else
+    if ((p.q_out == p.q && p.q_out_stride != p.q_stride && p.num_tokens > 1) ||
+        (p.k_out && p.k_out == p.k && p.k_out_stride != p.k_stride && p.num_tokens > 1))
+        return PA_ERR_INVALID_ARG;
+    const long long segs = (long long)(num_heads + (pool ? 2 : 1) * (long long)hkv) * p.num_maps;
+    if (segs * seg >= (1LL << 31))
+        return PA_ERR_UNSUPPORTED;
+    p.q_segs = num_heads * p.num_maps;
+    p.k_segs = hkv * p.num_maps;
+    p.v_segs = pool ? hkv * p.num_maps : 0;
+    DeviceState *ds;
+    const int rc = device_state(&ds);
+    if (rc != PA_OK)
+        return rc;
+    p.err = ds->err;
+    const RopeKernel k = rope_kernel(p, dtype == PA_DTYPE_BF16, head_dim, interleaved != 0,
+                                     ds->num_sms);
+    if (!k.fn)
+        return PA_ERR_UNSUPPORTED;
+    void *args[] = {&p};
+    return launch_dependent(k.fn, dim3((unsigned)k.blocks), dim3(k.threads), 0,
+                            static_cast<cudaStream_t>(stream), args);
+}
+
+int pa_rope_and_cache(void *q_out, const void *q, const void *k_new, const void *v_new,
+                      void *k_cache, void *v_cache, const int64_t *slot_mapping,
+                      const int32_t *positions, const float *cos_sin, const void *q_norm,
+                      const void *k_norm, int num_tokens, int num_heads, int num_kv_heads,
+                      int head_dim, int num_maps, int block_size, int num_blocks,
+                      int max_position, int rotary_dim, int interleaved, float eps,
+                      int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t q_out_stride,
+                      int dtype, void *stream)
+{
+    const int rc = check_common(num_kv_heads, head_dim, block_size, num_blocks, dtype);
+    if (rc != PA_OK)
+        return rc;
+    RopeParams p{};
+    p.q_out = q_out;
+    p.q = q;
+    p.k = k_new;
+    p.v = v_new;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.slots = slot_mapping;
+    p.positions = positions;
+    p.cos_sin = cos_sin;
+    p.q_norm = q_norm;
+    p.k_norm = k_norm;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.q_out_stride = q_out_stride;
+    p.num_slots = (long long)num_blocks * kBlockSize;
+    p.num_tokens = num_tokens;
+    p.num_kv_heads = num_kv_heads;
+    p.num_maps = num_maps;
+    p.rotary_dim = rotary_dim;
+    p.max_position = max_position;
+    p.eps = eps;
+    return rope_impl(p, true, num_heads, head_dim, interleaved, dtype, stream);
+}
+
+int pa_qk_norm_rope(void *q_out, void *k_out, const void *q, const void *k,
+                    const int32_t *positions, const float *cos_sin, const void *q_norm,
+                    const void *k_norm, int num_tokens, int num_heads, int num_kv_heads,
+                    int head_dim, int num_maps, int max_position, int rotary_dim, int interleaved,
+                    float eps, int64_t q_stride, int64_t k_stride, int64_t q_out_stride,
+                    int64_t k_out_stride, int dtype, void *stream)
+{
+    const int rc = check_common(num_kv_heads, head_dim, kBlockSize, 1, dtype);
+    if (rc != PA_OK)
+        return rc;
+    RopeParams p{};
+    p.q_out = q_out;
+    p.k_out = k_out;
+    p.q = q;
+    p.k = k;
+    p.positions = positions;
+    p.cos_sin = cos_sin;
+    p.q_norm = q_norm;
+    p.k_norm = k_norm;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.q_out_stride = q_out_stride;
+    p.k_out_stride = k_out_stride;
+    p.num_tokens = num_tokens;
+    p.num_kv_heads = num_kv_heads;
+    p.num_maps = num_maps;
+    p.rotary_dim = rotary_dim;
+    p.max_position = max_position;
+    p.eps = eps;
+    return rope_impl(p, false, num_heads, head_dim, interleaved, dtype, stream);
 }
 
 int pa_copy_blocks(void *k_cache, void *v_cache, const int64_t *block_mapping, int num_pairs,

@@ -146,6 +146,40 @@ int pa_decode(void *out, const void *q, const void *k_cache, const void *v_cache
               void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Differential attention, one query token per sequence: every head takes the
+ * difference of two softmax maps over the same values.  The pages describe no
+ * such operator; it reads the pool the plain decode reads, with two queries in
+ * a head's q row and two keys in a pool row, head_dim / 2 channels each, side
+ * by side (H = head_dim / 2):
+ *     s1_t = scale * q[:H].k_t[:H],   s2_t = scale * q[H:].k_t[H:]
+ *     y    = sum_t softmax_t(s1) v_t - lambda[h] * sum_t softmax_t(s2) v_t
+ *     out  = out_scale * y * norm_weight / sqrt(mean y^2 + norm_eps)
+ * or out = out_scale * y if norm_weight is NULL; the mean is over the head's
+ * head_dim channels.  A model's learned vectors give lambda once, when its weights
+ * are loaded.  fp32 throughout (the weights of the softmax enter the product
+ * with V as two 16-bit terms each), one rounding at the end.  A sequence of
+ * length 0 yields zeros.  Keys and values of live tokens must be finite; slots
+ * past a sequence's end may hold anything.
+ *
+ *   lambda       [num_heads] fp32
+ *   norm_weight  [head_dim] dtype, 16-byte aligned, or NULL
+ *   norm_eps     finite, >= 0; out_scale finite
+ *   scale        typically 1/sqrt(head_dim / 2)
+ *   workspace    at least pa_diff_decode_workspace_size(...) bytes, else as pa_decode
+ * Groups of 1..8 heads per kv head (PA_ERR_UNSUPPORTED beyond).  Other
+ * arguments, the split (that of partition_size 0), launches and errors as pa_decode.
+ */
+size_t pa_diff_decode_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                     int max_blocks_per_seq);
+
+int pa_diff_decode(void *out, const void *q, const void *k_cache, const void *v_cache,
+                   const int32_t *block_tables, const int32_t *seq_lens, const float *lambda,
+                   const void *norm_weight, int num_seqs, int num_heads, int num_kv_heads,
+                   int head_dim, int block_size, int max_blocks_per_seq, int num_blocks,
+                   float scale, float norm_eps, float out_scale, int dtype, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/*
  * Chunked-prefill attention over the paged pool: the newest tokens of each
  * sequence (a prompt chunk) attend causally to everything before them and to
  * one another.  Long prompts are cut into chunks that share steps with
@@ -197,6 +231,24 @@ int pa_prefill(void *out, const void *q, const void *k_cache, const void *v_cach
                int num_seqs, int max_query_len, int num_heads, int num_kv_heads, int head_dim,
                int block_size, int max_blocks_per_seq, int num_blocks, float scale, int dtype,
                void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * pa_prefill as differential attention: the formulas, lambda, norm_weight,
+ * norm_eps and out_scale of pa_diff_decode, the chunks, the causal mask, the
+ * work order and the other arguments of pa_prefill (groups up to 128 heads,
+ * scale > 0).  The softmax weights are rounded to dtype before the product
+ * with V.  Rows of out past query_start[num_seqs] are left as they were.
+ */
+size_t pa_diff_prefill_workspace_size(int num_seqs, int max_query_len, int num_heads,
+                                      int num_kv_heads);
+
+int pa_diff_prefill(void *out, const void *q, const void *k_cache, const void *v_cache,
+                    const int32_t *block_tables, const int32_t *seq_lens,
+                    const int32_t *query_start, const float *lambda, const void *norm_weight,
+                    int num_seqs, int max_query_len, int num_heads, int num_kv_heads, int head_dim,
+                    int block_size, int max_blocks_per_seq, int num_blocks, float scale,
+                    float norm_eps, float out_scale, int dtype, void *workspace,
+                    size_t workspace_bytes, void *stream);
 
 /*
  * One decode step with the new tokens appended on the way: the result equals

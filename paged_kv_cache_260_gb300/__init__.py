@@ -20,7 +20,9 @@ import threading
 __all__ = [
     "PagedAttnError", "load", "version", "decode", "decode_workspace_size", "workspace_for",
     "decode_noalloc", "decode_append", "decode_shared_prefix",
-    "decode_shared_prefix_workspace_size", "prefill", "prefill_workspace_size",
+    "decode_shared_prefix_workspace_size", "diff_decode", "diff_decode_workspace_size",
+    "diff_decode_workspace_for", "prefill", "prefill_workspace_size", "diff_prefill",
+    "diff_prefill_workspace_size", "diff_prefill_workspace_for",
     "reshape_and_cache", "rope_and_cache", "qk_norm_rope", "copy_blocks", "swap_blocks", "gather_kv",
     "validate_tables", "selftest_bounded_wait", "get_device_error",
     "PA_DTYPE_F16", "PA_DTYPE_BF16", "DEVERR", "STATUS",
@@ -100,6 +102,14 @@ def load(path: str = LIB_PATH):
                                  sz, vp]
         L.pa_prefill_workspace_size.restype = sz
         L.pa_prefill_workspace_size.argtypes = [i, i, i, i]
+        L.pa_diff_decode_workspace_size.restype = sz
+        L.pa_diff_decode_workspace_size.argtypes = [i] * 5
+        L.pa_diff_decode.restype = i
+        L.pa_diff_decode.argtypes = [vp] * 8 + [i] * 7 + [f] * 3 + [i, vp, sz, vp]
+        L.pa_diff_prefill_workspace_size.restype = sz
+        L.pa_diff_prefill_workspace_size.argtypes = [i] * 4
+        L.pa_diff_prefill.restype = i
+        L.pa_diff_prefill.argtypes = [vp] * 9 + [i] * 8 + [f] * 3 + [i, vp, sz, vp]
         L.pa_selftest_bounded_wait.restype = i
         L.pa_selftest_bounded_wait.argtypes = [i, vp]
         L.pa_get_device_error.restype = i
@@ -311,6 +321,112 @@ def prefill(out, q, k_cache, v_cache, block_tables, seq_lens, query_start, max_q
                            bs, block_tables.shape[1], nb, float(scale), _dtype_code(q),
                            _ptr(workspace), wbytes, _stream(stream))
     _check("pa_prefill", rc)
+    return out
+
+
+def _diff_args(out, q, k_cache, v_cache, block_tables, seq_lens, lam, norm_weight, workspace):
+    """Checks what diff_decode and diff_prefill share; the workspace's bytes."""
+    torch = _torch()
+    hq, d = q.shape[1:]
+    n, dt, dev = seq_lens.shape[0], q.dtype, q.get_device()
+    _require(dev >= 0 and dev == torch.cuda.current_device(),
+             "tensors must be on the current CUDA device")
+    _require(out.shape == q.shape and k_cache.shape[3] == d and v_cache.shape == k_cache.shape,
+             "shapes")
+    _require(out.dtype == dt and k_cache.dtype == dt and v_cache.dtype == dt,
+             "out and the pools: q's dtype")
+    _require(block_tables.dim() == 2 and block_tables.shape[0] == n and seq_lens.dim() == 1,
+             "table shapes")
+    _require(block_tables.dtype == torch.int32 and seq_lens.dtype == torch.int32, "tables: int32")
+    _require(lam.shape == (hq,) and lam.dtype == torch.float32, "lam: float32 [num_heads]")
+    for t in (out, q, k_cache, v_cache, block_tables, seq_lens, lam):
+        _require(t.get_device() == dev and t.is_contiguous(),
+                 "tensors must be contiguous, on the current CUDA device")
+    if norm_weight is not None:
+        _require(norm_weight.shape == (d,) and norm_weight.dtype == dt and
+                 norm_weight.is_contiguous() and norm_weight.get_device() == dev,
+                 "norm_weight: [head_dim] of q's dtype")
+    if workspace is None:
+        return 0
+    _require(workspace.get_device() == dev and workspace.is_contiguous(),
+             "workspace: contiguous, on the current CUDA device")
+    return workspace.numel() * workspace.element_size()
+
+
+def diff_decode_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim,
+                               max_blocks_per_seq) -> int:
+    return int(load().pa_diff_decode_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim,
+                                                    max_blocks_per_seq))
+
+
+def diff_decode_workspace_for(q, k_cache, block_tables, stream=None):
+    """A workspace tensor sized for pa_diff_decode on these shapes."""
+    n, hq, d = q.shape
+    nbytes = diff_decode_workspace_size(n, hq, k_cache.shape[1], d, block_tables.shape[1])
+    return _scratch(nbytes, q.device, stream) if nbytes else None
+
+
+def diff_decode(out, q, k_cache, v_cache, block_tables, seq_lens, lam, scale, norm_weight=None,
+                eps=1e-6, out_scale=1.0, workspace=None, stream=None):
+    """pa_diff_decode: differential attention of one query token per sequence.
+
+    q, out [num_seqs, num_heads, head_dim], a head's row holding its two
+    queries; the pools of decode, a key row holding the two keys; lam float32
+    [num_heads] weighs the second map.  With norm_weight [head_dim] the result is
+    RMS-normalised over the head, and it is multiplied by out_scale either way.
+    """
+    n, hq, d = q.shape
+    _require(seq_lens.shape == (n,), "table shapes")
+    if workspace is None:
+        workspace = diff_decode_workspace_for(q, k_cache, block_tables, stream)
+    wbytes = _diff_args(out, q, k_cache, v_cache, block_tables, seq_lens, lam, norm_weight,
+                        workspace)
+    nb, hkv, bs, _ = k_cache.shape
+    rc = load().pa_diff_decode(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                               _ptr(block_tables), _ptr(seq_lens), _ptr(lam), _ptr(norm_weight), n,
+                               hq, hkv, d, bs, block_tables.shape[1], nb, float(scale), float(eps),
+                               float(out_scale), _dtype_code(q), _ptr(workspace), wbytes,
+                               _stream(stream))
+    _check("pa_diff_decode", rc)
+    return out
+
+
+def diff_prefill_workspace_size(num_seqs, max_query_len, num_heads, num_kv_heads) -> int:
+    return int(load().pa_diff_prefill_workspace_size(num_seqs, max_query_len, num_heads,
+                                                     num_kv_heads))
+
+
+def diff_prefill_workspace_for(q, k_cache, seq_lens, max_query_len, stream=None):
+    """A workspace tensor sized for pa_diff_prefill on these shapes."""
+    nbytes = diff_prefill_workspace_size(seq_lens.shape[0], int(max_query_len), q.shape[1],
+                                         k_cache.shape[1])
+    return _scratch(nbytes, q.device, stream) if nbytes else None
+
+
+def diff_prefill(out, q, k_cache, v_cache, block_tables, seq_lens, query_start, max_query_len, lam,
+                 scale, norm_weight=None, eps=1e-6, out_scale=1.0, workspace="auto", stream=None):
+    """pa_diff_prefill: differential attention of each sequence's newest chunk, causal.
+
+    Rows, tables, query_start, max_query_len and workspace as prefill; lam,
+    norm_weight, eps and out_scale as diff_decode.
+    """
+    t, hq, d = q.shape
+    n = seq_lens.shape[0]
+    _require(query_start.shape == (n + 1,) and query_start.dtype == _torch().int32 and
+             query_start.get_device() == q.get_device() and query_start.is_contiguous(),
+             "query_start: int32 [num_seqs + 1]")
+    if isinstance(workspace, str):
+        workspace = diff_prefill_workspace_for(q, k_cache, seq_lens, max_query_len, stream)
+    wbytes = _diff_args(out, q, k_cache, v_cache, block_tables, seq_lens, lam, norm_weight,
+                        workspace)
+    nb, hkv, bs, _ = k_cache.shape
+    rc = load().pa_diff_prefill(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                _ptr(block_tables), _ptr(seq_lens), _ptr(query_start), _ptr(lam),
+                                _ptr(norm_weight), n, int(max_query_len), hq, hkv, d, bs,
+                                block_tables.shape[1], nb, float(scale), float(eps),
+                                float(out_scale), _dtype_code(q), _ptr(workspace), wbytes,
+                                _stream(stream))
+    _check("pa_diff_prefill", rc)
     return out
 
 

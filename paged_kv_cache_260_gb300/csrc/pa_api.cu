@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cuda.h>
 #include <cudaTypedefs.h>
+#include <limits.h>
 #include <math.h>
 #include <mutex>
 #include <stdint.h>
@@ -402,6 +403,10 @@ struct DecodeExtra {
     // pieces to the caller's merge (no merge_cut); *pieces says where they are
     int32_t *cut_of_run = nullptr;
     CutPieces *pieces = nullptr;
+    // differential attention: the maps' factors, non-null, and the output norm
+    const float *lambda = nullptr;
+    const void *norm_w = nullptr;
+    float norm_eps = 0.f, out_scale = 1.f;
 };
 
 static int decode_impl(void *out, const void *q, const void *k_cache, const void *v_cache,
@@ -419,7 +424,8 @@ static int decode_impl(void *out, const void *q, const void *k_cache, const void
     if (num_heads % num_kv_heads)
         return PA_ERR_INVALID_ARG;
     const int group = num_heads / num_kv_heads;
-    if (group > kMaxGroup)
+    const bool diff = x.lambda != nullptr;
+    if (group > (diff ? kMaxDiffGroup : kMaxGroup))
         return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0)
         return PA_OK;
@@ -442,7 +448,10 @@ static int decode_impl(void *out, const void *q, const void *k_cache, const void
 
     KernelSet ks{};
     bool found;
-    if (group <= 8)
+    if (diff)
+        found = dtype == PA_DTYPE_F16 ? diff_decode_kernels_f16(head_dim, group, &ks)
+                                      : diff_decode_kernels_bf16(head_dim, group, &ks);
+    else if (group <= 8)
         found = dtype == PA_DTYPE_F16 ? decode_kernels_f16(head_dim, &ks)
                                       : decode_kernels_bf16(head_dim, &ks);
     else
@@ -502,8 +511,9 @@ static int decode_impl(void *out, const void *q, const void *k_cache, const void
     const int p_max = mode == kModeFixed ? (max_blocks_per_seq + pt - 1) / pt : 1;
     // sized for the most workers any call on this device can use, so the
     // size does not depend on the launch configuration chosen here
-    const WorkspaceLayout wl = workspace_layout(mode, num_seqs, num_heads, num_kv_heads, head_dim,
-                                                p_max, ds->num_sms * kMaxWarpsPerSM);
+    const WorkspaceLayout wl = workspace_layout(mode, num_seqs, (diff ? 2 : 1) * num_heads,
+                                                num_kv_heads, head_dim, p_max,
+                                                ds->num_sms * kMaxWarpsPerSM);
     if (wl.total > 0 && (!workspace || workspace_bytes < wl.total || !aligned(workspace, 256)))
         return PA_ERR_WORKSPACE;
 
@@ -521,6 +531,10 @@ static int decode_impl(void *out, const void *q, const void *k_cache, const void
     p.out_l = x.out_l;
     p.out_o = x.out_o;
     p.cut_of_run = x.cut_of_run;
+    p.lambda = x.lambda;
+    p.norm_w = x.norm_w;
+    p.norm_eps = x.norm_eps;
+    p.out_scale = x.out_scale;
     char *ws = static_cast<char *>(workspace);
     if (wl.total > 0) {
         p.ws_m = reinterpret_cast<float *>(ws + wl.m_off);
@@ -604,6 +618,50 @@ int pa_decode(void *out, const void *q, const void *k_cache, const void *v_cache
     return decode_impl(out, q, k_cache, v_cache, block_tables, seq_lens, num_seqs, num_heads,
                        num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks, scale,
                        dtype, partition_size, workspace, workspace_bytes, stream, DecodeExtra{});
+}
+
+// The arguments that the two differential entry points share beyond those of
+// the plain ones.
+static int check_diff(const float *lambda, const void *norm_weight, float norm_eps,
+                      float out_scale, bool work)
+{
+    if (!isfinite(norm_eps) || norm_eps < 0.f || !isfinite(out_scale))
+        return PA_ERR_INVALID_ARG;
+    if (work && (!lambda || !aligned(lambda, 4) || !aligned(norm_weight, 16)))
+        return PA_ERR_INVALID_ARG;
+    return PA_OK;
+}
+
+size_t pa_diff_decode_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                     int max_blocks_per_seq)
+{
+    if (num_heads <= 0 || num_heads > INT_MAX / 2 || num_kv_heads <= 0 ||
+        num_heads % num_kv_heads)
+        return 0;
+    return pa_decode_workspace_size(num_seqs, 2 * num_heads, num_kv_heads, head_dim,
+                                    max_blocks_per_seq, 0);
+}
+
+int pa_diff_decode(void *out, const void *q, const void *k_cache, const void *v_cache,
+                   const int32_t *block_tables, const int32_t *seq_lens, const float *lambda,
+                   const void *norm_weight, int num_seqs, int num_heads, int num_kv_heads,
+                   int head_dim, int block_size, int max_blocks_per_seq, int num_blocks,
+                   float scale, float norm_eps, float out_scale, int dtype, void *workspace,
+                   size_t workspace_bytes, void *stream)
+{
+    const int rc = check_diff(lambda, norm_weight, norm_eps, out_scale, num_seqs > 0);
+    if (rc != PA_OK)
+        return rc;
+    // an empty batch has no factors to read, but its other arguments are checked as ever
+    static const float none = 0.f;
+    DecodeExtra x;
+    x.lambda = lambda ? lambda : &none;
+    x.norm_w = norm_weight;
+    x.norm_eps = norm_eps;
+    x.out_scale = out_scale;
+    return decode_impl(out, q, k_cache, v_cache, block_tables, seq_lens, num_seqs, num_heads,
+                       num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks, scale,
+                       dtype, 0, workspace, workspace_bytes, stream, x);
 }
 
 int pa_decode_append(void *out, const void *q, void *k_cache, void *v_cache,
@@ -843,34 +901,58 @@ int pa_decode_shared_prefix(void *out, const void *q, void *k_cache, void *v_cac
     return cuda_status(launch_shared_merge(sp, dtype == PA_DTYPE_BF16, st));
 }
 
-// Query tiles per (sequence, kv head) of a prefill grid, 0 on bad arguments.
-static long long prefill_q_ranks(int max_query_len, int num_heads, int num_kv_heads)
+// Query tiles per (sequence, kv head) of a prefill grid, 0 on bad arguments;
+// `tiles`: the 128-row query tiles of a thread block.
+static long long prefill_q_ranks(int max_query_len, int num_heads, int num_kv_heads,
+                                 int tiles = kPrefillTiles)
 {
     if (max_query_len <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads ||
         num_heads / num_kv_heads > kPrefillRows)
         return 0;
-    const int tokens_per_block = kPrefillTiles * (kPrefillRows / (num_heads / num_kv_heads));
+    const int tokens_per_block = tiles * (kPrefillRows / (num_heads / num_kv_heads));
     return (max_query_len + tokens_per_block - 1) / tokens_per_block;
 }
 
 // Work-order workspace: the pair count and the order's kind (two ints, 16
 // bytes), one word per (sequence, query tile) pair, then each sequence's
 // first pair and pair count (int32 each).
-size_t pa_prefill_workspace_size(int num_seqs, int max_query_len, int num_heads,
-                                 int num_kv_heads)
+static size_t prefill_workspace_bytes(int num_seqs, long long q_ranks)
 {
-    const long long q_ranks = prefill_q_ranks(max_query_len, num_heads, num_kv_heads);
     if (num_seqs <= 0 || q_ranks <= 0)
         return 0;
     return round_up(16 + 4 * (size_t)num_seqs * (size_t)q_ranks + 8 * (size_t)num_seqs, 256);
 }
 
-int pa_prefill(void *out, const void *q, const void *k_cache, const void *v_cache,
-               const int32_t *block_tables, const int32_t *seq_lens, const int32_t *query_start,
-               int num_seqs, int max_query_len, int num_heads, int num_kv_heads, int head_dim,
-               int block_size, int max_blocks_per_seq, int num_blocks, float scale, int dtype,
-               void *workspace, size_t workspace_bytes, void *stream)
+size_t pa_prefill_workspace_size(int num_seqs, int max_query_len, int num_heads,
+                                 int num_kv_heads)
 {
+    return prefill_workspace_bytes(num_seqs,
+                                   prefill_q_ranks(max_query_len, num_heads, num_kv_heads));
+}
+
+size_t pa_diff_prefill_workspace_size(int num_seqs, int max_query_len, int num_heads,
+                                      int num_kv_heads)
+{
+    return prefill_workspace_bytes(num_seqs,
+                                   prefill_q_ranks(max_query_len, num_heads, num_kv_heads, 1));
+}
+
+// What a differential prefill does beyond pa_prefill (lambda non-null).
+struct PrefillExtra {
+    const float *lambda = nullptr;
+    const void *norm_w = nullptr;
+    float norm_eps = 0.f, out_scale = 1.f;
+};
+
+static int prefill_impl(void *out, const void *q, const void *k_cache, const void *v_cache,
+                        const int32_t *block_tables, const int32_t *seq_lens,
+                        const int32_t *query_start, int num_seqs, int max_query_len, int num_heads,
+                        int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                        int num_blocks, float scale, int dtype, void *workspace,
+                        size_t workspace_bytes, void *stream, const PrefillExtra &x)
+{
+    const bool diff = x.lambda != nullptr;
+    const int tiles = diff ? 1 : kPrefillTiles;
     int rc = check_common(num_kv_heads, head_dim, block_size, num_blocks, dtype);
     if (rc != PA_OK)
         return rc;
@@ -888,7 +970,7 @@ int pa_prefill(void *out, const void *q, const void *k_cache, const void *v_cach
         !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(query_start, 4))
         return PA_ERR_INVALID_ARG;
     const long long pool_rows = (long long)num_blocks * num_kv_heads * kBlockSize;
-    const long long q_ranks = prefill_q_ranks(max_query_len, num_heads, num_kv_heads);
+    const long long q_ranks = prefill_q_ranks(max_query_len, num_heads, num_kv_heads, tiles);
     const long long grid = q_ranks * num_seqs * num_kv_heads;
     if ((long long)max_blocks_per_seq * kBlockSize >= (1LL << 30) || pool_rows >= (1LL << 31) ||
         grid >= (1LL << 31))
@@ -899,12 +981,11 @@ int pa_prefill(void *out, const void *q, const void *k_cache, const void *v_cach
         if (num_seqs > 65535 || q_ranks > 65535)
             return PA_ERR_UNSUPPORTED;
         if (!aligned(workspace, 256) ||
-            workspace_bytes < pa_prefill_workspace_size(num_seqs, max_query_len, num_heads,
-                                                        num_kv_heads))
+            workspace_bytes < prefill_workspace_bytes(num_seqs, q_ranks))
             return PA_ERR_WORKSPACE;
     }
     PrefillKernel kk{};
-    if (!prefill_kernel(dtype, head_dim, &kk))
+    if (!(diff ? diff_prefill_kernel(dtype, head_dim, &kk) : prefill_kernel(dtype, head_dim, &kk)))
         return PA_ERR_UNSUPPORTED;
     DeviceState *ds;
     rc = device_state(&ds);
@@ -942,6 +1023,10 @@ int pa_prefill(void *out, const void *q, const void *k_cache, const void *v_cach
     p.q_ranks = (int)q_ranks;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.wave = ds->num_sms;
+    p.lambda = x.lambda;
+    p.norm_w = x.norm_w;
+    p.norm_eps = x.norm_eps;
+    p.out_scale = x.out_scale;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (planned) {
         int *count = static_cast<int *>(workspace);
@@ -954,7 +1039,7 @@ int pa_prefill(void *out, const void *q, const void *k_cache, const void *v_cach
         p.plan_by_seq = by_seq;
         p.plan_seq_start = seq_start;
         p.plan_seq_nq = seq_nq;
-        int tpb = kPrefillTiles * (kPrefillRows / group), bn = kPrefillKeys;
+        int tpb = tiles * (kPrefillRows / group), bn = kPrefillKeys;
         // K and V bytes a token holds over all kv heads, and the L2 size: the
         // plan keeps each sequence's tiles together when the batch's K/V
         // does not fit in L2
@@ -969,6 +1054,42 @@ int pa_prefill(void *out, const void *q, const void *k_cache, const void *v_cach
     // plan finishes and read no global memory before it has completed
     void *args[] = {&p, &tmk, &tmv};
     return launch_dependent(kk.fn, dim3((unsigned)grid), dim3(kk.threads), kk.smem, st, args);
+}
+
+int pa_prefill(void *out, const void *q, const void *k_cache, const void *v_cache,
+               const int32_t *block_tables, const int32_t *seq_lens, const int32_t *query_start,
+               int num_seqs, int max_query_len, int num_heads, int num_kv_heads, int head_dim,
+               int block_size, int max_blocks_per_seq, int num_blocks, float scale, int dtype,
+               void *workspace, size_t workspace_bytes, void *stream)
+{
+    return prefill_impl(out, q, k_cache, v_cache, block_tables, seq_lens, query_start, num_seqs,
+                        max_query_len, num_heads, num_kv_heads, head_dim, block_size,
+                        max_blocks_per_seq, num_blocks, scale, dtype, workspace, workspace_bytes,
+                        stream, PrefillExtra{});
+}
+
+int pa_diff_prefill(void *out, const void *q, const void *k_cache, const void *v_cache,
+                    const int32_t *block_tables, const int32_t *seq_lens,
+                    const int32_t *query_start, const float *lambda, const void *norm_weight,
+                    int num_seqs, int max_query_len, int num_heads, int num_kv_heads, int head_dim,
+                    int block_size, int max_blocks_per_seq, int num_blocks, float scale,
+                    float norm_eps, float out_scale, int dtype, void *workspace,
+                    size_t workspace_bytes, void *stream)
+{
+    const int rc = check_diff(lambda, norm_weight, norm_eps, out_scale,
+                              num_seqs > 0 && max_query_len > 0);
+    if (rc != PA_OK)
+        return rc;
+    static const float none = 0.f;
+    PrefillExtra x;
+    x.lambda = lambda ? lambda : &none;
+    x.norm_w = norm_weight;
+    x.norm_eps = norm_eps;
+    x.out_scale = out_scale;
+    return prefill_impl(out, q, k_cache, v_cache, block_tables, seq_lens, query_start, num_seqs,
+                        max_query_len, num_heads, num_kv_heads, head_dim, block_size,
+                        max_blocks_per_seq, num_blocks, scale, dtype, workspace, workspace_bytes,
+                        stream, x);
 }
 
 int pa_reshape_and_cache(const void *k_new, const void *v_new, void *k_cache, void *v_cache,

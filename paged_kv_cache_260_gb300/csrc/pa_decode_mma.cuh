@@ -34,6 +34,19 @@
 //    the input type for the second product and transposed in registers
 //    (movmatrix), so every lane owns the same heads in S and in O: the
 //    online-softmax rescale needs no data exchange between lanes.
+//  * Differential attention (DIFF): a head has two queries q1, q2 and each
+//    token two keys k1, k2 of head_dim / 2 channels, side by side in the q row
+//    and in the pool's key row; the values are shared and head_dim wide:
+//        y = sum_t softmax_t(scale q1.k1_t) v_t - lambda sum_t softmax_t(scale q2.k2_t) v_t
+//    followed by an optional RMS norm over head_dim.  The two maps are two
+//    query columns of one decode: column 1 is q1 with zeros in the second half
+//    of its channels, column 2 the reverse, so K and V leave HBM once for both
+//    and the loop below stays as it is.  Groups of up to 4 heads fit one
+//    8-column tile (columns 0-3 map 1, 4-7 map 2); 5 to 8 heads take a tile
+//    for each map, and each tile runs the k-steps of its own half alone.
+//    The difference cancels what the maps share, and with it part of the
+//    result that a rounding of P is relative to; so P enters the second
+//    product as two 16-bit terms, its rounded value and the rounded rest.
 //  * Large batches (more than kSeqsInSmem sequences) keep the per-sequence
 //    lengths and unit prefix in the workspace, built once by two small
 //    kernels, instead of in every block's shared memory.
@@ -47,7 +60,7 @@
 
 namespace pa {
 
-template <int D, int NT>
+template <int D, int NT, bool DIFF = false>
 struct MmaShape {
     static_assert(D == 64 || D == 128, "head_dim");
     static_assert(NT == 1 || NT == 2, "query columns: 8 or 16");
@@ -55,14 +68,15 @@ struct MmaShape {
     static constexpr int BOX = kBlockSize * 128;              // bytes of one box (16 rows x 128 B)
     static constexpr int TILE = NB * BOX;                     // bytes of K (or V) per tile
     static constexpr int KSTEPS = D / 16;                     // QK: k-steps; PV: m-tiles
-    static constexpr int QB_MAX = 8 * NT * D * 2;             // q group, up to 8 * NT heads
+    static constexpr int HEADS = (DIFF ? 4 : 8) * NT;         // most heads of a group
+    static constexpr int QB_MAX = HEADS * D * 2;              // q group
     static constexpr int QSLOT = (QB_MAX + 1023) / 1024 * 1024;
     static constexpr int STAGE = 2 * TILE + QSLOT;            // multiple of 1024 (swizzle atom)
 };
 
-template <int D, int NT, int W, int S>
+template <int D, int NT, int W, int S, bool DIFF = false>
 struct MmaLayout {
-    using Sh = MmaShape<D, NT>;
+    using Sh = MmaShape<D, NT, DIFF>;
     static constexpr size_t stages = (size_t)W * S * Sh::STAGE;
     static constexpr size_t bars = (size_t)W * S * 8;
     // +1024: the dynamic shared memory base is aligned up to the swizzle atom
@@ -171,18 +185,119 @@ __device__ __forceinline__ uint64_t l2_evict_normal_policy()
     return pol;
 }
 
+// Differential attention, a run one warp has read whole: the difference of
+// the two maps' results, its norm over head_dim, and the output row.  Lane
+// (r, qd) holds rows 16 mt + r (+ 8) of its columns.  With one column tile the
+// lanes qd and qd ^ 2 hold the two maps of the same heads: each hands half of
+// its rows to the other and keeps the difference of the rest.
+template <typename T, int D, int NT>
+__device__ __forceinline__ void diff_whole(const DecodeParams &p, const float (&o)[NT][D / 16][4],
+                                           const float (&l)[NT][2], int s, int h, int G, int r,
+                                           int qd)
+{
+    using E = Elem<T>;
+    constexpr uint32_t FULL = 0xffffffffu;
+    constexpr int KS = D / 16, ROWS = NT == 1 ? KS / 2 : KS;
+    const int map = NT == 1 ? qd >> 1 : 0;
+    const int h0 = NT == 1 ? (2 * qd & 3) : 2 * qd, h1 = h0 + 1;
+    const float lam0 = h0 < G ? __ldg(p.lambda + h * G + h0) : 0.f;
+    const float lam1 = h1 < G ? __ldg(p.lambda + h * G + h1) : 0.f;
+    float y[ROWS][4];
+    if constexpr (NT == 1) {
+        const float f0 = (map ? -lam0 : 1.f) / l[0][0], f1 = (map ? -lam1 : 1.f) / l[0][1];
+#pragma unroll
+        for (int mt = 0; mt < ROWS; ++mt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float f = c & 1 ? f1 : f0;
+                const float lo = o[0][mt][c] * f, hi = o[0][mt + ROWS][c] * f;
+                y[mt][c] = (map ? hi : lo) + __shfl_xor_sync(FULL, map ? lo : hi, 2);
+            }
+    } else {
+        const float f0 = 1.f / l[0][0], f1 = 1.f / l[0][1];
+        const float g0 = -lam0 / l[NT - 1][0], g1 = -lam1 / l[NT - 1][1];
+#pragma unroll
+        for (int mt = 0; mt < ROWS; ++mt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                y[mt][c] = fmaf(o[NT - 1][mt][c], c & 1 ? g1 : g0, o[0][mt][c] * (c & 1 ? f1 : f0));
+    }
+    float k0 = p.out_scale, k1 = p.out_scale;
+    const T *w = static_cast<const T *>(p.norm_w);
+    if (w) {
+        float q0 = 0.f, q1 = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < ROWS; ++mt) {
+            q0 = fmaf(y[mt][0], y[mt][0], fmaf(y[mt][2], y[mt][2], q0));
+            q1 = fmaf(y[mt][1], y[mt][1], fmaf(y[mt][3], y[mt][3], q1));
+        }
+#pragma unroll
+        for (int off = NT == 1 ? 2 : 4; off < 32; off <<= 1) {
+            q0 += __shfl_xor_sync(FULL, q0, off);
+            q1 += __shfl_xor_sync(FULL, q1, off);
+        }
+        k0 *= rsqrtf(q0 * (1.f / D) + p.norm_eps);
+        k1 *= rsqrtf(q1 * (1.f / D) + p.norm_eps);
+    }
+    T *out = static_cast<T *>(p.out) + ((size_t)s * p.num_heads + h * G) * D;
+#pragma unroll
+    for (int mt = 0; mt < ROWS; ++mt) {
+        const int d0 = 16 * (mt + map * ROWS) + r;
+        const float w0 = w ? E::to_f(w[d0]) : 1.f, w8 = w ? E::to_f(w[d0 + 8]) : 1.f;
+        if (h0 < G) {
+            out[h0 * D + d0] = E::from_f(y[mt][0] * (k0 * w0));
+            out[h0 * D + d0 + 8] = E::from_f(y[mt][2] * (k0 * w8));
+        }
+        if (h1 < G) {
+            out[h1 * D + d0] = E::from_f(y[mt][1] * (k1 * w0));
+            out[h1 * D + d0 + 8] = E::from_f(y[mt][3] * (k1 * w8));
+        }
+    }
+}
+
+// A cut piece of a run: both maps' partial results go to this worker's slot,
+// rows map * G + head of 2 G.  A column whose scores were all -inf has l = 0
+// and leaves zeros.
+template <int D, int NT>
+__device__ __forceinline__ void diff_piece(const DecodeParams &p, const float (&o)[NT][D / 16][4],
+                                           const float (&m)[NT][2], const float (&l)[NT][2],
+                                           int slot, int G, int r, int qd)
+{
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int map = NT == 1 ? qd >> 1 : j;
+            const int hq = (NT == 1 ? (2 * qd & 3) : 2 * qd) + e;
+            if (hq >= G)
+                continue;
+            const size_t row = slot_row(2 * G, slot, map * G + hq);
+            const float inv = l[j][e] > 0.f ? 1.f / l[j][e] : l[j][e];
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt) {
+                p.ws_so[row * D + 16 * mt + r] = o[j][mt][e] * inv;
+                p.ws_so[row * D + 16 * mt + r + 8] = o[j][mt][e + 2] * inv;
+            }
+            if (r == 0) {
+                p.ws_sm[row] = m[j][e] * kLn2;
+                p.ws_sl[row] = l[j][e];
+            }
+        }
+}
+
 // One warp's whole walk: its pieces, tile by tile, and their results.
 // SHARE: some sequence of the batch shares its first block with a
 // neighbour; only then are the neighbours' table entries looked up per tile
 // (the check costs the unshared loop a few per cent even when it never
 // fires, so the kernel holds two copies of the loop and picks one per block).
-template <typename T, int D, int NT, int W, int S, bool SHARE, bool PARTIAL>
+template <typename T, int D, int NT, int W, int S, bool SHARE, bool PARTIAL, bool DIFF>
 __device__ __forceinline__ void decode_worker(const DecodeParams &p, const CUtensorMap &tmk,
                                               const CUtensorMap &tmv, unsigned char *smem,
                                               uint64_t *bars, const int32_t *pre,
                                               const int32_t *lens, const uint8_t *share)
 {
-    using Sh = MmaShape<D, NT>;
+    static_assert(!(PARTIAL && DIFF), "no partial outputs of a difference");
+    using Sh = MmaShape<D, NT, DIFF>;
     using E = Elem<T>;
     using M = Mma<T>;
     constexpr int KS = Sh::KSTEPS;
@@ -323,7 +438,7 @@ __device__ __forceinline__ void decode_worker(const DecodeParams &p, const CUten
         bool app = false;
         int app_phys = 0;
         uint4 app_row = make_uint4(0u, 0u, 0u, 0u);
-        if (p.k_new != nullptr && L > 0 && cons.te == cons.nt) {
+        if (!DIFF && p.k_new != nullptr && L > 0 && cons.te == cons.nt) {
             const int64_t slot = __ldg(p.slot_mapping + cons.s);
             if (slot >= 0) {
                 app_phys = __ldg(p.block_tables + (size_t)cons.s * p.max_blocks + last_tile);
@@ -355,12 +470,15 @@ __device__ __forceinline__ void decode_worker(const DecodeParams &p, const CUten
                 const unsigned char *qs = wst + (size_t)st * Sh::STAGE + 2 * Sh::TILE;
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    const int hq = 8 * j + r;     // B column: query head of the group
+                    // B column: query head of the group (and map)
+                    const int hq = !DIFF ? 8 * j + r : NT == 1 ? (r & 3) : r;
+                    const int map = NT == 1 ? r >> 2 : j;
                     const uint32_t *qrow = reinterpret_cast<const uint32_t *>(qs + (size_t)hq * D * 2);
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks) {
-                        qf[j][ks][0] = hq < G ? qrow[(16 * ks + 2 * qd) / 2] : 0u;
-                        qf[j][ks][1] = hq < G ? qrow[(16 * ks + 8 + 2 * qd) / 2] : 0u;
+                        const bool on = hq < G && (!DIFF || ks / (KS / 2) == map);
+                        qf[j][ks][0] = on ? qrow[(16 * ks + 2 * qd) / 2] : 0u;
+                        qf[j][ks][1] = on ? qrow[(16 * ks + 8 + 2 * qd) / 2] : 0u;
                     }
                 }
                 need_q = false;
@@ -396,10 +514,12 @@ __device__ __forceinline__ void decode_worker(const DecodeParams &p, const CUten
                 ldsm_x4(kst + (ks >> 2) * Sh::BOX + swz(krow, 2 * (ks & 3) + kcs), a[0], a[1], a[2], a[3]);
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
-                    M::run((ks & 1) ? sb[j] : sa[j], a, qf[j][ks][0], qf[j][ks][1]);
+                    if (!DIFF || NT == 1 || ks / (KS / 2) == j)
+                        M::run((ks & 1) ? sb[j] : sa[j], a, qf[j][ks][0], qf[j][ks][1]);
             }
             const bool masked = nvalid < kBlockSize;
             uint32_t pb[NT][2];
+            uint32_t pr[NT][2];                   // DIFF: what rounding P left over
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 float x0 = (sa[j][0] + sb[j][0]) * p.scale_log2;   // token r,   head h0
@@ -421,7 +541,10 @@ __device__ __forceinline__ void decode_worker(const DecodeParams &p, const CUten
                 }
                 if (__any_sync(FULL, (mx0 > m[j][0]) | (mx1 > m[j][1]))) {
                     const float n0 = fmaxf(m[j][0], mx0), n1 = fmaxf(m[j][1], mx1);
-                    const float a0 = exp2f(m[j][0] - n0), a1 = exp2f(m[j][1] - n1);
+                    // DIFF: a column that has only seen -inf keeps weights of
+                    // zero (the other column brought us here)
+                    const float a0 = DIFF && n0 == -INFINITY ? 1.f : exp2f(m[j][0] - n0);
+                    const float a1 = DIFF && n1 == -INFINITY ? 1.f : exp2f(m[j][1] - n1);
                     m[j][0] = n0;
                     m[j][1] = n1;
                     l[j][0] *= a0;
@@ -434,13 +557,21 @@ __device__ __forceinline__ void decode_worker(const DecodeParams &p, const CUten
                         o[j][mt][3] *= a1;
                     }
                 }
-                const float p0 = exp2f(x0 - m[j][0]), p1 = exp2f(x1 - m[j][1]);
-                const float p2 = exp2f(x2 - m[j][0]), p3 = exp2f(x3 - m[j][1]);
+                const float s0 = DIFF && m[j][0] == -INFINITY ? 0.f : m[j][0];
+                const float s1 = DIFF && m[j][1] == -INFINITY ? 0.f : m[j][1];
+                const float p0 = exp2f(x0 - s0), p1 = exp2f(x1 - s1);
+                const float p2 = exp2f(x2 - s0), p3 = exp2f(x3 - s1);
                 l[j][0] += p0 + p2;
                 l[j][1] += p1 + p3;
                 // P^T as the B operand: rows of P (tokens) become columns
-                pb[j][0] = movmatrix_trans(M::pack(p0, p1));
-                pb[j][1] = movmatrix_trans(M::pack(p2, p3));
+                const uint32_t u0 = M::pack(p0, p1), u1 = M::pack(p2, p3);
+                pb[j][0] = movmatrix_trans(u0);
+                pb[j][1] = movmatrix_trans(u1);
+                if constexpr (DIFF) {
+                    const float2 f0 = E::to_f2(u0), f1 = E::to_f2(u1);
+                    pr[j][0] = movmatrix_trans(M::pack(p0 - f0.x, p1 - f0.y));
+                    pr[j][1] = movmatrix_trans(M::pack(p2 - f1.x, p3 - f1.y));
+                }
             }
 
             // O^T += V^T . P^T ; value rows past the end are zeroed (0 * NaN is NaN)
@@ -460,8 +591,11 @@ __device__ __forceinline__ void decode_worker(const DecodeParams &p, const CUten
                 a[2] &= mhi;
                 a[3] &= mhi;
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
+                for (int j = 0; j < NT; ++j) {
                     M::run(o[j][mt], a, pb[j][0], pb[j][1]);
+                    if constexpr (DIFF)
+                        M::run(o[j][mt], a, pr[j][0], pr[j][1]);
+                }
             }
             __syncwarp();
             if (!aborted)
@@ -474,8 +608,21 @@ __device__ __forceinline__ void decode_worker(const DecodeParams &p, const CUten
         const bool whole = cons.whole_run();
         const bool wp = !whole && cons.whole_part();
         const int slot = 2 * worker + (cons.first ? 0 : 1);
+        if constexpr (DIFF) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) {
+                    l[j][0] += __shfl_xor_sync(FULL, l[j][0], off);
+                    l[j][1] += __shfl_xor_sync(FULL, l[j][1], off);
+                }
+            if (whole)
+                diff_whole<T, D, NT>(p, o, l, s, h, G, r, qd);
+            else
+                diff_piece<D, NT>(p, o, m, l, slot, G, r, qd);
+        }
+#pragma unroll
+        for (int j = 0; j < (DIFF ? 0 : NT); ++j) {
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) {
                 l[j][0] += __shfl_xor_sync(FULL, l[j][0], off);
@@ -589,12 +736,12 @@ __device__ __forceinline__ void decode_worker(const DecodeParams &p, const CUten
     }
 }
 
-template <typename T, int D, int NT, int W, int S, bool PARTIAL>
+template <typename T, int D, int NT, int W, int S, bool PARTIAL, bool DIFF = false>
 __global__ void __launch_bounds__(W * 32)
 decode_mma_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmk,
                   const __grid_constant__ CUtensorMap tmv)
 {
-    using Lay = MmaLayout<D, NT, W, S>;
+    using Lay = MmaLayout<D, NT, W, S, DIFF>;
     using E = Elem<T>;
 
     extern __shared__ unsigned char smem_raw[];
@@ -669,9 +816,11 @@ decode_mma_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmk,
     }
 
     if (any_share)
-        decode_worker<T, D, NT, W, S, true, PARTIAL>(p, tmk, tmv, smem, bars, pre, lens, share);
+        decode_worker<T, D, NT, W, S, true, PARTIAL, DIFF>(p, tmk, tmv, smem, bars, pre, lens,
+                                                           share);
     else
-        decode_worker<T, D, NT, W, S, false, PARTIAL>(p, tmk, tmv, smem, bars, pre, lens, share);
+        decode_worker<T, D, NT, W, S, false, PARTIAL, DIFF>(p, tmk, tmv, smem, bars, pre, lens,
+                                                            share);
 }
 
 // ---------------------------------------------------------------------------
@@ -863,6 +1012,127 @@ __global__ void __launch_bounds__(512) merge_part_kernel(const DecodeParams p)
         T *out = reinterpret_cast<T *>(p.out);
         out[((size_t)s * Hq + h * G + g) * D + tid] = E::from_f(o / W);
     }
+}
+
+// Differential attention's merge of the cut runs: warp g folds the pieces of
+// head g's two maps, takes the difference and the norm and writes the output
+// row, lane by lane D/32 channels.
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kMaxDiffGroup) merge_cut_diff_kernel(const DecodeParams p)
+{
+    constexpr int V = D / 32;
+    constexpr int CH = 4;
+    grid_dependents_launch();
+    grid_dependency_wait();
+    const CutDesc *dp = p.ws_desc + blockIdx.x;
+    const int valid = __ldcg(&dp->valid);
+    const int Hkv = p.num_kv_heads, Hq = p.num_heads, G = Hq / Hkv;
+    const int g = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (!valid || g >= G)
+        return;
+    const int s = __ldcg(&dp->s), h = __ldcg(&dp->h);
+    const int u0 = __ldcg(&dp->u0), nu = __ldcg(&dp->nu), R = __ldcg(&dp->R);
+    const int c0 = blockIdx.x, c1 = cut_last_worker(u0, nu, R);
+    const int npieces = c1 - c0 + 1;
+    const float lam = __ldg(p.lambda + h * G + g);
+
+    float Mx[2] = {-INFINITY, -INFINITY}, Ws[2] = {0.f, 0.f}, acc[2][V];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        acc[0][v] = acc[1][v] = 0.f;
+    for (int base = 0; base < npieces; base += CH) {
+        float mv[CH][2], lv[CH][2], ov[CH][2][V];
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            if (base + i < npieces) {
+                const int slot = cut_piece_slot(c0 + base + i, c0, u0 != c0 * R);
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    const size_t row = slot_row(2 * G, slot, a * G + g);
+                    mv[i][a] = __ldcg(p.ws_sm + row);
+                    lv[i][a] = __ldcg(p.ws_sl + row);
+                    const float *src = p.ws_so + row * D + lane * V;
+                    if constexpr (V == 4) {
+                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
+                        ov[i][a][0] = x.x, ov[i][a][1] = x.y, ov[i][a][2] = x.z, ov[i][a][3] = x.w;
+                    } else {
+                        const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
+                        ov[i][a][0] = x.x, ov[i][a][1] = x.y;
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            if (base + i < npieces) {
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    const float nM = fmaxf(Mx[a], mv[i][a]);
+                    const float f = Mx[a] == -INFINITY ? 0.f : exp2f((Mx[a] - nM) * kLog2e);
+                    const float b = mv[i][a] == -INFINITY
+                                        ? lv[i][a]       // zero, or NaN if a score was
+                                        : lv[i][a] * exp2f((mv[i][a] - nM) * kLog2e);
+                    Ws[a] = Ws[a] * f + b;
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        acc[a][v] = acc[a][v] * f + b * ov[i][a][v];
+                    Mx[a] = nM;
+                }
+            }
+        }
+    }
+    const float i0 = 1.f / Ws[0], i1 = -lam / Ws[1];
+    float y[V], ss = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        y[v] = fmaf(acc[1][v], i1, acc[0][v] * i0);
+        ss = fmaf(y[v], y[v], ss);
+    }
+    float k = p.out_scale;
+    const T *w = static_cast<const T *>(p.norm_w);
+    if (w) {
+#pragma unroll
+        for (int off = 16; off; off >>= 1)
+            ss += __shfl_xor_sync(0xffffffffu, ss, off);
+        k *= rsqrtf(ss * (1.f / D) + p.norm_eps);
+    }
+    using M = Mma<T>;
+    T *dst = static_cast<T *>(p.out) + ((size_t)s * Hq + h * G + g) * D + lane * V;
+    uint32_t *d32 = reinterpret_cast<uint32_t *>(dst);
+#pragma unroll
+    for (int v = 0; v < V; v += 2) {
+        float w0 = k, w1 = k;
+        if (w) {
+            w0 *= Elem<T>::to_f(w[lane * V + v]);
+            w1 *= Elem<T>::to_f(w[lane * V + v + 1]);
+        }
+        d32[v / 2] = M::pack(y[v] * w0, y[v + 1] * w1);
+    }
+}
+
+template <typename T, int D, int NT>
+inline void fill_diff_kernel_set(KernelSet *ks)
+{
+    constexpr int S = 2;
+    constexpr int W = D == 128 ? 7 : 12;
+    ks->decode = reinterpret_cast<const void *>(&decode_mma_kernel<T, D, NT, W, S, false, true>);
+    ks->warps = W;
+    ks->smem_fixed = MmaLayout<D, NT, W, S, true>::fixed;
+    ks->prep = reinterpret_cast<const void *>(&decode_prep_kernel<kPrepThreads>);
+    ks->prep_fix = reinterpret_cast<const void *>(&decode_prep_fix_kernel<kPrepThreads>);
+    ks->merge_cut = reinterpret_cast<const void *>(&merge_cut_diff_kernel<T, D>);
+}
+
+template <typename T>
+inline bool diff_kernels(int head_dim, int group, KernelSet *ks)
+{
+    if (head_dim == 128)
+        group <= 4 ? fill_diff_kernel_set<T, 128, 1>(ks) : fill_diff_kernel_set<T, 128, 2>(ks);
+    else if (head_dim == 64)
+        group <= 4 ? fill_diff_kernel_set<T, 64, 1>(ks) : fill_diff_kernel_set<T, 64, 2>(ks);
+    else
+        return false;
+    return true;
 }
 
 template <typename T, int D, int NT>

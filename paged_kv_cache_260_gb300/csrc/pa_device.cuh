@@ -175,6 +175,7 @@ struct Elem<__half> {
         return __half22float2(h);
     }
     static __device__ __forceinline__ __half from_f(float x) { return __float2half_rn(x); }
+    static __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
 };
 
 template <>
@@ -185,6 +186,7 @@ struct Elem<__nv_bfloat16> {
         return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
     }
     static __device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat16_rn(x); }
+    static __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 };
 
 // ---------------------------------------------------------------------------

@@ -44,6 +44,12 @@ struct PrefillParams {
     // L2 with the query rows of block b + wave, which starts about when a
     // block of this wave ends
     int wave;
+    // differential attention only: each head's factor of the second map
+    // [num_heads], the output norm's weights [head_dim] or null, its epsilon
+    // and the factor of the output
+    const float *lambda;
+    const void *norm_w;
+    float norm_eps, out_scale;
 };
 
 struct PrefillKernel {
@@ -57,8 +63,10 @@ struct PrefillKernel {
 };
 
 bool prefill_kernel(int dtype, int head_dim, PrefillKernel *k);
+bool diff_prefill_kernel(int dtype, int head_dim, PrefillKernel *k);
 constexpr int kPrefillRows = 128;   // (token, head) rows of one prefill query tile
-constexpr int kPrefillTiles = 2;    // query tiles of one prefill thread block
+constexpr int kPrefillTiles = 2;    // query tiles of one prefill thread block (differential
+                                    // attention: one, against two key maps)
 constexpr int kPrefillKeys = 128;   // keys per prefill key tile
 
 }  // namespace pa

@@ -1,0 +1,395 @@
+"""diff_decode and diff_prefill against the formula in 64 bits (diff_util: the
+tolerance and its derivation).  Pool slots that hold no live token are NaN."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from diff_util import assert_close, reference
+from gpu_util import TORCH_DTYPE
+from paged_kv_cache_260_gb300.block_manager import BlockManager
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-5
+# what rounds a softmax weight: the decode keeps a rounded weight's rest, the prefill does not
+P_DECODE = {"f16": 2.0 ** -21, "bf16": 2.0 ** -17}
+P_PREFILL = {"f16": 2.0 ** -11, "bf16": 2.0 ** -8}
+
+
+class Pool:
+    def __init__(self, lens, hq, hkv, d, dtype, chunks=None, norm=True, seed=0, maxb=None,
+                 gain=2.0, out_scale=0.4):
+        g = torch.Generator().manual_seed(seed)
+        dt = TORCH_DTYPE[dtype]
+        self.dtype, self.lens_h, n = dtype, list(lens), len(lens)
+        used = [(x + 15) // 16 for x in lens]
+        nb = sum(used) + 3
+        mb = maxb or max(1, max(used, default=0))
+        order = torch.randperm(nb, generator=g)
+        self.tables_h = torch.full((n, mb), -1, dtype=torch.int32)
+        at = 0
+        self.k_h, self.v_h = (torch.full((nb, hkv, 16, d), float("nan"), dtype=dt)
+                              for _ in range(2))
+        for s, x in enumerate(lens):
+            for b in range(used[s]):
+                blk = int(order[at + b])
+                self.tables_h[s, b] = blk
+                live = min(16, x - 16 * b)
+                self.k_h[blk, :, :live] = torch.randn(hkv, live, d, generator=g).to(dt)
+                self.v_h[blk, :, :live] = torch.randn(hkv, live, d, generator=g).to(dt)
+            at += used[s]
+        self.k, self.v, self.tables = self.k_h.cuda(), self.v_h.cuda(), self.tables_h.cuda()
+        self.lens = torch.tensor(self.lens_h, dtype=torch.int32).cuda()
+        self.chunks = chunks
+        rows = n if chunks is None else sum(chunks)
+        self.q_h = (gain * torch.randn(rows, hq, d, generator=g)).to(dt)
+        self.q = self.q_h.cuda()
+        self.lam = torch.rand(hq, generator=g).mul(1.2).cuda()
+        self.w = (1 + 0.3 * torch.randn(d, generator=g)).to(dt).cuda() if norm else None
+        self.scale, self.out_scale = (d // 2) ** -0.5, out_scale
+        self.out = torch.full((rows + 2, hq, d), 7.0, dtype=dt, device="cuda")
+        if chunks is not None:
+            self.start_h = [0] + np.cumsum(chunks).tolist()
+            self.start = torch.tensor(self.start_h, dtype=torch.int32).cuda()
+
+    def decode(self, pa, out=None, **kw):
+        out = self.out[:len(self.lens_h)] if out is None else out
+        pa.diff_decode(out, self.q, self.k, self.v, self.tables, self.lens, self.lam, self.scale,
+                       norm_weight=self.w, eps=EPS, out_scale=self.out_scale, **kw)
+        return out
+
+    def prefill(self, pa, out=None, longest=None, **kw):
+        out = self.out[:self.start_h[-1]] if out is None else out
+        pa.diff_prefill(out, self.q, self.k, self.v, self.tables, self.lens, self.start,
+                        max(self.chunks) if longest is None else longest, self.lam, self.scale,
+                        norm_weight=self.w, eps=EPS, out_scale=self.out_scale, **kw)
+        return out
+
+    def rows(self, s):
+        """(first row, positions) of sequence s."""
+        if self.chunks is None:
+            return s, [self.lens_h[s] - 1]
+        c = self.chunks[s]
+        return self.start_h[s], list(range(self.lens_h[s] - c, self.lens_h[s]))
+
+    def check(self, out, only=None):
+        p = (P_DECODE if self.chunks is None else P_PREFILL)[self.dtype]
+        w = None if self.w is None else self.w.cpu()
+        for s in range(len(self.lens_h)) if only is None else only:
+            r0, pos = self.rows(s)
+            ref, tol = reference(self.q_h[r0:r0 + len(pos)], self.k_h, self.v_h, self.tables_h, s,
+                                 pos, self.lam.cpu(), self.scale, w, EPS, self.out_scale, p)
+            assert_close(out[r0:r0 + len(pos)], ref, tol, f"sequence {s}")
+        assert bool((self.out[out.shape[0]:] == 7).all()), "rows past the last sequence"
+
+
+LENS = [0, 1, 2, 15, 16, 17, 31, 33, 100, 257, 700, 1029]
+
+
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("hq,hkv,d,dtype", [
+    (2, 2, 64, "f16"), (8, 8, 128, "bf16"), (4, 2, 128, "f16"), (6, 2, 64, "bf16"),
+    (32, 8, 128, "bf16"), (4, 1, 64, "f16"), (5, 1, 128, "f16"), (12, 2, 64, "bf16"),
+    (7, 1, 64, "f16"), (16, 2, 128, "bf16"), (24, 3, 64, "f16")])
+def test_decode_ragged(pa, hq, hkv, d, dtype, norm):
+    x = Pool(LENS, hq, hkv, d, dtype, norm=norm, seed=hq + d)
+    x.check(x.decode(pa))
+    assert bool((x.out[0] == 0).all())                       # length 0: zeros
+    assert pa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d,dtype", [(8, 8, 64, "f16"), (8, 2, 128, "bf16"),
+                                            (10, 2, 128, "f16")])
+@pytest.mark.parametrize("lens", [[1], [16], [100, 3, 0, 77], [128] * 4])
+def test_decode_short_runs_are_not_split(pa, hq, hkv, d, dtype, lens):
+    x = Pool(lens, hq, hkv, d, dtype, seed=len(lens), maxb=8)
+    x.check(x.decode(pa))
+    assert pa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d,dtype", [(4, 1, 128, "bf16"), (8, 1, 64, "f16")])
+def test_decode_one_long_sequence(pa, hq, hkv, d, dtype):
+    x = Pool([20011], hq, hkv, d, dtype, seed=5)             # cut across every worker
+    x.check(x.decode(pa))
+
+
+def test_decode_large_batch(pa):
+    # more sequences than the decode keeps in shared memory
+    rng = np.random.default_rng(4)
+    lens = rng.integers(0, 40, 2300).tolist()
+    x = Pool(lens, 4, 2, 64, "f16", seed=6)
+    x.check(x.decode(pa), only=list(range(0, 2300, 97)) + [2299])
+    zero = torch.tensor([i for i, n in enumerate(lens) if n == 0]).cuda()
+    assert bool((x.out[zero] == 0).all())
+    assert pa.get_device_error() == 0
+
+
+def test_decode_empty_batch_and_all_empty(pa):
+    x = Pool([0, 0, 0], 8, 2, 128, "f16")
+    x.check(x.decode(pa))
+    e = Pool([4], 8, 2, 128, "f16")
+    pa.diff_decode(e.out[:0], e.q[:0], e.k, e.v, e.tables[:0], e.lens[:0], e.lam, 1.0)
+    assert bool((e.out == 7).all())
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (12, 2, 64)])
+def test_zero_lambda_is_plain_attention_of_the_first_map(pa, hq, hkv, d):
+    x = Pool([40, 300, 7], hq, hkv, d, "f16", norm=False, out_scale=1.0)
+    x.lam.zero_()
+    got = x.decode(pa).clone()
+    q = x.q.clone()
+    q[..., d // 2:] = 0
+    out = torch.empty_like(got)
+    pa.decode(out, q, x.k, x.v, x.tables, x.lens, x.scale)
+    # both are within half a step (and the weights' rounding) of the same value
+    assert float((got.float() - out.float()).abs().max()) <= 4e-3
+    # equal maps and a factor of one leave nothing, so the norm sees zeros
+    x.k[..., d // 2:] = x.k[..., :d // 2]
+    x.q[..., d // 2:] = x.q[..., :d // 2]
+    x.lam.fill_(1.0)
+    x.w = torch.ones(d, dtype=torch.float16, device="cuda")
+    out = x.decode(pa)
+    # y is at most 2 * 2^-19 of the values, |v| < 6; divided by sqrt(EPS)
+    assert float(out.abs().max()) <= x.out_scale * 2 * 2.0 ** -19 * 6 / math.sqrt(EPS)
+
+
+@pytest.mark.parametrize("kind", ["decode", "prefill"])
+def test_large_scores_and_growing_maxima(pa, kind):
+    # scores of about a hundred, the maximum rising along the sequence
+    lens = [500, 131]
+    x = Pool(lens, 8, 2, 128, "bf16", chunks=None if kind == "decode" else [70, 131], gain=8.0)
+    for s, n in enumerate(lens):
+        for t in range(n):
+            b = int(x.tables_h[s, t // 16])
+            x.k_h[b, :, t % 16] *= 0.2 + 3.0 * t / n
+    x.k.copy_(x.k_h)
+    x.check(x.decode(pa) if kind == "decode" else x.prefill(pa))
+
+
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("hq,hkv,d,dtype", [
+    (2, 2, 64, "f16"), (4, 4, 128, "bf16"), (8, 2, 128, "f16"), (6, 2, 64, "bf16"),
+    (10, 2, 128, "bf16"), (7, 1, 64, "f16"), (16, 1, 128, "bf16")])
+@pytest.mark.parametrize("plan", [True, False])
+def test_prefill_ragged(pa, hq, hkv, d, dtype, norm, plan):
+    lens = [1, 16, 70, 300, 129, 128, 517, 40]
+    chunks = [1, 16, 3, 140, 129, 128, 1, 0]
+    x = Pool(lens, hq, hkv, d, dtype, chunks=chunks, norm=norm, seed=hq)
+    x.check(x.prefill(pa, workspace="auto" if plan else None))
+    assert pa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d,dtype", [(8, 2, 128, "bf16"), (4, 4, 64, "f16")])
+def test_prefill_longer(pa, hq, hkv, d, dtype):
+    x = Pool([2000, 900], hq, hkv, d, dtype, chunks=[333, 900], seed=3)
+    x.check(x.prefill(pa))
+
+
+def test_prefill_rows_outside_chunks_stay(pa):
+    x = Pool([50, 20], 8, 2, 64, "f16", chunks=[30, 20])
+    x.prefill(pa)
+    keep = x.out.clone()
+    # two padding sequences without rows, and a longest chunk that none reaches
+    x.lens = torch.cat([x.lens, torch.zeros(2, dtype=torch.int32, device="cuda")])
+    x.start = torch.cat([x.start, x.start[-1:].repeat(2)])
+    x.tables = torch.cat([x.tables, torch.full_like(x.tables, -1)])
+    x.out.fill_(7.0)
+    x.prefill(pa, longest=200)
+    assert torch.equal(x.out, keep) and pa.get_device_error() == 0
+
+
+def test_prefill_of_one_row_is_a_decode(pa):
+    x = Pool([77, 300, 16], 8, 2, 128, "bf16", chunks=[1, 1, 1], seed=9)
+    x.check(x.prefill(pa))
+    x.chunks = None
+    x.check(x.decode(pa))
+
+
+@pytest.mark.parametrize("kind", ["decode", "prefill"])
+def test_bad_tables_and_lengths_are_reported(pa, kind):
+    x = Pool([40, 60, 33], 8, 2, 128, "f16", chunks=None if kind == "decode" else [10, 60, 33])
+    run = x.decode if kind == "decode" else x.prefill
+    x.k.nan_to_num_(0.0)
+    x.v.nan_to_num_(0.0)
+    good = run(pa).clone()
+    r0, pos = x.rows(1)
+    keep = torch.ones(good.shape[0], dtype=torch.bool, device="cuda")
+    keep[r0:r0 + len(pos)] = False
+    for value in (x.k.shape[0], -3, 2 ** 31 - 1):
+        x.tables[1, 2] = value
+        out = run(pa).clone()
+        assert pa.get_device_error() == pa.DEVERR["TABLE_RANGE"]
+        assert torch.equal(out[keep], good[keep])            # the others are not touched
+    x.tables.copy_(x.tables_h)
+    for value in (-1, 16 * x.tables.shape[1] + 1):
+        x.lens[1] = value
+        out = run(pa).clone()
+        assert pa.get_device_error() & pa.DEVERR["SEQLEN_RANGE"]
+        assert torch.equal(out[keep], good[keep])
+
+
+@pytest.mark.parametrize("kind", ["decode", "prefill"])
+def test_graph_replay_with_changing_inputs(pa, kind):
+    mk = lambda lens, seed: Pool(lens, 8, 2, 128, "bf16",  # noqa: E731
+                                 chunks=None if kind == "decode" else [9, 9, 9], seed=seed,
+                                 maxb=40)
+    x = mk([300, 20, 600], 1)
+    run = x.decode if kind == "decode" else x.prefill
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run(pa)
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(3):                                   # back to back in one graph
+            run(pa)
+    g.replay()
+    x.check(x.out[:x.q.shape[0]])
+    y = mk([17, 620, 64], 2)
+    big = torch.full((max(x.k.shape[0], y.k.shape[0]), *x.k.shape[1:]), float("nan"),
+                     dtype=x.k.dtype)
+    assert y.k.shape[0] <= x.k.shape[0]                      # it fits the captured pool
+    for a, b in ((x.k, y.k_h), (x.v, y.v_h)):
+        big[:b.shape[0]] = b
+        a.copy_(big[:a.shape[0]])
+    for a, b in ((x.q, y.q), (x.tables, y.tables), (x.lens, y.lens), (x.lam, y.lam), (x.w, y.w)):
+        a.copy_(b)
+    g.replay()
+    y.check(x.out[:x.q.shape[0]])
+    assert pa.get_device_error() == 0
+
+
+def test_two_streams_with_workspaces_of_their_own(pa):
+    xs = [Pool([900, 33, 400], 8, 2, 128, "bf16", seed=20 + i) for i in range(2)]
+    want = [x.decode(pa).clone() for x in xs]
+    torch.cuda.synchronize()
+    ss = [torch.cuda.Stream() for _ in xs]
+    for _ in range(10):
+        for x, s in zip(xs, ss):
+            x.decode(pa, stream=s)
+    torch.cuda.synchronize()
+    for x, w in zip(xs, want):
+        assert torch.equal(x.out[:3], w)                     # bit-stable too
+
+
+def test_offsets_past_32_bits(pa):
+    # a pool of more than 2^31 elements whose live blocks lie at its end
+    hkv, d = 8, 128
+    nb = (2 ** 31 // (hkv * 16 * d)) + 300
+    k = torch.zeros(nb, hkv, 16, d, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    x = Pool([100, 300], 16, hkv, d, "bf16", chunks=[20, 33], seed=30)
+    small = x.k.shape[0]
+    k[-small:], v[-small:] = x.k, x.v
+    tables = torch.where(x.tables >= 0, x.tables + (nb - small), x.tables)
+    want = x.prefill(pa).clone()
+    x.k, x.v, x.tables = k, v, tables
+    assert torch.equal(x.prefill(pa), want)
+    y = Pool([100, 300], 16, hkv, d, "bf16", seed=30)
+    want = y.decode(pa).clone()
+    k[-small:], v[-small:] = y.k, y.v
+    y.tables = torch.where(y.tables >= 0, y.tables + (nb - small), y.tables)
+    y.k, y.v = k, v
+    assert torch.equal(y.decode(pa), want)
+    assert pa.get_device_error() == 0
+
+
+def test_refusals(pa):
+    x = Pool([40, 60], 8, 2, 128, "f16")
+    ok = dict(out=x.out[:2], q=x.q, k_cache=x.k, v_cache=x.v, block_tables=x.tables,
+              seq_lens=x.lens, lam=x.lam, scale=1.0)
+    for kw in (dict(lam=x.lam[:4]), dict(lam=x.lam.half()), dict(lam=x.lam.cpu()),
+               dict(q=x.q.bfloat16()), dict(out=x.out), dict(seq_lens=x.lens.long()),
+               dict(block_tables=x.tables.long()), dict(block_tables=x.tables[:1]),
+               dict(norm_weight=torch.ones(128, device="cuda")),
+               dict(norm_weight=torch.ones(64, device="cuda", dtype=torch.float16)),
+               dict(v_cache=x.v[:, :1]), dict(q=x.q.cpu()),
+               dict(q=x.q.transpose(0, 1).contiguous().transpose(0, 1))):
+        with pytest.raises(ValueError):
+            pa.diff_decode(**{**ok, **kw})
+    for kw in (dict(eps=-1.0, norm_weight=None), dict(scale=math.nan), dict(out_scale=math.inf)):
+        with pytest.raises(pa.PagedAttnError) as e:
+            pa.diff_decode(**{**ok, **kw})
+        assert e.value.status == 1
+    need = pa.diff_decode_workspace_size(2, 8, 2, 128, x.tables.shape[1])
+    big = Pool([400, 60], 8, 2, 128, "f16")                  # wide tables: the split needs it
+    need = pa.diff_decode_workspace_size(2, 8, 2, 128, big.tables.shape[1])
+    with pytest.raises(pa.PagedAttnError) as e:
+        big.decode(pa, workspace=torch.empty(need - 256, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == 3
+    big.check(big.decode(pa, workspace=torch.empty(need, dtype=torch.uint8, device="cuda")))
+    g9 = Pool([40], 9, 1, 64, "f16")
+    with pytest.raises(pa.PagedAttnError) as e:
+        g9.decode(pa)
+    assert e.value.status == 2
+    torch.cuda.synchronize()
+    assert bool((x.out == 7).all())                          # nothing was launched
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,d", [("bf16", 8, 2, 128), ("f16", 6, 1, 64)])
+def test_serving_flow(pa, dtype, hq, hkv, d):
+    """Prompts and decode steps of a differential-attention model: rope_and_cache fills the
+    pool with both keys of a head, diff_prefill attends the chunks, a sequence is forked,
+    copy_blocks separates the samples, and rope_and_cache + diff_decode go on."""
+    g = torch.Generator().manual_seed(40)
+    dt = TORCH_DTYPE[dtype]
+    nb, maxb, scale = 96, 12, (d // 2) ** -0.5
+    kc, vc = (torch.randn(nb, hkv, 16, d, generator=g).to(dt).cuda() for _ in range(2))
+    lam = torch.rand(hq, generator=g).cuda()
+    w = (1 + 0.2 * torch.randn(d, generator=g)).to(dt).cuda()
+    qn, kn = ((1.4 + 0.1 * torch.randn(d // 2, generator=g)).to(dt).cuda() for _ in range(2))
+    ang = torch.arange(400).double()[:, None] * 10000.0 ** (-torch.arange(0, d // 2, 2) / (d / 2))
+    cs = torch.cat([ang.cos(), ang.sin()], 1).float().cuda()
+    bm = BlockManager(nb)
+
+    def step(sids, chunks):
+        """One engine step over the sequences' next tokens; checks every row."""
+        slots, pairs, pos = [], [], []
+        for s, c in zip(sids, chunks):
+            before = bm.block_table(s, maxb)[2]
+            sl, cow = bm.append(s, c)
+            slots += sl.tolist()
+            pos += list(range(before, before + c))
+            if cow:
+                pairs.append(cow)
+        if pairs:
+            pa.copy_blocks(kc, vc, torch.tensor(pairs).cuda())
+        t = len(slots)
+        qkv = torch.randn(t, (hq + 2 * hkv) * d, generator=g).to(dt).cuda()
+        q, k, v = (a.view(t, -1, d) for a in qkv.split([hq * d, hkv * d, hkv * d], 1))
+        qo = torch.empty(t, hq, d, dtype=dt, device="cuda")
+        pa.rope_and_cache(qo, q, k, v, kc, vc, torch.tensor(slots).cuda(),
+                          torch.tensor(pos).int().cuda(), cs, q_norm=qn, k_norm=kn, eps=EPS,
+                          num_maps=2)
+        tables = torch.from_numpy(np.stack([bm.block_table(s, maxb)[0] for s in sids]))
+        lens = [bm.block_table(s, maxb)[2] for s in sids]
+        out = torch.full((t, hq, d), float("nan"), dtype=dt, device="cuda")
+        args = (out, qo, kc, vc, tables.cuda(), torch.tensor(lens).int().cuda())
+        decode = chunks == [1] * len(sids)
+        if decode:
+            pa.diff_decode(*args, lam, scale, norm_weight=w, eps=EPS, out_scale=0.3)
+        else:
+            start = torch.tensor([0] + np.cumsum(chunks).tolist()).int().cuda()
+            pa.diff_prefill(*args, start, max(chunks), lam, scale, norm_weight=w, eps=EPS,
+                            out_scale=0.3)
+        assert pa.get_device_error() == 0
+        row = 0
+        for i, (s, c) in enumerate(zip(sids, chunks)):
+            p = list(range(lens[i] - c, lens[i]))
+            ref, tol = reference(qo[row:row + c].cpu(), kc.cpu(), vc.cpu(), tables, i, p, lam.cpu(),
+                                 scale, w.cpu(), EPS, 0.3,
+                                 (P_DECODE if decode else P_PREFILL)[dtype])
+            assert_close(out[row:row + c], ref, tol, f"sequence {s}")
+            row += c
+
+    for s in (1, 2, 3):
+        bm.add_sequence(s)
+    step([1, 2, 3], [60, 17, 1])
+    step([1, 2], [43, 30])
+    bm.fork(1, 4)                                            # 103 tokens: a shared, part-filled block
+    for _ in range(3):
+        step([1, 4, 2, 3], [1, 1, 1, 1])
+    step([3, 4], [33, 2])

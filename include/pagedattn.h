@@ -406,8 +406,8 @@ int pa_reshape_and_cache(const void *k_new, const void *v_new,
  *   q_norm, k_norm [head_dim / num_maps] dtype, or NULL
  *   num_maps  1 or 2; rotary_dim a multiple of 16, 16..head_dim / num_maps
  *   eps       finite, >= 0
- * A token with a negative slot or position is padding: nothing of it is read
- * or written, its q_out row stays as it was.  A position >= max_position sets
+ * A token with a negative slot or position is padding: nothing of it is
+ * written, its q_out row stays as it was.  A position >= max_position sets
  * PA_DEVERR_POSITION_RANGE, a slot >= num_blocks*16 PA_DEVERR_SLOT_RANGE; both
  * skip the token whole.  Two tokens naming the same slot race.  The kernel is
  * a programmatic dependent launch, as the decode's are.

@@ -324,33 +324,25 @@ def prefill(out, q, k_cache, v_cache, block_tables, seq_lens, query_start, max_q
     return out
 
 
-def _diff_args(out, q, k_cache, v_cache, block_tables, seq_lens, lam, norm_weight, workspace):
-    """Checks what diff_decode and diff_prefill share; the workspace's bytes."""
+def _diff_pointers(out, q, k_cache, v_cache, block_tables, seq_lens, lam, norm_weight):
+    """Checks what diff_decode and diff_prefill share; the device and the addresses."""
     torch = _torch()
-    hq, d = q.shape[1:]
-    n, dt, dev = seq_lens.shape[0], q.dtype, q.get_device()
-    _require(dev >= 0 and dev == torch.cuda.current_device(),
-             "tensors must be on the current CUDA device")
-    _require(out.shape == q.shape and k_cache.shape[3] == d and v_cache.shape == k_cache.shape,
-             "shapes")
-    _require(out.dtype == dt and k_cache.dtype == dt and v_cache.dtype == dt,
-             "out and the pools: q's dtype")
-    _require(block_tables.dim() == 2 and block_tables.shape[0] == n and seq_lens.dim() == 1,
-             "table shapes")
-    _require(block_tables.dtype == torch.int32 and seq_lens.dtype == torch.int32, "tables: int32")
-    _require(lam.shape == (hq,) and lam.dtype == torch.float32, "lam: float32 [num_heads]")
-    for t in (out, q, k_cache, v_cache, block_tables, seq_lens, lam):
-        _require(t.get_device() == dev and t.is_contiguous(),
-                 "tensors must be contiguous, on the current CUDA device")
-    if norm_weight is not None:
-        _require(norm_weight.shape == (d,) and norm_weight.dtype == dt and
-                 norm_weight.is_contiguous() and norm_weight.get_device() == dev,
-                 "norm_weight: [head_dim] of q's dtype")
-    if workspace is None:
-        return 0
-    _require(workspace.get_device() == dev and workspace.is_contiguous(),
-             "workspace: contiguous, on the current CUDA device")
-    return workspace.numel() * workspace.element_size()
+    i32 = torch.int32
+    shape, pool, tables = q.shape, k_cache.shape, block_tables.shape
+    dt, dev = q.dtype, _current(q)
+    if (out.shape != shape or pool[3] != shape[2] or v_cache.shape != pool or len(tables) != 2 or
+            seq_lens.shape != tables[:1] or lam.shape != shape[1:2]):
+        raise ValueError("shapes")
+    return dev, (_near(out, dt, dev), _near(q, dt, dev), _near(k_cache, dt, dev),
+                 _near(v_cache, dt, dev), _near(block_tables, i32, dev),
+                 _near(seq_lens, i32, dev)), (_near(lam, torch.float32, dev),
+                                              _weights(norm_weight, shape[2], dt, dev))
+
+
+def _bytes_of(workspace, dev):
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: contiguous, on the current CUDA device")
+    return workspace.nbytes
 
 
 def diff_decode_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim,
@@ -376,18 +368,19 @@ def diff_decode(out, q, k_cache, v_cache, block_tables, seq_lens, lam, scale, no
     RMS-normalised over the head, and it is multiplied by out_scale either way.
     """
     n, hq, d = q.shape
-    _require(seq_lens.shape == (n,), "table shapes")
+    nb, hkv, bs, _ = k_cache.shape
+    if seq_lens.shape != (n,):
+        raise ValueError("shapes")
+    dev, at, factors = _diff_pointers(out, q, k_cache, v_cache, block_tables, seq_lens, lam,
+                                      norm_weight)
     if workspace is None:
         workspace = diff_decode_workspace_for(q, k_cache, block_tables, stream)
-    wbytes = _diff_args(out, q, k_cache, v_cache, block_tables, seq_lens, lam, norm_weight,
-                        workspace)
-    nb, hkv, bs, _ = k_cache.shape
-    rc = load().pa_diff_decode(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                               _ptr(block_tables), _ptr(seq_lens), _ptr(lam), _ptr(norm_weight), n,
-                               hq, hkv, d, bs, block_tables.shape[1], nb, float(scale), float(eps),
-                               float(out_scale), _dtype_code(q), _ptr(workspace), wbytes,
-                               _stream(stream))
-    _check("pa_diff_decode", rc)
+    wptr, wbytes = ((None, 0) if workspace is None else
+                    (workspace.data_ptr(), _bytes_of(workspace, dev)))
+    rc = load().pa_diff_decode(*at, *factors, n, hq, hkv, d, bs, block_tables.shape[1], nb, float(scale),
+                               float(eps), float(out_scale), _dtype_code(q), wptr, wbytes, _stream(stream))
+    if rc:
+        raise PagedAttnError("pa_diff_decode", rc)
     return out
 
 
@@ -411,22 +404,21 @@ def diff_prefill(out, q, k_cache, v_cache, block_tables, seq_lens, query_start, 
     norm_weight, eps and out_scale as diff_decode.
     """
     t, hq, d = q.shape
-    n = seq_lens.shape[0]
-    _require(query_start.shape == (n + 1,) and query_start.dtype == _torch().int32 and
-             query_start.get_device() == q.get_device() and query_start.is_contiguous(),
-             "query_start: int32 [num_seqs + 1]")
-    if isinstance(workspace, str):
-        workspace = diff_prefill_workspace_for(q, k_cache, seq_lens, max_query_len, stream)
-    wbytes = _diff_args(out, q, k_cache, v_cache, block_tables, seq_lens, lam, norm_weight,
-                        workspace)
     nb, hkv, bs, _ = k_cache.shape
-    rc = load().pa_diff_prefill(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                _ptr(block_tables), _ptr(seq_lens), _ptr(query_start), _ptr(lam),
-                                _ptr(norm_weight), n, int(max_query_len), hq, hkv, d, bs,
-                                block_tables.shape[1], nb, float(scale), float(eps),
-                                float(out_scale), _dtype_code(q), _ptr(workspace), wbytes,
-                                _stream(stream))
-    _check("pa_diff_prefill", rc)
+    n, longest = seq_lens.shape[0], int(max_query_len)
+    if query_start.shape != (n + 1,):
+        raise ValueError("shapes")
+    dev, at, factors = _diff_pointers(out, q, k_cache, v_cache, block_tables, seq_lens, lam,
+                                      norm_weight)
+    if isinstance(workspace, str):
+        workspace = diff_prefill_workspace_for(q, k_cache, seq_lens, longest, stream)
+    wptr, wbytes = ((None, 0) if workspace is None else
+                    (workspace.data_ptr(), _bytes_of(workspace, dev)))
+    rc = load().pa_diff_prefill(*at, _near(query_start, _torch().int32, dev), *factors, n, longest,
+                                hq, hkv, d, bs, block_tables.shape[1], nb, float(scale), float(eps), float(out_scale),
+                                _dtype_code(q), wptr, wbytes, _stream(stream))
+    if rc:
+        raise PagedAttnError("pa_diff_prefill", rc)
     return out
 
 
@@ -462,36 +454,43 @@ def reshape_and_cache(k_new, v_new, k_cache, v_cache, slot_mapping, stream=None)
     _check("pa_reshape_and_cache", rc)
 
 
-def _rows(t, dtype, device):
+_NEAR = "tensors must be contiguous, of the right type and on the current CUDA device"
+
+
+def _rows(t, shape, dtype, device):
     """Elements between the tokens of [tokens, heads, head_dim] rows whose heads lie
     one after the other (any distance between tokens: slices of a projection's output)."""
-    n, h, d = t.shape
+    n, h, d = shape
     st, sh, se = t.stride()
-    _require(t.dtype == dtype and t.get_device() == device, "rows: dtype or device")
-    _require((se == 1 or d == 1) and (sh == d or h == 1), "rows: a token's heads must be contiguous")
+    if (t.shape != shape or t.dtype is not dtype or t.get_device() != device or se != 1 or
+            (sh != d and h != 1)):
+        raise ValueError(f"rows: {tuple(shape)} of {dtype} on device {device}, a token's heads "
+                         "one after the other")
     return st if n > 1 else h * d
 
 
-def _rope_args(q_out, q, k, positions, cos_sin, q_norm, k_norm, num_maps):
-    """Checks what rope_and_cache and qk_norm_rope share; (device, dtype)."""
-    torch = _torch()
-    n, hq, d = q.shape
-    dt, dev = q.dtype, q.get_device()
-    _require(dev >= 0 and dev == torch.cuda.current_device(),
-             "tensors must be on the current CUDA device")
-    _require(k.dim() == 3 and k.shape[0] == n and k.shape[2] == d and q_out.shape == q.shape,
-             "shapes")
-    _require(positions.shape == (n,) and positions.dtype == torch.int32, "positions: int32 [tokens]")
-    _require(cos_sin.dim() == 2 and cos_sin.dtype == torch.float32, "cos_sin: float32 [positions, "
-             "rotary_dim]")
-    for t in (positions, cos_sin):
-        _require(t.get_device() == dev and t.is_contiguous(),
-                 "tensors must be contiguous, on the current CUDA device")
-    for w in (q_norm, k_norm):
-        if w is not None:
-            _require(w.numel() * num_maps == d and w.dtype == dt and w.is_contiguous() and
-                     w.get_device() == dev, "norm weights: [head_dim / num_maps] of q's dtype")
-    return dev, dt
+def _near(t, dtype, device):
+    """The address of a contiguous tensor of this type on this device."""
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(_NEAR)
+    return t.data_ptr()
+
+
+def _current(t):
+    """The device of t, which has to be the current one."""
+    dev = t.get_device()
+    if dev < 0 or dev != _torch()._C._cuda_getDevice():
+        raise ValueError("tensors must be on the current CUDA device")
+    return dev
+
+
+def _weights(w, size, dtype, device):
+    """The address of optional norm weights [size]."""
+    if w is None:
+        return None
+    if w.shape != (size,):
+        raise ValueError(f"norm weights: [{size}]")
+    return _near(w, dtype, device)
 
 
 def rope_and_cache(q_out, q, k_new, v_new, k_cache, v_cache, slot_mapping, positions, cos_sin,
@@ -508,24 +507,25 @@ def rope_and_cache(q_out, q, k_new, v_new, k_cache, v_cache, slot_mapping, posit
         cos_sin = torch.cat([a.cos(), a.sin()], 1).float()
     num_maps=2 treats a head as two keys of half its size (differential attention).
     """
-    n, hq, d = q.shape
-    nb, hkv, bs, d2 = k_cache.shape
-    dev, dt = _rope_args(q_out, q, k_new, positions, cos_sin, q_norm, k_norm, num_maps)
-    _require(d2 == d and v_cache.shape == k_cache.shape and k_new.shape[1] == hkv and
-             v_new.shape == k_new.shape, "shapes")
-    _require(slot_mapping.shape == (n,) and slot_mapping.dtype == _torch().int64,
-             "slot_mapping: int64 [tokens]")
-    for t in (k_cache, v_cache, slot_mapping):
-        _require(t.get_device() == dev and t.is_contiguous(),
-                 "tensors must be contiguous, on the current CUDA device")
-    _require(k_cache.dtype == dt and v_cache.dtype == dt, "pools: q's dtype")
+    torch = _torch()
+    n, hq, d = q_shape = q.shape
+    nb, hkv, bs, d2 = pool = k_cache.shape
+    table, rot = cos_sin.shape
+    new = (n, hkv, d)
+    dt, dev, num_maps = q.dtype, _current(q), int(num_maps)
+    seg = d // num_maps if num_maps > 0 else 0
+    if d2 != d or v_cache.shape != pool or positions.shape != (n,) or slot_mapping.shape != (n,):
+        raise ValueError("shapes")
     rc = load().pa_rope_and_cache(
-        _ptr(q_out), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
-        _ptr(slot_mapping), _ptr(positions), _ptr(cos_sin), _ptr(q_norm), _ptr(k_norm), n, hq, hkv,
-        d, int(num_maps), bs, nb, cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0,
-        float(eps), _rows(q, dt, dev), _rows(k_new, dt, dev), _rows(v_new, dt, dev),
-        _rows(q_out, dt, dev), _dtype_code(q), _stream(stream))
-    _check("pa_rope_and_cache", rc)
+        q_out.data_ptr(), q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+        _near(k_cache, dt, dev), _near(v_cache, dt, dev), _near(slot_mapping, torch.int64, dev),
+        _near(positions, torch.int32, dev), _near(cos_sin, torch.float32, dev),
+        _weights(q_norm, seg, dt, dev), _weights(k_norm, seg, dt, dev), n, hq, hkv, d, num_maps,
+        bs, nb, table, rot, 1 if interleaved else 0, float(eps), _rows(q, q_shape, dt, dev),
+        _rows(k_new, new, dt, dev), _rows(v_new, new, dt, dev), _rows(q_out, q_shape, dt, dev),
+        _dtype_code(q), _stream(stream))
+    if rc:
+        raise PagedAttnError("pa_rope_and_cache", rc)
     return q_out
 
 
@@ -534,15 +534,24 @@ def qk_norm_rope(q_out, k_out, q, k, positions, cos_sin, q_norm=None, k_norm=Non
     """pa_qk_norm_rope: rope_and_cache's normalisation and rotation without the pool, for
     decode_append and decode_shared_prefix, which write the new tokens themselves.
     q_out may be q and k_out may be k."""
-    n, hq, d = q.shape
-    dev, dt = _rope_args(q_out, q, k, positions, cos_sin, q_norm, k_norm, num_maps)
-    _require(k_out.shape == k.shape, "shapes")
+    torch = _torch()
+    n, hq, d = q_shape = q.shape
+    hkv = k.shape[1]
+    table, rot = cos_sin.shape
+    new = (n, hkv, d)
+    dt, dev, num_maps = q.dtype, _current(q), int(num_maps)
+    seg = d // num_maps if num_maps > 0 else 0
+    if positions.shape != (n,):
+        raise ValueError("shapes")
     rc = load().pa_qk_norm_rope(
-        _ptr(q_out), _ptr(k_out), _ptr(q), _ptr(k), _ptr(positions), _ptr(cos_sin), _ptr(q_norm),
-        _ptr(k_norm), n, hq, k.shape[1], d, int(num_maps), cos_sin.shape[0], cos_sin.shape[1],
-        1 if interleaved else 0, float(eps), _rows(q, dt, dev), _rows(k, dt, dev),
-        _rows(q_out, dt, dev), _rows(k_out, dt, dev), _dtype_code(q), _stream(stream))
-    _check("pa_qk_norm_rope", rc)
+        q_out.data_ptr(), k_out.data_ptr(), q.data_ptr(), k.data_ptr(),
+        _near(positions, torch.int32, dev), _near(cos_sin, torch.float32, dev),
+        _weights(q_norm, seg, dt, dev), _weights(k_norm, seg, dt, dev), n, hq, hkv, d, num_maps,
+        table, rot, 1 if interleaved else 0, float(eps), _rows(q, q_shape, dt, dev),
+        _rows(k, new, dt, dev), _rows(q_out, q_shape, dt, dev), _rows(k_out, new, dt, dev),
+        _dtype_code(q), _stream(stream))
+    if rc:
+        raise PagedAttnError("pa_qk_norm_rope", rc)
     return q_out, k_out
 
 

@@ -1158,7 +1158,7 @@ static int rope_impl(RopeParams &p, bool pool, int num_heads, int head_dim, int 
         (p.k_out && p.k_out == p.k && p.k_out_stride != p.k_stride && p.num_tokens > 1))
         return PA_ERR_INVALID_ARG;
     const long long segs = (long long)(num_heads + (pool ? 2 : 1) * (long long)hkv) * p.num_maps;
-    if (segs * seg >= (1LL << 31))
+    if (segs * seg * kBlockSize >= (1LL << 31))        // offsets within a token's rows: 32 bits
         return PA_ERR_UNSUPPORTED;
     p.q_segs = num_heads * p.num_maps;
     p.k_segs = hkv * p.num_maps;
@@ -1172,8 +1172,17 @@ static int rope_impl(RopeParams &p, bool pool, int num_heads, int head_dim, int 
                                      ds->num_sms);
     if (!k.fn)
         return PA_ERR_UNSUPPORTED;
-    void *args[] = {&p};
-    return launch_dependent(k.fn, dim3((unsigned)k.blocks), dim3(k.threads), 0,
+    if (k.smem) {
+        int dev = 0;
+        cudaGetDevice(&dev);
+        const int rs = ensure_smem(k.fn, dev, k.smem);
+        if (rs != PA_OK)
+            return rs;
+    }
+    int iters = k.iters;
+    RopeSplit split = k.split;
+    void *args[] = {&p, &iters, &split};   // a kernel without a split takes the first two
+    return launch_dependent(k.fn, dim3((unsigned)k.blocks), dim3(k.threads), k.smem,
                             static_cast<cudaStream_t>(stream), args);
 }
 

@@ -27,9 +27,20 @@ struct RopeParams {
     float eps;
 };
 
+// How many units are handed out: the first long_blocks blocks share the first
+// long_units evenly, the blocks after them take short_units each.
+struct RopeSplit {
+    unsigned long_blocks, long_units, short_units;
+};
+
+// A launch with arguments (RopeParams, int iters, and for the kernel with
+// dynamic shared memory RopeSplit).
 struct RopeKernel {
     const void *fn;
     int threads, blocks;
+    size_t smem;                   // dynamic shared memory a block
+    int iters;                     // rounds of segments in a unit of work
+    RopeSplit split;
 };
 
 // The kernel and its grid for one call; fn is null if the call has more units

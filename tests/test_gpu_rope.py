@@ -144,6 +144,38 @@ def test_qk_norm_rope(pa, t, hq, hkv, d, dtype, maps, rot, norm, fused, inter, i
     assert pa.get_device_error() == 0
 
 
+# Enough tokens for the kernel that copies rows through shared memory: with a
+# few units of work a warp, and with so many that the last are handed out apart.
+@pytest.mark.parametrize("t,hq,hkv,d,dtype,maps,rot,norm,fused,inter", [
+    (5003, 32, 8, 128, "bf16", 1, 128, "qk", True, False),
+    (7001, 10, 2, 128, "f16", 1, 96, "k", False, True),
+    (11003, 6, 3, 64, "bf16", 2, 16, "qk", True, False),
+    (13001, 9, 3, 64, "f16", 1, 64, "", False, True),
+    (80111, 1, 1, 64, "f16", 1, 48, "q", True, False),
+    (81001, 1, 1, 128, "bf16", 2, 64, "qk", False, True)])
+def test_append_many(pa, t, hq, hkv, d, dtype, maps, rot, norm, fused, inter):
+    x = Tokens(t, hq, hkv, d, dtype, maps, rot, norm, fused, seed=t)
+    skipped = [0, 1, 17, t // 2, t - 1]
+    x.slots[0], x.slots[17], x.pos[t // 2] = -1, -7, -1
+    x.pos[1], x.slots[t - 1] = 300, x.nb * 16               # outside the table, the pool
+    x.check(pa, lambda: x.append(pa, inter), inter, skipped=skipped)
+    assert pa.get_device_error() == pa.DEVERR["POSITION_RANGE"] | pa.DEVERR["SLOT_RANGE"]
+
+
+@pytest.mark.parametrize("t,hq,hkv,d,dtype,inter", [(9001, 12, 4, 64, "f16", False),
+                                                    (4001, 32, 8, 128, "bf16", True)])
+def test_qk_norm_rope_many_in_place(pa, t, hq, hkv, d, dtype, inter):
+    x = Tokens(t, hq, hkv, d, dtype, seed=t, fused=True, pool=False)
+    rq, mq = reference(x.q, x.qw, x.cs, x.pos, 1, inter)
+    rk, mk = reference(x.k, x.kw, x.cs, x.pos, 1, inter)
+    v = x.v.clone()
+    pa.qk_norm_rope(x.q, x.k, x.q, x.k, x.pos, x.cs, q_norm=x.qw, k_norm=x.kw, eps=EPS,
+                    interleaved=inter)
+    close(x.q, rq, mq, "q")
+    close(x.k, rk, mk, "k")
+    assert torch.equal(x.v, v) and pa.get_device_error() == 0
+
+
 def test_padding_and_bad_entries_are_skipped(pa):
     x = Tokens(40, 8, 2, 128, "bf16", seed=3, fused=True)
     x.slots[4] = -1
@@ -195,10 +227,10 @@ def test_far_positions(pa):
 
 def test_bit_stable_over_batches(pa):
     # a token's result does not depend on the tokens beside it, or on their number
-    big = Tokens(700, 12, 4, 128, "bf16", seed=7)
+    big = Tokens(12000, 12, 4, 128, "bf16", seed=7)
     big.append(pa)
-    for n in (1, 3, 64):
-        out = torch.empty_like(big.q_out[:n])
+    for n in (1, 3, 64, 700):
+        out = torch.full_like(big.q_out[:n], 7.0)
         kc, vc = big.kc.clone(), big.vc.clone()
         pa.rope_and_cache(out, big.q[:n], big.k[:n], big.v[:n], kc, vc, big.slots[:n],
                           big.pos[:n], big.cs, q_norm=big.qw, k_norm=big.kw, eps=EPS)

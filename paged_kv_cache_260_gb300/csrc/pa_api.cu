@@ -933,8 +933,7 @@ size_t pa_prefill_workspace_size(int num_seqs, int max_query_len, int num_heads,
 size_t pa_diff_prefill_workspace_size(int num_seqs, int max_query_len, int num_heads,
                                       int num_kv_heads)
 {
-    return prefill_workspace_bytes(num_seqs,
-                                   prefill_q_ranks(max_query_len, num_heads, num_kv_heads, 1));
+    return pa_prefill_workspace_size(num_seqs, max_query_len, num_heads, num_kv_heads);
 }
 
 // What a differential prefill does beyond pa_prefill (lambda non-null).
@@ -952,7 +951,6 @@ static int prefill_impl(void *out, const void *q, const void *k_cache, const voi
                         size_t workspace_bytes, void *stream, const PrefillExtra &x)
 {
     const bool diff = x.lambda != nullptr;
-    const int tiles = diff ? 1 : kPrefillTiles;
     int rc = check_common(num_kv_heads, head_dim, block_size, num_blocks, dtype);
     if (rc != PA_OK)
         return rc;
@@ -970,8 +968,11 @@ static int prefill_impl(void *out, const void *q, const void *k_cache, const voi
         !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(query_start, 4))
         return PA_ERR_INVALID_ARG;
     const long long pool_rows = (long long)num_blocks * num_kv_heads * kBlockSize;
+    // differential: a unit is two blocks' query tiles, unless every chunk fits one
+    const bool pairs = diff && max_query_len > kPrefillRows / group;
+    const int tiles = diff && !pairs ? 1 : kPrefillTiles;
     const long long q_ranks = prefill_q_ranks(max_query_len, num_heads, num_kv_heads, tiles);
-    const long long grid = q_ranks * num_seqs * num_kv_heads;
+    const long long grid = q_ranks * num_seqs * num_kv_heads * (pairs ? 2 : 1);
     if ((long long)max_blocks_per_seq * kBlockSize >= (1LL << 30) || pool_rows >= (1LL << 31) ||
         grid >= (1LL << 31))
         return PA_ERR_UNSUPPORTED;
@@ -985,7 +986,7 @@ static int prefill_impl(void *out, const void *q, const void *k_cache, const voi
             return PA_ERR_WORKSPACE;
     }
     PrefillKernel kk{};
-    if (!(diff ? diff_prefill_kernel(dtype, head_dim, &kk) : prefill_kernel(dtype, head_dim, &kk)))
+    if (!(diff ? diff_prefill_kernel(dtype, head_dim, pairs, &kk) : prefill_kernel(dtype, head_dim, &kk)))
         return PA_ERR_UNSUPPORTED;
     DeviceState *ds;
     rc = device_state(&ds);

@@ -1,0 +1,691 @@
+// pa_diff_prefill.cu -- chunked prefill of differential attention on the
+// fifth-generation tensor cores (tcgen05), over the paged pool.
+//
+// A head's q row and a token's key row hold two queries and two keys of
+// head_dim / 2 channels side by side (map 0, map 1); the values are shared:
+//     y = sum_t softmax_t(scale q0.k0_t) v_t - lambda sum_t softmax_t(scale q1.k1_t) v_t
+// over the positions a row sees, then an optional RMS norm over head_dim.
+//
+// One thread block (one per SM) computes 128 rows = (token, q head) pairs of
+// one sequence and kv head.  The two maps run side by side on the same Q, K and
+// V tiles: per key tile j (BN keys) and map g
+//     S_g,j = Q[:, g] . K_j[:, g]^T     (M 128, N BN, K = head_dim / 2)
+//     O_g  += P_g,j . V_j               (M 128, N head_dim, K BN)
+// so K and V are staged once for both, and O_0, O_1 end up in the same TMEM
+// lanes, where the difference is taken.
+//
+// Warp roles (384 threads):
+//   warp 0     TMA producer: K tiles and V tiles through a ring each, K one tile
+//              ahead;
+//   warps 1-2  issue the MMAs of map 0 and 1 (warp 1 owns the TMEM; the whole warp
+//              runs the loop, one elected lane issues);
+//   warp 3     warms L2 with the query rows of the block one wave later;
+//   warps 4-7 map 0, 8-11 map 1: load the Q tile, then one thread per row (its
+//              TMEM lane): scores from TMEM, causal mask, online softmax in base
+//              2 with a lazy rescale of O (only when the running maximum grows
+//              by more than 2^8), P into TMEM, rounded to the operand type (the
+//              row sum takes the unrounded weights); at the end each map forms
+//              the difference of half of the row's channels.
+// TMEM (512 columns), map g from 256 g: S in BN columns, P packed two keys a
+// column in BN / 2, O in head_dim columns.
+// Every wait is bounded; a wait that gives up records PA_DEVERR_TIMEOUT and
+// the block drains its copies and MMAs before it frees TMEM and exits.
+#include <cuda.h>
+#include <type_traits>
+
+#include "pa_device.cuh"
+#include "pa_prefill_abi.h"
+#include "pa_prefill_plan.cuh"
+#include "pa_tcgen05.cuh"
+
+namespace pa {
+
+namespace {
+
+template <int D>
+struct DiffShape {
+    static constexpr int BM = kPrefillRows;                 // rows of the block
+    static constexpr int BN = kPrefillKeys;                 // keys per tile
+    static constexpr int NB = BN / kBlockSize;              // pool blocks per tile
+    static constexpr int HALVES = D / 64;                   // 128-byte column boxes
+    static constexpr int BOX = 2048;                        // 16 rows x 128 B
+    static constexpr int Q_BYTES = BM * D * 2;              // [half][128 rows][128 B]
+    static constexpr int SLOT_BYTES = BN * D * 2;           // [half][NB blocks][16 rows][128 B]
+    static constexpr int NSLOT = D == 128 ? 3 : 6;          // K slots, and V slots
+    static constexpr int OFF_K = Q_BYTES;
+    static constexpr int OFF_V = OFF_K + NSLOT * SLOT_BYTES;
+    static constexpr int OFF_X = OFF_V + NSLOT * SLOT_BYTES;   // the maps' exchange: [4][128] fp32
+    static constexpr int DATA = OFF_X + 4 * BM * 4;
+    // kfull, kempty, vfull, vempty [NSLOT]; s, read, o, p low, p high, drain [2];
+    // q, z; then the TMEM base and the abort flag
+    static constexpr int NBAR = 4 * NSLOT + 12 + 2;
+    static constexpr int BAR_BYTES = NBAR * 8 + 8;
+    // The operands are aligned up to 1024 bytes inside the dynamic allocation;
+    // the barriers sit in whichever end of the 1024-byte slack has room.
+    static constexpr int SMEM = DATA + 1024;
+    static constexpr int THREADS = 384;
+    static constexpr uint32_t TMEM_COLS = 512;
+    static constexpr uint32_t MAP_COLS = 256;
+    static constexpr uint32_t COL_O = 128;
+    static constexpr bool SEPARATE_P = COL_O + D + BN / 2 <= MAP_COLS;
+    static constexpr uint32_t COL_P = SEPARATE_P ? COL_O + D : 0;
+    static_assert(D == 64 || D == 128, "head_dim");
+    static_assert(OFF_K % 1024 == 0 && SLOT_BYTES % 2048 == 0, "swizzle atoms");
+    static_assert(BAR_BYTES <= 512, "barriers fit either end of the slack");
+    static_assert(SMEM <= 227 * 1024, "one block per SM");
+};
+
+// All softmax warps together.
+__device__ __forceinline__ void softmax_warps_sync()
+{
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+}
+
+// The pool rows of a run of key tiles, in order: lane l holds the row of block
+// NB * win + l of a window of 32 / NB tiles; the next window's table entries are
+// already in flight.
+template <int NB>
+struct TableWindow {
+    static constexpr int WT = 32 / NB;
+    const PrefillParams &p;
+    const int32_t *table;
+    int nblk, h, lane, win, cur, nxt;
+
+    __device__ __forceinline__ TableWindow(const PrefillParams &p_, int s, int h_, int nblk_)
+        : p(p_), table(p_.block_tables + (size_t)s * p_.max_blocks), nblk(nblk_), h(h_),
+          lane(threadIdx.x & 31), win(0)
+    {
+        cur = to_row(0, fetch(0));
+        nxt = fetch(WT);
+    }
+    __device__ __forceinline__ int fetch(int w0) const
+    {
+        const int lb = NB * w0 + lane;
+        return lb < nblk ? __ldg(table + lb) : 0;
+    }
+    __device__ __forceinline__ int to_row(int w0, int phys) const
+    {
+        if (NB * w0 + lane >= nblk)
+            return -1;                  // blocks past the sequence are not loaded
+        if ((unsigned)phys >= (unsigned)p.num_blocks) {
+            record_error(p.err, PA_DEVERR_TABLE_RANGE);
+            phys = 0;
+        }
+        return (phys * p.num_kv_heads + h) * kBlockSize;
+    }
+    // Row of this lane's block (lane % NB) of tile j; called for tiles in order.
+    __device__ __forceinline__ int row(int j)
+    {
+        if (j == win + WT) {
+            win += WT;
+            cur = to_row(win, nxt);
+            nxt = fetch(win + WT);
+        }
+        return __shfl_sync(0xffffffffu, cur, NB * (j - win) + lane % NB);
+    }
+};
+
+template <typename T, int D, int CL>
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(DiffShape<D>::THREADS)
+diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap tmk,
+                      const __grid_constant__ CUtensorMap tmv)
+{
+    using Sh = DiffShape<D>;
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr uint32_t FULL = 0xffffffffu;
+    constexpr int NS = Sh::NSLOT;
+    constexpr uint16_t kAll = (1u << CL) - 1;     // every block of the cluster
+
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t raw_addr = smem_addr(smem_raw);
+    unsigned char *smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+    const uint32_t sbase = smem_addr(smem);
+    unsigned char *bars = (smem - smem_raw) >= Sh::BAR_BYTES ? smem_raw : smem + Sh::DATA;
+    const uint32_t bar_addr = smem_addr(bars);
+    auto kfull = [&](int i) { return bar_addr + 8u * i; };
+    auto kempty = [&](int i) { return bar_addr + 8u * (NS + i); };
+    auto vfull = [&](int i) { return bar_addr + 8u * (2 * NS + i); };
+    auto vempty = [&](int i) { return bar_addr + 8u * (3 * NS + i); };
+    auto s_bar = [&](int g) { return bar_addr + 8u * (4 * NS + g); };         // S_g,j is there
+    auto read_bar = [&](int g) { return bar_addr + 8u * (4 * NS + 2 + g); };  // and has been read
+    auto o_bar = [&](int g) { return bar_addr + 8u * (4 * NS + 4 + g); };     // O_g has taken P_g,j
+    auto p_bar = [&](int g, int hf) { return bar_addr + 8u * (4 * NS + 6 + 2 * hf + g); };  // half of P_g,j is there
+    auto drain_bar = [&](int g) { return bar_addr + 8u * (4 * NS + 10 + g); };
+    const uint32_t q_bar = bar_addr + 8u * (4 * NS + 12);       // the Q tile is there
+    const uint32_t z_bar = bar_addr + 8u * (4 * NS + 13);       // value rows past the end are zero
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Sh::NBAR * 8);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int Hkv = p.num_kv_heads, Hq = p.num_heads, G = Hq / Hkv;
+    const int TPB = Sh::BM / G;                   // chunk tokens per block
+    const int unit = blockIdx.x / CL;             // of the cluster: CL query tiles
+    const int cr = CL > 1 ? (int)cluster_rank() : 0;
+    int h = unit % Hkv;
+
+    // ---- the block's rows and key range (uniform over the block) ----------
+    // no global memory is read before the preceding kernel (the plan) is done
+    grid_dependency_wait();
+    int s, rank = 0, tile = 0;
+    if (p.plan) {
+        if (!plan_block(p, unit, s, tile, h))
+            return;
+    } else {
+        const int per_rank = p.num_seqs * Hkv;
+        rank = unit / per_rank;
+        s = (unit % per_rank) / Hkv;
+    }
+    const int L = __ldg(p.seq_lens + s);
+    const int qs = __ldg(p.query_start + s);
+    const int c = __ldg(p.query_start + s + 1) - qs;
+    const bool reporter = !p.plan && rank == 0 && h == 0 && tid == 0 && cr == 0;   // the plan reports itself
+    if (L < 0 || L > p.max_blocks * kBlockSize) {
+        if (reporter)
+            record_error(p.err, PA_DEVERR_SEQLEN_RANGE);
+        return;
+    }
+    if (c < 0 || c > L) {
+        if (reporter)
+            record_error(p.err, PA_DEVERR_QUERY_RANGE);
+        return;
+    }
+    if (!p.plan) {
+        const int nq = (c + CL * TPB - 1) / (CL * TPB);
+        if (nq > p.q_ranks && reporter)
+            record_error(p.err, PA_DEVERR_QUERY_RANGE);   // max_query_len too small
+        if (rank >= nq)
+            return;
+        tile = nq - 1 - rank;                     // rank 0 = the last (longest) tile
+    }
+    const int t0 = (tile * CL + cr) * TPB;        // may lie past the chunk (no rows of its own)
+    const int p_last = L - c + min((tile + 1) * CL * TPB, c) - 1;   // the cluster's last row
+    const int nt = p_last / Sh::BN + 1;           // key tiles, the same for the whole cluster
+    const int nblk = (L + kBlockSize - 1) / kBlockSize;
+    // the last tile reaches past the sequence: its value rows there are zeroed
+    const bool ragged = nt * Sh::BN > L;
+
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(kfull(i), 1);
+            mbar_init(kempty(i), 2 * CL);         // both maps' issuers, of every block
+            mbar_init(vfull(i), 1);
+            mbar_init(vempty(i), 2 * CL);
+        }
+        for (int g = 0; g < 2; ++g) {
+            mbar_init(s_bar(g), 1);
+            mbar_init(read_bar(g), 4);            // one lane of each softmax warp
+            mbar_init(p_bar(g, 0), 4);
+            mbar_init(p_bar(g, 1), 4);
+            mbar_init(o_bar(g), 1);
+            mbar_init(drain_bar(g), 1);
+        }
+        mbar_init(q_bar, 8);
+        mbar_init(z_bar, 8);
+        *abort_flag = 0;
+        mbar_init_fence();
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(smem_addr(tmem_slot), Sh::TMEM_COLS);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if constexpr (CL > 1)
+        cluster_sync();                           // the other block's barriers are there too
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+
+    auto give_up = [&]() {
+        *abort_flag = 1;
+        record_error(p.err, PA_DEVERR_TIMEOUT);
+    };
+
+    if (warp == 0) {
+        // ---------------- producer: K_0, then K_j+1, V_j for every j ----------------
+        // The whole warp works: lane 0 waits for the slot and arms its barrier,
+        // lanes (hf, b) issue the tile's boxes in parallel.
+        TableWindow<Sh::NB> kw(p, s, h, nblk), vw(p, s, h, nblk);
+        auto load = [&](int j, int row, const CUtensorMap &tm, uint32_t slots, uint32_t full,
+                        uint32_t empty) {
+            bool ready = true;
+            if (lane == 0)
+                ready = !*abort_flag &&
+                        (j < NS || mbar_wait_bounded(empty, (uint32_t)((j / NS - 1) & 1)));
+            if (!__shfl_sync(FULL, ready, 0))
+                return false;
+            const int nv = min(Sh::NB, nblk - Sh::NB * j);
+            if (lane == 0)
+                mbar_arrive_expect_tx(full, (uint32_t)(nv * Sh::HALVES * Sh::BOX));
+            __syncwarp();
+            const int b = lane % Sh::NB, hf = lane / Sh::NB;
+            // the blocks of a cluster copy every CL-th box each, into all of them
+            const uint32_t dst = slots + (j % NS) * Sh::SLOT_BYTES + (hf * Sh::NB + b) * Sh::BOX;
+            if (hf < Sh::HALVES && row >= 0 && b % CL == cr) {
+                if constexpr (CL > 1)
+                    tma_load_2d_multicast(dst, &tm, 64 * hf, row, full, kAll);
+                else
+                    tma_load_2d(dst, &tm, 64 * hf, row, full);
+            }
+            return true;
+        };
+        int nk = 0, nv = 0;                       // tiles issued
+        bool ok = true;
+        for (int j = -1; ok && j < nt; ++j) {
+            if (j + 1 < nt) {
+                ok = load(j + 1, kw.row(j + 1), tmk, sbase + Sh::OFF_K, kfull((j + 1) % NS),
+                          kempty((j + 1) % NS));
+                nk += ok;
+            }
+            if (ok && j >= 0) {
+                ok = load(j, vw.row(j), tmv, sbase + Sh::OFF_V, vfull(j % NS), vempty(j % NS));
+                nv += ok;
+            }
+        }
+        if (!ok && lane == 0 && !*abort_flag)
+            give_up();
+        // every issued copy lands before the block may exit
+        if (lane < NS) {
+            for (int j = max(0, nk - NS); j < nk; ++j)
+                if (j % NS == lane && !mbar_wait_bounded(kfull(lane), (j / NS) & 1))
+                    give_up();
+            for (int j = max(0, nv - NS); j < nv; ++j)
+                if (j % NS == lane && !mbar_wait_bounded(vfull(lane), (j / NS) & 1))
+                    give_up();
+        }
+    } else if (warp <= 2) {
+        // ---------------- MMA issuer of map g (the whole warp, one elected lane issues) ----
+        const int g = warp - 1;
+        constexpr uint32_t idS = tc::idesc_f16(kBf16, Sh::BM, Sh::BN, false, false);
+        constexpr uint32_t idO = tc::idesc_f16(kBf16, Sh::BM, D, false, true);
+        // map 1's channels of the Q and K tiles start D/2 further: the next
+        // 64-channel half, or 64 bytes into the row
+        const uint32_t mo = g * (D == 128 ? Sh::BM * 128 : D);
+        const uint64_t q_desc = tc::sdesc_sw128(sbase + mo, 16, 1024);
+        const uint64_t k_desc = tc::sdesc_sw128(sbase + Sh::OFF_K + mo, 16, 1024);
+        const uint64_t v_desc = tc::sdesc_sw128(sbase + Sh::OFF_V, Sh::NB * Sh::BOX, 1024);
+        const uint32_t ts = tmem + g * Sh::MAP_COLS, tp = ts + Sh::COL_P, to = ts + Sh::COL_O;
+        static_assert(Sh::BM * 128 == Sh::NB * Sh::BOX, "Q and K halves 16 KB apart");
+        auto wait_all = [&](uint32_t bar, uint32_t parity) {
+            return __all_sync(FULL, mbar_wait_bounded(bar, parity));
+        };
+        // a slot's wait costs 100 to 250 cycles even when its copy has long
+        // landed, so it comes before the wait for the softmax or the last P.V
+        auto k_ready = [&](int j) { return wait_all(kfull(j % NS), (j / NS) & 1); };
+        auto v_ready = [&](int j) { return wait_all(vfull(j % NS), (j / NS) & 1); };
+        // a slot is free once both maps of every block of the cluster have read it
+        auto release = [&](uint32_t bar) {
+            if constexpr (CL > 1)
+                tc::commit_warp_multicast(bar, kAll);
+            else
+                tc::commit_warp(bar);
+        };
+        auto issue_s = [&](int j) {
+            const int sl = j % NS;
+            tc::fence_after_sync();
+            const uint64_t kd = k_desc + (uint64_t)((sl * Sh::SLOT_BYTES) >> 4);
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k)      // 32 bytes along the 128-byte row a step
+                tc::mma_ss_warp(ts, q_desc + 2 * k, kd + 2 * k, idS, k > 0);
+            tc::commit_warp(s_bar(g));
+            release(kempty(sl));
+        };
+        // O_g += P_g,j . V_j, each half of the keys once the softmax has written
+        // its P
+        auto issue_pv = [&](int j) -> bool {
+            const int sl = j % NS;
+            const uint64_t vd = v_desc + (uint64_t)((sl * Sh::SLOT_BYTES) >> 4);
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                if (!wait_all(p_bar(g, hf), j & 1))
+                    return false;
+                tc::fence_after_sync();
+#pragma unroll
+                for (int kk = 4 * hf; kk < 4 * hf + 4; ++kk)
+                    // A = P: keys 16kk.. = 8 packed columns; B = V block kk (MN-major:
+                    // 64-channel groups NB boxes apart, 8-key groups 1 KB apart)
+                    tc::mma_ts_warp(to, tp + 8 * kk, vd + (uint64_t)((kk * Sh::BOX) >> 4), idO,
+                                    (j > 0 || kk > 0) ? 1u : 0u);
+            }
+            tc::commit_warp(o_bar(g));
+            release(vempty(sl));
+            return true;
+        };
+        bool ok = k_ready(0) && wait_all(q_bar, 0);
+        if (ok)
+            issue_s(0);
+        for (int j = 0; ok && j < nt; ++j) {
+            if (__any_sync(FULL, *abort_flag != 0)) {
+                ok = false;
+                break;
+            }
+            const bool more = j + 1 < nt;
+            ok = v_ready(j) && (!more || k_ready(j + 1)) &&
+                 (!ragged || more || wait_all(z_bar, 0));
+            if constexpr (Sh::SEPARATE_P) {
+                // S_g,j+1 only needs the softmax to have read S_g,j
+                if (ok && more && (ok = wait_all(read_bar(g), j & 1)))
+                    issue_s(j + 1);
+                ok = ok && issue_pv(j);
+            } else {
+                ok = ok && issue_pv(j);
+                // S_g,j+1 reuses the TMEM columns P_g,j . V_j reads
+                if (ok && more && (ok = wait_all(o_bar(g), j & 1)))
+                    issue_s(j + 1);
+            }
+        }
+        if (!ok && lane == 0)
+            give_up();
+        // no MMA may still run when TMEM is freed
+        tc::commit_warp(drain_bar(g));
+        if (!wait_all(drain_bar(g), 0) && lane == 0)
+            give_up();
+    } else if (warp == 3) {
+        // while the block works: warm L2 with the query rows of the block one
+        // wave later (its pair and kv head from the work order)
+        int s2, tile2, h2;
+        if (p.plan && plan_block(p, unit + p.wave / CL, s2, tile2, h2)) {
+            const int qs2 = __ldg(p.query_start + s2);
+            const int t02 = (tile2 * CL + cr) * TPB;
+            const int ntok = min(TPB, __ldg(p.query_start + s2 + 1) - qs2 - t02);
+            const int lines = G * D * 2 / 128;      // 128-byte lines of a token's G heads
+            const T *qg = reinterpret_cast<const T *>(p.q);
+            for (int i = lane; i < ntok * lines; i += 32)
+                prefetch_l2(qg + ((size_t)(qs2 + t02 + i / lines) * Hq + h2 * G) * D +
+                            (i % lines) * 64);
+        }
+    } else if (warp >= 4) {
+        // ---------------- Q tile -> shared memory ----------------
+        // K-major with the 128-byte swizzle.  Row rr = (token t0 + rr / G, q head
+        // h*G + rr % G); rows past the chunk and the rows 128 - TPB*G that do not
+        // fill a token are zero.  Thread lt takes 16-byte chunk lt % CPR of every
+        // (256 / CPR)-th row, all its loads in flight at once.
+        const int lt = tid - 128;
+        {
+            constexpr int CPR = D / 8;            // 16-byte chunks per row
+            constexpr int RSTEP = 256 / CPR;
+            constexpr int NPT = Sh::BM / RSTEP;
+            const T *qg = reinterpret_cast<const T *>(p.q);
+            const int ch = lt % CPR, hf = ch >> 3, c8 = ch & 7;
+            uint4 qv[NPT];
+#pragma unroll
+            for (int i = 0; i < NPT; ++i) {
+                const int rr = lt / CPR + i * RSTEP;
+                const int tok = rr / G, hg = rr % G;
+                qv[i] = make_uint4(0, 0, 0, 0);
+                if (rr < TPB * G && t0 + tok < c)
+                    qv[i] = __ldg(reinterpret_cast<const uint4 *>(
+                        qg + ((size_t)(qs + t0 + tok) * Hq + h * G + hg) * D + ch * 8));
+            }
+#pragma unroll
+            for (int i = 0; i < NPT; ++i) {
+                const int rr = lt / CPR + i * RSTEP;
+                *reinterpret_cast<uint4 *>(smem + hf * (Sh::BM * 128) + rr * 128 +
+                                           ((c8 ^ (rr & 7)) << 4)) = qv[i];
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(q_bar);
+        }
+
+        // ---------------- softmax: one thread per row of its map ----------
+        const int grp = (warp - 4) >> 2;
+        const int q4 = warp & 3;                   // TMEM lane quarter of this warp
+        const int rr = q4 * 32 + lane;             // row
+        const uint32_t lanes = tmem + ((uint32_t)(q4 * 32) << 16);
+        const uint32_t tg = lanes + grp * Sh::MAP_COLS;
+        const int tok = rr / G, hg = rr % G;
+        const bool row_valid = rr < TPB * G && t0 + tok < c;
+        const int pos = row_valid ? L - c + t0 + tok : L - 1;
+        const float sl2 = p.scale_log2;
+        auto arrive = [&](uint32_t bar) {          // once a warp, after its lanes' work
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar);
+        };
+        float m = 0.f, l = 0.f;
+        bool ok = true;
+        for (int j = 0; j < nt; ++j) {
+            if (__any_sync(FULL, *abort_flag != 0)) {
+                ok = false;
+                break;
+            }
+            if (!__all_sync(FULL, mbar_wait_bounded(s_bar(grp), j & 1))) {
+                ok = false;
+                break;
+            }
+            tc::fence_after_sync();
+            const int k0 = j * Sh::BN;
+            const int vis = pos - k0;              // keys [0, vis] of the tile are visible
+            // the 128 scores of the row, both halves held in registers
+            uint32_t v[2][64];
+            __syncwarp();                        // tcgen05.ld is warp-collective
+            tc::tmem_ld64(tg, v[0]);
+            tc::tmem_ld64(tg + 64, v[1]);
+            if constexpr (Sh::SEPARATE_P) {
+                tc::fence_before_sync();
+                arrive(read_bar(grp));           // S_g,j+1 may go in
+            }
+            // tiles left of the diagonal (the common case) need no mask
+            const bool full = __all_sync(FULL, vis >= Sh::BN - 1);
+            if (!full) {
+#pragma unroll
+                for (int e = 0; e < Sh::BN; ++e)
+                    if (e > vis)
+                        v[e >> 6][e & 63] = __float_as_uint(-INFINITY);
+            }
+            // row maximum as a tree, three operands per instruction
+            float mx[8];
+#pragma unroll
+            for (int a = 0; a < 8; ++a) {
+                auto x = [&](int i) { return __uint_as_float(v[i >> 6][i & 63]); };
+                float t = fmax3(x(a), x(a + 8), x(a + 16));
+#pragma unroll
+                for (int i = a + 24; i < 120; i += 16)
+                    t = fmax3(t, x(i), x(i + 8));
+                mx[a] = fmaxf(t, x(a + 120));
+            }
+            float mt = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
+                             fmaxf(mx[6], mx[7]));
+            mt *= sl2;                           // scale > 0: max commutes with it
+            // running maximum, raised lazily: only when the tile's maximum
+            // exceeds it by more than 8 (P stays below 2^8 otherwise)
+            bool grow = false;
+            float alpha = 1.f;
+            if (j == 0) {
+                m = fmaxf(mt, -3e38f);           // finite also if every score is -inf
+            } else if (mt > m + 8.f) {
+                grow = true;
+                alpha = ex2_approx(m - mt);
+                m = mt;
+            }
+            // P = 2^(scale*s - m) packed to the operand type; scale-and-subtract
+            // and the row sum run two values per instruction
+            const uint64_t sl2x2 = f2_pack(sl2, sl2), nmx2 = f2_pack(-m, -m);
+            uint64_t sum2[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                uint32_t pw[32];
+#pragma unroll
+                for (int e = 0; e < 64; e += 2) {
+                    float y0, y1;
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(v[hf][e]), __uint_as_float(v[hf][e + 1])),
+                                     sl2x2, nmx2),
+                              y0, y1);
+                    const float p0 = ex2_approx(y0);
+                    const float p1 = ex2_approx(y1);
+                    sum2[(e >> 1) & 3] = f2_add(sum2[(e >> 1) & 3], f2_pack(p0, p1));
+                    pw[e / 2] = Mma<T>::pack(p0, p1);
+                }
+                if (Sh::SEPARATE_P && hf == 0) {
+                    // P_g,j overwrites P_g,j-1, and O may be rescaled below: both
+                    // wait for P_g,j-1 . V_j-1 (with P over S, S_g,j came after it)
+                    if (j > 0 && !__all_sync(FULL, mbar_wait_bounded(o_bar(grp), (j - 1) & 1))) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after_sync();
+                }
+                __syncwarp();
+                tc::tmem_st32(tg + Sh::COL_P + 32 * hf, pw);
+                if (hf == 0) {
+                    // value rows of keys >= L are zeroed (0 * NaN is NaN in the
+                    // MMA), by both maps' threads; both issuers wait for all of them
+                    if (ragged && j == nt - 1) {
+                        const int sl = j % NS;
+                        if (!__all_sync(FULL, mbar_wait_bounded(vfull(sl), (j / NS) & 1))) {
+                            ok = false;
+                            break;
+                        }
+                        const int first = L - k0;
+                        const int n16 = (Sh::BN - first) * Sh::HALVES * 8;
+                        unsigned char *vb = smem + Sh::OFF_V + sl * Sh::SLOT_BYTES;
+                        for (int idx = lt; idx < n16; idx += 256) {
+                            const int row = first + idx / (Sh::HALVES * 8);
+                            const int rem = idx % (Sh::HALVES * 8);
+                            *reinterpret_cast<uint4 *>(vb +
+                                                       ((rem >> 3) * Sh::NB + (row >> 4)) * Sh::BOX +
+                                                       (row & 15) * 128 + (rem & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_shared();
+                        arrive(z_bar);
+                    }
+                    // O rescale: P_g,j-1 . V_j-1 has completed
+                    if (__any_sync(FULL, grow)) {
+#pragma unroll
+                        for (int cc = 0; cc < D; cc += 32) {
+                            uint32_t o[32];
+                            tc::tmem_ld32(tg + Sh::COL_O + cc, o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tc::tmem_st32(tg + Sh::COL_O + cc, o);
+                        }
+                    }
+                }
+                tc::fence_before_sync();
+                arrive(p_bar(grp, hf));
+            }
+            if (!ok)
+                break;
+            float sum[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float a, b;
+                f2_unpack(sum2[q], a, b);
+                sum[q] = a + b;
+            }
+            l = fmaf(l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+        }
+        if (ok && !__all_sync(FULL, mbar_wait_bounded(o_bar(grp), (nt - 1) & 1)))
+            ok = false;
+
+        // ---------------- the difference, its norm, the output ----------------
+        // Row sums and the halves' sums of squares go through shared memory.
+        // Every softmax thread takes part in both barriers, also after a wait that
+        // gave up; past the first, both maps' last P.V are known to be done.
+        float *xl = reinterpret_cast<float *>(smem + Sh::OFF_X);      // [2][128]
+        float *xq = xl + 2 * Sh::BM;                                  // [2][128]
+        if (!ok)
+            give_up();
+        xl[grp * Sh::BM + rr] = l;
+        tc::fence_before_sync();
+        softmax_warps_sync();
+        tc::fence_after_sync();
+        ok = !__any_sync(FULL, *abort_flag != 0);
+        const float i0 = 1.f / xl[rr];
+        const float i1 = -__ldg(p.lambda + h * G + hg) / xl[Sh::BM + rr];
+        const uint32_t half = lanes + Sh::COL_O + grp * (D / 2);
+        float y[D / 2], ss = 0.f;
+        if (ok) {
+#pragma unroll
+            for (int cc = 0; cc < D / 2; cc += 32) {
+                uint32_t a[32], b[32];
+                __syncwarp();
+                tc::tmem_ld32(half + cc, a);
+                tc::tmem_ld32(half + Sh::MAP_COLS + cc, b);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    y[cc + e] = fmaf(__uint_as_float(b[e]), i1, __uint_as_float(a[e]) * i0);
+                    ss = fmaf(y[cc + e], y[cc + e], ss);
+                }
+            }
+        }
+        xq[grp * Sh::BM + rr] = ss;
+        softmax_warps_sync();
+        if (ok && row_valid) {
+            const T *w = static_cast<const T *>(p.norm_w);
+            float k = p.out_scale;
+            if (w)
+                k *= rsqrtf((xq[rr] + xq[Sh::BM + rr]) * (1.f / D) + p.norm_eps);
+            T *orow = reinterpret_cast<T *>(p.out) +
+                      ((size_t)(qs + t0 + tok) * Hq + h * G + hg) * D + grp * (D / 2);
+#pragma unroll
+            for (int e = 0; e < D / 2; e += 8) {
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    f[i] = k;
+                if (w) {
+                    const uint4 wv = __ldg(reinterpret_cast<const uint4 *>(w + grp * (D / 2) + e));
+                    const uint32_t w32[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 x = Elem<T>::to_f2(w32[i]);
+                        f[2 * i] *= x.x;
+                        f[2 * i + 1] *= x.y;
+                    }
+                }
+                uint4 u;
+                u.x = Mma<T>::pack(y[e] * f[0], y[e + 1] * f[1]);
+                u.y = Mma<T>::pack(y[e + 2] * f[2], y[e + 3] * f[3]);
+                u.z = Mma<T>::pack(y[e + 4] * f[4], y[e + 5] * f[5]);
+                u.w = Mma<T>::pack(y[e + 6] * f[6], y[e + 7] * f[7]);
+                *reinterpret_cast<uint4 *>(orow + e) = u;
+            }
+        }
+    }
+
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, Sh::TMEM_COLS);
+    }
+    // the other block may still copy into this one's shared memory or arrive on
+    // its barriers
+    if constexpr (CL > 1)
+        cluster_sync();
+}
+
+template <typename T, int D, int CL>
+void entry(PrefillKernel *k)
+{
+    k->fn = reinterpret_cast<const void *>(&diff_prefill_kernel_t<T, D, CL>);
+    k->threads = DiffShape<D>::THREADS;
+    k->smem = DiffShape<D>::SMEM;
+}
+
+template <int CL>
+void pick(int dtype, int head_dim, PrefillKernel *k)
+{
+    const bool bf = dtype == PA_DTYPE_BF16;
+    if (head_dim == 64)
+        bf ? entry<__nv_bfloat16, 64, CL>(k) : entry<__half, 64, CL>(k);
+    else
+        bf ? entry<__nv_bfloat16, 128, CL>(k) : entry<__half, 128, CL>(k);
+}
+
+}  // namespace
+
+bool diff_prefill_kernel(int dtype, int head_dim, bool pairs, PrefillKernel *k)
+{
+    // the work order is the plain prefill's
+    if (!prefill_kernel(dtype, head_dim, k))
+        return false;
+    pairs ? pick<2>(dtype, head_dim, k) : pick<1>(dtype, head_dim, k);
+    return true;
+}
+
+}  // namespace pa

@@ -41,18 +41,6 @@
 // overwrites S's first 64 columns at head_dim 128; at head_dim 64 it has the
 // group's last 64 columns, and S_g,j+1 is then issued as soon as the softmax
 // has read S_g,j.
-//
-// Differential attention (DIFF): a head's q row and a token's key row hold two
-// queries and two keys of head_dim / 2 channels side by side, and
-//     y = sum_t softmax_t(scale q1.k1_t) v_t - lambda sum_t softmax_t(scale q2.k2_t) v_t
-// The block takes one query tile and its two groups are the two maps: group g
-// reads channels [g D/2, (g+1) D/2) of the same Q tile and of every K tile
-// (S_g has half the k-steps), both multiply the same V tile, and the two O
-// accumulators lie side by side in the same TMEM lanes.  At the end group g
-// forms the difference of half of the row's channels from both accumulators;
-// the row sums and the halves' sums of squares (the optional RMS norm) are
-// exchanged through the Q tile's shared memory, which no MMA reads any more.
-//
 // Every wait is bounded; a wait that gives up records PA_DEVERR_TIMEOUT and
 // the block drains its copies and MMAs before it frees TMEM and exits.
 #pragma once
@@ -62,11 +50,12 @@
 
 #include "pa_device.cuh"
 #include "pa_prefill_abi.h"
+#include "pa_prefill_plan.cuh"
 #include "pa_tcgen05.cuh"
 
 namespace pa {
 
-template <int D, bool DIFF = false>
+template <int D>
 struct PrefillShape {
     static constexpr int BM = kPrefillRows;                 // rows per group (tile)
     static constexpr int NG = kPrefillTiles;                // groups per block
@@ -74,11 +63,10 @@ struct PrefillShape {
     static constexpr int NB = BN / kBlockSize;              // pool blocks per tile
     static constexpr int HALVES = D / 64;                   // 128-byte column boxes
     static constexpr int BOX = 2048;                        // 16 rows x 128 B
-    static constexpr int QT = DIFF ? 1 : NG;                // query tiles per block
-    static constexpr int Q_BYTES = BM * D * 2;              // per tile: [half][128 rows][128 B]
+    static constexpr int Q_BYTES = BM * D * 2;              // per group: [half][128 rows][128 B]
     static constexpr int SLOT_BYTES = BN * D * 2;           // [half][8 blocks][16 rows][128 B]
-    static constexpr int NSLOT = (227 * 1024 - 1024 - QT * Q_BYTES) / SLOT_BYTES;   // K/V ring
-    static constexpr int OFF_SLOT = QT * Q_BYTES;
+    static constexpr int NSLOT = (227 * 1024 - 1024 - NG * Q_BYTES) / SLOT_BYTES;   // K/V ring
+    static constexpr int OFF_SLOT = NG * Q_BYTES;
     static constexpr int DATA = OFF_SLOT + NSLOT * SLOT_BYTES;   // 1024-aligned operand region
     // full[NSLOT] empty[NSLOT] s[2] p[2] o[2] drain q[2] read[2], then TMEM
     // base and abort flag
@@ -98,48 +86,18 @@ struct PrefillShape {
     static constexpr bool SEPARATE_P = COL_O + D + BN / 2 <= GROUP_COLS;
     static constexpr uint32_t COL_P = SEPARATE_P ? COL_O + D : COL_S;
     static_assert(D == 64 || D == 128, "head_dim");
-    static_assert(NSLOT >= 4 && NSLOT <= 32, "at least two tiles of K/V in flight");
+    static_assert(NSLOT >= 4, "at least two tiles of K/V in flight");
     static_assert(OFF_SLOT % 1024 == 0 && SLOT_BYTES % 1024 == 0, "swizzle atoms");
     static_assert(BAR_BYTES <= 512, "barriers fit either end of the slack");
     static_assert(SMEM <= 227 * 1024, "one block per SM");
 };
 
-// The (sequence, query tile, kv head) of block b under the work order;
-// false past the end of the order.
-__device__ __forceinline__ bool plan_block(const PrefillParams &p, int b, int &s, int &tile,
-                                           int &h)
-{
-    const int Hkv = p.num_kv_heads;
-    const int k = b / Hkv;
-    if (k >= *p.plan_count)
-        return false;
-    uint32_t e = p.plan[k];
-    if (*p.plan_by_seq) {
-        const int s0 = (int)(e >> 16);
-        const int st = p.plan_seq_start[s0], nq = p.plan_seq_nq[s0];
-        const int local = b - Hkv * st;
-        h = local / nq;
-        e = p.plan[st + local % nq];
-    } else {
-        h = b % Hkv;
-    }
-    s = (int)(e >> 16);
-    tile = (int)(e & 0xffffu);
-    return true;
-}
-
-// All softmax warps (2 to 9) together.
-__device__ __forceinline__ void softmax_warps_sync(int threads)
-{
-    asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
-}
-
-template <typename T, int D, bool DIFF>
-__global__ void __launch_bounds__(PrefillShape<D, DIFF>::THREADS)
+template <typename T, int D>
+__global__ void __launch_bounds__(PrefillShape<D>::THREADS)
 prefill_tc_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmk,
                   const __grid_constant__ CUtensorMap tmv)
 {
-    using Sh = PrefillShape<D, DIFF>;
+    using Sh = PrefillShape<D>;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr uint32_t FULL = 0xffffffffu;
     constexpr int NS = Sh::NSLOT;
@@ -165,8 +123,8 @@ prefill_tc_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmk
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int Hkv = p.num_kv_heads, Hq = p.num_heads, G = Hq / Hkv;
-    const int TPG = Sh::BM / G;                   // chunk tokens per query tile
-    const int TPB = Sh::QT * TPG;                 // chunk tokens per block
+    const int TPG = Sh::BM / G;                   // chunk tokens per group
+    const int TPB = Sh::NG * TPG;                 // chunk tokens per block
     int h = blockIdx.x % Hkv;
 
     // ---- the block's rows and key range (uniform over the block) ----------
@@ -323,14 +281,11 @@ prefill_tc_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmk
             if (!wait_all(full_bar(sl), (i / NS) & 1))
                 return false;
             tc::fence_after_sync();
-            // DIFF: map g's channels of the one Q tile and of the K tile start
-            // D/2 further, in the next 64-channel half or within the row
-            const uint64_t mo = DIFF ? (uint64_t)((g * (D == 128 ? Sh::BM * 128 : D)) >> 4) : 0;
-            const uint64_t qd = q_desc + (DIFF ? mo : (uint64_t)((g * Sh::Q_BYTES) >> 4));
-            const uint64_t kd = k_desc + mo + (uint64_t)((sl * Sh::SLOT_BYTES) >> 4);
+            const uint64_t qd = q_desc + (uint64_t)((g * Sh::Q_BYTES) >> 4);
+            const uint64_t kd = k_desc + (uint64_t)((sl * Sh::SLOT_BYTES) >> 4);
             const uint32_t d = tmem + g * Sh::GROUP_COLS + Sh::COL_S;
 #pragma unroll
-            for (int k = 0; k < D / (DIFF ? 32 : 16); ++k) {
+            for (int k = 0; k < D / 16; ++k) {
                 // K step k: 32 bytes along the 128-byte row; the next 64
                 // channels are 16 KB further (Q: 128 rows, K: 8 boxes)
                 const uint64_t ko = (uint64_t)(((k & 3) * 32 + (k >> 2) * (Sh::BM * 128)) >> 4);
@@ -381,7 +336,7 @@ prefill_tc_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmk
         }
         bool ok = true;
         for (int g = 0; ok && g < Sh::NG; ++g)
-            ok = (DIFF && g > 0 || wait_all(q_bar(g), 0)) && issue_s(g, 0);
+            ok = wait_all(q_bar(g), 0) && issue_s(g, 0);
         for (int j = 0; ok && j < nt; ++j) {
             if (__any_sync(FULL, *abort_flag != 0)) {
                 ok = false;
@@ -419,8 +374,8 @@ prefill_tc_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmk
         {
             constexpr int CPR = D / 8;            // 16-byte chunks per row
             constexpr int RSTEP = Sh::NG * 128 / CPR;
-            constexpr int NPT = Sh::QT * Sh::BM / RSTEP;
-            constexpr int PER_G = NPT / Sh::QT;   // a thread's chunks in each tile
+            constexpr int NPT = Sh::NG * Sh::BM / RSTEP;
+            constexpr int PER_G = NPT / Sh::NG;   // a thread's chunks in each group
             const T *qg = reinterpret_cast<const T *>(p.q);
             const int lt = tid - 64, ch = lt % CPR, hf = ch >> 3, c8 = ch & 7;
             uint4 qv[NPT];
@@ -458,7 +413,7 @@ prefill_tc_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmk
         const int q4 = warp & 3;                   // TMEM lane quarter of this warp
         const int rr = q4 * 32 + lane;             // row within the group
         const uint32_t tg = tmem + ((uint32_t)(q4 * 32) << 16) + grp * Sh::GROUP_COLS;
-        const int tok = (DIFF ? 0 : grp * TPG) + rr / G, hg = rr % G;
+        const int tok = grp * TPG + rr / G, hg = rr % G;
         const bool row_valid = rr < TPG * G && t0 + tok < c;
         const int pos = row_valid ? L - c + t0 + tok : L - 1;
         const float sl2 = p.scale_log2;
@@ -512,9 +467,7 @@ prefill_tc_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmk
             bool grow = false;
             float alpha = 1.f;
             if (j == 0) {
-                // finite: key 0 is visible to every row (DIFF: also when every
-                // score of the tile is -inf; a later tile's maximum then wins)
-                m = DIFF ? fmaxf(mt, -3e38f) : mt;
+                m = mt;                          // finite: key 0 is visible to every row
             } else if (mt > m + 8.f) {
                 grow = true;
                 alpha = ex2_approx(m - mt);
@@ -602,72 +555,7 @@ prefill_tc_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmk
         }
         if (ok && !__all_sync(FULL, mbar_wait_bounded(o_bar(grp), (nt - 1) & 1)))
             ok = false;
-        if constexpr (DIFF) {
-            // Every softmax thread takes part in both barriers, also after a
-            // wait that gave up.
-            float *xl = reinterpret_cast<float *>(smem);          // row sums [2][128]
-            float *xq = xl + 2 * Sh::BM;                          // sums of squares [2][128]
-            if (!ok)
-                give_up();
-            else
-                xl[grp * Sh::BM + rr] = l;
-            tc::fence_before_sync();
-            softmax_warps_sync(Sh::NG * 128);
-            tc::fence_after_sync();
-            ok = !__any_sync(FULL, *abort_flag != 0);
-            const float i0 = 1.f / xl[rr];
-            const float i1 = -__ldg(p.lambda + h * G + hg) / xl[Sh::BM + rr];
-            const uint32_t t0c = tg - grp * Sh::GROUP_COLS + Sh::COL_O + grp * (D / 2);
-            float y[D / 2], ss = 0.f;
-            if (ok) {
-#pragma unroll
-                for (int cc = 0; cc < D / 2; cc += 32) {
-                    uint32_t a[32], b[32];
-                    __syncwarp();
-                    tc::tmem_ld32(t0c + cc, a);
-                    tc::tmem_ld32(t0c + Sh::GROUP_COLS + cc, b);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        y[cc + e] = fmaf(__uint_as_float(b[e]), i1, __uint_as_float(a[e]) * i0);
-                        ss = fmaf(y[cc + e], y[cc + e], ss);
-                    }
-                }
-            }
-            xq[grp * Sh::BM + rr] = ss;
-            softmax_warps_sync(Sh::NG * 128);
-            if (ok && row_valid) {
-                const T *w = static_cast<const T *>(p.norm_w);
-                float k = p.out_scale;
-                if (w)
-                    k *= rsqrtf((xq[rr] + xq[Sh::BM + rr]) * (1.f / D) + p.norm_eps);
-                T *orow = reinterpret_cast<T *>(p.out) +
-                          ((size_t)(qs + t0 + tok) * Hq + h * G + hg) * D + grp * (D / 2);
-#pragma unroll
-                for (int e = 0; e < D / 2; e += 8) {
-                    float f[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        f[i] = k;
-                    if (w) {
-                        const uint4 wv =
-                            __ldg(reinterpret_cast<const uint4 *>(w + grp * (D / 2) + e));
-                        const uint32_t w32[4] = {wv.x, wv.y, wv.z, wv.w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 x = Elem<T>::to_f2(w32[i]);
-                            f[2 * i] *= x.x;
-                            f[2 * i + 1] *= x.y;
-                        }
-                    }
-                    uint4 u;
-                    u.x = Mma<T>::pack(y[e] * f[0], y[e + 1] * f[1]);
-                    u.y = Mma<T>::pack(y[e + 2] * f[2], y[e + 3] * f[3]);
-                    u.z = Mma<T>::pack(y[e + 4] * f[4], y[e + 5] * f[5]);
-                    u.w = Mma<T>::pack(y[e + 6] * f[6], y[e + 7] * f[7]);
-                    *reinterpret_cast<uint4 *>(orow + e) = u;
-                }
-            }
-        } else if (ok) {
+        if (ok) {
             tc::fence_after_sync();
             __syncwarp();
             const float inv = 1.f / l;

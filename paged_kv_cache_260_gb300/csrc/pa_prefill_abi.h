@@ -63,7 +63,8 @@ struct PrefillKernel {
 };
 
 bool prefill_kernel(int dtype, int head_dim, PrefillKernel *k);
-bool diff_prefill_kernel(int dtype, int head_dim, PrefillKernel *k);
+// pairs: two blocks on consecutive query tiles share their K/V copies
+bool diff_prefill_kernel(int dtype, int head_dim, bool pairs, PrefillKernel *k);
 constexpr int kPrefillRows = 128;   // (token, head) rows of one prefill query tile
 constexpr int kPrefillTiles = 2;    // query tiles of one prefill thread block (differential
                                     // attention: one, against two key maps)

@@ -63,8 +63,8 @@ def test_prefill_refuses(lib):
     assert _prefill(lib, longest=-1) == 1 and _prefill(lib, longest=0) == 0
     assert _prefill(lib, ws=0x1010, wb=4096) == 3            # misaligned workspace
     assert _prefill(lib, ws=0x1000, wb=16) == 3
-    # one 128-row tile a block: 32 tokens of 4 heads; 16 + 4 n tiles + 8 n
-    assert lib.pa_diff_prefill_workspace_size(8, 512, 32, 8) == 768     # 16 + 512 + 64
+    # 16 + 4 * seqs * query tile pairs + 8 * seqs, rounded up to 256
+    assert lib.pa_diff_prefill_workspace_size(8, 512, 32, 8) == 512     # 16 + 256 + 64
     assert lib.pa_diff_prefill_workspace_size(8, 512, 30, 8) == 0
 
 

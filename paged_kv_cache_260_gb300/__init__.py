@@ -377,8 +377,9 @@ def diff_decode(out, q, k_cache, v_cache, block_tables, seq_lens, lam, scale, no
         workspace = diff_decode_workspace_for(q, k_cache, block_tables, stream)
     wptr, wbytes = ((None, 0) if workspace is None else
                     (workspace.data_ptr(), _bytes_of(workspace, dev)))
-    rc = load().pa_diff_decode(*at, *factors, n, hq, hkv, d, bs, block_tables.shape[1], nb, float(scale),
-                               float(eps), float(out_scale), _dtype_code(q), wptr, wbytes, _stream(stream))
+    rc = load().pa_diff_decode(*at, *factors, n, hq, hkv, d, bs, block_tables.shape[1], nb,
+                               float(scale), float(eps), float(out_scale), _dtype_code(q), wptr,
+                               wbytes, _stream(stream))
     if rc:
         raise PagedAttnError("pa_diff_decode", rc)
     return out
@@ -415,8 +416,9 @@ def diff_prefill(out, q, k_cache, v_cache, block_tables, seq_lens, query_start, 
     wptr, wbytes = ((None, 0) if workspace is None else
                     (workspace.data_ptr(), _bytes_of(workspace, dev)))
     rc = load().pa_diff_prefill(*at, _near(query_start, _torch().int32, dev), *factors, n, longest,
-                                hq, hkv, d, bs, block_tables.shape[1], nb, float(scale), float(eps), float(out_scale),
-                                _dtype_code(q), wptr, wbytes, _stream(stream))
+                                hq, hkv, d, bs, block_tables.shape[1], nb, float(scale),
+                                float(eps), float(out_scale), _dtype_code(q), wptr, wbytes,
+                                _stream(stream))
     if rc:
         raise PagedAttnError("pa_diff_prefill", rc)
     return out

@@ -901,8 +901,8 @@ int pa_decode_shared_prefix(void *out, const void *q, void *k_cache, void *v_cac
     return cuda_status(launch_shared_merge(sp, dtype == PA_DTYPE_BF16, st));
 }
 
-// Query tiles per (sequence, kv head) of a prefill grid, 0 on bad arguments;
-// `tiles`: the 128-row query tiles of a thread block.
+// Units of work per (sequence, kv head) of a prefill, 0 on bad arguments;
+// `tiles`: the 128-row query tiles of a unit.
 static long long prefill_q_ranks(int max_query_len, int num_heads, int num_kv_heads,
                                  int tiles = kPrefillTiles)
 {
@@ -986,7 +986,8 @@ static int prefill_impl(void *out, const void *q, const void *k_cache, const voi
             return PA_ERR_WORKSPACE;
     }
     PrefillKernel kk{};
-    if (!(diff ? diff_prefill_kernel(dtype, head_dim, pairs, &kk) : prefill_kernel(dtype, head_dim, &kk)))
+    if (!(diff ? diff_prefill_kernel(dtype, head_dim, pairs, &kk)
+               : prefill_kernel(dtype, head_dim, &kk)))
         return PA_ERR_UNSUPPORTED;
     DeviceState *ds;
     rc = device_state(&ds);

@@ -8,11 +8,29 @@
 //
 // One thread block (one per SM) computes 128 rows = (token, q head) pairs of
 // one sequence and kv head.  The two maps run side by side on the same Q, K and
-// V tiles: per key tile j (BN keys) and map g
-//     S_g,j = Q[:, g] . K_j[:, g]^T     (M 128, N BN, K = head_dim / 2)
-//     O_g  += P_g,j . V_j               (M 128, N head_dim, K BN)
+// V tiles: per 128-key tile j and map g
+//     S_g,j = Q[:, g] . K_j[:, g]^T     (M 128, N 128, K = head_dim / 2)
+//     O_g  += P_g,j . V_j               (M 128, N head_dim, K 128)
 // so K and V are staged once for both, and O_0, O_1 end up in the same TMEM
 // lanes, where the difference is taken.
+//
+// What bounds it, measured on two 2048-token chunks at 16K (32/8 heads x 128,
+// bf16; 1.55 TFLOP):
+//  * A block of 128 rows reads K and V twice as often as the plain prefill's 256
+//    rows do: 64 KB a tile, 5.7 TB/s out of L2 over all SMs, and every version
+//    that read them so ended at 1420 to 1510 us.  So two blocks of a cluster take
+//    consecutive query tiles and copy every other K/V box each, into both
+//    (multicast): 1276 us.
+//  * Then each map's chain S -> softmax -> P.V -> next S (P lies over the score
+//    columns it came from, and TMEM has no others): about 2,600 cycles a tile,
+//    1,450 of them the softmax of one warp per sub-core, while the tensor core
+//    works for 1,536.  P.V starts on the first 64 keys while the softmax is at
+//    the others; each map has an issuing warp of its own (one for both was busy
+//    for 2,300 cycles: every wait on a barrier costs it 100 to 250, completed or
+//    not); and map 1 runs half a tile behind map 0.  1196 us: 1.29 PFLOP/s.
+//  * P through shared memory, which lets the next S go ahead, costs more shared
+//    memory bandwidth than there is (1437 us before the multicast); 80-key tiles
+//    with P in columns of its own 1702; two threads a row 1382 against 1197.
 //
 // Warp roles (384 threads):
 //   warp 0     TMA producer: K tiles and V tiles through a ring each, K one tile
@@ -23,11 +41,15 @@
 //   warps 4-7 map 0, 8-11 map 1: load the Q tile, then one thread per row (its
 //              TMEM lane): scores from TMEM, causal mask, online softmax in base
 //              2 with a lazy rescale of O (only when the running maximum grows
-//              by more than 2^8), P into TMEM, rounded to the operand type (the
-//              row sum takes the unrounded weights); at the end each map forms
-//              the difference of half of the row's channels.
-// TMEM (512 columns), map g from 256 g: S in BN columns, P packed two keys a
-// column in BN / 2, O in head_dim columns.
+//              by more than 2^8), P into TMEM in two halves, rounded to the
+//              operand type (the row sum takes the unrounded weights; the product
+//              with V needs 16-bit operands, and a second product with what the
+//              rounding left over would add a third to the tensor work); at the
+//              end each map forms the difference of half of the row's channels.
+// TMEM (512 columns): map g has S in [256g, 256g + 128) and O in
+// [256g + 128, 256g + 128 + head_dim).  P, packed two per column, overwrites
+// S's first 64 columns at head_dim 128; at head_dim 64 it has the map's last 64
+// columns, and S_g,j+1 is then issued as soon as the softmax has read S_g,j.
 // Every wait is bounded; a wait that gives up records PA_DEVERR_TIMEOUT and
 // the block drains its copies and MMAs before it frees TMEM and exits.
 #include <cuda.h>
@@ -57,8 +79,8 @@ struct DiffShape {
     static constexpr int OFF_X = OFF_V + NSLOT * SLOT_BYTES;   // the maps' exchange: [4][128] fp32
     static constexpr int DATA = OFF_X + 4 * BM * 4;
     // kfull, kempty, vfull, vempty [NSLOT]; s, read, o, p low, p high, drain [2];
-    // q, z; then the TMEM base and the abort flag
-    static constexpr int NBAR = 4 * NSLOT + 12 + 2;
+    // q, z, start; then the TMEM base and the abort flag
+    static constexpr int NBAR = 4 * NSLOT + 12 + 3;
     static constexpr int BAR_BYTES = NBAR * 8 + 8;
     // The operands are aligned up to 1024 bytes inside the dynamic allocation;
     // the barriers sit in whichever end of the 1024-byte slack has room.
@@ -149,10 +171,12 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
     auto s_bar = [&](int g) { return bar_addr + 8u * (4 * NS + g); };         // S_g,j is there
     auto read_bar = [&](int g) { return bar_addr + 8u * (4 * NS + 2 + g); };  // and has been read
     auto o_bar = [&](int g) { return bar_addr + 8u * (4 * NS + 4 + g); };     // O_g has taken P_g,j
-    auto p_bar = [&](int g, int hf) { return bar_addr + 8u * (4 * NS + 6 + 2 * hf + g); };  // half of P_g,j is there
+    // half of P_g,j is there
+    auto p_bar = [&](int g, int hf) { return bar_addr + 8u * (4 * NS + 6 + 2 * hf + g); };
     auto drain_bar = [&](int g) { return bar_addr + 8u * (4 * NS + 10 + g); };
     const uint32_t q_bar = bar_addr + 8u * (4 * NS + 12);       // the Q tile is there
     const uint32_t z_bar = bar_addr + 8u * (4 * NS + 13);       // value rows past the end are zero
+    const uint32_t start_bar = bar_addr + 8u * (4 * NS + 14);   // map 0 is half a tile ahead
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Sh::NBAR * 8);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -178,7 +202,8 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
     const int L = __ldg(p.seq_lens + s);
     const int qs = __ldg(p.query_start + s);
     const int c = __ldg(p.query_start + s + 1) - qs;
-    const bool reporter = !p.plan && rank == 0 && h == 0 && tid == 0 && cr == 0;   // the plan reports itself
+    // the plan reports itself
+    const bool reporter = !p.plan && rank == 0 && h == 0 && tid == 0 && cr == 0;
     if (L < 0 || L > p.max_blocks * kBlockSize) {
         if (reporter)
             record_error(p.err, PA_DEVERR_SEQLEN_RANGE);
@@ -221,6 +246,7 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
         }
         mbar_init(q_bar, 8);
         mbar_init(z_bar, 8);
+        mbar_init(start_bar, 4);
         *abort_flag = 0;
         mbar_init_fence();
     }
@@ -350,14 +376,14 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
             release(vempty(sl));
             return true;
         };
-        bool ok = k_ready(0) && wait_all(q_bar, 0);
+        // map 1 starts half a tile behind: the maps' softmaxes then alternate on
+        // the sub-cores and their MMAs on the tensor core (1213 us against 1281 on
+        // two 2048-token chunks at 16K, 213 against 227 on 8 x 512 tokens).  Taking
+        // turns at the exponentials tile by tile cost more than it gave (1287, 221).
+        bool ok = k_ready(0) && wait_all(q_bar, 0) && (g == 0 || wait_all(start_bar, 0));
         if (ok)
             issue_s(0);
         for (int j = 0; ok && j < nt; ++j) {
-            if (__any_sync(FULL, *abort_flag != 0)) {
-                ok = false;
-                break;
-            }
             const bool more = j + 1 < nt;
             ok = v_ready(j) && (!more || k_ready(j + 1)) &&
                  (!ragged || more || wait_all(z_bar, 0));
@@ -446,10 +472,6 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
         float m = 0.f, l = 0.f;
         bool ok = true;
         for (int j = 0; j < nt; ++j) {
-            if (__any_sync(FULL, *abort_flag != 0)) {
-                ok = false;
-                break;
-            }
             if (!__all_sync(FULL, mbar_wait_bounded(s_bar(grp), j & 1))) {
                 ok = false;
                 break;
@@ -509,9 +531,9 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
 #pragma unroll
                 for (int e = 0; e < 64; e += 2) {
                     float y0, y1;
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(v[hf][e]), __uint_as_float(v[hf][e + 1])),
-                                     sl2x2, nmx2),
-                              y0, y1);
+                    const uint64_t x2 = f2_pack(__uint_as_float(v[hf][e]),
+                                                __uint_as_float(v[hf][e + 1]));
+                    f2_unpack(f2_fma(x2, sl2x2, nmx2), y0, y1);
                     const float p0 = ex2_approx(y0);
                     const float p1 = ex2_approx(y1);
                     sum2[(e >> 1) & 3] = f2_add(sum2[(e >> 1) & 3], f2_pack(p0, p1));
@@ -543,10 +565,10 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
                         for (int idx = lt; idx < n16; idx += 256) {
                             const int row = first + idx / (Sh::HALVES * 8);
                             const int rem = idx % (Sh::HALVES * 8);
-                            *reinterpret_cast<uint4 *>(vb +
-                                                       ((rem >> 3) * Sh::NB + (row >> 4)) * Sh::BOX +
-                                                       (row & 15) * 128 + (rem & 7) * 16) =
-                                make_uint4(0, 0, 0, 0);
+                            unsigned char *at = vb +
+                                                ((rem >> 3) * Sh::NB + (row >> 4)) * Sh::BOX +
+                                                (row & 15) * 128 + (rem & 7) * 16;
+                            *reinterpret_cast<uint4 *>(at) = make_uint4(0, 0, 0, 0);
                         }
                         fence_proxy_async_shared();
                         arrive(z_bar);
@@ -566,6 +588,8 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
                 }
                 tc::fence_before_sync();
                 arrive(p_bar(grp, hf));
+                if (j == 0 && hf == 0 && grp == 0)
+                    arrive(start_bar);
             }
             if (!ok)
                 break;

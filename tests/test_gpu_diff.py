@@ -389,7 +389,7 @@ def test_serving_flow(pa, dtype, hq, hkv, d):
         bm.add_sequence(s)
     step([1, 2, 3], [60, 17, 1])
     step([1, 2], [43, 30])
-    bm.fork(1, 4)                                            # 103 tokens: a shared, part-filled block
+    bm.fork(1, 4)                        # 103 tokens: the last block is shared and part-filled
     for _ in range(3):
         step([1, 4, 2, 3], [1, 1, 1, 1])
     step([3, 4], [33, 2])

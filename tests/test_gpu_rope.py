@@ -262,7 +262,8 @@ def test_graph_replay_and_other_stream(pa):
 
 def test_binding_refusals(pa):
     x = Tokens(4, 8, 2, 64, "f16")
-    args = lambda **kw: {**dict(q_out=x.q_out, q=x.q, k_new=x.k, v_new=x.v, k_cache=x.kc,  # noqa: E731
+    args = lambda **kw: {**dict(q_out=x.q_out, q=x.q, k_new=x.k, v_new=x.v,  # noqa: E731
+                                k_cache=x.kc,
                                 v_cache=x.vc, slot_mapping=x.slots, positions=x.pos,
                                 cos_sin=x.cs), **kw}
     bad = [dict(q=x.q.cpu()), dict(positions=x.pos.long()), dict(slot_mapping=x.slots.int()),

@@ -159,7 +159,8 @@ int pa_decode(void *out, const void *q, const void *k_cache, const void *v_cache
  * are loaded.  fp32 throughout (the weights of the softmax enter the product
  * with V as two 16-bit terms each), one rounding at the end.  A sequence of
  * length 0 yields zeros.  Keys and values of live tokens must be finite; slots
- * past a sequence's end may hold anything.
+ * past a sequence's end may hold anything.  out overlaps no input (out == q is
+ * refused).
  *
  *   lambda       [num_heads] fp32
  *   norm_weight  [head_dim] dtype, 16-byte aligned, or NULL

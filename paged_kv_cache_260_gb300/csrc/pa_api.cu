@@ -622,12 +622,13 @@ int pa_decode(void *out, const void *q, const void *k_cache, const void *v_cache
 
 // The arguments that the two differential entry points share beyond those of
 // the plain ones.
-static int check_diff(const float *lambda, const void *norm_weight, float norm_eps,
-                      float out_scale, bool work)
+static int check_diff(const void *out, const void *q, const float *lambda, const void *norm_weight,
+                      float norm_eps, float out_scale, bool work)
 {
     if (!isfinite(norm_eps) || norm_eps < 0.f || !isfinite(out_scale))
         return PA_ERR_INVALID_ARG;
-    if (work && (!lambda || !aligned(lambda, 4) || !aligned(norm_weight, 16)))
+    // (out == q: a row would be written while another worker still reads its queries)
+    if (work && (!lambda || !aligned(lambda, 4) || !aligned(norm_weight, 16) || (q && out == q)))
         return PA_ERR_INVALID_ARG;
     return PA_OK;
 }
@@ -649,7 +650,7 @@ int pa_diff_decode(void *out, const void *q, const void *k_cache, const void *v_
                    float scale, float norm_eps, float out_scale, int dtype, void *workspace,
                    size_t workspace_bytes, void *stream)
 {
-    const int rc = check_diff(lambda, norm_weight, norm_eps, out_scale, num_seqs > 0);
+    const int rc = check_diff(out, q, lambda, norm_weight, norm_eps, out_scale, num_seqs > 0);
     if (rc != PA_OK)
         return rc;
     // an empty batch has no factors to read, but its other arguments are checked as ever
@@ -1078,7 +1079,7 @@ int pa_diff_prefill(void *out, const void *q, const void *k_cache, const void *v
                     float norm_eps, float out_scale, int dtype, void *workspace,
                     size_t workspace_bytes, void *stream)
 {
-    const int rc = check_diff(lambda, norm_weight, norm_eps, out_scale,
+    const int rc = check_diff(out, q, lambda, norm_weight, norm_eps, out_scale,
                               num_seqs > 0 && max_query_len > 0);
     if (rc != PA_OK)
         return rc;

@@ -20,7 +20,7 @@ def lib():
 
 
 def _decode(lib, **kw):
-    a = dict(out=FAKE, q=FAKE, k=FAKE, v=FAKE, tables=FAKE, lens=FAKE, lam=FAKE, w=None, n=4, hq=8,
+    a = dict(out=0x2000, q=FAKE, k=FAKE, v=FAKE, tables=FAKE, lens=FAKE, lam=FAKE, w=None, n=4, hq=8,
              hkv=2, d=128, bs=16, mb=8, nb=64, scale=0.1, eps=1e-6, os=1.0, dtype=0, ws=None,
              wb=0)
     a.update(kw)
@@ -29,7 +29,7 @@ def _decode(lib, **kw):
 
 
 def _prefill(lib, **kw):
-    a = dict(out=FAKE, q=FAKE, k=FAKE, v=FAKE, tables=FAKE, lens=FAKE, start=FAKE, lam=FAKE, w=None,
+    a = dict(out=0x2000, q=FAKE, k=FAKE, v=FAKE, tables=FAKE, lens=FAKE, start=FAKE, lam=FAKE, w=None,
              n=4, longest=32, hq=8, hkv=2, d=128, bs=16, mb=8, nb=64, scale=0.1, eps=1e-6, os=1.0,
              dtype=0, ws=None, wb=0)
     a.update(kw)
@@ -42,7 +42,7 @@ def _prefill(lib, **kw):
     (dict(d=96), 2), (dict(bs=8), 2), (dict(dtype=3), 2), (dict(hq=7), 1), (dict(n=-1), 1),
     (dict(mb=0), 1), (dict(nb=0), 1), (dict(hkv=0), 1), (dict(scale=math.nan), 1),
     (dict(eps=-1.0), 1), (dict(eps=math.inf), 1), (dict(os=math.nan), 1), (dict(lam=None), 1),
-    (dict(lam=0x1002), 1), (dict(w=0x1008), 1), (dict(q=None), 1), (dict(out=None), 1),
+    (dict(lam=0x1002), 1), (dict(w=0x1008), 1), (dict(q=None), 1), (dict(out=None), 1), (dict(out=FAKE), 1),
     (dict(q=0x1008), 1), (dict(tables=None), 1), (dict(lens=0x1001), 1),
     (dict(n=0, lam=None), 0), (dict(n=0, d=96), 2)])
 def test_both_refuse(lib, call, kw, status):

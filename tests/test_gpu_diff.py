@@ -187,6 +187,35 @@ def test_prefill_longer(pa, hq, hkv, d, dtype):
     x.check(x.prefill(pa))
 
 
+@pytest.mark.parametrize("hq,chunks", [(96, [3, 1, 2]), (128, [3, 1, 2]), (128, [1, 1, 1]),
+                                       (43, [7, 1, 2])])
+def test_prefill_wide_groups(pa, hq, chunks):
+    # one token's heads, or a few, fill a query tile
+    x = Pool([200, 1, 130], hq, 1, 64, "bf16", chunks=chunks, seed=hq)
+    x.check(x.prefill(pa))
+
+
+@pytest.mark.parametrize("plan", [True, False])
+@pytest.mark.parametrize("longest", [20, 64])
+def test_prefill_longest_chunk_understated(pa, plan, longest):
+    """A chunk longer than max_query_len is reported, its last rows are right, no row
+    outside it is touched; the other sequences are whole."""
+    x = Pool([400, 90], 8, 2, 128, "f16", chunks=[300, 15], seed=8)
+    out = x.prefill(pa, longest=longest, workspace="auto" if plan else None)
+    assert pa.get_device_error() == pa.DEVERR["QUERY_RANGE"]
+    good = out.clone()
+    x.check(x.prefill(pa))
+    same = (good == out).flatten(1).all(1)
+    assert bool(same[300:].all()) and bool(same[288:300].all())   # from the last whole tile on
+    assert bool((good[~same] == 7).all())
+
+
+def test_decode_negative_scale(pa):
+    x = Pool([40, 300, 17], 8, 2, 128, "bf16", seed=12)
+    x.scale = -x.scale
+    x.check(x.decode(pa))
+
+
 def test_prefill_rows_outside_chunks_stay(pa):
     x = Pool([50, 20], 8, 2, 64, "f16", chunks=[30, 20])
     x.prefill(pa)

@@ -167,8 +167,8 @@ int pa_decode(void *out, const void *q, const void *k_cache, const void *v_cache
  *   norm_eps     finite, >= 0; out_scale finite
  *   scale        typically 1/sqrt(head_dim / 2)
  *   workspace    at least pa_diff_decode_workspace_size(...) bytes, else as pa_decode
- * Groups of 1..8 heads per kv head (PA_ERR_UNSUPPORTED beyond).  Other
- * arguments, the split (that of partition_size 0), launches and errors as pa_decode.
+ * Other arguments, the groups of 1..16 heads per kv head, the split (that of
+ * partition_size 0), launches and errors as pa_decode.
  */
 size_t pa_diff_decode_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
                                      int max_blocks_per_seq);

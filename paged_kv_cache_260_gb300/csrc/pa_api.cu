@@ -425,7 +425,7 @@ static int decode_impl(void *out, const void *q, const void *k_cache, const void
         return PA_ERR_INVALID_ARG;
     const int group = num_heads / num_kv_heads;
     const bool diff = x.lambda != nullptr;
-    if (group > (diff ? kMaxDiffGroup : kMaxGroup))
+    if (group > kMaxGroup)
         return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0)
         return PA_OK;

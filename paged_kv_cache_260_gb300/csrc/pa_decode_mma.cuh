@@ -43,7 +43,7 @@
 //    of its channels, column 2 the reverse, so K and V leave HBM once for both
 //    and the loop below stays as it is.  Groups of up to 4 heads fit one
 //    8-column tile (columns 0-3 map 1, 4-7 map 2); 5 to 8 heads take a tile
-//    for each map, and each tile runs the k-steps of its own half alone.
+//    for each map, 9 to 16 two, and a tile runs the k-steps of its own half alone.
 //    The difference cancels what the maps share, and with it part of the
 //    result that a rounding of P is relative to; so P enters the second
 //    product as two 16-bit terms, its rounded value and the rounded rest.
@@ -63,7 +63,9 @@ namespace pa {
 template <int D, int NT, bool DIFF = false>
 struct MmaShape {
     static_assert(D == 64 || D == 128, "head_dim");
-    static_assert(NT == 1 || NT == 2, "query columns: 8 or 16");
+    static_assert(NT == 1 || NT == 2 || (DIFF && NT == 4), "query columns: 8, 16, or 32");
+    // differential attention with more than one column tile: tiles of each map
+    static constexpr int MT = NT == 1 ? 1 : NT / 2;
     static constexpr int NB = D / 64;                         // 64-column boxes per tile
     static constexpr int BOX = kBlockSize * 128;              // bytes of one box (16 rows x 128 B)
     static constexpr int TILE = NB * BOX;                     // bytes of K (or V) per tile
@@ -197,60 +199,64 @@ __device__ __forceinline__ void diff_whole(const DecodeParams &p, const float (&
 {
     using E = Elem<T>;
     constexpr uint32_t FULL = 0xffffffffu;
-    constexpr int KS = D / 16, ROWS = NT == 1 ? KS / 2 : KS;
+    constexpr int KS = D / 16, ROWS = NT == 1 ? KS / 2 : KS, MT = NT == 1 ? 1 : NT / 2;
     const int map = NT == 1 ? qd >> 1 : 0;
-    const int h0 = NT == 1 ? (2 * qd & 3) : 2 * qd, h1 = h0 + 1;
-    const float lam0 = h0 < G ? __ldg(p.lambda + h * G + h0) : 0.f;
-    const float lam1 = h1 < G ? __ldg(p.lambda + h * G + h1) : 0.f;
-    float y[ROWS][4];
-    if constexpr (NT == 1) {
-        const float f0 = (map ? -lam0 : 1.f) / l[0][0], f1 = (map ? -lam1 : 1.f) / l[0][1];
 #pragma unroll
-        for (int mt = 0; mt < ROWS; ++mt)
+    for (int t = 0; t < MT; ++t) {                // column tiles of a map
+        const int h0 = NT == 1 ? (2 * qd & 3) : 8 * t + 2 * qd, h1 = h0 + 1;
+        const float lam0 = h0 < G ? __ldg(p.lambda + h * G + h0) : 0.f;
+        const float lam1 = h1 < G ? __ldg(p.lambda + h * G + h1) : 0.f;
+        float y[ROWS][4];
+        if constexpr (NT == 1) {
+            const float f0 = (map ? -lam0 : 1.f) / l[0][0], f1 = (map ? -lam1 : 1.f) / l[0][1];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float f = c & 1 ? f1 : f0;
-                const float lo = o[0][mt][c] * f, hi = o[0][mt + ROWS][c] * f;
-                y[mt][c] = (map ? hi : lo) + __shfl_xor_sync(FULL, map ? lo : hi, 2);
+            for (int mt = 0; mt < ROWS; ++mt)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float f = c & 1 ? f1 : f0;
+                    const float lo = o[0][mt][c] * f, hi = o[0][mt + ROWS][c] * f;
+                    y[mt][c] = (map ? hi : lo) + __shfl_xor_sync(FULL, map ? lo : hi, 2);
+                }
+        } else {
+            const float f0 = 1.f / l[t][0], f1 = 1.f / l[t][1];
+            const float g0 = -lam0 / l[MT + t][0], g1 = -lam1 / l[MT + t][1];
+#pragma unroll
+            for (int mt = 0; mt < ROWS; ++mt)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    y[mt][c] = fmaf(o[MT + t][mt][c], c & 1 ? g1 : g0,
+                                    o[t][mt][c] * (c & 1 ? f1 : f0));
+        }
+        float k0 = p.out_scale, k1 = p.out_scale;
+        const T *w = static_cast<const T *>(p.norm_w);
+        if (w) {
+            float q0 = 0.f, q1 = 0.f;
+#pragma unroll
+            for (int mt = 0; mt < ROWS; ++mt) {
+                q0 = fmaf(y[mt][0], y[mt][0], fmaf(y[mt][2], y[mt][2], q0));
+                q1 = fmaf(y[mt][1], y[mt][1], fmaf(y[mt][3], y[mt][3], q1));
             }
-    } else {
-        const float f0 = 1.f / l[0][0], f1 = 1.f / l[0][1];
-        const float g0 = -lam0 / l[NT - 1][0], g1 = -lam1 / l[NT - 1][1];
 #pragma unroll
-        for (int mt = 0; mt < ROWS; ++mt)
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                y[mt][c] = fmaf(o[NT - 1][mt][c], c & 1 ? g1 : g0, o[0][mt][c] * (c & 1 ? f1 : f0));
-    }
-    float k0 = p.out_scale, k1 = p.out_scale;
-    const T *w = static_cast<const T *>(p.norm_w);
-    if (w) {
-        float q0 = 0.f, q1 = 0.f;
+            for (int off = NT == 1 ? 2 : 4; off < 32; off <<= 1) {
+                q0 += __shfl_xor_sync(FULL, q0, off);
+                q1 += __shfl_xor_sync(FULL, q1, off);
+            }
+            k0 *= rsqrtf(q0 * (1.f / D) + p.norm_eps);
+            k1 *= rsqrtf(q1 * (1.f / D) + p.norm_eps);
+        }
+        T *out = static_cast<T *>(p.out) + ((size_t)s * p.num_heads + h * G) * D;
 #pragma unroll
         for (int mt = 0; mt < ROWS; ++mt) {
-            q0 = fmaf(y[mt][0], y[mt][0], fmaf(y[mt][2], y[mt][2], q0));
-            q1 = fmaf(y[mt][1], y[mt][1], fmaf(y[mt][3], y[mt][3], q1));
-        }
-#pragma unroll
-        for (int off = NT == 1 ? 2 : 4; off < 32; off <<= 1) {
-            q0 += __shfl_xor_sync(FULL, q0, off);
-            q1 += __shfl_xor_sync(FULL, q1, off);
-        }
-        k0 *= rsqrtf(q0 * (1.f / D) + p.norm_eps);
-        k1 *= rsqrtf(q1 * (1.f / D) + p.norm_eps);
-    }
-    T *out = static_cast<T *>(p.out) + ((size_t)s * p.num_heads + h * G) * D;
-#pragma unroll
-    for (int mt = 0; mt < ROWS; ++mt) {
-        const int d0 = 16 * (mt + map * ROWS) + r;
-        const float w0 = w ? E::to_f(w[d0]) : 1.f, w8 = w ? E::to_f(w[d0 + 8]) : 1.f;
-        if (h0 < G) {
-            out[h0 * D + d0] = E::from_f(y[mt][0] * (k0 * w0));
-            out[h0 * D + d0 + 8] = E::from_f(y[mt][2] * (k0 * w8));
-        }
-        if (h1 < G) {
-            out[h1 * D + d0] = E::from_f(y[mt][1] * (k1 * w0));
-            out[h1 * D + d0 + 8] = E::from_f(y[mt][3] * (k1 * w8));
+            const int d0 = 16 * (mt + map * ROWS) + r;
+            const float w0 = w ? E::to_f(w[d0]) : 1.f, w8 = w ? E::to_f(w[d0 + 8]) : 1.f;
+            if (h0 < G) {
+                out[h0 * D + d0] = E::from_f(y[mt][0] * (k0 * w0));
+                out[h0 * D + d0 + 8] = E::from_f(y[mt][2] * (k0 * w8));
+            }
+            if (h1 < G) {
+                out[h1 * D + d0] = E::from_f(y[mt][1] * (k1 * w0));
+                out[h1 * D + d0 + 8] = E::from_f(y[mt][3] * (k1 * w8));
+            }
         }
     }
 }
@@ -267,8 +273,9 @@ __device__ __forceinline__ void diff_piece(const DecodeParams &p, const float (&
     for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int map = NT == 1 ? qd >> 1 : j;
-            const int hq = (NT == 1 ? (2 * qd & 3) : 2 * qd) + e;
+            constexpr int MT = NT == 1 ? 1 : NT / 2;
+            const int map = NT == 1 ? qd >> 1 : j / MT;
+            const int hq = (NT == 1 ? (2 * qd & 3) : 8 * (j % MT) + 2 * qd) + e;
             if (hq >= G)
                 continue;
             const size_t row = slot_row(2 * G, slot, map * G + hq);
@@ -471,8 +478,8 @@ __device__ __forceinline__ void decode_worker(const DecodeParams &p, const CUten
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
                     // B column: query head of the group (and map)
-                    const int hq = !DIFF ? 8 * j + r : NT == 1 ? (r & 3) : r;
-                    const int map = NT == 1 ? r >> 2 : j;
+                    const int hq = !DIFF ? 8 * j + r : NT == 1 ? (r & 3) : 8 * (j % Sh::MT) + r;
+                    const int map = NT == 1 ? r >> 2 : j / Sh::MT;
                     const uint32_t *qrow = reinterpret_cast<const uint32_t *>(qs + (size_t)hq * D * 2);
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks) {
@@ -514,7 +521,7 @@ __device__ __forceinline__ void decode_worker(const DecodeParams &p, const CUten
                 ldsm_x4(kst + (ks >> 2) * Sh::BOX + swz(krow, 2 * (ks & 3) + kcs), a[0], a[1], a[2], a[3]);
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
-                    if (!DIFF || NT == 1 || ks / (KS / 2) == j)
+                    if (!DIFF || NT == 1 || ks / (KS / 2) == j / Sh::MT)
                         M::run((ks & 1) ? sb[j] : sa[j], a, qf[j][ks][0], qf[j][ks][1]);
             }
             const bool masked = nvalid < kBlockSize;
@@ -1018,7 +1025,7 @@ __global__ void __launch_bounds__(512) merge_part_kernel(const DecodeParams p)
 // head g's two maps, takes the difference and the norm and writes the output
 // row, lane by lane D/32 channels.
 template <typename T, int D>
-__global__ void __launch_bounds__(32 * kMaxDiffGroup) merge_cut_diff_kernel(const DecodeParams p)
+__global__ void __launch_bounds__(32 * kMaxGroup) merge_cut_diff_kernel(const DecodeParams p)
 {
     constexpr int V = D / 32;
     constexpr int CH = 4;
@@ -1113,8 +1120,15 @@ __global__ void __launch_bounds__(32 * kMaxDiffGroup) merge_cut_diff_kernel(cons
 template <typename T, int D, int NT>
 inline void fill_diff_kernel_set(KernelSet *ks)
 {
+    // Warps per SM, measured on four sequences of 32K to 131K tokens (K/V floor
+    // 201 us): D=128 with one column tile 7 (209 us; 6 and 8 to 10 between 208 and
+    // 227 over runs, and 7 the fastest on the batch-128 lengths, 81.1 us against
+    // 82 to 85), two tiles 8 (216; 7 224, 9 231, 6 255), four tiles 8 (290; 7 320),
+    // where the MMAs and not HBM set the time; D=64 12 (205), 12 (211; 11 239,
+    // 13 222) and 8 (333; 7 373, 9 402).  P's second term costs a microsecond of
+    // the batch (80.2 without).
     constexpr int S = 2;
-    constexpr int W = D == 128 ? 7 : 12;
+    constexpr int W = D == 128 ? (NT == 1 ? 7 : 8) : (NT == 4 ? 8 : 12);
     ks->decode = reinterpret_cast<const void *>(&decode_mma_kernel<T, D, NT, W, S, false, true>);
     ks->warps = W;
     ks->smem_fixed = MmaLayout<D, NT, W, S, true>::fixed;
@@ -1123,13 +1137,24 @@ inline void fill_diff_kernel_set(KernelSet *ks)
     ks->merge_cut = reinterpret_cast<const void *>(&merge_cut_diff_kernel<T, D>);
 }
 
+template <typename T, int D>
+inline void fill_diff_kernel_set(int group, KernelSet *ks)
+{
+    if (group <= 4)
+        fill_diff_kernel_set<T, D, 1>(ks);
+    else if (group <= 8)
+        fill_diff_kernel_set<T, D, 2>(ks);
+    else
+        fill_diff_kernel_set<T, D, 4>(ks);
+}
+
 template <typename T>
 inline bool diff_kernels(int head_dim, int group, KernelSet *ks)
 {
     if (head_dim == 128)
-        group <= 4 ? fill_diff_kernel_set<T, 128, 1>(ks) : fill_diff_kernel_set<T, 128, 2>(ks);
+        fill_diff_kernel_set<T, 128>(group, ks);
     else if (head_dim == 64)
-        group <= 4 ? fill_diff_kernel_set<T, 64, 1>(ks) : fill_diff_kernel_set<T, 64, 2>(ks);
+        fill_diff_kernel_set<T, 64>(group, ks);
     else
         return false;
     return true;

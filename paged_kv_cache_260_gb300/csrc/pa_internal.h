@@ -101,14 +101,13 @@ constexpr int kMinTiles = 2;          // split modes: least tiles per worker (wa
 constexpr int kWholeMaxBlocks = 8;
 constexpr int kWholeRunsPerSM = 4;
 constexpr int kMaxGroup = 16;         // query heads per kv head: two 8-column tiles
-constexpr int kMaxDiffGroup = 8;      // differential attention: two query columns a head
 
 bool decode_kernels_f16(int head_dim, KernelSet *ks);       // groups 1..8
 bool decode_kernels_bf16(int head_dim, KernelSet *ks);
 bool decode_kernels_f16_g16(int head_dim, KernelSet *ks);   // groups 9..16
 bool decode_kernels_bf16_g16(int head_dim, KernelSet *ks);
 // differential attention, `group` heads per kv head: 1..4 share one column
-// tile between the two maps, 5..8 take one for each
+// tile between the two maps, 5..8 take one for each, 9..16 two
 bool diff_decode_kernels_f16(int head_dim, int group, KernelSet *ks);
 bool diff_decode_kernels_bf16(int head_dim, int group, KernelSet *ks);
 

@@ -50,7 +50,8 @@ def test_both_refuse(lib, call, kw, status):
 
 
 def test_decode_refuses_wide_groups(lib):
-    assert _decode(lib, hq=18) == 2                          # group 9
+    assert _decode(lib, hq=34) == 2                          # group 17
+    assert _decode(lib, hq=32, q=None) == 1                  # group 16 is served
     assert lib.pa_diff_decode_workspace_size(0, 8, 2, 128, 8) == 0
     assert lib.pa_diff_decode_workspace_size(4, 7, 2, 128, 8) == 0
     assert lib.pa_diff_decode_workspace_size(4, 2 ** 31 - 2, 2, 128, 8) == 0

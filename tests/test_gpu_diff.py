@@ -92,7 +92,8 @@ LENS = [0, 1, 2, 15, 16, 17, 31, 33, 100, 257, 700, 1029]
 @pytest.mark.parametrize("hq,hkv,d,dtype", [
     (2, 2, 64, "f16"), (8, 8, 128, "bf16"), (4, 2, 128, "f16"), (6, 2, 64, "bf16"),
     (32, 8, 128, "bf16"), (4, 1, 64, "f16"), (5, 1, 128, "f16"), (12, 2, 64, "bf16"),
-    (7, 1, 64, "f16"), (16, 2, 128, "bf16"), (24, 3, 64, "f16")])
+    (7, 1, 64, "f16"), (16, 2, 128, "bf16"), (24, 3, 64, "f16"), (9, 1, 128, "f16"),
+    (16, 1, 64, "bf16"), (26, 2, 128, "bf16"), (30, 2, 64, "f16"), (16, 1, 128, "f16")])
 def test_decode_ragged(pa, hq, hkv, d, dtype, norm):
     x = Pool(LENS, hq, hkv, d, dtype, norm=norm, seed=hq + d)
     x.check(x.decode(pa))
@@ -101,7 +102,7 @@ def test_decode_ragged(pa, hq, hkv, d, dtype, norm):
 
 
 @pytest.mark.parametrize("hq,hkv,d,dtype", [(8, 8, 64, "f16"), (8, 2, 128, "bf16"),
-                                            (10, 2, 128, "f16")])
+                                            (10, 2, 128, "f16"), (24, 2, 64, "bf16")])
 @pytest.mark.parametrize("lens", [[1], [16], [100, 3, 0, 77], [128] * 4])
 def test_decode_short_runs_are_not_split(pa, hq, hkv, d, dtype, lens):
     x = Pool(lens, hq, hkv, d, dtype, seed=len(lens), maxb=8)
@@ -109,7 +110,8 @@ def test_decode_short_runs_are_not_split(pa, hq, hkv, d, dtype, lens):
     assert pa.get_device_error() == 0
 
 
-@pytest.mark.parametrize("hq,hkv,d,dtype", [(4, 1, 128, "bf16"), (8, 1, 64, "f16")])
+@pytest.mark.parametrize("hq,hkv,d,dtype", [(4, 1, 128, "bf16"), (8, 1, 64, "f16"),
+                                            (13, 1, 128, "bf16")])
 def test_decode_one_long_sequence(pa, hq, hkv, d, dtype):
     x = Pool([20011], hq, hkv, d, dtype, seed=5)             # cut across every worker
     x.check(x.decode(pa))
@@ -350,9 +352,9 @@ def test_refusals(pa):
         big.decode(pa, workspace=torch.empty(need - 256, dtype=torch.uint8, device="cuda"))
     assert e.value.status == 3
     big.check(big.decode(pa, workspace=torch.empty(need, dtype=torch.uint8, device="cuda")))
-    g9 = Pool([40], 9, 1, 64, "f16")
+    g17 = Pool([40], 17, 1, 64, "f16")
     with pytest.raises(pa.PagedAttnError) as e:
-        g9.decode(pa)
+        g17.decode(pa)
     assert e.value.status == 2
     torch.cuda.synchronize()
     assert bool((x.out == 7).all())                          # nothing was launched

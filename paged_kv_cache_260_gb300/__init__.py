@@ -23,8 +23,8 @@ __all__ = [
     "decode_shared_prefix_workspace_size", "diff_decode", "diff_decode_workspace_size",
     "diff_decode_workspace_for", "prefill", "prefill_workspace_size", "diff_prefill",
     "diff_prefill_workspace_size", "diff_prefill_workspace_for",
-    "reshape_and_cache", "rope_and_cache", "qk_norm_rope", "copy_blocks", "swap_blocks", "gather_kv",
-    "validate_tables", "selftest_bounded_wait", "get_device_error",
+    "reshape_and_cache", "rope_and_cache", "qk_norm_rope", "copy_blocks", "swap_blocks",
+    "gather_kv", "validate_tables", "selftest_bounded_wait", "get_device_error",
     "PA_DTYPE_F16", "PA_DTYPE_BF16", "DEVERR", "STATUS",
 ]
 
@@ -164,6 +164,27 @@ def _stream(stream):
         else:
             _current_raw_stream = lambda: torch.cuda.current_stream().cuda_stream
     return _current_raw_stream()
+
+
+class _Names:
+    """What the hot wrappers look up in torch, once."""
+
+    def __init__(self):
+        torch = _torch()
+        self.i32, self.i64, self.f32 = torch.int32, torch.int64, torch.float32
+        self.codes = {torch.float16: PA_DTYPE_F16, torch.bfloat16: PA_DTYPE_BF16}
+        self.device = torch._C._cuda_getDevice
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+_names = None
+
+
+def _hot():
+    global _names
+    if _names is None:
+        _names = _Names()
+    return _names
 
 
 def _scratch(nbytes, device, stream):
@@ -324,19 +345,61 @@ def prefill(out, q, k_cache, v_cache, block_tables, seq_lens, query_start, max_q
     return out
 
 
-def _diff_pointers(out, q, k_cache, v_cache, block_tables, seq_lens, lam, norm_weight):
+_NEAR = "tensors must be contiguous, of the right type and on the current CUDA device"
+
+
+def _near(t, dtype, device):
+    """The address of a contiguous tensor of this type on this device."""
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(_NEAR)
+    return t.data_ptr()
+
+
+def _current(t, names):
+    """The device of t, which has to be the current one."""
+    dev = t.get_device()
+    if dev < 0 or dev != names.device():
+        raise ValueError("tensors must be on the current CUDA device")
+    return dev
+
+
+def _code(dtype, names):
+    code = names.codes.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
+
+
+def _weights(w, size, dtype, device):
+    """The address of optional norm weights [size]."""
+    if w is None:
+        return None
+    if w.shape != (size,):
+        raise ValueError(f"norm weights: [{size}]")
+    return _near(w, dtype, device)
+
+
+def _diff_pointers(out, q, k_cache, v_cache, block_tables, seq_lens, lam, norm_weight, names):
     """Checks what diff_decode and diff_prefill share; the device and the addresses."""
-    torch = _torch()
-    i32 = torch.int32
+    i32 = names.i32
     shape, pool, tables = q.shape, k_cache.shape, block_tables.shape
-    dt, dev = q.dtype, _current(q)
+    dt, dev = q.dtype, _current(q, names)
     if (out.shape != shape or pool[3] != shape[2] or v_cache.shape != pool or len(tables) != 2 or
             seq_lens.shape != tables[:1] or lam.shape != shape[1:2]):
         raise ValueError("shapes")
-    return dev, (_near(out, dt, dev), _near(q, dt, dev), _near(k_cache, dt, dev),
-                 _near(v_cache, dt, dev), _near(block_tables, i32, dev),
-                 _near(seq_lens, i32, dev)), (_near(lam, torch.float32, dev),
-                                              _weights(norm_weight, shape[2], dt, dev))
+    if (out.dtype is not dt or k_cache.dtype is not dt or v_cache.dtype is not dt or
+            block_tables.dtype is not i32 or seq_lens.dtype is not i32 or
+            lam.dtype is not names.f32 or out.get_device() != dev or
+            k_cache.get_device() != dev or v_cache.get_device() != dev or
+            block_tables.get_device() != dev or seq_lens.get_device() != dev or
+            lam.get_device() != dev or
+            not (q.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous() and
+                 v_cache.is_contiguous() and block_tables.is_contiguous() and
+                 seq_lens.is_contiguous() and lam.is_contiguous())):
+        raise ValueError(_NEAR)
+    w = None if norm_weight is None else _weights(norm_weight, shape[2], dt, dev)
+    return dev, (out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                 block_tables.data_ptr(), seq_lens.data_ptr()), (lam.data_ptr(), w)
 
 
 def _bytes_of(workspace, dev):
@@ -371,15 +434,17 @@ def diff_decode(out, q, k_cache, v_cache, block_tables, seq_lens, lam, scale, no
     nb, hkv, bs, _ = k_cache.shape
     if seq_lens.shape != (n,):
         raise ValueError("shapes")
+    names = _hot()
     dev, at, factors = _diff_pointers(out, q, k_cache, v_cache, block_tables, seq_lens, lam,
-                                      norm_weight)
+                                      norm_weight, names)
     if workspace is None:
         workspace = diff_decode_workspace_for(q, k_cache, block_tables, stream)
     wptr, wbytes = ((None, 0) if workspace is None else
                     (workspace.data_ptr(), _bytes_of(workspace, dev)))
     rc = load().pa_diff_decode(*at, *factors, n, hq, hkv, d, bs, block_tables.shape[1], nb,
-                               float(scale), float(eps), float(out_scale), _dtype_code(q), wptr,
-                               wbytes, _stream(stream))
+                               float(scale), float(eps), float(out_scale),
+                               _code(q.dtype, names), wptr, wbytes,
+                               names.raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         raise PagedAttnError("pa_diff_decode", rc)
     return out
@@ -409,16 +474,17 @@ def diff_prefill(out, q, k_cache, v_cache, block_tables, seq_lens, query_start, 
     n, longest = seq_lens.shape[0], int(max_query_len)
     if query_start.shape != (n + 1,):
         raise ValueError("shapes")
+    names = _hot()
     dev, at, factors = _diff_pointers(out, q, k_cache, v_cache, block_tables, seq_lens, lam,
-                                      norm_weight)
+                                      norm_weight, names)
     if isinstance(workspace, str):
         workspace = diff_prefill_workspace_for(q, k_cache, seq_lens, longest, stream)
     wptr, wbytes = ((None, 0) if workspace is None else
                     (workspace.data_ptr(), _bytes_of(workspace, dev)))
-    rc = load().pa_diff_prefill(*at, _near(query_start, _torch().int32, dev), *factors, n, longest,
-                                hq, hkv, d, bs, block_tables.shape[1], nb, float(scale),
-                                float(eps), float(out_scale), _dtype_code(q), wptr, wbytes,
-                                _stream(stream))
+    rc = load().pa_diff_prefill(*at, _near(query_start, names.i32, dev), *factors, n, longest, hq,
+                                hkv, d, bs, block_tables.shape[1], nb, float(scale), float(eps),
+                                float(out_scale), _code(q.dtype, names), wptr, wbytes,
+                                names.raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         raise PagedAttnError("pa_diff_prefill", rc)
     return out
@@ -456,9 +522,6 @@ def reshape_and_cache(k_new, v_new, k_cache, v_cache, slot_mapping, stream=None)
     _check("pa_reshape_and_cache", rc)
 
 
-_NEAR = "tensors must be contiguous, of the right type and on the current CUDA device"
-
-
 def _rows(t, shape, dtype, device):
     """Elements between the tokens of [tokens, heads, head_dim] rows whose heads lie
     one after the other (any distance between tokens: slices of a projection's output)."""
@@ -469,30 +532,6 @@ def _rows(t, shape, dtype, device):
         raise ValueError(f"rows: {tuple(shape)} of {dtype} on device {device}, a token's heads "
                          "one after the other")
     return st if n > 1 else h * d
-
-
-def _near(t, dtype, device):
-    """The address of a contiguous tensor of this type on this device."""
-    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
-        raise ValueError(_NEAR)
-    return t.data_ptr()
-
-
-def _current(t):
-    """The device of t, which has to be the current one."""
-    dev = t.get_device()
-    if dev < 0 or dev != _torch()._C._cuda_getDevice():
-        raise ValueError("tensors must be on the current CUDA device")
-    return dev
-
-
-def _weights(w, size, dtype, device):
-    """The address of optional norm weights [size]."""
-    if w is None:
-        return None
-    if w.shape != (size,):
-        raise ValueError(f"norm weights: [{size}]")
-    return _near(w, dtype, device)
 
 
 def rope_and_cache(q_out, q, k_new, v_new, k_cache, v_cache, slot_mapping, positions, cos_sin,
@@ -509,23 +548,33 @@ def rope_and_cache(q_out, q, k_new, v_new, k_cache, v_cache, slot_mapping, posit
         cos_sin = torch.cat([a.cos(), a.sin()], 1).float()
     num_maps=2 treats a head as two keys of half its size (differential attention).
     """
-    torch = _torch()
+    names = _hot()
     n, hq, d = q_shape = q.shape
     nb, hkv, bs, d2 = pool = k_cache.shape
     table, rot = cos_sin.shape
     new = (n, hkv, d)
-    dt, dev, num_maps = q.dtype, _current(q), int(num_maps)
-    seg = d // num_maps if num_maps > 0 else 0
+    dt, dev, num_maps = q.dtype, _current(q, names), int(num_maps)
     if d2 != d or v_cache.shape != pool or positions.shape != (n,) or slot_mapping.shape != (n,):
         raise ValueError("shapes")
+    if (k_cache.dtype is not dt or v_cache.dtype is not dt or
+            slot_mapping.dtype is not names.i64 or positions.dtype is not names.i32 or
+            cos_sin.dtype is not names.f32 or k_cache.get_device() != dev or
+            v_cache.get_device() != dev or slot_mapping.get_device() != dev or
+            positions.get_device() != dev or cos_sin.get_device() != dev or
+            not (k_cache.is_contiguous() and v_cache.is_contiguous() and
+                 slot_mapping.is_contiguous() and positions.is_contiguous() and
+                 cos_sin.is_contiguous())):
+        raise ValueError(_NEAR)
+    seg = d // num_maps if num_maps > 0 else 0
+    qw = None if q_norm is None else _weights(q_norm, seg, dt, dev)
+    kw = None if k_norm is None else _weights(k_norm, seg, dt, dev)
     rc = load().pa_rope_and_cache(
-        q_out.data_ptr(), q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
-        _near(k_cache, dt, dev), _near(v_cache, dt, dev), _near(slot_mapping, torch.int64, dev),
-        _near(positions, torch.int32, dev), _near(cos_sin, torch.float32, dev),
-        _weights(q_norm, seg, dt, dev), _weights(k_norm, seg, dt, dev), n, hq, hkv, d, num_maps,
-        bs, nb, table, rot, 1 if interleaved else 0, float(eps), _rows(q, q_shape, dt, dev),
-        _rows(k_new, new, dt, dev), _rows(v_new, new, dt, dev), _rows(q_out, q_shape, dt, dev),
-        _dtype_code(q), _stream(stream))
+        q_out.data_ptr(), q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), cos_sin.data_ptr(), qw,
+        kw, n, hq, hkv, d, num_maps, bs, nb, table, rot, 1 if interleaved else 0, float(eps),
+        _rows(q, q_shape, dt, dev), _rows(k_new, new, dt, dev), _rows(v_new, new, dt, dev),
+        _rows(q_out, q_shape, dt, dev), _code(dt, names),
+        names.raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         raise PagedAttnError("pa_rope_and_cache", rc)
     return q_out
@@ -536,22 +585,27 @@ def qk_norm_rope(q_out, k_out, q, k, positions, cos_sin, q_norm=None, k_norm=Non
     """pa_qk_norm_rope: rope_and_cache's normalisation and rotation without the pool, for
     decode_append and decode_shared_prefix, which write the new tokens themselves.
     q_out may be q and k_out may be k."""
-    torch = _torch()
+    names = _hot()
     n, hq, d = q_shape = q.shape
     hkv = k.shape[1]
     table, rot = cos_sin.shape
     new = (n, hkv, d)
-    dt, dev, num_maps = q.dtype, _current(q), int(num_maps)
-    seg = d // num_maps if num_maps > 0 else 0
+    dt, dev, num_maps = q.dtype, _current(q, names), int(num_maps)
     if positions.shape != (n,):
         raise ValueError("shapes")
+    if (positions.dtype is not names.i32 or cos_sin.dtype is not names.f32 or
+            positions.get_device() != dev or cos_sin.get_device() != dev or
+            not (positions.is_contiguous() and cos_sin.is_contiguous())):
+        raise ValueError(_NEAR)
+    seg = d // num_maps if num_maps > 0 else 0
+    qw = None if q_norm is None else _weights(q_norm, seg, dt, dev)
+    kw = None if k_norm is None else _weights(k_norm, seg, dt, dev)
     rc = load().pa_qk_norm_rope(
-        q_out.data_ptr(), k_out.data_ptr(), q.data_ptr(), k.data_ptr(),
-        _near(positions, torch.int32, dev), _near(cos_sin, torch.float32, dev),
-        _weights(q_norm, seg, dt, dev), _weights(k_norm, seg, dt, dev), n, hq, hkv, d, num_maps,
-        table, rot, 1 if interleaved else 0, float(eps), _rows(q, q_shape, dt, dev),
-        _rows(k, new, dt, dev), _rows(q_out, q_shape, dt, dev), _rows(k_out, new, dt, dev),
-        _dtype_code(q), _stream(stream))
+        q_out.data_ptr(), k_out.data_ptr(), q.data_ptr(), k.data_ptr(), positions.data_ptr(),
+        cos_sin.data_ptr(), qw, kw, n, hq, hkv, d, num_maps, table, rot, 1 if interleaved else 0,
+        float(eps), _rows(q, q_shape, dt, dev), _rows(k, new, dt, dev),
+        _rows(q_out, q_shape, dt, dev), _rows(k_out, new, dt, dev), _code(dt, names),
+        names.raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         raise PagedAttnError("pa_qk_norm_rope", rc)
     return q_out, k_out

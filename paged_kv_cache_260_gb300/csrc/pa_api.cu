@@ -977,7 +977,7 @@ static int prefill_impl(void *out, const void *q, const void *k_cache, const voi
     if ((long long)max_blocks_per_seq * kBlockSize >= (1LL << 30) || pool_rows >= (1LL << 31) ||
         grid >= (1LL << 31))
         return PA_ERR_UNSUPPORTED;
-    const bool planned = workspace != nullptr;
+    bool planned = workspace != nullptr;
     if (planned) {
         // plan entries pack (sequence, tile) into 16 + 16 bits
         if (num_seqs > 65535 || q_ranks > 65535)
@@ -1031,6 +1031,10 @@ static int prefill_impl(void *out, const void *q, const void *k_cache, const voi
     p.norm_eps = x.norm_eps;
     p.out_scale = x.out_scale;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // differential: blocks that all run at once need no order, and no launch to
+    // make one (chunks of 5 and 70 tokens: 8.3 us in a graph against 10.4)
+    if (diff && grid <= ds->num_sms)
+        planned = false;
     if (planned) {
         int *count = static_cast<int *>(workspace);
         int *by_seq = count + 1;

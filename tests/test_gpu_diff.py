@@ -189,6 +189,25 @@ def test_prefill_longer(pa, hq, hkv, d, dtype):
     x.check(x.prefill(pa))
 
 
+@pytest.mark.parametrize("plan", [True, False])
+def test_prefill_more_blocks_than_sms(pa, plan):
+    # enough blocks for the work order, whose K/V fits in L2
+    lens = [700, 300, 128, 513, 64]
+    x = Pool(lens, 16, 8, 128, "bf16", chunks=[700, 299, 128, 1, 64], seed=14)
+    x.check(x.prefill(pa, workspace="auto" if plan else None))
+    assert pa.get_device_error() == 0
+
+
+def test_prefill_order_by_sequence(pa):
+    # K/V past L2: the order goes sequence by sequence
+    lens, chunks = [13000, 12001, 12500], [150, 70, 90]
+    x = Pool(lens, 16, 8, 128, "bf16", chunks=chunks, seed=15)
+    a = x.prefill(pa).clone()
+    x.check(a, only=[1])
+    assert torch.equal(x.prefill(pa, workspace=None), a)     # the order changes no result
+    assert pa.get_device_error() == 0
+
+
 @pytest.mark.parametrize("hq,chunks", [(96, [3, 1, 2]), (128, [3, 1, 2]), (128, [1, 1, 1]),
                                        (43, [7, 1, 2])])
 def test_prefill_wide_groups(pa, hq, chunks):

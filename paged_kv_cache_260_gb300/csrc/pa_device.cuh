@@ -295,11 +295,16 @@ __device__ __forceinline__ uint32_t cluster_rank()
     return r;
 }
 
-// Every thread of every CTA of the cluster; writes before it are visible after.
-__device__ __forceinline__ void cluster_sync()
+// The cluster's barrier in two halves, each executed once by every thread of
+// every CTA of the cluster: writes before the arrival are visible after the wait.
+__device__ __forceinline__ void cluster_arrive()
 {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait()
+{
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Programmatic dependent launch: wait until the grids this launch depends on

@@ -113,16 +113,17 @@ struct TableWindow {
     const int32_t *table;
     int nblk, h, lane, win, cur, nxt;
 
-    __device__ __forceinline__ TableWindow(const PrefillParams &p_, int s, int h_, int nblk_)
-        : p(p_), table(p_.block_tables + (size_t)s * p_.max_blocks), nblk(nblk_), h(h_),
-          lane(threadIdx.x & 31), win(0)
+    // first, second: this lane's entries of the first two windows (fetch)
+    __device__ __forceinline__ TableWindow(const PrefillParams &p_, const int32_t *table_, int h_,
+                                           int nblk_, int first, int second)
+        : p(p_), table(table_), nblk(nblk_), h(h_), lane(threadIdx.x & 31), win(0), nxt(second)
     {
-        cur = to_row(0, fetch(0));
-        nxt = fetch(WT);
+        cur = to_row(0, first);
     }
-    __device__ __forceinline__ int fetch(int w0) const
+    // Entry of block NB * w0 + lane, 0 past the sequence.
+    static __device__ __forceinline__ int fetch(const int32_t *table, int nblk, int w0)
     {
-        const int lb = NB * w0 + lane;
+        const int lb = NB * w0 + (threadIdx.x & 31);
         return lb < nblk ? __ldg(table + lb) : 0;
     }
     __device__ __forceinline__ int to_row(int w0, int phys) const
@@ -141,7 +142,7 @@ struct TableWindow {
         if (j == win + WT) {
             win += WT;
             cur = to_row(win, nxt);
-            nxt = fetch(win + WT);
+            nxt = fetch(table, nblk, win + WT);
         }
         return __shfl_sync(0xffffffffu, cur, NB * (j - win) + lane % NB);
     }
@@ -187,48 +188,8 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
     const int cr = CL > 1 ? (int)cluster_rank() : 0;
     int h = unit % Hkv;
 
-    // ---- the block's rows and key range (uniform over the block) ----------
-    // no global memory is read before the preceding kernel (the plan) is done
-    grid_dependency_wait();
-    int s, rank = 0, tile = 0;
-    if (p.plan) {
-        if (!plan_block(p, unit, s, tile, h))
-            return;
-    } else {
-        const int per_rank = p.num_seqs * Hkv;
-        rank = unit / per_rank;
-        s = (unit % per_rank) / Hkv;
-    }
-    const int L = __ldg(p.seq_lens + s);
-    const int qs = __ldg(p.query_start + s);
-    const int c = __ldg(p.query_start + s + 1) - qs;
-    // the plan reports itself
-    const bool reporter = !p.plan && rank == 0 && h == 0 && tid == 0 && cr == 0;
-    if (L < 0 || L > p.max_blocks * kBlockSize) {
-        if (reporter)
-            record_error(p.err, PA_DEVERR_SEQLEN_RANGE);
-        return;
-    }
-    if (c < 0 || c > L) {
-        if (reporter)
-            record_error(p.err, PA_DEVERR_QUERY_RANGE);
-        return;
-    }
-    if (!p.plan) {
-        const int nq = (c + CL * TPB - 1) / (CL * TPB);
-        if (nq > p.q_ranks && reporter)
-            record_error(p.err, PA_DEVERR_QUERY_RANGE);   // max_query_len too small
-        if (rank >= nq)
-            return;
-        tile = nq - 1 - rank;                     // rank 0 = the last (longest) tile
-    }
-    const int t0 = (tile * CL + cr) * TPB;        // may lie past the chunk (no rows of its own)
-    const int p_last = L - c + min((tile + 1) * CL * TPB, c) - 1;   // the cluster's last row
-    const int nt = p_last / Sh::BN + 1;           // key tiles, the same for the whole cluster
-    const int nblk = (L + kBlockSize - 1) / kBlockSize;
-    // the last tile reaches past the sequence: its value rows there are zeroed
-    const bool ragged = nt * Sh::BN > L;
-
+    // the barriers first: while their initialisation reaches the other block of
+    // the cluster, this one finds out what to do
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(kfull(i), 1);
@@ -250,6 +211,84 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
         *abort_flag = 0;
         mbar_init_fence();
     }
+    __syncwarp();
+    if constexpr (CL > 1)
+        cluster_arrive();
+    auto no_work = [&]() {                        // the same for the whole cluster
+        if constexpr (CL > 1)
+            cluster_wait();
+    };
+
+    // ---- the block's rows and key range (uniform over the block) ----------
+    // no global memory is read before the preceding kernel (the plan) is done
+    grid_dependency_wait();
+    int s, rank = 0, tile = 0;
+    if (p.plan) {
+        if (!plan_block(p, unit, s, tile, h))
+            return no_work();
+    } else {
+        const int per_rank = p.num_seqs * Hkv;
+        rank = unit / per_rank;
+        s = (unit % per_rank) / Hkv;
+    }
+    const int L = __ldg(p.seq_lens + s);
+    const int qs = __ldg(p.query_start + s);
+    const int c = __ldg(p.query_start + s + 1) - qs;
+    // the plan reports itself
+    const bool reporter = !p.plan && rank == 0 && h == 0 && tid == 0 && cr == 0;
+    if (L < 0 || L > p.max_blocks * kBlockSize) {
+        if (reporter)
+            record_error(p.err, PA_DEVERR_SEQLEN_RANGE);
+        return no_work();
+    }
+    if (c < 0 || c > L) {
+        if (reporter)
+            record_error(p.err, PA_DEVERR_QUERY_RANGE);
+        return no_work();
+    }
+    if (!p.plan) {
+        const int nq = (c + CL * TPB - 1) / (CL * TPB);
+        if (nq > p.q_ranks && reporter)
+            record_error(p.err, PA_DEVERR_QUERY_RANGE);   // max_query_len too small
+        if (rank >= nq)
+            return no_work();
+        tile = nq - 1 - rank;                     // rank 0 = the last (longest) tile
+    }
+    const int t0 = (tile * CL + cr) * TPB;        // may lie past the chunk (no rows of its own)
+    const int p_last = L - c + min((tile + 1) * CL * TPB, c) - 1;   // the cluster's last row
+    const int nt = p_last / Sh::BN + 1;           // key tiles, the same for the whole cluster
+    const int nblk = (L + kBlockSize - 1) / kBlockSize;
+    // the last tile reaches past the sequence: its value rows there are zeroed
+    const bool ragged = nt * Sh::BN > L;
+
+    // What the block reads first is in flight over its last barrier: the block
+    // table's first windows (producer), and the Q tile (softmax warps).  Q row
+    // rr = (token t0 + rr / G, q head h*G + rr % G); rows past the chunk and the
+    // rows 128 - TPB*G that do not fill a token are zero; thread lt takes 16-byte
+    // chunk lt % CPR of every (256 / CPR)-th row.
+    using Window = TableWindow<Sh::NB>;
+    const int32_t *table = p.block_tables + (size_t)s * p.max_blocks;
+    constexpr int CPR = D / 8;                    // 16-byte chunks per row
+    constexpr int RSTEP = 256 / CPR;
+    constexpr int NPT = Sh::BM / RSTEP;
+    const int lt = tid - 128;                     // softmax thread
+    uint4 qv[NPT];
+    int entry0 = 0, entry1 = 0;
+    if (warp == 0) {
+        entry0 = Window::fetch(table, nblk, 0);
+        entry1 = Window::fetch(table, nblk, Window::WT);
+    } else if (warp >= 4) {
+        const T *qg = reinterpret_cast<const T *>(p.q);
+#pragma unroll
+        for (int i = 0; i < NPT; ++i) {
+            const int rr = lt / CPR + i * RSTEP;
+            const int tok = rr / G, hg = rr % G;
+            qv[i] = make_uint4(0, 0, 0, 0);
+            if (rr < TPB * G && t0 + tok < c)
+                qv[i] = __ldg(reinterpret_cast<const uint4 *>(
+                    qg + ((size_t)(qs + t0 + tok) * Hq + h * G + hg) * D + (lt % CPR) * 8));
+        }
+    }
     if (warp == 1) {
         tc::tmem_alloc(smem_addr(tmem_slot), Sh::TMEM_COLS);
         tc::tmem_relinquish();
@@ -257,10 +296,18 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
     tc::fence_before_sync();
     __syncthreads();
     if constexpr (CL > 1)
-        cluster_sync();                           // the other block's barriers are there too
+        cluster_wait();                           // the other block's barriers are there too
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
 
+    // Every warp, once: it will not touch the other block of the cluster again
+    // (whose shared memory the producer copies into, whose barriers the issuers
+    // arrive on).  A block ends after both blocks' warps have all said so.
+    auto leave = [&]() {
+        __syncwarp();
+        if constexpr (CL > 1)
+            cluster_arrive();
+    };
     auto give_up = [&]() {
         *abort_flag = 1;
         record_error(p.err, PA_DEVERR_TIMEOUT);
@@ -270,7 +317,7 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
         // ---------------- producer: K_0, then K_j+1, V_j for every j ----------------
         // The whole warp works: lane 0 waits for the slot and arms its barrier,
         // lanes (hf, b) issue the tile's boxes in parallel.
-        TableWindow<Sh::NB> kw(p, s, h, nblk), vw(p, s, h, nblk);
+        Window kw(p, table, h, nblk, entry0, entry1), vw = kw;
         auto load = [&](int j, int row, const CUtensorMap &tm, uint32_t slots, uint32_t full,
                         uint32_t empty) {
             bool ready = true;
@@ -318,6 +365,7 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
                 if (j % NS == lane && !mbar_wait_bounded(vfull(lane), (j / NS) & 1))
                     give_up();
         }
+        leave();
     } else if (warp <= 2) {
         // ---------------- MMA issuer of map g (the whole warp, one elected lane issues) ----
         const int g = warp - 1;
@@ -405,7 +453,9 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
         tc::commit_warp(drain_bar(g));
         if (!wait_all(drain_bar(g), 0) && lane == 0)
             give_up();
+        leave();
     } else if (warp == 3) {
+        leave();
         // while the block works: warm L2 with the query rows of the block one
         // wave later (its pair and kv head from the work order)
         int s2, tile2, h2;
@@ -421,38 +471,17 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
         }
     } else if (warp >= 4) {
         // ---------------- Q tile -> shared memory ----------------
-        // K-major with the 128-byte swizzle.  Row rr = (token t0 + rr / G, q head
-        // h*G + rr % G); rows past the chunk and the rows 128 - TPB*G that do not
-        // fill a token are zero.  Thread lt takes 16-byte chunk lt % CPR of every
-        // (256 / CPR)-th row, all its loads in flight at once.
-        const int lt = tid - 128;
-        {
-            constexpr int CPR = D / 8;            // 16-byte chunks per row
-            constexpr int RSTEP = 256 / CPR;
-            constexpr int NPT = Sh::BM / RSTEP;
-            const T *qg = reinterpret_cast<const T *>(p.q);
-            const int ch = lt % CPR, hf = ch >> 3, c8 = ch & 7;
-            uint4 qv[NPT];
+        // K-major with the 128-byte swizzle
 #pragma unroll
-            for (int i = 0; i < NPT; ++i) {
-                const int rr = lt / CPR + i * RSTEP;
-                const int tok = rr / G, hg = rr % G;
-                qv[i] = make_uint4(0, 0, 0, 0);
-                if (rr < TPB * G && t0 + tok < c)
-                    qv[i] = __ldg(reinterpret_cast<const uint4 *>(
-                        qg + ((size_t)(qs + t0 + tok) * Hq + h * G + hg) * D + ch * 8));
-            }
-#pragma unroll
-            for (int i = 0; i < NPT; ++i) {
-                const int rr = lt / CPR + i * RSTEP;
-                *reinterpret_cast<uint4 *>(smem + hf * (Sh::BM * 128) + rr * 128 +
-                                           ((c8 ^ (rr & 7)) << 4)) = qv[i];
-            }
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(q_bar);
+        for (int i = 0; i < NPT; ++i) {
+            const int rr = lt / CPR + i * RSTEP, ch = lt % CPR;
+            *reinterpret_cast<uint4 *>(smem + (ch >> 3) * (Sh::BM * 128) + rr * 128 +
+                                       (((ch & 7) ^ (rr & 7)) << 4)) = qv[i];
         }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(q_bar);
 
         // ---------------- softmax: one thread per row of its map ----------
         const int grp = (warp - 4) >> 2;
@@ -464,6 +493,7 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
         const bool row_valid = rr < TPB * G && t0 + tok < c;
         const int pos = row_valid ? L - c + t0 + tok : L - 1;
         const float sl2 = p.scale_log2;
+        const float lam = __ldg(p.lambda + h * G + hg);
         auto arrive = [&](uint32_t bar) {          // once a warp, after its lanes' work
             __syncwarp();
             if (lane == 0)
@@ -602,10 +632,19 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
             }
             l = fmaf(l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
         }
+        // ---------------- the difference, its norm, the output ----------------
+        // This thread's half of the channels; the norm's weights are in flight
+        // over the last P.V.
+        constexpr int HC = D / 2, CH = HC / 8;    // channels, 16-byte chunks
+        uint4 wv[CH];
+        const bool normed = p.norm_w != nullptr;
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+            wv[i] = normed ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.norm_w) +
+                                                                   grp * HC) + i)
+                           : make_uint4(0, 0, 0, 0);
         if (ok && !__all_sync(FULL, mbar_wait_bounded(o_bar(grp), (nt - 1) & 1)))
             ok = false;
-
-        // ---------------- the difference, its norm, the output ----------------
         // Row sums and the halves' sums of squares go through shared memory.
         // Every softmax thread takes part in both barriers, also after a wait that
         // gave up; past the first, both maps' last P.V are known to be done.
@@ -617,14 +656,15 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
         tc::fence_before_sync();
         softmax_warps_sync();
         tc::fence_after_sync();
+        leave();
         ok = !__any_sync(FULL, *abort_flag != 0);
         const float i0 = 1.f / xl[rr];
-        const float i1 = -__ldg(p.lambda + h * G + hg) / xl[Sh::BM + rr];
-        const uint32_t half = lanes + Sh::COL_O + grp * (D / 2);
-        float y[D / 2], ss = 0.f;
+        const float i1 = -lam / xl[Sh::BM + rr];
+        const uint32_t half = lanes + Sh::COL_O + grp * HC;
+        float y[HC], ss = 0.f;
         if (ok) {
 #pragma unroll
-            for (int cc = 0; cc < D / 2; cc += 32) {
+            for (int cc = 0; cc < HC; cc += 32) {
                 uint32_t a[32], b[32];
                 __syncwarp();
                 tc::tmem_ld32(half + cc, a);
@@ -638,35 +678,39 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
         }
         xq[grp * Sh::BM + rr] = ss;
         softmax_warps_sync();
-        if (ok && row_valid) {
-            const T *w = static_cast<const T *>(p.norm_w);
+        if (ok) {
             float k = p.out_scale;
-            if (w)
+            if (normed)
                 k *= rsqrtf((xq[rr] + xq[Sh::BM + rr]) * (1.f / D) + p.norm_eps);
-            T *orow = reinterpret_cast<T *>(p.out) +
-                      ((size_t)(qs + t0 + tok) * Hq + h * G + hg) * D + grp * (D / 2);
+            // Through the warp's part of the Q tile's shared memory (no MMA reads
+            // Q any more), so that a warp's stores are whole 128-byte lines: a
+            // row to a thread, they touched 32 lines an instruction.
+            uint4 *st = reinterpret_cast<uint4 *>(smem) + (warp - 4) * 32 * CH;
 #pragma unroll
-            for (int e = 0; e < D / 2; e += 8) {
+            for (int i = 0; i < CH; ++i) {
                 float f[8];
+                const uint32_t w32[4] = {wv[i].x, wv[i].y, wv[i].z, wv[i].w};
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    f[i] = k;
-                if (w) {
-                    const uint4 wv = __ldg(reinterpret_cast<const uint4 *>(w + grp * (D / 2) + e));
-                    const uint32_t w32[4] = {wv.x, wv.y, wv.z, wv.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 x = Elem<T>::to_f2(w32[i]);
-                        f[2 * i] *= x.x;
-                        f[2 * i + 1] *= x.y;
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const float2 x = normed ? Elem<T>::to_f2(w32[e]) : make_float2(1.f, 1.f);
+                    f[2 * e] = y[8 * i + 2 * e] * (k * x.x);
+                    f[2 * e + 1] = y[8 * i + 2 * e + 1] * (k * x.y);
                 }
-                uint4 u;
-                u.x = Mma<T>::pack(y[e] * f[0], y[e + 1] * f[1]);
-                u.y = Mma<T>::pack(y[e + 2] * f[2], y[e + 3] * f[3]);
-                u.z = Mma<T>::pack(y[e + 4] * f[4], y[e + 5] * f[5]);
-                u.w = Mma<T>::pack(y[e + 6] * f[6], y[e + 7] * f[7]);
-                *reinterpret_cast<uint4 *>(orow + e) = u;
+                st[lane * CH + (i ^ (lane % CH))] =
+                    make_uint4(Mma<T>::pack(f[0], f[1]), Mma<T>::pack(f[2], f[3]),
+                               Mma<T>::pack(f[4], f[5]), Mma<T>::pack(f[6], f[7]));
+            }
+            __syncwarp();
+            const long long mine =
+                row_valid ? ((long long)(qs + t0 + tok) * Hq + h * G + hg) * D + grp * HC : -1;
+            T *out = reinterpret_cast<T *>(p.out);
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                const int row = i * (32 / CH) + lane / CH, ch = lane % CH;
+                const long long at = __shfl_sync(FULL, mine, row);
+                if (at >= 0)
+                    *reinterpret_cast<uint4 *>(out + at + 8 * ch) =
+                        st[row * CH + (ch ^ (row % CH))];
             }
         }
     }
@@ -677,10 +721,8 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, Sh::TMEM_COLS);
     }
-    // the other block may still copy into this one's shared memory or arrive on
-    // its barriers
     if constexpr (CL > 1)
-        cluster_sync();
+        cluster_wait();                           // see leave()
 }
 
 template <typename T, int D, int CL>

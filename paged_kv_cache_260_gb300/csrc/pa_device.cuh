@@ -296,10 +296,12 @@ __device__ __forceinline__ uint32_t cluster_rank()
 }
 
 // The cluster's barrier in two halves, each executed once by every thread of
-// every CTA of the cluster: writes before the arrival are visible after the wait.
-__device__ __forceinline__ void cluster_arrive()
+// every CTA of the cluster.  The arrival orders no writes (its releasing form
+// costs several hundred cycles); barrier initialisations are released by
+// mbar_init_fence().
+__device__ __forceinline__ void cluster_arrive_relaxed()
 {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void cluster_wait()

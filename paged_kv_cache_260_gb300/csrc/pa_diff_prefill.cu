@@ -27,7 +27,14 @@
 //    works for 1,536.  P.V starts on the first 64 keys while the softmax is at
 //    the others; each map has an issuing warp of its own (one for both was busy
 //    for 2,300 cycles: every wait on a barrier costs it 100 to 250, completed or
-//    not); and map 1 runs half a tile behind map 0.  1196 us: 1.29 PFLOP/s.
+//    not); and map 1 runs half a tile behind map 0.  1197 us.
+//  * Short contexts: a block's start and end.  8 x 512 tokens over 0.5K to 4K are
+//    6.7 blocks an SM of about 16 tiles each, and 15,600 of a block's 56,000 cycles
+//    passed before its first softmax, after its last P and between blocks.  The
+//    barriers first, K_0 and the query rows in flight over the block's last
+//    barrier, no releasing cluster arrivals, the norm's weights and lambda loaded
+//    ahead, output rows stored by whole lines: 11,200 cycles, 211 -> 197 us; the
+//    long chunks 1189 us, 1.30 PFLOP/s.
 //  * P through shared memory, which lets the next S go ahead, costs more shared
 //    memory bandwidth than there is (1437 us before the multicast); 80-key tiles
 //    with P in columns of its own 1702; two threads a row 1382 against 1197.
@@ -190,30 +197,24 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
 
     // the barriers first: while their initialisation reaches the other block of
     // the cluster, this one finds out what to do
-    if (tid == 0) {
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(kfull(i), 1);
-            mbar_init(kempty(i), 2 * CL);         // both maps' issuers, of every block
-            mbar_init(vfull(i), 1);
-            mbar_init(vempty(i), 2 * CL);
+    if (warp == 0) {
+        for (int i = lane; i < Sh::NBAR; i += 32) {
+            const int k = i - 4 * NS;             // past the slots' barriers
+            int count = 1;                        // a commit, or the producer
+            if (k < 0)
+                count = (i / NS) & 1 ? 2 * CL : 1;   // empty: both maps' issuers, of every block
+            else if ((k >= 2 && k < 4) || (k >= 6 && k < 10) || k == 14)
+                count = 4;                        // read, p, start: one lane of each of 4 warps
+            else if (k == 12 || k == 13)
+                count = 8;                        // q, z: of every softmax warp
+            mbar_init(bar_addr + 8u * i, count);
         }
-        for (int g = 0; g < 2; ++g) {
-            mbar_init(s_bar(g), 1);
-            mbar_init(read_bar(g), 4);            // one lane of each softmax warp
-            mbar_init(p_bar(g, 0), 4);
-            mbar_init(p_bar(g, 1), 4);
-            mbar_init(o_bar(g), 1);
-            mbar_init(drain_bar(g), 1);
-        }
-        mbar_init(q_bar, 8);
-        mbar_init(z_bar, 8);
-        mbar_init(start_bar, 4);
         *abort_flag = 0;
         mbar_init_fence();
     }
     __syncwarp();
     if constexpr (CL > 1)
-        cluster_arrive();
+        cluster_arrive_relaxed();
     auto no_work = [&]() {                        // the same for the whole cluster
         if constexpr (CL > 1)
             cluster_wait();
@@ -277,6 +278,16 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
     if (warp == 0) {
         entry0 = Window::fetch(table, nblk, 0);
         entry1 = Window::fetch(table, nblk, Window::WT);
+        // K_0 at once, each block its own copy: the other one's barriers may not
+        // be there yet
+        Window w(p, table, h, nblk, entry0, entry1);
+        const int row = w.row(0);
+        if (lane == 0)
+            mbar_arrive_expect_tx(kfull(0), (uint32_t)(min(Sh::NB, nblk) * Sh::HALVES * Sh::BOX));
+        __syncwarp();
+        if (lane < Sh::HALVES * Sh::NB && row >= 0)
+            tma_load_2d(sbase + Sh::OFF_K + lane * Sh::BOX, &tmk, 64 * (lane / Sh::NB), row,
+                        kfull(0));
     } else if (warp >= 4) {
         const T *qg = reinterpret_cast<const T *>(p.q);
 #pragma unroll
@@ -306,7 +317,7 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
     auto leave = [&]() {
         __syncwarp();
         if constexpr (CL > 1)
-            cluster_arrive();
+            cluster_arrive_relaxed();
     };
     auto give_up = [&]() {
         *abort_flag = 1;
@@ -314,7 +325,7 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
     };
 
     if (warp == 0) {
-        // ---------------- producer: K_0, then K_j+1, V_j for every j ----------------
+        // ---------------- producer: K_j+1, V_j for every j ----------------
         // The whole warp works: lane 0 waits for the slot and arms its barrier,
         // lanes (hf, b) issue the tile's boxes in parallel.
         Window kw(p, table, h, nblk, entry0, entry1), vw = kw;
@@ -341,15 +352,15 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
             }
             return true;
         };
-        int nk = 0, nv = 0;                       // tiles issued
+        int nk = 1, nv = 0;                       // tiles issued: K_0 has been
         bool ok = true;
-        for (int j = -1; ok && j < nt; ++j) {
+        for (int j = 0; ok && j < nt; ++j) {
             if (j + 1 < nt) {
                 ok = load(j + 1, kw.row(j + 1), tmk, sbase + Sh::OFF_K, kfull((j + 1) % NS),
                           kempty((j + 1) % NS));
                 nk += ok;
             }
-            if (ok && j >= 0) {
+            if (ok) {
                 ok = load(j, vw.row(j), tmv, sbase + Sh::OFF_V, vfull(j % NS), vempty(j % NS));
                 nv += ok;
             }

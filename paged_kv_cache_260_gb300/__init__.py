@@ -188,14 +188,15 @@ def _hot():
 
 
 def _scratch(nbytes, device, stream):
-    """A uint8 scratch tensor for one call.  It is tied to the call's stream,
-    so the caching allocator does not hand its memory out again before the
-    kernels that use it have run."""
+    """A uint8 scratch tensor for one call, out of the call's stream's memory: the
+    caching allocator may otherwise hand out memory that kernels on the
+    current stream still use, or hand this out again before the call's kernels
+    have run."""
     torch = _torch()
-    t = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def _check(fn: str, rc: int):

@@ -325,6 +325,22 @@ def test_two_streams_with_workspaces_of_their_own(pa):
         assert torch.equal(x.out[:3], w)                     # bit-stable too
 
 
+def test_scratch_comes_from_the_calls_stream(pa):
+    # memory that the current stream has just freed may still be in use there
+    x = Pool([900, 33], 8, 2, 128, "bf16", chunks=[100, 33], seed=23)
+    y = Pool([900, 33], 8, 2, 128, "bf16", seed=23)
+    s = torch.cuda.Stream()
+    for make in (lambda **k: pa.diff_decode_workspace_for(y.q, y.k, y.tables, **k),
+                 lambda **k: pa.diff_prefill_workspace_for(x.q, x.k, x.lens, 100, **k),
+                 lambda **k: pa.workspace_for(y.q, y.k, y.tables, **k)):
+        torch.cuda.synchronize()
+        first = make()
+        at = first.data_ptr()
+        del first
+        assert make().data_ptr() == at                       # the allocator does reuse it
+        assert make(stream=s).data_ptr() != at
+
+
 def test_offsets_past_32_bits(pa):
     # a pool of more than 2^31 elements whose live blocks lie at its end
     hkv, d = 8, 128

@@ -157,7 +157,8 @@ int pa_decode(void *out, const void *q, const void *k_cache, const void *v_cache
  * or out = out_scale * y if norm_weight is NULL; the mean is over the head's
  * head_dim channels.  A model's learned vectors give lambda once, when its weights
  * are loaded.  fp32 throughout (the weights of the softmax enter the product
- * with V as two 16-bit terms each), one rounding at the end.  A sequence of
+ * with V as two 16-bit terms each, in groups of more than 8 heads rounded to
+ * dtype), one rounding at the end.  A sequence of
  * length 0 yields zeros.  Keys and values of live tokens must be finite; slots
  * past a sequence's end may hold anything.  out overlaps no input (out == q is
  * refused).

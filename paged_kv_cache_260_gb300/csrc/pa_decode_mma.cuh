@@ -46,7 +46,11 @@
 //    for each map, 9 to 16 two, and a tile runs the k-steps of its own half alone.
 //    The difference cancels what the maps share, and with it part of the
 //    result that a rounding of P is relative to; so P enters the second
-//    product as two 16-bit terms, its rounded value and the rounded rest.
+//    product as two 16-bit terms, its rounded value and the rounded rest
+//    (without the rest the error against 64 bits is 1.15 times as large).  Up to
+//    two column tiles HBM hides those MMAs; with four they would set the time
+//    (290 us against 254 on four sequences of 32K to 131K tokens, 128/8 heads x
+//    128), and P is rounded once, as in the plain decode.
 //  * Large batches (more than kSeqsInSmem sequences) keep the per-sequence
 //    lengths and unit prefix in the workspace, built once by two small
 //    kernels, instead of in every block's shared memory.
@@ -304,6 +308,7 @@ __device__ __forceinline__ void decode_worker(const DecodeParams &p, const CUten
                                               const int32_t *lens, const uint8_t *share)
 {
     static_assert(!(PARTIAL && DIFF), "no partial outputs of a difference");
+    constexpr bool TWO_TERMS = DIFF && NT <= 2;
     using Sh = MmaShape<D, NT, DIFF>;
     using E = Elem<T>;
     using M = Mma<T>;
@@ -526,7 +531,7 @@ __device__ __forceinline__ void decode_worker(const DecodeParams &p, const CUten
             }
             const bool masked = nvalid < kBlockSize;
             uint32_t pb[NT][2];
-            uint32_t pr[NT][2];                   // DIFF: what rounding P left over
+            uint32_t pr[NT][2];                   // two terms: what rounding P left over
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 float x0 = (sa[j][0] + sb[j][0]) * p.scale_log2;   // token r,   head h0
@@ -574,7 +579,7 @@ __device__ __forceinline__ void decode_worker(const DecodeParams &p, const CUten
                 const uint32_t u0 = M::pack(p0, p1), u1 = M::pack(p2, p3);
                 pb[j][0] = movmatrix_trans(u0);
                 pb[j][1] = movmatrix_trans(u1);
-                if constexpr (DIFF) {
+                if constexpr (TWO_TERMS) {
                     const float2 f0 = E::to_f2(u0), f1 = E::to_f2(u1);
                     pr[j][0] = movmatrix_trans(M::pack(p0 - f0.x, p1 - f0.y));
                     pr[j][1] = movmatrix_trans(M::pack(p2 - f1.x, p3 - f1.y));
@@ -600,7 +605,7 @@ __device__ __forceinline__ void decode_worker(const DecodeParams &p, const CUten
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
                     M::run(o[j][mt], a, pb[j][0], pb[j][1]);
-                    if constexpr (DIFF)
+                    if constexpr (TWO_TERMS)
                         M::run(o[j][mt], a, pr[j][0], pr[j][1]);
                 }
             }
@@ -1123,10 +1128,11 @@ inline void fill_diff_kernel_set(KernelSet *ks)
     // Warps per SM, measured on four sequences of 32K to 131K tokens (K/V floor
     // 201 us): D=128 with one column tile 7 (209 us; 6 and 8 to 10 between 208 and
     // 227 over runs, and 7 the fastest on the batch-128 lengths, 81.1 us against
-    // 82 to 85), two tiles 8 (216; 7 224, 9 231, 6 255), four tiles 8 (290; 7 320),
-    // where the MMAs and not HBM set the time; D=64 12 (205), 12 (211; 11 239,
-    // 13 222) and 8 (333; 7 373, 9 402).  P's second term costs a microsecond of
-    // the batch (80.2 without).
+    // 82 to 85), two tiles 8 (216; 7 224, 9 231, 6 255), four tiles 8 (254; with
+    // P in two terms 290, 7 warps 320, 6 365), where the MMAs and not HBM set the
+    // time; D=64 12 (205), 12 (211; 11 239, 13 222) and 8 (304; with two terms
+    // 333, 7 373, 9 402).  P's second term costs a microsecond of the batch (80.2
+    // without).
     constexpr int S = 2;
     constexpr int W = D == 128 ? (NT == 1 ? 7 : 8) : (NT == 4 ? 8 : 12);
     ks->decode = reinterpret_cast<const void *>(&decode_mma_kernel<T, D, NT, W, S, false, true>);

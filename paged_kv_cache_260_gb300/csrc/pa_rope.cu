@@ -17,7 +17,7 @@
 // the launch a decode step's few tokens); behind HBM, instruction issue: packed
 // two-wide fp32 arithmetic, angles once per unit of work and weights once per
 // warp took 32768 tokens of 32/8 heads x 128 from 155 to 135 us, the rings and
-// the split of rope_many_kernel to 127 us, 95 % of the measured copy rate.
+// the split of rope_many_kernel to 126 us, 95 % of the measured copy rate.
 #include <algorithm>
 
 #include "pa_device.cuh"
@@ -28,8 +28,13 @@ namespace pa {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeRounds = 4;     // rounds of a unit, at most
-constexpr int kRopeStages = 3;     // units in flight per warp
+// Rounds of a unit, at most: in registers, and through the rings, whose two
+// stages a warp hold as many bytes as three of four rounds (32768 tokens without
+// the pool write 127.4 us against 130.2, 16384 with it 66.5 against 69.7: fewer
+// units, each with its own angles and copies)
+constexpr int kFewRounds = 4;
+constexpr int kManyRounds = 6;
+constexpr int kRopeStages = 2;     // units in flight per warp
 
 // eight 16-bit channels as four packed pairs of fp32, and back
 template <typename T>
@@ -337,7 +342,7 @@ template <typename T, int TS, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads, 2)
 rope_few_kernel(const RopeParams p, const int iters)
 {
-    constexpr int U = kRopeRounds;
+    constexpr int U = kFewRounds;
     using Lane = RopeLane<T, TS, INTER>;
     constexpr int d = Lane::d, GPW = Lane::GPW;
     grid_dependents_launch();
@@ -390,7 +395,7 @@ rope_few_kernel(const RopeParams p, const int iters)
 // stages, kRopeStages units ahead, about 200 KB in flight an SM.  Warps never
 // wait for each other.
 struct RopeStage {
-    static constexpr int kRows = kRopeRounds * 1024;   // a round is 32 lanes x 32 bytes
+    static constexpr int kRows = kManyRounds * 1024;   // a round is 32 lanes x 32 bytes
     static constexpr int kTable = 512;                 // a table row of at most 128 floats
     static constexpr int kBytes = kRows + kTable;
 };
@@ -548,21 +553,26 @@ RopeKernel rope_kernel(const RopeParams &p, bool bf16, int head_dim, bool interl
     const int gpw = 32 / ts;
     const long long segs = (long long)p.q_segs + p.k_segs + p.v_segs;
     const long long rounds = (segs + gpw - 1) / gpw;
-    // a unit of at most kRopeRounds rounds; fewer where that would leave SMs
-    // without warps
-    long long chunks = (rounds + kRopeRounds - 1) / kRopeRounds;
     const long long resident = 2LL * W * num_sms;      // warps of one wave
-    chunks = std::max(chunks, std::min(rounds, resident / p.num_tokens));
     RopeKernel r{};
-    r.iters = (int)((rounds + chunks - 1) / chunks);
-    const long long units = (rounds + r.iters - 1) / r.iters * p.num_tokens;
-    if (units >= (1LL << 31))
-        return r;
+    // units of at most `most` rounds, of fewer where that would leave SMs without
+    // warps
+    auto cut = [&](int most) {
+        long long chunks = (rounds + most - 1) / most;
+        chunks = std::max(chunks, std::min(rounds, resident / p.num_tokens));
+        r.iters = (int)((rounds + chunks - 1) / chunks);
+        return (rounds + r.iters - 1) / r.iters * p.num_tokens;
+    };
+    long long units = cut(kFewRounds);
     // Few units go one to a warp, rows into registers; from four a warp on,
     // through the rings.  Measured (32/8 heads x 128, bf16, pool write, in a
     // graph): 1024 tokens 8.1 us either way, 2048 13.9 against 15.0 through the
     // rings, 4096 22.4 against 22.0, 8192 40.2 against 35.7.
     const bool many = units > 4 * resident;
+    if (many)
+        units = cut(kManyRounds);
+    if (units >= (1LL << 31))
+        return r;
     bf16 ? pick<__nv_bfloat16>(&r, ts, interleaved, many) : pick<__half>(&r, ts, interleaved, many);
     r.threads = kRopeThreads;
     r.blocks = (int)((units + W - 1) / W);
@@ -570,12 +580,13 @@ RopeKernel rope_kernel(const RopeParams &p, bool bf16, int head_dim, bool interl
         return r;
     // One wave of blocks takes an even share each, then blocks of one unit a
     // warp the remainder.  With many units a warp the SMs drift apart (13 % of
-    // their time idle at 40 units a warp), so a tenth is left to blocks of two
-    // units a warp, which the hardware hands out as SMs come free: 32768 tokens
-    // 127.6 us against 135.2 with the pool write (130.4 against 129.0 without);
-    // at 20 units a warp 66.7 against 69.1 and 69.9 against 67.7, so not there.
+    // their time idle at 40 units of four rounds), so a tenth is left to blocks of
+    // two units a warp, which the hardware hands out as SMs come free.  With the
+    // pool write 32768 tokens (27 units a warp) 126.3 us against 134.0, 16384 66.5
+    // against 69.5, 8192 (6.7 units) 38.2 against 36.0; without it 127.4 against
+    // 136.0, 67.4 against 69.9, and 6000 tokens 31.4 against 28.9.
     const long long each = units / resident;
-    const bool spare = each >= 32;
+    const bool spare = each >= 12;
     const long long tail = W * (spare ? 2 : 1);
     r.split.long_blocks = 2 * num_sms;
     r.split.long_units = (unsigned)((spare ? each - each / 10 : each) * resident);

@@ -397,8 +397,13 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
         // landed, so it comes before the wait for the softmax or the last P.V
         auto k_ready = [&](int j) { return wait_all(kfull(j % NS), (j / NS) & 1); };
         auto v_ready = [&](int j) { return wait_all(vfull(j % NS), (j / NS) & 1); };
-        // a slot is free once both maps of every block of the cluster have read it
-        auto release = [&](uint32_t bar) {
+        // A slot is free once both maps of every block of the cluster have read
+        // tile j.  Only said of slots that a later tile takes: then the other
+        // block's producer waits for every arrival on its barriers, and none is
+        // under way to a block that has ended.
+        auto release = [&](uint32_t bar, int j) {
+            if (j + NS >= nt)
+                return;
             if constexpr (CL > 1)
                 tc::commit_warp_multicast(bar, kAll);
             else
@@ -412,7 +417,7 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
             for (int k = 0; k < D / 32; ++k)      // 32 bytes along the 128-byte row a step
                 tc::mma_ss_warp(ts, q_desc + 2 * k, kd + 2 * k, idS, k > 0);
             tc::commit_warp(s_bar(g));
-            release(kempty(sl));
+            release(kempty(sl), j);
         };
         // O_g += P_g,j . V_j, each half of the keys once the softmax has written
         // its P
@@ -432,7 +437,7 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
                                     (j > 0 || kk > 0) ? 1u : 0u);
             }
             tc::commit_warp(o_bar(g));
-            release(vempty(sl));
+            release(vempty(sl), j);
             return true;
         };
         // map 1 starts half a tile behind: the maps' softmaxes then alternate on

@@ -86,6 +86,7 @@ __device__ __forceinline__ uint64_t f2_neg(uint64_t x)
 template <bool INTER>
 struct RopeAngles {
     uint64_t c[INTER ? 8 : 4], s[INTER ? 8 : 4];
+    uint64_t n[INTER ? 1 : 4];                // half-split: -s
 };
 
 // A lane's part of the work, the same in both kernels below.  A warp takes a
@@ -170,6 +171,9 @@ struct RopeLane {
             g.c[2] = f2_pack(z.x, z.y), g.c[3] = f2_pack(z.z, z.w);
             g.s[0] = f2_pack(y.x, y.y), g.s[1] = f2_pack(y.z, y.w);
             g.s[2] = f2_pack(w.x, w.y), g.s[3] = f2_pack(w.z, w.w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                g.n[i] = f2_neg(g.s[i]);
         }
     }
 
@@ -208,7 +212,7 @@ struct RopeLane {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint64_t a = x[i], b = x[4 + i];
-                x[i] = f2_fma(a, g.c[i], f2_neg(f2_mul(b, g.s[i])));
+                x[i] = f2_fma(a, g.c[i], f2_mul(b, g.n[i]));
                 x[4 + i] = f2_fma(b, g.c[i], f2_mul(a, g.s[i]));
             }
         }
@@ -505,8 +509,24 @@ rope_many_kernel(const RopeParams p, const int iters, const RopeSplit split)
             RopeAngles<INTER> g;
             me.angles(p, reinterpret_cast<const float *>(stage + RopeStage::kRows), g);
             const typename Lane::Target to = me.target(p, tok, slot);
-#pragma unroll 2
-            for (int first = begin; first < end; first += GPW) {
+            int first = begin;
+            // the rounds that hold queries alone, by far the most, without the
+            // choices of round() (4096 tokens 21.8 -> 20.5 us; 32768, where HBM is
+            // the bound, 126.7 -> 127.5)
+            const int qend = min(end, me.k0) - GPW;
+            const unsigned char *from = stage + me.grp * (d * 2);
+            T *dst = to.q + (begin + me.grp) * d;
+#pragma unroll 3
+            for (; first <= qend; first += GPW) {
+                uint4 xa = reinterpret_cast<const uint4 *>(from)[me.va];
+                uint4 xb = reinterpret_cast<const uint4 *>(from)[me.vb];
+                me.turn(p, me.qw, p.q_norm != nullptr, g, xa, xb);
+                me.put(dst, me.va, me.vb, xa, xb);
+                from += GPW * d * 2;
+                dst += GPW * d;
+            }
+#pragma unroll 1
+            for (; first < end; first += GPW) {
                 const int seg = first + me.grp;
                 uint4 xa = make_uint4(0u, 0u, 0u, 0u), xb = xa;
                 if (seg < end) {
@@ -564,11 +584,11 @@ RopeKernel rope_kernel(const RopeParams &p, bool bf16, int head_dim, bool interl
         return (rounds + r.iters - 1) / r.iters * p.num_tokens;
     };
     long long units = cut(kFewRounds);
-    // Few units go one to a warp, rows into registers; from four a warp on,
+    // Few units go one to a warp, rows into registers; from three a warp on,
     // through the rings.  Measured (32/8 heads x 128, bf16, pool write, in a
-    // graph): 1024 tokens 8.1 us either way, 2048 13.9 against 15.0 through the
-    // rings, 4096 22.4 against 22.0, 8192 40.2 against 35.7.
-    const bool many = units > 4 * resident;
+    // graph): 1536 tokens 10.3 us against 12.5 through the rings, 2048 13.4
+    // against 14.7, 2560 16.3 against 15.4, 4096 22.4 against 20.7.
+    const bool many = units > 3 * resident;
     if (many)
         units = cut(kManyRounds);
     if (units >= (1LL << 31))
@@ -581,10 +601,11 @@ RopeKernel rope_kernel(const RopeParams &p, bool bf16, int head_dim, bool interl
     // One wave of blocks takes an even share each, then blocks of one unit a
     // warp the remainder.  With many units a warp the SMs drift apart (13 % of
     // their time idle at 40 units of four rounds), so a tenth is left to blocks of
-    // two units a warp, which the hardware hands out as SMs come free.  With the
-    // pool write 32768 tokens (27 units a warp) 126.3 us against 134.0, 16384 66.5
-    // against 69.5, 8192 (6.7 units) 38.2 against 36.0; without it 127.4 against
-    // 136.0, 67.4 against 69.9, and 6000 tokens 31.4 against 28.9.
+    // two units a warp, which the hardware hands out as SMs come free.  Before
+    // the queries had a loop of their own: with the pool write 32768 tokens (27
+    // units a warp) 126.3 us against 134.0, 16384 66.5 against 69.5, 8192 (6.7
+    // units) 38.2 against 36.0; without it 127.4 against 136.0, 67.4 against 69.9,
+    // and 6000 tokens 31.4 against 28.9.
     const long long each = units / resident;
     const bool spare = each >= 12;
     const long long tail = W * (spare ? 2 : 1);

@@ -17,7 +17,7 @@
 // the launch a decode step's few tokens); behind HBM, instruction issue: packed
 // two-wide fp32 arithmetic, angles once per unit of work and weights once per
 // warp took 32768 tokens of 32/8 heads x 128 from 155 to 135 us, the rings and
-// the split of rope_many_kernel to 126 us, 95 % of the measured copy rate.
+// the split of rope_many_kernel to 127 us, 95 % of the measured copy rate.
 #include <algorithm>
 
 #include "pa_device.cuh"

@@ -21,23 +21,27 @@
 //    that read them so ended at 1420 to 1510 us.  So two blocks of a cluster take
 //    consecutive query tiles and copy every other K/V box each, into both
 //    (multicast): 1276 us.
-//  * Then each map's chain S -> softmax -> P.V -> next S (P lies over the score
-//    columns it came from, and TMEM has no others): about 2,600 cycles a tile,
-//    1,450 of them the softmax of one warp per sub-core, while the tensor core
-//    works for 1,536.  P.V starts on the first 64 keys while the softmax is at
-//    the others; each map has an issuing warp of its own (one for both was busy
-//    for 2,300 cycles: every wait on a barrier costs it 100 to 250, completed or
-//    not); and map 1 runs half a tile behind map 0.  1197 us.
+//  * Then each map's chain S -> softmax -> P.V -> next S: P lies over score
+//    columns, and TMEM has no others.  P.V starts on the first 64 keys while the
+//    softmax is at the others; each map has an issuing warp of its own (one for
+//    both was busy for 2,300 cycles a tile: every wait on a barrier costs it 100 to
+//    250, completed or not); and map 1 starts half a tile behind map 0: 1197 us,
+//    2,600 cycles a tile.  P needs only the second half of the score columns, so the
+//    next tile's first 64 keys are scored into the first half while the softmax
+//    is at its exponentials (M 128, N 64 reads Q from shared memory twice as often
+//    and takes 1.5 times as long): 1146 us, 2,480 cycles, of which the tensor core
+//    works for 1,792 and the 256 exponentials of a sub-core take 1,050.
 //  * Short contexts: a block's start and end.  8 x 512 tokens over 0.5K to 4K are
 //    6.7 blocks an SM of about 16 tiles each, and 15,600 of a block's 56,000 cycles
 //    passed before its first softmax, after its last P and between blocks.  The
 //    barriers first, K_0 and the query rows in flight over the block's last
 //    barrier, no releasing cluster arrivals, the norm's weights and lambda loaded
-//    ahead, output rows stored by whole lines: 11,200 cycles, 211 -> 197 us; the
-//    long chunks 1189 us, 1.30 PFLOP/s.
+//    ahead, output rows stored by whole lines: 11,200 cycles, 211 -> 197 us.
 //  * P through shared memory, which lets the next S go ahead, costs more shared
 //    memory bandwidth than there is (1437 us before the multicast); 80-key tiles
-//    with P in columns of its own 1702; two threads a row 1382 against 1197.
+//    with P in columns of its own 1702; two threads a row 1382 against 1197; turns
+//    at the exponentials 1174, and those of the first 64 keys before the others'
+//    scores are there 1294, against 1146.
 //
 // Warp roles (384 threads):
 //   warp 0     TMA producer: K tiles and V tiles through a ring each, K one tile
@@ -54,9 +58,11 @@
 //              rounding left over would add a third to the tensor work); at the
 //              end each map forms the difference of half of the row's channels.
 // TMEM (512 columns): map g has S in [256g, 256g + 128) and O in
-// [256g + 128, 256g + 128 + head_dim).  P, packed two per column, overwrites
-// S's first 64 columns at head_dim 128; at head_dim 64 it has the map's last 64
-// columns, and S_g,j+1 is then issued as soon as the softmax has read S_g,j.
+// [256g + 128, 256g + 128 + head_dim).  P, packed two per column, overwrites S's
+// last 64 columns at head_dim 128, and S_g,j+1 comes in two halves: the first 64
+// keys as soon as the softmax has read those of S_g,j, the others after P_g,j . V_j.
+// At head_dim 64 P has the map's last 64 columns, and all of S_g,j+1 is issued as
+// soon as the softmax has read S_g,j.
 // Every wait is bounded; a wait that gives up records PA_DEVERR_TIMEOUT and
 // the block drains its copies and MMAs before it frees TMEM and exits.
 #include <cuda.h>
@@ -86,8 +92,8 @@ struct DiffShape {
     static constexpr int OFF_X = OFF_V + NSLOT * SLOT_BYTES;   // the maps' exchange: [4][128] fp32
     static constexpr int DATA = OFF_X + 4 * BM * 4;
     // kfull, kempty, vfull, vempty [NSLOT]; s, read, o, p low, p high, drain [2];
-    // q, z, start; then the TMEM base and the abort flag
-    static constexpr int NBAR = 4 * NSLOT + 12 + 3;
+    // q, z, start; s high [2]; then the TMEM base and the abort flag
+    static constexpr int NBAR = 4 * NSLOT + 12 + 3 + 2;
     static constexpr int BAR_BYTES = NBAR * 8 + 8;
     // The operands are aligned up to 1024 bytes inside the dynamic allocation;
     // the barriers sit in whichever end of the 1024-byte slack has room.
@@ -97,7 +103,7 @@ struct DiffShape {
     static constexpr uint32_t MAP_COLS = 256;
     static constexpr uint32_t COL_O = 128;
     static constexpr bool SEPARATE_P = COL_O + D + BN / 2 <= MAP_COLS;
-    static constexpr uint32_t COL_P = SEPARATE_P ? COL_O + D : 0;
+    static constexpr uint32_t COL_P = SEPARATE_P ? COL_O + D : BN / 2;
     static_assert(D == 64 || D == 128, "head_dim");
     static_assert(OFF_K % 1024 == 0 && SLOT_BYTES % 2048 == 0, "swizzle atoms");
     static_assert(BAR_BYTES <= 512, "barriers fit either end of the slack");
@@ -177,6 +183,8 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
     auto vfull = [&](int i) { return bar_addr + 8u * (2 * NS + i); };
     auto vempty = [&](int i) { return bar_addr + 8u * (3 * NS + i); };
     auto s_bar = [&](int g) { return bar_addr + 8u * (4 * NS + g); };         // S_g,j is there
+    // (SEPARATE_P: all of it; else keys 0..63, and the others)
+    auto s_high_bar = [&](int g) { return bar_addr + 8u * (4 * NS + 15 + g); };
     auto read_bar = [&](int g) { return bar_addr + 8u * (4 * NS + 2 + g); };  // and has been read
     auto o_bar = [&](int g) { return bar_addr + 8u * (4 * NS + 4 + g); };     // O_g has taken P_g,j
     // half of P_g,j is there
@@ -380,7 +388,6 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
     } else if (warp <= 2) {
         // ---------------- MMA issuer of map g (the whole warp, one elected lane issues) ----
         const int g = warp - 1;
-        constexpr uint32_t idS = tc::idesc_f16(kBf16, Sh::BM, Sh::BN, false, false);
         constexpr uint32_t idO = tc::idesc_f16(kBf16, Sh::BM, D, false, true);
         // map 1's channels of the Q and K tiles start D/2 further: the next
         // 64-channel half, or 64 bytes into the row
@@ -409,15 +416,20 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
             else
                 tc::commit_warp(bar);
         };
-        auto issue_s = [&](int j) {
+        // S of tile j: all of it, or (P over S) half hf of its keys
+        auto issue_s = [&](int j, int hf) {
+            constexpr int N = Sh::SEPARATE_P ? Sh::BN : Sh::BN / 2;
+            constexpr uint32_t idS = tc::idesc_f16(kBf16, Sh::BM, N, false, false);
             const int sl = j % NS;
             tc::fence_after_sync();
-            const uint64_t kd = k_desc + (uint64_t)((sl * Sh::SLOT_BYTES) >> 4);
+            const uint64_t kd =
+                k_desc + (uint64_t)((sl * Sh::SLOT_BYTES + hf * N * 128) >> 4);
 #pragma unroll
             for (int k = 0; k < D / 32; ++k)      // 32 bytes along the 128-byte row a step
-                tc::mma_ss_warp(ts, q_desc + 2 * k, kd + 2 * k, idS, k > 0);
-            tc::commit_warp(s_bar(g));
-            release(kempty(sl), j);
+                tc::mma_ss_warp(ts + hf * N, q_desc + 2 * k, kd + 2 * k, idS, k > 0);
+            tc::commit_warp(hf ? s_high_bar(g) : s_bar(g));
+            if (Sh::SEPARATE_P || hf)
+                release(kempty(sl), j);
         };
         // O_g += P_g,j . V_j, each half of the keys once the softmax has written
         // its P
@@ -440,28 +452,25 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
             release(vempty(sl), j);
             return true;
         };
-        // map 1 starts half a tile behind: the maps' softmaxes then alternate on
-        // the sub-cores and their MMAs on the tensor core (1213 us against 1281 on
-        // two 2048-token chunks at 16K, 213 against 227 on 8 x 512 tokens).  Taking
-        // turns at the exponentials tile by tile cost more than it gave (1287, 221).
+        // map 1 starts half a tile behind: the maps' softmaxes then alternate on the
+        // sub-cores and their MMAs on the tensor core, for a while (1146 us against 1156
+        // on two 2048-token chunks at 16K, 195 against 199 on 8 x 512 tokens)
         bool ok = k_ready(0) && wait_all(q_bar, 0) && (g == 0 || wait_all(start_bar, 0));
         if (ok)
-            issue_s(0);
+            issue_s(0, 0);
+        if (ok && !Sh::SEPARATE_P)
+            issue_s(0, 1);
         for (int j = 0; ok && j < nt; ++j) {
             const bool more = j + 1 < nt;
             ok = v_ready(j) && (!more || k_ready(j + 1)) &&
                  (!ragged || more || wait_all(z_bar, 0));
-            if constexpr (Sh::SEPARATE_P) {
-                // S_g,j+1 only needs the softmax to have read S_g,j
-                if (ok && more && (ok = wait_all(read_bar(g), j & 1)))
-                    issue_s(j + 1);
-                ok = ok && issue_pv(j);
-            } else {
-                ok = ok && issue_pv(j);
-                // S_g,j+1 reuses the TMEM columns P_g,j . V_j reads
-                if (ok && more && (ok = wait_all(o_bar(g), j & 1)))
-                    issue_s(j + 1);
-            }
+            // S_g,j+1, or its first half, only needs the softmax to have read S_g,j's
+            if (ok && more && (ok = wait_all(read_bar(g), j & 1)))
+                issue_s(j + 1, 0);
+            ok = ok && issue_pv(j);
+            // the second half goes where P_g,j was
+            if (!Sh::SEPARATE_P && ok && more && (ok = wait_all(o_bar(g), j & 1)))
+                issue_s(j + 1, 1);
         }
         if (!ok && lane == 0)
             give_up();
@@ -525,33 +534,51 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
             tc::fence_after_sync();
             const int k0 = j * Sh::BN;
             const int vis = pos - k0;              // keys [0, vis] of the tile are visible
-            // the 128 scores of the row, both halves held in registers
+            // the 128 scores of the row, both halves held in registers; the first
+            // half's maximum is taken while the second half is on its way
             uint32_t v[2][64];
-            __syncwarp();                        // tcgen05.ld is warp-collective
-            tc::tmem_ld64(tg, v[0]);
-            tc::tmem_ld64(tg + 64, v[1]);
-            if constexpr (Sh::SEPARATE_P) {
-                tc::fence_before_sync();
-                arrive(read_bar(grp));           // S_g,j+1 may go in
-            }
             // tiles left of the diagonal (the common case) need no mask
             const bool full = __all_sync(FULL, vis >= Sh::BN - 1);
-            if (!full) {
+            auto mask = [&](int from, int to) {
+                if (!full) {
 #pragma unroll
-                for (int e = 0; e < Sh::BN; ++e)
-                    if (e > vis)
-                        v[e >> 6][e & 63] = __float_as_uint(-INFINITY);
-            }
-            // row maximum as a tree, three operands per instruction
-            float mx[8];
+                    for (int e = 0; e < Sh::BN; ++e)
+                        if (e >= from && e < to && e > vis)
+                            v[e >> 6][e & 63] = __float_as_uint(-INFINITY);
+                }
+            };
+            auto x = [&](int i) { return __uint_as_float(v[i >> 6][i & 63]); };
+            float mx[8];                         // trees, three operands per instruction
+            __syncwarp();                        // tcgen05.ld is warp-collective
+            tc::tmem_ld64(tg, v[0]);
+            if constexpr (Sh::SEPARATE_P)
+                tc::tmem_ld64(tg + 64, v[1]);
+            tc::fence_before_sync();
+            arrive(read_bar(grp));               // S_g,j+1 (its first half) may go in
+            mask(0, Sh::SEPARATE_P ? Sh::BN : 64);
 #pragma unroll
             for (int a = 0; a < 8; ++a) {
-                auto x = [&](int i) { return __uint_as_float(v[i >> 6][i & 63]); };
                 float t = fmax3(x(a), x(a + 8), x(a + 16));
+                t = fmax3(t, x(a + 24), x(a + 32));
+                t = fmax3(t, x(a + 40), x(a + 48));
+                mx[a] = fmaxf(t, x(a + 56));
+            }
+            if constexpr (!Sh::SEPARATE_P) {
+                if (!__all_sync(FULL, mbar_wait_bounded(s_high_bar(grp), j & 1))) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after_sync();
+                __syncwarp();
+                tc::tmem_ld64(tg + 64, v[1]);
+                mask(64, Sh::BN);
+            }
 #pragma unroll
-                for (int i = a + 24; i < 120; i += 16)
-                    t = fmax3(t, x(i), x(i + 8));
-                mx[a] = fmaxf(t, x(a + 120));
+            for (int a = 0; a < 8; ++a) {
+                float t = fmax3(mx[a], x(a + 64), x(a + 72));
+                t = fmax3(t, x(a + 80), x(a + 88));
+                t = fmax3(t, x(a + 96), x(a + 104));
+                mx[a] = fmax3(t, x(a + 112), x(a + 120));
             }
             float mt = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
                              fmaxf(mx[6], mx[7]));
@@ -656,8 +683,8 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
         const bool normed = p.norm_w != nullptr;
 #pragma unroll
         for (int i = 0; i < CH; ++i)
-            wv[i] = normed ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.norm_w) +
-                                                                   grp * HC) + i)
+            wv[i] = normed ? __ldg(reinterpret_cast<const uint4 *>(
+                                       static_cast<const T *>(p.norm_w) + grp * HC) + i)
                            : make_uint4(0, 0, 0, 0);
         if (ok && !__all_sync(FULL, mbar_wait_bounded(o_bar(grp), (nt - 1) & 1)))
             ok = false;

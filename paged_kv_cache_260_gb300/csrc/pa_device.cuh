@@ -78,6 +78,18 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
     return true;
 }
 
+// The same for a converged warp, which leaves the loop together (all lanes
+// exit on one vote: no branch the warp could diverge at).
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity)
+{
+    const uint64_t t0 = global_ns();
+    while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+        if (__any_sync(0xffffffffu, global_ns() - t0 > kWaitLimitNs))
+            return false;
+    }
+    return true;
+}
+
 // 2^x on the special-function unit (PTX ex2.approx.ftz: relative error
 // about 2^-22, subnormal results flushed to zero, 2^-inf = 0).
 __device__ __forceinline__ float ex2_approx(float x)

@@ -29,8 +29,9 @@
 //    2,600 cycles a tile.  P needs only the second half of the score columns, so the
 //    next tile's first 64 keys are scored into the first half while the softmax
 //    is at its exponentials (M 128, N 64 reads Q from shared memory twice as often
-//    and takes 1.5 times as long): 1146 us, 2,480 cycles, of which the tensor core
-//    works for 1,792 and the 256 exponentials of a sub-core take 1,050.
+//    and takes 1.5 times as long): 1146 us, and 1130 with waits that a warp leaves
+//    together; 2,450 cycles, of which the tensor core works for 1,792 and the 256
+//    exponentials of a sub-core take 1,050.
 //  * Short contexts: a block's start and end.  8 x 512 tokens over 0.5K to 4K are
 //    6.7 blocks an SM of about 16 tiles each, and 15,600 of a block's 56,000 cycles
 //    passed before its first softmax, after its last P and between blocks.  The
@@ -397,13 +398,10 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
         const uint64_t v_desc = tc::sdesc_sw128(sbase + Sh::OFF_V, Sh::NB * Sh::BOX, 1024);
         const uint32_t ts = tmem + g * Sh::MAP_COLS, tp = ts + Sh::COL_P, to = ts + Sh::COL_O;
         static_assert(Sh::BM * 128 == Sh::NB * Sh::BOX, "Q and K halves 16 KB apart");
-        auto wait_all = [&](uint32_t bar, uint32_t parity) {
-            return __all_sync(FULL, mbar_wait_bounded(bar, parity));
-        };
         // a slot's wait costs 100 to 250 cycles even when its copy has long
         // landed, so it comes before the wait for the softmax or the last P.V
-        auto k_ready = [&](int j) { return wait_all(kfull(j % NS), (j / NS) & 1); };
-        auto v_ready = [&](int j) { return wait_all(vfull(j % NS), (j / NS) & 1); };
+        auto k_ready = [&](int j) { return mbar_wait_warp(kfull(j % NS), (j / NS) & 1); };
+        auto v_ready = [&](int j) { return mbar_wait_warp(vfull(j % NS), (j / NS) & 1); };
         // A slot is free once both maps of every block of the cluster have read
         // tile j.  Only said of slots that a later tile takes: then the other
         // block's producer waits for every arrival on its barriers, and none is
@@ -438,7 +436,7 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
             const uint64_t vd = v_desc + (uint64_t)((sl * Sh::SLOT_BYTES) >> 4);
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-                if (!wait_all(p_bar(g, hf), j & 1))
+                if (!mbar_wait_warp(p_bar(g, hf), j & 1))
                     return false;
                 tc::fence_after_sync();
 #pragma unroll
@@ -455,28 +453,35 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
         // map 1 starts half a tile behind: the maps' softmaxes then alternate on the
         // sub-cores and their MMAs on the tensor core, for a while (1146 us against 1156
         // on two 2048-token chunks at 16K, 195 against 199 on 8 x 512 tokens)
-        bool ok = k_ready(0) && wait_all(q_bar, 0) && (g == 0 || wait_all(start_bar, 0));
+        bool ok = k_ready(0) && mbar_wait_warp(q_bar, 0) &&
+                  (g == 0 || mbar_wait_warp(start_bar, 0));
         if (ok)
             issue_s(0, 0);
         if (ok && !Sh::SEPARATE_P)
             issue_s(0, 1);
         for (int j = 0; ok && j < nt; ++j) {
             const bool more = j + 1 < nt;
-            ok = v_ready(j) && (!more || k_ready(j + 1)) &&
-                 (!ragged || more || wait_all(z_bar, 0));
+            // V_j is waited for before S_g,j+1 goes out at head_dim 64, where that has
+            // time (2 x 2048 tokens at 16K: 982 us against 999), after it at 128
+            ok = (!Sh::SEPARATE_P ||
+                  (v_ready(j) && (!ragged || more || mbar_wait_warp(z_bar, 0)))) &&
+                 (!more || k_ready(j + 1));
             // S_g,j+1, or its first half, only needs the softmax to have read S_g,j's
-            if (ok && more && (ok = wait_all(read_bar(g), j & 1)))
+            if (ok && more && (ok = mbar_wait_warp(read_bar(g), j & 1)))
                 issue_s(j + 1, 0);
-            ok = ok && issue_pv(j);
+            ok = ok &&
+                 (Sh::SEPARATE_P ||
+                  (v_ready(j) && (!ragged || more || mbar_wait_warp(z_bar, 0)))) &&
+                 issue_pv(j);
             // the second half goes where P_g,j was
-            if (!Sh::SEPARATE_P && ok && more && (ok = wait_all(o_bar(g), j & 1)))
+            if (!Sh::SEPARATE_P && ok && more && (ok = mbar_wait_warp(o_bar(g), j & 1)))
                 issue_s(j + 1, 1);
         }
         if (!ok && lane == 0)
             give_up();
         // no MMA may still run when TMEM is freed
         tc::commit_warp(drain_bar(g));
-        if (!wait_all(drain_bar(g), 0) && lane == 0)
+        if (!mbar_wait_warp(drain_bar(g), 0) && lane == 0)
             give_up();
         leave();
     } else if (warp == 3) {
@@ -527,7 +532,7 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
         float m = 0.f, l = 0.f;
         bool ok = true;
         for (int j = 0; j < nt; ++j) {
-            if (!__all_sync(FULL, mbar_wait_bounded(s_bar(grp), j & 1))) {
+            if (!mbar_wait_warp(s_bar(grp), j & 1)) {
                 ok = false;
                 break;
             }
@@ -564,7 +569,7 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
                 mx[a] = fmaxf(t, x(a + 56));
             }
             if constexpr (!Sh::SEPARATE_P) {
-                if (!__all_sync(FULL, mbar_wait_bounded(s_high_bar(grp), j & 1))) {
+                if (!mbar_wait_warp(s_high_bar(grp), j & 1)) {
                     ok = false;
                     break;
                 }
@@ -615,7 +620,7 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
                 if (Sh::SEPARATE_P && hf == 0) {
                     // P_g,j overwrites P_g,j-1, and O may be rescaled below: both
                     // wait for P_g,j-1 . V_j-1 (with P over S, S_g,j came after it)
-                    if (j > 0 && !__all_sync(FULL, mbar_wait_bounded(o_bar(grp), (j - 1) & 1))) {
+                    if (j > 0 && !mbar_wait_warp(o_bar(grp), (j - 1) & 1)) {
                         ok = false;
                         break;
                     }
@@ -628,7 +633,7 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
                     // MMA), by both maps' threads; both issuers wait for all of them
                     if (ragged && j == nt - 1) {
                         const int sl = j % NS;
-                        if (!__all_sync(FULL, mbar_wait_bounded(vfull(sl), (j / NS) & 1))) {
+                        if (!mbar_wait_warp(vfull(sl), (j / NS) & 1)) {
                             ok = false;
                             break;
                         }
@@ -686,7 +691,7 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
             wv[i] = normed ? __ldg(reinterpret_cast<const uint4 *>(
                                        static_cast<const T *>(p.norm_w) + grp * HC) + i)
                            : make_uint4(0, 0, 0, 0);
-        if (ok && !__all_sync(FULL, mbar_wait_bounded(o_bar(grp), (nt - 1) & 1)))
+        if (ok && !mbar_wait_warp(o_bar(grp), (nt - 1) & 1))
             ok = false;
         // Row sums and the halves' sums of squares go through shared memory.
         // Every softmax thread takes part in both barriers, also after a wait that

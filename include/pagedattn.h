@@ -437,6 +437,53 @@ int pa_qk_norm_rope(void *q_out, void *k_out, const void *q, const void *k,
                     int64_t q_out_stride, int64_t k_out_stride, int dtype, void *stream);
 
 /*
+ * The four calls above with their arguments in one struct, for language bindings
+ * that pay for every argument (27 of them through ctypes 2.3 us, one 0.4).  The
+ * fields are those calls' arguments of the same names; `size` is the struct's
+ * size, anything else is PA_ERR_INVALID_ARG.  The struct is read during the
+ * call alone.  Doubles are rounded to float.
+ *
+ * pa_rope_args: k and v are pa_rope_and_cache's k_new and v_new; it does not
+ * look at k_out and k_out_stride, nor pa_qk_norm_rope at v, k_cache, v_cache,
+ * slot_mapping, v_stride, block_size and num_blocks.  pa_diff_args:
+ * pa_diff_decode does not look at query_start and max_query_len.
+ */
+struct pa_rope_args {
+    uint64_t size;
+    void *q_out, *k_out;
+    const void *q, *k, *v;
+    void *k_cache, *v_cache;
+    const int64_t *slot_mapping;
+    const int32_t *positions;
+    const float *cos_sin;
+    const void *q_norm, *k_norm;
+    void *stream;
+    int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+    double eps;
+    int32_t num_tokens, num_heads, num_kv_heads, head_dim, num_maps, block_size, num_blocks,
+        max_position, rotary_dim, interleaved, dtype;
+};
+
+struct pa_diff_args {
+    uint64_t size;
+    void *out;
+    const void *q, *k_cache, *v_cache;
+    const int32_t *block_tables, *seq_lens, *query_start;
+    const float *lambda;
+    const void *norm_weight;
+    void *workspace, *stream;
+    uint64_t workspace_bytes;
+    double scale, norm_eps, out_scale;
+    int32_t num_seqs, max_query_len, num_heads, num_kv_heads, head_dim, block_size,
+        max_blocks_per_seq, num_blocks, dtype;
+};
+
+int pa_rope_and_cache_args(const struct pa_rope_args *args);
+int pa_qk_norm_rope_args(const struct pa_rope_args *args);
+int pa_diff_decode_args(const struct pa_diff_args *args);
+int pa_diff_prefill_args(const struct pa_diff_args *args);
+
+/*
  * Copy-on-write of shared blocks: for every pair i,
  *     k_cache[dst] = k_cache[src], v_cache[dst] = v_cache[src]
  * whole blocks (every kv head and slot), with (src, dst) =

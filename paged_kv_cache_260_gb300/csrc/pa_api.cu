@@ -8,6 +8,7 @@
 #include <math.h>
 #include <mutex>
 #include <stdint.h>
+#include <string.h>
 
 #include "pa_cache.h"
 #include "pa_internal.h"
@@ -337,6 +338,19 @@ int decode_mode(int partition_size, int *mode, int *part_tiles)
         return PA_ERR_INVALID_ARG;
     }
     return PA_OK;
+}
+
+// The struct forms: a copy of the caller's, whose address need not be aligned.
+template <typename A>
+bool read_args(const A *from, A *to)
+{
+    if (!from)
+        return false;
+    memcpy(&to->size, from, sizeof(to->size));
+    if (to->size != sizeof(A))
+        return false;
+    memcpy(to, from, sizeof(A));
+    return true;
 }
 
 }  // namespace
@@ -1261,6 +1275,53 @@ int pa_qk_norm_rope(void *q_out, void *k_out, const void *q, const void *k,
     p.max_position = max_position;
     p.eps = eps;
     return rope_impl(p, false, num_heads, head_dim, interleaved, dtype, stream);
+}
+
+int pa_rope_and_cache_args(const struct pa_rope_args *args)
+{
+    pa_rope_args a;
+    if (!read_args(args, &a))
+        return PA_ERR_INVALID_ARG;
+    return pa_rope_and_cache(a.q_out, a.q, a.k, a.v, a.k_cache, a.v_cache, a.slot_mapping,
+                             a.positions, a.cos_sin, a.q_norm, a.k_norm, a.num_tokens, a.num_heads,
+                             a.num_kv_heads, a.head_dim, a.num_maps, a.block_size, a.num_blocks,
+                             a.max_position, a.rotary_dim, a.interleaved, (float)a.eps, a.q_stride,
+                             a.k_stride, a.v_stride, a.q_out_stride, a.dtype, a.stream);
+}
+
+int pa_qk_norm_rope_args(const struct pa_rope_args *args)
+{
+    pa_rope_args a;
+    if (!read_args(args, &a))
+        return PA_ERR_INVALID_ARG;
+    return pa_qk_norm_rope(a.q_out, a.k_out, a.q, a.k, a.positions, a.cos_sin, a.q_norm, a.k_norm,
+                           a.num_tokens, a.num_heads, a.num_kv_heads, a.head_dim, a.num_maps,
+                           a.max_position, a.rotary_dim, a.interleaved, (float)a.eps, a.q_stride,
+                           a.k_stride, a.q_out_stride, a.k_out_stride, a.dtype, a.stream);
+}
+
+int pa_diff_decode_args(const struct pa_diff_args *args)
+{
+    pa_diff_args a;
+    if (!read_args(args, &a))
+        return PA_ERR_INVALID_ARG;
+    return pa_diff_decode(a.out, a.q, a.k_cache, a.v_cache, a.block_tables, a.seq_lens, a.lambda,
+                          a.norm_weight, a.num_seqs, a.num_heads, a.num_kv_heads, a.head_dim,
+                          a.block_size, a.max_blocks_per_seq, a.num_blocks, (float)a.scale,
+                          (float)a.norm_eps, (float)a.out_scale, a.dtype, a.workspace,
+                          a.workspace_bytes, a.stream);
+}
+
+int pa_diff_prefill_args(const struct pa_diff_args *args)
+{
+    pa_diff_args a;
+    if (!read_args(args, &a))
+        return PA_ERR_INVALID_ARG;
+    return pa_diff_prefill(a.out, a.q, a.k_cache, a.v_cache, a.block_tables, a.seq_lens,
+                           a.query_start, a.lambda, a.norm_weight, a.num_seqs, a.max_query_len,
+                           a.num_heads, a.num_kv_heads, a.head_dim, a.block_size,
+                           a.max_blocks_per_seq, a.num_blocks, (float)a.scale, (float)a.norm_eps,
+                           (float)a.out_scale, a.dtype, a.workspace, a.workspace_bytes, a.stream);
 }
 
 int pa_copy_blocks(void *k_cache, void *v_cache, const int64_t *block_mapping, int num_pairs,

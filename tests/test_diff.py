@@ -107,3 +107,34 @@ def test_reference_by_hand():
     q[..., 2:], k[..., 2:] = q[..., :2], k[..., :2]
     ref, _ = reference(q, k, v, tables, 0, [2], torch.tensor([1.0]), 0.5, None, 0.0, 1.0, 0.0)
     assert float(ref.abs().max()) < 1e-12
+
+
+def _packed(entry, size=None, **kw):
+    from paged_kv_cache_260_gb300 import _DIFF_ARGS
+    a = dict(out=0x2000, q=FAKE, k=FAKE, v=FAKE, tables=FAKE, lens=FAKE, start=FAKE, lam=FAKE, w=0,
+             ws=0, stream=0, wb=0, scale=0.1, eps=1e-6, os=1.0, n=4, longest=32, hq=8, hkv=2, d=128,
+             bs=16, mb=8, nb=64, dtype=0)
+    a.update(kw)
+    return entry(_DIFF_ARGS.pack(_DIFF_ARGS.size if size is None else size, *a.values()))
+
+
+@pytest.mark.parametrize("name", ["pa_diff_decode_args", "pa_diff_prefill_args"])
+@pytest.mark.parametrize("kw,status", [
+    (dict(n=0), 0), (dict(n=0, size=0), 1), (dict(n=0, size=184), 1), (dict(n=-1), 1),
+    (dict(hq=7), 1), (dict(hkv=0), 1), (dict(d=96), 2), (dict(bs=8), 2), (dict(mb=0), 1),
+    (dict(nb=0), 1), (dict(dtype=3), 2), (dict(scale=math.nan), 1), (dict(eps=-1.0), 1),
+    (dict(os=1e300), 1), (dict(out=0), 1), (dict(out=FAKE), 1), (dict(q=0x1008), 1),
+    (dict(k=0), 1), (dict(v=0x1008), 1), (dict(tables=0), 1), (dict(lens=0x1001), 1),
+    (dict(lam=0), 1), (dict(w=0x1008), 1)])
+def test_packed_arguments_arrive(lib, name, kw, status):
+    assert _packed(getattr(lib, name), **kw) == status
+
+
+def test_packed_arguments_of_one(lib):
+    assert lib.pa_diff_decode_args(None) == 1 and lib.pa_diff_prefill_args(None) == 1
+    assert _packed(lib.pa_diff_decode_args, hq=34) == 2
+    assert _packed(lib.pa_diff_prefill_args, start=0) == 1
+    assert _packed(lib.pa_diff_prefill_args, longest=-1) == 1
+    assert _packed(lib.pa_diff_prefill_args, longest=0) == 0
+    assert _packed(lib.pa_diff_prefill_args, ws=0x1010, wb=4096) == 3
+    assert _packed(lib.pa_diff_prefill_args, ws=0x1000, wb=16) == 3

@@ -76,3 +76,40 @@ def test_bindings_refuse_host_tensors():
         pa.qk_norm_rope(q, k, q, k, pos, cs)
     with pytest.raises(ValueError):
         pa.rope_and_cache(q, q, k, k, pool, pool, pos.long(), pos, cs)
+
+
+def _packed(entry, size=None, **kw):
+    from paged_kv_cache_260_gb300 import _ROPE_ARGS
+    a = dict(q_out=FAKE, k_out=FAKE, q=FAKE, k=FAKE, v=FAKE, kc=FAKE, vc=FAKE, slots=FAKE, pos=FAKE,
+             cs=FAKE, qn=0, kn=0, stream=0, qs=1024, ks=256, vs=256, qos=1024, kos=256, eps=1e-6,
+             tokens=0, hq=8, hkv=2, d=128, maps=1, bs=16, nb=64, table=32, rot=128, inter=0,
+             dtype=0)
+    a.update(kw)
+    return entry(_ROPE_ARGS.pack(_ROPE_ARGS.size if size is None else size, *a.values()))
+
+
+@pytest.mark.parametrize("name", ["pa_rope_and_cache_args", "pa_qk_norm_rope_args"])
+@pytest.mark.parametrize("kw,status", [
+    (dict(), 0), (dict(size=0), 1), (dict(size=200), 1), (dict(tokens=-1), 1), (dict(hq=7), 1),
+    (dict(hkv=0), 1), (dict(d=96, rot=64), 2), (dict(maps=3), 2), (dict(rot=24), 2),
+    (dict(table=0), 1), (dict(dtype=5), 2), (dict(eps=-1.0), 1), (dict(eps=1e300), 1),
+    (dict(tokens=4, q=0), 1), (dict(tokens=4, k=0x1008), 1), (dict(tokens=4, q_out=0), 1),
+    (dict(tokens=4, pos=0), 1), (dict(tokens=4, cs=0x1004), 1), (dict(tokens=4, qn=0x1002), 1),
+    (dict(tokens=4, kn=0x1002), 1), (dict(tokens=4, qs=1028), 1), (dict(tokens=4, ks=255), 1),
+    (dict(tokens=4, qos=1016), 1)])
+def test_packed_arguments_arrive(lib, name, kw, status):
+    assert _packed(getattr(lib, name), **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(bs=32), 2), (dict(nb=0), 1), (dict(tokens=4, v=0), 1), (dict(tokens=4, kc=0x1004), 1),
+    (dict(tokens=4, vc=0), 1), (dict(tokens=4, slots=0), 1), (dict(tokens=4, vs=248), 1)])
+def test_packed_arguments_of_the_pool_arrive(lib, kw, status):
+    assert _packed(lib.pa_rope_and_cache_args, **kw) == status
+
+
+def test_packed_arguments_null(lib):
+    assert lib.pa_rope_and_cache_args(None) == 1
+    assert lib.pa_qk_norm_rope_args(None) == 1
+    assert _packed(lib.pa_qk_norm_rope_args, tokens=4, k_out=0) == 1
+    assert _packed(lib.pa_qk_norm_rope_args, tokens=4, kos=248) == 1

@@ -239,7 +239,10 @@ int pa_prefill(void *out, const void *q, const void *k_cache, const void *v_cach
  * norm_eps and out_scale of pa_diff_decode, the chunks, the causal mask, the
  * work order and the other arguments of pa_prefill (groups up to 128 heads,
  * scale > 0).  The softmax weights are rounded to dtype before the product
- * with V.  Rows of out past query_start[num_seqs] are left as they were.
+ * with V.  Rows of out past query_start[num_seqs] are left as they were.  A few
+ * query tiles against a long table are spread over the SMs by their keys; over
+ * how many, and with it the last bit of a result, follows from the sizes
+ * passed and the sequence's length, not from the run.
  */
 size_t pa_diff_prefill_workspace_size(int num_seqs, int max_query_len, int num_heads,
                                       int num_kv_heads);

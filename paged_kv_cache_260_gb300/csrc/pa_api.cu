@@ -66,6 +66,14 @@ constexpr int kMaxOcc = 512;
 OccEntry g_occ[kMaxOcc];
 int g_occ_count = 0;
 
+struct ClusterEntry {
+    const void *func;
+    int device, cluster, active;
+};
+constexpr int kMaxCluster = 256;
+ClusterEntry g_cluster[kMaxCluster];
+int g_cluster_count = 0;
+
 int device_state(DeviceState **out)
 {
     int dev = 0;
@@ -166,6 +174,41 @@ int occupancy(const void *func, int dev, int threads, size_t smem, int *blocks)
     return PA_OK;
 }
 
+// How many clusters of this many blocks the device runs at once (which SMs share
+// a GPC differs between devices), 0 if it cannot.
+int active_clusters(const void *func, int dev, int threads, size_t smem, int cluster)
+{
+    {
+        std::lock_guard<std::mutex> lock(g_mutex);
+        for (int i = 0; i < g_cluster_count; ++i)
+            if (g_cluster[i].func == func && g_cluster[i].device == dev &&
+                g_cluster[i].cluster == cluster)
+                return g_cluster[i].active;
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(cluster);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if ((cluster > 8 &&
+         cudaFuncSetAttribute(func, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+             cudaSuccess) ||
+        cudaOccupancyMaxActiveClusters(&n, func, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+    }
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (g_cluster_count < kMaxCluster)
+        g_cluster[g_cluster_count++] = ClusterEntry{func, dev, cluster, n};
+    return n;
+}
+
 // cuTensorMapEncodeTiled, reached through the runtime so the library needs no
 // direct link against the driver library.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
@@ -233,18 +276,21 @@ int make_pool_map(CUtensorMap *tm, const void *pool, int dtype, int head_dim, lo
 }
 
 int launch_dependent(const void *func, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                     void **args)
+                     void **args, int cluster = 1)
 {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelExC(&cfg, func, args) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -986,8 +1032,8 @@ static int prefill_impl(void *out, const void *q, const void *k_cache, const voi
     // differential: a unit is two blocks' query tiles, unless every chunk fits one
     const bool pairs = diff && max_query_len > kPrefillRows / group;
     const int tiles = diff && !pairs ? 1 : kPrefillTiles;
-    const long long q_ranks = prefill_q_ranks(max_query_len, num_heads, num_kv_heads, tiles);
-    const long long grid = q_ranks * num_seqs * num_kv_heads * (pairs ? 2 : 1);
+    long long q_ranks = prefill_q_ranks(max_query_len, num_heads, num_kv_heads, tiles);
+    long long grid = q_ranks * num_seqs * num_kv_heads * (pairs ? 2 : 1);
     if ((long long)max_blocks_per_seq * kBlockSize >= (1LL << 30) || pool_rows >= (1LL << 31) ||
         grid >= (1LL << 31))
         return PA_ERR_UNSUPPORTED;
@@ -1016,6 +1062,31 @@ static int prefill_impl(void *out, const void *q, const void *k_cache, const voi
         return rc;
     if (kk.smem > limit)
         return PA_ERR_UNSUPPORTED;
+    // Differential, and query tiles for half the SMs at most: a cluster of blocks
+    // shares the keys of each, two key tiles or more a block, as many blocks as
+    // leave all clusters running at once (one tile against 16K keys: 209 us on
+    // one block, 35 on 8).
+    int split = 1;
+    const long long one = prefill_q_ranks(max_query_len, num_heads, num_kv_heads, 1);
+    const long long units = one * num_seqs * num_kv_heads;
+    const int key_tiles = (max_blocks_per_seq * kBlockSize + kPrefillKeys - 1) / kPrefillKeys;
+    if (diff && key_tiles >= 4 && 2 * units <= ds->num_sms) {
+        PrefillKernel ks{};
+        if (!diff_prefill_kernel(dtype, head_dim, false, &ks))
+            return PA_ERR_UNSUPPORTED;
+        rc = ensure_smem(ks.fn, dev, ks.smem);
+        if (rc != PA_OK)
+            return rc;
+        for (int n : kSplits)
+            if (split == 1 && 2 * n <= key_tiles &&
+                units <= active_clusters(ks.fn, dev, ks.threads, ks.smem, n))
+                split = n;
+        if (split > 1) {
+            kk = ks;
+            q_ranks = one;
+            grid = units * split;
+        }
+    }
     rc = ensure_smem(kk.fn, dev, kk.smem);
     if (rc != PA_OK)
         return rc;
@@ -1047,7 +1118,7 @@ static int prefill_impl(void *out, const void *q, const void *k_cache, const voi
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // differential: blocks that all run at once need no order, and no launch to
     // make one (chunks of 5 and 70 tokens: 8.3 us in a graph against 10.4)
-    if (diff && grid <= ds->num_sms)
+    if (diff && (split > 1 || grid <= ds->num_sms))
         planned = false;
     if (planned) {
         int *count = static_cast<int *>(workspace);
@@ -1074,7 +1145,8 @@ static int prefill_impl(void *out, const void *q, const void *k_cache, const voi
     // a programmatic dependent launch: its blocks may be scheduled while the
     // plan finishes and read no global memory before it has completed
     void *args[] = {&p, &tmk, &tmv};
-    return launch_dependent(kk.fn, dim3((unsigned)grid), dim3(kk.threads), kk.smem, st, args);
+    return launch_dependent(kk.fn, dim3((unsigned)grid), dim3(kk.threads), kk.smem, st, args,
+                            split);
 }
 
 int pa_prefill(void *out, const void *q, const void *k_cache, const void *v_cache,

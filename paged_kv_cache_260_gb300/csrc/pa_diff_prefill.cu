@@ -38,6 +38,14 @@
 //    barriers first, K_0 and the query rows in flight over the block's last
 //    barrier, no releasing cluster arrivals, the norm's weights and lambda loaded
 //    ahead, output rows stored by whole lines: 11,200 cycles, 211 -> 197 us.
+//  * Few query tiles (short chunks against long caches): the SMs without one. A
+//    cluster of up to 16 blocks shares the keys of one tile, each block a run of
+//    them, and joins its results through distributed shared memory (join_split;
+//    128 KB of O, one row in so many to a block; no workspace and no second
+//    launch).  16 tokens at 16K, bf16, head_dim 128: 1 x 4/1 heads 208 us on one
+//    block, 24 on 16; 2 x 32/8 heads 210, on clusters of 6 46.  As many blocks as
+//    let all clusters run at once: with clusters of 8, of which 15 fit, the
+//    latter's 16 tiles took 71 us.
 //  * P through shared memory, which lets the next S go ahead, costs more shared
 //    memory bandwidth than there is (1437 us before the multicast); 80-key tiles
 //    with P in columns of its own 1702; two threads a row 1382 against 1197; turns
@@ -162,10 +170,103 @@ struct TableWindow {
     }
 };
 
+// The blocks of a cluster have each left, for every row of the unit (`rows` of
+// them) and map, their keys' maximum and sum (OFF_X: sums, then maxima) and O
+// (OFF_K: [map][row][D] fp32, 16-byte chunk i at i ^ (row & 7)).  Block `rank`
+// joins the rows rank, rank + SE, ..: 2 SE threads a row, or the power of two
+// below.
+template <typename T, int D, int SE>
+__device__ __forceinline__ void join_split(const PrefillParams &p, uint32_t sbase,
+                                           uint32_t abort_addr, int rank, int lt, int rows,
+                                           int G, int h, size_t token)
+{
+    using Sh = DiffShape<D>;
+    constexpr int TPR = SE == 3 ? 4 : SE == 6 ? 8 : 2 * SE;
+    constexpr int NC = D / 4 < TPR ? 1 : D / 4 / TPR;   // 16-byte chunks of a thread
+    static_assert((TPR & (TPR - 1)) == 0 && 256 / TPR * SE >= Sh::BM, "every row has its threads");
+    const int row = lt / TPR * SE + rank, tr = lt % TPR;
+    const bool live = row < rows && tr < D / 4;
+    float y[NC][4], ss = 0.f;
+    bool fine = true;
+#pragma unroll
+    for (int k = 0; k < NC; ++k)
+        y[k][0] = y[k][1] = y[k][2] = y[k][3] = 0.f;
+    if (live) {
+        float f[2][SE];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            float l[SE], top = -INFINITY, sum = 0.f;
+            const uint32_t at = sbase + Sh::OFF_X + (g * Sh::BM + row) * 4;
+#pragma unroll
+            for (int c = 0; c < SE; ++c) {
+                l[c] = cluster_load(cluster_addr(at, c));
+                f[g][c] = cluster_load(cluster_addr(at + 2 * Sh::BM * 4, c));
+            }
+#pragma unroll
+            for (int c = 0; c < SE; ++c)
+                top = fmaxf(top, f[g][c]);
+#pragma unroll
+            for (int c = 0; c < SE; ++c) {
+                f[g][c] = ex2_approx(f[g][c] - top);
+                sum = fmaf(l[c], f[g][c], sum);
+            }
+            const float of = (g ? -__ldg(p.lambda + h * G + row % G) : 1.f) / sum;
+#pragma unroll
+            for (int c = 0; c < SE; ++c)
+                f[g][c] *= of;
+        }
+#pragma unroll
+        for (int c = 0; c < SE; ++c) {
+            fine = fine && __float_as_int(cluster_load(cluster_addr(abort_addr, c))) == 0;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const uint32_t at =
+                    cluster_addr(sbase + Sh::OFF_K + (g * Sh::BM + row) * (D * 4), c);
+#pragma unroll
+                for (int k = 0; k < NC; ++k) {
+                    const float4 o = cluster_load4(at + (((k * TPR + tr) ^ (row & 7)) << 4));
+                    y[k][0] = fmaf(o.x, f[g][c], y[k][0]);
+                    y[k][1] = fmaf(o.y, f[g][c], y[k][1]);
+                    y[k][2] = fmaf(o.z, f[g][c], y[k][2]);
+                    y[k][3] = fmaf(o.w, f[g][c], y[k][3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < NC; ++k)
+            ss += fmaf(y[k][0], y[k][0], y[k][1] * y[k][1]) +
+                  fmaf(y[k][2], y[k][2], y[k][3] * y[k][3]);
+    }
+    __syncwarp();
+    float k0 = p.out_scale;
+    if (p.norm_w) {
+#pragma unroll
+        for (int off = 1; off < TPR; off <<= 1)
+            ss += __shfl_xor_sync(0xffffffffu, ss, off);
+        k0 *= rsqrtf(ss * (1.f / D) + p.norm_eps);
+    }
+    if (!live || !fine)
+        return;
+    T *out = static_cast<T *>(p.out) +
+             ((token + row / G) * p.num_heads + h * G + row % G) * D;
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+        const int ch = k * TPR + tr;              // 4 channels
+        float w[4] = {k0, k0, k0, k0};
+        if (p.norm_w) {
+            const uint2 wv = __ldg(static_cast<const uint2 *>(p.norm_w) + ch);
+            const float2 a = Elem<T>::to_f2(wv.x), b = Elem<T>::to_f2(wv.y);
+            w[0] *= a.x, w[1] *= a.y, w[2] *= b.x, w[3] *= b.y;
+        }
+        reinterpret_cast<uint2 *>(out)[ch] =
+            make_uint2(Mma<T>::pack(y[k][0] * w[0], y[k][1] * w[1]),
+                       Mma<T>::pack(y[k][2] * w[2], y[k][3] * w[3]));
+    }
+}
+
 template <typename T, int D, int CL>
-__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(DiffShape<D>::THREADS)
-diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap tmk,
-                      const __grid_constant__ CUtensorMap tmv)
+__device__ __forceinline__ void diff_prefill(const PrefillParams &p, const CUtensorMap &tmk,
+                                             const CUtensorMap &tmv)
 {
     using Sh = DiffShape<D>;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -200,7 +301,9 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int Hkv = p.num_kv_heads, Hq = p.num_heads, G = Hq / Hkv;
     const int TPB = Sh::BM / G;                   // chunk tokens per block
-    const int unit = blockIdx.x / CL;             // of the cluster: CL query tiles
+    // the cluster's work: CL query tiles, or one whose keys its blocks share out
+    const int split = CL > 1 ? 1 : (int)cluster_size(), part = CL > 1 ? 0 : (int)cluster_rank();
+    const int unit = blockIdx.x / (CL > 1 ? CL : split);
     const int cr = CL > 1 ? (int)cluster_rank() : 0;
     int h = unit % Hkv;
 
@@ -245,7 +348,7 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
     const int qs = __ldg(p.query_start + s);
     const int c = __ldg(p.query_start + s + 1) - qs;
     // the plan reports itself
-    const bool reporter = !p.plan && rank == 0 && h == 0 && tid == 0 && cr == 0;
+    const bool reporter = !p.plan && rank == 0 && h == 0 && tid == 0 && cr == 0 && part == 0;
     if (L < 0 || L > p.max_blocks * kBlockSize) {
         if (reporter)
             record_error(p.err, PA_DEVERR_SEQLEN_RANGE);
@@ -266,10 +369,19 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
     }
     const int t0 = (tile * CL + cr) * TPB;        // may lie past the chunk (no rows of its own)
     const int p_last = L - c + min((tile + 1) * CL * TPB, c) - 1;   // the cluster's last row
-    const int nt = p_last / Sh::BN + 1;           // key tiles, the same for the whole cluster
-    const int nblk = (L + kBlockSize - 1) / kBlockSize;
+    const int nt_all = p_last / Sh::BN + 1;       // key tiles, the same for the whole cluster
+    // 2, 3, 4, 6, 8 or 16 of the cluster's blocks share them, two tiles or more each
+    const int most = min(split, nt_all / 2);
+    const int parts = most >= 16 ? 16 : most >= 8 ? 8 : most >= 6 ? 6 : max(1, min(most, 4));
+    if (part >= parts)
+        return;
+    const int j0 = nt_all * part / parts;         // this block's first tile, and how many
+    const int nt = nt_all * (part + 1) / parts - j0;
+    // everything below counts keys, tiles and table entries from there
+    const int Lk = L - j0 * Sh::BN;
+    const int nblk = (Lk + kBlockSize - 1) / kBlockSize;
     // the last tile reaches past the sequence: its value rows there are zeroed
-    const bool ragged = nt * Sh::BN > L;
+    const bool ragged = nt * Sh::BN > Lk;
 
     // What the block reads first is in flight over its last barrier: the block
     // table's first windows (producer), and the Q tile (softmax warps).  Q row
@@ -277,7 +389,7 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
     // rows 128 - TPB*G that do not fill a token are zero; thread lt takes 16-byte
     // chunk lt % CPR of every (256 / CPR)-th row.
     using Window = TableWindow<Sh::NB>;
-    const int32_t *table = p.block_tables + (size_t)s * p.max_blocks;
+    const int32_t *table = p.block_tables + (size_t)s * p.max_blocks + j0 * Sh::NB;
     constexpr int CPR = D / 8;                    // 16-byte chunks per row
     constexpr int RSTEP = 256 / CPR;
     constexpr int NPT = Sh::BM / RSTEP;
@@ -521,7 +633,7 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
         const uint32_t tg = lanes + grp * Sh::MAP_COLS;
         const int tok = rr / G, hg = rr % G;
         const bool row_valid = rr < TPB * G && t0 + tok < c;
-        const int pos = row_valid ? L - c + t0 + tok : L - 1;
+        const int pos = (row_valid ? L - c + t0 + tok : L - 1) - j0 * Sh::BN;
         const float sl2 = p.scale_log2;
         const float lam = __ldg(p.lambda + h * G + hg);
         auto arrive = [&](uint32_t bar) {          // once a warp, after its lanes' work
@@ -637,7 +749,7 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
                             ok = false;
                             break;
                         }
-                        const int first = L - k0;
+                        const int first = Lk - k0;
                         const int n16 = (Sh::BN - first) * Sh::HALVES * 8;
                         unsigned char *vb = smem + Sh::OFF_V + sl * Sh::SLOT_BYTES;
                         for (int idx = lt; idx < n16; idx += 256) {
@@ -680,85 +792,115 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
             }
             l = fmaf(l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
         }
-        // ---------------- the difference, its norm, the output ----------------
-        // This thread's half of the channels; the norm's weights are in flight
-        // over the last P.V.
-        constexpr int HC = D / 2, CH = HC / 8;    // channels, 16-byte chunks
-        uint4 wv[CH];
-        const bool normed = p.norm_w != nullptr;
+        if (parts > 1) {
+            // ---------------- this block's keys' share, for join_split ----------------
+            if (ok && !mbar_wait_warp(o_bar(grp), (nt - 1) & 1))
+                ok = false;
+            if (!ok)
+                give_up();
+            float *xs = reinterpret_cast<float *>(smem + Sh::OFF_X);  // [sum, maximum][2][128]
+            xs[grp * Sh::BM + rr] = l;
+            xs[(2 + grp) * Sh::BM + rr] = m;
+            // past this barrier both maps' MMAs are done with the K and V tiles
+            tc::fence_before_sync();
+            softmax_warps_sync();
+            tc::fence_after_sync();
+            if (!__any_sync(FULL, *abort_flag != 0)) {
+                float4 *to = reinterpret_cast<float4 *>(smem + Sh::OFF_K) +
+                             (size_t)(grp * Sh::BM + rr) * (D / 4);
+#pragma unroll 1
+                for (int cc = 0; cc < D; cc += 32) {
+                    uint32_t o[32];
+                    __syncwarp();
+                    tc::tmem_ld32(tg + Sh::COL_O + cc, o);
 #pragma unroll
-        for (int i = 0; i < CH; ++i)
-            wv[i] = normed ? __ldg(reinterpret_cast<const uint4 *>(
-                                       static_cast<const T *>(p.norm_w) + grp * HC) + i)
-                           : make_uint4(0, 0, 0, 0);
-        if (ok && !mbar_wait_warp(o_bar(grp), (nt - 1) & 1))
-            ok = false;
-        // Row sums and the halves' sums of squares go through shared memory.
-        // Every softmax thread takes part in both barriers, also after a wait that
-        // gave up; past the first, both maps' last P.V are known to be done.
-        float *xl = reinterpret_cast<float *>(smem + Sh::OFF_X);      // [2][128]
-        float *xq = xl + 2 * Sh::BM;                                  // [2][128]
-        if (!ok)
-            give_up();
-        xl[grp * Sh::BM + rr] = l;
-        tc::fence_before_sync();
-        softmax_warps_sync();
-        tc::fence_after_sync();
-        leave();
-        ok = !__any_sync(FULL, *abort_flag != 0);
-        const float i0 = 1.f / xl[rr];
-        const float i1 = -lam / xl[Sh::BM + rr];
-        const uint32_t half = lanes + Sh::COL_O + grp * HC;
-        float y[HC], ss = 0.f;
-        if (ok) {
+                    for (int e = 0; e < 32; e += 4)
+                        to[((cc + e) / 4) ^ (rr & 7)] =
+                            make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                                        __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+                }
+            }
+        } else {
+            // ---------------- the difference, its norm, the output ----------------
+            // This thread's half of the channels; the norm's weights are in flight
+            // over the last P.V.
+            constexpr int HC = D / 2, CH = HC / 8;    // channels, 16-byte chunks
+            uint4 wv[CH];
+            const bool normed = p.norm_w != nullptr;
 #pragma unroll
-            for (int cc = 0; cc < HC; cc += 32) {
-                uint32_t a[32], b[32];
+            for (int i = 0; i < CH; ++i)
+                wv[i] = normed ? __ldg(reinterpret_cast<const uint4 *>(
+                                           static_cast<const T *>(p.norm_w) + grp * HC) + i)
+                               : make_uint4(0, 0, 0, 0);
+            if (ok && !mbar_wait_warp(o_bar(grp), (nt - 1) & 1))
+                ok = false;
+            // Row sums and the halves' sums of squares go through shared memory.
+            // Every softmax thread takes part in both barriers, also after a wait that
+            // gave up; past the first, both maps' last P.V are known to be done.
+            float *xl = reinterpret_cast<float *>(smem + Sh::OFF_X);      // [2][128]
+            float *xq = xl + 2 * Sh::BM;                                  // [2][128]
+            if (!ok)
+                give_up();
+            xl[grp * Sh::BM + rr] = l;
+            tc::fence_before_sync();
+            softmax_warps_sync();
+            tc::fence_after_sync();
+            leave();
+            ok = !__any_sync(FULL, *abort_flag != 0);
+            const float i0 = 1.f / xl[rr];
+            const float i1 = -lam / xl[Sh::BM + rr];
+            const uint32_t half = lanes + Sh::COL_O + grp * HC;
+            float y[HC], ss = 0.f;
+            if (ok) {
+#pragma unroll
+                for (int cc = 0; cc < HC; cc += 32) {
+                    uint32_t a[32], b[32];
+                    __syncwarp();
+                    tc::tmem_ld32(half + cc, a);
+                    tc::tmem_ld32(half + Sh::MAP_COLS + cc, b);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        y[cc + e] = fmaf(__uint_as_float(b[e]), i1, __uint_as_float(a[e]) * i0);
+                        ss = fmaf(y[cc + e], y[cc + e], ss);
+                    }
+                }
+            }
+            xq[grp * Sh::BM + rr] = ss;
+            softmax_warps_sync();
+            if (ok) {
+                float k = p.out_scale;
+                if (normed)
+                    k *= rsqrtf((xq[rr] + xq[Sh::BM + rr]) * (1.f / D) + p.norm_eps);
+                // Through the warp's part of the Q tile's shared memory (no MMA reads
+                // Q any more), so that a warp's stores are whole 128-byte lines: a
+                // row to a thread, they touched 32 lines an instruction.
+                uint4 *st = reinterpret_cast<uint4 *>(smem) + (warp - 4) * 32 * CH;
+#pragma unroll
+                for (int i = 0; i < CH; ++i) {
+                    float f[8];
+                    const uint32_t w32[4] = {wv[i].x, wv[i].y, wv[i].z, wv[i].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 x = normed ? Elem<T>::to_f2(w32[e]) : make_float2(1.f, 1.f);
+                        f[2 * e] = y[8 * i + 2 * e] * (k * x.x);
+                        f[2 * e + 1] = y[8 * i + 2 * e + 1] * (k * x.y);
+                    }
+                    st[lane * CH + (i ^ (lane % CH))] =
+                        make_uint4(Mma<T>::pack(f[0], f[1]), Mma<T>::pack(f[2], f[3]),
+                                   Mma<T>::pack(f[4], f[5]), Mma<T>::pack(f[6], f[7]));
+                }
                 __syncwarp();
-                tc::tmem_ld32(half + cc, a);
-                tc::tmem_ld32(half + Sh::MAP_COLS + cc, b);
+                const long long mine =
+                    row_valid ? ((long long)(qs + t0 + tok) * Hq + h * G + hg) * D + grp * HC : -1;
+                T *out = reinterpret_cast<T *>(p.out);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    y[cc + e] = fmaf(__uint_as_float(b[e]), i1, __uint_as_float(a[e]) * i0);
-                    ss = fmaf(y[cc + e], y[cc + e], ss);
+                for (int i = 0; i < CH; ++i) {
+                    const int row = i * (32 / CH) + lane / CH, ch = lane % CH;
+                    const long long at = __shfl_sync(FULL, mine, row);
+                    if (at >= 0)
+                        *reinterpret_cast<uint4 *>(out + at + 8 * ch) =
+                            st[row * CH + (ch ^ (row % CH))];
                 }
-            }
-        }
-        xq[grp * Sh::BM + rr] = ss;
-        softmax_warps_sync();
-        if (ok) {
-            float k = p.out_scale;
-            if (normed)
-                k *= rsqrtf((xq[rr] + xq[Sh::BM + rr]) * (1.f / D) + p.norm_eps);
-            // Through the warp's part of the Q tile's shared memory (no MMA reads
-            // Q any more), so that a warp's stores are whole 128-byte lines: a
-            // row to a thread, they touched 32 lines an instruction.
-            uint4 *st = reinterpret_cast<uint4 *>(smem) + (warp - 4) * 32 * CH;
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                float f[8];
-                const uint32_t w32[4] = {wv[i].x, wv[i].y, wv[i].z, wv[i].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 x = normed ? Elem<T>::to_f2(w32[e]) : make_float2(1.f, 1.f);
-                    f[2 * e] = y[8 * i + 2 * e] * (k * x.x);
-                    f[2 * e + 1] = y[8 * i + 2 * e + 1] * (k * x.y);
-                }
-                st[lane * CH + (i ^ (lane % CH))] =
-                    make_uint4(Mma<T>::pack(f[0], f[1]), Mma<T>::pack(f[2], f[3]),
-                               Mma<T>::pack(f[4], f[5]), Mma<T>::pack(f[6], f[7]));
-            }
-            __syncwarp();
-            const long long mine =
-                row_valid ? ((long long)(qs + t0 + tok) * Hq + h * G + hg) * D + grp * HC : -1;
-            T *out = reinterpret_cast<T *>(p.out);
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int row = i * (32 / CH) + lane / CH, ch = lane % CH;
-                const long long at = __shfl_sync(FULL, mine, row);
-                if (at >= 0)
-                    *reinterpret_cast<uint4 *>(out + at + 8 * ch) =
-                        st[row * CH + (ch ^ (row % CH))];
             }
         }
     }
@@ -771,12 +913,59 @@ diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap
     }
     if constexpr (CL > 1)
         cluster_wait();                           // see leave()
+    if (CL == 1 && parts > 1) {
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        if (warp >= 4) {
+            const uint32_t aborts = smem_addr(const_cast<int *>(abort_flag));
+            const int rows = min(TPB, c - t0) * G;
+            const size_t token = (size_t)(qs + t0);
+            auto join = [&](auto se) {
+                join_split<T, D, decltype(se)::value>(p, sbase, aborts, part, lt, rows, G, h,
+                                                      token);
+            };
+            switch (parts) {
+            case 16: join(std::integral_constant<int, 16>{}); break;
+            case 8: join(std::integral_constant<int, 8>{}); break;
+            case 6: join(std::integral_constant<int, 6>{}); break;
+            case 4: join(std::integral_constant<int, 4>{}); break;
+            case 3: join(std::integral_constant<int, 3>{}); break;
+            default: join(std::integral_constant<int, 2>{}); break;
+            }
+        }
+        // no block ends while another reads its shared memory
+        __syncwarp();
+        cluster_arrive_relaxed();
+        cluster_wait();
+    }
+}
+
+// one block a query tile, or a cluster of kSplits blocks (by the launch)
+template <typename T, int D>
+__global__ void __launch_bounds__(DiffShape<D>::THREADS)
+diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap tmk,
+                      const __grid_constant__ CUtensorMap tmv)
+{
+    diff_prefill<T, D, 1>(p, tmk, tmv);
+}
+
+// two blocks on consecutive query tiles
+template <typename T, int D>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DiffShape<D>::THREADS)
+diff_prefill_pairs_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap tmk,
+                            const __grid_constant__ CUtensorMap tmv)
+{
+    diff_prefill<T, D, 2>(p, tmk, tmv);
 }
 
 template <typename T, int D, int CL>
 void entry(PrefillKernel *k)
 {
-    k->fn = reinterpret_cast<const void *>(&diff_prefill_kernel_t<T, D, CL>);
+    if constexpr (CL == 1)
+        k->fn = reinterpret_cast<const void *>(&diff_prefill_kernel_t<T, D>);
+    else
+        k->fn = reinterpret_cast<const void *>(&diff_prefill_pairs_kernel_t<T, D>);
     k->threads = DiffShape<D>::THREADS;
     k->smem = DiffShape<D>::SMEM;
 }

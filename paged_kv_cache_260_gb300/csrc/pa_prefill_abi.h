@@ -69,5 +69,8 @@ constexpr int kPrefillRows = 128;   // (token, head) rows of one prefill query t
 constexpr int kPrefillTiles = 2;    // query tiles of one prefill thread block (differential
                                     // attention: one, against two key maps)
 constexpr int kPrefillKeys = 128;   // keys per prefill key tile
+// differential attention: how many blocks of a cluster may share the keys of one
+// query tile
+constexpr int kSplits[] = {16, 8, 6, 4, 3, 2};
 
 }  // namespace pa

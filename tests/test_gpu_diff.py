@@ -463,3 +463,95 @@ def test_serving_flow(pa, dtype, hq, hkv, d):
     for _ in range(3):
         step([1, 4, 2, 3], [1, 1, 1, 1])
     step([3, 4], [33, 2])
+
+
+# A few query tiles against long caches: clusters of 2, 4 or 8 blocks share a tile's
+# keys where the table holds 4, 8 or 16 key tiles and the blocks stay below 129.
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("hq,hkv,d,dtype", [
+    (4, 1, 128, "bf16"), (1, 1, 64, "f16"), (3, 1, 64, "bf16"), (5, 1, 128, "f16"),
+    (14, 2, 128, "bf16"), (128, 1, 64, "f16"), (96, 1, 128, "bf16")])
+@pytest.mark.parametrize("lens,chunks", [
+    ([4100], [1]), ([2049, 4096, 130, 7], [1, 1, 1, 1]), ([3000, 257, 1], [9, 8, 1]),
+    ([2700, 0, 640], [23, 0, 31])])
+def test_prefill_shares_out_keys(pa, hq, hkv, d, dtype, norm, lens, chunks):
+    x = Pool(lens, hq, hkv, d, dtype, chunks=chunks, norm=norm, seed=hq + d)
+    x.check(x.prefill(pa))
+    first = x.out.clone()
+    x.prefill(pa, workspace=None)                            # neither order nor workspace matter
+    assert torch.equal(x.out, first)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 4, 128), (4, 4, 64)])
+@pytest.mark.parametrize("n", [5, 8, 11])                    # 4, 4 and 2 blocks a tile
+def test_prefill_shares_out_keys_of_several(pa, hq, hkv, d, n):
+    lens = [1100 + 97 * i for i in range(n)]
+    x = Pool(lens, hq, hkv, d, "bf16", chunks=[1 + 5 * i for i in range(n)], seed=n)
+    x.check(x.prefill(pa))
+
+
+@pytest.mark.parametrize("hq,hkv,d,dtype", [(2, 1, 128, "bf16"), (1, 1, 64, "f16")])
+@pytest.mark.parametrize("n", [127, 128, 129, 1025, 2300])
+def test_prefill_whole_prompt_shares_out_keys(pa, hq, hkv, d, dtype, n):
+    x = Pool([n], hq, hkv, d, dtype, chunks=[n], seed=n, maxb=160)
+    x.check(x.prefill(pa))
+
+
+@pytest.mark.parametrize("n", [1, 127, 128, 255, 256, 257, 384, 511, 512, 513, 900, 1023, 1024, 1025])
+def test_prefill_short_sequences_in_a_wide_table(pa, n):
+    """How many of a cluster's blocks share a sequence's keys follows its length."""
+    x = Pool([n, 2500, 33], 4, 1, 128, "f16", chunks=[min(n, 13), 2, 5], seed=n, maxb=400)
+    x.check(x.prefill(pa))
+
+
+def test_prefill_shared_out_large_scores(pa):
+    x = Pool([4000, 2100], 4, 1, 128, "bf16", chunks=[20, 3], seed=3)
+    x.scale = 4.0                                            # maxima grow from block to block
+    x.check(x.prefill(pa))
+
+
+def test_prefill_shared_out_reports(pa):
+    x = Pool([2100, 2500, 2300], 4, 1, 64, "bf16", chunks=[4, 30, 2], seed=4)
+    x.k.nan_to_num_(0.0)
+    x.v.nan_to_num_(0.0)
+    good = x.prefill(pa).clone()
+    r0, pos = x.rows(1)
+    keep = torch.ones(good.shape[0], dtype=torch.bool, device="cuda")
+    keep[r0:r0 + len(pos)] = False
+    x.tables[1, 100] = x.k.shape[0]
+    out = x.prefill(pa).clone()
+    assert pa.get_device_error() == pa.DEVERR["TABLE_RANGE"]
+    assert torch.equal(out[keep], good[keep])
+    x.tables.copy_(x.tables_h)
+    for value in (-1, 16 * x.tables.shape[1] + 1):
+        x.lens[1] = value
+        out = x.prefill(pa).clone()
+        assert pa.get_device_error() & pa.DEVERR["SEQLEN_RANGE"]
+        assert torch.equal(out[keep], good[keep])
+
+
+def test_prefill_shared_out_in_a_graph_and_on_two_streams(pa):
+    xs = [Pool([3900, 33, 1400], 8, 2, 128, "bf16", chunks=[9, 9, 9], seed=30 + i)
+          for i in range(2)]
+    want = [x.prefill(pa, workspace=None).clone() for x in xs]
+    torch.cuda.synchronize()
+    ss = [torch.cuda.Stream() for _ in xs]
+    for _ in range(10):                                      # at once
+        for x, s in zip(xs, ss):
+            x.prefill(pa, workspace=None, stream=s)
+    torch.cuda.synchronize()
+    for x, w in zip(xs, want):
+        assert torch.equal(x.out[:w.shape[0]], w)            # bit-stable too
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(3):
+            for x in xs:
+                x.prefill(pa, workspace=None)
+    for x in xs:
+        x.out.fill_(7.0)
+    g.replay()
+    g.replay()
+    torch.cuda.synchronize()
+    for x, w in zip(xs, want):
+        assert torch.equal(x.out[:w.shape[0]], w)
+        x.check(x.out[:w.shape[0]])

@@ -77,6 +77,7 @@ struct KernelSet {
     const void *prep;        // large batches: build the per-sequence arrays in the workspace,
     const void *prep_fix;    //   block by block, then add the earlier blocks' unit counts
     const void *merge_cut;   // combines the pieces of cut units
+    const void *merge_wide;  // the same with a block per run and head (or null)
     const void *merge_part;  // fixed mode: merges partitions into the output
 };
 
@@ -100,6 +101,8 @@ constexpr int kMinTiles = 2;          // split modes: least tiles per worker (wa
 // many blocks wide and the runs number at most kWholeRunsPerSM per SM.
 constexpr int kWholeMaxBlocks = 8;
 constexpr int kWholeRunsPerSM = 4;
+constexpr int kWideWarps = 16;        // of a block of merge_wide
+constexpr int kWidePieces = 22;       // merge_wide from this many workers a run and wave on
 constexpr int kMaxGroup = 16;         // query heads per kv head: two 8-column tiles
 
 bool decode_kernels_f16(int head_dim, KernelSet *ks);       // groups 1..8

@@ -555,3 +555,43 @@ def test_prefill_shared_out_in_a_graph_and_on_two_streams(pa):
     for x, w in zip(xs, want):
         assert torch.equal(x.out[:w.shape[0]], w)
         x.check(x.out[:w.shape[0]])
+
+
+# Few runs, each cut into many pieces: merged by a block per run and head
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("hq,hkv,d,dtype", [
+    (4, 1, 128, "bf16"), (1, 1, 64, "f16"), (7, 1, 128, "f16"), (16, 1, 64, "bf16"),
+    (32, 2, 128, "bf16"), (10, 2, 64, "f16"), (8, 8, 64, "bf16")])
+@pytest.mark.parametrize("lens", [[6000], [700], [130], [0, 2500, 17], [2049, 1, 300, 16]])
+def test_decode_few_runs_of_many_pieces(pa, hq, hkv, d, dtype, norm, lens):
+    x = Pool(lens, hq, hkv, d, dtype, norm=norm, seed=hq + d + len(lens), maxb=400)
+    x.check(x.decode(pa))
+    first = x.out.clone()
+    x.decode(pa)
+    assert torch.equal(x.out, first)
+
+
+def test_decode_few_runs_large_scores(pa):
+    x = Pool([5000], 4, 1, 128, "bf16", seed=3)
+    x.scale = 4.0                                            # maxima differ from piece to piece
+    x.check(x.decode(pa))
+
+
+def test_decode_few_runs_in_a_graph_with_changing_lengths(pa):
+    x = Pool([3000, 2000], 4, 1, 64, "f16", seed=5)
+    x.decode(pa)
+    g = torch.cuda.CUDAGraph()
+    ws = pa.diff_decode_workspace_for(x.q, x.k, x.tables)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        x.decode(pa, workspace=ws)
+        x.decode(pa, workspace=ws)
+    for lens in ([3000, 2000], [5, 2000], [0, 33], [2999, 0], [1, 1]):
+        x.lens_h = lens
+        x.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        x.k.nan_to_num_(0.5)
+        x.v.nan_to_num_(0.5)
+        x.out.fill_(7.0)
+        g.replay()
+        x.check(x.out[:2])
+    assert pa.get_device_error() == 0

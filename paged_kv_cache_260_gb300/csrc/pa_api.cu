@@ -667,10 +667,13 @@ static int decode_impl(void *out, const void *q, const void *k_cache, const void
     // wave costs about what the other merge takes for 22 pieces (bf16, D 128 and
     // 64, us a decode, other against wide: 32 runs x 4 heads, 33 and 57 pieces
     // 29.0 / 23.5, 32.7 / 18.4; 64 x 1, 17 and 29 pieces 37.7 / 37.1, 28.4 / 24.0;
-    // 64 x 4, two waves 38.4 / 43.0, 29.7 / 29.9; 32 x 16, four, 50.8 / 54.9)
+    // 64 x 4, two waves 38.4 / 43.0, 29.7 / 29.9; 32 x 16, four, 50.8 / 54.9;
+    // no run has more pieces than its table holds (9 runs x 4 of 378 tokens 9.7 / 12,
+    // of 700 13.1 / 12.4, of 2500 25.4 / 12.9)
     const long long runs = (long long)num_seqs * num_kv_heads;
     const long long waves = (runs * group + ds->num_sms - 1) / ds->num_sms;
-    if (ks.merge_wide && kWidePieces * waves * runs <= workers)
+    if (ks.merge_wide && kWidePieces * waves * runs <= workers &&
+        kWidePieces * waves * kMinTiles <= max_blocks_per_seq)
         return launch_dependent(ks.merge_wide, dim3((unsigned)runs, group), dim3(32 * kWideWarps),
                                 0, st, margs);
     rc = launch_dependent(ks.merge_cut, dim3(workers), dim3(32 * group), 0, st, margs);

@@ -43,7 +43,7 @@
 //    them, and joins its results through distributed shared memory (join_split;
 //    128 KB of O, one row in so many to a block; no workspace and no second
 //    launch).  16 tokens at 16K, bf16, head_dim 128: 1 x 4/1 heads 208 us on one
-//    block, 24 on 16; 2 x 32/8 heads 210, on clusters of 6 46.  As many blocks as
+//    block, 23 on 16; 2 x 32/8 heads 210, on clusters of 6 46.  As many blocks as
 //    let all clusters run at once: with clusters of 8, of which 15 fit, the
 //    latter's 16 tiles took 71 us.
 //  * P through shared memory, which lets the next S go ahead, costs more shared
@@ -187,28 +187,33 @@ __device__ __forceinline__ void join_split(const PrefillParams &p, uint32_t sbas
     const int row = lt / TPR * SE + rank, tr = lt % TPR;
     const bool live = row < rows && tr < D / 4;
     float y[NC][4], ss = 0.f;
-    bool fine = true;
+    int aborted = 0;
 #pragma unroll
     for (int k = 0; k < NC; ++k)
         y[k][0] = y[k][1] = y[k][2] = y[k][3] = 0.f;
     if (live) {
-        float f[2][SE];
+        // all of a step's loads before the first use: one latency, not one a block
+        float f[2][SE], l[2][SE];
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            float l[SE], top = -INFINITY, sum = 0.f;
-            const uint32_t at = sbase + Sh::OFF_X + (g * Sh::BM + row) * 4;
+        for (int c = 0; c < SE; ++c) {
+            aborted |= __float_as_int(cluster_load(cluster_addr(abort_addr, c)));
 #pragma unroll
-            for (int c = 0; c < SE; ++c) {
-                l[c] = cluster_load(cluster_addr(at, c));
+            for (int g = 0; g < 2; ++g) {
+                const uint32_t at = sbase + Sh::OFF_X + (g * Sh::BM + row) * 4;
+                l[g][c] = cluster_load(cluster_addr(at, c));
                 f[g][c] = cluster_load(cluster_addr(at + 2 * Sh::BM * 4, c));
             }
+        }
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            float top = -INFINITY, sum = 0.f;
 #pragma unroll
             for (int c = 0; c < SE; ++c)
                 top = fmaxf(top, f[g][c]);
 #pragma unroll
             for (int c = 0; c < SE; ++c) {
                 f[g][c] = ex2_approx(f[g][c] - top);
-                sum = fmaf(l[c], f[g][c], sum);
+                sum = fmaf(l[g][c], f[g][c], sum);
             }
             const float of = (g ? -__ldg(p.lambda + h * G + row % G) : 1.f) / sum;
 #pragma unroll
@@ -217,7 +222,6 @@ __device__ __forceinline__ void join_split(const PrefillParams &p, uint32_t sbas
         }
 #pragma unroll
         for (int c = 0; c < SE; ++c) {
-            fine = fine && __float_as_int(cluster_load(cluster_addr(abort_addr, c))) == 0;
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
                 const uint32_t at =
@@ -245,7 +249,7 @@ __device__ __forceinline__ void join_split(const PrefillParams &p, uint32_t sbas
             ss += __shfl_xor_sync(0xffffffffu, ss, off);
         k0 *= rsqrtf(ss * (1.f / D) + p.norm_eps);
     }
-    if (!live || !fine)
+    if (!live || aborted)
         return;
     T *out = static_cast<T *>(p.out) +
              ((token + row / G) * p.num_heads + h * G + row % G) * D;

@@ -1042,11 +1042,11 @@ static int prefill_impl(void *out, const void *q, const void *k_cache, const voi
         !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(query_start, 4))
         return PA_ERR_INVALID_ARG;
     const long long pool_rows = (long long)num_blocks * num_kv_heads * kBlockSize;
-    // differential: a unit is two blocks' query tiles, unless every chunk fits one
-    const bool pairs = diff && max_query_len > kPrefillRows / group;
-    const int tiles = diff && !pairs ? 1 : kPrefillTiles;
+    // differential: a unit is two query tiles of a block each, unless every chunk
+    // fits one
+    int tiles = diff && max_query_len <= kPrefillRows / group ? 1 : kPrefillTiles;
     long long q_ranks = prefill_q_ranks(max_query_len, num_heads, num_kv_heads, tiles);
-    long long grid = q_ranks * num_seqs * num_kv_heads * (pairs ? 2 : 1);
+    long long grid = q_ranks * num_seqs * num_kv_heads * (diff ? tiles : 1);
     if ((long long)max_blocks_per_seq * kBlockSize >= (1LL << 30) || pool_rows >= (1LL << 31) ||
         grid >= (1LL << 31))
         return PA_ERR_UNSUPPORTED;
@@ -1060,7 +1060,7 @@ static int prefill_impl(void *out, const void *q, const void *k_cache, const voi
             return PA_ERR_WORKSPACE;
     }
     PrefillKernel kk{};
-    if (!(diff ? diff_prefill_kernel(dtype, head_dim, pairs, &kk)
+    if (!(diff ? diff_prefill_kernel(dtype, head_dim, &kk)
                : prefill_kernel(dtype, head_dim, &kk)))
         return PA_ERR_UNSUPPORTED;
     DeviceState *ds;
@@ -1075,6 +1075,9 @@ static int prefill_impl(void *out, const void *q, const void *k_cache, const voi
         return rc;
     if (kk.smem > limit)
         return PA_ERR_UNSUPPORTED;
+    rc = ensure_smem(kk.fn, dev, kk.smem);
+    if (rc != PA_OK)
+        return rc;
     // Differential, and query tiles for half the SMs at most: a cluster of blocks
     // shares the keys of each, two key tiles or more a block, as many blocks as
     // leave all clusters running at once (one tile against 16K keys: 209 us on
@@ -1084,25 +1087,16 @@ static int prefill_impl(void *out, const void *q, const void *k_cache, const voi
     const long long units = one * num_seqs * num_kv_heads;
     const int key_tiles = (max_blocks_per_seq * kBlockSize + kPrefillKeys - 1) / kPrefillKeys;
     if (diff && key_tiles >= 4 && 2 * units <= ds->num_sms) {
-        PrefillKernel ks{};
-        if (!diff_prefill_kernel(dtype, head_dim, false, &ks))
-            return PA_ERR_UNSUPPORTED;
-        rc = ensure_smem(ks.fn, dev, ks.smem);
-        if (rc != PA_OK)
-            return rc;
         for (int n : kSplits)
             if (split == 1 && 2 * n <= key_tiles &&
-                units <= active_clusters(ks.fn, dev, ks.threads, ks.smem, n))
+                units <= active_clusters(kk.fn, dev, kk.threads, kk.smem, n))
                 split = n;
         if (split > 1) {
-            kk = ks;
+            tiles = 1;
             q_ranks = one;
             grid = units * split;
         }
     }
-    rc = ensure_smem(kk.fn, dev, kk.smem);
-    if (rc != PA_OK)
-        return rc;
     CUtensorMap tmk, tmv;
     rc = make_pool_map(&tmk, k_cache, dtype, head_dim, pool_rows);
     if (rc == PA_OK)
@@ -1124,6 +1118,7 @@ static int prefill_impl(void *out, const void *q, const void *k_cache, const voi
     p.q_ranks = (int)q_ranks;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.wave = ds->num_sms;
+    p.unit_tiles = tiles;
     p.lambda = x.lambda;
     p.norm_w = x.norm_w;
     p.norm_eps = x.norm_eps;

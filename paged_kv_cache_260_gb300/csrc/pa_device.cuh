@@ -288,18 +288,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void *tmap, int 
         : "memory");
 }
 
-// The same copy, written at this offset into the shared memory of every CTA of
-// the cluster whose bit is set in `mask`, completing on each one's own `bar`.
-__device__ __forceinline__ void tma_load_2d_multicast(uint32_t dst, const void *tmap, int x, int y,
-                                                      uint32_t bar, uint16_t mask)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".multicast::cluster [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-        "l"(tmap), "r"(x), "r"(y), "r"(bar), "h"(mask)
-        : "memory");
-}
-
 __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;

@@ -15,29 +15,27 @@
 // lanes, where the difference is taken.
 //
 // What bounds it, measured on two 2048-token chunks at 16K (32/8 heads x 128,
-// bf16; 1.55 TFLOP):
+// bf16; 1.55 TFLOP): 1400 us, 1.10 PFLOP/s.
 //  * A block of 128 rows reads K and V twice as often as the plain prefill's 256
-//    rows do: 64 KB a tile, 5.7 TB/s out of L2 over all SMs, and every version
-//    that read them so ended at 1420 to 1510 us.  So two blocks of a cluster take
-//    consecutive query tiles and copy every other K/V box each, into both
-//    (multicast): 1276 us.
-//  * Then each map's chain S -> softmax -> P.V -> next S: P lies over score
+//    rows do: 64 KB a tile, 5.7 TB/s out of L2 over all SMs, the most that any
+//    form of this kernel has drawn.  With half of each V tile left out of the
+//    copies an earlier form went from 1419 to 1237 us.  The 512 TMEM columns hold
+//    two score tiles and two O of 128 columns each, so a block has room for no
+//    more rows.  The copies are plain ones, into the block's own shared memory:
+//    replicas on several GPUs load this library, and a multicast load must not
+//    run there.
+//  * Behind that, each map's chain S -> softmax -> P.V -> next S: P lies over score
 //    columns, and TMEM has no others.  P.V starts on the first 64 keys while the
 //    softmax is at the others; each map has an issuing warp of its own (one for
 //    both was busy for 2,300 cycles a tile: every wait on a barrier costs it 100 to
-//    250, completed or not); and map 1 starts half a tile behind map 0: 1197 us,
-//    2,600 cycles a tile.  P needs only the second half of the score columns, so the
-//    next tile's first 64 keys are scored into the first half while the softmax
-//    is at its exponentials (M 128, N 64 reads Q from shared memory twice as often
-//    and takes 1.5 times as long): 1146 us, and 1130 with waits that a warp leaves
-//    together; 2,450 cycles, of which the tensor core works for 1,792 and the 256
-//    exponentials of a sub-core take 1,050.
-//  * Short contexts: a block's start and end.  8 x 512 tokens over 0.5K to 4K are
-//    6.7 blocks an SM of about 16 tiles each, and 15,600 of a block's 56,000 cycles
-//    passed before its first softmax, after its last P and between blocks.  The
-//    barriers first, K_0 and the query rows in flight over the block's last
-//    barrier, no releasing cluster arrivals, the norm's weights and lambda loaded
-//    ahead, output rows stored by whole lines: 11,200 cycles, 211 -> 197 us.
+//    250, completed or not); map 1 starts half a tile behind map 0; and as P needs
+//    only the second half of the score columns, the next tile's first 64 keys are
+//    scored into the first half while the softmax is at its exponentials.
+//  * Short contexts (8 x 512 tokens over 0.5K to 4K, 227 us): also a block's start
+//    and end, 11,000 cycles of which its first softmax and its last P are the
+//    bounds.  The barriers come first, K_0 and the query rows are in flight over
+//    the block's last barrier, the norm's weights and lambda are loaded ahead, and
+//    output rows are stored by whole lines.
 //  * Few query tiles (short chunks against long caches): the SMs without one. A
 //    cluster of up to 16 blocks shares the keys of one tile, each block a run of
 //    them, and joins its results through distributed shared memory (join_split;
@@ -47,10 +45,8 @@
 //    let all clusters run at once: with clusters of 8, of which 15 fit, the
 //    latter's 16 tiles took 71 us.
 //  * P through shared memory, which lets the next S go ahead, costs more shared
-//    memory bandwidth than there is (1437 us before the multicast); 80-key tiles
-//    with P in columns of its own 1702; two threads a row 1382 against 1197; turns
-//    at the exponentials 1174, and those of the first 64 keys before the others'
-//    scores are there 1294, against 1146.
+//    memory bandwidth than there is; 80-key tiles with P in columns of its own and
+//    two threads a row were slower as well.
 //
 // Warp roles (384 threads):
 //   warp 0     TMA producer: K tiles and V tiles through a ring each, K one tile
@@ -268,15 +264,16 @@ __device__ __forceinline__ void join_split(const PrefillParams &p, uint32_t sbas
     }
 }
 
-template <typename T, int D, int CL>
-__device__ __forceinline__ void diff_prefill(const PrefillParams &p, const CUtensorMap &tmk,
-                                             const CUtensorMap &tmv)
+// one block a query tile, or a cluster of kSplits blocks (by the launch)
+template <typename T, int D>
+__global__ void __launch_bounds__(DiffShape<D>::THREADS)
+diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap tmk,
+                      const __grid_constant__ CUtensorMap tmv)
 {
     using Sh = DiffShape<D>;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr uint32_t FULL = 0xffffffffu;
     constexpr int NS = Sh::NSLOT;
-    constexpr uint16_t kAll = (1u << CL) - 1;     // every block of the cluster
 
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw_addr = smem_addr(smem_raw);
@@ -305,20 +302,20 @@ __device__ __forceinline__ void diff_prefill(const PrefillParams &p, const CUten
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int Hkv = p.num_kv_heads, Hq = p.num_heads, G = Hq / Hkv;
     const int TPB = Sh::BM / G;                   // chunk tokens per block
-    // the cluster's work: CL query tiles, or one whose keys its blocks share out
-    const int split = CL > 1 ? 1 : (int)cluster_size(), part = CL > 1 ? 0 : (int)cluster_rank();
-    const int unit = blockIdx.x / (CL > 1 ? CL : split);
-    const int cr = CL > 1 ? (int)cluster_rank() : 0;
+    // a cluster's blocks share out the keys of one query tile
+    const int split = (int)cluster_size(), part = (int)cluster_rank();
+    // the blocks of a unit take its query tiles, the last and longest first
+    const int U = p.unit_tiles;
+    const int unit = blockIdx.x / (split * U);
+    const int ut = U - 1 - blockIdx.x / split % U;
     int h = unit % Hkv;
 
-    // the barriers first: while their initialisation reaches the other block of
-    // the cluster, this one finds out what to do
     if (warp == 0) {
         for (int i = lane; i < Sh::NBAR; i += 32) {
             const int k = i - 4 * NS;             // past the slots' barriers
             int count = 1;                        // a commit, or the producer
             if (k < 0)
-                count = (i / NS) & 1 ? 2 * CL : 1;   // empty: both maps' issuers, of every block
+                count = (i / NS) & 1 ? 2 : 1;     // empty: both maps' issuers
             else if ((k >= 2 && k < 4) || (k >= 6 && k < 10) || k == 14)
                 count = 4;                        // read, p, start: one lane of each of 4 warps
             else if (k == 12 || k == 13)
@@ -329,12 +326,6 @@ __device__ __forceinline__ void diff_prefill(const PrefillParams &p, const CUten
         mbar_init_fence();
     }
     __syncwarp();
-    if constexpr (CL > 1)
-        cluster_arrive_relaxed();
-    auto no_work = [&]() {                        // the same for the whole cluster
-        if constexpr (CL > 1)
-            cluster_wait();
-    };
 
     // ---- the block's rows and key range (uniform over the block) ----------
     // no global memory is read before the preceding kernel (the plan) is done
@@ -342,7 +333,7 @@ __device__ __forceinline__ void diff_prefill(const PrefillParams &p, const CUten
     int s, rank = 0, tile = 0;
     if (p.plan) {
         if (!plan_block(p, unit, s, tile, h))
-            return no_work();
+            return;
     } else {
         const int per_rank = p.num_seqs * Hkv;
         rank = unit / per_rank;
@@ -352,27 +343,29 @@ __device__ __forceinline__ void diff_prefill(const PrefillParams &p, const CUten
     const int qs = __ldg(p.query_start + s);
     const int c = __ldg(p.query_start + s + 1) - qs;
     // the plan reports itself
-    const bool reporter = !p.plan && rank == 0 && h == 0 && tid == 0 && cr == 0 && part == 0;
+    const bool reporter = !p.plan && rank == 0 && h == 0 && tid == 0 && ut == 0 && part == 0;
     if (L < 0 || L > p.max_blocks * kBlockSize) {
         if (reporter)
             record_error(p.err, PA_DEVERR_SEQLEN_RANGE);
-        return no_work();
+        return;
     }
     if (c < 0 || c > L) {
         if (reporter)
             record_error(p.err, PA_DEVERR_QUERY_RANGE);
-        return no_work();
+        return;
     }
     if (!p.plan) {
-        const int nq = (c + CL * TPB - 1) / (CL * TPB);
+        const int nq = (c + U * TPB - 1) / (U * TPB);
         if (nq > p.q_ranks && reporter)
             record_error(p.err, PA_DEVERR_QUERY_RANGE);   // max_query_len too small
         if (rank >= nq)
-            return no_work();
-        tile = nq - 1 - rank;                     // rank 0 = the last (longest) tile
+            return;
+        tile = nq - 1 - rank;                     // rank 0 = the last (longest) unit
     }
-    const int t0 = (tile * CL + cr) * TPB;        // may lie past the chunk (no rows of its own)
-    const int p_last = L - c + min((tile + 1) * CL * TPB, c) - 1;   // the cluster's last row
+    const int t0 = (tile * U + ut) * TPB;
+    if (t0 >= c)
+        return;                                   // a unit's last tile may have no rows
+    const int p_last = L - c + min(t0 + TPB, c) - 1;   // the tile's last row
     const int nt_all = p_last / Sh::BN + 1;       // key tiles, the same for the whole cluster
     // 2, 3, 4, 6, 8 or 16 of the cluster's blocks share them, two tiles or more each
     const int most = min(split, nt_all / 2);
@@ -403,8 +396,7 @@ __device__ __forceinline__ void diff_prefill(const PrefillParams &p, const CUten
     if (warp == 0) {
         entry0 = Window::fetch(table, nblk, 0);
         entry1 = Window::fetch(table, nblk, Window::WT);
-        // K_0 at once, each block its own copy: the other one's barriers may not
-        // be there yet
+        // K_0 at once
         Window w(p, table, h, nblk, entry0, entry1);
         const int row = w.row(0);
         if (lane == 0)
@@ -431,19 +423,9 @@ __device__ __forceinline__ void diff_prefill(const PrefillParams &p, const CUten
     }
     tc::fence_before_sync();
     __syncthreads();
-    if constexpr (CL > 1)
-        cluster_wait();                           // the other block's barriers are there too
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
 
-    // Every warp, once: it will not touch the other block of the cluster again
-    // (whose shared memory the producer copies into, whose barriers the issuers
-    // arrive on).  A block ends after both blocks' warps have all said so.
-    auto leave = [&]() {
-        __syncwarp();
-        if constexpr (CL > 1)
-            cluster_arrive_relaxed();
-    };
     auto give_up = [&]() {
         *abort_flag = 1;
         record_error(p.err, PA_DEVERR_TIMEOUT);
@@ -467,14 +449,9 @@ __device__ __forceinline__ void diff_prefill(const PrefillParams &p, const CUten
                 mbar_arrive_expect_tx(full, (uint32_t)(nv * Sh::HALVES * Sh::BOX));
             __syncwarp();
             const int b = lane % Sh::NB, hf = lane / Sh::NB;
-            // the blocks of a cluster copy every CL-th box each, into all of them
-            const uint32_t dst = slots + (j % NS) * Sh::SLOT_BYTES + (hf * Sh::NB + b) * Sh::BOX;
-            if (hf < Sh::HALVES && row >= 0 && b % CL == cr) {
-                if constexpr (CL > 1)
-                    tma_load_2d_multicast(dst, &tm, 64 * hf, row, full, kAll);
-                else
-                    tma_load_2d(dst, &tm, 64 * hf, row, full);
-            }
+            if (hf < Sh::HALVES && row >= 0)
+                tma_load_2d(slots + (j % NS) * Sh::SLOT_BYTES + (hf * Sh::NB + b) * Sh::BOX, &tm,
+                            64 * hf, row, full);
             return true;
         };
         int nk = 1, nv = 0;                       // tiles issued: K_0 has been
@@ -501,7 +478,6 @@ __device__ __forceinline__ void diff_prefill(const PrefillParams &p, const CUten
                 if (j % NS == lane && !mbar_wait_bounded(vfull(lane), (j / NS) & 1))
                     give_up();
         }
-        leave();
     } else if (warp <= 2) {
         // ---------------- MMA issuer of map g (the whole warp, one elected lane issues) ----
         const int g = warp - 1;
@@ -518,16 +494,10 @@ __device__ __forceinline__ void diff_prefill(const PrefillParams &p, const CUten
         // landed, so it comes before the wait for the softmax or the last P.V
         auto k_ready = [&](int j) { return mbar_wait_warp(kfull(j % NS), (j / NS) & 1); };
         auto v_ready = [&](int j) { return mbar_wait_warp(vfull(j % NS), (j / NS) & 1); };
-        // A slot is free once both maps of every block of the cluster have read
-        // tile j.  Only said of slots that a later tile takes: then the other
-        // block's producer waits for every arrival on its barriers, and none is
-        // under way to a block that has ended.
+        // a slot is free once both maps have read tile j; said of slots that a later
+        // tile takes
         auto release = [&](uint32_t bar, int j) {
-            if (j + NS >= nt)
-                return;
-            if constexpr (CL > 1)
-                tc::commit_warp_multicast(bar, kAll);
-            else
+            if (j + NS < nt)
                 tc::commit_warp(bar);
         };
         // S of tile j: all of it, or (P over S) half hf of its keys
@@ -599,15 +569,14 @@ __device__ __forceinline__ void diff_prefill(const PrefillParams &p, const CUten
         tc::commit_warp(drain_bar(g));
         if (!mbar_wait_warp(drain_bar(g), 0) && lane == 0)
             give_up();
-        leave();
     } else if (warp == 3) {
-        leave();
         // while the block works: warm L2 with the query rows of the block one
         // wave later (its pair and kv head from the work order)
         int s2, tile2, h2;
-        if (p.plan && plan_block(p, unit + p.wave / CL, s2, tile2, h2)) {
+        const int b2 = blockIdx.x + p.wave;
+        if (p.plan && plan_block(p, b2 / U, s2, tile2, h2)) {
             const int qs2 = __ldg(p.query_start + s2);
-            const int t02 = (tile2 * CL + cr) * TPB;
+            const int t02 = (tile2 * U + U - 1 - b2 % U) * TPB;
             const int ntok = min(TPB, __ldg(p.query_start + s2 + 1) - qs2 - t02);
             const int lines = G * D * 2 / 128;      // 128-byte lines of a token's G heads
             const T *qg = reinterpret_cast<const T *>(p.q);
@@ -849,7 +818,6 @@ __device__ __forceinline__ void diff_prefill(const PrefillParams &p, const CUten
             tc::fence_before_sync();
             softmax_warps_sync();
             tc::fence_after_sync();
-            leave();
             ok = !__any_sync(FULL, *abort_flag != 0);
             const float i0 = 1.f / xl[rr];
             const float i1 = -lam / xl[Sh::BM + rr];
@@ -915,9 +883,7 @@ __device__ __forceinline__ void diff_prefill(const PrefillParams &p, const CUten
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, Sh::TMEM_COLS);
     }
-    if constexpr (CL > 1)
-        cluster_wait();                           // see leave()
-    if (CL == 1 && parts > 1) {
+    if (parts > 1) {
         __syncwarp();
         cluster_arrive();
         cluster_wait();
@@ -945,53 +911,26 @@ __device__ __forceinline__ void diff_prefill(const PrefillParams &p, const CUten
     }
 }
 
-// one block a query tile, or a cluster of kSplits blocks (by the launch)
 template <typename T, int D>
-__global__ void __launch_bounds__(DiffShape<D>::THREADS)
-diff_prefill_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap tmk,
-                      const __grid_constant__ CUtensorMap tmv)
-{
-    diff_prefill<T, D, 1>(p, tmk, tmv);
-}
-
-// two blocks on consecutive query tiles
-template <typename T, int D>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DiffShape<D>::THREADS)
-diff_prefill_pairs_kernel_t(const PrefillParams p, const __grid_constant__ CUtensorMap tmk,
-                            const __grid_constant__ CUtensorMap tmv)
-{
-    diff_prefill<T, D, 2>(p, tmk, tmv);
-}
-
-template <typename T, int D, int CL>
 void entry(PrefillKernel *k)
 {
-    if constexpr (CL == 1)
-        k->fn = reinterpret_cast<const void *>(&diff_prefill_kernel_t<T, D>);
-    else
-        k->fn = reinterpret_cast<const void *>(&diff_prefill_pairs_kernel_t<T, D>);
+    k->fn = reinterpret_cast<const void *>(&diff_prefill_kernel_t<T, D>);
     k->threads = DiffShape<D>::THREADS;
     k->smem = DiffShape<D>::SMEM;
 }
 
-template <int CL>
-void pick(int dtype, int head_dim, PrefillKernel *k)
-{
-    const bool bf = dtype == PA_DTYPE_BF16;
-    if (head_dim == 64)
-        bf ? entry<__nv_bfloat16, 64, CL>(k) : entry<__half, 64, CL>(k);
-    else
-        bf ? entry<__nv_bfloat16, 128, CL>(k) : entry<__half, 128, CL>(k);
-}
-
 }  // namespace
 
-bool diff_prefill_kernel(int dtype, int head_dim, bool pairs, PrefillKernel *k)
+bool diff_prefill_kernel(int dtype, int head_dim, PrefillKernel *k)
 {
     // the work order is the plain prefill's
     if (!prefill_kernel(dtype, head_dim, k))
         return false;
-    pairs ? pick<2>(dtype, head_dim, k) : pick<1>(dtype, head_dim, k);
+    const bool bf = dtype == PA_DTYPE_BF16;
+    if (head_dim == 64)
+        bf ? entry<__nv_bfloat16, 64>(k) : entry<__half, 64>(k);
+    else
+        bf ? entry<__nv_bfloat16, 128>(k) : entry<__half, 128>(k);
     return true;
 }
 

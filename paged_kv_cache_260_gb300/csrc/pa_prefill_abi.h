@@ -44,9 +44,11 @@ struct PrefillParams {
     // L2 with the query rows of block b + wave, which starts about when a
     // block of this wave ends
     int wave;
-    // differential attention only: each head's factor of the second map
+    // differential attention only: the query tiles of a unit of work (of a pair
+    // above, of q_ranks), a block each; each head's factor of the second map
     // [num_heads], the output norm's weights [head_dim] or null, its epsilon
     // and the factor of the output
+    int unit_tiles;
     const float *lambda;
     const void *norm_w;
     float norm_eps, out_scale;
@@ -63,8 +65,7 @@ struct PrefillKernel {
 };
 
 bool prefill_kernel(int dtype, int head_dim, PrefillKernel *k);
-// pairs: two blocks on consecutive query tiles share their K/V copies
-bool diff_prefill_kernel(int dtype, int head_dim, bool pairs, PrefillKernel *k);
+bool diff_prefill_kernel(int dtype, int head_dim, PrefillKernel *k);
 constexpr int kPrefillRows = 128;   // (token, head) rows of one prefill query tile
 constexpr int kPrefillTiles = 2;    // query tiles of one prefill thread block (differential
                                     // attention: one, against two key maps)

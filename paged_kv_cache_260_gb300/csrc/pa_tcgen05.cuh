@@ -90,19 +90,6 @@ __device__ __forceinline__ void commit_warp(uint32_t bar)
         : "memory");
 }
 
-// The same, arriving on the barrier at this offset in every CTA of the
-// cluster whose bit is set in `mask`.
-__device__ __forceinline__ void commit_warp_multicast(uint32_t bar, uint16_t mask)
-{
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster"
-        ".multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
-        "h"(mask)
-        : "memory");
-}
-
 // Warp-wide: allocate `ncols` TMEM columns (a power of two >= 32); the base
 // address is written to shared memory at `dst`.
 __device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t ncols)

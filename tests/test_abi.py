@@ -149,3 +149,10 @@ def test_prefill_workspace_size(lib):
     assert lib.pa_prefill_workspace_size(100, 1000, 32, 8) == 7424      # 16 + 6400 + 800
     assert lib.pa_prefill_workspace_size(0, 512, 32, 8) == 0
     assert lib.pa_prefill_workspace_size(8, 512, 30, 8) == 0            # not a multiple
+
+
+def test_no_multicast_copies():
+    # the library is loaded by replicas on several GPUs, whatever pool they pass
+    csrc = os.path.join(ROOT, "paged_kv_cache_260_gb300", "csrc")
+    for name in sorted(os.listdir(csrc)):
+        assert "multicast::cluster" not in open(os.path.join(csrc, name)).read(), name

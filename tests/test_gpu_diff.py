@@ -595,3 +595,79 @@ def test_decode_few_runs_in_a_graph_with_changing_lengths(pa):
         g.replay()
         x.check(x.out[:2])
     assert pa.get_device_error() == 0
+
+
+# Grids of more blocks than SMs, which alone follow the work order
+def ordered(pa, x, longest=None, by_seq=False, pairs=None):
+    """A prefill of x that has to make a work order: the grid is large enough, and the
+    order's head says how many (sequence, unit) pairs it holds and of which kind it is."""
+    longest = max(x.chunks) if longest is None else longest
+    n, (hq, hkv) = len(x.chunks), (x.q_h.shape[1], x.k_h.shape[1])
+    tokens = 128 // (hq // hkv)                              # of a query tile
+    tiles = 1 if longest <= tokens else 2                    # of a unit
+    units = -(-longest // (tiles * tokens))
+    props = torch.cuda.get_device_properties(0)
+    assert units * tiles * n * hkv > props.multi_processor_count
+    assert 2 * -(-longest // tokens) * n * hkv > props.multi_processor_count
+    kv = sum(L for L, c in zip(x.lens_h, x.chunks) if c) * hkv * x.k_h.shape[3] * 4
+    assert (kv > props.L2_cache_size) == by_seq
+    ws = torch.full((pa.diff_prefill_workspace_size(n, longest, hq, hkv),), 0x5a,
+                    dtype=torch.uint8, device="cuda")
+    x.prefill(pa, longest=longest, workspace=ws)
+    want = sum(min(units, -(-c // (tiles * tokens))) for c in x.chunks)
+    assert ws[:8].view(torch.int32).tolist() == [want, int(by_seq)]
+    return x.out[:x.start_h[-1]].clone()
+
+
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("hq,hkv,d,dtype", [
+    (10, 2, 128, "bf16"), (21, 3, 64, "f16"), (24, 8, 64, "bf16"), (8, 8, 128, "f16")])
+def test_prefill_ordered(pa, hq, hkv, d, dtype, norm):
+    lens = [1, 300, 140, 129, 0, 517, 40, 700]
+    x = Pool(lens, hq, hkv, d, dtype, chunks=[1, 300, 3, 129, 0, 517, 0, 333], norm=norm, seed=hq)
+    got = ordered(pa, x)
+    x.check(got)
+    assert torch.equal(x.prefill(pa, workspace=None), got)   # the order changes no result
+    assert pa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d,dtype", [(16, 4, 64, "f16"), (20, 4, 128, "bf16")])
+def test_prefill_ordered_units_of_one_tile(pa, hq, hkv, d, dtype):
+    rng = np.random.default_rng(9)
+    chunks = [0, 25, 1] + rng.integers(0, 26, 45).tolist()
+    lens = [c + int(rng.integers(0, 400)) for c in chunks]
+    x = Pool(lens, hq, hkv, d, dtype, chunks=chunks, seed=40)
+    got = ordered(pa, x)
+    x.check(got)
+    assert torch.equal(x.prefill(pa, workspace=None), got)
+    assert pa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d,dtype,chunks", [
+    (16, 8, 128, "bf16", [400, 130, 257]), (24, 8, 128, "f16", [260, 0, 85]),
+    (32, 16, 64, "f16", [130, 70, 90])])
+def test_prefill_ordered_by_sequence(pa, hq, hkv, d, dtype, chunks):
+    # K/V past L2
+    x = Pool([13500, 12001, 24500], hq, hkv, d, dtype, chunks=chunks, seed=15)
+    got = ordered(pa, x, by_seq=True)
+    x.check(got)
+    assert torch.equal(x.prefill(pa, workspace=None), got)
+    assert pa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d,dtype,longest,kept", [
+    (16, 8, 128, "f16", 130, 128),                           # 3 units of 128 tokens, 2 in the grid
+    (24, 8, 64, "bf16", 168, 168),                           # 4 units of 84, 2 in the grid
+    (56, 8, 64, "f16", 18, 288)])                            # 17 units of 18, 1 in the grid
+def test_prefill_ordered_longest_chunk_understated(pa, hq, hkv, d, dtype, longest, kept):
+    chunks = [15, 300, 0, 1, 18] + [10] * 16
+    x = Pool([90, 400, 0, 17, 18] + [33] * 16, hq, hkv, d, dtype, chunks=chunks, seed=8)
+    good = ordered(pa, x)
+    x.check(good)
+    x.out.fill_(7.0)
+    out = ordered(pa, x, longest=longest)
+    assert pa.get_device_error() == pa.DEVERR["QUERY_RANGE"]
+    skipped = slice(15, 15 + kept)
+    assert bool((out[skipped] == 7).all())
+    good[skipped] = 7
+    assert torch.equal(out, good)

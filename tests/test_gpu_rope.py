@@ -339,3 +339,17 @@ def test_append_then_decode(pa, dtype):
                             np.array(lens, np.int32), scale, dtype)
         assert np.abs(out.double().cpu().numpy() - ref).max() <= TOL[dtype]
         assert pa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("t,hq,hkv,maps,rot,norm,fused", [(9001, 10, 2, 1, 96, "k", False),
+                                                          (8003, 24, 8, 2, 48, "qk", True)])
+def test_append_through_the_rings_128_channels_f16(pa, t, hq, hkv, maps, rot, norm, fused, inter):
+    # rows go through the rings above three units of (at most four) rounds a resident warp
+    d = 128
+    rounds = -(-(hq + 2 * hkv) * maps // (512 * maps // d))
+    assert t * -(-rounds // 4) > 3 * 16 * torch.cuda.get_device_properties(0).multi_processor_count
+    x = Tokens(t, hq, hkv, d, "f16", maps, rot, norm, fused, seed=t)
+    x.slots[5], x.pos[t - 2] = -1, -3
+    x.check(pa, lambda: x.append(pa, inter), inter, skipped=[5, t - 2])
+    assert pa.get_device_error() == 0

@@ -465,8 +465,9 @@ def test_serving_flow(pa, dtype, hq, hkv, d):
     step([3, 4], [33, 2])
 
 
-# A few query tiles against long caches: clusters of 2, 4 or 8 blocks share a tile's
-# keys where the table holds 4, 8 or 16 key tiles and the blocks stay below 129.
+# A few query tiles, for half of the SMs at most, against long caches: clusters of 2, 3,
+# 4, 6, 8 or 16 blocks share a tile's keys where the table holds two key tiles a block and
+# all clusters run at once.
 @pytest.mark.parametrize("norm", [False, True])
 @pytest.mark.parametrize("hq,hkv,d,dtype", [
     (4, 1, 128, "bf16"), (1, 1, 64, "f16"), (3, 1, 64, "bf16"), (5, 1, 128, "f16"),
@@ -483,7 +484,7 @@ def test_prefill_shares_out_keys(pa, hq, hkv, d, dtype, norm, lens, chunks):
 
 
 @pytest.mark.parametrize("hq,hkv,d", [(8, 4, 128), (4, 4, 64)])
-@pytest.mark.parametrize("n", [5, 8, 11])                    # 4, 4 and 2 blocks a tile
+@pytest.mark.parametrize("n", [5, 8, 11])                    # up to 6 blocks a tile
 def test_prefill_shares_out_keys_of_several(pa, hq, hkv, d, n):
     lens = [1100 + 97 * i for i in range(n)]
     x = Pool(lens, hq, hkv, d, "bf16", chunks=[1 + 5 * i for i in range(n)], seed=n)
@@ -671,3 +672,13 @@ def test_prefill_ordered_longest_chunk_understated(pa, hq, hkv, d, dtype, longes
     assert bool((out[skipped] == 7).all())
     good[skipped] = 7
     assert torch.equal(out, good)
+
+
+@pytest.mark.parametrize("n", [640, 768, 769, 895, 896, 1535, 1536, 1537, 2047, 2048, 2049])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 1, 128), (3, 1, 64)])
+def test_prefill_shares_of_part_of_a_cluster(pa, n, hq, hkv, d):
+    """A wide table gives a tile a cluster of 16 blocks; a sequence of 5 key tiles uses 2
+    of them, of 6 and 7 three, of 12 to 15 six, of 16 and more eight."""
+    x = Pool([n, 3000, 1], hq, hkv, d, "bf16", chunks=[7, 2, 1], seed=n, maxb=400)
+    x.check(x.prefill(pa))
+    assert pa.get_device_error() == 0

@@ -1292,8 +1292,9 @@ inline void fill_diff_kernel_set(KernelSet *ks)
     // 82 to 85), two tiles 8 (216; 7 224, 9 231, 6 255), four tiles 8 (254; with
     // P in two terms 290, 7 warps 320, 6 365), where the MMAs and not HBM set the
     // time; D=64 12 (205), 12 (211; 11 239, 13 222) and 8 (304; with two terms
-    // 333, 7 373, 9 402).  P's second term costs a microsecond of the batch (80.2
-    // without).
+    // 333, 7 373, 9 402).  Four tiles at D=128 take all 255 registers and spill 200
+    // bytes; the others spill nothing.  P's second term costs a microsecond of the
+    // batch (80.2 without).
     constexpr int S = 2;
     constexpr int W = D == 128 ? (NT == 1 ? 7 : 8) : (NT == 4 ? 8 : 12);
     ks->decode = reinterpret_cast<const void *>(&decode_mma_kernel<T, D, NT, W, S, false, true>);

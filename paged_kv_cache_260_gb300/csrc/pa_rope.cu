@@ -586,8 +586,8 @@ RopeKernel rope_kernel(const RopeParams &p, bool bf16, int head_dim, bool interl
     long long units = cut(kFewRounds);
     // Few units go one to a warp, rows into registers; from three a warp on,
     // through the rings.  Measured (32/8 heads x 128, bf16, pool write, in a
-    // graph): 1536 tokens 10.3 us against 12.5 through the rings, 2048 13.4
-    // against 14.7, 2560 16.3 against 15.4, 4096 22.4 against 20.7.
+    // graph): 1536 tokens 9.8 us against 11.9 through the rings, 2048 13.1
+    // against 13.5, 2560 16.0 against 14.7, 4096 21.8 against 19.9.
     const bool many = units > 3 * resident;
     if (many)
         units = cut(kManyRounds);
@@ -601,11 +601,10 @@ RopeKernel rope_kernel(const RopeParams &p, bool bf16, int head_dim, bool interl
     // One wave of blocks takes an even share each, then blocks of one unit a
     // warp the remainder.  With many units a warp the SMs drift apart (13 % of
     // their time idle at 40 units of four rounds), so a tenth is left to blocks of
-    // two units a warp, which the hardware hands out as SMs come free.  Before
-    // the queries had a loop of their own: with the pool write 32768 tokens (27
-    // units a warp) 126.3 us against 134.0, 16384 66.5 against 69.5, 8192 (6.7
-    // units) 38.2 against 36.0; without it 127.4 against 136.0, 67.4 against 69.9,
-    // and 6000 tokens 31.4 against 28.9.
+    // two units a warp, which the hardware hands out as SMs come free.  With the
+    // pool write 32768 tokens (27 units a warp) 127.4 us against 136.7, 16384
+    // 66.0 against 71.0, 8192 (6.7 units) 36.1 against 34.6; without it 107.0
+    // against 115.6, 55.0 against 58.2, and 6000 tokens (4.9) 24.3 against 23.1.
     const long long each = units / resident;
     const bool spare = each >= 12;
     const long long tail = W * (spare ? 2 : 1);

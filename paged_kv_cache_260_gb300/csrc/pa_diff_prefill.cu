@@ -17,7 +17,7 @@
 // What bounds it, measured on two 2048-token chunks at 16K (32/8 heads x 128,
 // bf16; 1.55 TFLOP): 1400 us, 1.10 PFLOP/s.
 //  * A block of 128 rows reads K and V twice as often as the plain prefill's 256
-//    rows do: 64 KB a tile, 5.7 TB/s out of L2 over all SMs, the most that any
+//    rows do: 64 KB a tile, 5.8 TB/s out of L2 over all SMs, the most that any
 //    form of this kernel has drawn.  With half of each V tile left out of the
 //    copies an earlier form went from 1419 to 1237 us.  The 512 TMEM columns hold
 //    two score tiles and two O of 128 columns each, so a block has room for no
@@ -32,8 +32,8 @@
 //    only the second half of the score columns, the next tile's first 64 keys are
 //    scored into the first half while the softmax is at its exponentials.
 //  * Short contexts (8 x 512 tokens over 0.5K to 4K, 227 us): also a block's start
-//    and end, 11,000 cycles of which its first softmax and its last P are the
-//    bounds.  The barriers come first, K_0 and the query rows are in flight over
+//    and end, about 11,000 cycles before its first softmax, after its last P and
+//    between blocks.  The barriers come first, K_0 and the query rows in flight over
 //    the block's last barrier, the norm's weights and lambda are loaded ahead, and
 //    output rows are stored by whole lines.
 //  * Few query tiles (short chunks against long caches): the SMs without one. A

@@ -682,3 +682,65 @@ def test_prefill_shares_of_part_of_a_cluster(pa, n, hq, hkv, d):
     x = Pool([n, 3000, 1], hq, hkv, d, "bf16", chunks=[7, 2, 1], seed=n, maxb=400)
     x.check(x.prefill(pa))
     assert pa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d,dtype", [(8, 2, 64, "f16"), (8, 1, 128, "bf16"),
+                                            (22, 2, 128, "f16"), (16, 1, 64, "bf16")])
+def test_decode_shared_blocks(pa, hq, hkv, d, dtype):
+    """Samples of one prompt: neighbours' tables name the same blocks, one names a block
+    twice."""
+    x = Pool([700, 700, 690, 33, 40, 1500], hq, hkv, d, dtype, seed=hq, maxb=100)
+    for s, n in ((1, 43), (2, 43), (4, 2)):
+        x.tables_h[s, :n] = x.tables_h[s - 1, :n]
+    x.tables_h[5, 3] = x.tables_h[5, 4]
+    x.tables.copy_(x.tables_h)
+    x.check(x.decode(pa))
+    assert pa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("kind,chunks", [("decode", None), ("prefill", [3, 40, 1]),
+                                         ("prefill", [3, 400, 1])])
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (12, 2, 64), (24, 2, 128)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_bad_queries_stay_apart(pa, kind, chunks, hq, hkv, d, bad):
+    x = Pool([700, 1400, 33], hq, hkv, d, "bf16", chunks=chunks, seed=7)
+    run = x.decode if kind == "decode" else x.prefill
+    good = run(pa).clone()
+    row = x.rows(1)[0]
+    x.q[row, 1, 3] = bad                                     # one head's first map
+    x.q[row, hq - 1, d - 1] = bad                            # another's second
+    out = run(pa)
+    assert not bool(torch.isfinite(out[row, [1, hq - 1]]).any())
+    keep = torch.ones(good.shape[:2], dtype=torch.bool, device="cuda")
+    keep[row, 1] = keep[row, hq - 1] = False
+    assert torch.equal(out[keep], good[keep])
+
+
+def test_prefill_ordered_on_two_streams_and_in_two_graphs(pa):
+    xs = [Pool([700, 300, 128, 513, 64], 16, 8, 128, "bf16", chunks=[700, 299, 128, 1, 64],
+               seed=50 + i) for i in range(2)]
+    want = [ordered(pa, x) for x in xs]
+    for x, w in zip(xs, want):
+        x.check(w, only=[1, 3])
+    ss = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for x, s in zip(xs, ss):
+            x.prefill(pa, stream=s)
+    torch.cuda.synchronize()
+    for x, w in zip(xs, want):
+        assert torch.equal(x.out[:w.shape[0]], w)
+        x.out.fill_(7.0)
+    graphs = []
+    for x in xs:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            x.prefill(pa)
+    for _ in range(10):
+        for g, s in zip(graphs, ss):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for x, w in zip(xs, want):
+        assert torch.equal(x.out[:w.shape[0]], w)
+    assert pa.get_device_error() == 0

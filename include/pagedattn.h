@@ -62,7 +62,8 @@ enum pa_dtype { PA_DTYPE_F16 = 0, PA_DTYPE_BF16 = 1 };
 #define PA_DEVERR_SEQLEN_RANGE 0x8u  /* seq_len < 0 or > max_blocks_per_seq*block_size */
 #define PA_DEVERR_TIMEOUT      0x10u /* a bounded wait on a copy expired */
 #define PA_DEVERR_APPEND_SLOT  0x20u /* decode_append: slot is not the last position's */
-#define PA_DEVERR_QUERY_RANGE  0x40u /* prefill: chunk < 0, > seq_len or > max_query_len */
+#define PA_DEVERR_QUERY_RANGE  0x40u /* prefill: chunk < 0, > seq_len or > max_query_len;
+                                      * block_bounds: start outside [0, seq_len] */
 #define PA_DEVERR_POSITION_RANGE 0x80u /* rotation: position >= max_position */
 
 /* PAGEDATTN_VERSION of the loaded library. */
@@ -485,6 +486,148 @@ int pa_rope_and_cache_args(const struct pa_rope_args *args);
 int pa_qk_norm_rope_args(const struct pa_rope_args *args);
 int pa_diff_decode_args(const struct pa_diff_args *args);
 int pa_diff_prefill_args(const struct pa_diff_args *args);
+
+/*
+ * Long contexts: reading only the blocks that matter to a query, and keeping only
+ * the tokens that matter.  The pages describe neither; both work on the pool and the
+ * tables of the calls above.  All six take one struct, whose `size` is its own
+ * (anything else is PA_ERR_INVALID_ARG) and which is read during the call alone;
+ * each call looks at the fields that its comment names, besides num_seqs,
+ * num_kv_heads, head_dim, block_size, num_blocks, dtype and stream.  Doubles are
+ * rounded to float.  Pointers and sizes are checked as in pa_decode; workspaces are
+ * those of pa_decode (256-byte aligned, caller-owned, no initialisation, calls
+ * that share one ordered on one stream).  Kernels are programmatic dependent
+ * launches.  A length outside [0, max_blocks_per_seq * 16] sets
+ * PA_DEVERR_SEQLEN_RANGE and a table entry outside the pool
+ * PA_DEVERR_TABLE_RANGE, with what each call then does.
+ */
+struct pa_sparse_args {
+    uint64_t size;
+    void *out;
+    float *mass;
+    const void *q;
+    void *k_cache, *v_cache, *bounds;
+    const int32_t *block_tables, *seq_lens, *query_start, *starts, *new_lens;
+    int32_t *tiles, *tile_lens;
+    void *workspace, *stream;
+    uint64_t workspace_bytes;
+    double scale, decay;
+    int32_t num_seqs, num_queries, max_query_len, num_heads, num_kv_heads, head_dim, block_size,
+        max_blocks_per_seq, num_blocks, keep, keep_first, keep_last, dtype, reserved;
+};
+
+/*
+ * The bounds of blocks' keys: for every block b that holds positions starts[s] ..
+ * seq_lens[s] - 1 of a sequence, every kv head h and channel c,
+ *     bounds[b][h][0][c] = min_t k[b][h][t][c],  bounds[b][h][1][c] = max_t k[b][h][t][c]
+ * over the block's live tokens (all of them, also those before starts[s]).  Exact;
+ * a NaN among the keys makes the channel's bounds NaN.  After a decode step starts is
+ * seq_lens - 1, after a prompt chunk the chunk's first position; NULL is 0.
+ *
+ *   bounds [num_blocks][num_kv_heads][2][head_dim] dtype, written; k_cache,
+ *   block_tables, seq_lens, starts [num_seqs] int32 or NULL, max_blocks_per_seq
+ * A start outside [0, seq_len] sets PA_DEVERR_QUERY_RANGE and counts as the
+ * nearer end.  Lengths are clamped, bad table entries skipped.  A block that two
+ * sequences hold to different lengths gets the bounds of one of them.
+ */
+int pa_block_bounds(const struct pa_sparse_args *args);
+
+/*
+ * The blocks a query token should read.  A block's score for kv head h is the
+ * largest q.k that its bounds allow to any of the group's heads,
+ *     score_j = max_g sum_c max(q_gc * min_jc, q_gc * max_jc),
+ * so a block that holds a large score ranks before those that cannot.  Of a
+ * sequence's n = ceil(seq_len / 16) blocks each head keeps `keep`: the keep_first
+ * first, the keep_last last, and of the rest those with the largest scores, ties to
+ * the lowest position; all of them if n <= keep.  The choice is that of exact sums
+ * (blocks whose 32-bit scores are too close to tell apart are summed again with
+ * 46 bits).  Blocks whose score is not finite (an infinity or NaN among the bounds
+ * or queries) rank first.
+ *
+ *   tiles     [num_seqs][num_kv_heads][keep] int32, written: the kept blocks in the
+ *             order of their positions, as pool tiles block * num_kv_heads + h;
+ *             -1 past the last
+ *   tile_lens [num_seqs][num_kv_heads] int32, written: tokens those hold
+ *   q         [num_seqs][num_heads][head_dim]; groups of 1..16
+ *   bounds    as pa_block_bounds leaves them; block_tables, seq_lens,
+ *             max_blocks_per_seq
+ *   keep > 0, keep_first >= 0, keep_last >= 1 (the last block may be partly
+ *             filled), keep_first + keep_last <= keep
+ * Lengths are clamped; a bad table entry counts as block 0.
+ */
+size_t pa_select_blocks_workspace_size(int num_seqs, int num_kv_heads, int max_blocks_per_seq);
+int pa_select_blocks(const struct pa_sparse_args *args);
+
+/*
+ * pa_decode (partition_size 0) over the listed tiles alone, each kv head its own:
+ * query head h of sequence s attends to tokens 0 .. tile_lens[s][h / G] - 1 of the
+ * tiles tiles[s][h / G][..], 16 tokens a tile.  Lists need not come from
+ * pa_select_blocks: any tile may be named, and one named twice counts twice.
+ *   out, q, k_cache, v_cache, tiles, tile_lens, keep, scale; out may not be q
+ * 0 <= tile_lens <= keep * 16 (else PA_DEVERR_SEQLEN_RANGE, clamped); entries past
+ * ceil(tile_lens / 16) are not read, others outside
+ * [0, num_blocks * num_kv_heads) set PA_DEVERR_TABLE_RANGE and read tile 0.
+ */
+size_t pa_sparse_decode_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
+                                       int head_dim, int keep);
+int pa_sparse_decode(const struct pa_sparse_args *args);
+
+/*
+ * pa_decode (partition_size 0) that also keeps account of the softmax weights:
+ *     mass[s][h][t] = decay * mass[s][h][t] + sum_g softmax_t(scale * q_g . k_t)
+ * over the heads g of kv head h, for t < seq_lens[s].  The newest token, t =
+ * seq_lens[s] - 1, has no weight from before: its old entry is not read, nor is
+ * any with decay 0.  Entries past the length are left as they were.  fp32
+ * throughout, no atomics.  Keys of live tokens must be finite.
+ *   out, q, k_cache, v_cache, block_tables, seq_lens, max_blocks_per_seq, scale,
+ *   mass [num_seqs][num_kv_heads][max_blocks_per_seq * 16] fp32, decay (finite);
+ *   out may not be q.  The workspace holds the scores: 4 bytes for each query head
+ *   and position of the tables.
+ * Errors as pa_decode.
+ */
+size_t pa_decode_mass_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                     int max_blocks_per_seq);
+int pa_decode_mass(const struct pa_sparse_args *args);
+
+/*
+ * The weights that a prompt chunk's queries give, without their outputs:
+ *     mass[s][h][t] = decay * mass[s][h][t] + sum_{i, g} softmax_t(scale * q_ig . k_t)
+ * over the chunk's rows i and the heads g of kv head h, causal as in pa_prefill (a
+ * row at position p sees t <= p).  The chunk's own tokens have no weight from before.
+ * Chunk after chunk it accumulates a prompt's weights; on a prompt's last rows alone
+ * (q and query_start of those, decay 0) it says which tokens the end of the prompt
+ * looks at.  Sequences without rows are left as they were.
+ *   mass, q [num_queries][num_heads][head_dim], k_cache, block_tables, seq_lens,
+ *   query_start [num_seqs + 1] int32, max_query_len, max_blocks_per_seq, scale > 0,
+ *   decay; groups of 1..128
+ * A chunk that is negative, longer than its sequence or than max_query_len (beyond the
+ * last row block, of 2 * (128 / group) rows), or whose rows lie outside q sets
+ * PA_DEVERR_QUERY_RANGE; that, or a bad length, leaves the sequence as it was.
+ * Bad table entries read block 0.
+ */
+size_t pa_prefill_mass_workspace_size(int num_seqs, int max_query_len, int num_heads,
+                                      int num_kv_heads, int max_blocks_per_seq);
+int pa_prefill_mass(const struct pa_sparse_args *args);
+
+/*
+ * Eviction: each sequence longer than new_lens[s] = B is cut to B tokens in place.
+ * Each kv head for itself keeps the keep_last last tokens (at most B), the
+ * keep_first first ones (at most what is left) and of the rest those with the largest
+ * mass, ties to the lowest slot, a NaN before all.  The last ones keep their
+ * order at slots B - keep_last .. B - 1; the others keep their slots, but for those
+ * that lie past the last ones' new place: they move, in ascending order, to the slots
+ * before it that dropped tokens leave, in ascending order.  (Attention of a later
+ * token does not depend on the order of the keys before it; what was rotated into
+ * a key stays with it.)  mass moves along.  Slots from B on are left as they were, as
+ * are sequences of at most B tokens.  The caller shortens seq_lens to B, and may give
+ * back the blocks past it; pa_block_bounds of the sequence are out of date.
+ *   k_cache, v_cache, mass (written), block_tables, seq_lens, new_lens [num_seqs]
+ *   int32, max_blocks_per_seq, keep_first >= 0, keep_last >= 0
+ * The sequence's blocks must be its own (copy-on-write first).  A negative new_len, a
+ * bad length or table entry leaves the sequence as it was.
+ */
+size_t pa_evict_workspace_size(int num_seqs, int num_kv_heads, int max_blocks_per_seq);
+int pa_evict(const struct pa_sparse_args *args);
 
 /*
  * Copy-on-write of shared blocks: for every pair i,

@@ -1,6 +1,6 @@
 """GB300 (sm_103a) paged KV cache: decode attention, chunked prefill, both
-also as differential attention, reshape_and_cache, rope_and_cache,
-copy_blocks, swap_blocks.
+also as differential attention, decode over selected blocks, eviction by
+attention weight, reshape_and_cache, rope_and_cache, copy_blocks, swap_blocks.
 
 A thin ctypes binding over ``libpagedattn.so`` (the C ABI in
 ``include/pagedattn.h``).  Functions take torch CUDA tensors, pass their data
@@ -24,6 +24,11 @@ __all__ = [
     "decode_shared_prefix_workspace_size", "diff_decode", "diff_decode_workspace_size",
     "diff_decode_workspace_for", "prefill", "prefill_workspace_size", "diff_prefill",
     "diff_prefill_workspace_size", "diff_prefill_workspace_for",
+    "block_bounds", "select_blocks", "select_blocks_workspace_size",
+    "select_blocks_workspace_for", "sparse_decode", "sparse_decode_workspace_size",
+    "sparse_decode_workspace_for", "decode_mass", "decode_mass_workspace_size",
+    "decode_mass_workspace_for", "prefill_mass", "prefill_mass_workspace_size",
+    "prefill_mass_workspace_for", "evict", "evict_workspace_size", "evict_workspace_for",
     "reshape_and_cache", "rope_and_cache", "qk_norm_rope", "copy_blocks", "swap_blocks",
     "gather_kv", "validate_tables", "selftest_bounded_wait", "get_device_error",
     "PA_DTYPE_F16", "PA_DTYPE_BF16", "DEVERR", "STATUS",
@@ -42,6 +47,7 @@ DEVERR = {"SLOT_RANGE": 0x1, "BLOCK_RANGE": 0x2, "TABLE_RANGE": 0x4, "SEQLEN_RAN
 # less than ctypes' conversion of 27
 _ROPE_ARGS = struct.Struct("Q13P5qd11i0Q")
 _DIFF_ARGS = struct.Struct("Q11PQ3d9i0Q")
+_SPARSE_ARGS = struct.Struct("Q15PQ2d14i0Q")         # struct pa_sparse_args
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpagedattn.so")
@@ -103,6 +109,14 @@ def load(path: str = LIB_PATH):
                      "pa_diff_prefill_args"):
             fn = getattr(L, name)
             fn.restype, fn.argtypes = i, [C.c_char_p]
+        for name in ("pa_block_bounds", "pa_select_blocks", "pa_sparse_decode", "pa_decode_mass",
+                     "pa_prefill_mass", "pa_evict"):
+            fn = getattr(L, name)
+            fn.restype, fn.argtypes = i, [C.c_char_p]
+        for name, count in (("pa_select_blocks", 3), ("pa_sparse_decode", 5),
+                            ("pa_decode_mass", 5), ("pa_prefill_mass", 5), ("pa_evict", 3)):
+            fn = getattr(L, name + "_workspace_size")
+            fn.restype, fn.argtypes = sz, [i] * count
         L.pa_copy_blocks.restype = i
         L.pa_copy_blocks.argtypes = [vp, vp, vp, i, i, i, i, i, i, vp]
         L.pa_swap_blocks.restype = i
@@ -619,6 +633,242 @@ def qk_norm_rope(q_out, k_out, q, k, positions, cos_sin, q_norm=None, k_norm=Non
     if rc:
         raise PagedAttnError("pa_qk_norm_rope", rc)
     return q_out, k_out
+
+
+def _sparse_call(fn, dev, names, stream, *, out=0, mass=0, q=0, k=0, v=0, bounds=0, tables=0,
+                 lens=0, start=0, starts=0, new_lens=0, tiles=0, tile_lens=0, workspace=None,
+                 scale=1.0, decay=1.0, n=0, rows=0, longest=0, hq=0, hkv=0, d=0, bs=BLOCK_SIZE,
+                 mb=0, nb=0, keep=0, first=0, last=0, code=0):
+    """One call with struct pa_sparse_args; tensors' addresses as ints, 0 for NULL."""
+    wptr, wbytes = ((0, 0) if workspace is None else
+                    (workspace.data_ptr(), _bytes_of(workspace, dev)))
+    rc = getattr(load(), fn)(_SPARSE_ARGS.pack(
+        _SPARSE_ARGS.size, out, mass, q, k, v, bounds, tables, lens, start, starts, new_lens,
+        tiles, tile_lens, wptr, names.raw_stream(dev) if stream is None else stream.cuda_stream,
+        wbytes, scale, decay, n, rows, longest, hq, hkv, d, bs, mb, nb, keep, first, last, code,
+        0))
+    if rc:
+        raise PagedAttnError(fn, rc)
+
+
+def _tables(block_tables, seq_lens, names, dev):
+    """Sequences, table width and the addresses of tables and lengths."""
+    n, mb = block_tables.shape
+    if seq_lens.shape != (n,):
+        raise ValueError("table shapes")
+    return n, mb, _near(block_tables, names.i32, dev), _near(seq_lens, names.i32, dev)
+
+
+def _mass_rows(mass, n, hkv, mb, names, dev):
+    """The address of mass [n, hkv, mb * 16]."""
+    if mass.shape != (n, hkv, mb * BLOCK_SIZE):
+        raise ValueError(f"mass: [{n}, {hkv}, {mb * BLOCK_SIZE}]")
+    return _near(mass, names.f32, dev)
+
+
+def block_bounds(bounds, k_cache, block_tables, seq_lens, starts=None, stream=None):
+    """pa_block_bounds: bounds[b, h, 0] and [b, h, 1] become the least and greatest key of
+    each channel over block b's live tokens, for the blocks that hold positions
+    starts[s] .. seq_lens[s] - 1 (all of a sequence's without starts).
+
+    bounds [num_blocks, num_kv_heads, 2, head_dim] in the pool's type; starts int32
+    [num_seqs]: seq_lens - 1 after a decode step, a chunk's first position after it.
+    """
+    names = _hot()
+    nb, hkv, bs, d = k_cache.shape
+    dt, dev = k_cache.dtype, _current(k_cache, names)
+    n, mb, tables, lens = _tables(block_tables, seq_lens, names, dev)
+    if bounds.shape != (nb, hkv, 2, d) or (starts is not None and starts.shape != (n,)):
+        raise ValueError("shapes")
+    _sparse_call("pa_block_bounds", dev, names, stream, k=_near(k_cache, dt, dev),
+                 bounds=_near(bounds, dt, dev), tables=tables, lens=lens,
+                 starts=0 if starts is None else _near(starts, names.i32, dev), n=n, hkv=hkv, d=d,
+                 bs=bs, mb=mb, nb=nb, code=_code(dt, names))
+    return bounds
+
+
+def select_blocks_workspace_size(num_seqs, num_kv_heads, max_blocks_per_seq) -> int:
+    return int(load().pa_select_blocks_workspace_size(num_seqs, num_kv_heads, max_blocks_per_seq))
+
+
+def select_blocks_workspace_for(q, bounds, block_tables, stream=None):
+    """A workspace tensor sized for pa_select_blocks on these shapes."""
+    nbytes = select_blocks_workspace_size(q.shape[0], bounds.shape[1], block_tables.shape[1])
+    return _scratch(nbytes, q.device, stream) if nbytes else None
+
+
+def select_blocks(tiles, tile_lens, q, bounds, block_tables, seq_lens, keep_first=0, keep_last=1,
+                  workspace=None, stream=None):
+    """pa_select_blocks: the tiles.shape[2] blocks that each (sequence, kv head) should read
+    for the new token's queries q [num_seqs, num_heads, head_dim]: the first keep_first, the
+    last keep_last and those whose bounds allow the largest scores.
+
+    tiles int32 [num_seqs, num_kv_heads, keep] becomes pool tiles
+    block * num_kv_heads + head in the order of the positions, -1 past the last;
+    tile_lens int32 [num_seqs, num_kv_heads] the tokens they hold.
+    """
+    names = _hot()
+    n, hq, d = q.shape
+    nb, hkv, two, d2 = bounds.shape
+    dt, dev = q.dtype, _current(q, names)
+    n2, mb, tables, lens = _tables(block_tables, seq_lens, names, dev)
+    if (n2 != n or two != 2 or d2 != d or tiles.shape[:2] != (n, hkv) or tiles.dim() != 3 or
+            tile_lens.shape != (n, hkv)):
+        raise ValueError("shapes")
+    if workspace is None:
+        workspace = select_blocks_workspace_for(q, bounds, block_tables, stream)
+    _sparse_call("pa_select_blocks", dev, names, stream, q=_near(q, dt, dev),
+                 bounds=_near(bounds, dt, dev), tables=tables, lens=lens,
+                 tiles=_near(tiles, names.i32, dev), tile_lens=_near(tile_lens, names.i32, dev),
+                 workspace=workspace, n=n, hq=hq, hkv=hkv, d=d, mb=mb, nb=nb, keep=tiles.shape[2],
+                 first=int(keep_first), last=int(keep_last), code=_code(dt, names))
+    return tiles, tile_lens
+
+
+def sparse_decode_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, keep) -> int:
+    return int(load().pa_sparse_decode_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim,
+                                                      keep))
+
+
+def sparse_decode_workspace_for(q, k_cache, tiles, stream=None):
+    """A workspace tensor sized for pa_sparse_decode on these shapes."""
+    n, hq, d = q.shape
+    nbytes = sparse_decode_workspace_size(n, hq, k_cache.shape[1], d, tiles.shape[2])
+    return _scratch(nbytes, q.device, stream) if nbytes else None
+
+
+def _qkv(out, q, k_cache, v_cache, names):
+    """Checks of a decode's tensors; the device and the addresses of out, q, k and v."""
+    dt, dev, pool = q.dtype, _current(q, names), k_cache.shape
+    if out.shape != q.shape or v_cache.shape != pool or pool[3] != q.shape[2]:
+        raise ValueError("shapes")
+    return dev, [_near(x, dt, dev) for x in (out, q, k_cache, v_cache)]
+
+
+def sparse_decode(out, q, k_cache, v_cache, tiles, tile_lens, scale, workspace=None, stream=None):
+    """pa_sparse_decode: decode over the first tile_lens[s, h] tokens of the pool tiles
+    tiles[s, h] alone (as select_blocks leaves them), each kv head its own."""
+    names = _hot()
+    n, hq, d = q.shape
+    nb, hkv, bs, _ = k_cache.shape
+    dev, (o, qq, k, v) = _qkv(out, q, k_cache, v_cache, names)
+    if tiles.dim() != 3 or tiles.shape[:2] != (n, hkv) or tile_lens.shape != (n, hkv):
+        raise ValueError("shapes")
+    if workspace is None:
+        workspace = sparse_decode_workspace_for(q, k_cache, tiles, stream)
+    _sparse_call("pa_sparse_decode", dev, names, stream, out=o, q=qq, k=k, v=v,
+                 tiles=_near(tiles, names.i32, dev), tile_lens=_near(tile_lens, names.i32, dev),
+                 workspace=workspace, scale=scale, n=n, hq=hq, hkv=hkv, d=d, bs=bs, nb=nb,
+                 keep=tiles.shape[2], code=_code(q.dtype, names))
+    return out
+
+
+def decode_mass_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim,
+                               max_blocks_per_seq) -> int:
+    return int(load().pa_decode_mass_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim,
+                                                    max_blocks_per_seq))
+
+
+def decode_mass_workspace_for(q, k_cache, block_tables, stream=None):
+    """A workspace tensor sized for pa_decode_mass on these shapes."""
+    n, hq, d = q.shape
+    nbytes = decode_mass_workspace_size(n, hq, k_cache.shape[1], d, block_tables.shape[1])
+    return _scratch(nbytes, q.device, stream) if nbytes else None
+
+
+def decode_mass(out, mass, q, k_cache, v_cache, block_tables, seq_lens, scale, decay=1.0,
+                workspace=None, stream=None):
+    """pa_decode_mass: decode that also keeps account of the weights,
+        mass[s, h, t] = decay * mass[s, h, t] + sum of softmax_t over kv head h's queries,
+    for t < seq_lens[s]; the newest token starts without any.
+
+    mass float32 [num_seqs, num_kv_heads, 16 * block_tables.shape[1]], rows in the order of
+    the tables'.
+    """
+    names = _hot()
+    n, hq, d = q.shape
+    nb, hkv, bs, _ = k_cache.shape
+    dev, (o, qq, k, v) = _qkv(out, q, k_cache, v_cache, names)
+    n2, mb, tables, lens = _tables(block_tables, seq_lens, names, dev)
+    if n2 != n:
+        raise ValueError("table shapes")
+    m = _mass_rows(mass, n, hkv, mb, names, dev)
+    if workspace is None:
+        workspace = decode_mass_workspace_for(q, k_cache, block_tables, stream)
+    _sparse_call("pa_decode_mass", dev, names, stream, out=o, mass=m, q=qq, k=k, v=v,
+                 tables=tables, lens=lens, workspace=workspace, scale=scale, decay=decay, n=n,
+                 hq=hq, hkv=hkv, d=d, bs=bs, mb=mb, nb=nb, code=_code(q.dtype, names))
+    return out, mass
+
+
+def prefill_mass_workspace_size(num_seqs, max_query_len, num_heads, num_kv_heads,
+                                max_blocks_per_seq) -> int:
+    return int(load().pa_prefill_mass_workspace_size(num_seqs, max_query_len, num_heads,
+                                                     num_kv_heads, max_blocks_per_seq))
+
+
+def prefill_mass_workspace_for(q, k_cache, block_tables, max_query_len, stream=None):
+    """A workspace tensor sized for pa_prefill_mass on these shapes."""
+    n, mb = block_tables.shape
+    nbytes = prefill_mass_workspace_size(n, int(max_query_len), q.shape[1], k_cache.shape[1], mb)
+    return _scratch(nbytes, q.device, stream) if nbytes else None
+
+
+def prefill_mass(mass, q, k_cache, block_tables, seq_lens, query_start, max_query_len, scale,
+                 decay=1.0, workspace=None, stream=None):
+    """pa_prefill_mass: the weights that each sequence's newest chunk of queries gives the
+    tokens it sees, added to mass as decode_mass does; the chunk's own tokens start without
+    any.  Rows, tables, query_start and max_query_len as prefill; on a prompt's last rows
+    alone, with decay=0, it says what the end of the prompt looks at."""
+    names = _hot()
+    t, hq, d = q.shape
+    nb, hkv, bs, d2 = k_cache.shape
+    dt, dev = q.dtype, _current(q, names)
+    n, mb, tables, lens = _tables(block_tables, seq_lens, names, dev)
+    if d2 != d or query_start.shape != (n + 1,):
+        raise ValueError("shapes")
+    m = _mass_rows(mass, n, hkv, mb, names, dev)
+    if workspace is None:
+        workspace = prefill_mass_workspace_for(q, k_cache, block_tables, max_query_len, stream)
+    _sparse_call("pa_prefill_mass", dev, names, stream, mass=m, q=_near(q, dt, dev),
+                 k=_near(k_cache, dt, dev), tables=tables, lens=lens,
+                 start=_near(query_start, names.i32, dev), workspace=workspace, scale=scale,
+                 decay=decay, n=n, rows=t, longest=int(max_query_len), hq=hq, hkv=hkv, d=d, bs=bs,
+                 mb=mb, nb=nb, code=_code(dt, names))
+    return mass
+
+
+def evict_workspace_size(num_seqs, num_kv_heads, max_blocks_per_seq) -> int:
+    return int(load().pa_evict_workspace_size(num_seqs, num_kv_heads, max_blocks_per_seq))
+
+
+def evict_workspace_for(k_cache, block_tables, stream=None):
+    """A workspace tensor sized for pa_evict on these shapes."""
+    n, mb = block_tables.shape
+    nbytes = evict_workspace_size(n, k_cache.shape[1], mb)
+    return _scratch(nbytes, k_cache.device, stream) if nbytes else None
+
+
+def evict(k_cache, v_cache, mass, block_tables, seq_lens, new_lens, keep_first=0, keep_last=0,
+          workspace=None, stream=None):
+    """pa_evict: every sequence longer than new_lens[s] is cut to that many tokens in place:
+    each kv head keeps its first keep_first, its last keep_last and the heaviest of the rest
+    by mass, which moves along.  The caller shortens seq_lens to new_lens, gives back the
+    blocks past it and renews the bounds; the sequence's blocks must be its own."""
+    names = _hot()
+    nb, hkv, bs, d = k_cache.shape
+    dt, dev = k_cache.dtype, _current(k_cache, names)
+    n, mb, tables, lens = _tables(block_tables, seq_lens, names, dev)
+    if v_cache.shape != k_cache.shape or new_lens.shape != (n,):
+        raise ValueError("shapes")
+    m = _mass_rows(mass, n, hkv, mb, names, dev)
+    if workspace is None:
+        workspace = evict_workspace_for(k_cache, block_tables, stream)
+    _sparse_call("pa_evict", dev, names, stream, mass=m, k=_near(k_cache, dt, dev),
+                 v=_near(v_cache, dt, dev), tables=tables, lens=lens,
+                 new_lens=_near(new_lens, names.i32, dev), workspace=workspace, n=n, hkv=hkv, d=d,
+                 bs=bs, mb=mb, nb=nb, first=int(keep_first), last=int(keep_last),
+                 code=_code(dt, names))
 
 
 def copy_blocks(k_cache, v_cache, block_mapping, stream=None):

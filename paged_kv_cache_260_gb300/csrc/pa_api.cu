@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cuda.h>
 #include <cudaTypedefs.h>
+#include <initializer_list>
 #include <limits.h>
 #include <math.h>
 #include <mutex>
@@ -12,10 +13,12 @@
 
 #include "pa_cache.h"
 #include "pa_internal.h"
+#include "pa_mass.h"
 #include "pa_prefill_abi.h"
 #include "pa_rope.h"
 #include "pa_schedule.cuh"
 #include "pa_shared.h"
+#include "pa_sparse.h"
 #include "pagedattn.h"
 
 namespace pa {
@@ -467,6 +470,9 @@ struct DecodeExtra {
     const float *lambda = nullptr;
     const void *norm_w = nullptr;
     float norm_eps = 0.f, out_scale = 1.f;
+    // weight accounting: where the scores and statistics go, non-null
+    float *scores = nullptr;
+    float2 *stat = nullptr;
 };
 
 static int decode_impl(void *out, const void *q, const void *k_cache, const void *v_cache,
@@ -511,6 +517,9 @@ static int decode_impl(void *out, const void *q, const void *k_cache, const void
     if (diff)
         found = dtype == PA_DTYPE_F16 ? diff_decode_kernels_f16(head_dim, group, &ks)
                                       : diff_decode_kernels_bf16(head_dim, group, &ks);
+    else if (x.scores)
+        found = dtype == PA_DTYPE_F16 ? mass_decode_kernels_f16(head_dim, group, &ks)
+                                      : mass_decode_kernels_bf16(head_dim, group, &ks);
     else if (group <= 8)
         found = dtype == PA_DTYPE_F16 ? decode_kernels_f16(head_dim, &ks)
                                       : decode_kernels_bf16(head_dim, &ks);
@@ -595,6 +604,8 @@ static int decode_impl(void *out, const void *q, const void *k_cache, const void
     p.norm_w = x.norm_w;
     p.norm_eps = x.norm_eps;
     p.out_scale = x.out_scale;
+    p.scores = x.scores;
+    p.stat = x.stat;
     char *ws = static_cast<char *>(workspace);
     if (wl.total > 0) {
         p.ws_m = reinterpret_cast<float *>(ws + wl.m_off);
@@ -1405,6 +1416,463 @@ int pa_diff_prefill_args(const struct pa_diff_args *args)
                            a.num_heads, a.num_kv_heads, a.head_dim, a.block_size,
                            a.max_blocks_per_seq, a.num_blocks, (float)a.scale, (float)a.norm_eps,
                            (float)a.out_scale, a.dtype, a.workspace, a.workspace_bytes, a.stream);
+}
+
+// ---- block selection, weight accounting and eviction ------------------------------
+
+// What the struct's calls share: the struct itself, the pool's sizes, counts and the
+// 32-bit limits of pa_decode.
+static int sparse_common(const struct pa_sparse_args *args, pa_sparse_args *a)
+{
+    if (!read_args(args, a))
+        return PA_ERR_INVALID_ARG;
+    const int rc = check_common(a->num_kv_heads, a->head_dim, a->block_size, a->num_blocks,
+                                a->dtype);
+    if (rc != PA_OK)
+        return rc;
+    if (a->num_seqs < 0)
+        return PA_ERR_INVALID_ARG;
+    if ((long long)a->num_blocks * a->num_kv_heads * kBlockSize >= (1LL << 31) ||
+        (long long)a->num_seqs * a->num_kv_heads >= (1LL << 31))
+        return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
+// Tables of max_blocks_per_seq entries: the limits that flat indices set.
+static int sparse_tables(const pa_sparse_args &a)
+{
+    if (a.max_blocks_per_seq <= 0)
+        return PA_ERR_INVALID_ARG;
+    if ((long long)a.num_seqs * a.max_blocks_per_seq * a.num_kv_heads >= (1LL << 31) ||
+        (long long)a.max_blocks_per_seq * kBlockSize >= (1LL << 30))
+        return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
+static int sparse_heads(const pa_sparse_args &a, int most)
+{
+    if (a.num_heads <= 0 || a.num_heads % a.num_kv_heads)
+        return PA_ERR_INVALID_ARG;
+    return a.num_heads / a.num_kv_heads > most ? PA_ERR_UNSUPPORTED : PA_OK;
+}
+
+static bool all_aligned(std::initializer_list<const void *> list, uintptr_t to)
+{
+    for (const void *x : list)
+        if (!x || !aligned(x, to))
+            return false;
+    return true;
+}
+
+// Thread blocks of a kernel whose warps share out `units` units: at most `per_sm` an SM.
+static unsigned share_grid(long long units, int threads, int per_sm, const DeviceState *ds)
+{
+    const long long warps = threads / 32;
+    return (unsigned)std::max(1LL, std::min((long long)ds->num_sms * per_sm,
+                                            (units + warps - 1) / warps));
+}
+
+int pa_block_bounds(const struct pa_sparse_args *args)
+{
+    pa_sparse_args a;
+    int rc = sparse_common(args, &a);
+    if (rc == PA_OK)
+        rc = sparse_tables(a);
+    if (rc != PA_OK || a.num_seqs == 0)
+        return rc;
+    if (!all_aligned({a.k_cache, a.bounds}, 16) || !all_aligned({a.block_tables, a.seq_lens}, 4) ||
+        !aligned(a.starts, 4))
+        return PA_ERR_INVALID_ARG;
+    DeviceState *ds;
+    rc = device_state(&ds);
+    if (rc != PA_OK)
+        return rc;
+    BoundsParams p{};
+    p.k_cache = a.k_cache;
+    p.bounds = a.bounds;
+    p.block_tables = a.block_tables;
+    p.seq_lens = a.seq_lens;
+    p.starts = a.starts;
+    p.err = ds->err;
+    p.num_seqs = a.num_seqs;
+    p.num_kv_heads = a.num_kv_heads;
+    p.max_blocks = a.max_blocks_per_seq;
+    p.num_blocks = a.num_blocks;
+    const SparseKernel k = bounds_kernel(a.dtype == PA_DTYPE_BF16, a.head_dim);
+    const long long units = (long long)a.num_seqs * a.max_blocks_per_seq * a.num_kv_heads;
+    void *kargs[] = {&p};
+    return launch_dependent(k.fn, dim3(share_grid(units, k.threads, 5, ds)), dim3(k.threads), 0,
+                            static_cast<cudaStream_t>(a.stream), kargs);
+}
+
+// Workspace of pa_select_blocks: the scores, the reach of 16 blocks each, and the longer
+// scores of blocks in doubt.
+struct SelectLayout {
+    size_t reach_off, exact_off, total;
+    long long row;
+};
+
+static SelectLayout select_layout(int num_seqs, int num_kv_heads, int max_blocks)
+{
+    SelectLayout w{};
+    w.row = ((long long)max_blocks + 15) / 16 * 16;
+    const size_t n = (size_t)num_seqs * num_kv_heads * w.row;
+    w.reach_off = round_up(4 * n, 256);
+    w.exact_off = w.reach_off + round_up(4 * (n / 16), 256);
+    w.total = w.exact_off + round_up(8 * n, 256);
+    return w;
+}
+
+size_t pa_select_blocks_workspace_size(int num_seqs, int num_kv_heads, int max_blocks_per_seq)
+{
+    if (num_seqs <= 0 || num_kv_heads <= 0 || max_blocks_per_seq <= 0)
+        return 0;
+    return select_layout(num_seqs, num_kv_heads, max_blocks_per_seq).total;
+}
+
+int pa_select_blocks(const struct pa_sparse_args *args)
+{
+    pa_sparse_args a;
+    int rc = sparse_common(args, &a);
+    if (rc == PA_OK)
+        rc = sparse_tables(a);
+    if (rc == PA_OK)
+        rc = sparse_heads(a, kMaxGroup);
+    if (rc != PA_OK)
+        return rc;
+    if (a.keep <= 0 || a.keep_first < 0 || a.keep_last < 1 || a.keep_first > a.keep ||
+        a.keep_last > a.keep - a.keep_first)
+        return PA_ERR_INVALID_ARG;
+    if (a.num_seqs == 0)
+        return PA_OK;
+    if (!all_aligned({a.q, a.bounds}, 16) ||
+        !all_aligned({a.block_tables, a.seq_lens, a.tiles, a.tile_lens}, 4))
+        return PA_ERR_INVALID_ARG;
+    const SelectLayout w = select_layout(a.num_seqs, a.num_kv_heads, a.max_blocks_per_seq);
+    if (!a.workspace || a.workspace_bytes < w.total || !aligned(a.workspace, 256))
+        return PA_ERR_WORKSPACE;
+    DeviceState *ds;
+    rc = device_state(&ds);
+    if (rc != PA_OK)
+        return rc;
+    char *ws = static_cast<char *>(a.workspace);
+    SelectParams p{};
+    p.tiles = a.tiles;
+    p.tile_lens = a.tile_lens;
+    p.q = a.q;
+    p.bounds = a.bounds;
+    p.block_tables = a.block_tables;
+    p.seq_lens = a.seq_lens;
+    p.scores = reinterpret_cast<float *>(ws);
+    p.reach = reinterpret_cast<float *>(ws + w.reach_off);
+    p.exact = reinterpret_cast<unsigned long long *>(ws + w.exact_off);
+    p.err = ds->err;
+    p.num_seqs = a.num_seqs;
+    p.num_heads = a.num_heads;
+    p.num_kv_heads = a.num_kv_heads;
+    p.max_blocks = a.max_blocks_per_seq;
+    p.num_blocks = a.num_blocks;
+    p.keep = a.keep;
+    p.keep_first = a.keep_first;
+    p.keep_last = a.keep_last;
+    p.row = (int)w.row;
+    const bool bf16 = a.dtype == PA_DTYPE_BF16;
+    const int group = a.num_heads / a.num_kv_heads;
+    cudaStream_t st = static_cast<cudaStream_t>(a.stream);
+    void *kargs[] = {&p};
+    if (a.max_blocks_per_seq > a.keep) {         // else all blocks are kept
+        const SparseKernel k = block_score_kernel(bf16, a.head_dim, group);
+        const long long units = (long long)a.num_seqs * a.num_kv_heads * (w.row / 16);
+        rc = launch_dependent(k.fn, dim3(share_grid(units, k.threads, 5, ds)), dim3(k.threads), 0,
+                              st, kargs);
+        if (rc != PA_OK)
+            return rc;
+    }
+    const SparseKernel k = block_select_kernel(bf16, a.head_dim);
+    return launch_dependent(k.fn, dim3((unsigned)a.num_seqs * a.num_kv_heads), dim3(k.threads), 0,
+                            st, kargs);
+}
+
+// The pool with a kv head's tile as a block of its own: every (sequence, kv head) is a
+// sequence of `keep` blocks with one kv head.
+size_t pa_sparse_decode_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                       int keep)
+{
+    if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads ||
+        (long long)num_seqs * num_kv_heads > INT_MAX)
+        return 0;
+    return pa_decode_workspace_size(num_seqs * num_kv_heads, num_heads / num_kv_heads, 1, head_dim,
+                                    keep, 0);
+}
+
+int pa_sparse_decode(const struct pa_sparse_args *args)
+{
+    pa_sparse_args a;
+    int rc = sparse_common(args, &a);
+    if (rc == PA_OK)
+        rc = sparse_heads(a, kMaxGroup);
+    if (rc != PA_OK)
+        return rc;
+    if (a.num_seqs > 0 && a.out && a.out == a.q)
+        return PA_ERR_INVALID_ARG;
+    return decode_impl(a.out, a.q, a.k_cache, a.v_cache, a.tiles, a.tile_lens,
+                       a.num_seqs * a.num_kv_heads, a.num_heads / a.num_kv_heads, 1, a.head_dim,
+                       a.block_size, a.keep, a.num_blocks * a.num_kv_heads, (float)a.scale, a.dtype,
+                       0, a.workspace, a.workspace_bytes, a.stream, DecodeExtra{});
+}
+
+// Workspace of pa_decode_mass: the decode's own, the statistics, the scores.
+struct MassLayout {
+    size_t stat_off, score_off, total;
+};
+
+static MassLayout mass_layout(size_t decode_bytes, int num_seqs, int num_heads, int num_kv_heads,
+                              int max_blocks)
+{
+    MassLayout w{};
+    w.stat_off = round_up(decode_bytes, 256);
+    w.score_off = w.stat_off + round_up(sizeof(float2) * (size_t)num_seqs * num_heads, 256);
+    w.total = w.score_off + sizeof(float) * (size_t)num_seqs * num_kv_heads * max_blocks *
+                                kBlockSize * score_cols(num_heads / num_kv_heads);
+    return w;
+}
+
+size_t pa_decode_mass_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                     int max_blocks_per_seq)
+{
+    if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads ||
+        max_blocks_per_seq <= 0)
+        return 0;
+    const size_t own = pa_decode_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim,
+                                                max_blocks_per_seq, 0);
+    return own ? mass_layout(own, num_seqs, num_heads, num_kv_heads, max_blocks_per_seq).total : 0;
+}
+
+int pa_decode_mass(const struct pa_sparse_args *args)
+{
+    pa_sparse_args a;
+    int rc = sparse_common(args, &a);
+    if (rc == PA_OK)
+        rc = sparse_tables(a);
+    if (rc == PA_OK)
+        rc = sparse_heads(a, kMaxGroup);
+    if (rc != PA_OK)
+        return rc;
+    const float scale = (float)a.scale, decay = (float)a.decay;
+    if (!isfinite(scale) || !isfinite(decay))
+        return PA_ERR_INVALID_ARG;
+    if (a.num_seqs == 0)
+        return PA_OK;
+    if (!all_aligned({a.mass, a.out, a.q, a.k_cache, a.v_cache}, 16) ||
+        !all_aligned({a.block_tables, a.seq_lens}, 4) || a.out == a.q)
+        return PA_ERR_INVALID_ARG;
+    const size_t own = pa_decode_workspace_size(a.num_seqs, a.num_heads, a.num_kv_heads, a.head_dim,
+                                                a.max_blocks_per_seq, 0);
+    const MassLayout w = mass_layout(own, a.num_seqs, a.num_heads, a.num_kv_heads,
+                                     a.max_blocks_per_seq);
+    if (!a.workspace || a.workspace_bytes < w.total || !aligned(a.workspace, 256))
+        return PA_ERR_WORKSPACE;
+    DeviceState *ds;
+    rc = device_state(&ds);
+    if (rc != PA_OK)
+        return rc;
+    char *ws = static_cast<char *>(a.workspace);
+    DecodeExtra x;
+    x.stat = reinterpret_cast<float2 *>(ws + w.stat_off);
+    x.scores = reinterpret_cast<float *>(ws + w.score_off);
+    rc = decode_impl(a.out, a.q, a.k_cache, a.v_cache, a.block_tables, a.seq_lens, a.num_seqs,
+                     a.num_heads, a.num_kv_heads, a.head_dim, a.block_size, a.max_blocks_per_seq,
+                     a.num_blocks, scale, a.dtype, 0, a.workspace, own, a.stream, x);
+    if (rc != PA_OK)
+        return rc;
+    DecodeMassParams p{};
+    p.mass = a.mass;
+    p.scores = x.scores;
+    p.stat = x.stat;
+    p.seq_lens = a.seq_lens;
+    p.err = ds->err;
+    p.num_seqs = a.num_seqs;
+    p.num_heads = a.num_heads;
+    p.num_kv_heads = a.num_kv_heads;
+    p.max_blocks = a.max_blocks_per_seq;
+    p.decay = decay;
+    // units of 128 tokens
+    const long long units = (long long)a.num_seqs * a.num_kv_heads * ((a.max_blocks_per_seq + 7) / 8);
+    void *kargs[] = {&p};
+    return launch_dependent(decode_mass_finish(),
+                            dim3(share_grid(units, kMassFinishThreads, 4, ds)),
+                            dim3(kMassFinishThreads), 0, static_cast<cudaStream_t>(a.stream), kargs);
+}
+
+// How pa_prefill_mass cuts its work: units of 2 x 128 rows, and a unit's keys into as many
+// parts as give every SM three blocks, two key tiles a part at least.
+struct PrefillMassPlan {
+    long long row_blocks, splits, units;
+    size_t sums_off, total;
+};
+
+static bool prefill_mass_plan(int num_seqs, int max_query_len, int num_heads, int num_kv_heads,
+                              int max_blocks, int num_sms, PrefillMassPlan *w)
+{
+    if (num_seqs <= 0 || max_query_len <= 0 || num_heads <= 0 || num_kv_heads <= 0 ||
+        num_heads % num_kv_heads || num_heads / num_kv_heads > kMassRows || max_blocks <= 0)
+        return false;
+    const long long tokens = kMassTiles * (kMassRows / (num_heads / num_kv_heads));
+    w->row_blocks = (max_query_len + tokens - 1) / tokens;
+    w->units = (long long)num_seqs * num_kv_heads * w->row_blocks;
+    const long long key_tiles = ((long long)max_blocks * kBlockSize + kMassKeys - 1) / kMassKeys;
+    w->splits = std::max(1LL, std::min((key_tiles + 1) / 2, 3LL * num_sms / w->units));
+    w->sums_off = round_up(sizeof(float2) * (size_t)w->units * w->splits * kMassTiles * kMassRows,
+                           256);
+    w->total = w->sums_off + sizeof(float) * (size_t)w->units * kMassTiles * max_blocks * kBlockSize;
+    return true;
+}
+
+size_t pa_prefill_mass_workspace_size(int num_seqs, int max_query_len, int num_heads,
+                                      int num_kv_heads, int max_blocks_per_seq)
+{
+    DeviceState *ds;
+    PrefillMassPlan w{};
+    if (num_seqs <= 0 || max_query_len <= 0 || device_state(&ds) != PA_OK ||
+        !prefill_mass_plan(num_seqs, max_query_len, num_heads, num_kv_heads, max_blocks_per_seq,
+                           ds->num_sms, &w))
+        return 0;
+    return w.total;
+}
+
+int pa_prefill_mass(const struct pa_sparse_args *args)
+{
+    pa_sparse_args a;
+    int rc = sparse_common(args, &a);
+    if (rc == PA_OK)
+        rc = sparse_tables(a);
+    if (rc == PA_OK)
+        rc = sparse_heads(a, kMassRows);
+    if (rc != PA_OK)
+        return rc;
+    const float scale = (float)a.scale, decay = (float)a.decay;
+    if (!isfinite(scale) || !(scale > 0.f) || !isfinite(decay) || a.max_query_len < 0 ||
+        a.num_queries < 0)
+        return PA_ERR_INVALID_ARG;
+    if (a.num_seqs == 0 || a.max_query_len == 0)
+        return PA_OK;
+    if (!all_aligned({a.mass, a.q, a.k_cache}, 16) ||
+        !all_aligned({a.block_tables, a.seq_lens, a.query_start}, 4))
+        return PA_ERR_INVALID_ARG;
+    DeviceState *ds;
+    rc = device_state(&ds);
+    if (rc != PA_OK)
+        return rc;
+    PrefillMassPlan w{};
+    if (!prefill_mass_plan(a.num_seqs, a.max_query_len, a.num_heads, a.num_kv_heads,
+                           a.max_blocks_per_seq, ds->num_sms, &w))
+        return PA_ERR_INVALID_ARG;
+    if (w.units * w.splits >= (1LL << 31))
+        return PA_ERR_UNSUPPORTED;
+    if (!a.workspace || a.workspace_bytes < w.total || !aligned(a.workspace, 256))
+        return PA_ERR_WORKSPACE;
+    MassKernels k{};
+    if (!prefill_mass_kernels(a.dtype == PA_DTYPE_BF16, a.head_dim, &k))
+        return PA_ERR_UNSUPPORTED;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    for (const void *fn : {k.stats, k.sums}) {
+        rc = ensure_smem(fn, dev, k.smem);
+        if (rc != PA_OK)
+            return rc;
+    }
+    CUtensorMap tmk;
+    rc = make_pool_map(&tmk, a.k_cache, a.dtype, a.head_dim,
+                       (long long)a.num_blocks * a.num_kv_heads * kBlockSize);
+    if (rc != PA_OK)
+        return rc;
+    PrefillMassParams p{};
+    p.mass = a.mass;
+    p.q = a.q;
+    p.block_tables = a.block_tables;
+    p.seq_lens = a.seq_lens;
+    p.query_start = a.query_start;
+    p.stats = static_cast<float2 *>(a.workspace);
+    p.sums = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + w.sums_off);
+    p.err = ds->err;
+    p.num_seqs = a.num_seqs;
+    p.num_heads = a.num_heads;
+    p.num_kv_heads = a.num_kv_heads;
+    p.max_blocks = a.max_blocks_per_seq;
+    p.num_blocks = a.num_blocks;
+    p.num_queries = a.num_queries;
+    p.row_blocks = (int)w.row_blocks;
+    p.splits = (int)w.splits;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.decay = decay;
+    cudaStream_t st = static_cast<cudaStream_t>(a.stream);
+    void *kargs[] = {&p, &tmk};
+    const dim3 grid((unsigned)(w.units * w.splits));
+    rc = launch_dependent(k.stats, grid, dim3(k.threads), k.smem, st, kargs);
+    if (rc == PA_OK)
+        rc = launch_dependent(k.sums, grid, dim3(k.threads), k.smem, st, kargs);
+    if (rc != PA_OK)
+        return rc;
+    const long long units = (long long)a.num_seqs * a.num_kv_heads * ((a.max_blocks_per_seq + 7) / 8);
+    void *fargs[] = {&p};
+    return launch_dependent(prefill_mass_finish(),
+                            dim3(share_grid(units, kMassFinishThreads, 4, ds)),
+                            dim3(kMassFinishThreads), 0, st, fargs);
+}
+
+// Workspace of pa_evict: per (sequence, kv head) the holes and the slots that move into
+// them, at most half of the table's each (they are as many as both what is kept from
+// beyond the new end and what is dropped before it).
+size_t pa_evict_workspace_size(int num_seqs, int num_kv_heads, int max_blocks_per_seq)
+{
+    if (num_seqs <= 0 || num_kv_heads <= 0 || max_blocks_per_seq <= 0)
+        return 0;
+    return 4 * (size_t)num_seqs * num_kv_heads * max_blocks_per_seq * kBlockSize;
+}
+
+int pa_evict(const struct pa_sparse_args *args)
+{
+    pa_sparse_args a;
+    int rc = sparse_common(args, &a);
+    if (rc == PA_OK)
+        rc = sparse_tables(a);
+    if (rc != PA_OK)
+        return rc;
+    if (a.keep_first < 0 || a.keep_last < 0)
+        return PA_ERR_INVALID_ARG;
+    if (a.num_seqs == 0)
+        return PA_OK;
+    if (!all_aligned({a.k_cache, a.v_cache, a.mass}, 16) ||
+        !all_aligned({a.block_tables, a.seq_lens, a.new_lens}, 4))
+        return PA_ERR_INVALID_ARG;
+    if (!a.workspace || !aligned(a.workspace, 256) ||
+        a.workspace_bytes < pa_evict_workspace_size(a.num_seqs, a.num_kv_heads,
+                                                    a.max_blocks_per_seq))
+        return PA_ERR_WORKSPACE;
+    DeviceState *ds;
+    rc = device_state(&ds);
+    if (rc != PA_OK)
+        return rc;
+    EvictParams p{};
+    p.k_cache = a.k_cache;
+    p.v_cache = a.v_cache;
+    p.mass = a.mass;
+    p.block_tables = a.block_tables;
+    p.seq_lens = a.seq_lens;
+    p.new_lens = a.new_lens;
+    p.lists = static_cast<int32_t *>(a.workspace);
+    p.err = ds->err;
+    p.num_seqs = a.num_seqs;
+    p.num_kv_heads = a.num_kv_heads;
+    p.max_blocks = a.max_blocks_per_seq;
+    p.num_blocks = a.num_blocks;
+    p.keep_first = a.keep_first;
+    p.keep_last = a.keep_last;
+    p.list = a.max_blocks_per_seq * kBlockSize / 2;
+    const SparseKernel k = evict_kernel(a.head_dim);
+    void *kargs[] = {&p};
+    return launch_dependent(k.fn, dim3((unsigned)a.num_seqs * a.num_kv_heads), dim3(k.threads), 0,
+                            static_cast<cudaStream_t>(a.stream), kargs);
 }
 
 int pa_copy_blocks(void *k_cache, void *v_cache, const int64_t *block_mapping, int num_pairs,

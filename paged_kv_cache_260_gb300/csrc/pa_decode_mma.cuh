@@ -301,13 +301,14 @@ __device__ __forceinline__ void diff_piece(const DecodeParams &p, const float (&
 // neighbour; only then are the neighbours' table entries looked up per tile
 // (the check costs the unshared loop a few per cent even when it never
 // fires, so the kernel holds two copies of the loop and picks one per block).
-template <typename T, int D, int NT, int W, int S, bool SHARE, bool PARTIAL, bool DIFF>
+template <typename T, int D, int NT, int W, int S, bool SHARE, bool PARTIAL, bool DIFF, bool MASS>
 __device__ __forceinline__ void decode_worker(const DecodeParams &p, const CUtensorMap &tmk,
                                               const CUtensorMap &tmv, unsigned char *smem,
                                               uint64_t *bars, const int32_t *pre,
                                               const int32_t *lens, const uint8_t *share)
 {
     static_assert(!(PARTIAL && DIFF), "no partial outputs of a difference");
+    static_assert(!MASS || (!PARTIAL && !DIFF), "accounting is the plain decode's");
     constexpr bool TWO_TERMS = DIFF && NT <= 2;
     using Sh = MmaShape<D, NT, DIFF>;
     using E = Elem<T>;
@@ -545,6 +546,16 @@ __device__ __forceinline__ void decode_worker(const DecodeParams &p, const CUten
                     if (r + 8 >= nvalid)
                         x2 = x3 = -INFINITY;
                 }
+                if constexpr (MASS) {
+                    const int cols = score_cols(G), h0 = 8 * j + 2 * qd;
+                    if (h0 < cols) {
+                        float *dst = p.scores +
+                                     (((size_t)cons.s * Hkv + cons.h) * p.max_blocks + tile) *
+                                         kBlockSize * cols + h0;
+                        *reinterpret_cast<float2 *>(dst + r * cols) = make_float2(x0, x1);
+                        *reinterpret_cast<float2 *>(dst + (r + 8) * cols) = make_float2(x2, x3);
+                    }
+                }
                 float mx0 = fmaxf(x0, x2), mx1 = fmaxf(x1, x3);
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) {
@@ -668,6 +679,12 @@ __device__ __forceinline__ void decode_worker(const DecodeParams &p, const CUten
                     }
                 }
             } else if (whole) {
+                if constexpr (MASS) {
+                    if (r == 0 && h0 < G)
+                        p.stat[(size_t)s * Hq + h * G + h0] = make_float2(m[j][0], inv0);
+                    if (r == 0 && h1 < G)
+                        p.stat[(size_t)s * Hq + h * G + h1] = make_float2(m[j][1], inv1);
+                }
                 T *out = reinterpret_cast<T *>(p.out) + ((size_t)s * Hq + h * G) * D;
 #pragma unroll
                 for (int mt = 0; mt < KS; ++mt) {
@@ -748,7 +765,8 @@ __device__ __forceinline__ void decode_worker(const DecodeParams &p, const CUten
     }
 }
 
-template <typename T, int D, int NT, int W, int S, bool PARTIAL, bool DIFF = false>
+template <typename T, int D, int NT, int W, int S, bool PARTIAL, bool DIFF = false,
+          bool MASS = false>
 __global__ void __launch_bounds__(W * 32)
 decode_mma_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmk,
                   const __grid_constant__ CUtensorMap tmv)
@@ -828,11 +846,11 @@ decode_mma_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmk,
     }
 
     if (any_share)
-        decode_worker<T, D, NT, W, S, true, PARTIAL, DIFF>(p, tmk, tmv, smem, bars, pre, lens,
-                                                           share);
+        decode_worker<T, D, NT, W, S, true, PARTIAL, DIFF, MASS>(p, tmk, tmv, smem, bars, pre,
+                                                                 lens, share);
     else
-        decode_worker<T, D, NT, W, S, false, PARTIAL, DIFF>(p, tmk, tmv, smem, bars, pre, lens,
-                                                            share);
+        decode_worker<T, D, NT, W, S, false, PARTIAL, DIFF, MASS>(p, tmk, tmv, smem, bars, pre,
+                                                                  lens, share);
 }
 
 // ---------------------------------------------------------------------------
@@ -923,6 +941,8 @@ __global__ void __launch_bounds__(512) merge_cut_kernel(const DecodeParams p)
         }
     } else {
         using M = Mma<T>;
+        if (p.stat && lane == 0)
+            p.stat[(size_t)s * Hq + h * G + g] = make_float2(Mx * kLog2e, inv);
         T *dst = reinterpret_cast<T *>(p.out) + ((size_t)s * Hq + h * G + g) * D + lane * V;
         uint32_t *d32 = reinterpret_cast<uint32_t *>(dst);
 #pragma unroll
@@ -1350,6 +1370,33 @@ inline void fill_kernel_set(KernelSet *ks)
     ks->prep_fix = reinterpret_cast<const void *>(&decode_prep_fix_kernel<kPrepThreads>);
     ks->merge_cut = reinterpret_cast<const void *>(&merge_cut_kernel<T, D>);
     ks->merge_part = reinterpret_cast<const void *>(&merge_part_kernel<T, D>);
+}
+
+// The decode of pa_decode_mass: the same kernels, leaving scores and statistics.
+template <typename T, int D, int NT>
+inline void fill_mass_kernel_set(KernelSet *ks)
+{
+    constexpr int S = 2;
+    constexpr int W = D == 128 ? (NT == 1 ? 7 : 8) : 12;
+    ks->decode = reinterpret_cast<const void *>(
+        &decode_mma_kernel<T, D, NT, W, S, false, false, true>);
+    ks->warps = W;
+    ks->smem_fixed = MmaLayout<D, NT, W, S>::fixed;
+    ks->prep = reinterpret_cast<const void *>(&decode_prep_kernel<kPrepThreads>);
+    ks->prep_fix = reinterpret_cast<const void *>(&decode_prep_fix_kernel<kPrepThreads>);
+    ks->merge_cut = reinterpret_cast<const void *>(&merge_cut_kernel<T, D>);
+}
+
+template <typename T>
+inline bool mass_kernels(int head_dim, int group, KernelSet *ks)
+{
+    if (head_dim == 128)
+        group <= 8 ? fill_mass_kernel_set<T, 128, 1>(ks) : fill_mass_kernel_set<T, 128, 2>(ks);
+    else if (head_dim == 64)
+        group <= 8 ? fill_mass_kernel_set<T, 64, 1>(ks) : fill_mass_kernel_set<T, 64, 2>(ks);
+    else
+        return false;
+    return true;
 }
 
 template <typename T, int NT>

@@ -1,6 +1,7 @@
 // pa_internal.h -- structures shared by the host dispatch and the kernels.
 #pragma once
 
+#include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -66,7 +67,15 @@ struct DecodeParams {
     const float *lambda;
     const void *norm_w;
     float norm_eps, out_scale;
+    // weight accounting only (null otherwise): every score in base 2, run by run
+    // [num_seqs * num_kv_heads][max_blocks * 16][score_cols(group)], and for each
+    // (sequence, query head) its maximum in base 2 and the reciprocal of its sum
+    float *scores;
+    float2 *stat;
 };
+
+// Scores of a token, an even number so that a lane stores its two heads at once.
+inline __host__ __device__ int score_cols(int group) { return (group + 1) & ~1; }
 
 // Kernels of one (dtype, head_dim, query columns) instantiation.
 struct KernelSet {
@@ -113,5 +122,8 @@ bool decode_kernels_bf16_g16(int head_dim, KernelSet *ks);
 // tile between the two maps, 5..8 take one for each, 9..16 two
 bool diff_decode_kernels_f16(int head_dim, int group, KernelSet *ks);
 bool diff_decode_kernels_bf16(int head_dim, int group, KernelSet *ks);
+// the plain decode that leaves its scores and statistics for the accounting
+bool mass_decode_kernels_f16(int head_dim, int group, KernelSet *ks);
+bool mass_decode_kernels_bf16(int head_dim, int group, KernelSet *ks);
 
 }  // namespace pa

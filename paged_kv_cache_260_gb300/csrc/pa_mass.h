@@ -1,0 +1,54 @@
+// pa_mass.h -- what the host side of pa_decode_mass and pa_prefill_mass shares
+// with the kernels that add up softmax weights per token.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace pa {
+
+// The accounting after a decode: scores and statistics of DecodeParams.
+struct DecodeMassParams {
+    float *mass;                   // [num_seqs][num_kv_heads][max_blocks * 16]
+    const float *scores;           // [num_seqs * num_kv_heads][max_blocks * 16][score_cols]
+    const float2 *stat;            // [num_seqs][num_heads] maximum (base 2), 1 / sum
+    const int32_t *seq_lens;
+    uint32_t *err;
+    int num_seqs, num_heads, num_kv_heads, max_blocks;
+    float decay;
+};
+
+// The weights a chunk's queries give: two passes over the keys and a sum.
+struct PrefillMassParams {
+    float *mass;
+    const void *q;
+    const int32_t *block_tables;
+    const int32_t *seq_lens;
+    const int32_t *query_start;
+    float2 *stats;                 // [unit][split][2 * 128 rows] maximum (base 2), sum
+    float *sums;                   // [num_seqs * num_kv_heads][2 * row_blocks][max_blocks * 16]
+    uint32_t *err;
+    int num_seqs, num_heads, num_kv_heads, max_blocks, num_blocks;
+    int num_queries;               // rows of q
+    int row_blocks;                // units of 2 x 128 (token, head) rows per (sequence, kv head)
+    int splits;                    // parts of a unit's keys, a thread block each
+    float scale_log2, decay;
+};
+
+constexpr int kMassRows = 128;     // (token, head) rows of one query tile
+constexpr int kMassTiles = 2;      // query tiles of a unit
+constexpr int kMassKeys = 128;     // keys of a tile
+
+struct MassKernels {
+    const void *stats, *sums;      // (PrefillMassParams, tensor map of the key pool)
+    int threads;
+    size_t smem;
+};
+
+bool prefill_mass_kernels(bool bf16, int head_dim, MassKernels *k);
+const void *prefill_mass_finish();     // (PrefillMassParams)
+const void *decode_mass_finish();      // (DecodeMassParams)
+constexpr int kMassFinishThreads = 256;
+
+}  // namespace pa

@@ -1505,10 +1505,10 @@ int pa_block_bounds(const struct pa_sparse_args *args)
                             static_cast<cudaStream_t>(a.stream), kargs);
 }
 
-// Workspace of pa_select_blocks: the scores, the reach of 16 blocks each, and the longer
-// scores of blocks in doubt.
+// Workspace of pa_select_blocks: scores that do not fit in shared memory, and the longer
+// ones of blocks in doubt.
 struct SelectLayout {
-    size_t reach_off, exact_off, total;
+    size_t exact_off, total;
     long long row;
 };
 
@@ -1517,8 +1517,7 @@ static SelectLayout select_layout(int num_seqs, int num_kv_heads, int max_blocks
     SelectLayout w{};
     w.row = ((long long)max_blocks + 15) / 16 * 16;
     const size_t n = (size_t)num_seqs * num_kv_heads * w.row;
-    w.reach_off = round_up(4 * n, 256);
-    w.exact_off = w.reach_off + round_up(4 * (n / 16), 256);
+    w.exact_off = round_up(4 * n, 256);
     w.total = w.exact_off + round_up(8 * n, 256);
     return w;
 }
@@ -1564,7 +1563,6 @@ int pa_select_blocks(const struct pa_sparse_args *args)
     p.block_tables = a.block_tables;
     p.seq_lens = a.seq_lens;
     p.scores = reinterpret_cast<float *>(ws);
-    p.reach = reinterpret_cast<float *>(ws + w.reach_off);
     p.exact = reinterpret_cast<unsigned long long *>(ws + w.exact_off);
     p.err = ds->err;
     p.num_seqs = a.num_seqs;
@@ -1576,21 +1574,19 @@ int pa_select_blocks(const struct pa_sparse_args *args)
     p.keep_first = a.keep_first;
     p.keep_last = a.keep_last;
     p.row = (int)w.row;
-    const bool bf16 = a.dtype == PA_DTYPE_BF16;
-    const int group = a.num_heads / a.num_kv_heads;
-    cudaStream_t st = static_cast<cudaStream_t>(a.stream);
+    const int runs = a.num_seqs * a.num_kv_heads;
+    const SelectLaunch e = select_launch(a.dtype == PA_DTYPE_BF16, a.head_dim,
+                                         a.num_heads / a.num_kv_heads, runs, a.max_blocks_per_seq,
+                                         ds->num_sms);
+    p.near = e.near;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    rc = ensure_smem(e.fn, dev, e.smem);
+    if (rc != PA_OK)
+        return rc;
     void *kargs[] = {&p};
-    if (a.max_blocks_per_seq > a.keep) {         // else all blocks are kept
-        const SparseKernel k = block_score_kernel(bf16, a.head_dim, group);
-        const long long units = (long long)a.num_seqs * a.num_kv_heads * (w.row / 16);
-        rc = launch_dependent(k.fn, dim3(share_grid(units, k.threads, 5, ds)), dim3(k.threads), 0,
-                              st, kargs);
-        if (rc != PA_OK)
-            return rc;
-    }
-    const SparseKernel k = block_select_kernel(bf16, a.head_dim);
-    return launch_dependent(k.fn, dim3((unsigned)a.num_seqs * a.num_kv_heads), dim3(k.threads), 0,
-                            st, kargs);
+    return launch_dependent(e.fn, dim3((unsigned)(runs * e.cluster)), dim3(e.threads), e.smem,
+                            static_cast<cudaStream_t>(a.stream), kargs, e.cluster);
 }
 
 // The pool with a kv head's tile as a block of its own: every (sequence, kv head) is a
@@ -1869,10 +1865,19 @@ int pa_evict(const struct pa_sparse_args *args)
     p.keep_first = a.keep_first;
     p.keep_last = a.keep_last;
     p.list = a.max_blocks_per_seq * kBlockSize / 2;
-    const SparseKernel k = evict_kernel(a.head_dim);
+    const EvictLaunch e = evict_launch(a.head_dim, a.num_seqs * a.num_kv_heads,
+                                       a.max_blocks_per_seq, ds->num_sms);
+    p.keys = e.keys;
+    p.table = e.table;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    rc = ensure_smem(e.fn, dev, e.smem);
+    if (rc != PA_OK)
+        return rc;
     void *kargs[] = {&p};
-    return launch_dependent(k.fn, dim3((unsigned)a.num_seqs * a.num_kv_heads), dim3(k.threads), 0,
-                            static_cast<cudaStream_t>(a.stream), kargs);
+    return launch_dependent(e.fn, dim3((unsigned)(a.num_seqs * a.num_kv_heads * e.cluster)),
+                            dim3(e.threads), e.smem, static_cast<cudaStream_t>(a.stream), kargs,
+                            e.cluster);
 }
 
 int pa_copy_blocks(void *k_cache, void *v_cache, const int64_t *block_mapping, int num_pairs,

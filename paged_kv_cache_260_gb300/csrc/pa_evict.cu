@@ -8,16 +8,18 @@
 // new end into the holes that dropped tokens left before it.  The sources of those
 // moves lie past all of their destinations, so they need no order among
 // themselves.
-#include <float.h>
+#include <limits.h>
 
 #include "pa_device.cuh"
 #include "pa_sparse.h"
+#include "pa_tally.cuh"
 
 namespace pa {
 
 namespace {
 
-constexpr int kEvictThreads = 1024;
+// Holes and sources up to this many a run stay in shared memory, others in the workspace.
+constexpr int kEvictList = 256;
 
 // The order of masses as unsigned numbers: -0 as 0, a NaN above all.
 __device__ __forceinline__ uint32_t mass_key(float x)
@@ -26,20 +28,27 @@ __device__ __forceinline__ uint32_t mass_key(float x)
     return x != x ? 0xffffffffu : u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kEvictThreads) evict_kernel_t(const EvictParams p)
+// One (sequence, kv head) per thread block, or per cluster of blocks that share out its
+// slots and its moves (CLUSTER).
+template <int D, int NTH, bool CLUSTER>
+__global__ void __launch_bounds__(NTH) evict_kernel_t(const EvictParams p)
 {
-    constexpr int NTH = kEvictThreads, NW = NTH / 32;
+    constexpr int NW = NTH / 32;
     constexpr uint32_t FULL = 0xffffffffu;
-    constexpr int KR = 8;                         // keys a thread holds in registers
     constexpr int CPR = D / 8;                    // 16-byte chunks of a row
     constexpr int RPW = 32 / (2 * CPR);           // tokens (K and V row) a warp moves at once
     constexpr int U = 8;                          // loads in flight a lane
-    static_assert(NW == 32, "a lane reads each warp's count");
-    __shared__ int part[2][3][NW];
+    // keys of the block's slots (p.keys of them), the table, holes and sources
+    extern __shared__ uint32_t smem[];
+    uint32_t *keys = smem;
+    int32_t *sm_table = reinterpret_cast<int32_t *>(smem + p.keys);
+    int32_t *sm_list = sm_table + p.table;
+    __shared__ TallySmem<NW> counts;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int Hkv = p.num_kv_heads;
-    const int run = blockIdx.x, s = run / Hkv, h = run % Hkv;
+    Tally<NW, CLUSTER> tally(counts);
+    const int C = tally.blocks, rank = tally.rank;
+    const int run = blockIdx.x / C, s = run / Hkv, h = run % Hkv;
     grid_dependents_launch();
     grid_dependency_wait();
     const int L = __ldg(p.seq_lens + s);
@@ -51,187 +60,176 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel_t(const EvictParam
     }
     if (B >= L)
         return;
-    // a table that does not hold leaves the sequence as it was
-    const int32_t *table = p.block_tables + (size_t)s * p.max_blocks;
-    bool bad = false;
-    for (int j = tid; j < (L + kBlockSize - 1) / kBlockSize; j += NTH)
-        bad |= (unsigned)__ldg(table + j) >= (unsigned)p.num_blocks;
-    if (__syncthreads_or(bad)) {
-        if (tid == 0)
-            record_error(p.err, PA_DEVERR_TABLE_RANGE);
-        return;
-    }
     const int R = min(p.keep_last, B), F = min(p.keep_first, B - R);
     const int edge = B - R, want = edge - F, hi = L - R;   // slots [F, hi) compete for `want`
     float *mass = p.mass + (size_t)run * p.max_blocks * kBlockSize;
 
-    // this thread's slots: F + seg * warp + 32 i + lane, i < steps
-    const int steps = ((hi - F + NW - 1) / NW + 31) / 32;
-    const int slot0 = F + warp * steps * 32 + lane;
-    uint32_t reg[KR];
-#pragma unroll
-    for (int i = 0; i < KR; ++i)
-        reg[i] = i < steps && slot0 + 32 * i < hi ? mass_key(__ldcg(mass + slot0 + 32 * i)) : 0;
-    auto each = [&](auto &&f) {                   // f(slot, key) over this thread's slots
-#pragma unroll
-        for (int i = 0; i < KR; ++i)
-            if (i < steps)
-                f(slot0 + 32 * i, reg[i]);
-        for (int i = KR; i < steps; ++i) {
-            const int t = slot0 + 32 * i;
-            f(t, t < hi ? mass_key(__ldcg(mass + t)) : 0u);
-        }
-    };
-
-    // the want-th largest key, two bits at a time: how many keys reach each of three
-    // thresholds.  (A slot past hi has key 0, which no threshold lets through.)
-    uint32_t T = 0;
-    int above = 0;                                // keys >= T + 1 at the end
-    if (want > 0) {
-        for (int bit = 30, round = 0; bit >= 0; bit -= 2, ++round) {
-            const uint32_t t1 = T | 1u << bit, t2 = T | 2u << bit, t3 = T | 3u << bit;
-            int n1 = 0, n2 = 0, n3 = 0;
-            each([&](int, uint32_t k) {
-                n1 += k >= t1;
-                n2 += k >= t2;
-                n3 += k >= t3;
-            });
-            n1 = __reduce_add_sync(FULL, n1);
-            n2 = __reduce_add_sync(FULL, n2);
-            n3 = __reduce_add_sync(FULL, n3);
-            int(*c)[NW] = part[round & 1];
-            if (lane == 0) {
-                c[0][warp] = n1;
-                c[1][warp] = n2;
-                c[2][warp] = n3;
-            }
-            __syncthreads();
-            n1 = __reduce_add_sync(FULL, c[0][lane]);
-            n2 = __reduce_add_sync(FULL, c[1][lane]);
-            n3 = __reduce_add_sync(FULL, c[2][lane]);
-            // (a NaN's key is all ones: T + 1 is never asked for it)
-            T = n3 >= want ? t3 : n2 >= want ? t2 : n1 >= want ? t1 : T;
-        }
-        int n = 0;
-        each([&](int, uint32_t k) { n += k > T; });
-        n = __reduce_add_sync(FULL, n);
-        if (lane == 0)
-            part[0][0][warp] = n;
-        __syncthreads();
-        above = __reduce_add_sync(FULL, part[0][0][lane]);
-        __syncthreads();
+    // the block's slots [lo, end), in it a warp's [w0, w1): steps of 32, the first p.keys of
+    // the block's keys in shared memory
+    const int span = ((hi - F + C * NTH - 1) / (C * NTH)) * NTH;
+    const int lo = min(hi, F + rank * span), end = min(hi, lo + span);
+    const int steps = span / NTH;
+    const int w0 = lo + warp * steps * 32;
+    // a table that does not hold leaves the sequence as it was
+    const int32_t *gtable = p.block_tables + (size_t)s * p.max_blocks;
+    const bool near = p.table > 0;
+    bool bad = false;
+    for (int j = tid; j < (L + kBlockSize - 1) / kBlockSize; j += NTH) {
+        const int b = __ldg(gtable + j);
+        bad |= (unsigned)b >= (unsigned)p.num_blocks;
+        if (near)
+            sm_table[j] = b;
     }
-    // of the keys equal to T the first ones: this warp's share of them
-    auto before_me = [&](int mine, int buf, int row) {
-        if (lane == 0)
-            part[buf][row][warp] = mine;
-        __syncthreads();
-        return __reduce_add_sync(FULL, lane < warp ? part[buf][row][lane] : 0);
+    for (int t = lo + tid; t < min(end, lo + p.keys); t += NTH)
+        keys[t - lo] = mass_key(__ldcg(mass + t));
+    if (__syncthreads_or(bad)) {                  // (the same in every block of the cluster)
+        if (tid == 0)
+            record_error(p.err, PA_DEVERR_TABLE_RANGE);
+        return;
+    }
+    const int32_t *table = near ? sm_table : gtable;
+    auto key_of = [&](int t) {                    // past the end 0, below every real key
+        return t >= end ? 0u : t - lo < p.keys ? keys[t - lo] : mass_key(__ldcg(mass + t));
     };
-    int ties = 0;
-    each([&](int t, uint32_t k) { ties += __popc(__ballot_sync(FULL, t < hi && k == T)); });
-    int quota = want - above - before_me(ties, 1, 0);
-    quota = want > 0 ? max(0, quota) : 0;
-    // kept(slot, key), to be asked in ascending order of the slots
+    auto each = [&](auto &&f) {                   // f(slot, key) over the warp's slots
+        for (int i = 0; i < steps; ++i) {
+            const int t = w0 + 32 * i + lane;
+            f(t, key_of(t));
+        }
+    };
+    // the want-th largest key, two bits at a time: how many keys reach each of three
+    // thresholds, until exactly `want` reach one
+    uint32_t T = want > 0 ? 0u : 0xffffffffu;
+    int4 all, before;
+    int reach = 0;
+    for (int bit = 30; want > 0 && bit >= 0 && reach != want; bit -= 2) {
+        const uint32_t t1 = T | 1u << bit, t2 = T | 2u << bit, t3 = T | 3u << bit;
+        int n1 = 0, n2 = 0, n3 = 0;
+        each([&](int, uint32_t k) {
+            n1 += k >= t1;
+            n2 += k >= t2;
+            n3 += k >= t3;
+        });
+        tally.sums(__reduce_add_sync(FULL, n1), __reduce_add_sync(FULL, n2),
+                   __reduce_add_sync(FULL, n3), all, before);
+        if (all.x >= want) {
+            T = all.z >= want ? t3 : all.y >= want ? t2 : t1;
+            reach = all.z >= want ? all.z : all.y >= want ? all.y : all.x;
+        }
+    }
+    // of the keys equal to T the first ones (all of them if just `want` reach it)
+    int quota = want > 0 ? INT_MAX : 0;
+    if (reach != want) {
+        int above = 0, ties = 0;
+        each([&](int t, uint32_t k) {
+            above += k > T;
+            ties += t < end && k == T;
+        });
+        tally.sums(__reduce_add_sync(FULL, above), __reduce_add_sync(FULL, ties), 0, all, before);
+        quota = max(0, want - all.x - before.y);
+    }
     int used = 0;
-    auto kept = [&](int t, uint32_t k) {
-        const unsigned tie = __ballot_sync(FULL, want > 0 && t < hi && k == T);
-        const bool in = want > 0 && t < hi &&
-                        (k > T || (k == T && used + __popc(tie & ((1u << lane) - 1)) < quota));
+    auto kept = [&](int t, uint32_t k) {          // asked in ascending order
+        const unsigned tie = __ballot_sync(FULL, t < end && k == T);
+        const bool in = t < end && (k > T || (k == T && used + __popc(tie & ((1u << lane) - 1)) < quota));
         used += __popc(tie);
         return in;
     };
     int holes = 0, movers = 0;
     each([&](int t, uint32_t k) {
         const bool in = kept(t, k);
-        holes += __popc(__ballot_sync(FULL, !in && t < edge));
+        holes += __popc(__ballot_sync(FULL, !in && t < min(edge, end)));
         movers += __popc(__ballot_sync(FULL, in && t >= edge));
     });
-    int hole = before_me(holes, 1, 1), mover = before_me(movers, 1, 2);
-    const int moves = __reduce_add_sync(FULL, part[1][2][lane]);
-    int32_t *to = p.lists + (size_t)run * 2 * p.list, *from = to + p.list;
+    tally.sums(holes, movers, 0, all, before);
+    const int moves = all.y;
+    int hole = before.x, mover = before.y;
+    const bool few = !CLUSTER && moves <= kEvictList;
+    int32_t *to = few ? sm_list : p.lists + (size_t)run * 2 * p.list;
+    int32_t *from = to + (few ? kEvictList : p.list);
     used = 0;
-    each([&](int t, uint32_t k) {
-        const bool in = kept(t, k);
-        const unsigned below = (1u << lane) - 1;
-        const unsigned hb = __ballot_sync(FULL, !in && t < edge);
-        const unsigned mb = __ballot_sync(FULL, in && t >= edge);
-        if (!in && t < edge)
-            to[hole + __popc(hb & below)] = t;
-        if (in && t >= edge)
-            from[mover + __popc(mb & below)] = t;
-        hole += __popc(hb);
-        mover += __popc(mb);
-    });
-    __syncthreads();
+    if (moves > 0)
+        each([&](int t, uint32_t k) {
+            const bool in = kept(t, k), is_hole = !in && t < min(edge, end), moving = in && t >= edge;
+            const unsigned below = (1u << lane) - 1;
+            const unsigned hb = __ballot_sync(FULL, is_hole), mb = __ballot_sync(FULL, moving);
+            if (is_hole)
+                to[hole + __popc(hb & below)] = t;
+            if (moving)
+                from[mover + __popc(mb & below)] = t;
+            hole += __popc(hb);
+            mover += __popc(mb);
+        });
+    tally.sync();
 
-    // a lane's 16 bytes of a token's K row or V row
+    // The moves, then the last ones' way down by L - B, in rounds that are loaded whole before
+    // they are stored: what a round writes lies before all that later rounds read.  A
+    // lane takes 16 bytes of a token's K row or V row.
     const int sub = lane / (2 * CPR), ch = lane % (2 * CPR);
     uint4 *pool = static_cast<uint4 *>(ch < CPR ? p.k_cache : p.v_cache) + ch % CPR;
     auto row_of = [&](int t) {
-        return pool + (((size_t)__ldg(table + t / kBlockSize) * Hkv + h) * kBlockSize +
-                       t % kBlockSize) * CPR;
+        return pool + (((size_t)table[t / kBlockSize] * Hkv + h) * kBlockSize + t % kBlockSize) * CPR;
     };
-    for (int base = warp * RPW + sub; base < moves; base += NW * RPW * U) {
+    const int per = C * NW * RPW;                 // tokens the run's warps take at once
+    const int mine = (rank * NW + warp) * RPW + sub;
+    for (int base = 0; base < moves + R; base += per * U) {
         uint4 x[U];
         float m[U];
+        int dst[U];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            const int j = base + i * NW * RPW;
-            if (j < moves) {
-                const int t = __ldcg(from + j);
-                x[i] = __ldcg(row_of(t));
+            const int j = base + i * per + mine;
+            dst[i] = -1;
+            if (j < moves + R) {
+                const int src = j < moves ? from[j] : hi + j - moves;
+                dst[i] = j < moves ? to[j] : edge + j - moves;
+                x[i] = __ldcg(row_of(src));
                 if (ch == 0)
-                    m[i] = __ldcg(mass + t);
+                    m[i] = __ldcg(mass + src);
             }
         }
+        if (base + per * U > moves)               // the last ones: their places may be read here
+            tally.sync();
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int j = base + i * NW * RPW;
-            if (j < moves) {
-                const int t = __ldcg(to + j);
-                *row_of(t) = x[i];
+        for (int i = 0; i < U; ++i)
+            if (dst[i] >= 0) {
+                *row_of(dst[i]) = x[i];
                 if (ch == 0)
-                    mass[t] = m[i];
+                    mass[dst[i]] = m[i];
             }
-        }
     }
-    // The last ones move down by L - B.  Rounds in ascending order, each loaded whole before
-    // it is stored: a round's destinations lie before every later round's sources.
-    __syncthreads();
-    for (int base = 0; base < R; base += NW * RPW * U) {
-        uint4 x[U];
-        float m[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int j = base + (i * NW + warp) * RPW + sub;
-            if (j < R) {
-                x[i] = __ldcg(row_of(hi + j));
-                if (ch == 0)
-                    m[i] = __ldcg(mass + hi + j);
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int j = base + (i * NW + warp) * RPW + sub;
-            if (j < R) {
-                *row_of(edge + j) = x[i];
-                if (ch == 0)
-                    mass[edge + j] = m[i];
-            }
-        }
-    }
+    tally.leave();
 }
+
+constexpr int kEvictKeys = 32768;                 // keys a block holds (128 KB)
+constexpr int kEvictTable = 8192;                 // table entries a block holds (32 KB)
 
 }  // namespace
 
-SparseKernel evict_kernel(int head_dim)
+// Short tables: a block of 128 threads a run.  Others: 256 threads, and where the runs leave
+// SMs idle a cluster of 2, 4 or 8 blocks shares a run, 1024 slots a block at least.
+EvictLaunch evict_launch(int head_dim, int num_runs, int max_blocks, int num_sms)
 {
-    return SparseKernel{head_dim == 128
-                            ? reinterpret_cast<const void *>(&evict_kernel_t<128>)
-                            : reinterpret_cast<const void *>(&evict_kernel_t<64>),
-                        kEvictThreads};
+    EvictLaunch e{};
+    const long long slots = (long long)max_blocks * kBlockSize;
+    const bool small = slots <= 2048;
+    e.threads = small ? 128 : 256;
+    e.cluster = 1;
+    while (!small && e.cluster < 8 && 2LL * e.cluster * num_runs <= 4LL * num_sms &&
+           slots >= 2048LL * e.cluster)
+        e.cluster *= 2;
+    if (small)
+        e.fn = head_dim == 128 ? reinterpret_cast<const void *>(&evict_kernel_t<128, 128, false>)
+                               : reinterpret_cast<const void *>(&evict_kernel_t<64, 128, false>);
+    else
+        e.fn = head_dim == 128 ? reinterpret_cast<const void *>(&evict_kernel_t<128, 256, true>)
+                               : reinterpret_cast<const void *>(&evict_kernel_t<64, 256, true>);
+    const long long share = (slots + (long long)e.cluster * e.threads - 1) /
+                            ((long long)e.cluster * e.threads) * e.threads;
+    e.keys = (int)(share < kEvictKeys ? share : kEvictKeys);
+    e.table = max_blocks <= kEvictTable ? max_blocks : 0;
+    e.smem = 4 * ((size_t)e.keys + e.table + 2 * kEvictList);
+    return e;
 }
 
 }  // namespace pa

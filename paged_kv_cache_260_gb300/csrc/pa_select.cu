@@ -8,6 +8,7 @@
 #include "pa_device.cuh"
 #include "pa_ragged.cuh"
 #include "pa_sparse.h"
+#include "pa_tally.cuh"
 
 namespace pa {
 
@@ -152,109 +153,151 @@ __global__ void __launch_bounds__(kBoundsThreads) block_bounds_kernel(const Boun
 }
 
 // ---------------------------------------------------------------------------
-// The score of a block is the largest q.k that its bounds allow, the greatest
-// of the group's heads:
+// The choice of blocks.  The score of a block is the largest q.k that its
+// bounds allow, the greatest of the group's heads:
 //     score_j = max_g sum_c max(q_gc min_jc, q_gc max_jc)
 //             = max_g (max(q_g, 0) . max_j + min(q_g, 0) . min_j),
 // a matrix product over 2 head_dim channels.  A warp takes 16 blocks (rows of
 // the A operand), the group's heads are the columns.  The channels of a product
 // may be taken in any order, so a lane loads 16 bytes of a row at a time
 // straight into its fragments (8 neighbouring channels, as two k-steps of four)
-// and the queries are laid out to match; no shared memory.
+// and the queries are laid out to match.
+//
+// Per (sequence, kv head) the keep_first first blocks, the keep_last last ones and
+// the best of the rest are kept.  The tensor cores' sums are off by a part of
+// sum |q||bound|, and the choice must not depend on that: with E the largest
+// error and T the lowest chosen score, a block whose score lies above T + 2 E is
+// in, one below T - 2 E is out, and the few between are summed again in pairs of
+// floats (46 bits) and ranked by that, ties to the lowest position.
+//
+// One thread block takes a (sequence, kv head), or a cluster of blocks a contiguous
+// part of its blocks each (CLUSTER); the scores stay in shared memory (in the
+// workspace, where a block's part is larger than p.near).
 // ---------------------------------------------------------------------------
-constexpr int kScoreThreads = 128;
+constexpr int kDoubt = 256;                       // blocks in doubt that are ranked directly
+constexpr int kSelectNear = 32768;                // scores a block holds (128 KB)
 
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kScoreThreads) block_score_kernel_t(const SelectParams p)
+// The order of floats as unsigned numbers (-0 as 0), and back.
+__device__ __forceinline__ uint32_t ordered(float x)
+{
+    const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ float from_ordered(uint32_t k)
+{
+    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+// (s, e) += x without loss of what falls off s
+__device__ __forceinline__ void two_add(float &s, float &e, float x)
+{
+    const float t = __fadd_rn(s, x), b = __fsub_rn(t, s);
+    e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(x, b)));
+    s = t;
+}
+
+template <typename T, int D, int NT, int NTH, bool CLUSTER>
+__global__ void __launch_bounds__(NTH, 512 / NTH) block_select_kernel_t(const SelectParams p)
 {
     using M = Mma<T>;
     constexpr uint32_t FULL = 0xffffffffu;
+    constexpr int NW = NTH / 32;
     constexpr int NI = D / 32;                    // 16-byte loads of a row's minima (maxima)
-    __shared__ RaggedSmem sm;
-    const int lane = threadIdx.x & 31;
-    const int warps = gridDim.x * (kScoreThreads / 32);
-    const int me = blockIdx.x * (kScoreThreads / 32) + (threadIdx.x >> 5);
+    extern __shared__ float near_scores[];
+    __shared__ float q[8 * NT * D];               // the group's queries
+    __shared__ unsigned long long near_keys[CLUSTER ? 1 : kDoubt];
+    __shared__ TallySmem<NW> counts;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int Hkv = p.num_kv_heads, G = p.num_heads / Hkv;
-    const int r = lane >> 2, qd = lane & 3;
+    Tally<NW, CLUSTER> tally(counts);
+    const int C = tally.blocks, rank = tally.rank;
+    const int run = blockIdx.x / C, s = run / Hkv, h = run % Hkv;
     grid_dependents_launch();
     grid_dependency_wait();
-    for (int begin = 0; begin < p.num_seqs; begin += kRaggedSeqs) {
-        const int n = min(kRaggedSeqs, p.num_seqs - begin);
-        ragged_prefix<kScoreThreads>(sm, begin, n, [&](int s) {
-            const int L = checked_len(p.seq_lens, s, p.max_blocks, p.err);
-            const int nb = (L + kBlockSize - 1) / kBlockSize;
-            return nb <= p.keep ? 0 : (nb + 15) / 16;   // all are kept: no scores wanted
-        });
-        const long long total = (long long)sm.pre[n] * Hkv;
-        const long long share = (total + warps - 1) / warps;
-        long long u = me * share;
-        const long long end = min(total, u + share);
-        if (u >= end)
-            continue;
-        int i = ragged_find(sm, n, (int)(u / Hkv));
-        int nt = sm.pre[i + 1] - sm.pre[i];
-        int h = (int)((u - (long long)sm.pre[i] * Hkv) / nt);
-        int t = (int)((u - (long long)sm.pre[i] * Hkv) % nt);
-        bool fresh = true;
+    int L = __ldg(p.seq_lens + s);
+    if (L < 0 || L > p.max_blocks * kBlockSize) {
+        if (tid == 0)
+            record_error(p.err, PA_DEVERR_SEQLEN_RANGE);
+        L = L < 0 ? 0 : p.max_blocks * kBlockSize;
+    }
+    const int nb = (L + kBlockSize - 1) / kBlockSize;
+    const int32_t *table = p.block_tables + (size_t)s * p.max_blocks;
+    int32_t *out = p.tiles + (size_t)run * p.keep;
+    // the pool tile of block j; a bad entry counts as block 0
+    auto tile_of = [&](int j) {
+        int phys = __ldg(table + j);
+        if ((unsigned)phys >= (unsigned)p.num_blocks) {
+            record_error(p.err, PA_DEVERR_TABLE_RANGE);
+            phys = 0;
+        }
+        return phys * Hkv + h;
+    };
+    if (tid == 0 && rank == 0)
+        p.tile_lens[run] = L - kBlockSize * max(0, nb - p.keep);
+    if (nb <= p.keep) {
+        for (int j = rank * NTH + tid; j < p.keep; j += C * NTH)
+            out[j] = j < nb ? tile_of(j) : -1;
+        return;
+    }
+    const int lo = p.keep_first, hi = nb - p.keep_last;   // the blocks that compete
+    int want = p.keep - p.keep_first - p.keep_last;       // how many of them are kept
+
+    // ---- scores of this thread block's part [b0, b1) ----
+    const int span = (nb + 16 * C - 1) / (16 * C) * 16;
+    const int b0 = min(nb, rank * span), b1 = min(nb, b0 + span);
+    float *score = (p.near >= span ? near_scores : p.scores + (size_t)run * p.row + b0) - b0;
+    const T *qg = static_cast<const T *>(p.q) + ((size_t)s * p.num_heads + h * G) * D;
+    const int r = lane >> 2, qd = lane & 3;
+    uint32_t big = 0;                             // the largest |bound|
+    {
         uint32_t qn[NT][NI][4], qp[NT][NI][4];    // min(q, 0) and max(q, 0)
-        int nb = 0;
-        for (; u < end; ++u) {
-            const int s = begin + i;
-            if (fresh) {
-                fresh = false;
-                const int L = min(max(__ldg(p.seq_lens + s), 0), p.max_blocks * kBlockSize);
-                nb = (L + kBlockSize - 1) / kBlockSize;
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const int g = 8 * j + r;
-                    const uint4 *src = reinterpret_cast<const uint4 *>(
-                        static_cast<const T *>(p.q) +
-                        ((size_t)s * p.num_heads + h * G + min(g, G - 1)) * D);
+        for (int j = 0; j < NT; ++j) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(qg + min(8 * j + r, G - 1) * D);
 #pragma unroll
-                    for (int k = 0; k < NI; ++k) {
-                        const uint4 x = __ldg(src + 4 * k + qd);
-                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            for (int k = 0; k < NI; ++k) {
+                const uint4 x = __ldg(src + 4 * k + qd);
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            qn[j][k][e] = min2<T>(w[e], 0u);
-                            qp[j][k][e] = max2<T>(w[e], 0u);
-                        }
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    qn[j][k][e] = min2<T>(w[e], 0u);
+                    qp[j][k][e] = max2<T>(w[e], 0u);
                 }
             }
-            // rows r and r + 8 of the 16 blocks; past the end the last block again
-            const int32_t *table = p.block_tables + (size_t)s * p.max_blocks;
-            const uint4 *row[2];
-#pragma unroll
-            for (int a = 0; a < 2; ++a) {
-                int phys = __ldg(table + min(16 * t + 8 * a + r, nb - 1));
-                if ((unsigned)phys >= (unsigned)p.num_blocks) {
-                    record_error(p.err, PA_DEVERR_TABLE_RANGE);
-                    phys = 0;
-                }
-                row[a] = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.bounds) +
-                                                         ((size_t)phys * Hkv + h) * 2 * D) + qd;
-            }
+        }
+        // rows r and r + 8 of the next 16 blocks; past the end the last block again
+        auto rows = [&](int b, int (&tile)[2]) {
+            tile[0] = tile_of(min(b + r, nb - 1));
+            tile[1] = tile_of(min(b + 8 + r, nb - 1));
+        };
+        int tile[2] = {0, 0};
+        if (b0 + 16 * warp < b1)
+            rows(b0 + 16 * warp, tile);
+        for (int b = b0 + 16 * warp; b < b1; b += 16 * NW) {
             uint4 x[2][2 * NI];
 #pragma unroll
             for (int k = 0; k < 2 * NI; ++k)
 #pragma unroll
                 for (int a = 0; a < 2; ++a)
-                    x[a][k] = __ldg(row[a] + 4 * k);
+                    x[a][k] = __ldg(reinterpret_cast<const uint4 *>(
+                                        static_cast<const T *>(p.bounds) + (size_t)tile[a] * 2 * D) +
+                                    4 * k + qd);
+            if (b + 16 * NW < b1)
+                rows(b + 16 * NW, tile);
             float acc[NT][4];
 #pragma unroll
             for (int j = 0; j < NT; ++j)
                 acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-            uint32_t big = 0;
 #pragma unroll
             for (int k = 0; k < 2 * NI; ++k) {
                 const uint32_t a0[4] = {x[0][k].x, x[1][k].x, x[0][k].y, x[1][k].y};
                 const uint32_t a1[4] = {x[0][k].z, x[1][k].z, x[0][k].w, x[1][k].w};
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    const uint32_t *q = k < NI ? qn[j][k] : qp[j][k - NI];
-                    M::run(acc[j], a0, q[0], q[1]);
-                    M::run(acc[j], a1, q[2], q[3]);
+                    const uint32_t *qq = k < NI ? qn[j][k] : qp[j][k - NI];
+                    M::run(acc[j], a0, qq[0], qq[1]);
+                    M::run(acc[j], a1, qq[2], qq[3]);
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -277,380 +320,233 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel_t(const Sele
                 best[0] = fmaxf(best[0], __shfl_xor_sync(FULL, best[0], off));
                 best[1] = fmaxf(best[1], __shfl_xor_sync(FULL, best[1], off));
             }
-            const float2 b2 = Elem<T>::to_f2(big);
-            float reach = fmaxf(b2.x, b2.y);
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1)
-                reach = fmaxf(reach, __shfl_xor_sync(FULL, reach, off));
-            const size_t out = ((size_t)s * Hkv + h) * p.row + 16 * t;
-            if (qd < 2 && 16 * t + 8 * qd + r < nb)
-                p.scores[out + 8 * qd + r] = best[qd];
-            if (lane == 0)
-                p.reach[out / 16] = reach;
-            if (++t == nt) {
-                t = 0;
-                fresh = true;
-                if (++h == Hkv) {
-                    h = 0;
-                    do
-                        ++i;
-                    while (i < n && sm.pre[i + 1] == sm.pre[i]);
-                    if (i < n)
-                        nt = sm.pre[i + 1] - sm.pre[i];
-                }
-            }
+            const int j = b + 8 * qd + r;
+            if (qd < 2 && j < b1)
+                score[j] = qd ? best[1] : best[0];
         }
     }
-}
-
-// ---------------------------------------------------------------------------
-// The choice: per (sequence, kv head) the keep_first first blocks, the keep_last
-// last ones and the best of the rest.  The tensor cores' sums are off by a part
-// of sum |q||bound|, and the choice must not depend on that: with E the largest
-// error, a block whose score lies more than 2 E above the lowest chosen one is
-// in, one that lies more than 2 E below is out, and the few between are
-// summed again in pairs of floats (46 bits) and ranked by that, ties to the lowest
-// position.
-// ---------------------------------------------------------------------------
-constexpr int kSelectThreads = 512;
-constexpr int kSelectBins = 2048;
-constexpr int kDoubt = 512;                       // blocks in doubt that are ranked directly
-
-// The order of floats as unsigned numbers (-0 as 0).
-__device__ __forceinline__ uint32_t ordered(float x)
-{
-    const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-
-// (s, e) += x without loss of what falls off s
-__device__ __forceinline__ void two_add(float &s, float &e, float x)
-{
-    const float t = __fadd_rn(s, x), b = __fsub_rn(t, s);
-    e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(x, b)));
-    s = t;
-}
-
-template <typename T, int D>
-__global__ void __launch_bounds__(kSelectThreads) block_select_kernel_t(const SelectParams p)
-{
-    constexpr int NTH = kSelectThreads, NW = NTH / 32;
-    constexpr uint32_t FULL = 0xffffffffu;
-    __shared__ float q[kMaxGroup * D];            // the group's queries
-    __shared__ int hist[kSelectBins];
-    __shared__ int doubt[kDoubt];
-    __shared__ unsigned long long key[kDoubt];
-    __shared__ float red[3][NW];
-    __shared__ int redi[2][NW];
-    __shared__ int count[2];                      // blocks in doubt, and above them
-    __shared__ int found;                         // the lowest chosen one's bin
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int Hkv = p.num_kv_heads, G = p.num_heads / Hkv;
-    const int run = blockIdx.x, s = run / Hkv, h = run % Hkv;
-    grid_dependents_launch();
-    grid_dependency_wait();
-    int L = __ldg(p.seq_lens + s);
-    if (L < 0 || L > p.max_blocks * kBlockSize) {
-        if (tid == 0)
-            record_error(p.err, PA_DEVERR_SEQLEN_RANGE);
-        L = L < 0 ? 0 : p.max_blocks * kBlockSize;
-    }
-    const int nb = (L + kBlockSize - 1) / kBlockSize;
-    const int32_t *table = p.block_tables + (size_t)s * p.max_blocks;
-    int32_t *out = p.tiles + (size_t)run * p.keep;
-    auto tile_of = [&](int j) {
-        const int phys = __ldg(table + j);
-        if ((unsigned)phys >= (unsigned)p.num_blocks) {
-            record_error(p.err, PA_DEVERR_TABLE_RANGE);
-            return h;                             // block 0's tile, as the score was taken
-        }
-        return phys * Hkv + h;
-    };
-    if (tid == 0)
-        p.tile_lens[run] = L - kBlockSize * max(0, nb - p.keep);
-    if (nb <= p.keep) {
-        for (int j = tid; j < p.keep; j += NTH)
-            out[j] = j < nb ? tile_of(j) : -1;
-        return;
-    }
-    const int lo = p.keep_first, hi = nb - p.keep_last;   // the blocks that compete
-    int want = p.keep - p.keep_first - p.keep_last;       // how many of them are kept
-    float *score = p.scores + (size_t)run * p.row;
-    const float *reach = p.reach + (size_t)run * (p.row / 16);
-
-    // queries, their largest sum of magnitudes, the largest |bound|, the scores' range
+    // ---- the queries, for those that are summed again, and their sums of magnitudes ----
     for (int i = tid; i < G * D; i += NTH)
-        q[i] = Elem<T>::to_f(static_cast<const T *>(p.q)[((size_t)s * p.num_heads + h * G) * D + i]);
-    for (int i = tid; i < kSelectBins; i += NTH)
-        hist[i] = 0;
-    if (tid < 2)
-        count[tid] = 0;
+        q[i] = Elem<T>::to_f(qg[i]);
     __syncthreads();
-    float most = 0.f, least_s = INFINITY, most_s = -INFINITY;
-    int first_of_all = 0;                         // scores that are not finite
-    for (int i = tid; i < (nb + 15) / 16; i += NTH)
-        most = fmaxf(most, __ldcg(reach + i));
-    for (int j = lo + tid; j < hi; j += NTH) {
-        const float x = __ldcg(score + j);
-        if (x == INFINITY) {
-            ++first_of_all;
-        } else {
-            least_s = fminf(least_s, x);
-            most_s = fmaxf(most_s, x);
-        }
-    }
     float l1 = 0.f;
     for (int g = warp; g < G; g += NW) {
         float a = 0.f;
-        for (int c = lane; c < D; c += 32)
-            a += fabsf(q[g * D + c]);
+#pragma unroll
+        for (int c = 0; c < D; c += 32)
+            a += fabsf(q[g * D + c + lane]);
 #pragma unroll
         for (int off = 16; off; off >>= 1)
             a += __shfl_xor_sync(FULL, a, off);
         l1 = fmaxf(l1, a);
     }
-#pragma unroll
-    for (int off = 16; off; off >>= 1) {
-        most = fmaxf(most, __shfl_xor_sync(FULL, most, off));
-        least_s = fminf(least_s, __shfl_xor_sync(FULL, least_s, off));
-        most_s = fmaxf(most_s, __shfl_xor_sync(FULL, most_s, off));
-    }
-    first_of_all = __reduce_add_sync(FULL, first_of_all);
-    if (lane == 0) {
-        red[0][warp] = most;
-        red[1][warp] = least_s;
-        red[2][warp] = most_s;
-        redi[0][warp] = first_of_all;
-        redi[1][warp] = __float_as_int(l1);       // not negative: ordered as an int
-    }
-    __syncthreads();
-    first_of_all = 0;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-        most = fmaxf(most, red[0][w]);
-        least_s = fminf(least_s, red[1][w]);
-        most_s = fmaxf(most_s, red[2][w]);
-        first_of_all += redi[0][w];
-        l1 = fmaxf(l1, __int_as_float(redi[1][w]));
-    }
-    // Largest error: 2 D / 16 steps each add 17 terms aligned to the largest, none above
-    // sum |q||bound| <= l1 * most, and lose 2^-23 of it a term
-    // (infinite bounds put everything in doubt)
-    const float twice = 2.f * (2 * D / 16) * 17 * 1.1920929e-7f * l1 * most;
-    const float slack = twice <= FLT_MAX ? twice : FLT_MAX;
-    // scores that are not finite rank first: all of them, or the foremost
-    int inf_left = min(first_of_all, want);
-    want -= inf_left;
-    // bins of equal width over the finite scores; the bin rises with the score
-    const float width = (most_s - least_s) / kSelectBins;
-    const float per = width > 0.f ? 1.f / width : 0.f;
-    auto bin_of = [&](float x) {
-        const float b = (x - least_s) * per;
-        return b >= (float)(kSelectBins - 1) ? kSelectBins - 1 : b > 0.f ? (int)b : 0;
+    // a warp's contiguous part of the blocks that compete: [w0, ..) in `steps` steps of 32
+    const int c0 = min(max(b0, lo), hi), c1 = max(c0, min(b1, hi));
+    const int steps = (c1 - c0 + NTH - 1) / NTH;
+    const int w0 = c0 + warp * steps * 32;
+    auto each = [&](auto &&f) {                   // f(block, score), -inf past the end
+        for (int i = 0; i < steps; ++i) {
+            const int j = w0 + 32 * i + lane;
+            f(j, j < c1 ? score[j] : -INFINITY);
+        }
     };
-    int cut = kSelectBins;                        // no bin lies above: none is kept
+    const float2 b2 = Elem<T>::to_f2(big);
+    uint32_t least = 0, most = 0;                 // of the finite scores, least upside down
+    int infs = 0;                                 // those that are not rank first
+    each([&](int j, float x) {
+        if (j < c1 && x != INFINITY) {
+            least = max(least, ~ordered(x));
+            most = max(most, ordered(x));
+        }
+        infs += x == INFINITY;
+    });
+    int4 all, before;
+    tally.sums(__reduce_add_sync(FULL, infs), 0, 0, all, before);
+    int inf_left = min(all.x, want);              // so many of them, the foremost
+    const int inf_before = before.x;
+    want -= inf_left;
+    const uint3 range = tally.most(least, most, __float_as_uint(fmaxf(b2.x, b2.y)));
+    const uint3 sizes = tally.most(__float_as_uint(l1), 0, 0);
+    // Largest error: 2 D / 16 steps each add 17 terms aligned to the largest, none above
+    // sum |q||bound| <= l1 * reach, and lose 2^-23 of it a term (infinite bounds put
+    // everything in doubt)
+    const float twice = 2.f * (2 * D / 16) * 17 * 1.1920929e-7f * __uint_as_float(sizes.x) *
+                        __uint_as_float(range.z);
+    const float slack = twice <= FLT_MAX ? twice : FLT_MAX;
+
+    // ---- T, the want-th largest score, two bits at a time from the first in which scores
+    // differ; just `want` scores reach it, or it is exact ----
+    float edge = INFINITY;                        // nothing lies above: none is kept
     if (want > 0) {
-        for (int j = lo + tid; j < hi; j += NTH) {
-            const float x = __ldcg(score + j);
-            if (x != INFINITY)
-                atomicAdd(&hist[bin_of(x)], 1);
-        }
-        __syncthreads();
-        // the bin of the want-th largest: each thread sums its bins, the warps' sums are
-        // scanned from the top
-        constexpr int BPT = kSelectBins / NTH;
-        int mine = 0;
-#pragma unroll
-        for (int b = 0; b < BPT; ++b)
-            mine += hist[kSelectBins - 1 - (tid * BPT + b)];
-        int incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(FULL, incl, o);
-            if (lane >= o)
-                incl += y;
-        }
-        if (lane == 31)
-            redi[0][warp] = incl;
-        __syncthreads();
-        int above = incl - mine;
-        for (int w = 0; w < warp; ++w)
-            above += redi[0][w];
-        if (above < want && above + mine >= want) {
-            int b = 0;
-            for (; b < BPT - 1 && above + hist[kSelectBins - 1 - (tid * BPT + b)] < want; ++b)
-                above += hist[kSelectBins - 1 - (tid * BPT + b)];
-            found = kSelectBins - 1 - (tid * BPT + b);
-        }
-        __syncthreads();
-        cut = found;
-        // in, out, or in doubt
-        int sure = 0;
-        for (int j = lo + tid; j < hi; j += NTH) {
-            const float x = __ldcg(score + j);
-            if (x == INFINITY)
-                continue;
-            if (bin_of(x - slack) > cut) {
-                ++sure;
-            } else if (bin_of(x + slack) >= cut) {
-                const int at = atomicAdd(&count[0], 1);
-                if (at < kDoubt)
-                    doubt[at] = j;
+        const uint32_t least_key = ~range.x;
+        int bit = least_key == range.y ? -2 : (31 - __clz(least_key ^ range.y)) & ~1;
+        uint32_t t = bit < 0 ? range.y : range.y & ~((4u << bit) - 1u);
+        int reach = 0;
+        for (; bit >= 0 && reach != want; bit -= 2) {
+            const uint32_t t1 = t | 1u << bit, t2 = t | 2u << bit, t3 = t | 3u << bit;
+            int n1 = 0, n2 = 0, n3 = 0;
+            each([&](int j, float x) {
+                const uint32_t k = j < c1 && x != INFINITY ? ordered(x) : 0u;
+                n1 += k >= t1;
+                n2 += k >= t2;
+                n3 += k >= t3;
+            });
+            tally.sums(__reduce_add_sync(FULL, n1), __reduce_add_sync(FULL, n2),
+                       __reduce_add_sync(FULL, n3), all, before);
+            if (all.x >= want) {
+                t = all.z >= want ? t3 : all.y >= want ? t2 : t1;
+                reach = all.z >= want ? all.z : all.y >= want ? all.y : all.x;
             }
         }
-        sure = __reduce_add_sync(FULL, sure);
-        if (lane == 0 && sure)
-            atomicAdd(&count[1], sure);
-        __syncthreads();
-        const int need = want - count[1];
-        const int c = count[0];
-        // the score of block j by the warp, as an ordered number of 64 bits
-        auto resum = [&](int j) {
-            const int phys = __ldg(table + j);
-            const T *b = static_cast<const T *>(p.bounds) +
-                         ((size_t)((unsigned)phys < (unsigned)p.num_blocks ? phys : 0) * Hkv + h) *
-                             2 * D;
-            unsigned long long best = 0;
-            for (int g = 0; g < G; ++g) {
-                float a = 0.f, e = 0.f;
-#pragma unroll
-                for (int cc = 0; cc < D; cc += 32) {
-                    const float qc = q[g * D + cc + lane];
-                    const float k = Elem<T>::to_f(b[(qc > 0.f ? D : 0) + cc + lane]);
-                    two_add(a, e, qc * k);        // an exact product
-                }
-#pragma unroll
-                for (int off = 16; off; off >>= 1) {
-                    const float oa = __shfl_xor_sync(FULL, a, off);
-                    const float oe = __shfl_xor_sync(FULL, e, off);
-                    two_add(a, e, oa);
-                    e += oe;
-                }
-                const float x = __fadd_rn(a, e), rest = __fsub_rn(e, __fsub_rn(x, a));
-                const unsigned long long kk =
-                    (unsigned long long)ordered(x) << 32 | ordered(rest);
-                best = kk > best ? kk : best;
-            }
-            return __shfl_sync(FULL, best, 0);
-        };
-        if (c <= kDoubt) {
-            for (int i = warp; i < c; i += NW) {
-                const unsigned long long k = resum(doubt[i]);
-                if (lane == 0)
-                    key[i] = k;
-            }
-            __syncthreads();
-            for (int i = tid; i < c; i += NTH) {
-                const unsigned long long k = key[i];
-                const int j = doubt[i];
-                int better = 0;
-                for (int o = 0; o < c; ++o)
-                    better += key[o] > k || (key[o] == k && doubt[o] < j);
-                // what is in stands at the top of its bins from here on, what is out at the bottom
-                score[j] = better < need ? FLT_MAX : -FLT_MAX;
-            }
+        // the lowest chosen score itself: just `want` reach t, or it is t
+        uint32_t lowest = 0;                      // upside down
+        each([&](int j, float x) {
+            if (j < c1 && x != INFINITY && ordered(x) >= t)
+                lowest = max(lowest, ~ordered(x));
+        });
+        edge = from_ordered(~tally.most(lowest, 0, 0).x);
+
+        // ---- in, out, or in doubt ----
+        auto doubtful = [&](float x) { return x != INFINITY && x - slack <= edge && x + slack >= edge; };
+        int sure = 0, doubts = 0;
+        each([&](int j, float x) {
+            sure += j < c1 && x != INFINITY && x - slack > edge;
+            doubts += j < c1 && doubtful(x);
+        });
+        tally.sums(__reduce_add_sync(FULL, sure), __reduce_add_sync(FULL, doubts), 0, all, before);
+        const int need = want - all.x, total = all.y, mine = before.y;
+        if (need == total) {
+            // all of them: no sums wanted
+            each([&](int j, float x) {
+                if (j < c1 && doubtful(x))
+                    score[j] = FLT_MAX;
+            });
         } else {
-            // very many scores close together (equal blocks): the need-th largest key bit
-            // by bit
-            unsigned long long *keys = p.exact + (size_t)run * p.row;
-            auto doubtful = [&](float x) {
-                return x != INFINITY && bin_of(x - slack) <= cut && bin_of(x + slack) >= cut;
-            };
-            for (int j = lo + warp; j < hi; j += NW) {
-                unsigned long long k = 0;
-                if (doubtful(__ldcg(score + j)))
-                    k = resum(j);
-                if (lane == 0)
-                    keys[j] = k;
-            }
-            __syncthreads();
-            unsigned long long edge = 0;
-            auto tally = [&](unsigned long long at_least) {
-                int m = 0;
-                for (int j = lo + tid; j < hi; j += NTH)
-                    m += __ldcg(keys + j) >= at_least;
-                m = __reduce_add_sync(FULL, m);
-                if (lane == 0)
-                    redi[1][warp] = m;
-                __syncthreads();
-                m = 0;
+            // the score of block j by the warp, as an ordered number of 64 bits
+            auto resum = [&](int j) {
+                const T *b = static_cast<const T *>(p.bounds) + (size_t)tile_of(j) * 2 * D;
+                unsigned long long best = 0;
+                for (int g = 0; g < G; ++g) {
+                    float a = 0.f, e = 0.f;
 #pragma unroll
-                for (int w = 0; w < NW; ++w)
-                    m += redi[1][w];
-                __syncthreads();
-                return m;
-            };
-            for (int bit = 63; bit >= 0; --bit)
-                if (tally(edge | 1ull << bit) >= need)
-                    edge |= 1ull << bit;
-            // of those at the edge the first ones
-            int left = need - tally(edge + 1);
-            for (int base = lo; base < hi; base += NTH) {
-                const int j = base + tid;
-                const unsigned long long k = j < hi ? __ldcg(keys + j) : 0;
-                const bool tie = j < hi && k == edge;
-                const unsigned ballot = __ballot_sync(FULL, tie);
-                if (lane == 0)
-                    redi[1][warp] = __popc(ballot);
-                __syncthreads();
-                int before = 0, all = 0;
+                    for (int cc = 0; cc < D; cc += 32) {
+                        const float qc = q[g * D + cc + lane];
+                        const float k = Elem<T>::to_f(b[(qc > 0.f ? D : 0) + cc + lane]);
+                        two_add(a, e, qc * k);    // an exact product
+                    }
 #pragma unroll
-                for (int w = 0; w < NW; ++w) {
-                    before += w < warp ? redi[1][w] : 0;
-                    all += redi[1][w];
+                    for (int off = 16; off; off >>= 1) {
+                        const float oa = __shfl_xor_sync(FULL, a, off);
+                        const float oe = __shfl_xor_sync(FULL, e, off);
+                        two_add(a, e, oa);
+                        e = __fadd_rn(e, oe);
+                    }
+                    const float x = __fadd_rn(a, e), rest = __fsub_rn(e, __fsub_rn(x, a));
+                    const unsigned long long kk =
+                        (unsigned long long)ordered(x) << 32 | ordered(rest);
+                    best = kk > best ? kk : best;
                 }
-                if (j < hi && k)
-                    score[j] = k > edge || (tie && before + __popc(ballot & ((1u << lane) - 1)) < left)
-                                   ? FLT_MAX
-                                   : -FLT_MAX;
-                left -= min(left, all);
-                __syncthreads();
-            }
-        }
-    }
-    __syncthreads();                              // the scores' marks
-    // the kept blocks in their order
-    int at = 0;
-    for (int base = 0; base < nb; base += NTH) {
-        const int j = base + tid;
-        bool in = false, inf = false;
-        if (j < nb) {
-            if (j < lo || j >= hi) {
-                in = true;
+                // (the lanes' sums differ in their last bits: the order of their terms does)
+                return __shfl_sync(FULL, best, 0);
+            };
+            // their keys in the order of their positions; key i of the run is in list[i]
+            unsigned long long *list =
+                !CLUSTER && total <= kDoubt ? near_keys : p.exact + (size_t)run * p.row;
+            int at = mine;
+            each([&](int j, float x) {
+                unsigned m = __ballot_sync(FULL, j < c1 && doubtful(x));
+                for (; m; m &= m - 1) {
+                    const int l = __ffs(m) - 1;
+                    const unsigned long long k = resum(j - lane + l);
+                    if (lane == 0)
+                        list[at] = k;
+                    ++at;
+                }
+            });
+            const int end = at;
+            tally.sync();
+            if (total <= kDoubt) {
+                // rank each among all
+                at = mine;
+                each([&](int j, float x) {
+                    unsigned m = __ballot_sync(FULL, j < c1 && doubtful(x));
+                    float mark = x;
+                    for (; m; m &= m - 1, ++at) {
+                        const unsigned long long k = list[at];
+                        int better = 0;
+                        for (int o = lane; o < total; o += 32)
+                            better += list[o] > k || (list[o] == k && o < at);
+                        better = __reduce_add_sync(FULL, better);
+                        if (lane == __ffs(m) - 1)
+                            mark = better < need ? FLT_MAX : -FLT_MAX;
+                    }
+                    if (j < c1)
+                        score[j] = mark;
+                });
             } else {
-                const float x = __ldcg(score + j);
-                inf = x == INFINITY;
-                in = !inf && want > 0 && (x == FLT_MAX || (x != -FLT_MAX && bin_of(x - slack) > cut));
+                // very many scores close together (equal blocks): the need-th largest key, two
+                // bits at a time
+                unsigned long long t64 = 0;
+                auto count = [&](unsigned long long at_least) {
+                    int n = 0;
+                    for (int i = mine + lane; i < end; i += 32)
+                        n += list[i] >= at_least;
+                    return __reduce_add_sync(FULL, n);
+                };
+                for (int bit64 = 62; bit64 >= 0; bit64 -= 2) {
+                    const unsigned long long t1 = t64 | 1ull << bit64, t2 = t64 | 2ull << bit64,
+                                             t3 = t64 | 3ull << bit64;
+                    tally.sums(count(t1), count(t2), count(t3), all, before);
+                    t64 = all.z >= need ? t3 : all.y >= need ? t2 : all.x >= need ? t1 : t64;
+                }
+                // of those equal to it the first ones
+                const int above = t64 == ~0ull ? 0 : count(t64 + 1);
+                tally.sums(above, count(t64) - above, 0, all, before);
+                int quota = need - all.x - before.y;
+                at = mine;
+                each([&](int j, float x) {
+                    const bool on = j < c1 && doubtful(x);
+                    const unsigned m = __ballot_sync(FULL, on), below = (1u << lane) - 1;
+                    const unsigned long long k = on ? list[at + __popc(m & below)] : 0;
+                    const unsigned tie = __ballot_sync(FULL, on && k == t64);
+                    if (on)
+                        score[j] = k > t64 || (k == t64 && __popc(tie & below) < quota) ? FLT_MAX
+                                                                                       : -FLT_MAX;
+                    quota -= __popc(tie);
+                    at += __popc(m);
+                });
             }
         }
-        const unsigned infb = __ballot_sync(FULL, inf);
-        const unsigned inb = __ballot_sync(FULL, in);
-        if (lane == 0) {
-            redi[0][warp] = __popc(inb);
-            redi[1][warp] = __popc(infb);
-        }
-        __syncthreads();
-        const unsigned below = (1u << lane) - 1;
-        int ins = 0, infs_before = 0, all_in = 0, all_inf = 0;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            if (w < warp) {
-                ins += redi[0][w];
-                infs_before += redi[1][w];
-            }
-            all_in += redi[0][w];
-            all_inf += redi[1][w];
-        }
-        ins += __popc(inb & below);
-        infs_before += __popc(infb & below);
-        if (inf)
-            in = infs_before < inf_left;
-        if (in)
-            out[at + ins + min(infs_before, inf_left)] = tile_of(j);
-        at += all_in + min(all_inf, inf_left);
-        inf_left -= min(all_inf, inf_left);
-        __syncthreads();
+        __syncwarp();                             // the marks, which the same warp reads
     }
+
+    // ---- the kept blocks in their order ----
+    int seen = inf_before;
+    auto kept = [&](int j, float x) {             // asked in ascending order
+        const unsigned inf = __ballot_sync(FULL, x == INFINITY);
+        const bool in = x == INFINITY ? seen + __popc(inf & ((1u << lane) - 1)) < inf_left
+                                      : j < c1 && (x == FLT_MAX || (x != -FLT_MAX && x - slack > edge));
+        seen += __popc(inf);
+        return in;
+    };
+    int ins = 0;
+    each([&](int j, float x) { ins += __popc(__ballot_sync(FULL, kept(j, x))); });
+    tally.sums(ins, 0, 0, all, before);
+    int at = lo + before.x;
+    seen = inf_before;
+    each([&](int j, float x) {
+        const bool in = kept(j, x);
+        const unsigned m = __ballot_sync(FULL, in);
+        if (in)
+            out[at + __popc(m & ((1u << lane) - 1))] = tile_of(j);
+        at += __popc(m);
+    });
+    for (int i = rank * NTH + tid; i < p.keep_first + p.keep_last; i += C * NTH)
+        if (i < lo)
+            out[i] = tile_of(i);
+        else
+            out[p.keep - p.keep_last + i - lo] = tile_of(hi + i - lo);
+    tally.leave();
 }
 
 }  // namespace
@@ -667,33 +563,45 @@ SparseKernel bounds_kernel(bool bf16, int head_dim)
     return k;
 }
 
-template <typename T, int D>
-static const void *score_fn(int group)
+namespace {
+
+template <typename T, int D, int NTH, bool CLUSTER>
+const void *select_fn(int group)
 {
-    return group <= 8 ? reinterpret_cast<const void *>(&block_score_kernel_t<T, D, 1>)
-                      : reinterpret_cast<const void *>(&block_score_kernel_t<T, D, 2>);
+    return group <= 8 ? reinterpret_cast<const void *>(&block_select_kernel_t<T, D, 1, NTH, CLUSTER>)
+                      : reinterpret_cast<const void *>(&block_select_kernel_t<T, D, 2, NTH, CLUSTER>);
 }
 
-SparseKernel block_score_kernel(bool bf16, int head_dim, int group)
+template <int NTH, bool CLUSTER>
+const void *select_fn(bool bf16, int head_dim, int group)
 {
-    SparseKernel k{nullptr, kScoreThreads};
     if (head_dim == 128)
-        k.fn = bf16 ? score_fn<__nv_bfloat16, 128>(group) : score_fn<__half, 128>(group);
-    else
-        k.fn = bf16 ? score_fn<__nv_bfloat16, 64>(group) : score_fn<__half, 64>(group);
-    return k;
+        return bf16 ? select_fn<__nv_bfloat16, 128, NTH, CLUSTER>(group)
+                    : select_fn<__half, 128, NTH, CLUSTER>(group);
+    return bf16 ? select_fn<__nv_bfloat16, 64, NTH, CLUSTER>(group)
+                : select_fn<__half, 64, NTH, CLUSTER>(group);
 }
 
-SparseKernel block_select_kernel(bool bf16, int head_dim)
+}  // namespace
+
+// Short tables: a block of 128 threads a run.  Others: 256 threads, and where the runs leave
+// SMs idle a cluster of 2, 4 or 8 blocks shares a run.
+SelectLaunch select_launch(bool bf16, int head_dim, int group, int num_runs, int max_blocks,
+                           int num_sms)
 {
-    SparseKernel k{nullptr, kSelectThreads};
-    if (head_dim == 128)
-        k.fn = bf16 ? reinterpret_cast<const void *>(&block_select_kernel_t<__nv_bfloat16, 128>)
-                    : reinterpret_cast<const void *>(&block_select_kernel_t<__half, 128>);
-    else
-        k.fn = bf16 ? reinterpret_cast<const void *>(&block_select_kernel_t<__nv_bfloat16, 64>)
-                    : reinterpret_cast<const void *>(&block_select_kernel_t<__half, 64>);
-    return k;
+    SelectLaunch e{};
+    const bool small = max_blocks <= 256;
+    e.threads = small ? 128 : 256;
+    e.cluster = 1;
+    while (!small && e.cluster < 8 && 2LL * e.cluster * num_runs <= 2LL * num_sms &&
+           max_blocks >= 256 * e.cluster)
+        e.cluster *= 2;
+    e.fn = small ? select_fn<128, false>(bf16, head_dim, group)
+                 : select_fn<256, true>(bf16, head_dim, group);
+    const long long span = ((long long)max_blocks + 16 * e.cluster - 1) / (16 * e.cluster) * 16;
+    e.near = span <= kSelectNear ? (int)span : 0;
+    e.smem = 4 * (size_t)e.near;
+    return e;
 }
 
 }  // namespace pa

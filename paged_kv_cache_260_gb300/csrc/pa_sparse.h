@@ -26,13 +26,21 @@ struct SelectParams {
     const void *bounds;
     const int32_t *block_tables;
     const int32_t *seq_lens;
-    float *scores;                 // workspace: [num_seqs][num_kv_heads][row] fp32 scores,
-    float *reach;                  //   [..][row / 16] the largest |bound| of 16 blocks,
+    float *scores;                 // workspace: [num_seqs][num_kv_heads][row] fp32 scores, if
+                                   //   a thread block's do not fit its shared memory,
     unsigned long long *exact;     //   [..][row] scores with more bits, of those in doubt
     uint32_t *err;
     int num_seqs, num_heads, num_kv_heads, max_blocks, num_blocks;
     int keep, keep_first, keep_last;
     int row;                       // max_blocks rounded up to 16
+    int near;                      // scores a thread block holds in shared memory, or 0
+};
+
+// A launch of the selection kernel.
+struct SelectLaunch {
+    const void *fn;
+    int threads, cluster, near;
+    size_t smem;
 };
 
 // pa_evict: a sequence shortened to its heaviest tokens.
@@ -47,6 +55,14 @@ struct EvictParams {
     int num_seqs, num_kv_heads, max_blocks, num_blocks;
     int keep_first, keep_last;
     int list;
+    int keys, table;               // masses and table entries a block holds in shared memory
+};
+
+// A launch of the eviction kernel.
+struct EvictLaunch {
+    const void *fn;
+    int threads, cluster, keys, table;
+    size_t smem;
 };
 
 struct SparseKernel {
@@ -55,9 +71,8 @@ struct SparseKernel {
 };
 
 SparseKernel bounds_kernel(bool bf16, int head_dim);
-// scores of 16 blocks a warp and step, for groups of up to 8 and up to 16 heads
-SparseKernel block_score_kernel(bool bf16, int head_dim, int group);
-SparseKernel block_select_kernel(bool bf16, int head_dim);
-SparseKernel evict_kernel(int head_dim);
+SelectLaunch select_launch(bool bf16, int head_dim, int group, int num_runs, int max_blocks,
+                           int num_sms);
+EvictLaunch evict_launch(int head_dim, int num_runs, int max_blocks, int num_sms);
 
 }  // namespace pa

@@ -44,6 +44,7 @@ __global__ void __launch_bounds__(NTH) evict_kernel_t(const EvictParams p)
     int32_t *sm_table = reinterpret_cast<int32_t *>(smem + p.keys);
     int32_t *sm_list = sm_table + p.table;
     __shared__ TallySmem<NW> counts;
+    __shared__ RadixSmem<NW> radix;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int Hkv = p.num_kv_heads;
     Tally<NW, CLUSTER> tally(counts);
@@ -74,14 +75,43 @@ __global__ void __launch_bounds__(NTH) evict_kernel_t(const EvictParams p)
     const int32_t *gtable = p.block_tables + (size_t)s * p.max_blocks;
     const bool near = p.table > 0;
     bool bad = false;
-    for (int j = tid; j < (L + kBlockSize - 1) / kBlockSize; j += NTH) {
-        const int b = __ldg(gtable + j);
-        bad |= (unsigned)b >= (unsigned)p.num_blocks;
-        if (near)
-            sm_table[j] = b;
+    constexpr int K = 8;                          // loads in flight a thread
+    for (int j0 = tid; j0 < (L + kBlockSize - 1) / kBlockSize; j0 += K * NTH) {
+        int b[K];
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+            b[i] = j0 + i * NTH < (L + kBlockSize - 1) / kBlockSize ? __ldg(gtable + j0 + i * NTH) : 0;
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            bad |= (unsigned)b[i] >= (unsigned)p.num_blocks;
+            if (near && j0 + i * NTH < p.table)
+                sm_table[j0 + i * NTH] = b[i];
+        }
     }
-    for (int t = lo + tid; t < min(end, lo + p.keys); t += NTH)
-        keys[t - lo] = mass_key(__ldcg(mass + t));
+    const int kept_keys = min(end - lo, p.keys);
+    uint32_t least = 0, most = 0;                 // of this thread's keys, least upside down
+    for (int t0 = tid; t0 < kept_keys; t0 += K * NTH) {
+        float m[K];
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+            m[i] = t0 + i * NTH < kept_keys ? __ldcg(mass + lo + t0 + i * NTH) : 0.f;
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+            if (t0 + i * NTH < kept_keys) {
+                const uint32_t k = mass_key(m[i]);
+                keys[t0 + i * NTH] = k;
+                least = max(least, ~k);
+                most = max(most, k);
+            }
+    }
+    const bool all_near = end - lo <= p.keys;
+    for (int t = lo + kept_keys + tid; t < end; t += NTH) {
+        const uint32_t k = mass_key(__ldcg(mass + t));
+        least = max(least, ~k);
+        most = max(most, k);
+    }
+    for (int i = tid; i < 2 * RadixSmem<NW>::BINS; i += NTH)
+        radix.hist[0][i] = 0;
     if (__syncthreads_or(bad)) {                  // (the same in every block of the cluster)
         if (tid == 0)
             record_error(p.err, PA_DEVERR_TABLE_RANGE);
@@ -92,56 +122,56 @@ __global__ void __launch_bounds__(NTH) evict_kernel_t(const EvictParams p)
         return t >= end ? 0u : t - lo < p.keys ? keys[t - lo] : mass_key(__ldcg(mass + t));
     };
     auto each = [&](auto &&f) {                   // f(slot, key) over the warp's slots
-        for (int i = 0; i < steps; ++i) {
-            const int t = w0 + 32 * i + lane;
-            f(t, key_of(t));
+        if (all_near) {
+            const uint32_t *k = keys + (w0 - lo) + lane;
+#pragma unroll 4
+            for (int i = 0; i < steps; ++i) {
+                const int t = w0 + 32 * i + lane;
+                f(t, t < end ? k[32 * i] : 0u);
+            }
+        } else {
+            for (int i = 0; i < steps; ++i) {
+                const int t = w0 + 32 * i + lane;
+                f(t, key_of(t));
+            }
         }
     };
-    // the want-th largest key, two bits at a time: how many keys reach each of three
-    // thresholds, until exactly `want` reach one
-    uint32_t T = want > 0 ? 0u : 0xffffffffu;
+    // the want-th largest key: what is above it is kept, and of those equal to it the first
+    // ones (just all, if no more than `want` reach it)
+    uint32_t T = 0xffffffffu;
     int4 all, before;
-    int reach = 0;
-    for (int bit = 30; want > 0 && bit >= 0 && reach != want; bit -= 2) {
-        const uint32_t t1 = T | 1u << bit, t2 = T | 2u << bit, t3 = T | 3u << bit;
-        int n1 = 0, n2 = 0, n3 = 0;
-        each([&](int, uint32_t k) {
-            n1 += k >= t1;
-            n2 += k >= t2;
-            n3 += k >= t3;
-        });
-        tally.sums(__reduce_add_sync(FULL, n1), __reduce_add_sync(FULL, n2),
-                   __reduce_add_sync(FULL, n3), all, before);
-        if (all.x >= want) {
-            T = all.z >= want ? t3 : all.y >= want ? t2 : t1;
-            reach = all.z >= want ? all.z : all.y >= want ? all.y : all.x;
+    int quota = 0;
+    if (want > 0) {
+        int above, reach, none;
+        const uint3 range = tally.most(0, least, most, 0u, none, none);
+        T = tally.threshold(
+            radix, [&](auto &&f) { each([&](int t, uint32_t k) { f(k, t < end); }); }, want,
+            ~range.x, range.y, above, reach);
+        quota = INT_MAX;
+        if (reach != want) {
+            int ties = 0;
+            each([&](int t, uint32_t k) { ties += t < end && k == T; });
+            tally.sums(__reduce_add_sync(FULL, ties), 0, 0, all, before);
+            quota = max(0, want - above - before.x);
         }
-    }
-    // of the keys equal to T the first ones (all of them if just `want` reach it)
-    int quota = want > 0 ? INT_MAX : 0;
-    if (reach != want) {
-        int above = 0, ties = 0;
-        each([&](int t, uint32_t k) {
-            above += k > T;
-            ties += t < end && k == T;
-        });
-        tally.sums(__reduce_add_sync(FULL, above), __reduce_add_sync(FULL, ties), 0, all, before);
-        quota = max(0, want - all.x - before.y);
     }
     int used = 0;
     auto kept = [&](int t, uint32_t k) {          // asked in ascending order
-        const unsigned tie = __ballot_sync(FULL, t < end && k == T);
-        const bool in = t < end && (k > T || (k == T && used + __popc(tie & ((1u << lane) - 1)) < quota));
-        used += __popc(tie);
-        return in;
+        bool tied = t < end && k == T;
+        if (quota != INT_MAX) {
+            const unsigned tie = __ballot_sync(FULL, tied);
+            tied = tied && used + __popc(tie & ((1u << lane) - 1)) < quota;
+            used += __popc(tie);
+        }
+        return t < end && (k > T || tied);
     };
     int holes = 0, movers = 0;
     each([&](int t, uint32_t k) {
         const bool in = kept(t, k);
-        holes += __popc(__ballot_sync(FULL, !in && t < min(edge, end)));
-        movers += __popc(__ballot_sync(FULL, in && t >= edge));
+        holes += !in && t < min(edge, end);
+        movers += in && t >= edge;
     });
-    tally.sums(holes, movers, 0, all, before);
+    tally.sums(__reduce_add_sync(FULL, holes), __reduce_add_sync(FULL, movers), 0, all, before);
     const int moves = all.y;
     int hole = before.x, mover = before.y;
     const bool few = !CLUSTER && moves <= kEvictList;

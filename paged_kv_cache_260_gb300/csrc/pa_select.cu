@@ -42,15 +42,6 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-// the larger of two pairs of magnitudes; a NaN loses
-template <typename T>
-__device__ __forceinline__ uint32_t most2(uint32_t a, uint32_t b)
-{
-    using V = typename Pair<T>::V;
-    const V r = __hmax2(*reinterpret_cast<V *>(&a), *reinterpret_cast<V *>(&b));
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-
 constexpr int kBoundsThreads = 256;
 
 // ---------------------------------------------------------------------------
@@ -165,10 +156,13 @@ __global__ void __launch_bounds__(kBoundsThreads) block_bounds_kernel(const Boun
 //
 // Per (sequence, kv head) the keep_first first blocks, the keep_last last ones and
 // the best of the rest are kept.  The tensor cores' sums are off by a part of
-// sum |q||bound|, and the choice must not depend on that: with E the largest
-// error and T the lowest chosen score, a block whose score lies above T + 2 E is
-// in, one below T - 2 E is out, and the few between are summed again in pairs of
-// floats (46 bits) and ranked by that, ties to the lowest position.
+// sum |q||bound|, and the choice must not depend on that.  With E the largest
+// error and t above the best score left out and not above the lowest one chosen,
+// a block whose score lies above t + 2 E is in (its exact score is larger than
+// those of all left out), one below t - 2 E is out, and the few between are
+// summed again in pairs of floats (46 bits) and ranked by that, ties to the
+// lowest position.  (Where scores are equal at the border, t is that score, and
+// all of them lie between.)
 //
 // One thread block takes a (sequence, kv head), or a cluster of blocks a contiguous
 // part of its blocks each (CLUSTER); the scores stay in shared memory (in the
@@ -208,6 +202,7 @@ __global__ void __launch_bounds__(NTH, 512 / NTH) block_select_kernel_t(const Se
     __shared__ float q[8 * NT * D];               // the group's queries
     __shared__ unsigned long long near_keys[CLUSTER ? 1 : kDoubt];
     __shared__ TallySmem<NW> counts;
+    __shared__ RadixSmem<NW> radix;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int Hkv = p.num_kv_heads, G = p.num_heads / Hkv;
     Tally<NW, CLUSTER> tally(counts);
@@ -249,7 +244,7 @@ __global__ void __launch_bounds__(NTH, 512 / NTH) block_select_kernel_t(const Se
     float *score = (p.near >= span ? near_scores : p.scores + (size_t)run * p.row + b0) - b0;
     const T *qg = static_cast<const T *>(p.q) + ((size_t)s * p.num_heads + h * G) * D;
     const int r = lane >> 2, qd = lane & 3;
-    uint32_t big = 0;                             // the largest |bound|
+    float size = 0.f;                             // the largest sum |q||bound|
     {
         uint32_t qn[NT][NI][4], qp[NT][NI][4];    // min(q, 0) and max(q, 0)
 #pragma unroll
@@ -285,14 +280,17 @@ __global__ void __launch_bounds__(NTH, 512 / NTH) block_select_kernel_t(const Se
                                     4 * k + qd);
             if (b + 16 * NW < b1)
                 rows(b + 16 * NW, tile);
-            float acc[NT][4];
+            // the scores, and sum |q||bound|: the same products of magnitudes
+            float acc[NT][4], mag[NT][4];
 #pragma unroll
             for (int j = 0; j < NT; ++j)
-                acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[j][e] = mag[j][e] = 0.f;
 #pragma unroll
             for (int k = 0; k < 2 * NI; ++k) {
-                const uint32_t a0[4] = {x[0][k].x, x[1][k].x, x[0][k].y, x[1][k].y};
-                const uint32_t a1[4] = {x[0][k].z, x[1][k].z, x[0][k].w, x[1][k].w};
+                uint32_t a0[4] = {x[0][k].x, x[1][k].x, x[0][k].y, x[1][k].y};
+                uint32_t a1[4] = {x[0][k].z, x[1][k].z, x[0][k].w, x[1][k].w};
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
                     const uint32_t *qq = k < NI ? qn[j][k] : qp[j][k - NI];
@@ -300,9 +298,15 @@ __global__ void __launch_bounds__(NTH, 512 / NTH) block_select_kernel_t(const Se
                     M::run(acc[j], a1, qq[2], qq[3]);
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    big = most2<T>(big, a0[e] & 0x7fff7fffu);
-                    big = most2<T>(big, a1[e] & 0x7fff7fffu);
+                for (int e = 0; e < 4; ++e) {     // -|min| and |max|
+                    a0[e] = k < NI ? a0[e] | 0x80008000u : a0[e] & 0x7fff7fffu;
+                    a1[e] = k < NI ? a1[e] | 0x80008000u : a1[e] & 0x7fff7fffu;
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const uint32_t *qq = k < NI ? qn[j][k] : qp[j][k - NI];
+                    M::run(mag[j], a0, qq[0], qq[1]);
+                    M::run(mag[j], a1, qq[2], qq[3]);
                 }
             }
             // the greatest head's score of block r (and r + 8); not finite: first of all
@@ -311,7 +315,9 @@ __global__ void __launch_bounds__(NTH, 512 / NTH) block_select_kernel_t(const Se
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float v = fabsf(acc[j][e]) <= FLT_MAX ? acc[j][e] : INFINITY;
+                    const bool finite = fabsf(acc[j][e]) <= FLT_MAX;
+                    size = finite ? fmaxf(size, mag[j][e]) : size;
+                    const float v = finite ? acc[j][e] : INFINITY;
                     if (8 * j + 2 * qd + (e & 1) < G)
                         best[e >> 1] = fmaxf(best[e >> 1], v);
                 }
@@ -325,21 +331,12 @@ __global__ void __launch_bounds__(NTH, 512 / NTH) block_select_kernel_t(const Se
                 score[j] = qd ? best[1] : best[0];
         }
     }
-    // ---- the queries, for those that are summed again, and their sums of magnitudes ----
+    // ---- the queries, for those that are summed again ----
     for (int i = tid; i < G * D; i += NTH)
         q[i] = Elem<T>::to_f(qg[i]);
+    for (int i = tid; i < 2 * RadixSmem<NW>::BINS; i += NTH)
+        radix.hist[0][i] = 0;
     __syncthreads();
-    float l1 = 0.f;
-    for (int g = warp; g < G; g += NW) {
-        float a = 0.f;
-#pragma unroll
-        for (int c = 0; c < D; c += 32)
-            a += fabsf(q[g * D + c + lane]);
-#pragma unroll
-        for (int off = 16; off; off >>= 1)
-            a += __shfl_xor_sync(FULL, a, off);
-        l1 = fmaxf(l1, a);
-    }
     // a warp's contiguous part of the blocks that compete: [w0, ..) in `steps` steps of 32
     const int c0 = min(max(b0, lo), hi), c1 = max(c0, min(b1, hi));
     const int steps = (c1 - c0 + NTH - 1) / NTH;
@@ -350,7 +347,6 @@ __global__ void __launch_bounds__(NTH, 512 / NTH) block_select_kernel_t(const Se
             f(j, j < c1 ? score[j] : -INFINITY);
         }
     };
-    const float2 b2 = Elem<T>::to_f2(big);
     uint32_t least = 0, most = 0;                 // of the finite scores, least upside down
     int infs = 0;                                 // those that are not rank first
     each([&](int j, float x) {
@@ -360,52 +356,29 @@ __global__ void __launch_bounds__(NTH, 512 / NTH) block_select_kernel_t(const Se
         }
         infs += x == INFINITY;
     });
-    int4 all, before;
-    tally.sums(__reduce_add_sync(FULL, infs), 0, 0, all, before);
-    int inf_left = min(all.x, want);              // so many of them, the foremost
-    const int inf_before = before.x;
+    int all_infs, inf_before;
+    const uint3 range = tally.most(__reduce_add_sync(FULL, infs), least, most,
+                                   __float_as_uint(size), all_infs, inf_before);
+    int inf_left = min(all_infs, want);           // so many of them, the foremost
     want -= inf_left;
-    const uint3 range = tally.most(least, most, __float_as_uint(fmaxf(b2.x, b2.y)));
-    const uint3 sizes = tally.most(__float_as_uint(l1), 0, 0);
     // Largest error: 2 D / 16 steps each add 17 terms aligned to the largest, none above
-    // sum |q||bound| <= l1 * reach, and lose 2^-23 of it a term (infinite bounds put
-    // everything in doubt)
-    const float twice = 2.f * (2 * D / 16) * 17 * 1.1920929e-7f * __uint_as_float(sizes.x) *
-                        __uint_as_float(range.z);
+    // sum |q||bound|, and lose 2^-23 of it a term (sums that are infinite put everything in
+    // doubt)
+    const float twice = 2.f * (2 * D / 16) * 17 * 1.1920929e-7f * __uint_as_float(range.z);
     const float slack = twice <= FLT_MAX ? twice : FLT_MAX;
+    int4 all, before;
+    int ins = 0, ins_before = -1;                 // kept by this warp; by those before it, if known
 
-    // ---- T, the want-th largest score, two bits at a time from the first in which scores
-    // differ; just `want` scores reach it, or it is exact ----
+    // ---- a score that just `want` reach, or else the want-th largest itself ----
     float edge = INFINITY;                        // nothing lies above: none is kept
     if (want > 0) {
-        const uint32_t least_key = ~range.x;
-        int bit = least_key == range.y ? -2 : (31 - __clz(least_key ^ range.y)) & ~1;
-        uint32_t t = bit < 0 ? range.y : range.y & ~((4u << bit) - 1u);
-        int reach = 0;
-        for (; bit >= 0 && reach != want; bit -= 2) {
-            const uint32_t t1 = t | 1u << bit, t2 = t | 2u << bit, t3 = t | 3u << bit;
-            int n1 = 0, n2 = 0, n3 = 0;
-            each([&](int j, float x) {
-                const uint32_t k = j < c1 && x != INFINITY ? ordered(x) : 0u;
-                n1 += k >= t1;
-                n2 += k >= t2;
-                n3 += k >= t3;
-            });
-            tally.sums(__reduce_add_sync(FULL, n1), __reduce_add_sync(FULL, n2),
-                       __reduce_add_sync(FULL, n3), all, before);
-            if (all.x >= want) {
-                t = all.z >= want ? t3 : all.y >= want ? t2 : t1;
-                reach = all.z >= want ? all.z : all.y >= want ? all.y : all.x;
-            }
-        }
-        // the lowest chosen score itself: just `want` reach t, or it is t
-        uint32_t lowest = 0;                      // upside down
-        each([&](int j, float x) {
-            if (j < c1 && x != INFINITY && ordered(x) >= t)
-                lowest = max(lowest, ~ordered(x));
-        });
-        edge = from_ordered(~tally.most(lowest, 0, 0).x);
-
+        int above, reach;
+        edge = from_ordered(tally.threshold(
+            radix,
+            [&](auto &&f) {
+                each([&](int j, float x) { f(ordered(x), j < c1 && x != INFINITY); });
+            },
+            want, ~range.x, range.y, above, reach));
         // ---- in, out, or in doubt ----
         auto doubtful = [&](float x) { return x != INFINITY && x - slack <= edge && x + slack >= edge; };
         int sure = 0, doubts = 0;
@@ -413,26 +386,34 @@ __global__ void __launch_bounds__(NTH, 512 / NTH) block_select_kernel_t(const Se
             sure += j < c1 && x != INFINITY && x - slack > edge;
             doubts += j < c1 && doubtful(x);
         });
-        tally.sums(__reduce_add_sync(FULL, sure), __reduce_add_sync(FULL, doubts), 0, all, before);
+        sure = __reduce_add_sync(FULL, sure);
+        doubts = __reduce_add_sync(FULL, doubts);
+        tally.sums(sure, doubts, 0, all, before);
         const int need = want - all.x, total = all.y, mine = before.y;
-        if (need == total) {
-            // all of them: no sums wanted
+        if (need == 0 || need == total) {
+            // none or all of them: no sums wanted
+            ins_before = before.x + (need ? before.y : 0);
             each([&](int j, float x) {
-                if (j < c1 && doubtful(x))
+                if (need && j < c1 && doubtful(x))
                     score[j] = FLT_MAX;
             });
         } else {
             // the score of block j by the warp, as an ordered number of 64 bits
             auto resum = [&](int j) {
                 const T *b = static_cast<const T *>(p.bounds) + (size_t)tile_of(j) * 2 * D;
+                float bound[2][D / 32];
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    bound[0][c] = Elem<T>::to_f(b[32 * c + lane]);
+                    bound[1][c] = Elem<T>::to_f(b[D + 32 * c + lane]);
+                }
                 unsigned long long best = 0;
                 for (int g = 0; g < G; ++g) {
                     float a = 0.f, e = 0.f;
 #pragma unroll
-                    for (int cc = 0; cc < D; cc += 32) {
-                        const float qc = q[g * D + cc + lane];
-                        const float k = Elem<T>::to_f(b[(qc > 0.f ? D : 0) + cc + lane]);
-                        two_add(a, e, qc * k);    // an exact product
+                    for (int c = 0; c < D / 32; ++c) {
+                        const float qc = q[g * D + 32 * c + lane];
+                        two_add(a, e, qc * (qc > 0.f ? bound[1][c] : bound[0][c]));   // exact
                     }
 #pragma unroll
                     for (int off = 16; off; off >>= 1) {
@@ -529,10 +510,16 @@ __global__ void __launch_bounds__(NTH, 512 / NTH) block_select_kernel_t(const Se
         seen += __popc(inf);
         return in;
     };
-    int ins = 0;
-    each([&](int j, float x) { ins += __popc(__ballot_sync(FULL, kept(j, x))); });
-    tally.sums(ins, 0, 0, all, before);
-    int at = lo + before.x;
+    if (want == 0)
+        ins_before = 0;
+    if (ins_before >= 0) {
+        ins_before += min(inf_before, inf_left);
+    } else {
+        each([&](int j, float x) { ins += __popc(__ballot_sync(FULL, kept(j, x))); });
+        tally.sums(ins, 0, 0, all, before);
+        ins_before = before.x;
+    }
+    int at = lo + ins_before;
     seen = inf_before;
     each([&](int j, float x) {
         const bool in = kept(j, x);

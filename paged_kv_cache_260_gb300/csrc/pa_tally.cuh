@@ -7,10 +7,22 @@
 
 namespace pa {
 
+constexpr int kTallyBlocks = 8;    // most blocks of a cluster
+
 template <int NW>
 struct TallySmem {
-    int part[2][3][NW];
+    int part[2][4][NW];
     int4 total[2];                 // read by the other blocks of the cluster
+};
+
+// How many keys have each value of a digit: four values a thread, 32 a group.
+template <int NW>
+struct RadixSmem {
+    static constexpr int BINS = 4 * 32 * NW, BITS = NW == 8 ? 10 : 9, GROUPS = BINS / 32;
+    static_assert(BINS == 1 << BITS, "128 or 256 threads");
+    alignas(16) int hist[2][BINS];
+    int group[2][GROUPS];          // both read by the other blocks of the cluster
+    int found[3];
 };
 
 template <int NW, bool CLUSTER>
@@ -63,8 +75,10 @@ struct Tally {
         ++round;
     }
 
-    // The largest of three unsigned values over all warps.
-    __device__ __forceinline__ uint3 most(uint32_t a, uint32_t b, uint32_t d)
+    // A count's sum over all warps and over those before this one, and the largest of three
+    // unsigned values.
+    __device__ __forceinline__ uint3 most(int n, uint32_t a, uint32_t b, uint32_t d, int &all,
+                                          int &before)
     {
         constexpr uint32_t FULL = 0xffffffffu;
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -73,29 +87,126 @@ struct Tally {
         b = __reduce_max_sync(FULL, b);
         d = __reduce_max_sync(FULL, d);
         if (lane == 0) {
-            c[0][warp] = (int)a;
-            c[1][warp] = (int)b;
-            c[2][warp] = (int)d;
+            c[0][warp] = n;
+            c[1][warp] = (int)a;
+            c[2][warp] = (int)b;
+            c[3][warp] = (int)d;
         }
         __syncthreads();
         auto over = [&](int row) {
             return __reduce_max_sync(FULL, lane < NW ? (uint32_t)c[row][lane] : 0u);
         };
-        uint3 all = make_uint3(over(0), over(1), over(2));
+        uint3 top = make_uint3(over(1), over(2), over(3));
+        all = __reduce_add_sync(FULL, lane < NW ? c[0][lane] : 0);
+        before = __reduce_add_sync(FULL, lane < warp ? c[0][lane] : 0);
         if (CLUSTER) {
             if (threadIdx.x == 0)
-                sm.total[round & 1] = make_int4((int)all.x, (int)all.y, (int)all.z, 0);
+                sm.total[round & 1] = make_int4(all, (int)top.x, (int)top.y, (int)top.z);
             cluster_arrive();
             cluster_wait();
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
             if (lane < blocks)
                 y = cluster_load4(cluster_addr(smem_addr(&sm.total[round & 1]), lane));
-            all = make_uint3(__reduce_max_sync(FULL, __float_as_uint(y.x)),
-                             __reduce_max_sync(FULL, __float_as_uint(y.y)),
-                             __reduce_max_sync(FULL, __float_as_uint(y.z)));
+            all = __reduce_add_sync(FULL, __float_as_int(y.x));
+            before += __reduce_add_sync(FULL, lane < rank ? __float_as_int(y.x) : 0);
+            top = make_uint3(__reduce_max_sync(FULL, __float_as_uint(y.y)),
+                             __reduce_max_sync(FULL, __float_as_uint(y.z)),
+                             __reduce_max_sync(FULL, __float_as_uint(y.w)));
         }
         ++round;
-        return all;
+        return top;
+    }
+
+    // A threshold that just `want` keys reach, or else the want-th largest key itself: digit
+    // by digit from the top, each round counts the keys of every value of the next digit, among
+    // those that share the digits found so far.  least and most are the smallest and the
+    // largest key; the digits are those of key - least, so that the first one already
+    // spreads the keys over its values (the leading bits of floats of one size are the
+    // same, and a count that all threads add to one at a time takes its time).  There are
+    // `want` > 0 keys at least.  each(f) calls f(key, whether it counts) for the caller's
+    // keys.  r.hist is zero and seen to be.  above: keys larger than the threshold's digits;
+    // reach: keys that are not smaller, -1 if all keys are equal.
+    template <typename F>
+    __device__ __forceinline__ uint32_t threshold(RadixSmem<NW> &r, const F &each, int want,
+                                                  uint32_t least, uint32_t most, int &above,
+                                                  int &reach)
+    {
+        constexpr uint32_t FULL = 0xffffffffu;
+        constexpr int BITS = RadixSmem<NW>::BITS;
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        above = 0;
+        reach = -1;
+        uint32_t t = 0;
+        int bits = 32 - __clz(most - least);
+        for (int buf = 0; bits > 0 && reach != want; buf ^= 1) {
+            const int shift = max(0, bits - BITS);
+            const uint32_t mask = (1u << (bits - shift)) - 1u;
+            int *hist = r.hist[buf];
+            const uint32_t high = bits < 32 ? t >> bits : 0u;
+            each([&](uint32_t k, bool on) {
+                k -= least;
+                if (on && (bits < 32 ? k >> bits : 0u) == high)
+                    atomicAdd(&hist[k >> shift & mask], 1);
+            });
+            __syncthreads();
+            const int4 v = reinterpret_cast<const int4 *>(hist)[threadIdx.x];
+            int n = v.x + v.y + v.z + v.w;
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1)
+                n += __shfl_xor_sync(FULL, n, o);
+            if (lane % 8 == 0)
+                r.group[buf][threadIdx.x / 8] = n;
+            sync();
+            // (the blocks have read the other buffer: they have been through this barrier)
+            reinterpret_cast<int4 *>(r.hist[buf ^ 1])[threadIdx.x] = make_int4(0, 0, 0, 0);
+            if (warp == 0) {
+                // the group with the want-th largest, then the value: a lane each, summed over
+                // the blocks with all loads in flight at once
+                int value = 0, over = above, top = 0;
+#pragma unroll
+                for (int level = 0; level < 2; ++level) {
+                    const int *row = level ? hist + 32 * value : r.group[buf];
+                    const bool on = level || lane < RadixSmem<NW>::GROUPS;
+                    int count = 0;
+                    if (CLUSTER) {
+                        int y[kTallyBlocks];
+#pragma unroll
+                        for (int c = 0; c < kTallyBlocks; ++c)
+                            y[c] = c < blocks && on ? __float_as_int(cluster_load(
+                                                          cluster_addr(smem_addr(row + lane), c)))
+                                                    : 0;
+#pragma unroll
+                        for (int c = 0; c < kTallyBlocks; ++c)
+                            count += y[c];
+                    } else if (on) {
+                        count = row[lane];
+                    }
+                    int incl = count;             // of this value and those above it
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int y = __shfl_down_sync(FULL, incl, o);
+                        if (lane + o < 32)
+                            incl += y;
+                    }
+                    // the highest lane that, with all above it, has enough
+                    const int at = 31 - __clz(__ballot_sync(FULL, over + incl >= want));
+                    top = over + __shfl_sync(FULL, incl, at);
+                    over = top - __shfl_sync(FULL, count, at);
+                    value = 32 * value + at;
+                }
+                if (lane == 0) {
+                    r.found[0] = value;
+                    r.found[1] = over;
+                    r.found[2] = top;
+                }
+            }
+            __syncthreads();
+            t |= (uint32_t)r.found[0] << shift;
+            above = r.found[1];
+            reach = r.found[2];
+            bits = shift;
+        }
+        return t + least;
     }
 
     // A barrier of the block, or of the cluster.

@@ -441,6 +441,13 @@ __device__ __forceinline__ void decode_worker(const DecodeParams &p, const CUten
         }
         const int L = lens[cons.s];
         bool need_q = true;
+        // accounting: this lane's place in the run's scores (token r, heads 2 qd and after)
+        const int cols = score_cols(G);
+        float *scores = nullptr;
+        if constexpr (MASS)
+            scores = p.scores +
+                     ((size_t)cons.s * Hkv + cons.h) * p.max_blocks * (kBlockSize * cols) +
+                     r * cols + 2 * qd;
 
         // Fused append: the new token sits at position L-1, in the run's last
         // tile, which only this warp reads.  Its K/V row is taken from
@@ -547,13 +554,10 @@ __device__ __forceinline__ void decode_worker(const DecodeParams &p, const CUten
                         x2 = x3 = -INFINITY;
                 }
                 if constexpr (MASS) {
-                    const int cols = score_cols(G), h0 = 8 * j + 2 * qd;
-                    if (h0 < cols) {
-                        float *dst = p.scores +
-                                     (((size_t)cons.s * Hkv + cons.h) * p.max_blocks + tile) *
-                                         kBlockSize * cols + h0;
-                        *reinterpret_cast<float2 *>(dst + r * cols) = make_float2(x0, x1);
-                        *reinterpret_cast<float2 *>(dst + (r + 8) * cols) = make_float2(x2, x3);
+                    if (8 * j + 2 * qd < G) {
+                        float *dst = scores + (size_t)tile * (kBlockSize * cols) + 8 * j;
+                        *reinterpret_cast<float2 *>(dst) = make_float2(x0, x1);
+                        *reinterpret_cast<float2 *>(dst + 8 * cols) = make_float2(x2, x3);
                     }
                 }
                 float mx0 = fmaxf(x0, x2), mx1 = fmaxf(x1, x3);

@@ -37,9 +37,8 @@ decode_mass_finish_kernel(const DecodeMassParams p)
 {
     constexpr int NTH = kMassFinishThreads, TOK = 128;
     __shared__ RaggedSmem sm;
-    __shared__ float2 stat[NTH / 32][kMaxGroup];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int warps = gridDim.x * (NTH / 32), me = blockIdx.x * (NTH / 32) + warp;
+    const int lane = threadIdx.x & 31;
+    const int warps = gridDim.x * (NTH / 32), me = blockIdx.x * (NTH / 32) + (threadIdx.x >> 5);
     const int Hkv = p.num_kv_heads, G = p.num_heads / Hkv, cols = score_cols(G);
     const int T = p.max_blocks * kBlockSize;
     grid_dependents_launch();
@@ -58,32 +57,45 @@ decode_mass_finish_kernel(const DecodeMassParams p)
             const int s = begin + i, h = at / nt, t0 = at % nt * TOK + lane;
             const int L = min(max(__ldg(p.seq_lens + s), 0), T);
             const size_t run = (size_t)s * Hkv + h;
-            __syncwarp();
-            if (lane < G)
-                stat[warp][lane] = __ldcg(p.stat + (size_t)s * p.num_heads + h * G + lane);
-            __syncwarp();
             const float *x = p.scores + (run * T + t0) * cols;
+            const float2 *stat = p.stat + (size_t)s * p.num_heads + h * G;
             float *mass = p.mass + run * T + t0;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int g = 0; g < G; g += 2) {
-                const float2 a = stat[warp][g], b = g + 1 < G ? stat[warp][g + 1] : make_float2(0.f, 0.f);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (t0 + 32 * k < L) {
-                        const float2 y = __ldcg(reinterpret_cast<const float2 *>(
-                            x + (size_t)32 * k * cols + g));
-                        sum[k] = fmaf(exp2f(y.x - a.x), a.y, sum[k]);
-                        if (g + 1 < G)
-                            sum[k] = fmaf(exp2f(y.y - b.x), b.y, sum[k]);
-                    }
-                }
-            }
+            // every load of four heads in flight at once, and the old masses with the first
+            float old[4], sum[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int t = t0 + 32 * k;
-                if (t < L)
-                    mass[32 * k] = add_mass(mass + 32 * k, p.decay, t == L - 1, sum[k]);
+                old[k] = t < L - 1 && p.decay != 0.f ? __ldcg(mass + 32 * k) : 0.f;
+                sum[k] = 0.f;
             }
+            for (int g = 0; g < G; g += 4) {
+                float2 st[4], y[4][2];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    st[i] = g + i < G ? __ldcg(stat + g + i) : make_float2(0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (t0 + 32 * k < L && g + 2 * i < G)
+                            y[k][i] = __ldcg(reinterpret_cast<const float2 *>(
+                                x + (size_t)32 * k * cols + g + 2 * i));
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (t0 + 32 * k < L && g + 2 * i < G) {
+                            sum[k] = fmaf(exp2f(y[k][i].x - st[2 * i].x), st[2 * i].y, sum[k]);
+                            if (g + 2 * i + 1 < G)
+                                sum[k] = fmaf(exp2f(y[k][i].y - st[2 * i + 1].x), st[2 * i + 1].y,
+                                              sum[k]);
+                        }
+            }
+            // (the newest token has no mass from before: old is 0)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (t0 + 32 * k < L)
+                    mass[32 * k] = fmaf(old[k], p.decay, sum[k]);
         }
     }
 }

@@ -1700,10 +1700,11 @@ int pa_decode_mass(const struct pa_sparse_args *args)
                             dim3(kMassFinishThreads), 0, static_cast<cudaStream_t>(a.stream), kargs);
 }
 
-// How pa_prefill_mass cuts its work: units of 2 x 128 rows, and a unit's keys into as many
-// parts as give every SM three blocks, two key tiles a part at least.
+// pa_prefill_mass's units of 2 x 128 rows, and its workspace: the statistics of the units'
+// pieces (one for each unit and one more for each border between two blocks' shares), and
+// each query tile's sums for every key.
 struct PrefillMassPlan {
-    long long row_blocks, splits, units;
+    long long row_blocks, units, tiles;
     size_t sums_off, total;
 };
 
@@ -1716,10 +1717,9 @@ static bool prefill_mass_plan(int num_seqs, int max_query_len, int num_heads, in
     const long long tokens = kMassTiles * (kMassRows / (num_heads / num_kv_heads));
     w->row_blocks = (max_query_len + tokens - 1) / tokens;
     w->units = (long long)num_seqs * num_kv_heads * w->row_blocks;
-    const long long key_tiles = ((long long)max_blocks * kBlockSize + kMassKeys - 1) / kMassKeys;
-    w->splits = std::max(1LL, std::min((key_tiles + 1) / 2, 3LL * num_sms / w->units));
-    w->sums_off = round_up(sizeof(float2) * (size_t)w->units * w->splits * kMassTiles * kMassRows,
-                           256);
+    w->tiles = w->units * (((long long)max_blocks * kBlockSize + kMassKeys - 1) / kMassKeys);
+    w->sums_off = round_up(
+        sizeof(float2) * (size_t)(w->units + num_sms) * 2 * kMassTiles * kMassRows, 256);
     w->total = w->sums_off + sizeof(float) * (size_t)w->units * kMassTiles * max_blocks * kBlockSize;
     return true;
 }
@@ -1763,7 +1763,7 @@ int pa_prefill_mass(const struct pa_sparse_args *args)
     if (!prefill_mass_plan(a.num_seqs, a.max_query_len, a.num_heads, a.num_kv_heads,
                            a.max_blocks_per_seq, ds->num_sms, &w))
         return PA_ERR_INVALID_ARG;
-    if (w.units * w.splits >= (1LL << 31))
+    if (w.tiles >= (1LL << 31))          // the list of key tiles is counted in 32 bits
         return PA_ERR_UNSUPPORTED;
     if (!a.workspace || a.workspace_bytes < w.total || !aligned(a.workspace, 256))
         return PA_ERR_WORKSPACE;
@@ -1798,12 +1798,12 @@ int pa_prefill_mass(const struct pa_sparse_args *args)
     p.num_blocks = a.num_blocks;
     p.num_queries = a.num_queries;
     p.row_blocks = (int)w.row_blocks;
-    p.splits = (int)w.splits;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.decay = decay;
     cudaStream_t st = static_cast<cudaStream_t>(a.stream);
     void *kargs[] = {&p, &tmk};
-    const dim3 grid((unsigned)(w.units * w.splits));
+    // one block an SM, two key tiles each at least
+    const dim3 grid((unsigned)std::min((long long)ds->num_sms, (w.tiles + 1) / 2));
     rc = launch_dependent(k.stats, grid, dim3(k.threads), k.smem, st, kargs);
     if (rc == PA_OK)
         rc = launch_dependent(k.sums, grid, dim3(k.threads), k.smem, st, kargs);

@@ -102,15 +102,28 @@ decode_mass_finish_kernel(const DecodeMassParams p)
 
 // ---------------------------------------------------------------------------
 // A chunk of queries, on the fifth-generation tensor cores.  A unit of work is
-// 2 x 128 (token, head) rows of a (sequence, kv head); they stay in shared
-// memory while the sequence's keys stream past in 128-key tiles (TMA, a ring of
-// slots), a part of them per thread block.  Pass 1 (SUMS false) takes
-// S = Q.K^T, a thread a query row, and leaves each row's maximum and sum over its
-// part; pass 2 takes S^T = K.Q^T, a thread a key, so that the sum over the
-// queries is a sum over the thread's own columns, with the row's statistics read
-// from shared memory as a broadcast.  Scores live in tensor memory, two buffers
-// a query tile, so the MMAs of the next key tile run while the softmax warps
-// read this one.
+// 2 x 128 (token, head) rows of a (sequence, kv head); they stay in
+// place while the sequence's keys stream past in 128-key tiles (TMA, a ring of
+// slots).  Pass 1 (SUMS false) takes S = Q.K^T, a thread a query row, and leaves
+// each row's maximum and sum; pass 2 takes S^T = K.Q^T, a thread a key, so that
+// the sum over the queries is a sum over the thread's own columns, with the
+// row's statistics read from shared memory as a broadcast.
+//
+// Shared memory's bandwidth is what a 128 x 128 product of two operands there
+// uses up (128 bytes a cycle, before the copies): pass 1 keeps its query rows in
+// tensor memory, beside three buffers of scores that its query tiles take in
+// turn, and pass 2 multiplies a key tile by both query tiles at once (128 x 256),
+// two buffers.  Of each query tile every other key tile is read by a second set of
+// four softmax warps: with one set, two warps a scheduler, their latencies cost
+// as much as the products.
+//
+// The key tiles of all units form one list, ordered by sequence, kv head and
+// row block; each block of the persistent grid takes an equal share of it.  A
+// unit cut by a share's border has a piece in each of several blocks; piece
+// statistics go to slot (unit + block), which no two pieces have in common
+// since both grow along the list.  Pass 2 folds a unit's pieces when it loads its
+// rows, and reads each piece's keys from the last tile back: those are the ones
+// that pass 1 left in L2.
 // ---------------------------------------------------------------------------
 template <int D>
 struct MassShape {
@@ -118,23 +131,114 @@ struct MassShape {
     static constexpr int NB = BN / kBlockSize;
     static constexpr int HALVES = D / 64;
     static constexpr int BOX = 2048;                      // 16 rows x 128 B
-    static constexpr int Q_BYTES = BM * D * 2;            // [half][128 rows][128 B]
+    static constexpr int Q_BYTES = NG * BM * D * 2;       // pass 2: [half][256 rows][128 B]
     static constexpr int SLOT_BYTES = BN * D * 2;         // [half][8 blocks][16 rows][128 B]
     static constexpr int NSLOT = D == 128 ? 5 : 8;
-    static constexpr int OFF_SLOT = NG * Q_BYTES;
+    static constexpr int OFF_SLOT = Q_BYTES;
     static constexpr int OFF_LSE = OFF_SLOT + NSLOT * SLOT_BYTES;
-    // full[NSLOT] empty[NSLOT] s[NG][2] read[NG][2] q[NG] drain, then TMEM base, abort flag
-    static constexpr int NBAR = 2 * NSLOT + 5 * NG + 1;
+    // full[NSLOT] empty[NSLOT] s[4] read[3] q[2] free[2] group[2] drain, then TMEM base and
+    // abort flag
+    static constexpr int NBAR = 2 * NSLOT + 14;
+    // tensor memory: score buffers of 128 (pass 1) or 256 columns, pass 1's query rows
+    static constexpr uint32_t COL_Q = 384;
     static constexpr int OFF_BAR = OFF_LSE + NG * BM * 4;
     static constexpr int SMEM = 1024 + OFF_BAR + NBAR * 8 + 8;
-    static constexpr int THREADS = 64 + NG * 128;
+    static constexpr int THREADS = 64 + NG * 256;
     static_assert(SMEM <= 227 * 1024, "one block per SM");
 };
 
-__device__ __forceinline__ void group_sync(int grp)
+// A sequence's chunk: its first row of q, rows, length and row blocks (0: nothing to do).
+struct MassSeq {
+    int L, c, qs, blocks;
+};
+
+__device__ __forceinline__ MassSeq mass_seq(const PrefillMassParams &p, int s, int TPB, bool report)
 {
-    asm volatile("bar.sync %0, 128;" ::"r"(1 + grp) : "memory");
+    MassSeq x;
+    x.L = __ldg(p.seq_lens + s);
+    x.qs = __ldg(p.query_start + s);
+    x.c = __ldg(p.query_start + s + 1) - x.qs;
+    x.blocks = 0;
+    if (x.L < 0 || x.L > p.max_blocks * kBlockSize) {
+        if (report)
+            record_error(p.err, PA_DEVERR_SEQLEN_RANGE);
+    } else if (x.c < 0 || x.c > x.L || x.qs < 0 || x.c > p.num_queries - x.qs ||
+               (x.c + TPB - 1) / TPB > p.row_blocks) {
+        if (report)
+            record_error(p.err, PA_DEVERR_QUERY_RANGE);
+    } else {
+        x.blocks = (x.c + TPB - 1) / TPB;
+    }
+    return x;
 }
+
+// Key tiles that row block b sees: up to its last row.
+__device__ __forceinline__ int mass_tiles(const MassSeq &x, int b, int TPB)
+{
+    return (x.L - x.c + min((b + 1) * TPB, x.c) - 1) / kMassKeys + 1;
+}
+
+__device__ __forceinline__ int mass_tiles(const MassSeq &x, int TPB)
+{
+    int n = 0;
+    for (int b = 0; b < x.blocks; ++b)
+        n += mass_tiles(x, b, TPB);
+    return n;
+}
+
+// One thread block's way along the list of key tiles.
+struct MassWalker {
+    MassSeq x;
+    int s, h, b;                   // sequence, kv head, row block
+    int first, nt;                 // the unit's first tile in the list, its tiles
+    int tb, te;                    // this piece's tiles of the unit
+    int end;                       // of the share
+    bool valid;
+
+    __device__ __forceinline__ void piece(int TPB, int from)
+    {
+        nt = mass_tiles(x, b, TPB);
+        tb = from - first;
+        te = min(nt, end - first);
+    }
+
+    // Start at place `at` of the list; sequence s0 begins at `from`.
+    __device__ __forceinline__ void init(const PrefillMassParams &p, int TPB, int s0, int from,
+                                         int at, int end_)
+    {
+        end = end_;
+        valid = at < end;
+        if (!valid)
+            return;
+        s = s0;
+        x = mass_seq(p, s, TPB, false);
+        const int per = mass_tiles(x, TPB);
+        h = (at - from) / per;
+        first = from + h * per;
+        b = 0;
+        while (first + mass_tiles(x, b, TPB) <= at)
+            first += mass_tiles(x, b++, TPB);
+        piece(TPB, at);
+    }
+
+    __device__ __forceinline__ void next(const PrefillMassParams &p, int TPB)
+    {
+        first += nt;
+        valid = first < end;
+        if (!valid)
+            return;
+        if (++b == x.blocks) {
+            b = 0;
+            if (++h == p.num_kv_heads) {
+                h = 0;
+                do
+                    x = mass_seq(p, ++s, TPB, false);
+                while (x.blocks == 0);
+            }
+        }
+        piece(TPB, first);
+    }
+};
 
 template <typename T, int D, bool SUMS>
 __global__ void __launch_bounds__(MassShape<D>::THREADS)
@@ -143,8 +247,9 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
     using Sh = MassShape<D>;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr uint32_t FULL = 0xffffffffu;
-    constexpr int NS = Sh::NSLOT;
+    constexpr int NS = Sh::NSLOT, NTH = Sh::THREADS, ROWS = Sh::NG * Sh::BM;
     extern __shared__ unsigned char smem_raw[];
+    __shared__ int scan[NTH / 32], start_seq, start_at;
     const uint32_t raw_addr = smem_addr(smem_raw);
     unsigned char *smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
     const uint32_t sbase = smem_addr(smem), slot_addr = sbase + Sh::OFF_SLOT;
@@ -152,10 +257,14 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
     const uint32_t bar_addr = sbase + Sh::OFF_BAR;
     auto full_bar = [&](int s) { return bar_addr + 8u * s; };
     auto empty_bar = [&](int s) { return bar_addr + 8u * (NS + s); };
-    auto s_bar = [&](int g, int b) { return bar_addr + 8u * (2 * NS + 2 * g + b); };
-    auto read_bar = [&](int g, int b) { return bar_addr + 8u * (2 * NS + 4 + 2 * g + b); };
-    auto q_bar = [&](int g) { return bar_addr + 8u * (2 * NS + 8 + g); };
-    const uint32_t drain_bar = bar_addr + 8u * (2 * NS + 10);
+    // scores are there for a set of softmax warps (pass 1: 2 * query tile + set); a buffer
+    // has been read; query rows are there; a piece's products have ended
+    auto s_bar = [&](int i) { return bar_addr + 8u * (2 * NS + i); };
+    auto read_bar = [&](int b) { return bar_addr + 8u * (2 * NS + 4 + b); };
+    auto q_bar = [&](int g) { return bar_addr + 8u * (2 * NS + 7 + g); };
+    auto free_bar = [&](int g) { return bar_addr + 8u * (2 * NS + 9 + g); };
+    auto group_bar = [&](int g) { return bar_addr + 8u * (2 * NS + 11 + g); };
+    const uint32_t drain_bar = bar_addr + 8u * (2 * NS + 13);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Sh::OFF_BAR + Sh::NBAR * 8);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -163,63 +272,73 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
     const int Hkv = p.num_kv_heads, Hq = p.num_heads, G = Hq / Hkv;
     const int TPG = Sh::BM / G, TPB = Sh::NG * TPG;       // chunk tokens of a tile, of a unit
     grid_dependents_launch();
-    grid_dependency_wait();
-    // blocks of one (sequence, head, part of the keys) lie side by side
-    int b = blockIdx.x;
-    const int rank = b % p.row_blocks;
-    b /= p.row_blocks;
-    const int split = b % p.splits;
-    b /= p.splits;
-    const int h = b % Hkv, s = b / Hkv;
-    const int L = __ldg(p.seq_lens + s);
-    const int qs = __ldg(p.query_start + s);
-    const int c = __ldg(p.query_start + s + 1) - qs;
-    const bool reporter = !SUMS && rank == 0 && split == 0 && h == 0 && tid == 0;
-    if (L < 0 || L > p.max_blocks * kBlockSize) {
-        if (reporter)
-            record_error(p.err, PA_DEVERR_SEQLEN_RANGE);
-        return;
-    }
-    if (c < 0 || c > L || qs < 0 || c > p.num_queries - qs || (c + TPB - 1) / TPB > p.row_blocks) {
-        if (reporter)
-            record_error(p.err, PA_DEVERR_QUERY_RANGE);
-        return;
-    }
-    const int t0 = rank * TPB;
-    if (t0 >= c)
-        return;
-    const int t_end = min(t0 + TPB, c);
-    const int ng = t_end - t0 > TPG ? 2 : 1;              // query tiles with rows
-    const int base = L - c + t0;                          // position of the unit's first token
-    const int nt = (L - c + t_end - 1) / Sh::BN + 1;
-    const int j0 = (int)((long long)nt * split / p.splits);
-    const int ntl = (int)((long long)nt * (split + 1) / p.splits) - j0;   // this block's tiles
-    const int nblk = (L + kBlockSize - 1) / kBlockSize;
-    const size_t unit = ((size_t)s * Hkv + h) * p.row_blocks + rank;
-    if (ntl == 0) {
-        // nothing here: an empty part of every row
-        if (!SUMS)
-            for (int i = tid; i < Sh::NG * Sh::BM; i += Sh::THREADS)
-                p.stats[(unit * p.splits + split) * (Sh::NG * Sh::BM) + i] =
-                    make_float2(-INFINITY, 0.f);
-        return;
-    }
-
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(full_bar(i), 1);
             mbar_init(empty_bar(i), 1);
         }
+        for (int i = 0; i < 4; ++i)
+            mbar_init(s_bar(i), 1);
+        for (int i = 0; i < 3; ++i)
+            mbar_init(read_bar(i), SUMS ? 256 : 128);
         for (int g = 0; g < Sh::NG; ++g) {
-            for (int i = 0; i < 2; ++i) {
-                mbar_init(s_bar(g, i), 1);
-                mbar_init(read_bar(g, i), 128);
-            }
-            mbar_init(q_bar(g), Sh::NG * 128);
+            mbar_init(q_bar(g), SUMS ? 512 : 256);
+            mbar_init(free_bar(g), 1);
+            mbar_init(group_bar(g), 256);
         }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
         mbar_init_fence();
+    }
+    grid_dependency_wait();
+
+    // ---- the block's share: the list's length, then the sequence its share starts in ----
+    auto tiles_of = [&](int s, bool report) {
+        const MassSeq x = mass_seq(p, s, TPB, report);
+        return Hkv * mass_tiles(x, TPB);
+    };
+    int total = 0;
+    const int mine = tid < p.num_seqs ? tiles_of(tid, !SUMS && blockIdx.x == 0) : 0;
+    for (int s = tid + NTH; s < p.num_seqs; s += NTH)
+        total += tiles_of(s, !SUMS && blockIdx.x == 0);
+    total = __reduce_add_sync(FULL, total + mine);
+    if (lane == 0)
+        scan[warp] = total;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < NTH / 32; ++w)
+        total += scan[w];
+    const int R = max((total + (int)gridDim.x - 1) / (int)gridDim.x, 2);
+    const long long share = (long long)blockIdx.x * R;
+    if (share >= total)
+        return;
+    const int at = (int)share, end = (int)min((long long)total, share + R);
+    int carry = 0;
+    for (int s0 = 0; s0 < p.num_seqs && carry <= at; s0 += NTH) {
+        const int s = s0 + tid;
+        const int n = s0 == 0 ? mine : s < p.num_seqs ? tiles_of(s, false) : 0;
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(FULL, incl, o);
+            if (lane >= o)
+                incl += y;
+        }
+        __syncthreads();                          // scan has been read
+        if (lane == 31)
+            scan[warp] = incl;
+        __syncthreads();
+        int before = carry + incl - n;
+#pragma unroll
+        for (int w = 0; w < NTH / 32; ++w) {
+            before += w < warp ? scan[w] : 0;
+            carry += scan[w];
+        }
+        if (n > 0 && before <= at && at < before + n) {
+            start_seq = s;
+            start_at = before;
+        }
     }
     if (warp == 1) {
         tc::tmem_alloc(smem_addr(tmem_slot), 512);
@@ -229,103 +348,139 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
+    MassWalker w;
+    w.init(p, TPB, start_seq, start_at, at, end);
     auto give_up = [&]() {
         *abort_flag = 1;
         record_error(p.err, PA_DEVERR_TIMEOUT);
     };
+    // query tiles of the piece's unit that have rows
+    auto groups = [&]() { return w.x.c - w.b * TPB > TPG ? 2 : 1; };
+    // the piece's i-th key tile
+    auto tile = [&](int i) { return SUMS ? w.te - 1 - i : w.tb + i; };
 
     if (warp == 0) {
         // ---------------- producer: key tiles into the ring ----------------
-        // lane l holds the pool row of block NB * win + l of a window of WT tiles; lane 0
-        // waits for the slot, lanes (half, block) issue the boxes
+        // lane l holds the pool row of block NB * win + l of a window of WT tiles, and the next
+        // window's table entries are in flight; lane 0 waits for the slot, lanes (half,
+        // block) issue the boxes
         constexpr int NB = Sh::NB, WT = 32 / NB;
-        const int32_t *table = p.block_tables + (size_t)s * p.max_blocks;
-        auto fetch = [&](int w0) {
-            const int lb = NB * w0 + lane;
-            return lb < nblk ? __ldg(table + lb) : 0;
-        };
-        auto to_row = [&](int w0, int phys) {
-            if (NB * w0 + lane >= nblk)
-                return -1;
-            if ((unsigned)phys >= (unsigned)p.num_blocks) {
-                record_error(p.err, PA_DEVERR_TABLE_RANGE);
-                phys = 0;
+        int it = 0, last = -1;                    // last: the last tile in this lane's slot
+        bool ok = true;
+        for (; ok && w.valid; w.next(p, TPB)) {
+            const int nblk = (w.x.L + kBlockSize - 1) / kBlockSize;
+            const int32_t *table = p.block_tables + (size_t)w.s * p.max_blocks;
+            auto fetch = [&](int w0) {
+                const int lb = NB * w0 + lane;
+                return w0 >= 0 && lb < nblk ? __ldg(table + lb) : 0;
+            };
+            auto to_row = [&](int w0, int phys) {
+                if (NB * w0 + lane >= nblk)
+                    return -1;
+                if ((unsigned)phys >= (unsigned)p.num_blocks) {
+                    record_error(p.err, PA_DEVERR_TABLE_RANGE);
+                    phys = 0;
+                }
+                return (phys * Hkv + w.h) * kBlockSize;
+            };
+            const int step = SUMS ? -WT : WT;
+            int win = tile(0) / WT * WT;
+            int cur = to_row(win, fetch(win));
+            int nxt = fetch(win + step);
+            for (int i = 0; i < w.te - w.tb; ++i, ++it) {
+                const int j = tile(i), sl = it % NS;
+                if (j / WT * WT != win) {
+                    win += step;
+                    cur = to_row(win, nxt);
+                    nxt = fetch(win + step);
+                }
+                bool ready = true;
+                if (lane == 0)
+                    ready = !*abort_flag &&
+                            (it < NS || mbar_wait_bounded(empty_bar(sl), ((it / NS) - 1) & 1));
+                if (!__shfl_sync(FULL, ready, 0)) {
+                    if (lane == 0 && !*abort_flag)
+                        give_up();
+                    ok = false;
+                    break;
+                }
+                const int nv = min(NB, nblk - NB * j);
+                if (lane == 0)
+                    mbar_arrive_expect_tx(full_bar(sl), (uint32_t)(nv * Sh::HALVES * Sh::BOX));
+                const int bb = lane % NB, hf = lane / NB;
+                const int row = __shfl_sync(FULL, cur, NB * (j - win) + bb);
+                __syncwarp();
+                if (hf < Sh::HALVES && row >= 0)
+                    tma_load_2d(slot_addr + sl * Sh::SLOT_BYTES + (hf * NB + bb) * Sh::BOX, &tmk,
+                                64 * hf, row, full_bar(sl));
+                if (lane == sl)
+                    last = it;
             }
-            return (phys * Hkv + h) * kBlockSize;
-        };
-        int win = j0;
-        int cur = to_row(j0, fetch(j0));
-        int nxt = fetch(j0 + WT);
-        int last = -1;
-        for (int i = 0; i < ntl; ++i) {
-            const int j = j0 + i, sl = i % NS;
-            if (j == win + WT) {
-                win += WT;
-                cur = to_row(win, nxt);
-                nxt = fetch(win + WT);
-            }
-            bool ready = true;
-            if (lane == 0)
-                ready = !*abort_flag &&
-                        (i < NS || mbar_wait_bounded(empty_bar(sl), ((i / NS) - 1) & 1));
-            if (!__shfl_sync(FULL, ready, 0)) {
-                if (lane == 0 && !*abort_flag)
-                    give_up();
-                break;
-            }
-            const int nv = min(NB, nblk - NB * j);
-            if (lane == 0)
-                mbar_arrive_expect_tx(full_bar(sl), (uint32_t)(nv * Sh::HALVES * Sh::BOX));
-            const int bb = lane % NB, hf = lane / NB;
-            const int row = __shfl_sync(FULL, cur, NB * (j - win) + bb);
-            __syncwarp();
-            if (hf < Sh::HALVES && row >= 0)
-                tma_load_2d(slot_addr + sl * Sh::SLOT_BYTES + (hf * NB + bb) * Sh::BOX, &tmk,
-                            64 * hf, row, full_bar(sl));
-            if (lane == sl)
-                last = i;
         }
         // every issued copy lands before the block may exit
         if (lane < NS && last >= 0 && !mbar_wait_bounded(full_bar(lane), (last / NS) & 1))
             give_up();
     } else if (warp == 1) {
         // ---------------- MMA issuer ----------------
-        constexpr uint32_t id = tc::idesc_f16(kBf16, 128, 128, false, false);
+        constexpr uint32_t id128 = tc::idesc_f16(kBf16, 128, 128, false, false);
+        constexpr uint32_t id256 = tc::idesc_f16(kBf16, 128, 256, false, false);
         const uint64_t q_desc = tc::sdesc_sw128(sbase, 16, 1024);
         const uint64_t k_desc = tc::sdesc_sw128(slot_addr, 16, 1024);
         auto wait_all = [&](uint32_t bar, uint32_t parity) {
             return __all_sync(FULL, mbar_wait_bounded(bar, parity));
         };
         bool ok = true;
-        for (int i = 0; ok && i < ntl; ++i) {
-            const int sl = i % NS, buf = i & 1;
-            if (__any_sync(FULL, *abort_flag != 0)) {
-                ok = false;
-                break;
-            }
-            for (int g = 0; ok && g < ng; ++g) {
-                if (i == 0)
-                    ok = wait_all(q_bar(g), 0);
-                if (ok && i >= 2)                        // the tile two before has been read
-                    ok = wait_all(read_bar(g, buf), ((i >> 1) - 1) & 1);
-                ok = ok && wait_all(full_bar(sl), (i / NS) & 1);
-                if (!ok)
-                    break;
-                tc::fence_after_sync();
-                const uint64_t qd = q_desc + (uint64_t)((g * Sh::Q_BYTES) >> 4);
+        int it = 0;                               // key tiles so far
+        int rows[Sh::NG] = {0, 0};                // units so far of each query tile
+        uint32_t used = 0, turns = 0;             // of each score buffer: used yet, parity
+        for (; ok && w.valid; w.next(p, TPB)) {
+            const int ng = groups();
+            for (int i = 0; ok && i < w.te - w.tb; ++i, ++it) {
+                const int sl = it % NS;
                 const uint64_t kd = k_desc + (uint64_t)((sl * Sh::SLOT_BYTES) >> 4);
-                const uint32_t d = tmem + g * 256 + buf * 128;
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint64_t ko = (uint64_t)(((k & 3) * 32 + (k >> 2) * (128 * 128)) >> 4);
-                    if (SUMS)
-                        tc::mma_ss_warp(d, kd + ko, qd + ko, id, k > 0);
-                    else
-                        tc::mma_ss_warp(d, qd + ko, kd + ko, id, k > 0);
+                if (__any_sync(FULL, *abort_flag != 0)) {
+                    ok = false;
+                    break;
                 }
-                tc::commit_warp(s_bar(g, buf));
-                if (g == ng - 1)
-                    tc::commit_warp(empty_bar(sl));
+                // a K step: 32 bytes along the 128-byte row; the next 64 channels are a half
+                // further
+#pragma unroll
+                for (int g = 0; g < (SUMS ? 1 : Sh::NG); ++g) {
+                    if (g >= ng || !ok)
+                        continue;
+                    const int buf = SUMS ? it & 1 : ng == 2 ? (2 * i + g) % 3 : i & 1;
+                    if (i == 0)
+                        ok = wait_all(q_bar(g), rows[g]++ & 1);
+                    // The buffer's last scores have been read.  With them all that its set of
+                    // warps was given before: a set never has two tiles ahead of it, whose
+                    // barrier's phases it could not tell apart.
+                    if (ok && (used >> buf & 1))
+                        ok = wait_all(read_bar(buf), ~turns >> buf & 1);
+                    used |= 1u << buf;
+                    turns ^= 1u << buf;
+                    ok = ok && wait_all(full_bar(sl), (it / NS) & 1);
+                    if (!ok)
+                        continue;
+                    tc::fence_after_sync();
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint64_t ko =
+                            (uint64_t)(((k & 3) * 32 + (k >> 2) * (128 * 128)) >> 4);
+                        if (SUMS)
+                            tc::mma_ss_warp(
+                                tmem + 256 * buf, kd + ko,
+                                q_desc + (uint64_t)(((k & 3) * 32 + (k >> 2) * (256 * 128)) >> 4),
+                                ng == 2 ? id256 : id128, k > 0);
+                        else
+                            tc::mma_ts_warp(tmem + 128 * buf, tmem + Sh::COL_Q + 64 * g + 8 * k,
+                                            kd + ko, id128, k > 0);
+                    }
+                    tc::commit_warp(s_bar(SUMS ? buf : 2 * g + (i & 1)));
+                    if (SUMS || g == ng - 1)
+                        tc::commit_warp(empty_bar(sl));
+                    if (i == w.te - w.tb - 1)
+                        tc::commit_warp(free_bar(g));
+                }
             }
         }
         if (!ok && lane == 0)
@@ -335,146 +490,212 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
         if (!wait_all(drain_bar, 0) && lane == 0)
             give_up();
     } else {
-        // ---------------- query rows -> shared memory ----------------
-        // K-major, 128-byte swizzle.  Row rr of tile g = (token t0 + g TPG + rr / G, head
-        // rr % G); rows past the chunk and those that do not fill a token are zero.
-        {
-            constexpr int CPR = D / 8, RSTEP = Sh::NG * 128 / CPR;
-            constexpr int NPT = Sh::NG * Sh::BM / RSTEP, PER_G = NPT / Sh::NG;
-            const T *qg = static_cast<const T *>(p.q);
-            const int lt = tid - 64, ch = lt % CPR, hf = ch >> 3, c8 = ch & 7;
-            uint4 qv[NPT];
-#pragma unroll
-            for (int i = 0; i < NPT; ++i) {
-                const int r = lt / CPR + i * RSTEP, g = r / Sh::BM, rr = r % Sh::BM;
-                const int tok = g * TPG + rr / G, hg = rr % G;
-                qv[i] = make_uint4(0, 0, 0, 0);
-                if (rr < TPG * G && t0 + tok < c)
-                    qv[i] = __ldg(reinterpret_cast<const uint4 *>(
-                        qg + ((size_t)(qs + t0 + tok) * Hq + h * G + hg) * D + ch * 8));
-            }
-#pragma unroll
-            for (int i = 0; i < NPT; ++i) {
-                const int r = lt / CPR + i * RSTEP, g = r / Sh::BM, rr = r % Sh::BM;
-                *reinterpret_cast<uint4 *>(smem + g * Sh::Q_BYTES + hf * (Sh::BM * 128) +
-                                           rr * 128 + ((c8 ^ (rr & 7)) << 4)) = qv[i];
-                if (i % PER_G == PER_G - 1) {
-                    fence_proxy_async_shared();
-                    mbar_arrive(q_bar(i / PER_G));
-                }
-            }
-        }
-        const int grp = (warp - 2) >> 2;
+        const int grp = (warp - 2) >> 3, set = ((warp - 2) >> 2) & 1;
         const int q4 = warp & 3;                          // TMEM lane quarter of this warp
         const int rr = q4 * 32 + lane;                    // this thread's TMEM lane
-        const uint32_t tg = tmem + ((uint32_t)(q4 * 32) << 16) + grp * 256;
-        const int tok = grp * TPG + rr / G;
-        const bool row_valid = rr < TPG * G && t0 + tok < t_end;
+        const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
         const float sl2 = p.scale_log2;
         const uint64_t sl2x2 = f2_pack(sl2, sl2);
-        const size_t stat0 = unit * p.splits * (Sh::NG * Sh::BM) + grp * Sh::BM + rr;
-        float m = -INFINITY, l = 0.f;
-        if (SUMS) {
-            // minus log2 of the row's sum over all parts; rows that are none: -inf
-            float M = -INFINITY;
-            for (int i = 0; i < p.splits; ++i) {
-                const float2 a = __ldcg(p.stats + stat0 + (size_t)i * (Sh::NG * Sh::BM));
-                const float nM = fmaxf(M, a.x);
-                if (nM > -INFINITY)
-                    l = l * exp2f(M - nM) + a.y * exp2f(a.x - nM);
-                M = nM;
-            }
-            lse[grp * Sh::BM + rr] = row_valid ? -(M + log2f(l)) : -INFINITY;
-            group_sync(grp);
-        }
-        float *sums = p.sums + (((size_t)s * Hkv + h) * (2 * p.row_blocks) + 2 * rank + grp) *
-                                   ((size_t)p.max_blocks * kBlockSize);
         bool ok = true;
-        for (int i = 0; grp < ng && i < ntl; ++i) {
-            const int buf = i & 1, k0 = (j0 + i) * Sh::BN;
-            if (__any_sync(FULL, *abort_flag != 0) ||
-                !__all_sync(FULL, mbar_wait_bounded(s_bar(grp, buf), (i >> 1) & 1))) {
+        int n0 = 0;                                       // key tiles before this piece
+        int turns = 0;                                    // of this set so far
+        int units = 0;                                    // this query tile's (pass 2: all) so far
+        int met = 0;
+        // the query tile's threads meet; bounded, since a warp that gave up does not come
+        auto meet = [&]() {
+            mbar_arrive(group_bar(grp));
+            return __all_sync(FULL, mbar_wait_bounded(group_bar(grp), met++ & 1));
+        };
+        for (; ok && w.valid; n0 += w.te - w.tb, w.next(p, TPB)) {
+            const int ng = groups();
+            if (!SUMS && grp >= ng)
+                continue;
+            const int t0 = w.b * TPB + grp * TPG;         // the tile's first chunk token
+            // ---- query rows ----
+            // Row r = (token t0 + r / G, head r % G); rows past the chunk and those that do not
+            // fill a token are zero.  The products of the piece before have ended.
+            if ((SUMS || set == 0) && units > 0 &&
+                !__all_sync(FULL, mbar_wait_bounded(free_bar(SUMS ? 0 : grp), (units - 1) & 1))) {
                 ok = false;
                 break;
             }
-            tc::fence_after_sync();
-            uint32_t v[2][64];
-            __syncwarp();
-            tc::tmem_ld64(tg + buf * 128, v[0]);
-            tc::tmem_ld64(tg + buf * 128 + 64, v[1]);
-            tc::fence_before_sync();
-            mbar_arrive(read_bar(grp, buf));
-            float mref = 0.f;
+            ++units;
+            const T *qg = static_cast<const T *>(p.q);
+            if (!SUMS && set == 0) {
+                // to tensor memory, a thread its lane's row
+                uint32_t x[D / 2];
+                const int tok = t0 + rr / G;
+                const bool on = rr < TPG * G && tok < w.x.c;
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    qg + ((size_t)(w.x.qs + (on ? tok : 0)) * Hq + w.h * G + rr % G) * D);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint4 y = on ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                    x[4 * i] = y.x, x[4 * i + 1] = y.y, x[4 * i + 2] = y.z, x[4 * i + 3] = y.w;
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i)
+                    tc::tmem_st32(tl + Sh::COL_Q + 64 * grp + 32 * i,
+                                  *reinterpret_cast<const uint32_t(*)[32]>(x + 32 * i));
+                tc::fence_before_sync();
+            }
             if (!SUMS) {
-                // keys [0, vis] of the tile are visible to this row
-                const int vis = row_valid ? base + tok - k0 : -1;
-                if (!__all_sync(FULL, vis >= Sh::BN - 1)) {
-#pragma unroll
-                    for (int e = 0; e < Sh::BN; ++e)
-                        if (e > vis)
-                            v[e >> 6][e & 63] = __float_as_uint(-INFINITY);
-                }
-                float mx[8];
-#pragma unroll
-                for (int a = 0; a < 8; ++a) {
-                    auto x = [&](int q) { return __uint_as_float(v[q >> 6][q & 63]); };
-                    float t = fmax3(x(a), x(a + 8), x(a + 16));
-#pragma unroll
-                    for (int q = a + 24; q < 120; q += 16)
-                        t = fmax3(t, x(q), x(q + 8));
-                    mx[a] = fmaxf(t, x(a + 120));
-                }
-                const float mt = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
-                                       fmaxf(mx[6], mx[7])) * sl2;    // scale > 0
-                if (mt > m) {
-                    l *= ex2_approx(m - mt);
-                    m = mt;
-                }
-                mref = m == -INFINITY ? 0.f : m;          // nothing seen yet: weights of zero
-            } else {
-                // columns [first, 128) of the tile see this key
-                const int first = min(max(k0 + rr - base - grp * TPG, 0), 128) * G;
-                if (!__all_sync(FULL, first <= 0)) {
-#pragma unroll
-                    for (int e = 0; e < 128; ++e)
-                        if (e < first)
-                            v[e >> 6][e & 63] = __float_as_uint(-INFINITY);
+                // the other set says that it has read all tiles before, and goes on with the
+                // first: it may have none in this piece, and would arrive for the next one
+                mbar_arrive(q_bar(grp));
+                if (set == 1 && !__all_sync(FULL, mbar_wait_bounded(q_bar(grp), (units - 1) & 1))) {
+                    ok = false;
+                    break;
                 }
             }
-            uint64_t sum2[4] = {0, 0, 0, 0};
-            const uint64_t nm2 = f2_pack(-mref, -mref);
-            const float4 *ls = reinterpret_cast<const float4 *>(lse + grp * Sh::BM);
+            if (SUMS) {
+                // to shared memory: K-major, 128-byte swizzle
+                constexpr int CPR = D / 8, RSTEP = 256 / CPR, NPT = Sh::BM / RSTEP;
+                const int lt = (tid - 64) & 255, ch = lt % CPR, hf = ch >> 3, c8 = ch & 7;
+                uint4 qv[NPT];
 #pragma unroll
-            for (int e = 0; e < 128; e += 4) {
-                uint64_t na = nm2, nb = nm2;
-                if (SUMS) {
-                    const float4 x = ls[e / 4];
-                    na = f2_pack(x.x, x.y);
-                    nb = f2_pack(x.z, x.w);
+                for (int i = 0; i < NPT; ++i) {
+                    const int r = lt / CPR + i * RSTEP, tok = t0 + r / G;
+                    qv[i] = make_uint4(0, 0, 0, 0);
+                    if (r < TPG * G && tok < w.x.c)
+                        qv[i] = __ldg(reinterpret_cast<const uint4 *>(
+                            qg + ((size_t)(w.x.qs + tok) * Hq + w.h * G + r % G) * D + ch * 8));
                 }
-                float y0, y1, y2, y3;
-                f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e >> 6][e & 63]),
-                                         __uint_as_float(v[e >> 6][(e & 63) + 1])), sl2x2, na),
-                          y0, y1);
-                f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e >> 6][(e & 63) + 2]),
-                                         __uint_as_float(v[e >> 6][(e & 63) + 3])), sl2x2, nb),
-                          y2, y3);
-                sum2[(e >> 2) & 1] =
-                    f2_add(sum2[(e >> 2) & 1], f2_pack(ex2_approx(y0), ex2_approx(y1)));
-                sum2[2 + ((e >> 2) & 1)] =
-                    f2_add(sum2[2 + ((e >> 2) & 1)], f2_pack(ex2_approx(y2), ex2_approx(y3)));
+#pragma unroll
+                for (int i = 0; i < NPT; ++i) {
+                    const int r = grp * Sh::BM + lt / CPR + i * RSTEP;
+                    *reinterpret_cast<uint4 *>(smem + hf * (256 * 128) + r * 128 +
+                                               ((c8 ^ (r & 7)) << 4)) = qv[i];
+                }
+                fence_proxy_async_shared();
+                mbar_arrive(q_bar(0));
             }
-            float a, bsum;
-            f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), a, bsum);
-            if (!SUMS)
-                l += a + bsum;
-            else if (k0 + rr < L)
-                sums[k0 + rr] = a + bsum;
+            const int tok = t0 + rr / G;
+            const bool row_valid = rr < TPG * G && tok < w.x.c;
+            const int unit = (w.s * Hkv + w.h) * p.row_blocks + w.b;
+            // a piece's statistics: [set][query tile][row]
+            float2 *stats = p.stats + (size_t)unit * (2 * ROWS) + grp * Sh::BM + rr;
+            float m = -INFINITY, l = 0.f;
+            if (SUMS) {
+                // minus log2 of the row's sum over the unit's pieces; rows that are none: -inf
+                float M = -INFINITY;
+                const int k1 = set ? -1 : (w.first + w.nt - 1) / R;
+                for (int k = w.first / R; k <= k1; ++k)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 a = __ldcg(stats + (size_t)k * (2 * ROWS) + i * ROWS);
+                        const float nM = fmaxf(M, a.x);
+                        if (nM > -INFINITY)
+                            l = l * exp2f(M - nM) + a.y * exp2f(a.x - nM);
+                        M = nM;
+                    }
+                ok = meet();                              // all are done with the piece before
+                if (!set)
+                    lse[grp * Sh::BM + rr] = row_valid ? -(M + log2f(l)) : -INFINITY;
+                ok = ok && meet();
+                if (!ok)
+                    break;
+            }
+            float *sums = p.sums + (((size_t)w.s * Hkv + w.h) * (2 * p.row_blocks) + 2 * w.b + grp) *
+                                       ((size_t)p.max_blocks * kBlockSize);
+            const int first_pos = w.x.L - w.x.c + t0;     // of the tile's first token
+            for (int i = 0; i < w.te - w.tb; ++i) {
+                const int k0 = tile(i) * Sh::BN;
+                const int buf = SUMS ? (n0 + i) & 1 : ng == 2 ? (2 * i + grp) % 3 : i & 1;
+                if (((SUMS ? n0 + i : i) & 1) != set)     // the other set's
+                    continue;
+                if (__any_sync(FULL, *abort_flag != 0) ||
+                    !__all_sync(FULL, mbar_wait_bounded(s_bar(SUMS ? set : 2 * grp + set),
+                                                        turns++ & 1))) {
+                    ok = false;
+                    break;
+                }
+                if (grp >= ng) {
+                    mbar_arrive(read_bar(buf));
+                    continue;
+                }
+                tc::fence_after_sync();
+                const uint32_t tg = tl + (SUMS ? 256 * buf + 128 * grp : 128 * buf);
+                // rows: keys [0, vis] of the tile are visible; keys: columns [first, 128) see it
+                const int vis = row_valid ? first_pos + rr / G - k0 : -1;
+                const int first = min(max(k0 + rr - first_pos, 0), 128) * G;
+                const bool full = __all_sync(FULL, SUMS ? first <= 0 : vis >= Sh::BN - 1);
+                float total_sum = 0.f;
+#pragma unroll
+                for (int hb = 0; hb < 2; ++hb) {
+                    uint32_t v[64];
+                    __syncwarp();
+                    tc::tmem_ld64(tg + 64 * hb, v);
+                    if (hb == 1) {
+                        tc::fence_before_sync();
+                        mbar_arrive(read_bar(buf));
+                    }
+                    if (!full) {
+#pragma unroll
+                        for (int e = 0; e < 64; ++e)
+                            if (SUMS ? e + 64 * hb < first : e + 64 * hb > vis)
+                                v[e] = __float_as_uint(-INFINITY);
+                    }
+                    float mref = 0.f;
+                    if (!SUMS) {
+                        float mx[4];
+#pragma unroll
+                        for (int a = 0; a < 4; ++a) {
+                            auto x = [&](int q) { return __uint_as_float(v[q]); };
+                            float t = fmax3(x(a), x(a + 4), x(a + 8));
+#pragma unroll
+                            for (int q = a + 12; q < 60; q += 8)
+                                t = fmax3(t, x(q), x(q + 4));
+                            mx[a] = fmaxf(t, x(a + 60));
+                        }
+                        const float mt =
+                            fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * sl2;    // scale > 0
+                        if (mt > m) {
+                            l *= ex2_approx(m - mt);
+                            m = mt;
+                        }
+                        mref = m == -INFINITY ? 0.f : m;  // nothing seen yet: weights of zero
+                    }
+                    uint64_t sum2[4] = {0, 0, 0, 0};
+                    const uint64_t nm2 = f2_pack(-mref, -mref);
+                    const float4 *ls =
+                        reinterpret_cast<const float4 *>(lse + grp * Sh::BM + 64 * hb);
+#pragma unroll
+                    for (int e = 0; e < 64; e += 4) {
+                        uint64_t na = nm2, nb = nm2;
+                        if (SUMS) {
+                            const float4 x = ls[e / 4];
+                            na = f2_pack(x.x, x.y);
+                            nb = f2_pack(x.z, x.w);
+                        }
+                        float y0, y1, y2, y3;
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])),
+                                         sl2x2, na),
+                                  y0, y1);
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e + 2]),
+                                                 __uint_as_float(v[e + 3])),
+                                         sl2x2, nb),
+                                  y2, y3);
+                        const int o = (e >> 2) & 1;
+                        sum2[o] = f2_add(sum2[o], f2_pack(ex2_approx(y0), ex2_approx(y1)));
+                        sum2[2 + o] = f2_add(sum2[2 + o], f2_pack(ex2_approx(y2), ex2_approx(y3)));
+                    }
+                    float a, b;
+                    f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), a, b);
+                    if (SUMS)
+                        total_sum += a + b;
+                    else
+                        l += a + b;
+                }
+                if (SUMS && k0 + rr < w.x.L)
+                    sums[k0 + rr] = total_sum;
+            }
+            if (ok && !SUMS)
+                stats[(size_t)blockIdx.x * (2 * ROWS) + set * ROWS] = make_float2(m, l);
         }
         if (!ok)
             give_up();
-        else if (!SUMS && grp < ng)
-            p.stats[stat0 + (size_t)split * (Sh::NG * Sh::BM)] = make_float2(m, l);
     }
 
     tc::fence_before_sync();
@@ -501,13 +722,9 @@ prefill_mass_finish_kernel(const PrefillMassParams p)
     for (int begin = 0; begin < p.num_seqs; begin += kRaggedSeqs) {
         const int n = min(kRaggedSeqs, p.num_seqs - begin);
         ragged_prefix<NTH>(sm, begin, n, [&](int s) {
-            const int L = __ldg(p.seq_lens + s), qs = __ldg(p.query_start + s);
-            const int c = __ldg(p.query_start + s + 1) - qs;
             // what the passes skipped stays as it was
-            return L < 0 || L > T || c <= 0 || c > L || qs < 0 || c > p.num_queries - qs ||
-                           (c + kMassTiles * TPG - 1) / (kMassTiles * TPG) > p.row_blocks
-                       ? 0
-                       : (L + TOK - 1) / TOK;
+            const MassSeq x = mass_seq(p, s, kMassTiles * TPG, false);
+            return x.blocks ? (x.L + TOK - 1) / TOK : 0;
         });
         const long long total = (long long)sm.pre[n] * Hkv;
         for (long long u = me; u < total; u += warps) {

@@ -26,13 +26,13 @@ struct PrefillMassParams {
     const int32_t *block_tables;
     const int32_t *seq_lens;
     const int32_t *query_start;
-    float2 *stats;                 // [unit][split][2 * 128 rows] maximum (base 2), sum
+    float2 *stats;                 // [unit + block][2 sets][2 * 128 rows] maximum (base 2),
+                                   // sum
     float *sums;                   // [num_seqs * num_kv_heads][2 * row_blocks][max_blocks * 16]
     uint32_t *err;
     int num_seqs, num_heads, num_kv_heads, max_blocks, num_blocks;
     int num_queries;               // rows of q
     int row_blocks;                // units of 2 x 128 (token, head) rows per (sequence, kv head)
-    int splits;                    // parts of a unit's keys, a thread block each
     float scale_log2, decay;
 };
 

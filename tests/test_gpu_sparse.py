@@ -417,6 +417,41 @@ def test_prefill_mass_of_long_keys(pa, lens, chunks, g):
     chunk_case(pa, gen(22, g), lens, chunks, "bf16", 128, 1, g, 0.9)
 
 
+@pytest.mark.parametrize("g,d,count", [(4, 128, 100), (3, 64, 77), (16, 64, 40), (1, 128, 60)])
+def test_prefill_mass_of_many_units(pa, g, d, count):
+    # shares of a few tiles that begin and end anywhere, units of one and of two query tiles
+    r = gen(38, g)
+    lens = [int(x) for x in torch.randint(0, 900, (count,), generator=r)]
+    chunks = [min(n, int(x)) for n, x in zip(lens, torch.randint(0, 300, (count,), generator=r))]
+    lens[3], chunks[3] = 900, 1
+    chunk_case(pa, r, lens, chunks, "bf16", d, 2, g, 1.0)
+
+
+def test_prefill_mass_again_and_again(pa):
+    r = gen(39)
+    for count, most, c in ((1, 20000, 200), (5, 3000, 64), (20, 700, 33), (300, 100, 20)):
+        lens = [int(x) for x in torch.randint(1, most, (count,), generator=r)]
+        chunks = [min(n, c + i % 40) for i, n in enumerate(lens)]
+        tables, nb = su.tables_for(r, lens)
+        start = [0]
+        for x in chunks:
+            start.append(start[-1] + x)
+        k, q = (torch.randn(s, generator=r).bfloat16().cuda()
+                for s in ((nb, 2, 16, 128), (start[-1], 8, 128)))
+        tt, ll, ss = cuda(tables, lens, start)
+        first = None
+        for _ in range(60):
+            m = torch.zeros(count, 2, 16 * tables.shape[1], device="cuda")
+            pa.prefill_mass(m, q, k, tt, ll, ss, max(chunks), 0.088)
+            first = m if first is None else first
+            assert torch.equal(m, first)
+        check(pa)
+        # every row gives a weight of one
+        total = first.double().sum(-1).cpu()
+        want = torch.tensor(chunks).double()[:, None] * 4
+        assert bool(((total - want).abs() <= 2e-4 * want).all())
+
+
 def test_prefill_mass_in_a_wide_table(pa):
     chunk_case(pa, gen(23), [300, 10], [20, 10], "f16", 64, 2, 4, 1.0, mb=500, longest=900)
 

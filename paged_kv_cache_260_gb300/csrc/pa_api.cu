@@ -1770,21 +1770,10 @@ int pa_prefill_mass(const struct pa_sparse_args *args)
     MassKernels k{};
     if (!prefill_mass_kernels(a.dtype == PA_DTYPE_BF16, a.head_dim, &k))
         return PA_ERR_UNSUPPORTED;
-    int dev = 0;
-    cudaGetDevice(&dev);
-    for (const void *fn : {k.stats, k.sums}) {
-        rc = ensure_smem(fn, dev, k.smem);
-        if (rc != PA_OK)
-            return rc;
-    }
-    CUtensorMap tmk;
-    rc = make_pool_map(&tmk, a.k_cache, a.dtype, a.head_dim,
-                       (long long)a.num_blocks * a.num_kv_heads * kBlockSize);
-    if (rc != PA_OK)
-        return rc;
     PrefillMassParams p{};
     p.mass = a.mass;
     p.q = a.q;
+    p.k_cache = a.k_cache;
     p.block_tables = a.block_tables;
     p.seq_lens = a.seq_lens;
     p.query_start = a.query_start;
@@ -1801,16 +1790,33 @@ int pa_prefill_mass(const struct pa_sparse_args *args)
     p.scale_log2 = scale * 1.4426950408889634f;
     p.decay = decay;
     cudaStream_t st = static_cast<cudaStream_t>(a.stream);
+    void *fargs[] = {&p};
+    const long long keys = (long long)a.max_blocks_per_seq * kBlockSize;
+    if (keys <= kMassShortKeys &&
+        keys * a.max_query_len * (a.num_heads / a.num_kv_heads) <= kMassShortWork)
+        return launch_dependent(k.whole, dim3((unsigned)a.num_seqs * a.num_kv_heads),
+                                dim3(kMassShortThreads), 0, st, fargs);
+    int dev = 0;
+    cudaGetDevice(&dev);
+    rc = ensure_smem(k.stats, dev, k.smem_stats);
+    if (rc == PA_OK)
+        rc = ensure_smem(k.sums, dev, k.smem_sums);
+    if (rc != PA_OK)
+        return rc;
+    CUtensorMap tmk;
+    rc = make_pool_map(&tmk, a.k_cache, a.dtype, a.head_dim,
+                       (long long)a.num_blocks * a.num_kv_heads * kBlockSize);
+    if (rc != PA_OK)
+        return rc;
     void *kargs[] = {&p, &tmk};
     // one block an SM, two key tiles each at least
     const dim3 grid((unsigned)std::min((long long)ds->num_sms, (w.tiles + 1) / 2));
-    rc = launch_dependent(k.stats, grid, dim3(k.threads), k.smem, st, kargs);
+    rc = launch_dependent(k.stats, grid, dim3(k.threads), k.smem_stats, st, kargs);
     if (rc == PA_OK)
-        rc = launch_dependent(k.sums, grid, dim3(k.threads), k.smem, st, kargs);
+        rc = launch_dependent(k.sums, grid, dim3(k.threads), k.smem_sums, st, kargs);
     if (rc != PA_OK)
         return rc;
     const long long units = (long long)a.num_seqs * a.num_kv_heads * ((a.max_blocks_per_seq + 7) / 8);
-    void *fargs[] = {&p};
     return launch_dependent(prefill_mass_finish(),
                             dim3(share_grid(units, kMassFinishThreads, 4, ds)),
                             dim3(kMassFinishThreads), 0, st, fargs);

@@ -113,9 +113,13 @@ decode_mass_finish_kernel(const DecodeMassParams p)
 // uses up (128 bytes a cycle, before the copies): pass 1 keeps its query rows in
 // tensor memory, beside three buffers of scores that its query tiles take in
 // turn, and pass 2 multiplies a key tile by both query tiles at once (128 x 256),
-// two buffers.  Of each query tile every other key tile is read by a second set of
-// four softmax warps: with one set, two warps a scheduler, their latencies cost
-// as much as the products.
+// two buffers.  Four sets of four warps take the exponentials, two of each query
+// tile: in pass 1 a set takes 64 keys of every key tile, so that a buffer is
+// free again as soon as it has been loaded (with 128 keys of every other one in
+// two steps, half of a set's time later, the products waited for the three
+// buffers); in pass 2, where a buffer's two tiles' time is longer, it takes the 128
+// rows of every other key tile, so that a key's sum over a query tile is one
+// thread's.
 //
 // The key tiles of all units form one list, ordered by sequence, kv head and
 // row block; each block of the persistent grid takes an equal share of it.  A
@@ -125,25 +129,25 @@ decode_mass_finish_kernel(const DecodeMassParams p)
 // rows, and reads each piece's keys from the last tile back: those are the ones
 // that pass 1 left in L2.
 // ---------------------------------------------------------------------------
-template <int D>
+template <int D, bool SUMS>
 struct MassShape {
     static constexpr int BM = kMassRows, NG = kMassTiles, BN = kMassKeys;
     static constexpr int NB = BN / kBlockSize;
     static constexpr int HALVES = D / 64;
     static constexpr int BOX = 2048;                      // 16 rows x 128 B
-    static constexpr int Q_BYTES = NG * BM * D * 2;       // pass 2: [half][256 rows][128 B]
+    static constexpr int Q_BYTES = SUMS ? NG * BM * D * 2 : 0;   // [half][256 rows][128 B]
     static constexpr int SLOT_BYTES = BN * D * 2;         // [half][8 blocks][16 rows][128 B]
-    static constexpr int NSLOT = D == 128 ? 5 : 8;
+    static constexpr int NSLOT = D == 64 ? 8 : SUMS ? 5 : 6;
     static constexpr int OFF_SLOT = Q_BYTES;
     static constexpr int OFF_LSE = OFF_SLOT + NSLOT * SLOT_BYTES;
     // full[NSLOT] empty[NSLOT] s[4] read[3] q[2] free[2] group[2] drain, then TMEM base and
     // abort flag
     static constexpr int NBAR = 2 * NSLOT + 14;
-    // tensor memory: score buffers of 128 (pass 1) or 256 columns, pass 1's query rows
-    static constexpr uint32_t COL_Q = 384;
     static constexpr int OFF_BAR = OFF_LSE + NG * BM * 4;
     static constexpr int SMEM = 1024 + OFF_BAR + NBAR * 8 + 8;
     static constexpr int THREADS = 64 + NG * 256;
+    // tensor memory: score buffers of 128 (pass 1) or 256 columns, pass 1's query rows
+    static constexpr uint32_t COL_Q = 384;
     static_assert(SMEM <= 227 * 1024, "one block per SM");
 };
 
@@ -241,10 +245,10 @@ struct MassWalker {
 };
 
 template <typename T, int D, bool SUMS>
-__global__ void __launch_bounds__(MassShape<D>::THREADS)
+__global__ void __launch_bounds__(MassShape<D, SUMS>::THREADS)
 prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorMap tmk)
 {
-    using Sh = MassShape<D>;
+    using Sh = MassShape<D, SUMS>;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr uint32_t FULL = 0xffffffffu;
     constexpr int NS = Sh::NSLOT, NTH = Sh::THREADS, ROWS = Sh::NG * Sh::BM;
@@ -257,8 +261,8 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
     const uint32_t bar_addr = sbase + Sh::OFF_BAR;
     auto full_bar = [&](int s) { return bar_addr + 8u * s; };
     auto empty_bar = [&](int s) { return bar_addr + 8u * (NS + s); };
-    // scores are there for a set of softmax warps (pass 1: 2 * query tile + set); a buffer
-    // has been read; query rows are there; a piece's products have ended
+    // scores are there (pass 1: for a query tile's every other turn; pass 2: in a buffer); a
+    // buffer has been read; query rows are there; a piece's products have ended
     auto s_bar = [&](int i) { return bar_addr + 8u * (2 * NS + i); };
     auto read_bar = [&](int b) { return bar_addr + 8u * (2 * NS + 4 + b); };
     auto q_bar = [&](int g) { return bar_addr + 8u * (2 * NS + 7 + g); };
@@ -280,7 +284,7 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
         for (int i = 0; i < 4; ++i)
             mbar_init(s_bar(i), 1);
         for (int i = 0; i < 3; ++i)
-            mbar_init(read_bar(i), SUMS ? 256 : 128);
+            mbar_init(read_bar(i), 256);
         for (int g = 0; g < Sh::NG; ++g) {
             mbar_init(q_bar(g), SUMS ? 512 : 256);
             mbar_init(free_bar(g), 1);
@@ -290,6 +294,10 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
         *abort_flag = 0;
         mbar_init_fence();
     }
+    if (warp == 1) {                              // (no two of these blocks fit on an SM)
+        tc::tmem_alloc(smem_addr(tmem_slot), 512);
+        tc::tmem_relinquish();
+    }
     grid_dependency_wait();
 
     // ---- the block's share: the list's length, then the sequence its share starts in ----
@@ -297,28 +305,11 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
         const MassSeq x = mass_seq(p, s, TPB, report);
         return Hkv * mass_tiles(x, TPB);
     };
-    int total = 0;
-    const int mine = tid < p.num_seqs ? tiles_of(tid, !SUMS && blockIdx.x == 0) : 0;
-    for (int s = tid + NTH; s < p.num_seqs; s += NTH)
-        total += tiles_of(s, !SUMS && blockIdx.x == 0);
-    total = __reduce_add_sync(FULL, total + mine);
-    if (lane == 0)
-        scan[warp] = total;
-    __syncthreads();
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < NTH / 32; ++w)
-        total += scan[w];
-    const int R = max((total + (int)gridDim.x - 1) / (int)gridDim.x, 2);
-    const long long share = (long long)blockIdx.x * R;
-    if (share >= total)
-        return;
-    const int at = (int)share, end = (int)min((long long)total, share + R);
-    int carry = 0;
-    for (int s0 = 0; s0 < p.num_seqs && carry <= at; s0 += NTH) {
+    int carry = 0, mine = 0, before = 0;          // of this thread's last sequence
+    auto scan_from = [&](int s0, bool report) {
         const int s = s0 + tid;
-        const int n = s0 == 0 ? mine : s < p.num_seqs ? tiles_of(s, false) : 0;
-        int incl = n;
+        mine = s < p.num_seqs ? tiles_of(s, report && !SUMS && blockIdx.x == 0) : 0;
+        int incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(FULL, incl, o);
@@ -329,27 +320,43 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
         if (lane == 31)
             scan[warp] = incl;
         __syncthreads();
-        int before = carry + incl - n;
+        before = carry + incl - mine;
 #pragma unroll
         for (int w = 0; w < NTH / 32; ++w) {
             before += w < warp ? scan[w] : 0;
             carry += scan[w];
         }
-        if (n > 0 && before <= at && at < before + n) {
-            start_seq = s;
-            start_at = before;
+    };
+    for (int s0 = 0; s0 < p.num_seqs; s0 += NTH)
+        scan_from(s0, true);
+    const int total = carry;
+    const int R = max((total + (int)gridDim.x - 1) / (int)gridDim.x, 2);
+    const long long share = (long long)blockIdx.x * R;
+    if (share < total) {
+        const int at = (int)share;
+        auto found = [&](int s0) {
+            if (mine > 0 && before <= at && at < before + mine) {
+                start_seq = s0 + tid;
+                start_at = before;
+            }
+        };
+        if (p.num_seqs <= NTH) {
+            found(0);
+        } else {
+            carry = 0;
+            for (int s0 = 0; s0 < p.num_seqs && carry <= at; s0 += NTH) {
+                scan_from(s0, false);
+                found(s0);
+            }
         }
-    }
-    if (warp == 1) {
-        tc::tmem_alloc(smem_addr(tmem_slot), 512);
-        tc::tmem_relinquish();
     }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     MassWalker w;
-    w.init(p, TPB, start_seq, start_at, at, end);
+    w.init(p, TPB, start_seq, start_at, (int)min(share, (long long)total),
+           (int)min((long long)total, share + R));
     auto give_up = [&]() {
         *abort_flag = 1;
         record_error(p.err, PA_DEVERR_TIMEOUT);
@@ -432,18 +439,18 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
         bool ok = true;
         int it = 0;                               // key tiles so far
         int rows[Sh::NG] = {0, 0};                // units so far of each query tile
-        uint32_t used = 0, turns = 0;             // of each score buffer: used yet, parity
+        int turn[Sh::NG] = {0, 0};                // key tiles so far of each query tile
+        uint32_t used = 0, odd = 0;               // of each score buffer: used yet, parity
         for (; ok && w.valid; w.next(p, TPB)) {
             const int ng = groups();
             for (int i = 0; ok && i < w.te - w.tb; ++i, ++it) {
                 const int sl = it % NS;
                 const uint64_t kd = k_desc + (uint64_t)((sl * Sh::SLOT_BYTES) >> 4);
-                if (__any_sync(FULL, *abort_flag != 0)) {
+                if (__any_sync(FULL, *abort_flag != 0) ||
+                    !wait_all(full_bar(sl), (it / NS) & 1)) {
                     ok = false;
                     break;
                 }
-                // a K step: 32 bytes along the 128-byte row; the next 64 channels are a half
-                // further
 #pragma unroll
                 for (int g = 0; g < (SUMS ? 1 : Sh::NG); ++g) {
                     if (g >= ng || !ok)
@@ -451,17 +458,18 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
                     const int buf = SUMS ? it & 1 : ng == 2 ? (2 * i + g) % 3 : i & 1;
                     if (i == 0)
                         ok = wait_all(q_bar(g), rows[g]++ & 1);
-                    // The buffer's last scores have been read.  With them all that its set of
-                    // warps was given before: a set never has two tiles ahead of it, whose
-                    // barrier's phases it could not tell apart.
+                    // The buffer's last scores have been read; and with them, three tiles (one
+                    // query tile: two) before, what the warps were given two turns before:
+                    // they never have more ahead of them than two barriers tell apart.
                     if (ok && (used >> buf & 1))
-                        ok = wait_all(read_bar(buf), ~turns >> buf & 1);
+                        ok = wait_all(read_bar(buf), ~odd >> buf & 1);
                     used |= 1u << buf;
-                    turns ^= 1u << buf;
-                    ok = ok && wait_all(full_bar(sl), (it / NS) & 1);
+                    odd ^= 1u << buf;
                     if (!ok)
                         continue;
                     tc::fence_after_sync();
+                    // a K step: 32 bytes along the 128-byte row; the next 64 channels are a half
+                    // further
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint64_t ko =
@@ -475,7 +483,7 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
                             tc::mma_ts_warp(tmem + 128 * buf, tmem + Sh::COL_Q + 64 * g + 8 * k,
                                             kd + ko, id128, k > 0);
                     }
-                    tc::commit_warp(s_bar(SUMS ? buf : 2 * g + (i & 1)));
+                    tc::commit_warp(s_bar(SUMS ? buf : 2 * g + (turn[g]++ & 1)));
                     if (SUMS || g == ng - 1)
                         tc::commit_warp(empty_bar(sl));
                     if (i == w.te - w.tb - 1)
@@ -490,15 +498,17 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
         if (!wait_all(drain_bar, 0) && lane == 0)
             give_up();
     } else {
-        const int grp = (warp - 2) >> 3, set = ((warp - 2) >> 2) & 1;
+        // Sets of four warps: of query tile grp, pass 1 takes keys 64 half .. + 63 of every key
+        // tile, pass 2 every other key tile.
+        const int set = (warp - 2) >> 2, grp = set >> 1, half = set & 1;
         const int q4 = warp & 3;                          // TMEM lane quarter of this warp
         const int rr = q4 * 32 + lane;                    // this thread's TMEM lane
         const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
         const float sl2 = p.scale_log2;
         const uint64_t sl2x2 = f2_pack(sl2, sl2);
         bool ok = true;
-        int n0 = 0;                                       // key tiles before this piece
-        int turns = 0;                                    // of this set so far
+        int it = 0;                                       // key tiles so far
+        int turn = 0;                                     // of this set's
         int units = 0;                                    // this query tile's (pass 2: all) so far
         int met = 0;
         // the query tile's threads meet; bounded, since a warp that gave up does not come
@@ -506,7 +516,7 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
             mbar_arrive(group_bar(grp));
             return __all_sync(FULL, mbar_wait_bounded(group_bar(grp), met++ & 1));
         };
-        for (; ok && w.valid; n0 += w.te - w.tb, w.next(p, TPB)) {
+        for (; ok && w.valid; w.next(p, TPB)) {
             const int ng = groups();
             if (!SUMS && grp >= ng)
                 continue;
@@ -514,53 +524,44 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
             // ---- query rows ----
             // Row r = (token t0 + r / G, head r % G); rows past the chunk and those that do not
             // fill a token are zero.  The products of the piece before have ended.
-            if ((SUMS || set == 0) && units > 0 &&
+            if (units > 0 &&
                 !__all_sync(FULL, mbar_wait_bounded(free_bar(SUMS ? 0 : grp), (units - 1) & 1))) {
                 ok = false;
                 break;
             }
             ++units;
             const T *qg = static_cast<const T *>(p.q);
-            if (!SUMS && set == 0) {
-                // to tensor memory, a thread its lane's row
-                uint32_t x[D / 2];
-                const int tok = t0 + rr / G;
-                const bool on = rr < TPG * G && tok < w.x.c;
-                const uint4 *src = reinterpret_cast<const uint4 *>(
-                    qg + ((size_t)(w.x.qs + (on ? tok : 0)) * Hq + w.h * G + rr % G) * D);
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 y = on ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-                    x[4 * i] = y.x, x[4 * i + 1] = y.y, x[4 * i + 2] = y.z, x[4 * i + 3] = y.w;
-                }
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < D / 64; ++i)
-                    tc::tmem_st32(tl + Sh::COL_Q + 64 * grp + 32 * i,
-                                  *reinterpret_cast<const uint32_t(*)[32]>(x + 32 * i));
-                tc::fence_before_sync();
-            }
+            const int tok = t0 + rr / G;
+            const bool row_valid = rr < TPG * G && tok < w.x.c;
             if (!SUMS) {
-                // the other set says that it has read all tiles before, and goes on with the
-                // first: it may have none in this piece, and would arrive for the next one
-                mbar_arrive(q_bar(grp));
-                if (set == 1 && !__all_sync(FULL, mbar_wait_bounded(q_bar(grp), (units - 1) & 1))) {
-                    ok = false;
-                    break;
+                // to tensor memory, a thread 64 channels of its lane's row
+                if (half < D / 64) {
+                    uint32_t x[32];
+                    const uint4 *src = reinterpret_cast<const uint4 *>(
+                        qg + ((size_t)(w.x.qs + (row_valid ? tok : 0)) * Hq + w.h * G + rr % G) * D +
+                        64 * half);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint4 y = row_valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                        x[4 * i] = y.x, x[4 * i + 1] = y.y, x[4 * i + 2] = y.z, x[4 * i + 3] = y.w;
+                    }
+                    __syncwarp();
+                    tc::tmem_st32(tl + Sh::COL_Q + 64 * grp + 32 * half, x);
                 }
-            }
-            if (SUMS) {
+                tc::fence_before_sync();
+                mbar_arrive(q_bar(grp));
+            } else {
                 // to shared memory: K-major, 128-byte swizzle
                 constexpr int CPR = D / 8, RSTEP = 256 / CPR, NPT = Sh::BM / RSTEP;
                 const int lt = (tid - 64) & 255, ch = lt % CPR, hf = ch >> 3, c8 = ch & 7;
                 uint4 qv[NPT];
 #pragma unroll
                 for (int i = 0; i < NPT; ++i) {
-                    const int r = lt / CPR + i * RSTEP, tok = t0 + r / G;
+                    const int r = lt / CPR + i * RSTEP, rt = t0 + r / G;
                     qv[i] = make_uint4(0, 0, 0, 0);
-                    if (r < TPG * G && tok < w.x.c)
+                    if (r < TPG * G && rt < w.x.c)
                         qv[i] = __ldg(reinterpret_cast<const uint4 *>(
-                            qg + ((size_t)(w.x.qs + tok) * Hq + w.h * G + r % G) * D + ch * 8));
+                            qg + ((size_t)(w.x.qs + rt) * Hq + w.h * G + r % G) * D + ch * 8));
                 }
 #pragma unroll
                 for (int i = 0; i < NPT; ++i) {
@@ -571,70 +572,83 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
                 fence_proxy_async_shared();
                 mbar_arrive(q_bar(0));
             }
-            const int tok = t0 + rr / G;
-            const bool row_valid = rr < TPG * G && tok < w.x.c;
             const int unit = (w.s * Hkv + w.h) * p.row_blocks + w.b;
-            // a piece's statistics: [set][query tile][row]
+            // a piece's statistics: [half of the key tiles][query tile][row]
             float2 *stats = p.stats + (size_t)unit * (2 * ROWS) + grp * Sh::BM + rr;
             float m = -INFINITY, l = 0.f;
             if (SUMS) {
                 // minus log2 of the row's sum over the unit's pieces; rows that are none: -inf
+                // (four loads in flight: a unit of few, long sequences has many pieces)
                 float M = -INFINITY;
-                const int k1 = set ? -1 : (w.first + w.nt - 1) / R;
-                for (int k = w.first / R; k <= k1; ++k)
+                const int k0 = w.first / R;
+                const int n = half || !row_valid ? 0 : 2 * ((w.first + w.nt - 1) / R - k0 + 1);
+                for (int j = 0; j < n; j += 4) {
+                    float2 a[4];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float2 a = __ldcg(stats + (size_t)k * (2 * ROWS) + i * ROWS);
-                        const float nM = fmaxf(M, a.x);
+                    for (int i = 0; i < 4; ++i)
+                        a[i] = j + i < n ? __ldcg(stats + (size_t)(2 * k0 + j + i) * ROWS)
+                                         : make_float2(-INFINITY, 0.f);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float nM = fmaxf(M, a[i].x);
                         if (nM > -INFINITY)
-                            l = l * exp2f(M - nM) + a.y * exp2f(a.x - nM);
+                            l = l * exp2f(M - nM) + a[i].y * exp2f(a[i].x - nM);
                         M = nM;
                     }
+                }
                 ok = meet();                              // all are done with the piece before
-                if (!set)
+                if (!half)
                     lse[grp * Sh::BM + rr] = row_valid ? -(M + log2f(l)) : -INFINITY;
                 ok = ok && meet();
                 if (!ok)
                     break;
             }
-            float *sums = p.sums + (((size_t)w.s * Hkv + w.h) * (2 * p.row_blocks) + 2 * w.b + grp) *
-                                       ((size_t)p.max_blocks * kBlockSize);
+            float *sums = p.sums + (size_t)(2 * unit + grp) * ((size_t)p.max_blocks * kBlockSize);
             const int first_pos = w.x.L - w.x.c + t0;     // of the tile's first token
-            for (int i = 0; i < w.te - w.tb; ++i) {
+            for (int i = 0; i < w.te - w.tb; ++i, ++it) {
                 const int k0 = tile(i) * Sh::BN;
-                const int buf = SUMS ? (n0 + i) & 1 : ng == 2 ? (2 * i + grp) % 3 : i & 1;
-                if (((SUMS ? n0 + i : i) & 1) != set)     // the other set's
-                    continue;
+                int buf, bar, phase;
+                if (SUMS) {
+                    buf = bar = it & 1;
+                    phase = it >> 1;
+                    if (buf != half)                      // the other set's
+                        continue;
+                } else {
+                    buf = ng == 2 ? (2 * i + grp) % 3 : i & 1;
+                    bar = 2 * grp + (turn & 1);
+                    phase = turn++ >> 1;
+                }
                 if (__any_sync(FULL, *abort_flag != 0) ||
-                    !__all_sync(FULL, mbar_wait_bounded(s_bar(SUMS ? set : 2 * grp + set),
-                                                        turns++ & 1))) {
+                    !__all_sync(FULL, mbar_wait_bounded(s_bar(bar), phase & 1))) {
                     ok = false;
                     break;
                 }
-                if (grp >= ng) {
+                if (grp >= ng) {                          // pass 2, one query tile
                     mbar_arrive(read_bar(buf));
                     continue;
                 }
                 tc::fence_after_sync();
+                // 64 columns at a time: keys for pass 1, rows for pass 2
+                const int c0 = SUMS ? 0 : 64 * half;
                 const uint32_t tg = tl + (SUMS ? 256 * buf + 128 * grp : 128 * buf);
                 // rows: keys [0, vis] of the tile are visible; keys: columns [first, 128) see it
                 const int vis = row_valid ? first_pos + rr / G - k0 : -1;
                 const int first = min(max(k0 + rr - first_pos, 0), 128) * G;
-                const bool full = __all_sync(FULL, SUMS ? first <= 0 : vis >= Sh::BN - 1);
-                float total_sum = 0.f;
-#pragma unroll
-                for (int hb = 0; hb < 2; ++hb) {
+                const bool full = __all_sync(FULL, SUMS ? first <= 0 : vis >= c0 + 63);
+                float sum = 0.f;
+#pragma unroll 1
+                for (int c = c0; c < (SUMS ? 128 : c0 + 64); c += 64) {
                     uint32_t v[64];
                     __syncwarp();
-                    tc::tmem_ld64(tg + 64 * hb, v);
-                    if (hb == 1) {
+                    tc::tmem_ld64(tg + c, v);
+                    if (!SUMS || c == 64) {
                         tc::fence_before_sync();
                         mbar_arrive(read_bar(buf));
                     }
                     if (!full) {
 #pragma unroll
                         for (int e = 0; e < 64; ++e)
-                            if (SUMS ? e + 64 * hb < first : e + 64 * hb > vis)
+                            if (SUMS ? e < first - c : e > vis - c)
                                 v[e] = __float_as_uint(-INFINITY);
                     }
                     float mref = 0.f;
@@ -659,8 +673,7 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
                     }
                     uint64_t sum2[4] = {0, 0, 0, 0};
                     const uint64_t nm2 = f2_pack(-mref, -mref);
-                    const float4 *ls =
-                        reinterpret_cast<const float4 *>(lse + grp * Sh::BM + 64 * hb);
+                    const float4 *ls = reinterpret_cast<const float4 *>(lse + grp * Sh::BM + c);
 #pragma unroll
                     for (int e = 0; e < 64; e += 4) {
                         uint64_t na = nm2, nb = nm2;
@@ -683,16 +696,15 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
                     }
                     float a, b;
                     f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), a, b);
-                    if (SUMS)
-                        total_sum += a + b;
-                    else
-                        l += a + b;
+                    sum += a + b;
                 }
-                if (SUMS && k0 + rr < w.x.L)
-                    sums[k0 + rr] = total_sum;
+                if (!SUMS)
+                    l += sum;
+                else if (k0 + rr < w.x.L)
+                    sums[k0 + rr] = sum;
             }
             if (ok && !SUMS)
-                stats[(size_t)blockIdx.x * (2 * ROWS) + set * ROWS] = make_float2(m, l);
+                stats[(size_t)blockIdx.x * (2 * ROWS) + half * ROWS] = make_float2(m, l);
         }
         if (!ok)
             give_up();
@@ -703,6 +715,151 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
     if (warp == 1) {
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The same for short sequences in one launch: a thread block takes a (sequence,
+// kv head) whole, its warps 16 (token, head) rows at a time with mma.sync.  The
+// channels of a product may be taken in any order, so rows of q and k are
+// loaded 16 bytes a lane straight into fragments.  A row's statistics never
+// leave its warp; the warps' sums for a key meet in shared memory.  Two chunks of
+// 5 and 70 tokens, 8/2 heads x 64: 11.5 us against 19 for the three launches, whose
+// own latencies those are.
+// ---------------------------------------------------------------------------
+template <typename T, int D>
+__global__ void __launch_bounds__(kMassShortThreads) prefill_mass_short_kernel(const PrefillMassParams p)
+{
+    using M = Mma<T>;
+    constexpr uint32_t FULL = 0xffffffffu;
+    constexpr int NW = kMassShortThreads / 32, NI = D / 32;
+    constexpr int N8 = 4;                         // 8-key steps in flight
+    __shared__ float acc[NW][kMassShortKeys];
+    __shared__ int tile_of[kMassShortKeys / kBlockSize];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int r = lane >> 2, qd = lane & 3;
+    const int Hkv = p.num_kv_heads, Hq = p.num_heads, G = Hq / Hkv;
+    const int s = blockIdx.x / Hkv, h = blockIdx.x % Hkv;
+    grid_dependents_launch();
+    grid_dependency_wait();
+    const MassSeq x = mass_seq(p, s, kMassTiles * (kMassRows / G), h == 0 && tid == 0);
+    if (x.blocks == 0)
+        return;
+    const int nblk = (x.L + kBlockSize - 1) / kBlockSize;
+    if (tid < nblk) {
+        int phys = __ldg(p.block_tables + (size_t)s * p.max_blocks + tid);
+        if ((unsigned)phys >= (unsigned)p.num_blocks) {
+            record_error(p.err, PA_DEVERR_TABLE_RANGE);
+            phys = 0;
+        }
+        tile_of[tid] = phys * Hkv + h;
+    }
+    for (int t = lane; t < nblk * kBlockSize; t += 32)
+        acc[warp][t] = 0.f;
+    __syncthreads();
+    const uint4 *kp = static_cast<const uint4 *>(p.k_cache) + qd;
+    const int rows = x.c * G, steps = (x.L + 7) / 8;
+    for (int row0 = 16 * warp; row0 < rows; row0 += 16 * NW) {
+        // rows row0 + r and + 8; past the last one that one again, without weight
+        uint32_t a[2 * NI][4];
+        int pos[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int row = min(row0 + r + 8 * e, rows - 1), tok = row / G;
+            pos[e] = row0 + r + 8 * e < rows ? x.L - x.c + tok : -1;
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                                   static_cast<const T *>(p.q) +
+                                   ((size_t)(x.qs + tok) * Hq + h * G + row % G) * D) + qd;
+#pragma unroll
+            for (int k = 0; k < NI; ++k) {
+                const uint4 y = __ldg(src + 4 * k);
+                a[2 * k][e] = y.x, a[2 * k][2 + e] = y.y;
+                a[2 * k + 1][e] = y.z, a[2 * k + 1][2 + e] = y.w;
+            }
+        }
+        // f(key step, scores in base 2: two keys of two rows) for every 8 keys that a row sees
+        const int last = min(steps, (x.L - x.c + (min(row0 + 15, rows - 1)) / G) / 8 + 1);
+        auto each = [&](auto &&f) {
+            for (int j0 = 0; j0 < last; j0 += N8) {
+                uint4 b[N8][NI];
+#pragma unroll
+                for (int i = 0; i < N8; ++i) {
+                    const int t = min(8 * (j0 + i) + r, x.L - 1);
+                    const uint4 *src = kp + ((size_t)tile_of[t / kBlockSize] * kBlockSize +
+                                             t % kBlockSize) * (D / 8);
+#pragma unroll
+                    for (int k = 0; k < NI; ++k)
+                        b[i][k] = __ldg(src + 4 * k);
+                }
+#pragma unroll
+                for (int i = 0; i < N8; ++i) {
+                    float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int k = 0; k < NI; ++k) {
+                        M::run(d, a[2 * k], b[i][k].x, b[i][k].y);
+                        M::run(d, a[2 * k + 1], b[i][k].z, b[i][k].w);
+                    }
+                    // d: (row r, keys 2 qd and + 1), (row r + 8, the same)
+                    const int t = 8 * (j0 + i) + 2 * qd;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        d[e] = t + (e & 1) <= pos[e >> 1] ? d[e] * p.scale_log2 : -INFINITY;
+                    if (j0 + i < last)
+                        f(j0 + i, d);
+                }
+            }
+        };
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        each([&](int, const float (&d)[4]) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float mx = fmaxf(d[2 * e], d[2 * e + 1]);
+                if (mx > m[e]) {
+                    l[e] *= exp2f(m[e] - mx);
+                    m[e] = mx;
+                }
+                if (m[e] > -INFINITY)
+                    l[e] += exp2f(d[2 * e] - m[e]) + exp2f(d[2 * e + 1] - m[e]);
+            }
+        });
+        // the row's four lanes
+        float top[2], inv[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            top[e] = m[e];
+#pragma unroll
+            for (int off = 1; off < 4; off <<= 1)
+                top[e] = fmaxf(top[e], __shfl_xor_sync(FULL, top[e], off));
+            float sum = m[e] > -INFINITY ? l[e] * exp2f(m[e] - top[e]) : 0.f;
+#pragma unroll
+            for (int off = 1; off < 4; off <<= 1)
+                sum += __shfl_xor_sync(FULL, sum, off);
+            inv[e] = pos[e] >= 0 ? 1.f / sum : 0.f;
+            top[e] = pos[e] >= 0 ? top[e] : 0.f;
+        }
+        each([&](int j, const float (&d)[4]) {
+            float w[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                w[e] = exp2f(d[e] - top[0]) * inv[0] + exp2f(d[2 + e] - top[1]) * inv[1];
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1)
+                    w[e] += __shfl_xor_sync(FULL, w[e], off);
+            }
+            if (r == 0) {
+                acc[warp][8 * j + 2 * qd] += w[0];
+                acc[warp][8 * j + 2 * qd + 1] += w[1];
+            }
+        });
+    }
+    __syncthreads();
+    float *mass = p.mass + (size_t)blockIdx.x * p.max_blocks * kBlockSize;
+    for (int t = tid; t < x.L; t += kMassShortThreads) {
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+            sum += acc[w][t];
+        mass[t] = add_mass(mass + t, p.decay, t >= x.L - x.c, sum);
     }
 }
 
@@ -737,15 +894,14 @@ prefill_mass_finish_kernel(const PrefillMassParams p)
             if (t >= L)
                 continue;
             const size_t run = (size_t)s * Hkv + h;
-            const float *part = p.sums + run * (2 * p.row_blocks) * T + t;
+            const float *part = p.sums + run * (kMassTiles * p.row_blocks) * T + t;
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
-            // tiles whose keys reach t (a unit's tiles end where its last row's do)
-            const int tiles = (c + TPG - 1) / TPG;
-            const int from = max(0, (t - (L - c)) / (kMassTiles * TPG)) * kMassTiles;
+            // query tiles whose keys reach t (a unit's end where its last row's do)
+            const int TPB = kMassTiles * TPG, tiles = (c + TPG - 1) / TPG;
 #pragma unroll 4
-            for (int k = from; k < tiles; ++k) {
+            for (int k = max(0, (t - (L - c)) / TPB) * kMassTiles; k < tiles; ++k) {
                 const float4 x = __ldcg(reinterpret_cast<const float4 *>(part + (size_t)k * T));
-                const int end = L - c + min((k / kMassTiles + 1) * kMassTiles * TPG, c);
+                const int end = L - c + min((k / kMassTiles + 1) * TPB, c);
                 sum[0] += x.x;                    // (t itself is reached by the first unit)
                 sum[1] += t + 1 < end ? x.y : 0.f;
                 sum[2] += t + 2 < end ? x.z : 0.f;
@@ -765,8 +921,10 @@ void fill(MassKernels *k)
 {
     k->stats = reinterpret_cast<const void *>(&prefill_mass_kernel<T, D, false>);
     k->sums = reinterpret_cast<const void *>(&prefill_mass_kernel<T, D, true>);
-    k->threads = MassShape<D>::THREADS;
-    k->smem = MassShape<D>::SMEM;
+    k->whole = reinterpret_cast<const void *>(&prefill_mass_short_kernel<T, D>);
+    k->threads = MassShape<D, false>::THREADS;
+    k->smem_stats = MassShape<D, false>::SMEM;
+    k->smem_sums = MassShape<D, true>::SMEM;
 }
 
 }  // namespace

@@ -22,11 +22,11 @@ struct DecodeMassParams {
 // The weights a chunk's queries give: two passes over the keys and a sum.
 struct PrefillMassParams {
     float *mass;
-    const void *q;
+    const void *q, *k_cache;
     const int32_t *block_tables;
     const int32_t *seq_lens;
     const int32_t *query_start;
-    float2 *stats;                 // [unit + block][2 sets][2 * 128 rows] maximum (base 2),
+    float2 *stats;                 // [unit + block][2 halves][2 * 128 rows] maximum (base 2),
                                    // sum
     float *sums;                   // [num_seqs * num_kv_heads][2 * row_blocks][max_blocks * 16]
     uint32_t *err;
@@ -40,10 +40,17 @@ constexpr int kMassRows = 128;     // (token, head) rows of one query tile
 constexpr int kMassTiles = 2;      // query tiles of a unit
 constexpr int kMassKeys = 128;     // keys of a tile
 
+// A batch whose tables hold at most kMassShortKeys tokens and whose chunks' rows make
+// at most kMassShortWork products with them takes the one-launch kernel.
+constexpr int kMassShortKeys = 512;
+constexpr long long kMassShortWork = 131072;
+constexpr int kMassShortThreads = 512;
+
 struct MassKernels {
     const void *stats, *sums;      // (PrefillMassParams, tensor map of the key pool)
+    const void *whole;             // (PrefillMassParams): short sequences
     int threads;
-    size_t smem;
+    size_t smem_stats, smem_sums;
 };
 
 bool prefill_mass_kernels(bool bf16, int head_dim, MassKernels *k);

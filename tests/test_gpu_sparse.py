@@ -410,6 +410,19 @@ def test_prefill_mass(pa, dt, d, hkv, g, decay):
                hkv, g, decay)
 
 
+@pytest.mark.parametrize("dt,d,hkv,g", [("f16", 64, 2, 4), ("bf16", 128, 1, 1), ("f16", 128, 2, 5),
+                                        ("bf16", 64, 1, 16), ("f16", 64, 3, 7),
+                                        ("bf16", 128, 2, 3), ("f16", 128, 1, 128)])
+@pytest.mark.parametrize("decay", [0.9, 0.0])
+def test_prefill_mass_of_short_sequences(pa, dt, d, hkv, g, decay):
+    # at most 512 keys and 131072 pairs a head: one launch
+    most = 131072 // (304 * g)
+    chunk_case(pa, gen(40, d, g), [150, 300, 1, 16, 0, 47, 17], [min(most, 5), min(most, 70), 1, 16
+                                                               if most >= 16 else 3, 0, 0, 1],
+               dt, d, hkv, g, decay)
+    chunk_case(pa, gen(41, d, g), [33, 8, 1], [min(33, most), min(8, most), 1], dt, d, hkv, g, decay)
+
+
 @pytest.mark.parametrize("lens,chunks,g", [([5000], [64], 4), ([3000, 200], [700, 1], 2),
                                            ([1, 1], [1, 1], 4), ([2049], [2049], 1),
                                            ([9000, 130, 17], [1, 33, 17], 8)])

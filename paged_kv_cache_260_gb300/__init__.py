@@ -635,28 +635,17 @@ def qk_norm_rope(q_out, k_out, q, k, positions, cos_sin, q_norm=None, k_norm=Non
     return q_out, k_out
 
 
-def _sparse_call(fn, dev, names, stream, *, out=0, mass=0, q=0, k=0, v=0, bounds=0, tables=0,
-                 lens=0, start=0, starts=0, new_lens=0, tiles=0, tile_lens=0, workspace=None,
-                 scale=1.0, decay=1.0, n=0, rows=0, longest=0, hq=0, hkv=0, d=0, bs=BLOCK_SIZE,
-                 mb=0, nb=0, keep=0, first=0, last=0, code=0):
-    """One call with struct pa_sparse_args; tensors' addresses as ints, 0 for NULL."""
-    wptr, wbytes = ((0, 0) if workspace is None else
-                    (workspace.data_ptr(), _bytes_of(workspace, dev)))
-    rc = getattr(load(), fn)(_SPARSE_ARGS.pack(
-        _SPARSE_ARGS.size, out, mass, q, k, v, bounds, tables, lens, start, starts, new_lens,
-        tiles, tile_lens, wptr, names.raw_stream(dev) if stream is None else stream.cuda_stream,
-        wbytes, scale, decay, n, rows, longest, hq, hkv, d, bs, mb, nb, keep, first, last, code,
-        0))
-    if rc:
-        raise PagedAttnError(fn, rc)
-
-
-def _tables(block_tables, seq_lens, names, dev):
-    """Sequences, table width and the addresses of tables and lengths."""
-    n, mb = block_tables.shape
-    if seq_lens.shape != (n,):
+def _tables_of(block_tables, seq_lens, n, names, dev):
+    """Checks tables [n, width] and lengths [n]; the width."""
+    rows, mb = block_tables.shape
+    if rows != n or seq_lens.shape != (n,):
         raise ValueError("table shapes")
-    return n, mb, _near(block_tables, names.i32, dev), _near(seq_lens, names.i32, dev)
+    i32 = names.i32
+    if (block_tables.dtype is not i32 or seq_lens.dtype is not i32 or
+            block_tables.get_device() != dev or seq_lens.get_device() != dev or
+            not (block_tables.is_contiguous() and seq_lens.is_contiguous())):
+        raise ValueError(_NEAR)
+    return mb
 
 
 def _mass_rows(mass, n, hkv, mb, names, dev):
@@ -676,14 +665,22 @@ def block_bounds(bounds, k_cache, block_tables, seq_lens, starts=None, stream=No
     """
     names = _hot()
     nb, hkv, bs, d = k_cache.shape
+    n = seq_lens.shape[0]
     dt, dev = k_cache.dtype, _current(k_cache, names)
-    n, mb, tables, lens = _tables(block_tables, seq_lens, names, dev)
+    mb = _tables_of(block_tables, seq_lens, n, names, dev)
     if bounds.shape != (nb, hkv, 2, d) or (starts is not None and starts.shape != (n,)):
         raise ValueError("shapes")
-    _sparse_call("pa_block_bounds", dev, names, stream, k=_near(k_cache, dt, dev),
-                 bounds=_near(bounds, dt, dev), tables=tables, lens=lens,
-                 starts=0 if starts is None else _near(starts, names.i32, dev), n=n, hkv=hkv, d=d,
-                 bs=bs, mb=mb, nb=nb, code=_code(dt, names))
+    if (bounds.dtype is not dt or bounds.get_device() != dev or
+            not (bounds.is_contiguous() and k_cache.is_contiguous())):
+        raise ValueError(_NEAR)
+    rc = load().pa_block_bounds(_SPARSE_ARGS.pack(
+        _SPARSE_ARGS.size, 0, 0, 0, k_cache.data_ptr(), 0, bounds.data_ptr(),
+        block_tables.data_ptr(), seq_lens.data_ptr(), 0,
+        0 if starts is None else _near(starts, names.i32, dev), 0, 0, 0, 0,
+        names.raw_stream(dev) if stream is None else stream.cuda_stream, 0, 0.0, 0.0, n, 0, 0, 0,
+        hkv, d, bs, mb, nb, 0, 0, 0, _code(dt, names), 0))
+    if rc:
+        raise PagedAttnError("pa_block_bounds", rc)
     return bounds
 
 
@@ -710,18 +707,28 @@ def select_blocks(tiles, tile_lens, q, bounds, block_tables, seq_lens, keep_firs
     names = _hot()
     n, hq, d = q.shape
     nb, hkv, two, d2 = bounds.shape
-    dt, dev = q.dtype, _current(q, names)
-    n2, mb, tables, lens = _tables(block_tables, seq_lens, names, dev)
-    if (n2 != n or two != 2 or d2 != d or tiles.shape[:2] != (n, hkv) or tiles.dim() != 3 or
-            tile_lens.shape != (n, hkv)):
+    keep = tiles.shape[-1]
+    dt, dev, i32 = q.dtype, _current(q, names), names.i32
+    mb = _tables_of(block_tables, seq_lens, n, names, dev)
+    if two != 2 or d2 != d or tiles.shape != (n, hkv, keep) or tile_lens.shape != (n, hkv):
         raise ValueError("shapes")
+    if (bounds.dtype is not dt or tiles.dtype is not i32 or tile_lens.dtype is not i32 or
+            bounds.get_device() != dev or tiles.get_device() != dev or
+            tile_lens.get_device() != dev or
+            not (q.is_contiguous() and bounds.is_contiguous() and tiles.is_contiguous() and
+                 tile_lens.is_contiguous())):
+        raise ValueError(_NEAR)
     if workspace is None:
         workspace = select_blocks_workspace_for(q, bounds, block_tables, stream)
-    _sparse_call("pa_select_blocks", dev, names, stream, q=_near(q, dt, dev),
-                 bounds=_near(bounds, dt, dev), tables=tables, lens=lens,
-                 tiles=_near(tiles, names.i32, dev), tile_lens=_near(tile_lens, names.i32, dev),
-                 workspace=workspace, n=n, hq=hq, hkv=hkv, d=d, mb=mb, nb=nb, keep=tiles.shape[2],
-                 first=int(keep_first), last=int(keep_last), code=_code(dt, names))
+    wptr, wbytes = ((0, 0) if workspace is None else
+                    (workspace.data_ptr(), _bytes_of(workspace, dev)))
+    rc = load().pa_select_blocks(_SPARSE_ARGS.pack(
+        _SPARSE_ARGS.size, 0, 0, q.data_ptr(), 0, 0, bounds.data_ptr(), block_tables.data_ptr(),
+        seq_lens.data_ptr(), 0, 0, 0, tiles.data_ptr(), tile_lens.data_ptr(), wptr,
+        names.raw_stream(dev) if stream is None else stream.cuda_stream, wbytes, 0.0, 0.0, n, 0, 0,
+        hq, hkv, d, BLOCK_SIZE, mb, nb, keep, keep_first, keep_last, _code(dt, names), 0))
+    if rc:
+        raise PagedAttnError("pa_select_blocks", rc)
     return tiles, tile_lens
 
 
@@ -738,11 +745,17 @@ def sparse_decode_workspace_for(q, k_cache, tiles, stream=None):
 
 
 def _qkv(out, q, k_cache, v_cache, names):
-    """Checks of a decode's tensors; the device and the addresses of out, q, k and v."""
+    """Checks of a decode's tensors; their device."""
     dt, dev, pool = q.dtype, _current(q, names), k_cache.shape
     if out.shape != q.shape or v_cache.shape != pool or pool[3] != q.shape[2]:
         raise ValueError("shapes")
-    return dev, [_near(x, dt, dev) for x in (out, q, k_cache, v_cache)]
+    if (out.dtype is not dt or k_cache.dtype is not dt or v_cache.dtype is not dt or
+            out.get_device() != dev or k_cache.get_device() != dev or
+            v_cache.get_device() != dev or
+            not (q.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous() and
+                 v_cache.is_contiguous())):
+        raise ValueError(_NEAR)
+    return dev
 
 
 def sparse_decode(out, q, k_cache, v_cache, tiles, tile_lens, scale, workspace=None, stream=None):
@@ -751,15 +764,25 @@ def sparse_decode(out, q, k_cache, v_cache, tiles, tile_lens, scale, workspace=N
     names = _hot()
     n, hq, d = q.shape
     nb, hkv, bs, _ = k_cache.shape
-    dev, (o, qq, k, v) = _qkv(out, q, k_cache, v_cache, names)
-    if tiles.dim() != 3 or tiles.shape[:2] != (n, hkv) or tile_lens.shape != (n, hkv):
+    keep, i32 = tiles.shape[-1], names.i32
+    dev = _qkv(out, q, k_cache, v_cache, names)
+    if tiles.shape != (n, hkv, keep) or tile_lens.shape != (n, hkv):
         raise ValueError("shapes")
+    if (tiles.dtype is not i32 or tile_lens.dtype is not i32 or tiles.get_device() != dev or
+            tile_lens.get_device() != dev or
+            not (tiles.is_contiguous() and tile_lens.is_contiguous())):
+        raise ValueError(_NEAR)
     if workspace is None:
         workspace = sparse_decode_workspace_for(q, k_cache, tiles, stream)
-    _sparse_call("pa_sparse_decode", dev, names, stream, out=o, q=qq, k=k, v=v,
-                 tiles=_near(tiles, names.i32, dev), tile_lens=_near(tile_lens, names.i32, dev),
-                 workspace=workspace, scale=scale, n=n, hq=hq, hkv=hkv, d=d, bs=bs, nb=nb,
-                 keep=tiles.shape[2], code=_code(q.dtype, names))
+    wptr, wbytes = ((0, 0) if workspace is None else
+                    (workspace.data_ptr(), _bytes_of(workspace, dev)))
+    rc = load().pa_sparse_decode(_SPARSE_ARGS.pack(
+        _SPARSE_ARGS.size, out.data_ptr(), 0, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        0, 0, 0, 0, 0, 0, tiles.data_ptr(), tile_lens.data_ptr(), wptr,
+        names.raw_stream(dev) if stream is None else stream.cuda_stream, wbytes, scale, 0.0, n, 0,
+        0, hq, hkv, d, bs, 0, nb, keep, 0, 0, _code(q.dtype, names), 0))
+    if rc:
+        raise PagedAttnError("pa_sparse_decode", rc)
     return out
 
 
@@ -788,16 +811,20 @@ def decode_mass(out, mass, q, k_cache, v_cache, block_tables, seq_lens, scale, d
     names = _hot()
     n, hq, d = q.shape
     nb, hkv, bs, _ = k_cache.shape
-    dev, (o, qq, k, v) = _qkv(out, q, k_cache, v_cache, names)
-    n2, mb, tables, lens = _tables(block_tables, seq_lens, names, dev)
-    if n2 != n:
-        raise ValueError("table shapes")
+    dev = _qkv(out, q, k_cache, v_cache, names)
+    mb = _tables_of(block_tables, seq_lens, n, names, dev)
     m = _mass_rows(mass, n, hkv, mb, names, dev)
     if workspace is None:
         workspace = decode_mass_workspace_for(q, k_cache, block_tables, stream)
-    _sparse_call("pa_decode_mass", dev, names, stream, out=o, mass=m, q=qq, k=k, v=v,
-                 tables=tables, lens=lens, workspace=workspace, scale=scale, decay=decay, n=n,
-                 hq=hq, hkv=hkv, d=d, bs=bs, mb=mb, nb=nb, code=_code(q.dtype, names))
+    wptr, wbytes = ((0, 0) if workspace is None else
+                    (workspace.data_ptr(), _bytes_of(workspace, dev)))
+    rc = load().pa_decode_mass(_SPARSE_ARGS.pack(
+        _SPARSE_ARGS.size, out.data_ptr(), m, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        0, block_tables.data_ptr(), seq_lens.data_ptr(), 0, 0, 0, 0, 0, wptr,
+        names.raw_stream(dev) if stream is None else stream.cuda_stream, wbytes, scale, decay, n, 0,
+        0, hq, hkv, d, bs, mb, nb, 0, 0, 0, _code(q.dtype, names), 0))
+    if rc:
+        raise PagedAttnError("pa_decode_mass", rc)
     return out, mass
 
 
@@ -823,18 +850,26 @@ def prefill_mass(mass, q, k_cache, block_tables, seq_lens, query_start, max_quer
     names = _hot()
     t, hq, d = q.shape
     nb, hkv, bs, d2 = k_cache.shape
+    n, longest = seq_lens.shape[0], int(max_query_len)
     dt, dev = q.dtype, _current(q, names)
-    n, mb, tables, lens = _tables(block_tables, seq_lens, names, dev)
+    mb = _tables_of(block_tables, seq_lens, n, names, dev)
     if d2 != d or query_start.shape != (n + 1,):
         raise ValueError("shapes")
+    if (k_cache.dtype is not dt or k_cache.get_device() != dev or
+            not (q.is_contiguous() and k_cache.is_contiguous())):
+        raise ValueError(_NEAR)
     m = _mass_rows(mass, n, hkv, mb, names, dev)
     if workspace is None:
-        workspace = prefill_mass_workspace_for(q, k_cache, block_tables, max_query_len, stream)
-    _sparse_call("pa_prefill_mass", dev, names, stream, mass=m, q=_near(q, dt, dev),
-                 k=_near(k_cache, dt, dev), tables=tables, lens=lens,
-                 start=_near(query_start, names.i32, dev), workspace=workspace, scale=scale,
-                 decay=decay, n=n, rows=t, longest=int(max_query_len), hq=hq, hkv=hkv, d=d, bs=bs,
-                 mb=mb, nb=nb, code=_code(dt, names))
+        workspace = prefill_mass_workspace_for(q, k_cache, block_tables, longest, stream)
+    wptr, wbytes = ((0, 0) if workspace is None else
+                    (workspace.data_ptr(), _bytes_of(workspace, dev)))
+    rc = load().pa_prefill_mass(_SPARSE_ARGS.pack(
+        _SPARSE_ARGS.size, 0, m, q.data_ptr(), k_cache.data_ptr(), 0, 0, block_tables.data_ptr(),
+        seq_lens.data_ptr(), _near(query_start, names.i32, dev), 0, 0, 0, 0, wptr,
+        names.raw_stream(dev) if stream is None else stream.cuda_stream, wbytes, scale, decay, n, t,
+        longest, hq, hkv, d, bs, mb, nb, 0, 0, 0, _code(dt, names), 0))
+    if rc:
+        raise PagedAttnError("pa_prefill_mass", rc)
     return mass
 
 
@@ -856,19 +891,27 @@ def evict(k_cache, v_cache, mass, block_tables, seq_lens, new_lens, keep_first=0
     by mass, which moves along.  The caller shortens seq_lens to new_lens, gives back the
     blocks past it and renews the bounds; the sequence's blocks must be its own."""
     names = _hot()
-    nb, hkv, bs, d = k_cache.shape
+    nb, hkv, bs, d = pool = k_cache.shape
+    n = seq_lens.shape[0]
     dt, dev = k_cache.dtype, _current(k_cache, names)
-    n, mb, tables, lens = _tables(block_tables, seq_lens, names, dev)
-    if v_cache.shape != k_cache.shape or new_lens.shape != (n,):
+    mb = _tables_of(block_tables, seq_lens, n, names, dev)
+    if v_cache.shape != pool or new_lens.shape != (n,):
         raise ValueError("shapes")
+    if (v_cache.dtype is not dt or v_cache.get_device() != dev or
+            not (k_cache.is_contiguous() and v_cache.is_contiguous())):
+        raise ValueError(_NEAR)
     m = _mass_rows(mass, n, hkv, mb, names, dev)
     if workspace is None:
         workspace = evict_workspace_for(k_cache, block_tables, stream)
-    _sparse_call("pa_evict", dev, names, stream, mass=m, k=_near(k_cache, dt, dev),
-                 v=_near(v_cache, dt, dev), tables=tables, lens=lens,
-                 new_lens=_near(new_lens, names.i32, dev), workspace=workspace, n=n, hkv=hkv, d=d,
-                 bs=bs, mb=mb, nb=nb, first=int(keep_first), last=int(keep_last),
-                 code=_code(dt, names))
+    wptr, wbytes = ((0, 0) if workspace is None else
+                    (workspace.data_ptr(), _bytes_of(workspace, dev)))
+    rc = load().pa_evict(_SPARSE_ARGS.pack(
+        _SPARSE_ARGS.size, 0, m, 0, k_cache.data_ptr(), v_cache.data_ptr(), 0,
+        block_tables.data_ptr(), seq_lens.data_ptr(), 0, 0, _near(new_lens, names.i32, dev), 0, 0,
+        wptr, names.raw_stream(dev) if stream is None else stream.cuda_stream, wbytes, 0.0, 0.0, n,
+        0, 0, 0, hkv, d, bs, mb, nb, 0, keep_first, keep_last, _code(dt, names), 0))
+    if rc:
+        raise PagedAttnError("pa_evict", rc)
 
 
 def copy_blocks(k_cache, v_cache, block_mapping, stream=None):

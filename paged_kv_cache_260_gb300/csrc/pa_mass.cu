@@ -746,6 +746,15 @@ __global__ void __launch_bounds__(kMassShortThreads) prefill_mass_short_kernel(c
     if (x.blocks == 0)
         return;
     const int nblk = (x.L + kBlockSize - 1) / kBlockSize;
+    const int rows = x.c * G, steps = (x.L + 7) / 8;
+    // everything that will be read is on its way to L2 before the first use waits for it
+    constexpr int LPR = D * 2 / 128;              // lines of a row
+    for (int i = tid; i < rows * LPR; i += kMassShortThreads)
+        prefetch_l2(static_cast<const T *>(p.q) +
+                    ((size_t)(x.qs + i / LPR / G) * Hq + h * G + i / LPR % G) * D + i % LPR * 64);
+    float *mass = p.mass + (size_t)blockIdx.x * p.max_blocks * kBlockSize;
+    if (tid * 32 < x.L)
+        prefetch_l2(mass + tid * 32);
     if (tid < nblk) {
         int phys = __ldg(p.block_tables + (size_t)s * p.max_blocks + tid);
         if ((unsigned)phys >= (unsigned)p.num_blocks) {
@@ -757,8 +766,11 @@ __global__ void __launch_bounds__(kMassShortThreads) prefill_mass_short_kernel(c
     for (int t = lane; t < nblk * kBlockSize; t += 32)
         acc[warp][t] = 0.f;
     __syncthreads();
+    for (int i = tid; i < x.L * LPR; i += kMassShortThreads)
+        prefetch_l2(static_cast<const T *>(p.k_cache) +
+                    ((size_t)tile_of[i / LPR / kBlockSize] * kBlockSize + i / LPR % kBlockSize) * D +
+                    i % LPR * 64);
     const uint4 *kp = static_cast<const uint4 *>(p.k_cache) + qd;
-    const int rows = x.c * G, steps = (x.L + 7) / 8;
     for (int row0 = 16 * warp; row0 < rows; row0 += 16 * NW) {
         // rows row0 + r and + 8; past the last one that one again, without weight
         uint32_t a[2 * NI][4];
@@ -853,7 +865,6 @@ __global__ void __launch_bounds__(kMassShortThreads) prefill_mass_short_kernel(c
         });
     }
     __syncthreads();
-    float *mass = p.mass + (size_t)blockIdx.x * p.max_blocks * kBlockSize;
     for (int t = tid; t < x.L; t += kMassShortThreads) {
         float sum = 0.f;
 #pragma unroll

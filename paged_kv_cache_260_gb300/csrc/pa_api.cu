@@ -1505,10 +1505,10 @@ int pa_block_bounds(const struct pa_sparse_args *args)
                             static_cast<cudaStream_t>(a.stream), kargs);
 }
 
-// Workspace of pa_select_blocks: scores that do not fit in shared memory, and the longer
-// ones of blocks in doubt.
+// Workspace of pa_select_blocks: scores, of 16 each the size of the sums, and the longer
+// scores of blocks in doubt.
 struct SelectLayout {
-    size_t exact_off, total;
+    size_t size_off, exact_off, total;
     long long row;
 };
 
@@ -1517,7 +1517,8 @@ static SelectLayout select_layout(int num_seqs, int num_kv_heads, int max_blocks
     SelectLayout w{};
     w.row = ((long long)max_blocks + 15) / 16 * 16;
     const size_t n = (size_t)num_seqs * num_kv_heads * w.row;
-    w.exact_off = round_up(4 * n, 256);
+    w.size_off = round_up(4 * n, 256);
+    w.exact_off = w.size_off + round_up(n / 4, 256);
     w.total = w.exact_off + round_up(8 * n, 256);
     return w;
 }
@@ -1563,6 +1564,7 @@ int pa_select_blocks(const struct pa_sparse_args *args)
     p.block_tables = a.block_tables;
     p.seq_lens = a.seq_lens;
     p.scores = reinterpret_cast<float *>(ws);
+    p.sizes = reinterpret_cast<float *>(ws + w.size_off);
     p.exact = reinterpret_cast<unsigned long long *>(ws + w.exact_off);
     p.err = ds->err;
     p.num_seqs = a.num_seqs;
@@ -1577,16 +1579,21 @@ int pa_select_blocks(const struct pa_sparse_args *args)
     const int runs = a.num_seqs * a.num_kv_heads;
     const SelectLaunch e = select_launch(a.dtype == PA_DTYPE_BF16, a.head_dim,
                                          a.num_heads / a.num_kv_heads, runs, a.max_blocks_per_seq,
-                                         ds->num_sms);
+                                         a.keep, ds->num_sms);
     p.near = e.near;
     int dev = 0;
     cudaGetDevice(&dev);
     rc = ensure_smem(e.fn, dev, e.smem);
     if (rc != PA_OK)
         return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(a.stream);
     void *kargs[] = {&p};
-    return launch_dependent(e.fn, dim3((unsigned)(runs * e.cluster)), dim3(e.threads), e.smem,
-                            static_cast<cudaStream_t>(a.stream), kargs, e.cluster);
+    if (e.score_fn) {
+        rc = launch_dependent(e.score_fn, dim3(e.score_blocks), dim3(e.score_threads), 0, st, kargs);
+        if (rc != PA_OK)
+            return rc;
+    }
+    return launch_dependent(e.fn, dim3((unsigned)runs), dim3(e.threads), e.smem, st, kargs);
 }
 
 // The pool with a kv head's tile as a block of its own: every (sequence, kv head) is a

@@ -164,12 +164,16 @@ __global__ void __launch_bounds__(kBoundsThreads) block_bounds_kernel(const Boun
 // lowest position.  (Where scores are equal at the border, t is that score, and
 // all of them lie between.)
 //
-// One thread block takes a (sequence, kv head), or a cluster of blocks a contiguous
-// part of its blocks each (CLUSTER); the scores stay in shared memory (in the
-// workspace, where a block's part is larger than p.near).
+// One thread block takes a (sequence, kv head), computes its scores and keeps them in
+// shared memory (in the workspace, where they are more than p.near).  Few long
+// sequences would leave most SMs idle: their scores are computed first, by a
+// kernel whose warps share out all of them evenly, and read from the workspace
+// (SCORED).
 // ---------------------------------------------------------------------------
+// A block a run from this many runs an SM on, else the scores apart.
+constexpr int kSelectRuns = 2;
 constexpr int kDoubt = 256;                       // blocks in doubt that are ranked directly
-constexpr int kSelectNear = 32768;                // scores a block holds (128 KB)
+constexpr int kSelectNear = 16384;                // scores a block holds (64 KB)
 
 // The order of floats as unsigned numbers (-0 as 0), and back.
 __device__ __forceinline__ uint32_t ordered(float x)
@@ -191,23 +195,208 @@ __device__ __forceinline__ void two_add(float &s, float &e, float x)
     s = t;
 }
 
-template <typename T, int D, int NT, int NTH, bool CLUSTER>
-__global__ void __launch_bounds__(NTH, 512 / NTH) block_select_kernel_t(const SelectParams p)
+// min(q, 0) and max(q, 0) of a (sequence, kv head)'s queries as fragments of the B
+// operand: lane (r, qd) holds channels 32 k + 8 qd .. + 7 of heads 8 j + r.
+template <typename T, int D, int NT>
+struct ScoreQueries {
+    static constexpr int NI = D / 32;             // 16-byte loads of a row's minima (maxima)
+    uint32_t neg[NT][NI][4], pos[NT][NI][4];
+
+    __device__ __forceinline__ void load(const T *q, int G, int r, int qd)
+    {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(q + min(8 * j + r, G - 1) * D);
+#pragma unroll
+            for (int k = 0; k < NI; ++k) {
+                const uint4 x = __ldg(src + 4 * k + qd);
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    neg[j][k][e] = min2<T>(w[e], 0u);
+                    pos[j][k][e] = max2<T>(w[e], 0u);
+                }
+            }
+        }
+    }
+};
+
+// The scores of 16 blocks by a warp: best[0] and [1] of blocks r and r + 8, the greatest
+// head's, infinite where one is not finite.  size rises to the largest sum |q||bound| of
+// the others.  tile: the pool tiles of blocks r and r + 8.  between() runs while the loads
+// are in flight.
+template <typename T, int D, int NT, typename F>
+__device__ __forceinline__ void score_tile(const ScoreQueries<T, D, NT> &q, const void *bounds,
+                                           const int (&tile)[2], int G, int qd, float (&best)[2],
+                                           float &size, const F &between)
 {
     using M = Mma<T>;
+    constexpr int NI = D / 32;
+    uint4 x[2][2 * NI];
+#pragma unroll
+    for (int k = 0; k < 2 * NI; ++k)
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+            x[a][k] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(bounds) +
+                                                            (size_t)tile[a] * 2 * D) +
+                            4 * k + qd);
+    between();
+    // the scores, and sum |q||bound|: the same products of magnitudes
+    float acc[NT][4], mag[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            acc[j][e] = mag[j][e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < 2 * NI; ++k) {
+        uint32_t a0[4] = {x[0][k].x, x[1][k].x, x[0][k].y, x[1][k].y};
+        uint32_t a1[4] = {x[0][k].z, x[1][k].z, x[0][k].w, x[1][k].w};
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const uint32_t *qq = k < NI ? q.neg[j][k] : q.pos[j][k - NI];
+            M::run(acc[j], a0, qq[0], qq[1]);
+            M::run(acc[j], a1, qq[2], qq[3]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {             // -|min| and |max|
+            a0[e] = k < NI ? a0[e] | 0x80008000u : a0[e] & 0x7fff7fffu;
+            a1[e] = k < NI ? a1[e] | 0x80008000u : a1[e] & 0x7fff7fffu;
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const uint32_t *qq = k < NI ? q.neg[j][k] : q.pos[j][k - NI];
+            M::run(mag[j], a0, qq[0], qq[1]);
+            M::run(mag[j], a1, qq[2], qq[3]);
+        }
+    }
+    best[0] = best[1] = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool finite = fabsf(acc[j][e]) <= FLT_MAX;
+            size = finite ? fmaxf(size, mag[j][e]) : size;
+            const float v = finite ? acc[j][e] : INFINITY;
+            if (8 * j + 2 * qd + (e & 1) < G)
+                best[e >> 1] = fmaxf(best[e >> 1], v);
+        }
+#pragma unroll
+    for (int off = 1; off < 4; off <<= 1) {
+        best[0] = fmaxf(best[0], __shfl_xor_sync(0xffffffffu, best[0], off));
+        best[1] = fmaxf(best[1], __shfl_xor_sync(0xffffffffu, best[1], off));
+    }
+}
+
+// All scores of the batch to the workspace, and of every 16 the largest sum |q||bound|.
+// The warps take equal shares of the list of (sequence, kv head, 16 blocks); a sequence
+// that keeps all of its blocks has none in it.
+constexpr int kScoreThreads = 128;
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kScoreThreads, 4) block_score_kernel_t(const SelectParams p)
+{
+    __shared__ RaggedSmem sm;
+    const int lane = threadIdx.x & 31;
+    const int warps = gridDim.x * (kScoreThreads / 32);
+    const int me = blockIdx.x * (kScoreThreads / 32) + (threadIdx.x >> 5);
+    const int Hkv = p.num_kv_heads, G = p.num_heads / Hkv;
+    const int r = lane >> 2, qd = lane & 3;
+    grid_dependents_launch();
+    grid_dependency_wait();
+    for (int begin = 0; begin < p.num_seqs; begin += kRaggedSeqs) {
+        const int n = min(kRaggedSeqs, p.num_seqs - begin);
+        ragged_prefix<kScoreThreads>(sm, begin, n, [&](int s) {
+            const int L = min(max(__ldg(p.seq_lens + s), 0), p.max_blocks * kBlockSize);
+            const int nb = (L + kBlockSize - 1) / kBlockSize;
+            return nb <= p.keep ? 0 : (nb + 15) / 16;
+        });
+        const long long total = (long long)sm.pre[n] * Hkv;
+        const long long share = (total + warps - 1) / warps;
+        long long u = me * share;
+        const long long end = min(total, u + share);
+        if (u >= end)
+            continue;
+        int i = ragged_find(sm, n, (int)(u / Hkv));
+        int nt = sm.pre[i + 1] - sm.pre[i];
+        int h = (int)((u - (long long)sm.pre[i] * Hkv) / nt);
+        int t = (int)((u - (long long)sm.pre[i] * Hkv) % nt);
+        int nb = 0;
+        // rows r and r + 8 of 16 blocks; past the end the last block again
+        auto tiles_of = [&](int (&tile)[2]) {
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+                int phys = __ldg(p.block_tables + (size_t)(begin + i) * p.max_blocks +
+                                 min(16 * t + 8 * a + r, nb - 1));
+                if ((unsigned)phys >= (unsigned)p.num_blocks) {
+                    record_error(p.err, PA_DEVERR_TABLE_RANGE);
+                    phys = 0;
+                }
+                tile[a] = phys * Hkv + h;
+            }
+        };
+        auto enter = [&]() {
+            const int L = min(max(__ldg(p.seq_lens + begin + i), 0), p.max_blocks * kBlockSize);
+            nb = (L + kBlockSize - 1) / kBlockSize;
+        };
+        enter();
+        ScoreQueries<T, D, NT> q;
+        bool fresh = true;
+        int tile[2], next[2] = {0, 0};
+        tiles_of(tile);
+        for (; u < end; ++u) {
+            const size_t run = (size_t)(begin + i) * Hkv + h;
+            const int first = 16 * t, blocks = nb;
+            if (fresh)
+                q.load(static_cast<const T *>(p.q) + run * G * D, G, r, qd);
+            fresh = false;
+            float best[2], size = 0.f;
+            score_tile<T, D, NT>(q, p.bounds, tile, G, qd, best, size, [&]() {
+                if (++t == nt) {
+                    t = 0;
+                    fresh = true;
+                    if (++h == Hkv) {
+                        h = 0;
+                        do
+                            ++i;
+                        while (i < n && sm.pre[i + 1] == sm.pre[i]);
+                        if (i < n) {
+                            nt = sm.pre[i + 1] - sm.pre[i];
+                            enter();
+                        }
+                    }
+                }
+                if (u + 1 < end)
+                    tiles_of(next);
+            });
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1)
+                size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, off));
+            const int j = first + 8 * qd + r;
+            if (qd < 2 && j < blocks)
+                p.scores[run * p.row + j] = qd ? best[1] : best[0];
+            if (lane == 0)
+                p.sizes[run * (p.row / 16) + first / 16] = size;
+            tile[0] = next[0];
+            tile[1] = next[1];
+        }
+    }
+}
+
+template <typename T, int D, int NT, int NTH, bool SCORED>
+__global__ void __launch_bounds__(NTH, SCORED ? 1 : 512 / NTH) block_select_kernel_t(const SelectParams p)
+{
     constexpr uint32_t FULL = 0xffffffffu;
     constexpr int NW = NTH / 32;
-    constexpr int NI = D / 32;                    // 16-byte loads of a row's minima (maxima)
     extern __shared__ float near_scores[];
     __shared__ float q[8 * NT * D];               // the group's queries
-    __shared__ unsigned long long near_keys[CLUSTER ? 1 : kDoubt];
+    __shared__ unsigned long long near_keys[kDoubt];
     __shared__ TallySmem<NW> counts;
     __shared__ RadixSmem<NW> radix;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int Hkv = p.num_kv_heads, G = p.num_heads / Hkv;
-    Tally<NW, CLUSTER> tally(counts);
-    const int C = tally.blocks, rank = tally.rank;
-    const int run = blockIdx.x / C, s = run / Hkv, h = run % Hkv;
+    Tally<NW, false> tally(counts);
+    const int run = blockIdx.x, s = run / Hkv, h = run % Hkv;
     grid_dependents_launch();
     grid_dependency_wait();
     int L = __ldg(p.seq_lens + s);
@@ -228,107 +417,53 @@ __global__ void __launch_bounds__(NTH, 512 / NTH) block_select_kernel_t(const Se
         }
         return phys * Hkv + h;
     };
-    if (tid == 0 && rank == 0)
+    if (tid == 0)
         p.tile_lens[run] = L - kBlockSize * max(0, nb - p.keep);
     if (nb <= p.keep) {
-        for (int j = rank * NTH + tid; j < p.keep; j += C * NTH)
+        for (int j = tid; j < p.keep; j += NTH)
             out[j] = j < nb ? tile_of(j) : -1;
         return;
     }
     const int lo = p.keep_first, hi = nb - p.keep_last;   // the blocks that compete
     int want = p.keep - p.keep_first - p.keep_last;       // how many of them are kept
 
-    // ---- scores of this thread block's part [b0, b1) ----
-    const int span = (nb + 16 * C - 1) / (16 * C) * 16;
-    const int b0 = min(nb, rank * span), b1 = min(nb, b0 + span);
-    float *score = (p.near >= span ? near_scores : p.scores + (size_t)run * p.row + b0) - b0;
-    const T *qg = static_cast<const T *>(p.q) + ((size_t)s * p.num_heads + h * G) * D;
-    const int r = lane >> 2, qd = lane & 3;
+    // ---- the scores ----
+    float *far_scores = p.scores + (size_t)run * p.row;
+    float *score = p.near >= nb ? near_scores : far_scores;
+    const T *qg = static_cast<const T *>(p.q) + (size_t)run * G * D;
     float size = 0.f;                             // the largest sum |q||bound|
-    {
-        uint32_t qn[NT][NI][4], qp[NT][NI][4];    // min(q, 0) and max(q, 0)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(qg + min(8 * j + r, G - 1) * D);
-#pragma unroll
-            for (int k = 0; k < NI; ++k) {
-                const uint4 x = __ldg(src + 4 * k + qd);
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    qn[j][k][e] = min2<T>(w[e], 0u);
-                    qp[j][k][e] = max2<T>(w[e], 0u);
-                }
-            }
+    if (SCORED) {
+        for (int i = tid; i < (nb + 15) / 16; i += NTH)
+            size = fmaxf(size, __ldcg(p.sizes + (size_t)run * (p.row / 16) + i));
+        if (p.near >= nb) {
+            const float4 *src = reinterpret_cast<const float4 *>(far_scores);
+#pragma unroll 4
+            for (int i = tid; i < (nb + 3) / 4; i += NTH)
+                reinterpret_cast<float4 *>(near_scores)[i] = __ldcg(src + i);
         }
+    } else {
+        const int r = lane >> 2, qd = lane & 3;
+        ScoreQueries<T, D, NT> queries;
+        queries.load(qg, G, r, qd);
         // rows r and r + 8 of the next 16 blocks; past the end the last block again
         auto rows = [&](int b, int (&tile)[2]) {
             tile[0] = tile_of(min(b + r, nb - 1));
             tile[1] = tile_of(min(b + 8 + r, nb - 1));
         };
-        int tile[2] = {0, 0};
-        if (b0 + 16 * warp < b1)
-            rows(b0 + 16 * warp, tile);
-        for (int b = b0 + 16 * warp; b < b1; b += 16 * NW) {
-            uint4 x[2][2 * NI];
-#pragma unroll
-            for (int k = 0; k < 2 * NI; ++k)
-#pragma unroll
-                for (int a = 0; a < 2; ++a)
-                    x[a][k] = __ldg(reinterpret_cast<const uint4 *>(
-                                        static_cast<const T *>(p.bounds) + (size_t)tile[a] * 2 * D) +
-                                    4 * k + qd);
-            if (b + 16 * NW < b1)
-                rows(b + 16 * NW, tile);
-            // the scores, and sum |q||bound|: the same products of magnitudes
-            float acc[NT][4], mag[NT][4];
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[j][e] = mag[j][e] = 0.f;
-#pragma unroll
-            for (int k = 0; k < 2 * NI; ++k) {
-                uint32_t a0[4] = {x[0][k].x, x[1][k].x, x[0][k].y, x[1][k].y};
-                uint32_t a1[4] = {x[0][k].z, x[1][k].z, x[0][k].w, x[1][k].w};
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const uint32_t *qq = k < NI ? qn[j][k] : qp[j][k - NI];
-                    M::run(acc[j], a0, qq[0], qq[1]);
-                    M::run(acc[j], a1, qq[2], qq[3]);
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {     // -|min| and |max|
-                    a0[e] = k < NI ? a0[e] | 0x80008000u : a0[e] & 0x7fff7fffu;
-                    a1[e] = k < NI ? a1[e] | 0x80008000u : a1[e] & 0x7fff7fffu;
-                }
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const uint32_t *qq = k < NI ? qn[j][k] : qp[j][k - NI];
-                    M::run(mag[j], a0, qq[0], qq[1]);
-                    M::run(mag[j], a1, qq[2], qq[3]);
-                }
-            }
-            // the greatest head's score of block r (and r + 8); not finite: first of all
-            float best[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const bool finite = fabsf(acc[j][e]) <= FLT_MAX;
-                    size = finite ? fmaxf(size, mag[j][e]) : size;
-                    const float v = finite ? acc[j][e] : INFINITY;
-                    if (8 * j + 2 * qd + (e & 1) < G)
-                        best[e >> 1] = fmaxf(best[e >> 1], v);
-                }
-#pragma unroll
-            for (int off = 1; off < 4; off <<= 1) {
-                best[0] = fmaxf(best[0], __shfl_xor_sync(FULL, best[0], off));
-                best[1] = fmaxf(best[1], __shfl_xor_sync(FULL, best[1], off));
-            }
+        int tile[2] = {0, 0}, next[2] = {0, 0};
+        if (16 * warp < nb)
+            rows(16 * warp, tile);
+        for (int b = 16 * warp; b < nb; b += 16 * NW) {
+            float best[2];
+            score_tile<T, D, NT>(queries, p.bounds, tile, G, qd, best, size, [&]() {
+                if (b + 16 * NW < nb)
+                    rows(b + 16 * NW, next);
+            });
             const int j = b + 8 * qd + r;
-            if (qd < 2 && j < b1)
+            if (qd < 2 && j < nb)
                 score[j] = qd ? best[1] : best[0];
+            tile[0] = next[0];
+            tile[1] = next[1];
         }
     }
     // ---- the queries, for those that are summed again ----
@@ -338,10 +473,10 @@ __global__ void __launch_bounds__(NTH, 512 / NTH) block_select_kernel_t(const Se
         radix.hist[0][i] = 0;
     __syncthreads();
     // a warp's contiguous part of the blocks that compete: [w0, ..) in `steps` steps of 32
-    const int c0 = min(max(b0, lo), hi), c1 = max(c0, min(b1, hi));
-    const int steps = (c1 - c0 + NTH - 1) / NTH;
-    const int w0 = c0 + warp * steps * 32;
+    const int c1 = hi, steps = (c1 - lo + NTH - 1) / NTH;
+    const int w0 = lo + warp * steps * 32;
     auto each = [&](auto &&f) {                   // f(block, score), -inf past the end
+#pragma unroll 4
         for (int i = 0; i < steps; ++i) {
             const int j = w0 + 32 * i + lane;
             f(j, j < c1 ? score[j] : -INFINITY);
@@ -432,7 +567,7 @@ __global__ void __launch_bounds__(NTH, 512 / NTH) block_select_kernel_t(const Se
             };
             // their keys in the order of their positions; key i of the run is in list[i]
             unsigned long long *list =
-                !CLUSTER && total <= kDoubt ? near_keys : p.exact + (size_t)run * p.row;
+                total <= kDoubt ? near_keys : p.exact + (size_t)run * p.row;
             int at = mine;
             each([&](int j, float x) {
                 unsigned m = __ballot_sync(FULL, j < c1 && doubtful(x));
@@ -528,12 +663,11 @@ __global__ void __launch_bounds__(NTH, 512 / NTH) block_select_kernel_t(const Se
             out[at + __popc(m & ((1u << lane) - 1))] = tile_of(j);
         at += __popc(m);
     });
-    for (int i = rank * NTH + tid; i < p.keep_first + p.keep_last; i += C * NTH)
+    for (int i = tid; i < p.keep_first + p.keep_last; i += NTH)
         if (i < lo)
             out[i] = tile_of(i);
         else
             out[p.keep - p.keep_last + i - lo] = tile_of(hi + i - lo);
-    tally.leave();
 }
 
 }  // namespace
@@ -552,41 +686,57 @@ SparseKernel bounds_kernel(bool bf16, int head_dim)
 
 namespace {
 
-template <typename T, int D, int NTH, bool CLUSTER>
-const void *select_fn(int group)
+// which: the selection with scores of its own by 128 or by 256 threads, that from given
+// scores by 1024, or the kernel that computes those
+enum Which { kSmall, kLarge, kGiven, kScores };
+
+template <typename T, int D, int NT>
+const void *select_fn(Which which)
 {
-    return group <= 8 ? reinterpret_cast<const void *>(&block_select_kernel_t<T, D, 1, NTH, CLUSTER>)
-                      : reinterpret_cast<const void *>(&block_select_kernel_t<T, D, 2, NTH, CLUSTER>);
+    switch (which) {
+    case kSmall:
+        return reinterpret_cast<const void *>(&block_select_kernel_t<T, D, NT, 128, false>);
+    case kLarge:
+        return reinterpret_cast<const void *>(&block_select_kernel_t<T, D, NT, 256, false>);
+    case kGiven:
+        return reinterpret_cast<const void *>(&block_select_kernel_t<T, D, NT, 1024, true>);
+    default:
+        return reinterpret_cast<const void *>(&block_score_kernel_t<T, D, NT>);
+    }
 }
 
-template <int NTH, bool CLUSTER>
-const void *select_fn(bool bf16, int head_dim, int group)
+const void *select_fn(bool bf16, int head_dim, int group, Which which)
 {
     if (head_dim == 128)
-        return bf16 ? select_fn<__nv_bfloat16, 128, NTH, CLUSTER>(group)
-                    : select_fn<__half, 128, NTH, CLUSTER>(group);
-    return bf16 ? select_fn<__nv_bfloat16, 64, NTH, CLUSTER>(group)
-                : select_fn<__half, 64, NTH, CLUSTER>(group);
+        return bf16 ? group <= 8 ? select_fn<__nv_bfloat16, 128, 1>(which)
+                                 : select_fn<__nv_bfloat16, 128, 2>(which)
+                    : group <= 8 ? select_fn<__half, 128, 1>(which)
+                                 : select_fn<__half, 128, 2>(which);
+    return bf16 ? group <= 8 ? select_fn<__nv_bfloat16, 64, 1>(which)
+                             : select_fn<__nv_bfloat16, 64, 2>(which)
+                : group <= 8 ? select_fn<__half, 64, 1>(which) : select_fn<__half, 64, 2>(which);
 }
 
 }  // namespace
 
-// Short tables: a block of 128 threads a run.  Others: 256 threads, and where the runs leave
-// SMs idle a cluster of 2, 4 or 8 blocks shares a run.
 SelectLaunch select_launch(bool bf16, int head_dim, int group, int num_runs, int max_blocks,
-                           int num_sms)
+                           int keep, int num_sms)
 {
     SelectLaunch e{};
     const bool small = max_blocks <= 256;
-    e.threads = small ? 128 : 256;
-    e.cluster = 1;
-    while (!small && e.cluster < 8 && 2LL * e.cluster * num_runs <= 2LL * num_sms &&
-           max_blocks >= 256 * e.cluster)
-        e.cluster *= 2;
-    e.fn = small ? select_fn<128, false>(bf16, head_dim, group)
-                 : select_fn<256, true>(bf16, head_dim, group);
-    const long long span = ((long long)max_blocks + 16 * e.cluster - 1) / (16 * e.cluster) * 16;
-    e.near = span <= kSelectNear ? (int)span : 0;
+    const bool apart = !small && max_blocks > keep && num_runs < kSelectRuns * num_sms;
+    e.threads = small ? 128 : apart ? 1024 : 256;
+    e.fn = select_fn(bf16, head_dim, group, small ? kSmall : apart ? kGiven : kLarge);
+    if (apart) {
+        e.score_fn = select_fn(bf16, head_dim, group, kScores);
+        e.score_threads = kScoreThreads;
+        // as many blocks as run at once, or as there is work for
+        const long long warps = (long long)num_runs * ((max_blocks + 15) / 16);
+        const long long blocks = (warps + kScoreThreads / 32 - 1) / (kScoreThreads / 32);
+        e.score_blocks = (int)(blocks < 4LL * num_sms ? blocks : 4LL * num_sms);
+    }
+    const long long all = ((long long)max_blocks + 15) / 16 * 16;
+    e.near = all <= kSelectNear ? (int)all : 0;
     e.smem = 4 * (size_t)e.near;
     return e;
 }

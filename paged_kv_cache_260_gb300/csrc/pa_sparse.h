@@ -27,7 +27,8 @@ struct SelectParams {
     const int32_t *block_tables;
     const int32_t *seq_lens;
     float *scores;                 // workspace: [num_seqs][num_kv_heads][row] fp32 scores, if
-                                   //   a thread block's do not fit its shared memory,
+                                   //   they are computed apart or do not fit shared memory,
+    float *sizes;                  //   [..][row / 16] with those the largest sum |q||bound|,
     unsigned long long *exact;     //   [..][row] scores with more bits, of those in doubt
     uint32_t *err;
     int num_seqs, num_heads, num_kv_heads, max_blocks, num_blocks;
@@ -36,10 +37,10 @@ struct SelectParams {
     int near;                      // scores a thread block holds in shared memory, or 0
 };
 
-// A launch of the selection kernel.
+// The selection's launch, and before it that of the scores (or null).
 struct SelectLaunch {
-    const void *fn;
-    int threads, cluster, near;
+    const void *fn, *score_fn;
+    int threads, near, score_threads, score_blocks;
     size_t smem;
 };
 
@@ -72,7 +73,7 @@ struct SparseKernel {
 
 SparseKernel bounds_kernel(bool bf16, int head_dim);
 SelectLaunch select_launch(bool bf16, int head_dim, int group, int num_runs, int max_blocks,
-                           int num_sms);
+                           int keep, int num_sms);
 EvictLaunch evict_launch(int head_dim, int num_runs, int max_blocks, int num_sms);
 
 }  // namespace pa

@@ -15,12 +15,14 @@ struct TallySmem {
     int4 total[2];                 // read by the other blocks of the cluster
 };
 
-// How many keys have each value of a digit: four values a thread, 32 a group.
+// How many keys have each value of a digit, a thread's values one after the other; 32
+// values a group.
 template <int NW>
 struct RadixSmem {
-    static constexpr int BINS = 4 * 32 * NW, BITS = NW == 8 ? 10 : 9, GROUPS = BINS / 32;
-    static_assert(BINS == 1 << BITS, "128 or 256 threads");
-    alignas(16) int hist[2][BINS];
+    static constexpr int BITS = NW == 4 ? 9 : 10, BINS = 1 << BITS, GROUPS = BINS / 32;
+    static constexpr int EACH = BINS / (32 * NW);          // values a thread
+    static_assert(NW == 4 || NW == 8 || NW == 16 || NW == 32, "128 to 1024 threads");
+    int hist[2][BINS];
     int group[2][GROUPS];          // both read by the other blocks of the cluster
     int found[3];
 };
@@ -149,16 +151,21 @@ struct Tally {
                     atomicAdd(&hist[k >> shift & mask], 1);
             });
             __syncthreads();
-            const int4 v = reinterpret_cast<const int4 *>(hist)[threadIdx.x];
-            int n = v.x + v.y + v.z + v.w;
+            constexpr int EACH = RadixSmem<NW>::EACH, SPAN = 32 / EACH;
+            int n = 0;
 #pragma unroll
-            for (int o = 1; o < 8; o <<= 1)
+            for (int i = 0; i < EACH; ++i)
+                n += hist[EACH * threadIdx.x + i];
+#pragma unroll
+            for (int o = 1; o < SPAN; o <<= 1)
                 n += __shfl_xor_sync(FULL, n, o);
-            if (lane % 8 == 0)
-                r.group[buf][threadIdx.x / 8] = n;
+            if (lane % SPAN == 0)
+                r.group[buf][threadIdx.x / SPAN] = n;
             sync();
             // (the blocks have read the other buffer: they have been through this barrier)
-            reinterpret_cast<int4 *>(r.hist[buf ^ 1])[threadIdx.x] = make_int4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < EACH; ++i)
+                r.hist[buf ^ 1][EACH * threadIdx.x + i] = 0;
             if (warp == 0) {
                 // the group with the want-th largest, then the value: a lane each, summed over
                 // the blocks with all loads in flight at once

@@ -205,6 +205,23 @@ def test_select_of_many_sequences(pa):
     same_choice(pa, q, b, tables, lens, 5, 1, 1)
 
 
+@pytest.mark.parametrize("runs,hkv", [(3, 1), (400, 1), (40, 8)])
+def test_select_in_long_tables(pa, runs, hkv):
+    # few runs: the scores apart; many: a block each
+    r = gen(42, runs, hkv)
+    lens = [int(x) for x in torch.randint(0, 16 * 300, (runs,), generator=r)]
+    lens[1] = 16 * 300
+    tables, nb = su.tables_for(r, lens)
+    b = torch.randn(nb, hkv, 2, 64, generator=r).half().sort(2).values.contiguous()
+    q = torch.randn(runs, hkv, 64, generator=r).half()
+    same_choice(pa, q, b, tables, lens, 20, 1, 1)
+    bad, as_zero = tables.clone(), tables.clone()
+    bad[1, 299], bad[1, 7], as_zero[1, 299], as_zero[1, 7] = nb, -1, 0, 0
+    got = run_select(pa, q, b, bad, lens, 20, 0, 1)
+    check(pa, pa.DEVERR["TABLE_RANGE"])
+    assert torch.equal(got[0].cpu(), su.select(q, b, as_zero, lens, 20, 0, 1)[0])
+
+
 def test_select_reports_bad_arguments(pa):
     r = gen(11)
     lens = [16 * 20, 16 * 20]

@@ -92,8 +92,8 @@ def test_one_refuses(lib, name, kw, status):
 
 
 def test_workspace_sizes(lib):
-    # scores, and 8 bytes a score in doubt: rows of 16 blocks
-    assert lib.pa_select_blocks_workspace_size(4, 2, 8) == 512 + 1024
+    # scores, 4 bytes for 16 of them, and 8 bytes a score in doubt: rows of 16 blocks
+    assert lib.pa_select_blocks_workspace_size(4, 2, 8) == 512 + 256 + 1024
     assert lib.pa_select_blocks_workspace_size(0, 2, 8) == 0
     assert lib.pa_evict_workspace_size(4, 2, 8) == 4 * 4 * 2 * 128
     assert lib.pa_evict_workspace_size(4, 0, 8) == 0

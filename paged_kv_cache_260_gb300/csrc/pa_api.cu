@@ -1709,7 +1709,7 @@ int pa_decode_mass(const struct pa_sparse_args *args)
 
 // pa_prefill_mass's units of 2 x 128 rows, and its workspace: the statistics of the units'
 // pieces (one for each unit and one more for each border between two blocks' shares), and
-// each query tile's sums for every key.
+// of several row blocks each query tile's sums for every key.
 struct PrefillMassPlan {
     long long row_blocks, units, tiles;
     size_t sums_off, total;
@@ -1727,7 +1727,9 @@ static bool prefill_mass_plan(int num_seqs, int max_query_len, int num_heads, in
     w->tiles = w->units * (((long long)max_blocks * kBlockSize + kMassKeys - 1) / kMassKeys);
     w->sums_off = round_up(
         sizeof(float2) * (size_t)(w->units + num_sms) * 2 * kMassTiles * kMassRows, 256);
-    w->total = w->sums_off + sizeof(float) * (size_t)w->units * kMassTiles * max_blocks * kBlockSize;
+    w->total = w->sums_off;
+    if (w->row_blocks > 1)
+        w->total += sizeof(float) * (size_t)w->units * kMassTiles * max_blocks * kBlockSize;
     return true;
 }
 
@@ -1821,7 +1823,7 @@ int pa_prefill_mass(const struct pa_sparse_args *args)
     rc = launch_dependent(k.stats, grid, dim3(k.threads), k.smem_stats, st, kargs);
     if (rc == PA_OK)
         rc = launch_dependent(k.sums, grid, dim3(k.threads), k.smem_sums, st, kargs);
-    if (rc != PA_OK)
+    if (rc != PA_OK || w.row_blocks == 1)       // one row block: the second pass made the mass
         return rc;
     const long long units = (long long)a.num_seqs * a.num_kv_heads * ((a.max_blocks_per_seq + 7) / 8);
     return launch_dependent(prefill_mass_finish(),

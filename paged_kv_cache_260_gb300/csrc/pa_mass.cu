@@ -137,13 +137,14 @@ struct MassShape {
     static constexpr int BOX = 2048;                      // 16 rows x 128 B
     static constexpr int Q_BYTES = SUMS ? NG * BM * D * 2 : 0;   // [half][256 rows][128 B]
     static constexpr int SLOT_BYTES = BN * D * 2;         // [half][8 blocks][16 rows][128 B]
-    static constexpr int NSLOT = D == 64 ? 8 : SUMS ? 5 : 6;
+    static constexpr int NSLOT = D == 64 ? 8 : SUMS ? 4 : 6;
     static constexpr int OFF_SLOT = Q_BYTES;
     static constexpr int OFF_LSE = OFF_SLOT + NSLOT * SLOT_BYTES;
-    // full[NSLOT] empty[NSLOT] s[4] read[3] q[2] free[2] group[2] drain, then TMEM base and
-    // abort flag
-    static constexpr int NBAR = 2 * NSLOT + 14;
-    static constexpr int OFF_BAR = OFF_LSE + NG * BM * 4;
+    static constexpr int OFF_PART = OFF_LSE + NG * BM * 4;       // [buffer][turn & 1][key]
+    // full[NSLOT] empty[NSLOT] s[4] read[3] q[2] free[2] group[2] sum[4] drain, then TMEM base
+    // and abort flag
+    static constexpr int NBAR = 2 * NSLOT + 18;
+    static constexpr int OFF_BAR = OFF_PART + (SUMS ? 4 * BN * 4 : 0);
     static constexpr int SMEM = 1024 + OFF_BAR + NBAR * 8 + 8;
     static constexpr int THREADS = 64 + NG * 256;
     // tensor memory: score buffers of 128 (pass 1) or 256 columns, pass 1's query rows
@@ -258,6 +259,7 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
     unsigned char *smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
     const uint32_t sbase = smem_addr(smem), slot_addr = sbase + Sh::OFF_SLOT;
     float *lse = reinterpret_cast<float *>(smem + Sh::OFF_LSE);      // minus the rows' log sums
+    float *part = reinterpret_cast<float *>(smem + Sh::OFF_PART);    // the first query tile's sums
     const uint32_t bar_addr = sbase + Sh::OFF_BAR;
     auto full_bar = [&](int s) { return bar_addr + 8u * s; };
     auto empty_bar = [&](int s) { return bar_addr + 8u * (NS + s); };
@@ -268,7 +270,8 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
     auto q_bar = [&](int g) { return bar_addr + 8u * (2 * NS + 7 + g); };
     auto free_bar = [&](int g) { return bar_addr + 8u * (2 * NS + 9 + g); };
     auto group_bar = [&](int g) { return bar_addr + 8u * (2 * NS + 11 + g); };
-    const uint32_t drain_bar = bar_addr + 8u * (2 * NS + 13);
+    auto sum_bar = [&](int i) { return bar_addr + 8u * (2 * NS + 13 + i); };
+    const uint32_t drain_bar = bar_addr + 8u * (2 * NS + 17);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Sh::OFF_BAR + Sh::NBAR * 8);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -281,8 +284,10 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
             mbar_init(full_bar(i), 1);
             mbar_init(empty_bar(i), 1);
         }
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) {
             mbar_init(s_bar(i), 1);
+            mbar_init(sum_bar(i), 128);
+        }
         for (int i = 0; i < 3; ++i)
             mbar_init(read_bar(i), 256);
         for (int g = 0; g < Sh::NG; ++g) {
@@ -603,7 +608,11 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
                 if (!ok)
                     break;
             }
+            // pass 2: one row block of the chunk makes the whole mass, the second query tile's
+            // threads adding the first one's sums; of several each leaves its sums
+            const bool alone = p.row_blocks == 1;
             float *sums = p.sums + (size_t)(2 * unit + grp) * ((size_t)p.max_blocks * kBlockSize);
+            float *mass = p.mass + ((size_t)w.s * Hkv + w.h) * p.max_blocks * kBlockSize;
             const int first_pos = w.x.L - w.x.c + t0;     // of the tile's first token
             for (int i = 0; i < w.te - w.tb; ++i, ++it) {
                 const int k0 = tile(i) * Sh::BN;
@@ -635,7 +644,9 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
                 const int vis = row_valid ? first_pos + rr / G - k0 : -1;
                 const int first = min(max(k0 + rr - first_pos, 0), 128) * G;
                 const bool full = __all_sync(FULL, SUMS ? first <= 0 : vis >= c0 + 63);
-                float sum = 0.f;
+                float sum = 0.f, old = 0.f;
+                if (SUMS && alone && grp == ng - 1 && k0 + rr < w.x.L - w.x.c && p.decay != 0.f)
+                    old = __ldcg(mass + k0 + rr);
 #pragma unroll 1
                 for (int c = c0; c < (SUMS ? 128 : c0 + 64); c += 64) {
                     uint32_t v[64];
@@ -698,10 +709,31 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
                     f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), a, b);
                     sum += a + b;
                 }
-                if (!SUMS)
+                if (!SUMS) {
                     l += sum;
-                else if (k0 + rr < w.x.L)
-                    sums[k0 + rr] = sum;
+                } else if (!alone) {
+                    if (k0 + rr < w.x.L)
+                        sums[k0 + rr] = sum;
+                } else {
+                    // Two places in turn: a set two of its tiles on has the other set of this
+                    // buffer past this one.
+                    if (ng == 2) {
+                        const int place = 2 * buf + (turn & 1);
+                        if (grp == 0) {
+                            part[place * Sh::BN + rr] = sum;
+                            mbar_arrive(sum_bar(place));
+                        } else {
+                            if (!__all_sync(FULL, mbar_wait_bounded(sum_bar(place), turn >> 1 & 1))) {
+                                ok = false;
+                                break;
+                            }
+                            sum += part[place * Sh::BN + rr];
+                        }
+                        ++turn;
+                    }
+                    if (grp == ng - 1 && k0 + rr < w.x.L)
+                        mass[k0 + rr] = fmaf(old, p.decay, sum);
+                }
             }
             if (ok && !SUMS)
                 stats[(size_t)blockIdx.x * (2 * ROWS) + half * ROWS] = make_float2(m, l);
@@ -874,8 +906,8 @@ __global__ void __launch_bounds__(kMassShortThreads) prefill_mass_short_kernel(c
     }
 }
 
-// The sum over a sequence's query tiles, added to the mass: a warp 128 tokens of a
-// (sequence, kv head), four a lane.
+// Several row blocks: the sum over a sequence's query tiles, added to the mass: a warp 128
+// tokens of a (sequence, kv head), four a lane.
 __global__ void __launch_bounds__(kMassFinishThreads)
 prefill_mass_finish_kernel(const PrefillMassParams p)
 {

@@ -222,6 +222,29 @@ def test_select_in_long_tables(pa, runs, hkv):
     assert torch.equal(got[0].cpu(), su.select(q, b, as_zero, lens, 20, 0, 1)[0])
 
 
+@pytest.mark.parametrize("runs", [2, 310])
+def test_select_of_more_scores_than_fit(pa, runs):
+    # a table wider than a thread block's shared memory holds scores for
+    r = gen(43, runs)
+    lens = [16 * (5 + i % 40) for i in range(runs)]
+    lens[-1] = 16 * 16500
+    tables, nb = su.tables_for(r, lens)
+    b = torch.randn(nb, 1, 2, 64, generator=r).half().sort(2).values.contiguous()
+    q = torch.randn(runs, 2, 64, generator=r).half()
+    same_choice(pa, q, b, tables, lens, 300, 2, 2)
+    b[tables[-1].long()] = b[0].clone()                # and all equal
+    same_choice(pa, q, b, tables, lens, 30, 2, 2)
+
+
+def test_select_between_equal_scores_of_many_runs(pa):
+    r = gen(44)
+    lens = [16 * 300] * 5 + [16 * (1 + i % 30) for i in range(310)]
+    tables, nb = su.tables_for(r, lens)
+    b = torch.randn(1, 1, 2, 64, generator=r).half().sort(2).values.repeat(nb, 1, 1, 1)
+    q = torch.randn(len(lens), 2, 64, generator=r).half()
+    same_choice(pa, q, b, tables, lens, 20, 1, 1)
+
+
 def test_select_reports_bad_arguments(pa):
     r = gen(11)
     lens = [16 * 20, 16 * 20]
@@ -567,6 +590,26 @@ def test_evict(pa, dt, d, hkv, first, last):
     ([40000], [39000], 10, 2000), ([1040] * 5, [1024] * 5, 4, 32), ([12000], [11000], 0, 11000)])
 def test_evict_long(pa, lens, new, first, last):
     evict_case(pa, gen(27, len(lens), first), lens, new, first, last, "bf16", 128, 1)
+
+
+def test_evict_in_wide_tables(pa):
+    # more table entries than a block holds, and (many runs, a block each) more masses
+    evict_case(pa, gen(45), [131200, 500], [100000, 40], 4, 64, "f16", 64, 1)
+    lens = [3 + i % 50 for i in range(320)]
+    lens[7], lens[200] = 40000, 35000
+    evict_case(pa, gen(46), lens, [min(n, 20) if n < 100 else 1000 for n in lens], 4, 5, "f16", 64, 1)
+    evict_case(pa, gen(47), lens, [min(n, 20) if n < 100 else 33000 for n in lens], 0, 40, "f16", 64,
+               1, mass=lambda *x: torch.randint(0, 3, x, generator=gen(48)).float())
+
+
+@pytest.mark.parametrize("runs,width", [(1, 4096), (30, 4096), (80, 8192), (150, 4096), (400, 2064),
+                                        (400, 2048)])
+def test_evict_by_blocks_and_clusters(pa, runs, width):
+    # as many thread blocks to a run as the runs leave room for, from eight to one
+    r = gen(49, runs)
+    lens = [int(x) for x in torch.randint(0, 900, (runs,), generator=r)]
+    lens[0] = width
+    evict_case(pa, r, lens, [n // 2 for n in lens], 3, 20, "bf16", 64, 1, mb=width // 16)
 
 
 def test_evict_ties_and_odd_masses(pa):

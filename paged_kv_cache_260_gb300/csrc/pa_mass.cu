@@ -32,7 +32,7 @@ __device__ __forceinline__ float add_mass(float *at, float decay, bool fresh, fl
 // After a decode: every token's weights from the kept scores.  A warp takes 128
 // tokens of a (sequence, kv head), four a lane a stride of 32 apart.
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(kMassFinishThreads)
+__global__ void __launch_bounds__(kMassFinishThreads, 4)
 decode_mass_finish_kernel(const DecodeMassParams p)
 {
     constexpr int NTH = kMassFinishThreads, TOK = 128;
@@ -278,7 +278,6 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int Hkv = p.num_kv_heads, Hq = p.num_heads, G = Hq / Hkv;
     const int TPG = Sh::BM / G, TPB = Sh::NG * TPG;       // chunk tokens of a tile, of a unit
-    grid_dependents_launch();
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(full_bar(i), 1);
@@ -303,7 +302,13 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
         tc::tmem_alloc(smem_addr(tmem_slot), 512);
         tc::tmem_relinquish();
     }
-    grid_dependency_wait();
+    // Pass 2 may be scheduled once every block of pass 1 is past the wait for what came before
+    // both: it then reads the caller's arrays at once, and waits for pass 1 where it reads
+    // statistics.
+    if (!SUMS) {
+        grid_dependency_wait();
+        grid_dependents_launch();
+    }
 
     // ---- the block's share: the list's length, then the sequence its share starts in ----
     auto tiles_of = [&](int s, bool report) {
@@ -584,6 +589,8 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
             if (SUMS) {
                 // minus log2 of the row's sum over the unit's pieces; rows that are none: -inf
                 // (four loads in flight: a unit of few, long sequences has many pieces)
+                if (units == 1)
+                    grid_dependency_wait();
                 float M = -INFINITY;
                 const int k0 = w.first / R;
                 const int n = half || !row_valid ? 0 : 2 * ((w.first + w.nt - 1) / R - k0 + 1);
@@ -611,8 +618,22 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
             // pass 2: one row block of the chunk makes the whole mass, the second query tile's
             // threads adding the first one's sums; of several each leaves its sums
             const bool alone = p.row_blocks == 1;
-            float *sums = p.sums + (size_t)(2 * unit + grp) * ((size_t)p.max_blocks * kBlockSize);
-            float *mass = p.mass + ((size_t)w.s * Hkv + w.h) * p.max_blocks * kBlockSize;
+            float *sums = (alone ? p.mass + (size_t)(w.s * Hkv + w.h) * p.max_blocks * kBlockSize
+                                 : p.sums + (size_t)(2 * unit + grp) * p.max_blocks * kBlockSize) + rr;
+            // a key of the second query tile's threads that waits for the first one's sum: it is
+            // there two tiles later, without delay
+            float due_sum = 0.f;
+            auto settle = [&](int i) {
+                const int place = 2 * half + (turn & 1);
+                if (!__all_sync(FULL, mbar_wait_bounded(sum_bar(place), turn >> 1 & 1)))
+                    return false;
+                ++turn;
+                const int k0 = tile(i) * Sh::BN;
+                if (k0 + rr < w.x.L)
+                    sums[k0] = due_sum + part[place * Sh::BN + rr];
+                return true;
+            };
+            const bool settles = SUMS && alone && ng == 2 && grp == 1;
             const int first_pos = w.x.L - w.x.c + t0;     // of the tile's first token
             for (int i = 0; i < w.te - w.tb; ++i, ++it) {
                 const int k0 = tile(i) * Sh::BN;
@@ -622,6 +643,10 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
                     phase = it >> 1;
                     if (buf != half)                      // the other set's
                         continue;
+                    if (settles && i >= 2 && !settle(i - 2)) {
+                        ok = false;
+                        break;
+                    }
                 } else {
                     buf = ng == 2 ? (2 * i + grp) % 3 : i & 1;
                     bar = 2 * grp + (turn & 1);
@@ -637,7 +662,8 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
                     continue;
                 }
                 tc::fence_after_sync();
-                // 64 columns at a time: keys for pass 1, rows for pass 2
+                // columns at a time: keys for pass 1, rows for pass 2 (32: with 64 it spills)
+                constexpr int CW = SUMS ? 32 : 64;
                 const int c0 = SUMS ? 0 : 64 * half;
                 const uint32_t tg = tl + (SUMS ? 256 * buf + 128 * grp : 128 * buf);
                 // rows: keys [0, vis] of the tile are visible; keys: columns [first, 128) see it
@@ -646,24 +672,27 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
                 const bool full = __all_sync(FULL, SUMS ? first <= 0 : vis >= c0 + 63);
                 float sum = 0.f, old = 0.f;
                 if (SUMS && alone && grp == ng - 1 && k0 + rr < w.x.L - w.x.c && p.decay != 0.f)
-                    old = __ldcg(mass + k0 + rr);
+                    old = __ldcg(sums + k0);
 #pragma unroll 1
-                for (int c = c0; c < (SUMS ? 128 : c0 + 64); c += 64) {
-                    uint32_t v[64];
+                for (int c = c0; c < (SUMS ? 128 : c0 + 64); c += CW) {
+                    uint32_t v[CW];
                     __syncwarp();
-                    tc::tmem_ld64(tg + c, v);
-                    if (!SUMS || c == 64) {
+                    if constexpr (SUMS)
+                        tc::tmem_ld32(tg + c, v);
+                    else
+                        tc::tmem_ld64(tg + c, v);
+                    if (!SUMS || c == 128 - CW) {
                         tc::fence_before_sync();
                         mbar_arrive(read_bar(buf));
                     }
                     if (!full) {
 #pragma unroll
-                        for (int e = 0; e < 64; ++e)
+                        for (int e = 0; e < CW; ++e)
                             if (SUMS ? e < first - c : e > vis - c)
                                 v[e] = __float_as_uint(-INFINITY);
                     }
                     float mref = 0.f;
-                    if (!SUMS) {
+                    if constexpr (!SUMS) {
                         float mx[4];
 #pragma unroll
                         for (int a = 0; a < 4; ++a) {
@@ -686,7 +715,7 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
                     const uint64_t nm2 = f2_pack(-mref, -mref);
                     const float4 *ls = reinterpret_cast<const float4 *>(lse + grp * Sh::BM + c);
 #pragma unroll
-                    for (int e = 0; e < 64; e += 4) {
+                    for (int e = 0; e < CW; e += 4) {
                         uint64_t na = nm2, nb = nm2;
                         if (SUMS) {
                             const float4 x = ls[e / 4];
@@ -713,27 +742,27 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
                     l += sum;
                 } else if (!alone) {
                     if (k0 + rr < w.x.L)
-                        sums[k0 + rr] = sum;
+                        sums[k0] = sum;
                 } else {
-                    // Two places in turn: a set two of its tiles on has the other set of this
-                    // buffer past this one.
-                    if (ng == 2) {
-                        const int place = 2 * buf + (turn & 1);
-                        if (grp == 0) {
-                            part[place * Sh::BN + rr] = sum;
-                            mbar_arrive(sum_bar(place));
-                        } else {
-                            if (!__all_sync(FULL, mbar_wait_bounded(sum_bar(place), turn >> 1 & 1))) {
-                                ok = false;
-                                break;
-                            }
-                            sum += part[place * Sh::BN + rr];
-                        }
-                        ++turn;
+                    // Two places in turn: a set that is two of its tiles on has the other set of
+                    // this buffer past the tile between, and so this one settled.
+                    sum = fmaf(old, p.decay, sum);
+                    if (ng == 2 && grp == 0) {
+                        const int place = 2 * half + (turn++ & 1);
+                        part[place * Sh::BN + rr] = sum;
+                        mbar_arrive(sum_bar(place));
+                    } else if (ng == 2) {
+                        due_sum = sum;
+                    } else if (k0 + rr < w.x.L) {
+                        sums[k0] = sum;
                     }
-                    if (grp == ng - 1 && k0 + rr < w.x.L)
-                        mass[k0 + rr] = fmaf(old, p.decay, sum);
                 }
+            }
+            // the set's last tile of the piece, if it has one
+            const int last = w.te - w.tb - 1 - ((it - 1 - half) & 1);
+            if (ok && settles && last >= 0 && !settle(last)) {
+                ok = false;
+                break;
             }
             if (ok && !SUMS)
                 stats[(size_t)blockIdx.x * (2 * ROWS) + half * ROWS] = make_float2(m, l);

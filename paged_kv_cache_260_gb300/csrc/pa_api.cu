@@ -1563,7 +1563,7 @@ int pa_select_blocks(const struct pa_sparse_args *args)
     p.bounds = a.bounds;
     p.block_tables = a.block_tables;
     p.seq_lens = a.seq_lens;
-    p.scores = reinterpret_cast<float *>(ws);
+    p.scores = reinterpret_cast<uint32_t *>(ws);
     p.sizes = reinterpret_cast<float *>(ws + w.size_off);
     p.exact = reinterpret_cast<unsigned long long *>(ws + w.exact_off);
     p.err = ds->err;

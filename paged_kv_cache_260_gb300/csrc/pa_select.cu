@@ -187,6 +187,15 @@ __device__ __forceinline__ float from_ordered(uint32_t k)
     return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
+// A block's score as the selection keeps it: one that is infinite above all others.
+constexpr uint32_t kFirst = 0xffffffffu;
+constexpr uint32_t kIn = kFirst - 1, kOut = 1;    // one that was in doubt
+
+__device__ __forceinline__ uint32_t score_key(float x)
+{
+    return x == INFINITY ? kFirst : ordered(x);
+}
+
 // (s, e) += x without loss of what falls off s
 __device__ __forceinline__ void two_add(float &s, float &e, float x)
 {
@@ -374,7 +383,7 @@ __global__ void __launch_bounds__(kScoreThreads, 4) block_score_kernel_t(const S
                 size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, off));
             const int j = first + 8 * qd + r;
             if (qd < 2 && j < blocks)
-                p.scores[run * p.row + j] = qd ? best[1] : best[0];
+                p.scores[run * p.row + j] = score_key(qd ? best[1] : best[0]);
             if (lane == 0)
                 p.sizes[run * (p.row / 16) + first / 16] = size;
             tile[0] = next[0];
@@ -388,7 +397,7 @@ __global__ void __launch_bounds__(NTH, SCORED ? 1 : 512 / NTH) block_select_kern
 {
     constexpr uint32_t FULL = 0xffffffffu;
     constexpr int NW = NTH / 32;
-    extern __shared__ float near_scores[];
+    extern __shared__ uint32_t near_scores[];
     __shared__ float q[8 * NT * D];               // the group's queries
     __shared__ unsigned long long near_keys[kDoubt];
     __shared__ TallySmem<NW> counts;
@@ -428,18 +437,34 @@ __global__ void __launch_bounds__(NTH, SCORED ? 1 : 512 / NTH) block_select_kern
     int want = p.keep - p.keep_first - p.keep_last;       // how many of them are kept
 
     // ---- the scores ----
-    float *far_scores = p.scores + (size_t)run * p.row;
-    float *score = p.near >= nb ? near_scores : far_scores;
+    uint32_t *far_scores = p.scores + (size_t)run * p.row;
+    uint32_t *score = p.near >= nb ? near_scores : far_scores;
     const T *qg = static_cast<const T *>(p.q) + (size_t)run * G * D;
     float size = 0.f;                             // the largest sum |q||bound|
+    uint32_t least = 0, most = 0;                 // of the finite scores, least upside down
+    int infs = 0;                                 // those that are not rank first
+    auto seen_score = [&](int j, uint32_t k) {
+        if (k != kFirst) {
+            least = max(least, ~k);
+            most = max(most, k);
+        } else {
+            infs += j >= lo && j < hi;
+        }
+    };
     if (SCORED) {
         for (int i = tid; i < (nb + 15) / 16; i += NTH)
             size = fmaxf(size, __ldcg(p.sizes + (size_t)run * (p.row / 16) + i));
-        if (p.near >= nb) {
-            const float4 *src = reinterpret_cast<const float4 *>(far_scores);
-#pragma unroll 4
-            for (int i = tid; i < (nb + 3) / 4; i += NTH)
-                reinterpret_cast<float4 *>(near_scores)[i] = __ldcg(src + i);
+        const uint4 *src = reinterpret_cast<const uint4 *>(far_scores);
+#pragma unroll 2
+        for (int i = tid; i < (nb + 3) / 4; i += NTH) {
+            const uint4 x = __ldcg(src + i);
+            const uint32_t k[4] = {x.x, x.y, x.z, x.w};
+            if (p.near >= nb)
+                reinterpret_cast<uint4 *>(near_scores)[i] = x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (4 * i + e < nb)
+                    seen_score(4 * i + e, k[e]);
         }
     } else {
         const int r = lane >> 2, qd = lane & 3;
@@ -460,8 +485,11 @@ __global__ void __launch_bounds__(NTH, SCORED ? 1 : 512 / NTH) block_select_kern
                     rows(b + 16 * NW, next);
             });
             const int j = b + 8 * qd + r;
-            if (qd < 2 && j < nb)
-                score[j] = qd ? best[1] : best[0];
+            if (qd < 2 && j < nb) {
+                const uint32_t k = score_key(qd ? best[1] : best[0]);
+                score[j] = k;
+                seen_score(j, k);
+            }
             tile[0] = next[0];
             tile[1] = next[1];
         }
@@ -475,51 +503,49 @@ __global__ void __launch_bounds__(NTH, SCORED ? 1 : 512 / NTH) block_select_kern
     // a warp's contiguous part of the blocks that compete: [w0, ..) in `steps` steps of 32
     const int c1 = hi, steps = (c1 - lo + NTH - 1) / NTH;
     const int w0 = lo + warp * steps * 32;
-    auto each = [&](auto &&f) {                   // f(block, score), -inf past the end
+    auto each = [&](auto &&f) {                   // f(block, score), 0 past the end
 #pragma unroll 4
         for (int i = 0; i < steps; ++i) {
             const int j = w0 + 32 * i + lane;
-            f(j, j < c1 ? score[j] : -INFINITY);
+            f(j, j < c1 ? score[j] : 0u);
         }
     };
-    uint32_t least = 0, most = 0;                 // of the finite scores, least upside down
-    int infs = 0;                                 // those that are not rank first
-    each([&](int j, float x) {
-        if (j < c1 && x != INFINITY) {
-            least = max(least, ~ordered(x));
-            most = max(most, ordered(x));
-        }
-        infs += x == INFINITY;
-    });
-    int all_infs, inf_before;
+    int all_infs, none;
     const uint3 range = tally.most(__reduce_add_sync(FULL, infs), least, most,
-                                   __float_as_uint(size), all_infs, inf_before);
-    int inf_left = min(all_infs, want);           // so many of them, the foremost
+                                   __float_as_uint(size), all_infs, none);
+    const int inf_left = min(all_infs, want);     // so many of them, the foremost
     want -= inf_left;
+    int4 all, before;
+    int inf_before = 0;                           // in the warps before this one
+    if (all_infs > 0) {
+        infs = 0;
+        each([&](int, uint32_t k) { infs += k == kFirst; });
+        tally.sums(__reduce_add_sync(FULL, infs), 0, 0, all, before);
+        inf_before = before.x;
+    }
     // Largest error: 2 D / 16 steps each add 17 terms aligned to the largest, none above
     // sum |q||bound|, and lose 2^-23 of it a term (sums that are infinite put everything in
     // doubt)
     const float twice = 2.f * (2 * D / 16) * 17 * 1.1920929e-7f * __uint_as_float(range.z);
     const float slack = twice <= FLT_MAX ? twice : FLT_MAX;
-    int4 all, before;
     int ins = 0, ins_before = -1;                 // kept by this warp; by those before it, if known
 
     // ---- a score that just `want` reach, or else the want-th largest itself ----
-    float edge = INFINITY;                        // nothing lies above: none is kept
+    uint32_t sure_above = kFirst - 1, doubt_from = kFirst - 1;   // none is kept
     if (want > 0) {
         int above, reach;
-        edge = from_ordered(tally.threshold(
+        const float edge = from_ordered(tally.threshold(
             radix,
-            [&](auto &&f) {
-                each([&](int j, float x) { f(ordered(x), j < c1 && x != INFINITY); });
-            },
-            want, ~range.x, range.y, above, reach));
+            [&](auto &&f) { each([&](int, uint32_t k) { f(k, k != 0 && k != kFirst); }); }, want,
+            ~range.x, range.y, above, reach));
         // ---- in, out, or in doubt ----
-        auto doubtful = [&](float x) { return x != INFINITY && x - slack <= edge && x + slack >= edge; };
+        sure_above = ordered(__fadd_ru(edge, slack));
+        doubt_from = ordered(__fadd_rd(edge, -slack));
+        auto doubtful = [&](uint32_t k) { return k >= doubt_from && k <= sure_above; };
         int sure = 0, doubts = 0;
-        each([&](int j, float x) {
-            sure += j < c1 && x != INFINITY && x - slack > edge;
-            doubts += j < c1 && doubtful(x);
+        each([&](int, uint32_t k) {
+            sure += k > sure_above && k != kFirst;
+            doubts += doubtful(k);
         });
         sure = __reduce_add_sync(FULL, sure);
         doubts = __reduce_add_sync(FULL, doubts);
@@ -528,9 +554,9 @@ __global__ void __launch_bounds__(NTH, SCORED ? 1 : 512 / NTH) block_select_kern
         if (need == 0 || need == total) {
             // none or all of them: no sums wanted
             ins_before = before.x + (need ? before.y : 0);
-            each([&](int j, float x) {
-                if (need && j < c1 && doubtful(x))
-                    score[j] = FLT_MAX;
+            each([&](int j, uint32_t k) {
+                if (need && doubtful(k))
+                    score[j] = kIn;
             });
         } else {
             // the score of block j by the warp, as an ordered number of 64 bits
@@ -569,8 +595,8 @@ __global__ void __launch_bounds__(NTH, SCORED ? 1 : 512 / NTH) block_select_kern
             unsigned long long *list =
                 total <= kDoubt ? near_keys : p.exact + (size_t)run * p.row;
             int at = mine;
-            each([&](int j, float x) {
-                unsigned m = __ballot_sync(FULL, j < c1 && doubtful(x));
+            each([&](int j, uint32_t x) {
+                unsigned m = __ballot_sync(FULL, doubtful(x));
                 for (; m; m &= m - 1) {
                     const int l = __ffs(m) - 1;
                     const unsigned long long k = resum(j - lane + l);
@@ -584,9 +610,9 @@ __global__ void __launch_bounds__(NTH, SCORED ? 1 : 512 / NTH) block_select_kern
             if (total <= kDoubt) {
                 // rank each among all
                 at = mine;
-                each([&](int j, float x) {
-                    unsigned m = __ballot_sync(FULL, j < c1 && doubtful(x));
-                    float mark = x;
+                each([&](int j, uint32_t x) {
+                    unsigned m = __ballot_sync(FULL, doubtful(x));
+                    uint32_t mark = x;
                     for (; m; m &= m - 1, ++at) {
                         const unsigned long long k = list[at];
                         int better = 0;
@@ -594,9 +620,9 @@ __global__ void __launch_bounds__(NTH, SCORED ? 1 : 512 / NTH) block_select_kern
                             better += list[o] > k || (list[o] == k && o < at);
                         better = __reduce_add_sync(FULL, better);
                         if (lane == __ffs(m) - 1)
-                            mark = better < need ? FLT_MAX : -FLT_MAX;
+                            mark = better < need ? kIn : kOut;
                     }
-                    if (j < c1)
+                    if (mark != x)
                         score[j] = mark;
                 });
             } else {
@@ -620,14 +646,13 @@ __global__ void __launch_bounds__(NTH, SCORED ? 1 : 512 / NTH) block_select_kern
                 tally.sums(above, count(t64) - above, 0, all, before);
                 int quota = need - all.x - before.y;
                 at = mine;
-                each([&](int j, float x) {
-                    const bool on = j < c1 && doubtful(x);
+                each([&](int j, uint32_t x) {
+                    const bool on = doubtful(x);
                     const unsigned m = __ballot_sync(FULL, on), below = (1u << lane) - 1;
                     const unsigned long long k = on ? list[at + __popc(m & below)] : 0;
                     const unsigned tie = __ballot_sync(FULL, on && k == t64);
                     if (on)
-                        score[j] = k > t64 || (k == t64 && __popc(tie & below) < quota) ? FLT_MAX
-                                                                                       : -FLT_MAX;
+                        score[j] = k > t64 || (k == t64 && __popc(tie & below) < quota) ? kIn : kOut;
                     quota -= __popc(tie);
                     at += __popc(m);
                 });
@@ -638,10 +663,12 @@ __global__ void __launch_bounds__(NTH, SCORED ? 1 : 512 / NTH) block_select_kern
 
     // ---- the kept blocks in their order ----
     int seen = inf_before;
-    auto kept = [&](int j, float x) {             // asked in ascending order
-        const unsigned inf = __ballot_sync(FULL, x == INFINITY);
-        const bool in = x == INFINITY ? seen + __popc(inf & ((1u << lane) - 1)) < inf_left
-                                      : j < c1 && (x == FLT_MAX || (x != -FLT_MAX && x - slack > edge));
+    auto kept = [&](uint32_t k) {                 // asked in ascending order
+        if (all_infs == 0)
+            return k > sure_above;
+        const unsigned inf = __ballot_sync(FULL, k == kFirst);
+        const bool in = k == kFirst ? seen + __popc(inf & ((1u << lane) - 1)) < inf_left
+                                    : k > sure_above;
         seen += __popc(inf);
         return in;
     };
@@ -650,14 +677,14 @@ __global__ void __launch_bounds__(NTH, SCORED ? 1 : 512 / NTH) block_select_kern
     if (ins_before >= 0) {
         ins_before += min(inf_before, inf_left);
     } else {
-        each([&](int j, float x) { ins += __popc(__ballot_sync(FULL, kept(j, x))); });
-        tally.sums(ins, 0, 0, all, before);
+        each([&](int, uint32_t k) { ins += kept(k); });
+        tally.sums(__reduce_add_sync(FULL, ins), 0, 0, all, before);
         ins_before = before.x;
     }
     int at = lo + ins_before;
     seen = inf_before;
-    each([&](int j, float x) {
-        const bool in = kept(j, x);
+    each([&](int j, uint32_t k) {
+        const bool in = kept(k);
         const unsigned m = __ballot_sync(FULL, in);
         if (in)
             out[at + __popc(m & ((1u << lane) - 1))] = tile_of(j);

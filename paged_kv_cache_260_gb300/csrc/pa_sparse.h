@@ -26,8 +26,9 @@ struct SelectParams {
     const void *bounds;
     const int32_t *block_tables;
     const int32_t *seq_lens;
-    float *scores;                 // workspace: [num_seqs][num_kv_heads][row] fp32 scores, if
-                                   //   they are computed apart or do not fit shared memory,
+    uint32_t *scores;              // workspace: [num_seqs][num_kv_heads][row] fp32 scores as
+                                   //   ordered numbers, if they are computed apart or do not
+                                   //   fit shared memory,
     float *sizes;                  //   [..][row / 16] with those the largest sum |q||bound|,
     unsigned long long *exact;     //   [..][row] scores with more bits, of those in doubt
     uint32_t *err;

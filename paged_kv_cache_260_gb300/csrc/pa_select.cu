@@ -170,8 +170,6 @@ __global__ void __launch_bounds__(kBoundsThreads) block_bounds_kernel(const Boun
 // kernel whose warps share out all of them evenly, and read from the workspace
 // (SCORED).
 // ---------------------------------------------------------------------------
-// A block a run from this many runs an SM on, else the scores apart.
-constexpr int kSelectRuns = 2;
 constexpr int kDoubt = 256;                       // blocks in doubt that are ranked directly
 constexpr int kSelectNear = 16384;                // scores a block holds (64 KB)
 
@@ -751,7 +749,10 @@ SelectLaunch select_launch(bool bf16, int head_dim, int group, int num_runs, int
 {
     SelectLaunch e{};
     const bool small = max_blocks <= 256;
-    const bool apart = !small && max_blocks > keep && num_runs < kSelectRuns * num_sms;
+    // A thread block a run, or, with few runs, the scores apart: bf16, 32/8 heads x 128, lengths
+    // to 16K, us of the one and of the other: 128 runs 17.4 / 14.7, 256 runs 20.2 / 22.6, 512
+    // runs 38.5 / 48.7; 32 runs of 32K to 131K tokens 98 / 24.3.
+    const bool apart = !small && max_blocks > keep && 2LL * num_runs < 3LL * num_sms;
     e.threads = small ? 128 : apart ? 1024 : 256;
     e.fn = select_fn(bf16, head_dim, group, small ? kSmall : apart ? kGiven : kLarge);
     if (apart) {

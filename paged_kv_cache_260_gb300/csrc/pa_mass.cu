@@ -587,30 +587,41 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
             float2 *stats = p.stats + (size_t)unit * (2 * ROWS) + grp * Sh::BM + rr;
             float m = -INFINITY, l = 0.f;
             if (SUMS) {
-                // minus log2 of the row's sum over the unit's pieces; rows that are none: -inf
-                // (four loads in flight: a unit of few, long sequences has many pieces)
+                // minus log2 of the row's sum over the unit's pieces; rows that are none: -inf.  A
+                // unit of few, long sequences has many pieces: each set folds those of one half
+                // of the key tiles, eight loads in flight.
                 if (units == 1)
                     grid_dependency_wait();
                 float M = -INFINITY;
                 const int k0 = w.first / R;
-                const int n = half || !row_valid ? 0 : 2 * ((w.first + w.nt - 1) / R - k0 + 1);
-                for (int j = 0; j < n; j += 4) {
-                    float2 a[4];
+                const int n = row_valid ? (w.first + w.nt - 1) / R - k0 + 1 : 0;
+                const float2 *from = stats + (size_t)(2 * k0 + half) * ROWS;
+                for (int j = 0; j < n; j += 8) {
+                    float2 a[8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        a[i] = j + i < n ? __ldcg(stats + (size_t)(2 * k0 + j + i) * ROWS)
+                    for (int i = 0; i < 8; ++i)
+                        a[i] = j + i < n ? __ldcg(from + (size_t)(j + i) * (2 * ROWS))
                                          : make_float2(-INFINITY, 0.f);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 8; ++i) {
                         const float nM = fmaxf(M, a[i].x);
                         if (nM > -INFINITY)
                             l = l * exp2f(M - nM) + a[i].y * exp2f(a[i].x - nM);
                         M = nM;
                     }
                 }
+                const float mine = l > 0.f ? M + log2f(l) : -INFINITY;
+                float *at = lse + grp * Sh::BM + rr;
                 ok = meet();                              // all are done with the piece before
-                if (!half)
-                    lse[grp * Sh::BM + rr] = row_valid ? -(M + log2f(l)) : -INFINITY;
+                if (half)
+                    *at = mine;
+                ok = ok && meet();
+                if (!half && row_valid) {
+                    const float other = *at, top = fmaxf(mine, other);
+                    *at = -(top + log2f(exp2f(mine - top) + exp2f(other - top)));
+                } else if (!half) {
+                    *at = -INFINITY;
+                }
                 ok = ok && meet();
                 if (!ok)
                     break;

@@ -57,44 +57,45 @@ decode_mass_finish_kernel(const DecodeMassParams p)
             const int s = begin + i, h = at / nt, t0 = at % nt * TOK + lane;
             const int L = min(max(__ldg(p.seq_lens + s), 0), T);
             const size_t run = (size_t)s * Hkv + h;
-            const float *x = p.scores + (run * T + t0) * cols;
+            const float2 *x = reinterpret_cast<const float2 *>(p.scores + (run * T + t0) * cols);
             const float2 *stat = p.stat + (size_t)s * p.num_heads + h * G;
             float *mass = p.mass + run * T + t0;
             // every load of four heads in flight at once, and the old masses with the first
+            // (the newest token has none from before)
+            const int step = 16 * cols;           // 32 tokens, in pairs of scores
             float old[4], sum[4];
+            bool on[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int t = t0 + 32 * k;
-                old[k] = t < L - 1 && p.decay != 0.f ? __ldcg(mass + 32 * k) : 0.f;
+                on[k] = t0 + 32 * k < L;
+                old[k] = t0 + 32 * k < L - 1 && p.decay != 0.f ? __ldcg(mass + 32 * k) : 0.f;
                 sum[k] = 0.f;
             }
-            for (int g = 0; g < G; g += 4) {
+            for (int g = 0; g < cols; g += 4) {
+                // heads past the group: a reciprocal of 0
                 float2 st[4], y[4][2];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     st[i] = g + i < G ? __ldcg(stat + g + i) : make_float2(0.f, 0.f);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (t0 + 32 * k < L && g + 2 * i < G)
-                            y[k][i] = __ldcg(reinterpret_cast<const float2 *>(
-                                x + (size_t)32 * k * cols + g + 2 * i));
+                    for (int k = 0; k < 4; ++k)
+                        y[k][i] = on[k] && g + 2 * i < cols ? __ldcg(x + k * step + g / 2 + i)
+                                                            : make_float2(0.f, 0.f);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                for (int i = 0; i < 2; ++i) {
+                    // (the odd group's last score of a pair is that of a query of zeros: finite)
+                    const float2 a = st[2 * i], b = st[2 * i + 1];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (t0 + 32 * k < L && g + 2 * i < G) {
-                            sum[k] = fmaf(exp2f(y[k][i].x - st[2 * i].x), st[2 * i].y, sum[k]);
-                            if (g + 2 * i + 1 < G)
-                                sum[k] = fmaf(exp2f(y[k][i].y - st[2 * i + 1].x), st[2 * i + 1].y,
-                                              sum[k]);
-                        }
+                    for (int k = 0; k < 4; ++k)
+                        sum[k] = fmaf(ex2_approx(y[k][i].x - a.x), a.y,
+                                      fmaf(ex2_approx(y[k][i].y - b.x), b.y, sum[k]));
+                }
             }
-            // (the newest token has no mass from before: old is 0)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                if (t0 + 32 * k < L)
+                if (on[k])
                     mass[32 * k] = fmaf(old[k], p.decay, sum[k]);
         }
     }

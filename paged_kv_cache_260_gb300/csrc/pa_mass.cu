@@ -789,6 +789,10 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, 512);
     }
+    // Pass 2 does not end before pass 1, also where no block of it had anything to wait for:
+    // what comes next waits for pass 2 alone.
+    if (SUMS)
+        grid_dependency_wait();
 }
 
 // ---------------------------------------------------------------------------

@@ -323,6 +323,19 @@ def test_sparse_decode_names_a_tile_twice(pa):
     su.close(out, ref, tol)
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.11])
+def test_sparse_decode_with_any_scale(pa, scale):
+    r = gen(51)
+    k, v = (su.pool(r, 90, 2, 128, torch.bfloat16) for _ in range(2))
+    held = torch.tensor([[800, 1], [0, 77]], dtype=torch.int32)
+    tiles = random_tiles(r, 2, 2, 50, 90, held)
+    q = torch.randn(2, 6, 128, generator=r).bfloat16()
+    ref, tol = su.sparse_decode(q, k, v, tiles, held, scale)
+    out = pa.sparse_decode(torch.empty_like(q).cuda(), *cuda(q, k, v, tiles, held), scale)
+    check(pa)
+    su.close(out, ref, tol)
+
+
 def test_sparse_decode_reports_bad_arguments(pa):
     r = gen(15)
     k, v = (su.pool(r, 4, 2, 64, torch.float16) for _ in range(2))
@@ -341,7 +354,8 @@ def test_sparse_decode_reports_bad_arguments(pa):
 # ---------------------------------------------------------------------------
 # decode_mass
 # ---------------------------------------------------------------------------
-def mass_case(pa, r, lens, dt, d, hkv, g, decay, mb=None, q_gain=2.0):
+def mass_case(pa, r, lens, dt, d, hkv, g, decay, mb=None, q_gain=2.0, scale=None):
+    scale = SCALE[d] if scale is None else scale
     tables, nb = su.tables_for(r, lens, mb)
     k, v = (su.pool(r, nb, hkv, d, DT[dt], su.dead_slots(tables, lens, nb)) for _ in range(2))
     n = len(lens)
@@ -354,10 +368,10 @@ def mass_case(pa, r, lens, dt, d, hkv, g, decay, mb=None, q_gain=2.0):
         elif m:
             mass[i, :, m - 1] = math.nan
         mass[i, :, m:] = math.nan
-    ref = su.decode_mass(q, mass, k, v, tables, lens, SCALE[d], decay)
+    ref = su.decode_mass(q, mass, k, v, tables, lens, scale, decay)
     out = torch.full_like(q, math.nan).cuda()
     qq, mm, kk, vv, tt, ll = cuda(q, mass, k, v, tables, lens)
-    got = pa.decode_mass(out, mm, qq, kk, vv, tt, ll, SCALE[d], decay=decay)
+    got = pa.decode_mass(out, mm, qq, kk, vv, tt, ll, scale, decay=decay)
     assert got[0] is out and got[1] is mm
     check(pa)
     su.close(out, ref[0], ref[1], "out")
@@ -367,7 +381,7 @@ def mass_case(pa, r, lens, dt, d, hkv, g, decay, mb=None, q_gain=2.0):
         if m:
             assert bool(torch.isfinite(mm[i, :, :m]).all())
     plain = torch.empty_like(out)
-    pa.decode(plain, qq, kk, vv, tt, ll, SCALE[d])
+    pa.decode(plain, qq, kk, vv, tt, ll, scale)
     assert torch.equal(su.bits(plain), su.bits(out))
 
 
@@ -396,6 +410,11 @@ def test_decode_mass_of_far_apart_scores(pa):
     mass_case(pa, gen(19), [700, 33, 1], "bf16", 128, 2, 4, 1.0, q_gain=30.0)
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.11])
+def test_decode_mass_with_any_scale(pa, scale):
+    mass_case(pa, gen(50), [700, 0, 33, 1, 6000], "bf16", 128, 2, 4, 0.5, scale=scale)
+
+
 def test_decode_mass_of_shared_blocks(pa):
     r = gen(20)
     lens = [40, 40, 35]
@@ -413,14 +432,14 @@ def test_decode_mass_of_shared_blocks(pa):
 # ---------------------------------------------------------------------------
 # prefill_mass
 # ---------------------------------------------------------------------------
-def chunk_case(pa, r, lens, chunks, dt, d, hkv, g, decay, mb=None, longest=None):
+def chunk_case(pa, r, lens, chunks, dt, d, hkv, g, decay, mb=None, longest=None, lead=0):
     tables, nb = su.tables_for(r, lens, mb)
     k = su.pool(r, nb, hkv, d, DT[dt], su.dead_slots(tables, lens, nb))
-    start = [0]
+    start = [lead]
     for c in chunks:
         start.append(start[-1] + c)
     q = torch.randn(start[-1] + 2, hkv * g, d, generator=r).to(DT[dt])
-    q[start[-1]:] = math.nan                           # rows that are no sequence's
+    q[:lead] = q[start[-1]:] = math.nan                # rows that are no sequence's
     mass = torch.rand(len(lens), hkv, 16 * tables.shape[1], generator=r) * 5
     for i, (m, c) in enumerate(zip(lens, chunks)):
         mass[i, :, m - c:] = math.nan
@@ -478,6 +497,63 @@ def test_prefill_mass_of_many_units(pa, g, d, count):
     chunks = [min(n, int(x)) for n, x in zip(lens, torch.randint(0, 300, (count,), generator=r))]
     lens[3], chunks[3] = 900, 1
     chunk_case(pa, r, lens, chunks, "bf16", d, 2, g, 1.0)
+
+
+def test_prefill_mass_of_many_sequences(pa):
+    r = gen(52)
+    for count, longest in ((700, 20), (2200, 150)):    # one row block, three
+        lens = [int(x) for x in torch.randint(0, 60, (count,), generator=r)]
+        chunks = [min(n, int(x)) for n, x in zip(lens, torch.randint(0, 20, (count,), generator=r))]
+        lens[count - 2], chunks[count - 2] = 620, 20
+        chunk_case(pa, r, lens, chunks, "f16", 64, 1, 4, 0.5, longest=longest, lead=3)
+
+
+def test_prefill_mass_without_rows(pa):
+    # a batch in which no sequence has any, then one that does, in every form
+    r = gen(53)
+    for mb, longest in ((60, 30), (60, 200), (8, 5)):
+        lens = [16 * mb, 40, 0]
+        tables, nb = su.tables_for(r, lens, mb)
+        k = su.pool(r, nb, 2, 64, torch.float16)
+        q = torch.randn(11, 4, 64, generator=r).half()
+        old = torch.rand(3, 2, 16 * mb, generator=r)
+        kk, qq, tt, ll, none, some = cuda(k, q, tables, lens, [4, 4, 4, 4], [1, 5, 11, 11])
+        ref, tol = su.prefill_mass(q, old, k, tables, lens, [1, 5, 11, 11], 0.125, 1.0)
+        for _ in range(10):
+            mm = old.cuda()
+            pa.prefill_mass(mm, qq, kk, tt, ll, none, longest, 0.125)
+            kept = mm.clone()
+            pa.prefill_mass(mm, qq, kk, tt, ll, none, longest, 0.125, decay=0.0)
+            pa.prefill_mass(mm, qq, kk, tt, ll, some, longest if longest > 5 else 6, 0.125)
+            assert torch.equal(kept.cpu(), old)
+            su.mass_close(mm, ref, tol)
+        check(pa)
+
+
+def test_a_block_named_twice(pa):
+    # by a table, in every call that reads
+    r = gen(54)
+    lens, hkv, d = [200, 90], 2, 64
+    tables = torch.tensor([[3, 1, 3, 0, 2, 1, 3, 3, 4, 5, 0, 0, 2], [5, 5, 5, 5, 5, 1, 0, 0, 0, 0, 0,
+                                                                   0, 0]], dtype=torch.int32)
+    k, v = (su.pool(r, 6, hkv, d, torch.float16) for _ in range(2))
+    q = torch.randn(2, 8, d, generator=r).half()
+    mass = torch.rand(2, hkv, 208, generator=r)
+    full = [208, 96]                                   # a block's bounds are of one length
+    bnd = su.bounds(torch.zeros(6, hkv, 2, d, dtype=torch.float16), k, tables, full)
+    got = pa.block_bounds(torch.zeros_like(bnd).cuda(), *cuda(k, tables, full))
+    assert torch.equal(su.bits(got), su.bits(bnd))
+    same_choice(pa, q, bnd, tables, lens, 5, 1, 1)
+    ref = su.decode_mass(q, mass, k, v, tables, lens, 0.125, 1.0)
+    out, m = pa.decode_mass(torch.empty_like(q).cuda(), *cuda(mass, q, k, v, tables, lens), 0.125)
+    su.close(out, *ref[:2])
+    su.mass_close(m, *ref[2:])
+    for longest in (1, 300):                           # both forms
+        ref, tol = su.prefill_mass(q, mass, k, tables, lens, [0, 1, 2], 0.125, 1.0)
+        m = cuda(mass)[0]
+        pa.prefill_mass(m, *cuda(q, k, tables, lens, [0, 1, 2]), longest, 0.125)
+        su.mass_close(m, ref, tol)
+    check(pa)
 
 
 def test_prefill_mass_again_and_again(pa):

@@ -541,8 +541,8 @@ int pa_block_bounds(const struct pa_sparse_args *args);
  * first, the keep_last last, and of the rest those with the largest scores, ties to
  * the lowest position; all of them if n <= keep.  The choice is that of exact sums
  * (blocks whose 32-bit scores are too close to tell apart are summed again with
- * 46 bits).  Blocks whose score is not finite (an infinity or NaN among the bounds
- * or queries) rank first.
+ * 46 bits; products below 2^-100 may count as zero).  Blocks whose score is not
+ * finite (an infinity or NaN among the bounds or queries) rank first.
  *
  *   tiles     [num_seqs][num_kv_heads][keep] int32, written: the kept blocks in the
  *             order of their positions, as pool tiles block * num_kv_heads + h;
@@ -596,7 +596,8 @@ int pa_decode_mass(const struct pa_sparse_args *args);
  * row at position p sees t <= p).  The chunk's own tokens have no weight from before.
  * Chunk after chunk it accumulates a prompt's weights; on a prompt's last rows alone
  * (q and query_start of those, decay 0) it says which tokens the end of the prompt
- * looks at.  Sequences without rows are left as they were.
+ * looks at.  Sequences without rows are left as they were.  Keys of live tokens must
+ * be finite.
  *   mass, q [num_queries][num_heads][head_dim], k_cache, block_tables, seq_lens,
  *   query_start [num_seqs + 1] int32, max_query_len, max_blocks_per_seq, scale > 0,
  *   decay; groups of 1..128

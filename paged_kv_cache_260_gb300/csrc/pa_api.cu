@@ -1693,7 +1693,6 @@ int pa_decode_mass(const struct pa_sparse_args *args)
     p.scores = x.scores;
     p.stat = x.stat;
     p.seq_lens = a.seq_lens;
-    p.err = ds->err;
     p.num_seqs = a.num_seqs;
     p.num_heads = a.num_heads;
     p.num_kv_heads = a.num_kv_heads;
@@ -1772,7 +1771,7 @@ int pa_prefill_mass(const struct pa_sparse_args *args)
     if (!prefill_mass_plan(a.num_seqs, a.max_query_len, a.num_heads, a.num_kv_heads,
                            a.max_blocks_per_seq, ds->num_sms, &w))
         return PA_ERR_INVALID_ARG;
-    if (w.tiles >= (1LL << 31))          // the list of key tiles is counted in 32 bits
+    if (w.tiles >= (1LL << 30))          // the list of key tiles is counted in 32 bits
         return PA_ERR_UNSUPPORTED;
     if (!a.workspace || a.workspace_bytes < w.total || !aligned(a.workspace, 256))
         return PA_ERR_WORKSPACE;

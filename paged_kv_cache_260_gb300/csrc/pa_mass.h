@@ -14,7 +14,6 @@ struct DecodeMassParams {
     const float *scores;           // [num_seqs * num_kv_heads][max_blocks * 16][score_cols]
     const float2 *stat;            // [num_seqs][num_heads] maximum (base 2), 1 / sum
     const int32_t *seq_lens;
-    uint32_t *err;
     int num_seqs, num_heads, num_kv_heads, max_blocks;
     float decay;
 };

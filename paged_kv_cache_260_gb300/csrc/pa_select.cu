@@ -311,82 +311,80 @@ __global__ void __launch_bounds__(kScoreThreads, 4) block_score_kernel_t(const S
     const int r = lane >> 2, qd = lane & 3;
     grid_dependents_launch();
     grid_dependency_wait();
-    for (int begin = 0; begin < p.num_seqs; begin += kRaggedSeqs) {
-        const int n = min(kRaggedSeqs, p.num_seqs - begin);
-        ragged_prefix<kScoreThreads>(sm, begin, n, [&](int s) {
-            const int L = min(max(__ldg(p.seq_lens + s), 0), p.max_blocks * kBlockSize);
-            const int nb = (L + kBlockSize - 1) / kBlockSize;
-            return nb <= p.keep ? 0 : (nb + 15) / 16;
-        });
-        const long long total = (long long)sm.pre[n] * Hkv;
-        const long long share = (total + warps - 1) / warps;
-        long long u = me * share;
-        const long long end = min(total, u + share);
-        if (u >= end)
-            continue;
-        int i = ragged_find(sm, n, (int)(u / Hkv));
-        int nt = sm.pre[i + 1] - sm.pre[i];
-        int h = (int)((u - (long long)sm.pre[i] * Hkv) / nt);
-        int t = (int)((u - (long long)sm.pre[i] * Hkv) % nt);
-        int nb = 0;
-        // rows r and r + 8 of 16 blocks; past the end the last block again
-        auto tiles_of = [&](int (&tile)[2]) {
+    const int n = p.num_seqs;                     // (few: see select_launch)
+    ragged_prefix<kScoreThreads>(sm, 0, n, [&](int s) {
+        const int L = min(max(__ldg(p.seq_lens + s), 0), p.max_blocks * kBlockSize);
+        const int nb = (L + kBlockSize - 1) / kBlockSize;
+        return nb <= p.keep ? 0 : (nb + 15) / 16;
+    });
+    const long long total = (long long)sm.pre[n] * Hkv;
+    const long long share = (total + warps - 1) / warps;
+    long long u = me * share;
+    const long long end = min(total, u + share);
+    if (u >= end)
+        return;
+    int i = ragged_find(sm, n, (int)(u / Hkv));
+    int nt = sm.pre[i + 1] - sm.pre[i];
+    int h = (int)((u - (long long)sm.pre[i] * Hkv) / nt);
+    int t = (int)((u - (long long)sm.pre[i] * Hkv) % nt);
+    int nb = 0;
+    // rows r and r + 8 of 16 blocks; past the end the last block again
+    auto tiles_of = [&](int (&tile)[2]) {
 #pragma unroll
-            for (int a = 0; a < 2; ++a) {
-                int phys = __ldg(p.block_tables + (size_t)(begin + i) * p.max_blocks +
-                                 min(16 * t + 8 * a + r, nb - 1));
-                if ((unsigned)phys >= (unsigned)p.num_blocks) {
-                    record_error(p.err, PA_DEVERR_TABLE_RANGE);
-                    phys = 0;
-                }
-                tile[a] = phys * Hkv + h;
+        for (int a = 0; a < 2; ++a) {
+            int phys = __ldg(p.block_tables + (size_t)i * p.max_blocks +
+                             min(16 * t + 8 * a + r, nb - 1));
+            if ((unsigned)phys >= (unsigned)p.num_blocks) {
+                record_error(p.err, PA_DEVERR_TABLE_RANGE);
+                phys = 0;
             }
-        };
-        auto enter = [&]() {
-            const int L = min(max(__ldg(p.seq_lens + begin + i), 0), p.max_blocks * kBlockSize);
-            nb = (L + kBlockSize - 1) / kBlockSize;
-        };
-        enter();
-        ScoreQueries<T, D, NT> q;
-        bool fresh = true;
-        int tile[2], next[2] = {0, 0};
-        tiles_of(tile);
-        for (; u < end; ++u) {
-            const size_t run = (size_t)(begin + i) * Hkv + h;
-            const int first = 16 * t, blocks = nb;
-            if (fresh)
-                q.load(static_cast<const T *>(p.q) + run * G * D, G, r, qd);
-            fresh = false;
-            float best[2], size = 0.f;
-            score_tile<T, D, NT>(q, p.bounds, tile, G, qd, best, size, [&]() {
-                if (++t == nt) {
-                    t = 0;
-                    fresh = true;
-                    if (++h == Hkv) {
-                        h = 0;
-                        do
-                            ++i;
-                        while (i < n && sm.pre[i + 1] == sm.pre[i]);
-                        if (i < n) {
-                            nt = sm.pre[i + 1] - sm.pre[i];
-                            enter();
-                        }
+            tile[a] = phys * Hkv + h;
+        }
+    };
+    auto enter = [&]() {
+        const int L = min(max(__ldg(p.seq_lens + i), 0), p.max_blocks * kBlockSize);
+        nb = (L + kBlockSize - 1) / kBlockSize;
+    };
+    enter();
+    ScoreQueries<T, D, NT> q;
+    bool fresh = true;
+    int tile[2], next[2] = {0, 0};
+    tiles_of(tile);
+    for (; u < end; ++u) {
+        const size_t run = (size_t)i * Hkv + h;
+        const int first = 16 * t, blocks = nb;
+        if (fresh)
+            q.load(static_cast<const T *>(p.q) + run * G * D, G, r, qd);
+        fresh = false;
+        float best[2], size = 0.f;
+        score_tile<T, D, NT>(q, p.bounds, tile, G, qd, best, size, [&]() {
+            if (++t == nt) {
+                t = 0;
+                fresh = true;
+                if (++h == Hkv) {
+                    h = 0;
+                    do
+                        ++i;
+                    while (i < n && sm.pre[i + 1] == sm.pre[i]);
+                    if (i < n) {
+                        nt = sm.pre[i + 1] - sm.pre[i];
+                        enter();
                     }
                 }
-                if (u + 1 < end)
-                    tiles_of(next);
-            });
+            }
+            if (u + 1 < end)
+                tiles_of(next);
+        });
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1)
-                size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, off));
-            const int j = first + 8 * qd + r;
-            if (qd < 2 && j < blocks)
-                p.scores[run * p.row + j] = score_key(qd ? best[1] : best[0]);
-            if (lane == 0)
-                p.sizes[run * (p.row / 16) + first / 16] = size;
-            tile[0] = next[0];
-            tile[1] = next[1];
-        }
+        for (int off = 1; off < 32; off <<= 1)
+            size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, off));
+        const int j = first + 8 * qd + r;
+        if (qd < 2 && j < blocks)
+            p.scores[run * p.row + j] = score_key(qd ? best[1] : best[0]);
+        if (lane == 0)
+            p.sizes[run * (p.row / 16) + first / 16] = size;
+        tile[0] = next[0];
+        tile[1] = next[1];
     }
 }
 
@@ -752,7 +750,8 @@ SelectLaunch select_launch(bool bf16, int head_dim, int group, int num_runs, int
     // A thread block a run, or, with few runs, the scores apart: bf16, 32/8 heads x 128, lengths
     // to 16K, us of the one and of the other: 128 runs 17.4 / 14.7, 256 runs 20.2 / 22.6, 512
     // runs 38.5 / 48.7; 32 runs of 32K to 131K tokens 98 / 24.3.
-    const bool apart = !small && max_blocks > keep && 2LL * num_runs < 3LL * num_sms;
+    const bool apart = !small && max_blocks > keep && 2LL * num_runs < 3LL * num_sms &&
+                       num_runs <= kRaggedSeqs;
     e.threads = small ? 128 : apart ? 1024 : 256;
     e.fn = select_fn(bf16, head_dim, group, small ? kSmall : apart ? kGiven : kLarge);
     if (apart) {

@@ -1801,7 +1801,8 @@ int pa_prefill_mass(const struct pa_sparse_args *args)
     void *fargs[] = {&p};
     const long long keys = (long long)a.max_blocks_per_seq * kBlockSize;
     if (keys <= kMassShortKeys &&
-        keys * a.max_query_len * (a.num_heads / a.num_kv_heads) <= kMassShortWork)
+        keys * a.head_dim * a.max_query_len * (a.num_heads / a.num_kv_heads) <=
+            (w.row_blocks == 1 ? kMassShortWork : kMassShortWorkOfBlocks))
         return launch_dependent(k.whole, dim3((unsigned)a.num_seqs * a.num_kv_heads),
                                 dim3(kMassShortThreads), 0, st, fargs);
     int dev = 0;
@@ -1817,8 +1818,12 @@ int pa_prefill_mass(const struct pa_sparse_args *args)
     if (rc != PA_OK)
         return rc;
     void *kargs[] = {&p, &tmk};
-    // one block an SM, two key tiles each at least
-    const dim3 grid((unsigned)std::min((long long)ds->num_sms, (w.tiles + 1) / 2));
+    // A key tile a block while the second pass's blocks find SMs of their own beside the first's,
+    // two of a unit's where they would not: 32 units of four tiles 13.1 us by one each, 11.0 by
+    // two, units of one tile 9.8 and 15.0.
+    const bool pairs = 2 * w.tiles > ds->num_sms && a.max_blocks_per_seq * kBlockSize > kMassKeys;
+    const dim3 grid((unsigned)std::min((long long)ds->num_sms,
+                                       pairs ? (w.tiles + 1) / 2 : w.tiles));
     rc = launch_dependent(k.stats, grid, dim3(k.threads), k.smem_stats, st, kargs);
     if (rc == PA_OK)
         rc = launch_dependent(k.sums, grid, dim3(k.threads), k.smem_sums, st, kargs);

@@ -341,7 +341,7 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
     for (int s0 = 0; s0 < p.num_seqs; s0 += NTH)
         scan_from(s0, true);
     const int total = carry;
-    const int R = max((total + (int)gridDim.x - 1) / (int)gridDim.x, 2);
+    const int R = (total + (int)gridDim.x - 1) / (int)gridDim.x;
     const long long share = (long long)blockIdx.x * R;
     if (share < total) {
         const int at = (int)share;
@@ -799,10 +799,11 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
 // The same for short sequences in one launch: a thread block takes a (sequence,
 // kv head) whole, its warps 16 (token, head) rows at a time with mma.sync.  The
 // channels of a product may be taken in any order, so rows of q and k are
-// loaded 16 bytes a lane straight into fragments.  A row's statistics never
-// leave its warp; the warps' sums for a key meet in shared memory.  Two chunks of
-// 5 and 70 tokens, 8/2 heads x 64: 11.5 us against 19 for the three launches, whose
-// own latencies those are.
+// loaded 16 bytes a lane straight into fragments.  Where the rows are few, the keys are
+// split between the warps, which exchange their rows' statistics; the warps' sums for a
+// key meet in shared memory.  What bounds it is one block's chain: lengths, table, rows,
+// then 1.0 us (64 channels) or 1.3 us (128) for every 32 keys of a warp and pass.  Two chunks
+// of 5 and 70 tokens, 8/2 heads x 64: 10.4 us in a graph, 14 by the passes and their sum.
 // ---------------------------------------------------------------------------
 template <typename T, int D>
 __global__ void __launch_bounds__(kMassShortThreads) prefill_mass_short_kernel(const PrefillMassParams p)
@@ -812,6 +813,7 @@ __global__ void __launch_bounds__(kMassShortThreads) prefill_mass_short_kernel(c
     constexpr int NW = kMassShortThreads / 32, NI = D / 32;
     constexpr int N8 = 4;                         // 8-key steps in flight
     __shared__ float acc[NW][kMassShortKeys];
+    __shared__ float2 part[NW][16];
     __shared__ int tile_of[kMassShortKeys / kBlockSize];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r = lane >> 2, qd = lane & 3;
@@ -840,15 +842,21 @@ __global__ void __launch_bounds__(kMassShortThreads) prefill_mass_short_kernel(c
         }
         tile_of[tid] = phys * Hkv + h;
     }
-    for (int t = lane; t < nblk * kBlockSize; t += 32)
-        acc[warp][t] = 0.f;
+    const int used = min((rows + 15) / 16, NW);   // rows of acc
+    if (warp < used)
+        for (int t = lane; t < nblk * kBlockSize; t += 32)
+            acc[warp][t] = 0.f;
     __syncthreads();
     for (int i = tid; i < x.L * LPR; i += kMassShortThreads)
         prefetch_l2(static_cast<const T *>(p.k_cache) +
                     ((size_t)tile_of[i / LPR / kBlockSize] * kBlockSize + i / LPR % kBlockSize) * D +
                     i % LPR * 64);
     const uint4 *kp = static_cast<const uint4 *>(p.k_cache) + qd;
-    for (int row0 = 16 * warp; row0 < rows; row0 += 16 * NW) {
+    // 16 rows a warp; a round that leaves warps over splits the keys of 16 rows into parts
+    for (int base = 0; base < rows; base += 16 * NW) {
+        const int groups = min((rows - base + 15) / 16, NW), parts = NW / groups;
+        const int mine = warp / groups, row0 = base + 16 * (warp % groups);   // no part: parts on
+        float *sums = acc[warp % groups];
         // rows row0 + r and + 8; past the last one that one again, without weight
         uint32_t a[2 * NI][4];
         int pos[2];
@@ -867,9 +875,11 @@ __global__ void __launch_bounds__(kMassShortThreads) prefill_mass_short_kernel(c
             }
         }
         // f(key step, scores in base 2: two keys of two rows) for every 8 keys that a row sees
-        const int last = min(steps, (x.L - x.c + (min(row0 + 15, rows - 1)) / G) / 8 + 1);
+        const int seen = min(steps, (x.L - x.c + (min(row0 + 15, rows - 1)) / G) / 8 + 1);
+        const int share = (seen + parts - 1) / parts;
+        const int from = mine * share, last = mine < parts ? min(seen, from + share) : 0;
         auto each = [&](auto &&f) {
-            for (int j0 = 0; j0 < last; j0 += N8) {
+            for (int j0 = from; j0 < last; j0 += N8) {
                 uint4 b[N8][NI];
 #pragma unroll
                 for (int i = 0; i < N8; ++i) {
@@ -919,11 +929,33 @@ __global__ void __launch_bounds__(kMassShortThreads) prefill_mass_short_kernel(c
 #pragma unroll
             for (int off = 1; off < 4; off <<= 1)
                 top[e] = fmaxf(top[e], __shfl_xor_sync(FULL, top[e], off));
-            float sum = m[e] > -INFINITY ? l[e] * exp2f(m[e] - top[e]) : 0.f;
+            inv[e] = m[e] > -INFINITY ? l[e] * exp2f(m[e] - top[e]) : 0.f;
 #pragma unroll
             for (int off = 1; off < 4; off <<= 1)
-                sum += __shfl_xor_sync(FULL, sum, off);
-            inv[e] = pos[e] >= 0 ? 1.f / sum : 0.f;
+                inv[e] += __shfl_xor_sync(FULL, inv[e], off);
+        }
+        if (parts > 1) {                          // (the last round alone)
+            if (mine < parts && qd == 0) {
+                part[warp][r] = make_float2(top[0], inv[0]);
+                part[warp][r + 8] = make_float2(top[1], inv[1]);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float M = -INFINITY, sum = 0.f;
+                for (int i = 0; i < parts; ++i)
+                    M = fmaxf(M, part[warp % groups + i * groups][r + 8 * e].x);
+                for (int i = 0; i < parts; ++i) {
+                    const float2 y = part[warp % groups + i * groups][r + 8 * e];
+                    sum += y.x > -INFINITY ? y.y * exp2f(y.x - M) : 0.f;
+                }
+                top[e] = M;
+                inv[e] = sum;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            inv[e] = pos[e] >= 0 ? 1.f / inv[e] : 0.f;
             top[e] = pos[e] >= 0 ? top[e] : 0.f;
         }
         each([&](int j, const float (&d)[4]) {
@@ -936,8 +968,8 @@ __global__ void __launch_bounds__(kMassShortThreads) prefill_mass_short_kernel(c
                     w[e] += __shfl_xor_sync(FULL, w[e], off);
             }
             if (r == 0) {
-                acc[warp][8 * j + 2 * qd] += w[0];
-                acc[warp][8 * j + 2 * qd + 1] += w[1];
+                sums[8 * j + 2 * qd] += w[0];
+                sums[8 * j + 2 * qd + 1] += w[1];
             }
         });
     }
@@ -946,7 +978,7 @@ __global__ void __launch_bounds__(kMassShortThreads) prefill_mass_short_kernel(c
         float sum = 0.f;
 #pragma unroll
         for (int w = 0; w < NW; ++w)
-            sum += acc[w][t];
+            sum += w < used ? acc[w][t] : 0.f;
         mass[t] = add_mass(mass + t, p.decay, t >= x.L - x.c, sum);
     }
 }

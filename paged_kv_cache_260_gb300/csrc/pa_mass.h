@@ -39,10 +39,17 @@ constexpr int kMassRows = 128;     // (token, head) rows of one query tile
 constexpr int kMassTiles = 2;      // query tiles of a unit
 constexpr int kMassKeys = 128;     // keys of a tile
 
-// A batch whose tables hold at most kMassShortKeys tokens and whose chunks' rows make
-// at most kMassShortWork products with them takes the one-launch kernel.
+// A batch whose tables hold at most kMassShortKeys tokens, and whose longest chunk's rows
+// make at most kMassShortWork multiplications with them, takes the one-launch kernel: 32
+// keys of 16 rows of 128 channels a warp.  Several row blocks cost the passes a third launch,
+// and more is worth it.  In us in a graph, bf16, one launch / the passes, for rows (tokens x
+// heads of a group) and keys, 32 runs of 128 channels: 4 x 512 10.3 / 11.0, 64 x 128 9.1 / 10.1,
+// 128 x 128 13.4 / 10.1, 64 x 256 13.6 / 10.1, 512 x 128 24.1 / 15.8; 4 runs of 64 channels:
+// 16 x 64 6.1 / 9.1, 4 x 512 8.2 / 9.5, 64 x 128 7.0 / 9.4, 128 x 128 9.9 / 9.2, 256 x 64
+// 7.9 / 10.8, 280 x 128 16.8 / 14.1; chunks of 5 and 70 tokens of four heads with a table of
+// 160 keys: 10.4 / 14.
 constexpr int kMassShortKeys = 512;
-constexpr long long kMassShortWork = 131072;
+constexpr long long kMassShortWork = 1 << 20, kMassShortWorkOfBlocks = 3 << 20;
 constexpr int kMassShortThreads = 512;
 
 struct MassKernels {

@@ -474,12 +474,24 @@ def test_prefill_mass(pa, dt, d, hkv, g, decay):
                                         ("bf16", 128, 2, 3), ("f16", 128, 1, 128)])
 @pytest.mark.parametrize("decay", [0.9, 0.0])
 def test_prefill_mass_of_short_sequences(pa, dt, d, hkv, g, decay):
-    # at most 512 keys and 131072 pairs a head: one launch
+    # small tables, chunks of one row block and of several
     most = 131072 // (304 * g)
     chunk_case(pa, gen(40, d, g), [150, 300, 1, 16, 0, 47, 17], [min(most, 5), min(most, 70), 1, 16
                                                                if most >= 16 else 3, 0, 0, 1],
                dt, d, hkv, g, decay)
     chunk_case(pa, gen(41, d, g), [33, 8, 1], [min(33, most), min(8, most), 1], dt, d, hkv, g, decay)
+
+
+@pytest.mark.parametrize("keys,rows,g", [
+    (512, 16, 1), (512, 1, 16), (256, 2, 16), (128, 16, 4), (64, 128, 1), (48, 42, 4), (160, 12, 4),
+    (16, 16, 16), (32, 2, 128), (160, 70, 4), (176, 17, 16), (80, 3, 128), (64, 60, 6), (64, 30, 12)])
+@pytest.mark.parametrize("dt,d", [("bf16", 128), ("f16", 64)])
+def test_prefill_mass_in_one_launch(pa, keys, rows, g, dt, d):
+    # few products: the warps take rows, and parts of the keys where there are few rows
+    rows = min(rows, keys)
+    lens, chunks = [keys, keys - 3, 1, 0, rows, keys // 2 + 1], [rows, 1, 1, 0, rows, min(3, rows)]
+    chunk_case(pa, gen(55, keys, rows, g), lens, chunks, dt, d, 2, g, 0.9, mb=keys // 16,
+               longest=rows)
 
 
 @pytest.mark.parametrize("lens,chunks,g", [([5000], [64], 4), ([3000, 200], [700, 1], 2),

@@ -29,14 +29,17 @@ __device__ __forceinline__ uint32_t mass_key(float x)
 }
 
 // One (sequence, kv head) per thread block, or per cluster of blocks that share out its
-// slots and its moves (CLUSTER).
+// slots and its moves (CLUSTER).  The choice is a chain of passes over the keys in shared
+// memory, a barrier each (two to four digits of a histogram, ties, holes and movers); the moves
+// are bound by HBM where many rows move (128 x 4096 tokens to 2048: 1.1 GB read and written in
+// 140 us).  A batch of 128 that gives back one block, 47 rows a run, 11.5 us: half the choice.
 template <int D, int NTH, bool CLUSTER>
 __global__ void __launch_bounds__(NTH) evict_kernel_t(const EvictParams p)
 {
     constexpr int NW = NTH / 32;
     constexpr uint32_t FULL = 0xffffffffu;
     constexpr int CPR = D / 8;                    // 16-byte chunks of a row
-    constexpr int RPW = 32 / (2 * CPR);           // tokens (K and V row) a warp moves at once
+    constexpr int RPW = 32 / (2 * CPR);           // tokens (K and V row) a warp loads at once
     constexpr int U = 8;                          // loads in flight a lane
     // keys of the block's slots (p.keys of them), the table, holes and sources
     extern __shared__ uint32_t smem[];
@@ -193,40 +196,48 @@ __global__ void __launch_bounds__(NTH) evict_kernel_t(const EvictParams p)
     tally.sync();
 
     // The moves, then the last ones' way down by L - B, in rounds that are loaded whole before
-    // they are stored: what a round writes lies before all that later rounds read.  A
-    // lane takes 16 bytes of a token's K row or V row.
+    // they are stored: what a round writes lies before all that later rounds read.  A warp takes
+    // neighbouring moves, a lane holds one's places (the next round's are fetched ahead) and its
+    // mass, and takes 16 bytes of a token's K row or V row.
+    constexpr int WT = U * RPW;                   // tokens of a warp's round
     const int sub = lane / (2 * CPR), ch = lane % (2 * CPR);
     uint4 *pool = static_cast<uint4 *>(ch < CPR ? p.k_cache : p.v_cache) + ch % CPR;
     auto row_of = [&](int t) {
         return pool + (((size_t)table[t / kBlockSize] * Hkv + h) * kBlockSize + t % kBlockSize) * CPR;
     };
-    const int per = C * NW * RPW;                 // tokens the run's warps take at once
-    const int mine = (rank * NW + warp) * RPW + sub;
-    for (int base = 0; base < moves + R; base += per * U) {
+    const int per = C * NW * WT;                  // tokens the run's warps take at once
+    auto places = [&](int base, int &src, int &dst) {
+        const int j = base + (rank * NW + warp) * WT + lane;
+        src = dst = -1;
+        if (lane < WT && j < moves + R) {
+            src = j < moves ? from[j] : hi + j - moves;
+            dst = j < moves ? to[j] : edge + j - moves;
+        }
+    };
+    int src, dst, src_next, dst_next;
+    places(0, src, dst);
+    for (int base = 0; base < moves + R; base += per) {
         uint4 x[U];
-        float m[U];
-        int dst[U];
+        const float m = dst >= 0 ? __ldcg(mass + src) : 0.f;
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            const int j = base + i * per + mine;
-            dst[i] = -1;
-            if (j < moves + R) {
-                const int src = j < moves ? from[j] : hi + j - moves;
-                dst[i] = j < moves ? to[j] : edge + j - moves;
-                x[i] = __ldcg(row_of(src));
-                if (ch == 0)
-                    m[i] = __ldcg(mass + src);
-            }
+            const int at = __shfl_sync(FULL, src, i * RPW + sub);
+            if (at >= 0)
+                x[i] = __ldcg(row_of(at));
         }
-        if (base + per * U > moves)               // the last ones: their places may be read here
+        places(base + per, src_next, dst_next);
+        if (base + per > moves)                   // the last ones: their places may be read here
             tally.sync();
 #pragma unroll
-        for (int i = 0; i < U; ++i)
-            if (dst[i] >= 0) {
-                *row_of(dst[i]) = x[i];
-                if (ch == 0)
-                    mass[dst[i]] = m[i];
-            }
+        for (int i = 0; i < U; ++i) {
+            const int at = __shfl_sync(FULL, dst, i * RPW + sub);
+            if (at >= 0)
+                *row_of(at) = x[i];
+        }
+        if (dst >= 0)
+            mass[dst] = m;
+        src = src_next;
+        dst = dst_next;
     }
     tally.leave();
 }
@@ -236,17 +247,26 @@ constexpr int kEvictTable = 8192;                 // table entries a block holds
 
 }  // namespace
 
-// Short tables: a block of 128 threads a run.  Others: 256 threads, and where the runs leave
-// SMs idle a cluster of 2, 4 or 8 blocks shares a run, 1024 slots a block at least.
+// 256 threads a block, three of which an SM holds; where the runs leave SMs idle, or a run's
+// masses would take an SM's shared memory, a cluster of 2, 4 or 8 blocks shares one.  More
+// short runs than fit at once: 128 threads, seven blocks an SM.  us in a graph, bf16, 8 heads x
+// 128, sequences x tokens -> kept.  128 / 256 threads: 128 x 1040 -> 1024 11.5 / 15.3, 128 x 2048
+// -> 2030 15.5 / 18.7, 128 x 2048 -> 1024 72.4 / 68.6, 32 x 1040 -> 1024 8.3 / 7.2.  1 / 2 / 4 / 8
+// blocks: 4 x 4096 -> 2048 23.0 / 18.5 / 15.0 / 16.7, 32 x 2048 -> 2030 8.3 / 12.4 / 21.8 / 42.3,
+// 16 x 8192 -> 8000 18.2 / 17.0 / 15.4 / 27.1, 8 x 32K -> 2048 77.5 / 46.2 / 31.3 / 26.2, 32 x 32K
+// -> 4096 222 / 157 / 150 / 141, 128 x 16K -> 2048 281 / 230 / 240 / 316, 64 x 8192 -> 2048
+// 103 / 106 / 115 / 150 (the bytes' time at HBM's rate 124: part of them stays in L2).
 EvictLaunch evict_launch(int head_dim, int num_runs, int max_blocks, int num_sms)
 {
     EvictLaunch e{};
     const long long slots = (long long)max_blocks * kBlockSize;
-    const bool small = slots <= 2048;
+    const bool small = slots <= 2048 && num_runs > 3LL * num_sms;
     e.threads = small ? 128 : 256;
     e.cluster = 1;
-    while (!small && e.cluster < 8 && 2LL * e.cluster * num_runs <= 4LL * num_sms &&
-           slots >= 2048LL * e.cluster)
+    while (!small && e.cluster < 8 &&
+           ((2LL * e.cluster * num_runs <= 4LL * num_sms && slots >= 4096LL * e.cluster) ||
+            (2LL * e.cluster * num_runs <= num_sms && slots >= 2048LL * e.cluster) ||
+            slots >= 16384LL * e.cluster))
         e.cluster *= 2;
     if (small)
         e.fn = head_dim == 128 ? reinterpret_cast<const void *>(&evict_kernel_t<128, 128, false>)

@@ -49,7 +49,9 @@ constexpr int kBoundsThreads = 256;
 // block's live tokens.  One warp takes a (block, kv head) tile: all of its
 // 16-byte loads (8 a lane at head_dim 128) are in flight at once, the rows meet
 // in packed 16-bit minima and maxima and one or two shuffles, and half of
-// the lanes write the minima, half the maxima.
+// the lanes write the minima, half the maxima.  HBM bounds it: 16 prompts of 16K tokens, 8
+// heads x 128, 604 MB in 100 us (6.0 TB/s; five blocks an SM is what 48 registers leave).  A
+// decode step's 1024 tiles are one round of loads: 3.9 us in a graph, the launch's time.
 // ---------------------------------------------------------------------------
 template <typename T, int D>
 __global__ void __launch_bounds__(kBoundsThreads) block_bounds_kernel(const BoundsParams p)
@@ -169,6 +171,12 @@ __global__ void __launch_bounds__(kBoundsThreads) block_bounds_kernel(const Boun
 // sequences would leave most SMs idle: their scores are computed first, by a
 // kernel whose warps share out all of them evenly, and read from the workspace
 // (SCORED).
+//
+// The bounds are read once, 4 head_dim bytes a block and kv head.  With many runs HBM
+// bounds the scores and a block's choice comes after its own: 1024 runs to 16K tokens, 278 MB,
+// 70 us cold (60 % of the copy rate).  With few runs the scores of 4 x 32K to 131K tokens, 84
+// MB, take 16 us and the choice of 256 of 8192 blocks 9 more: a chain of passes over the scores
+// in shared memory, a barrier each.
 // ---------------------------------------------------------------------------
 constexpr int kDoubt = 256;                       // blocks in doubt that are ranked directly
 constexpr int kSelectNear = 16384;                // scores a block holds (64 KB)
@@ -295,6 +303,18 @@ __device__ __forceinline__ void score_tile(const ScoreQueries<T, D, NT> &q, cons
     }
 }
 
+// Sends for the bounds of the 16 blocks after those that are being summed, to L2: the lines of
+// rows r and r + 8, one a lane of the row's four.
+template <typename T, int D>
+__device__ __forceinline__ void prefetch_tile(const void *bounds, const int (&tile)[2], int qd)
+{
+    constexpr int LINES = 2 * D * (int)sizeof(T) / 128;
+    if (qd < LINES)
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+            prefetch_l2(static_cast<const T *>(bounds) + (size_t)tile[a] * 2 * D + 64 * qd);
+}
+
 // All scores of the batch to the workspace, and of every 16 the largest sum |q||bound|.
 // The warps take equal shares of the list of (sequence, kv head, 16 blocks); a sequence
 // that keeps all of its blocks has none in it.
@@ -372,8 +392,10 @@ __global__ void __launch_bounds__(kScoreThreads, 4) block_score_kernel_t(const S
                     }
                 }
             }
-            if (u + 1 < end)
+            if (u + 1 < end) {
                 tiles_of(next);
+                prefetch_tile<T, D>(p.bounds, next, qd);
+            }
         });
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1)
@@ -477,8 +499,10 @@ __global__ void __launch_bounds__(NTH, SCORED ? 1 : 512 / NTH) block_select_kern
         for (int b = 16 * warp; b < nb; b += 16 * NW) {
             float best[2];
             score_tile<T, D, NT>(queries, p.bounds, tile, G, qd, best, size, [&]() {
-                if (b + 16 * NW < nb)
+                if (b + 16 * NW < nb) {
                     rows(b + 16 * NW, next);
+                    prefetch_tile<T, D>(p.bounds, next, qd);
+                }
             });
             const int j = b + 8 * qd + r;
             if (qd < 2 && j < nb) {
@@ -748,8 +772,12 @@ SelectLaunch select_launch(bool bf16, int head_dim, int group, int num_runs, int
     SelectLaunch e{};
     const bool small = max_blocks <= 256;
     // A thread block a run, or, with few runs, the scores apart: bf16, 32/8 heads x 128, lengths
-    // to 16K, us of the one and of the other: 128 runs 17.4 / 14.7, 256 runs 20.2 / 22.6, 512
-    // runs 38.5 / 48.7; 32 runs of 32K to 131K tokens 98 / 24.3.
+    // to 16K, us in a graph of the one and of the other: 128 runs 17.4 / 14.7, 256 runs 20.2 /
+    // 22.6, 512 runs 38.5 / 48.7; 32 runs of 32K to 131K tokens 98 / 24.3.  Short tables: 128
+    // threads against what they would else have: 8 runs of 4096 tokens 7.8 / 8.5 (apart), 64
+    // runs 10.3 / 11.9 (apart), 256 runs 12.6 / 10.6 (256 threads), 1024 runs 24.9 / 31.6, 4096
+    // runs 76.6 / 104.7; 32 runs to 1024 tokens of 64 channels 4.5 / 8.6 (apart).  Long ones
+    // without: 256 runs to 16K tokens 35.4 by 128 threads, 29.4 by 256; 512 runs 45.5 / 46.0.
     const bool apart = !small && max_blocks > keep && 2LL * num_runs < 3LL * num_sms &&
                        num_runs <= kRaggedSeqs;
     e.threads = small ? 128 : apart ? 1024 : 256;

@@ -1376,7 +1376,9 @@ inline void fill_kernel_set(KernelSet *ks)
     ks->merge_part = reinterpret_cast<const void *>(&merge_part_kernel<T, D>);
 }
 
-// The decode of pa_decode_mass: the same kernels, leaving scores and statistics.
+// The decode of pa_decode_mass: the same kernels, leaving scores and statistics.  The scores are 4
+// bytes beside 4 head_dim bytes of K and V a kv head (twice to eight times that in a group):
+// the batch-128 decode takes 79.7 us with them, 77.7 without.
 template <typename T, int D, int NT>
 inline void fill_mass_kernel_set(KernelSet *ks)
 {

@@ -30,7 +30,10 @@ __device__ __forceinline__ float add_mass(float *at, float decay, bool fresh, fl
 
 // ---------------------------------------------------------------------------
 // After a decode: every token's weights from the kept scores.  A warp takes 128
-// tokens of a (sequence, kv head), four a lane a stride of 32 apart.
+// tokens of a (sequence, kv head), four a lane a stride of 32 apart.  The batch-128
+// decode step, 32/8 heads: 19.2 MB in 8.4 us of the 88.1 that decode and accounting take in
+// a graph (the plain decode 77.7, leaving the scores 2): two or three runs a warp, each a
+// chain of length, statistics and scores.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kMassFinishThreads, 4)
 decode_mass_finish_kernel(const DecodeMassParams p)
@@ -129,6 +132,13 @@ decode_mass_finish_kernel(const DecodeMassParams p)
 // since both grow along the list.  Pass 2 folds a unit's pieces when it loads its
 // rows, and reads each piece's keys from the last tile back: those are the ones
 // that pass 1 left in L2.
+//
+// 64 rows x 4 heads over 8 sequences of 16K tokens, 8 kv heads x 128: 127 us in a graph,
+// 63 a pass, each 268 MB of keys and 34.4 GFLOP twice the masks' share included (4.2 TB/s and
+// 1.09 PFLOP/s over the two).  No one unit is full: the tensor pipe is active 42 % of the time,
+// the exponentials' 43 %, issue slots 53 %; 13 us a pass are its start and end.  Without
+// exponentials pass 1 takes 57 us, with its keys in L2 as well 55: what is left is the
+// products' hand-overs, 0.78 us a tile of 128 keys against 0.66 at the library's rate.
 // ---------------------------------------------------------------------------
 template <int D, bool SUMS>
 struct MassShape {
@@ -141,7 +151,7 @@ struct MassShape {
     static constexpr int NSLOT = D == 64 ? 8 : SUMS ? 4 : 6;
     static constexpr int OFF_SLOT = Q_BYTES;
     static constexpr int OFF_LSE = OFF_SLOT + NSLOT * SLOT_BYTES;
-    static constexpr int OFF_PART = OFF_LSE + NG * BM * 4;       // [buffer][turn & 1][key]
+    static constexpr int OFF_PART = OFF_LSE + 2 * NG * BM * 4;   // [buffer][turn & 1][key]
     // full[NSLOT] empty[NSLOT] s[4] read[3] q[2] free[2] group[2] sum[4] drain, then TMEM base
     // and abort flag
     static constexpr int NBAR = 2 * NSLOT + 18;
@@ -259,7 +269,7 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
     const uint32_t raw_addr = smem_addr(smem_raw);
     unsigned char *smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
     const uint32_t sbase = smem_addr(smem), slot_addr = sbase + Sh::OFF_SLOT;
-    float *lse = reinterpret_cast<float *>(smem + Sh::OFF_LSE);      // minus the rows' log sums
+    float *lse = reinterpret_cast<float *>(smem + Sh::OFF_LSE);      // [unit & 1] minus log sums
     float *part = reinterpret_cast<float *>(smem + Sh::OFF_PART);    // the first query tile's sums
     const uint32_t bar_addr = sbase + Sh::OFF_BAR;
     auto full_bar = [&](int s) { return bar_addr + 8u * s; };
@@ -535,17 +545,23 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
             // ---- query rows ----
             // Row r = (token t0 + r / G, head r % G); rows past the chunk and those that do not
             // fill a token are zero.  The products of the piece before have ended.
-            if (units > 0 &&
-                !__all_sync(FULL, mbar_wait_bounded(free_bar(SUMS ? 0 : grp), (units - 1) & 1))) {
-                ok = false;
-                break;
-            }
-            ++units;
             const T *qg = static_cast<const T *>(p.q);
             const int tok = t0 + rr / G;
             const bool row_valid = rr < TPG * G && tok < w.x.c;
+            const int unit = (w.s * Hkv + w.h) * p.row_blocks + w.b;
+            // a piece's statistics: [half of the key tiles][query tile][row]
+            float2 *stats = p.stats + (size_t)unit * (2 * ROWS) + grp * Sh::BM + rr;
+            float m = -INFINITY, l = 0.f;
+            auto free_rows = [&]() {
+                const int n = units++;
+                return n == 0 || __all_sync(FULL, mbar_wait_bounded(free_bar(SUMS ? 0 : grp),
+                                                                    (n - 1) & 1));
+            };
             if (!SUMS) {
                 // to tensor memory, a thread 64 channels of its lane's row
+                ok = free_rows();
+                if (!ok)
+                    break;
                 if (half < D / 64) {
                     uint32_t x[32];
                     const uint4 *src = reinterpret_cast<const uint4 *>(
@@ -574,6 +590,28 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
                         qv[i] = __ldg(reinterpret_cast<const uint4 *>(
                             qg + ((size_t)(w.x.qs + rt) * Hq + w.h * G + r % G) * D + ch * 8));
                 }
+                // Minus log2 of the row's sum over the unit's pieces (rows that are none: -inf): by
+                // the first set, or, with many pieces, by both; eight loads in flight, the first
+                // of them with the queries'.
+                if (units == 0)
+                    grid_dependency_wait();
+                constexpr int NF = 8;
+                const int k0 = w.first / R, pieces = (w.first + w.nt - 1) / R - k0 + 1;
+                const bool both = 2 * pieces > NF;
+                const int n = !row_valid ? 0 : both ? pieces : half ? 0 : 2 * pieces;
+                const int step = both ? 2 * ROWS : ROWS;
+                const float2 *from = stats + (size_t)(2 * k0 + half) * ROWS;
+                float2 a[NF];
+                auto fetch = [&](int j) {
+#pragma unroll
+                    for (int i = 0; i < NF; ++i)
+                        a[i] = j + i < n ? __ldcg(from + (size_t)(j + i) * step)
+                                         : make_float2(-INFINITY, 0.f);
+                };
+                fetch(0);
+                ok = free_rows();
+                if (!ok)
+                    break;
 #pragma unroll
                 for (int i = 0; i < NPT; ++i) {
                     const int r = grp * Sh::BM + lt / CPR + i * RSTEP;
@@ -582,47 +620,30 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
                 }
                 fence_proxy_async_shared();
                 mbar_arrive(q_bar(0));
-            }
-            const int unit = (w.s * Hkv + w.h) * p.row_blocks + w.b;
-            // a piece's statistics: [half of the key tiles][query tile][row]
-            float2 *stats = p.stats + (size_t)unit * (2 * ROWS) + grp * Sh::BM + rr;
-            float m = -INFINITY, l = 0.f;
-            if (SUMS) {
-                // minus log2 of the row's sum over the unit's pieces; rows that are none: -inf.  A
-                // unit of few, long sequences has many pieces: each set folds those of one half
-                // of the key tiles, eight loads in flight.
-                if (units == 1)
-                    grid_dependency_wait();
-                float M = -INFINITY;
-                const int k0 = w.first / R;
-                const int n = row_valid ? (w.first + w.nt - 1) / R - k0 + 1 : 0;
-                const float2 *from = stats + (size_t)(2 * k0 + half) * ROWS;
-                for (int j = 0; j < n; j += 8) {
-                    float2 a[8];
+                for (int j = 0; j < n; j += NF) {
+                    if (j)
+                        fetch(j);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        a[i] = j + i < n ? __ldcg(from + (size_t)(j + i) * (2 * ROWS))
-                                         : make_float2(-INFINITY, 0.f);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float nM = fmaxf(M, a[i].x);
+                    for (int i = 0; i < NF; ++i) {
+                        const float nM = fmaxf(m, a[i].x);
                         if (nM > -INFINITY)
-                            l = l * exp2f(M - nM) + a[i].y * exp2f(a[i].x - nM);
-                        M = nM;
+                            l = l * exp2f(m - nM) + a[i].y * exp2f(a[i].x - nM);
+                        m = nM;
                     }
                 }
-                const float mine = l > 0.f ? M + log2f(l) : -INFINITY;
-                float *at = lse + grp * Sh::BM + rr;
-                ok = meet();                              // all are done with the piece before
-                if (half)
-                    *at = mine;
-                ok = ok && meet();
-                if (!half && row_valid) {
+                // (two buffers: a thread still at the piece before reads the other)
+                float *at = lse + (units & 1) * ROWS + grp * Sh::BM + rr;
+                float mine = l > 0.f ? m + log2f(l) : -INFINITY;
+                if (both) {
+                    if (half)
+                        *at = mine;
+                    ok = meet();
                     const float other = *at, top = fmaxf(mine, other);
-                    *at = -(top + log2f(exp2f(mine - top) + exp2f(other - top)));
-                } else if (!half) {
-                    *at = -INFINITY;
+                    if (row_valid)
+                        mine = top + log2f(exp2f(mine - top) + exp2f(other - top));
                 }
+                if (!half)
+                    *at = row_valid ? -mine : -INFINITY;
                 ok = ok && meet();
                 if (!ok)
                     break;
@@ -725,7 +746,8 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
                     }
                     uint64_t sum2[4] = {0, 0, 0, 0};
                     const uint64_t nm2 = f2_pack(-mref, -mref);
-                    const float4 *ls = reinterpret_cast<const float4 *>(lse + grp * Sh::BM + c);
+                    const float4 *ls = reinterpret_cast<const float4 *>(
+                        lse + (units & 1) * ROWS + grp * Sh::BM + c);
 #pragma unroll
                     for (int e = 0; e < CW; e += 4) {
                         uint64_t na = nm2, nb = nm2;

@@ -1831,7 +1831,8 @@ int pa_prefill_mass(const struct pa_sparse_args *args)
         return rc;
     const long long units = (long long)a.num_seqs * a.num_kv_heads * ((a.max_blocks_per_seq + 7) / 8);
     return launch_dependent(prefill_mass_finish(),
-                            dim3(share_grid(units, kMassFinishThreads, 4, ds)),
+                            dim3(share_grid(units * (kMassFinishThreads / 32), kMassFinishThreads,
+                                            4, ds)),
                             dim3(kMassFinishThreads), 0, st, fargs);
 }
 

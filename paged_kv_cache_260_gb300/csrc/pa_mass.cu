@@ -1005,15 +1005,19 @@ __global__ void __launch_bounds__(kMassShortThreads) prefill_mass_short_kernel(c
     }
 }
 
-// Several row blocks: the sum over a sequence's query tiles, added to the mass: a warp 128
-// tokens of a (sequence, kv head), four a lane.
+// Several row blocks: the sum over a sequence's query tiles, added to the mass.  Eight warps
+// (with two row blocks, four) share out the query tiles of 128 tokens of a (sequence, kv
+// head), four tokens a lane.  What bounds it is a warp's chain of loads: 14 runs of 1130
+// tokens, 34 row blocks, 9 us (a warp for all of the tiles 25); 64 runs to 5534 tokens, 2 row
+// blocks, 51 us in all with four warps, 54 with eight.
 __global__ void __launch_bounds__(kMassFinishThreads)
 prefill_mass_finish_kernel(const PrefillMassParams p)
 {
-    constexpr int NTH = kMassFinishThreads, TOK = 128;
+    constexpr int NTH = kMassFinishThreads, NW = NTH / 32, TOK = 128;
     __shared__ RaggedSmem sm;
-    const int lane = threadIdx.x & 31;
-    const int warps = gridDim.x * (NTH / 32), me = blockIdx.x * (NTH / 32) + (threadIdx.x >> 5);
+    __shared__ float4 part[NW][TOK / 4];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int split = p.row_blocks == 2 ? 4 : NW;
     const int Hkv = p.num_kv_heads, G = p.num_heads / Hkv, TPG = kMassRows / G;
     const int T = p.max_blocks * kBlockSize;
     grid_dependents_launch();
@@ -1026,34 +1030,43 @@ prefill_mass_finish_kernel(const PrefillMassParams p)
             return x.blocks ? (x.L + TOK - 1) / TOK : 0;
         });
         const long long total = (long long)sm.pre[n] * Hkv;
-        for (long long u = me; u < total; u += warps) {
+        for (long long u0 = (long long)blockIdx.x * (NW / split); u0 < total;
+             u0 += (long long)gridDim.x * (NW / split)) {
+            // (past the end the last unit again, which is not written)
+            const long long u = min(u0 + warp / split, total - 1);
             const int i = ragged_find(sm, n, (int)(u / Hkv));
             const int nt = sm.pre[i + 1] - sm.pre[i];
             const int at = (int)(u - (long long)sm.pre[i] * Hkv);
-            const int s = begin + i, h = at / nt, t = at % nt * TOK + 4 * lane;
+            const int s = begin + i, h = at / nt, t0 = at % nt * TOK, t = t0 + 4 * lane;
             const int L = __ldg(p.seq_lens + s);
             const int c = __ldg(p.query_start + s + 1) - __ldg(p.query_start + s);
-            if (t >= L)
-                continue;
             const size_t run = (size_t)s * Hkv + h;
-            const float *part = p.sums + run * (kMassTiles * p.row_blocks) * T + t;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            const float *from = p.sums + run * (kMassTiles * p.row_blocks) * T + t;
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
             // query tiles whose keys reach t (a unit's end where its last row's do)
-            const int TPB = kMassTiles * TPG, tiles = (c + TPG - 1) / TPG;
+            const int TPB = kMassTiles * TPG, tiles = t < L ? (c + TPG - 1) / TPG : 0;
 #pragma unroll 4
-            for (int k = max(0, (t - (L - c)) / TPB) * kMassTiles; k < tiles; ++k) {
-                const float4 x = __ldcg(reinterpret_cast<const float4 *>(part + (size_t)k * T));
+            for (int k = max(0, (t - (L - c)) / TPB) * kMassTiles + warp % split; k < tiles;
+                 k += split) {
+                const float4 x = __ldcg(reinterpret_cast<const float4 *>(from + (size_t)k * T));
                 const int end = L - c + min((k / kMassTiles + 1) * TPB, c);
-                sum[0] += x.x;                    // (t itself is reached by the first unit)
-                sum[1] += t + 1 < end ? x.y : 0.f;
-                sum[2] += t + 2 < end ? x.z : 0.f;
-                sum[3] += t + 3 < end ? x.w : 0.f;
+                sum.x += x.x;                     // (t itself is reached by the first unit)
+                sum.y += t + 1 < end ? x.y : 0.f;
+                sum.z += t + 2 < end ? x.z : 0.f;
+                sum.w += t + 3 < end ? x.w : 0.f;
             }
-            float *mass = p.mass + run * T + t;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (t + k < L)
-                    mass[k] = add_mass(mass + k, p.decay, t + k >= L - c, sum[k]);
+            part[warp][lane] = sum;
+            __syncthreads();
+            // a warp's share of the 128 tokens
+            const int j = warp % split * (TOK / split) + lane;
+            if (lane < TOK / split && t0 + j < L && u0 + warp / split < total) {
+                float all = 0.f;
+                for (int w = 0; w < split; ++w)
+                    all += reinterpret_cast<const float *>(part[warp / split * split + w])[j];
+                float *mass = p.mass + run * T + t0 + j;
+                *mass = add_mass(mass, p.decay, t0 + j >= L - c, all);
+            }
+            __syncthreads();
         }
     }
 }

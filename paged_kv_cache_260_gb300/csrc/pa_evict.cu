@@ -247,9 +247,9 @@ constexpr int kEvictTable = 8192;                 // table entries a block holds
 
 }  // namespace
 
-// 256 threads a block, three of which an SM holds; where the runs leave SMs idle, or a run's
-// masses would take an SM's shared memory, a cluster of 2, 4 or 8 blocks shares one.  More
-// short runs than fit at once: 128 threads, seven blocks an SM.  us in a graph, bf16, 8 heads x
+// 256 threads a block, four of which an SM holds; where the runs leave SMs idle, or a run's
+// masses would take much of an SM's shared memory, a cluster of 2, 4 or 8 blocks shares one.
+// More than three short runs an SM: 128 threads, eight blocks an SM.  us in a graph, bf16, 8 heads x
 // 128, sequences x tokens -> kept.  128 / 256 threads: 128 x 1040 -> 1024 11.5 / 15.3, 128 x 2048
 // -> 2030 15.5 / 18.7, 128 x 2048 -> 1024 72.4 / 68.6, 32 x 1040 -> 1024 8.3 / 7.2.  1 / 2 / 4 / 8
 // blocks: 4 x 4096 -> 2048 23.0 / 18.5 / 15.0 / 16.7, 32 x 2048 -> 2030 8.3 / 12.4 / 21.8 / 42.3,

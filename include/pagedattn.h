@@ -601,9 +601,9 @@ int pa_decode_mass(const struct pa_sparse_args *args);
  *   mass, q [num_queries][num_heads][head_dim], k_cache, block_tables, seq_lens,
  *   query_start [num_seqs + 1] int32, max_query_len, max_blocks_per_seq, scale > 0,
  *   decay; groups of 1..128
- * A chunk that is negative, longer than its sequence or than max_query_len (beyond the
- * last row block, of 2 * (128 / group) rows), or whose rows lie outside q sets
- * PA_DEVERR_QUERY_RANGE; that, or a bad length, leaves the sequence as it was.
+ * A chunk that is negative, longer than its sequence or than max_query_len (it may be
+ * taken all the same up to the next 2 * (128 / group) rows), or whose rows lie outside q
+ * sets PA_DEVERR_QUERY_RANGE; that, or a bad length, leaves the sequence as it was.
  * Bad table entries read block 0.
  */
 size_t pa_prefill_mass_workspace_size(int num_seqs, int max_query_len, int num_heads,

@@ -1709,8 +1709,10 @@ int pa_decode_mass(const struct pa_sparse_args *args)
 // pa_prefill_mass's units of 2 x 128 rows, and its workspace: the statistics of the units'
 // pieces (one for each unit and one more for each border between two blocks' shares), and
 // of several row blocks each query tile's sums for every key.
+// Chunks of few rows keep their scores instead, with the statistics of the warps' pieces.
 struct PrefillMassPlan {
     long long row_blocks, units, tiles;
+    int few_cols, few_warps;       // 0: not the form for few rows
     size_t sums_off, total;
 };
 
@@ -1724,6 +1726,16 @@ static bool prefill_mass_plan(int num_seqs, int max_query_len, int num_heads, in
     w->row_blocks = (max_query_len + tokens - 1) / tokens;
     w->units = (long long)num_seqs * num_kv_heads * w->row_blocks;
     w->tiles = w->units * (((long long)max_blocks * kBlockSize + kMassKeys - 1) / kMassKeys);
+    const long long rows = (long long)max_query_len * (num_heads / num_kv_heads);
+    if (rows <= kMassFewRows && num_seqs <= kRaggedSeqs) {
+        const long long runs = (long long)num_seqs * num_kv_heads;
+        w->few_cols = score_cols((int)rows);
+        w->few_warps = num_sms * (rows <= 8 ? 4 : 3) * (kMassFewThreads / 32);
+        w->sums_off = round_up(sizeof(float2) * (size_t)(runs + w->few_warps) * kMassFewRows, 256);
+        w->total = w->sums_off +
+                   sizeof(float) * (size_t)runs * max_blocks * kBlockSize * w->few_cols;
+        return true;
+    }
     w->sums_off = round_up(
         sizeof(float2) * (size_t)(w->units + num_sms) * 2 * kMassTiles * kMassRows, 256);
     w->total = w->sums_off;
@@ -1805,6 +1817,21 @@ int pa_prefill_mass(const struct pa_sparse_args *args)
             (w.row_blocks == 1 ? kMassShortWork : kMassShortWorkOfBlocks))
         return launch_dependent(k.whole, dim3((unsigned)a.num_seqs * a.num_kv_heads),
                                 dim3(kMassShortThreads), 0, st, fargs);
+    if (w.few_cols) {
+        p.few_cols = w.few_cols;
+        p.few_tokens = a.max_query_len;
+        p.few_warps = w.few_warps;
+        rc = launch_dependent(k.few[w.few_cols > 8], dim3(w.few_warps / (kMassFewThreads / 32)),
+                              dim3(kMassFewThreads), 0, st, fargs);
+        if (rc != PA_OK)
+            return rc;
+        const long long blocks = (long long)a.num_seqs * a.num_kv_heads *
+                                 ((a.max_blocks_per_seq + 63) / 64);
+        return launch_dependent(k.few_finish,
+                                dim3(share_grid(blocks * (kMassFinishThreads / 32),
+                                                kMassFinishThreads, 4, ds)),
+                                dim3(kMassFinishThreads), 0, st, fargs);
+    }
     int dev = 0;
     cudaGetDevice(&dev);
     rc = ensure_smem(k.stats, dev, k.smem_stats);

@@ -74,6 +74,10 @@ struct DecodeParams {
     float2 *stat;
 };
 
+// Sequences whose unit counts a block holds at a time (pa_ragged.cuh); larger batches are
+// walked in parts of this many.
+constexpr int kRaggedSeqs = 2048;
+
 // Scores of a token, an even number so that a lane stores its two heads at once.
 inline __host__ __device__ int score_cols(int group) { return (group + 1) & ~1; }
 

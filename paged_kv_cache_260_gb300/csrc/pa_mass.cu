@@ -818,6 +818,299 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
 }
 
 // ---------------------------------------------------------------------------
+// A chunk of at most 16 (token, head) rows a kv head: a query tile of 128 would be mostly empty,
+// and the scores are fewer bytes than the keys, so they are kept and the keys read once.
+// The warps take equal shares of the list of (sequence, kv head, 32 keys): keys are the rows
+// of mma.sync's A operand, loaded 16 bytes a lane straight into fragments, the chunk's rows are
+// its columns.  A lane keeps the maximum and sum of its own keys for each of its columns; a
+// warp's piece of a (sequence, kv head) leaves them in slot (run + warp), which no two pieces
+// share.
+// ---------------------------------------------------------------------------
+constexpr int kFewThreads = kMassFewThreads, kFewKeys = 32;
+
+// The (sequence, kv head)'s units of 32 keys, none where there is nothing to do.
+__device__ __forceinline__ int few_units(const MassSeq &x)
+{
+    return x.blocks ? (x.L + kFewKeys - 1) / kFewKeys : 0;
+}
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kFewThreads, NT == 1 ? 4 : 3)
+prefill_mass_few_kernel(const PrefillMassParams p)
+{
+    using M = Mma<T>;
+    constexpr uint32_t FULL = 0xffffffffu;
+    constexpr int NI = D / 32;
+    __shared__ RaggedSmem sm;
+    const int lane = threadIdx.x & 31, r = lane >> 2, qd = lane & 3;
+    const int warps = gridDim.x * (kFewThreads / 32);
+    const int me = blockIdx.x * (kFewThreads / 32) + (threadIdx.x >> 5);
+    const int Hkv = p.num_kv_heads, Hq = p.num_heads, G = Hq / Hkv, n = p.num_seqs;
+    const int T16 = p.max_blocks * kBlockSize, cols = p.few_cols;
+    grid_dependents_launch();
+    grid_dependency_wait();
+    ragged_prefix<kFewThreads>(sm, 0, n, [&](int s) {
+        return few_units(mass_seq(p, s, p.few_tokens, blockIdx.x == 0));
+    });
+    const long long total = (long long)sm.pre[n] * Hkv;
+    const long long share = (total + warps - 1) / warps;
+    long long u = me * share;
+    const long long end = min(total, u + share);
+    if (u >= end)
+        return;
+    int i = ragged_find(sm, n, (int)(u / Hkv));
+    int nu = sm.pre[i + 1] - sm.pre[i];
+    int h = (int)((u - (long long)sm.pre[i] * Hkv) / nu);
+    int t = (int)((u - (long long)sm.pre[i] * Hkv) % nu);
+    MassSeq x = mass_seq(p, i, p.few_tokens, false);
+    // the pool tiles of blocks 2 t and 2 t + 1; past the end the last block again
+    auto tiles_of = [&](int (&tile)[2]) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            int phys = __ldg(p.block_tables + (size_t)i * p.max_blocks +
+                             min(2 * t + a, (x.L - 1) / kBlockSize));
+            if ((unsigned)phys >= (unsigned)p.num_blocks) {
+                record_error(p.err, PA_DEVERR_TABLE_RANGE);
+                phys = 0;
+            }
+            tile[a] = phys * Hkv + h;
+        }
+    };
+    const T *kp = static_cast<const T *>(p.k_cache);
+    uint4 q[NT][NI];
+    int lim[NT][2];                               // the last key that this lane's columns see
+    float m[NT][2], l[NT][2];
+    bool fresh = true;
+    int tile[2], next[2] = {0, 0};
+    tiles_of(tile);
+    for (; u < end; ++u) {
+        const int run = i * Hkv + h, L = x.L, key0 = kFewKeys * t;
+        if (fresh) {
+            const int rows = x.c * G;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int row = 8 * j + r;
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    static_cast<const T *>(p.q) +
+                    ((size_t)(x.qs + (row < rows ? row / G : 0)) * Hq + h * G + row % G) * D) + qd;
+#pragma unroll
+                for (int k = 0; k < NI; ++k)
+                    q[j][k] = row < rows ? __ldg(src + 4 * k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int col = 8 * j + 2 * qd + e;
+                    lim[j][e] = col < rows ? L - x.c + col / G : -1;
+                    m[j][e] = -INFINITY;
+                    l[j][e] = 0.f;
+                }
+            }
+            fresh = false;
+        }
+        uint4 k4[2][2][NI];                       // [block][rows r, r + 8]
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int k = 0; k < NI; ++k)
+                    k4[b][a][k] = __ldg(reinterpret_cast<const uint4 *>(
+                                            kp + ((size_t)tile[b] * kBlockSize + r + 8 * a) * D) +
+                                        4 * k + qd);
+        bool leave = false;                       // the piece ends
+        if (++t == nu) {
+            t = 0;
+            leave = true;
+            if (++h == Hkv) {
+                h = 0;
+                do
+                    ++i;
+                while (i < n && sm.pre[i + 1] == sm.pre[i]);
+                if (i < n) {
+                    nu = sm.pre[i + 1] - sm.pre[i];
+                    x = mass_seq(p, i, p.few_tokens, false);
+                }
+            }
+        }
+        if (u + 1 < end) {
+            tiles_of(next);
+            // the next 32 keys on their way to L2: two lines a lane
+            constexpr int LINES = kBlockSize * D * 2 / 128;
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+                for (int o = lane; o < LINES; o += 32)
+                    prefetch_l2(kp + (size_t)next[a] * kBlockSize * D + 64 * o);
+        }
+        float s4[2][NT][4];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    s4[b][j][e] = 0.f;
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int k = 0; k < NI; ++k) {
+                const uint4 &y = k4[b][0][k], &z = k4[b][1][k];
+                const uint32_t a0[4] = {y.x, z.x, y.y, z.y}, a1[4] = {y.z, z.z, y.w, z.w};
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    M::run(s4[b][j], a0, q[j][k].x, q[j][k].y);
+                    M::run(s4[b][j], a1, q[j][k].z, q[j][k].w);
+                }
+            }
+        float *dst = p.sums + ((size_t)run * T16 + key0 + r) * cols + 2 * qd;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                // (row r, columns 2 qd and + 1), (row r + 8, the same)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    s4[b][j][e] = key0 + 16 * b + r + 8 * (e >> 1) <= lim[j][e & 1]
+                                      ? s4[b][j][e] * p.scale_log2
+                                      : -INFINITY;
+                if (8 * j + 2 * qd < cols && key0 + 16 * b < L) {
+                    float *at = dst + (size_t)(16 * b) * cols + 8 * j;
+                    *reinterpret_cast<float2 *>(at) = make_float2(s4[b][j][0], s4[b][j][1]);
+                    *reinterpret_cast<float2 *>(at + 8 * cols) =
+                        make_float2(s4[b][j][2], s4[b][j][3]);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float y0 = s4[0][j][e], y1 = s4[0][j][2 + e], y2 = s4[1][j][e],
+                            y3 = s4[1][j][2 + e];
+                const float mx = fmaxf(fmaxf(y0, y1), fmaxf(y2, y3));
+                if (mx > m[j][e]) {
+                    l[j][e] *= ex2_approx(m[j][e] - mx);
+                    m[j][e] = mx;
+                }
+                const float mr = m[j][e] == -INFINITY ? 0.f : m[j][e];
+                l[j][e] += (ex2_approx(y0 - mr) + ex2_approx(y1 - mr)) +
+                           (ex2_approx(y2 - mr) + ex2_approx(y3 - mr));
+            }
+        }
+        if (leave || u + 1 == end) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float top = m[j][e];
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1)
+                        top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
+                    float sum = top > -INFINITY ? l[j][e] * ex2_approx(m[j][e] - top) : 0.f;
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1)
+                        sum += __shfl_xor_sync(FULL, sum, o);
+                    if (r == 0)
+                        p.stats[(size_t)(run + me) * kMassFewRows + 8 * j + 2 * qd + e] =
+                            make_float2(top, sum);
+                }
+            fresh = true;
+        }
+        tile[0] = next[0];
+        tile[1] = next[1];
+    }
+}
+
+// The weights from the kept scores: a block 1024 tokens of a (sequence, kv head), whose
+// pieces' statistics its threads fold first; a warp 128 of them, four a lane.
+__global__ void __launch_bounds__(kMassFinishThreads)
+prefill_mass_few_finish_kernel(const PrefillMassParams p)
+{
+    constexpr int NTH = kMassFinishThreads, TOK = NTH / 32 * 128, ROWS = kMassFewRows;
+    constexpr int PARTS = NTH / ROWS;
+    __shared__ RaggedSmem units, blocks;
+    __shared__ float2 part[PARTS][ROWS], fin[ROWS];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int Hkv = p.num_kv_heads, G = p.num_heads / Hkv, n = p.num_seqs, cols = p.few_cols;
+    const int T16 = p.max_blocks * kBlockSize;
+    grid_dependents_launch();
+    grid_dependency_wait();
+    ragged_prefix<NTH>(units, 0, n, [&](int s) {
+        return few_units(mass_seq(p, s, p.few_tokens, false));
+    });
+    ragged_prefix<NTH>(blocks, 0, n, [&](int s) {
+        const MassSeq x = mass_seq(p, s, p.few_tokens, false);
+        return x.blocks ? (x.L + TOK - 1) / TOK : 0;
+    });
+    const long long all = (long long)units.pre[n] * Hkv;
+    const long long share = (all + p.few_warps - 1) / p.few_warps;
+    const long long total = (long long)blocks.pre[n] * Hkv;
+    for (long long u = blockIdx.x; u < total; u += gridDim.x) {
+        const int i = ragged_find(blocks, n, (int)(u / Hkv));
+        const int nt = blocks.pre[i + 1] - blocks.pre[i];
+        const int at = (int)(u - (long long)blocks.pre[i] * Hkv);
+        const int h = at / nt, t0 = at % nt * TOK + 128 * warp + lane;
+        const MassSeq x = mass_seq(p, i, p.few_tokens, false);
+        const int run = i * Hkv + h, rows = x.c * G;
+        // the old masses and the first scores while the statistics meet
+        float *mass = p.mass + (size_t)run * T16 + t0;
+        const float2 *y = reinterpret_cast<const float2 *>(p.sums + ((size_t)run * T16 + t0) * cols);
+        float old[4], sum[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            old[k] = t0 + 32 * k < x.L - x.c && p.decay != 0.f ? __ldcg(mass + 32 * k) : 0.f;
+            sum[k] = 0.f;
+        }
+        // ---- the pieces' statistics ----
+        const int nu = units.pre[i + 1] - units.pre[i];
+        const long long first = (long long)units.pre[i] * Hkv + (long long)h * nu;
+        const int p0 = (int)(first / share), p1 = (int)((first + nu - 1) / share);
+        const int col = tid % ROWS;
+        float m = -INFINITY, l = 0.f;
+        if (col < rows)
+            for (int j = p0 + tid / ROWS; j <= p1; j += PARTS) {
+                const float2 z = __ldcg(p.stats + (size_t)(run + j) * ROWS + col);
+                const float nm = fmaxf(m, z.x);
+                if (nm > -INFINITY)
+                    l = l * exp2f(m - nm) + z.y * exp2f(z.x - nm);
+                m = nm;
+            }
+        part[tid / ROWS][col] = make_float2(m, l);
+        __syncthreads();
+        if (tid < ROWS) {
+            float top = -INFINITY, s = 0.f;
+#pragma unroll
+            for (int j = 0; j < PARTS; ++j)
+                top = fmaxf(top, part[j][tid].x);
+#pragma unroll
+            for (int j = 0; j < PARTS; ++j)
+                s += part[j][tid].x > -INFINITY ? part[j][tid].y * exp2f(part[j][tid].x - top) : 0.f;
+            fin[tid] = tid < rows ? make_float2(top, 1.f / s) : make_float2(0.f, 0.f);
+        }
+        __syncthreads();
+        // ---- the sums ----
+        for (int g = 0; g < cols; g += 4) {
+            float2 v[4][2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    v[k][e] = t0 + 32 * k < x.L && g + 2 * e < cols
+                                  ? __ldcg(y + (16 * k * cols + g / 2 + e))
+                                  : make_float2(-INFINITY, -INFINITY);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float2 a = fin[min(g + 2 * e, ROWS - 2)], b = fin[min(g + 2 * e, ROWS - 2) + 1];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    sum[k] = fmaf(ex2_approx(v[k][e].x - a.x), a.y,
+                                  fmaf(ex2_approx(v[k][e].y - b.x), b.y, sum[k]));
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (t0 + 32 * k < x.L)
+                mass[32 * k] = fmaf(old[k], p.decay, sum[k]);
+        __syncthreads();                          // part and fin are written again
+    }
+}
+
+// ---------------------------------------------------------------------------
 // The same for short sequences in one launch: a thread block takes a (sequence,
 // kv head) whole, its warps 16 (token, head) rows at a time with mma.sync.  The
 // channels of a product may be taken in any order, so rows of q and k are
@@ -1077,6 +1370,9 @@ void fill(MassKernels *k)
     k->stats = reinterpret_cast<const void *>(&prefill_mass_kernel<T, D, false>);
     k->sums = reinterpret_cast<const void *>(&prefill_mass_kernel<T, D, true>);
     k->whole = reinterpret_cast<const void *>(&prefill_mass_short_kernel<T, D>);
+    k->few[0] = reinterpret_cast<const void *>(&prefill_mass_few_kernel<T, D, 1>);
+    k->few[1] = reinterpret_cast<const void *>(&prefill_mass_few_kernel<T, D, 2>);
+    k->few_finish = reinterpret_cast<const void *>(&prefill_mass_few_finish_kernel);
     k->threads = MassShape<D, false>::THREADS;
     k->smem_stats = MassShape<D, false>::SMEM;
     k->smem_sums = MassShape<D, true>::SMEM;

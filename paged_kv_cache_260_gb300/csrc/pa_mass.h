@@ -32,6 +32,9 @@ struct PrefillMassParams {
     int num_seqs, num_heads, num_kv_heads, max_blocks, num_blocks;
     int num_queries;               // rows of q
     int row_blocks;                // units of 2 x 128 (token, head) rows per (sequence, kv head)
+    // few rows: columns of the kept scores (in sums, [run][max_blocks * 16][columns]), the longest
+    // chunk, the first kernel's warps; stats are [run + warp][kMassFewRows]
+    int few_cols, few_tokens, few_warps;
     float scale_log2, decay;
 };
 
@@ -52,9 +55,14 @@ constexpr int kMassShortKeys = 512;
 constexpr long long kMassShortWork = 1 << 20, kMassShortWorkOfBlocks = 3 << 20;
 constexpr int kMassShortThreads = 512;
 
+// Chunks of at most this many (token, head) rows a kv head keep their scores.
+constexpr int kMassFewRows = 16;
+constexpr int kMassFewThreads = 128;
+
 struct MassKernels {
     const void *stats, *sums;      // (PrefillMassParams, tensor map of the key pool)
     const void *whole;             // (PrefillMassParams): short sequences
+    const void *few[2], *few_finish;       // (PrefillMassParams): up to 8 and 16 rows
     int threads;
     size_t smem_stats, smem_sums;
 };

@@ -7,10 +7,6 @@
 
 namespace pa {
 
-// Sequences whose unit counts a block holds at a time; larger batches are
-// walked in parts of this many.
-constexpr int kRaggedSeqs = 2048;
-
 struct RaggedSmem {
     int32_t pre[kRaggedSeqs + 1];  // units of the part's sequences before this one
     int32_t warp_sum[32];

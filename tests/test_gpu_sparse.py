@@ -494,6 +494,59 @@ def test_prefill_mass_in_one_launch(pa, keys, rows, g, dt, d):
                longest=rows)
 
 
+@pytest.mark.parametrize("c,g", [(1, 1), (1, 4), (2, 4), (3, 1), (1, 7), (5, 3), (4, 4), (2, 8),
+                                 (1, 16), (16, 1), (3, 5)])
+@pytest.mark.parametrize("dt,d", [("bf16", 128), ("f16", 64)])
+@pytest.mark.parametrize("decay", [1.0, 0.0])
+def test_prefill_mass_of_few_rows(pa, c, g, dt, d, decay):
+    # chunks of at most 16 rows over keys that are read once
+    lens = [3000, 0, 17, 640, 1, 5000, 33, 1024, 1025]
+    chunks = [c, 0, min(c, 17), 1, 1, min(c, 2), 0, c, c]
+    chunk_case(pa, gen(56, c, g), lens, chunks, dt, d, 3, g, decay, longest=c, lead=2)
+
+
+def test_prefill_mass_of_few_rows_and_many_runs(pa):
+    r = gen(57)
+    lens = [int(x) for x in torch.randint(0, 700, (500,), generator=r)]
+    lens[-3] = 900
+    chunk_case(pa, r, lens, [min(n, 2) for n in lens], "bf16", 64, 2, 3, 0.9, longest=2)
+    lens = [int(x) for x in torch.randint(0, 40, (2100,), generator=r)]
+    lens[-3] = 800                                     # more sequences than the form takes
+    chunk_case(pa, r, lens, [min(n, 2) for n in lens], "f16", 64, 1, 2, 0.9, longest=2)
+
+
+def test_prefill_mass_of_few_rows_reports_bad_arguments(pa):
+    r = gen(58)
+    lens = [1000, 1000]
+    tables, nb = su.tables_for(r, lens)
+    k = su.pool(r, nb, 1, 64, torch.float16)
+    q = torch.randn(8, 4, 64, generator=r).half()
+    old = torch.rand(2, 1, 1008, generator=r)
+    kk, qq, tt = cuda(k, q, tables)
+
+    def run(lens, start, longest, want, tables=tt):
+        mm = old.cuda()
+        pa.prefill_mass(mm, qq, kk, tables, *cuda(lens, start), longest, 0.125)
+        check(pa, want)
+        return mm.cpu()
+
+    ref, bits = run(lens, [0, 2, 4], 2, 0), pa.DEVERR
+    good, tol = su.prefill_mass(q, old, k, tables, lens, [0, 2, 4], 0.125, 1.0)
+    su.mass_close(ref, good, tol)
+    for a, b, e in (([1000, 1], [0, 2, 4], bits["QUERY_RANGE"]),
+                    ([1000, 1009], [0, 2, 4], bits["SEQLEN_RANGE"]),
+                    ([1000, -1], [0, 2, 4], bits["SEQLEN_RANGE"]),
+                    (lens, [0, 2, 1], bits["QUERY_RANGE"]),
+                    (lens, [0, 2, 9], bits["QUERY_RANGE"]),
+                    (lens, [0, 2, 6], bits["QUERY_RANGE"])):
+        got = run(a, b, 2, e)
+        assert torch.equal(got[1], old[1]) and torch.equal(got[0], ref[0])
+    bad, zero = tables.clone(), tables.clone()
+    bad[1, 20], zero[1, 20] = nb, 0
+    assert torch.equal(run(lens, [0, 2, 4], 2, bits["TABLE_RANGE"], bad.cuda()),
+                       run(lens, [0, 2, 4], 2, 0, zero.cuda()))
+
+
 @pytest.mark.parametrize("lens,chunks,g", [([5000], [64], 4), ([3000, 200], [700, 1], 2),
                                            ([1, 1], [1, 1], 4), ([2049], [2049], 1),
                                            ([9000, 130, 17], [1, 33, 17], 8)])

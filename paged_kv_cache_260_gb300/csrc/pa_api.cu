@@ -1727,8 +1727,9 @@ static bool prefill_mass_plan(int num_seqs, int max_query_len, int num_heads, in
     w->units = (long long)num_seqs * num_kv_heads * w->row_blocks;
     w->tiles = w->units * (((long long)max_blocks * kBlockSize + kMassKeys - 1) / kMassKeys);
     const long long rows = (long long)max_query_len * (num_heads / num_kv_heads);
-    if (rows <= kMassFewRows && num_seqs <= kRaggedSeqs) {
-        const long long runs = (long long)num_seqs * num_kv_heads;
+    const long long runs = (long long)num_seqs * num_kv_heads;
+    if (rows <= kMassFewRows && num_seqs <= kRaggedSeqs &&
+        runs * max_blocks * kBlockSize * score_cols((int)rows) <= kMassFewScores) {
         w->few_cols = score_cols((int)rows);
         w->few_warps = num_sms * (rows <= 8 ? 4 : 3) * (kMassFewThreads / 32);
         w->sums_off = round_up(sizeof(float2) * (size_t)(runs + w->few_warps) * kMassFewRows, 256);
@@ -1812,7 +1813,8 @@ int pa_prefill_mass(const struct pa_sparse_args *args)
     cudaStream_t st = static_cast<cudaStream_t>(a.stream);
     void *fargs[] = {&p};
     const long long keys = (long long)a.max_blocks_per_seq * kBlockSize;
-    if (keys <= kMassShortKeys &&
+    const bool many = w.few_cols && a.num_seqs * a.num_kv_heads > ds->num_sms;
+    if (!many && keys <= kMassShortKeys &&
         keys * a.head_dim * a.max_query_len * (a.num_heads / a.num_kv_heads) <=
             (w.row_blocks == 1 ? kMassShortWork : kMassShortWorkOfBlocks))
         return launch_dependent(k.whole, dim3((unsigned)a.num_seqs * a.num_kv_heads),

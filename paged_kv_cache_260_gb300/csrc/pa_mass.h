@@ -55,8 +55,15 @@ constexpr int kMassShortKeys = 512;
 constexpr long long kMassShortWork = 1 << 20, kMassShortWorkOfBlocks = 3 << 20;
 constexpr int kMassShortThreads = 512;
 
-// Chunks of at most this many (token, head) rows a kv head keep their scores.
+// Chunks of at most this many (token, head) rows a kv head keep their scores (4 bytes a row
+// and key beside 2 head_dim).  us in a graph, kept scores / the passes, 8 kv heads x 128: 8 x 16K
+// keys 4 rows 57 / 108, 8 rows 63 / 108, 16 rows 79 / 109 (32 would write as many bytes as they
+// read); 4 x 2048 keys 4 rows 10.1 / 18.0, 16 rows 12.6 / 18.1.  Against the one launch: 512
+// runs of 512 keys 16.7 / 38.5, of 32 keys 10.8 / 24.9; up to an SM's run it is as fast or
+// faster: 32 runs of 128 keys 7.8 / 8.8, of 32 keys 7.4 / 6.9, 128 runs of 128 keys 9.7 / 8.8, 16
+// rows of 512 keys 13.6 / 10.3.
 constexpr int kMassFewRows = 16;
+constexpr long long kMassFewScores = 1 << 28;      // a gigabyte of workspace
 constexpr int kMassFewThreads = 128;
 
 struct MassKernels {

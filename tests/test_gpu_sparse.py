@@ -515,6 +515,12 @@ def test_prefill_mass_of_few_rows_and_many_runs(pa):
     chunk_case(pa, r, lens, [min(n, 2) for n in lens], "f16", 64, 1, 2, 0.9, longest=2)
 
 
+def test_prefill_mass_of_few_rows_in_very_wide_tables(pa):
+    # scores of all places of the tables would be more than a gigabyte: not kept
+    chunk_case(pa, gen(59), [500, 40], [4, 4], "f16", 64, 3, 4, 1.0, mb=180000)
+    chunk_case(pa, gen(60), [500, 40], [4, 4], "f16", 64, 3, 4, 1.0, mb=170000)
+
+
 def test_prefill_mass_of_few_rows_reports_bad_arguments(pa):
     r = gen(58)
     lens = [1000, 1000]

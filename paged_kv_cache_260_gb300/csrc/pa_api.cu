@@ -470,6 +470,9 @@ struct DecodeExtra {
     const float *lambda = nullptr;
     const void *norm_w = nullptr;
     float norm_eps = 0.f, out_scale = 1.f;
+    // few long runs may be merged by a block per run and head (pa_decode keeps the merge whose
+    // results it had: the order of the sums differs)
+    bool wide = false;
     // weight accounting: where the scores and statistics go, non-null
     float *scores = nullptr;
     float2 *stat = nullptr;
@@ -685,7 +688,7 @@ static int decode_impl(void *out, const void *q, const void *k_cache, const void
     // merge as well.
     const long long runs = (long long)num_seqs * num_kv_heads;
     const long long waves = (runs * group + ds->num_sms - 1) / ds->num_sms;
-    if (ks.merge_wide && kWidePieces * waves * runs <= workers &&
+    if (x.wide && kWidePieces * waves * runs <= workers &&
         kWidePieces * waves * kMinTiles <= max_blocks_per_seq)
         return launch_dependent(ks.merge_wide, dim3((unsigned)runs, group), dim3(32 * kWideWarps),
                                 0, st, margs);
@@ -742,6 +745,7 @@ int pa_diff_decode(void *out, const void *q, const void *k_cache, const void *v_
     // an empty batch has no factors to read, but its other arguments are checked as ever
     static const float none = 0.f;
     DecodeExtra x;
+    x.wide = true;
     x.lambda = lambda ? lambda : &none;
     x.norm_w = norm_weight;
     x.norm_eps = norm_eps;
@@ -1618,10 +1622,12 @@ int pa_sparse_decode(const struct pa_sparse_args *args)
         return rc;
     if (a.num_seqs > 0 && a.out && a.out == a.q)
         return PA_ERR_INVALID_ARG;
+    DecodeExtra x;
+    x.wide = true;
     return decode_impl(a.out, a.q, a.k_cache, a.v_cache, a.tiles, a.tile_lens,
                        a.num_seqs * a.num_kv_heads, a.num_heads / a.num_kv_heads, 1, a.head_dim,
                        a.block_size, a.keep, a.num_blocks * a.num_kv_heads, (float)a.scale, a.dtype,
-                       0, a.workspace, a.workspace_bytes, a.stream, DecodeExtra{});
+                       0, a.workspace, a.workspace_bytes, a.stream, x);
 }
 
 // Workspace of pa_decode_mass: the decode's own, the statistics, the scores.
@@ -1681,6 +1687,7 @@ int pa_decode_mass(const struct pa_sparse_args *args)
         return rc;
     char *ws = static_cast<char *>(a.workspace);
     DecodeExtra x;
+    x.wide = true;
     x.stat = reinterpret_cast<float2 *>(ws + w.stat_off);
     x.scores = reinterpret_cast<float *>(ws + w.score_off);
     rc = decode_impl(a.out, a.q, a.k_cache, a.v_cache, a.block_tables, a.seq_lens, a.num_seqs,

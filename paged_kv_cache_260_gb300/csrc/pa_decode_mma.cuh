@@ -1155,20 +1155,24 @@ __global__ void __launch_bounds__(32 * kMaxGroup) merge_cut_diff_kernel(const De
     diff_row<T, D>(p, acc, Ws, s, h * G + g, lane);
 }
 
-// The same for few long runs, each cut into many pieces: a block per run and head,
-// its warps taking a share of the pieces each.  The pieces' maxima and sums come
+// The merge of few long runs, each cut into many pieces (of differential attention, and
+// of decodes over selected tiles or that keep account of the weights): a block per run and
+// head, its warps taking a share of the pieces each.  The pieces' maxima and sums come
 // first, a lane a piece, then their results with the weights known, V channels a
 // lane and CH pieces in flight; warp 0 joins the shares.  One warp for all pieces
 // of a head: one sequence of 32K tokens, 32/8 heads x 128, 52.3 us a decode against
-// 27.8; 100K tokens, 16/1 heads, 332 against 39.4.
-template <typename T, int D>
-__global__ void __launch_bounds__(32 * kWideWarps) merge_wide_diff_kernel(const DecodeParams p)
+// 27.8; 100K tokens, 16/1 heads, 332 against 39.4 (differential); a selection of 256
+// blocks, 32/8 heads x 128, 29.0 against 11.8; one sequence of 131K tokens, 8/1 heads x
+// 128, with account of the weights 195 against 32.
+template <typename T, int D, bool DIFF>
+__global__ void __launch_bounds__(32 * kWideWarps) merge_wide_kernel(const DecodeParams p)
 {
+    constexpr int A = DIFF ? 2 : 1;               // maps of a head
     constexpr int V = D / 32;
     constexpr int CH = 8;
     constexpr uint32_t FULL = 0xffffffffu;
     constexpr int SHARE = D + 2;                  // D results, maximum, sum
-    __shared__ float share[kWideWarps * 2 * SHARE];        // [warp][map]
+    __shared__ float share[kWideWarps * A * SHARE];        // [warp][map]
     __shared__ int found;                         // the run's first worker
     grid_dependents_launch();
     grid_dependency_wait();
@@ -1194,15 +1198,15 @@ __global__ void __launch_bounds__(32 * kWideWarps) merge_wide_diff_kernel(const 
     const int n = npieces * (warp + 1) / kWideWarps - first;
 
     auto piece_row = [&](int i, int a) {          // piece i of this warp's, map a
-        return slot_row(2 * G, cut_piece_slot(c0 + first + i, c0, u0 != c0 * R), a * G + g);
+        return slot_row(A * G, cut_piece_slot(c0 + first + i, c0, u0 != c0 * R), a * G + g);
     };
-    float ov[CH][2][V];
+    float ov[CH][A][V];
     auto load = [&](int base) {
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             if (base + i < n) {
 #pragma unroll
-                for (int a = 0; a < 2; ++a) {
+                for (int a = 0; a < A; ++a) {
                     const float *src = p.ws_so + piece_row(base + i, a) * D + lane * V;
                     if constexpr (V == 4) {
                         const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
@@ -1216,10 +1220,10 @@ __global__ void __launch_bounds__(32 * kWideWarps) merge_wide_diff_kernel(const 
         }
     };
     // maxima and sums of pieces base + lane (none: -inf, 0)
-    float mv[2], lv[2];
+    float mv[A], lv[A];
     auto load_ml = [&](int base) {
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
+        for (int a = 0; a < A; ++a) {
             mv[a] = -INFINITY;
             lv[a] = 0.f;
             if (base + lane < n) {
@@ -1231,25 +1235,32 @@ __global__ void __launch_bounds__(32 * kWideWarps) merge_wide_diff_kernel(const 
     };
     load_ml(0);
     load(0);
-    float Mx[2] = {mv[0], mv[1]}, Ws[2] = {0.f, 0.f}, acc[2][V];
+    float Mx[A], Ws[A], acc[A][V];
+#pragma unroll
+    for (int a = 0; a < A; ++a) {
+        Mx[a] = mv[a];
+        Ws[a] = 0.f;
+    }
     for (int i = 32 + lane; i < n; i += 32)
 #pragma unroll
-        for (int a = 0; a < 2; ++a)
+        for (int a = 0; a < A; ++a)
             Mx[a] = fmaxf(Mx[a], __ldcg(p.ws_sm + piece_row(i, a)));
 #pragma unroll
-    for (int off = 16; off; off >>= 1) {
-        Mx[0] = fmaxf(Mx[0], __shfl_xor_sync(FULL, Mx[0], off));
-        Mx[1] = fmaxf(Mx[1], __shfl_xor_sync(FULL, Mx[1], off));
-    }
+    for (int off = 16; off; off >>= 1)
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-        acc[0][v] = acc[1][v] = 0.f;
+        for (int a = 0; a < A; ++a)
+            Mx[a] = fmaxf(Mx[a], __shfl_xor_sync(FULL, Mx[a], off));
+#pragma unroll
+    for (int a = 0; a < A; ++a)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            acc[a][v] = 0.f;
     for (int base = 0; base < n; base += 32) {
         if (base)
             load_ml(base);
-        float b[2];
+        float b[A];
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
+        for (int a = 0; a < A; ++a) {
             b[a] = mv[a] == -INFINITY ? lv[a]     // zero, or NaN if a score was
                                       : lv[a] * exp2f((mv[a] - Mx[a]) * kLog2e);
             Ws[a] += b[a];
@@ -1259,26 +1270,26 @@ __global__ void __launch_bounds__(32 * kWideWarps) merge_wide_diff_kernel(const 
                 load(at);
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
-                const float w0 = __shfl_sync(FULL, b[0], at - base + i);
-                const float w1 = __shfl_sync(FULL, b[1], at - base + i);
-                if (at + i < n) {
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        acc[0][v] = fmaf(w0, ov[i][0][v], acc[0][v]);
-                        acc[1][v] = fmaf(w1, ov[i][1][v], acc[1][v]);
+                for (int a = 0; a < A; ++a) {
+                    const float w = __shfl_sync(FULL, b[a], at - base + i);
+                    if (at + i < n) {
+#pragma unroll
+                        for (int v = 0; v < V; ++v)
+                            acc[a][v] = fmaf(w, ov[i][a][v], acc[a][v]);
                     }
                 }
             }
         }
     }
 #pragma unroll
-    for (int off = 16; off; off >>= 1) {
-        Ws[0] += __shfl_xor_sync(FULL, Ws[0], off);
-        Ws[1] += __shfl_xor_sync(FULL, Ws[1], off);
-    }
-    float *mine = share + warp * 2 * SHARE;
+    for (int off = 16; off; off >>= 1)
 #pragma unroll
-    for (int a = 0; a < 2; ++a) {
+        for (int a = 0; a < A; ++a)
+            Ws[a] += __shfl_xor_sync(FULL, Ws[a], off);
+    float *mine = share + warp * A * SHARE;
+#pragma unroll
+    for (int a = 0; a < A; ++a) {
 #pragma unroll
         for (int v = 0; v < V; ++v)
             mine[a * SHARE + lane * V + v] = acc[a][v];
@@ -1291,9 +1302,9 @@ __global__ void __launch_bounds__(32 * kWideWarps) merge_wide_diff_kernel(const 
     if (warp)
         return;
     for (int q = 1; q < kWideWarps; ++q) {
-        const float *from = share + q * 2 * SHARE;
+        const float *from = share + q * A * SHARE;
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
+        for (int a = 0; a < A; ++a) {
             const float m = from[a * SHARE + D], nM = fmaxf(Mx[a], m);
             const float f = Mx[a] == -INFINITY ? 1.f : exp2f((Mx[a] - nM) * kLog2e);
             const float e = m == -INFINITY ? 1.f : exp2f((m - nM) * kLog2e);
@@ -1304,7 +1315,18 @@ __global__ void __launch_bounds__(32 * kWideWarps) merge_wide_diff_kernel(const 
             Mx[a] = nM;
         }
     }
-    diff_row<T, D>(p, acc, Ws, s, h * G + g, lane);
+    if constexpr (DIFF) {
+        diff_row<T, D>(p, acc, Ws, s, h * G + g, lane);
+    } else {
+        const size_t head = (size_t)s * Hq + h * G + g;
+        const float inv = 1.f / Ws[0];
+        if (p.stat && lane == 0)
+            p.stat[head] = make_float2(Mx[0] * kLog2e, inv);
+        uint32_t *d32 = reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + head * D + lane * V);
+#pragma unroll
+        for (int v = 0; v < V; v += 2)
+            d32[v / 2] = Mma<T>::pack(acc[0][v] * inv, acc[0][v + 1] * inv);
+    }
 }
 
 template <typename T, int D, int NT>
@@ -1327,7 +1349,7 @@ inline void fill_diff_kernel_set(KernelSet *ks)
     ks->prep = reinterpret_cast<const void *>(&decode_prep_kernel<kPrepThreads>);
     ks->prep_fix = reinterpret_cast<const void *>(&decode_prep_fix_kernel<kPrepThreads>);
     ks->merge_cut = reinterpret_cast<const void *>(&merge_cut_diff_kernel<T, D>);
-    ks->merge_wide = reinterpret_cast<const void *>(&merge_wide_diff_kernel<T, D>);
+    ks->merge_wide = reinterpret_cast<const void *>(&merge_wide_kernel<T, D, true>);
 }
 
 template <typename T, int D>
@@ -1374,6 +1396,7 @@ inline void fill_kernel_set(KernelSet *ks)
     ks->prep_fix = reinterpret_cast<const void *>(&decode_prep_fix_kernel<kPrepThreads>);
     ks->merge_cut = reinterpret_cast<const void *>(&merge_cut_kernel<T, D>);
     ks->merge_part = reinterpret_cast<const void *>(&merge_part_kernel<T, D>);
+    ks->merge_wide = reinterpret_cast<const void *>(&merge_wide_kernel<T, D, false>);
 }
 
 // The decode of pa_decode_mass: the same kernels, leaving scores and statistics.  The scores are 4
@@ -1391,6 +1414,7 @@ inline void fill_mass_kernel_set(KernelSet *ks)
     ks->prep = reinterpret_cast<const void *>(&decode_prep_kernel<kPrepThreads>);
     ks->prep_fix = reinterpret_cast<const void *>(&decode_prep_fix_kernel<kPrepThreads>);
     ks->merge_cut = reinterpret_cast<const void *>(&merge_cut_kernel<T, D>);
+    ks->merge_wide = reinterpret_cast<const void *>(&merge_wide_kernel<T, D, false>);
 }
 
 template <typename T>

@@ -90,7 +90,7 @@ struct KernelSet {
     const void *prep;        // large batches: build the per-sequence arrays in the workspace,
     const void *prep_fix;    //   block by block, then add the earlier blocks' unit counts
     const void *merge_cut;   // combines the pieces of cut units
-    const void *merge_wide;  // the same with a block per run and head (or null)
+    const void *merge_wide;  // the same with a block per run and head
     const void *merge_part;  // fixed mode: merges partitions into the output
 };
 

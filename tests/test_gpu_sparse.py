@@ -382,7 +382,12 @@ def mass_case(pa, r, lens, dt, d, hkv, g, decay, mb=None, q_gain=2.0, scale=None
             assert bool(torch.isfinite(mm[i, :, :m]).all())
     plain = torch.empty_like(out)
     pa.decode(plain, qq, kk, vv, tt, ll, scale)
-    assert torch.equal(su.bits(plain), su.bits(out))
+    # the plain decode's sums, but for few long runs, whose pieces are added in another order
+    # (never in a table of less than 44 blocks, two for each of 22 pieces)
+    if tables.shape[1] < 44:
+        assert torch.equal(su.bits(plain), su.bits(out))
+    else:
+        su.close(plain, ref[0], ref[1], "plain")
 
 
 @pytest.mark.parametrize("dt,d,hkv,g", [("f16", 64, 8, 1), ("bf16", 128, 2, 4), ("f16", 128, 1, 5),
@@ -397,6 +402,29 @@ def test_decode_mass(pa, dt, d, hkv, g, decay):
                                      ([100] * 20, 8), ([127, 128, 1], 8)])
 def test_decode_mass_cut_and_whole(pa, lens, mb):
     mass_case(pa, gen(17, len(lens)), lens, "bf16", 128, 2, 4, 1.0, mb)
+
+
+@pytest.mark.parametrize("dt,d,hkv,g", [("f16", 64, 1, 1), ("bf16", 64, 3, 7), ("f16", 128, 1, 16),
+                                        ("bf16", 128, 2, 2)])
+@pytest.mark.parametrize("lens", [[30000], [5000, 40, 0, 9000]])
+def test_decode_mass_of_few_long_sequences(pa, dt, d, hkv, g, lens):
+    mass_case(pa, gen(61, d, g), lens, dt, d, hkv, g, 0.9)
+
+
+@pytest.mark.parametrize("dt,d,hkv,g,n,keep", [("bf16", 128, 1, 8, 1, 2000), ("f16", 64, 2, 3, 2, 900),
+                                               ("bf16", 64, 1, 16, 3, 700),
+                                               ("f16", 128, 4, 1, 2, 500)])
+def test_sparse_decode_of_few_long_lists(pa, dt, d, hkv, g, n, keep):
+    r = gen(62, keep)
+    k, v = (su.pool(r, 300, hkv, d, DT[dt]) for _ in range(2))
+    held = torch.randint(8 * keep, 16 * keep + 1, (n, hkv), generator=r).int()
+    held[-1, -1] = 5 if n > 1 else held[-1, -1]
+    tiles = random_tiles(r, n, hkv, keep, 300, held)
+    q = torch.randn(n, hkv * g, d, generator=r).to(DT[dt])
+    ref, tol = su.sparse_decode(q, k, v, tiles, held, SCALE[d])
+    out = pa.sparse_decode(torch.empty_like(q).cuda(), *cuda(q, k, v, tiles, held), SCALE[d])
+    check(pa)
+    su.close(out, ref, tol)
 
 
 def test_decode_mass_of_many_sequences(pa):

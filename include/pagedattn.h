@@ -604,7 +604,8 @@ int pa_decode_mass(const struct pa_sparse_args *args);
  * A chunk that is negative, longer than its sequence or than max_query_len (it may be
  * taken all the same up to the next 2 * (128 / group) rows), or whose rows lie outside q
  * sets PA_DEVERR_QUERY_RANGE; that, or a bad length, leaves the sequence as it was.
- * Bad table entries read block 0.
+ * Bad table entries read block 0.  A workspace of a longer max_query_len serves shorter
+ * ones too (its own, where chunks have few rows, lets the keys be read only once).
  */
 size_t pa_prefill_mass_workspace_size(int num_seqs, int max_query_len, int num_heads,
                                       int num_kv_heads, int max_blocks_per_seq);

@@ -1719,8 +1719,9 @@ int pa_decode_mass(const struct pa_sparse_args *args)
 // Chunks of few rows keep their scores instead, with the statistics of the warps' pieces.
 struct PrefillMassPlan {
     long long row_blocks, units, tiles;
-    int few_cols, few_warps;       // 0: not the form for few rows
     size_t sums_off, total;
+    int few_cols, few_warps;       // the form for few rows, or 0
+    size_t few_off, few_total;
 };
 
 static bool prefill_mass_plan(int num_seqs, int max_query_len, int num_heads, int num_kv_heads,
@@ -1739,10 +1740,9 @@ static bool prefill_mass_plan(int num_seqs, int max_query_len, int num_heads, in
         runs * max_blocks * kBlockSize * score_cols((int)rows) <= kMassFewScores) {
         w->few_cols = score_cols((int)rows);
         w->few_warps = num_sms * (rows <= 8 ? 4 : 3) * (kMassFewThreads / 32);
-        w->sums_off = round_up(sizeof(float2) * (size_t)(runs + w->few_warps) * kMassFewRows, 256);
-        w->total = w->sums_off +
-                   sizeof(float) * (size_t)runs * max_blocks * kBlockSize * w->few_cols;
-        return true;
+        w->few_off = round_up(sizeof(float2) * (size_t)(runs + w->few_warps) * kMassFewRows, 256);
+        w->few_total = w->few_off +
+                       sizeof(float) * (size_t)runs * max_blocks * kBlockSize * w->few_cols;
     }
     w->sums_off = round_up(
         sizeof(float2) * (size_t)(w->units + num_sms) * 2 * kMassTiles * kMassRows, 256);
@@ -1761,7 +1761,7 @@ size_t pa_prefill_mass_workspace_size(int num_seqs, int max_query_len, int num_h
         !prefill_mass_plan(num_seqs, max_query_len, num_heads, num_kv_heads, max_blocks_per_seq,
                            ds->num_sms, &w))
         return 0;
-    return w.total;
+    return std::max(w.total, w.few_total);
 }
 
 int pa_prefill_mass(const struct pa_sparse_args *args)
@@ -1820,13 +1820,15 @@ int pa_prefill_mass(const struct pa_sparse_args *args)
     cudaStream_t st = static_cast<cudaStream_t>(a.stream);
     void *fargs[] = {&p};
     const long long keys = (long long)a.max_blocks_per_seq * kBlockSize;
-    const bool many = w.few_cols && a.num_seqs * a.num_kv_heads > ds->num_sms;
+    const bool many = w.few_cols && a.workspace_bytes >= w.few_total &&
+                      a.num_seqs * a.num_kv_heads > ds->num_sms;
     if (!many && keys <= kMassShortKeys &&
         keys * a.head_dim * a.max_query_len * (a.num_heads / a.num_kv_heads) <=
             (w.row_blocks == 1 ? kMassShortWork : kMassShortWorkOfBlocks))
         return launch_dependent(k.whole, dim3((unsigned)a.num_seqs * a.num_kv_heads),
                                 dim3(kMassShortThreads), 0, st, fargs);
-    if (w.few_cols) {
+    if (w.few_cols && a.workspace_bytes >= w.few_total) {
+        p.sums = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + w.few_off);
         p.few_cols = w.few_cols;
         p.few_tokens = a.max_query_len;
         p.few_warps = w.few_warps;

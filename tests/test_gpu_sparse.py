@@ -543,6 +543,25 @@ def test_prefill_mass_of_few_rows_and_many_runs(pa):
     chunk_case(pa, r, lens, [min(n, 2) for n in lens], "f16", 64, 1, 2, 0.9, longest=2)
 
 
+def test_prefill_mass_with_the_workspace_of_longer_chunks(pa):
+    r = gen(63)
+    for n, length in ((2, 3000), (200, 90)):
+        lens = [length - i % 50 for i in range(n)]
+        tables, nb = su.tables_for(r, lens)
+        k = su.pool(r, nb, 2, 64, torch.bfloat16)
+        start = [2 * i for i in range(n + 1)]
+        q = torch.randn(2 * n, 8, 64, generator=r).bfloat16()
+        mass = torch.rand(n, 2, 16 * tables.shape[1], generator=r)
+        ref, tol = su.prefill_mass(q, mass, k, tables, lens, start, 0.125, 1.0)
+        qq, kk, tt, ll, ss = cuda(q, k, tables, lens, start)
+        for longest in (2, 64, 500):
+            ws = pa.prefill_mass_workspace_for(qq, kk, tt, longest)
+            mm = mass.cuda()
+            pa.prefill_mass(mm, qq, kk, tt, ll, ss, 2, 0.125, workspace=ws)
+            check(pa)
+            su.mass_close(mm, ref, tol)
+
+
 def test_prefill_mass_of_few_rows_in_very_wide_tables(pa):
     # scores of all places of the tables would be more than a gigabyte: not kept
     chunk_case(pa, gen(59), [500, 40], [4, 4], "f16", 64, 3, 4, 1.0, mb=180000)

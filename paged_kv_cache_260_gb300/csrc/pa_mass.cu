@@ -134,8 +134,8 @@ decode_mass_finish_kernel(const DecodeMassParams p)
 // that pass 1 left in L2.
 //
 // 64 rows x 4 heads over 8 sequences of 16K tokens, 8 kv heads x 128: 127 us in a graph,
-// 63 a pass, each 268 MB of keys and 34.4 GFLOP twice the masks' share included (4.2 TB/s and
-// 1.09 PFLOP/s over the two).  No one unit is full: the tensor pipe is active 42 % of the time,
+// 63 a pass, each 268 MB of keys and 68.7 GFLOP (4.2 TB/s and 1.08 PFLOP/s over the
+// two).  No one unit is full: the tensor pipe is active 42 % of the time,
 // the exponentials' 43 %, issue slots 53 %; 13 us a pass are its start and end.  Without
 // exponentials pass 1 takes 57 us, with its keys in L2 as well 55: what is left is the
 // products' hand-overs, 0.78 us a tile of 128 keys against 0.66 at the library's rate.

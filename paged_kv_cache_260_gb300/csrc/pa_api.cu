@@ -1715,10 +1715,12 @@ int pa_decode_mass(const struct pa_sparse_args *args)
 
 // pa_prefill_mass's units of 2 x 128 rows, and its workspace: the statistics of the units'
 // pieces (one for each unit and one more for each border between two blocks' shares), and
-// of several row blocks each query tile's sums for every key.
+// of several row blocks each query tile's sums for every key: of `most` row blocks at a time,
+// as many as kMassKept holds, so that a longer chunk takes passes of its own for every
+// `most` of them.
 // Chunks of few rows keep their scores instead, with the statistics of the warps' pieces.
 struct PrefillMassPlan {
-    long long row_blocks, units, tiles;
+    long long row_blocks, most;
     size_t sums_off, total;
     int few_cols, few_warps;       // the form for few rows, or 0
     size_t few_off, few_total;
@@ -1732,23 +1734,24 @@ static bool prefill_mass_plan(int num_seqs, int max_query_len, int num_heads, in
         return false;
     const long long tokens = kMassTiles * (kMassRows / (num_heads / num_kv_heads));
     w->row_blocks = (max_query_len + tokens - 1) / tokens;
-    w->units = (long long)num_seqs * num_kv_heads * w->row_blocks;
-    w->tiles = w->units * (((long long)max_blocks * kBlockSize + kMassKeys - 1) / kMassKeys);
     const long long rows = (long long)max_query_len * (num_heads / num_kv_heads);
     const long long runs = (long long)num_seqs * num_kv_heads;
+    if (runs >= (1LL << 31) || runs * max_blocks >= (1LL << 31))    // (as sparse_tables)
+        return false;
+    const long long keys = runs * max_blocks * kBlockSize;
+    w->most = std::max(1LL, std::min(w->row_blocks, kMassKept / (kMassTiles * keys)));
     if (rows <= kMassFewRows && num_seqs <= kRaggedSeqs &&
-        runs * max_blocks * kBlockSize * score_cols((int)rows) <= kMassFewScores) {
+        keys * score_cols((int)rows) <= kMassKept) {
         w->few_cols = score_cols((int)rows);
         w->few_warps = num_sms * (rows <= 8 ? 4 : 3) * (kMassFewThreads / 32);
         w->few_off = round_up(sizeof(float2) * (size_t)(runs + w->few_warps) * kMassFewRows, 256);
-        w->few_total = w->few_off +
-                       sizeof(float) * (size_t)runs * max_blocks * kBlockSize * w->few_cols;
+        w->few_total = w->few_off + sizeof(float) * (size_t)keys * w->few_cols;
     }
     w->sums_off = round_up(
-        sizeof(float2) * (size_t)(w->units + num_sms) * 2 * kMassTiles * kMassRows, 256);
+        sizeof(float2) * (size_t)(runs * w->most + num_sms) * 2 * kMassTiles * kMassRows, 256);
     w->total = w->sums_off;
     if (w->row_blocks > 1)
-        w->total += sizeof(float) * (size_t)w->units * kMassTiles * max_blocks * kBlockSize;
+        w->total += sizeof(float) * (size_t)(w->most * kMassTiles * keys);
     return true;
 }
 
@@ -1791,7 +1794,14 @@ int pa_prefill_mass(const struct pa_sparse_args *args)
     if (!prefill_mass_plan(a.num_seqs, a.max_query_len, a.num_heads, a.num_kv_heads,
                            a.max_blocks_per_seq, ds->num_sms, &w))
         return PA_ERR_INVALID_ARG;
-    if (w.tiles >= (1LL << 30))          // the list of key tiles is counted in 32 bits
+    // equal shares of the row blocks
+    const long long parts = (w.row_blocks + w.most - 1) / w.most;
+    const long long share = (w.row_blocks + parts - 1) / parts;
+    auto tiles_of = [&](long long row_blocks) {
+        return (long long)a.num_seqs * a.num_kv_heads * row_blocks *
+               (((long long)a.max_blocks_per_seq * kBlockSize + kMassKeys - 1) / kMassKeys);
+    };
+    if (tiles_of(share) >= (1LL << 30))  // the list of key tiles is counted in 32 bits
         return PA_ERR_UNSUPPORTED;
     if (!a.workspace || a.workspace_bytes < w.total || !aligned(a.workspace, 256))
         return PA_ERR_WORKSPACE;
@@ -1814,7 +1824,7 @@ int pa_prefill_mass(const struct pa_sparse_args *args)
     p.max_blocks = a.max_blocks_per_seq;
     p.num_blocks = a.num_blocks;
     p.num_queries = a.num_queries;
-    p.row_blocks = (int)w.row_blocks;
+    p.row_blocks = p.all_blocks = (int)w.row_blocks;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.decay = decay;
     cudaStream_t st = static_cast<cudaStream_t>(a.stream);
@@ -1856,22 +1866,28 @@ int pa_prefill_mass(const struct pa_sparse_args *args)
     if (rc != PA_OK)
         return rc;
     void *kargs[] = {&p, &tmk};
-    // A key tile a block while the second pass's blocks find SMs of their own beside the first's,
-    // two of a unit's where they would not: 32 units of four tiles 13.1 us by one each, 11.0 by
-    // two, units of one tile 9.8 and 15.0.
-    const bool pairs = 2 * w.tiles > ds->num_sms && a.max_blocks_per_seq * kBlockSize > kMassKeys;
-    const dim3 grid((unsigned)std::min((long long)ds->num_sms,
-                                       pairs ? (w.tiles + 1) / 2 : w.tiles));
-    rc = launch_dependent(k.stats, grid, dim3(k.threads), k.smem_stats, st, kargs);
-    if (rc == PA_OK)
-        rc = launch_dependent(k.sums, grid, dim3(k.threads), k.smem_sums, st, kargs);
-    if (rc != PA_OK || w.row_blocks == 1)       // one row block: the second pass made the mass
-        return rc;
     const long long units = (long long)a.num_seqs * a.num_kv_heads * ((a.max_blocks_per_seq + 7) / 8);
-    return launch_dependent(prefill_mass_finish(),
-                            dim3(share_grid(units * (kMassFinishThreads / 32), kMassFinishThreads,
-                                            4, ds)),
-                            dim3(kMassFinishThreads), 0, st, fargs);
+    for (long long first = 0; first < w.row_blocks && rc == PA_OK; first += share) {
+        p.block0 = (int)first;
+        p.row_blocks = (int)std::min(share, w.row_blocks - first);
+        // A key tile a block while the second pass's blocks find SMs of their own beside the
+        // first's, two of a unit's where they would not: 32 units of four tiles 13.1 us by one
+        // each, 11.0 by two, units of one tile 9.8 and 15.0.
+        const long long tiles = tiles_of(p.row_blocks);
+        const bool pairs = 2 * tiles > ds->num_sms && a.max_blocks_per_seq * kBlockSize > kMassKeys;
+        const dim3 grid((unsigned)std::min((long long)ds->num_sms,
+                                           pairs ? (tiles + 1) / 2 : tiles));
+        rc = launch_dependent(k.stats, grid, dim3(k.threads), k.smem_stats, st, kargs);
+        if (rc == PA_OK)
+            rc = launch_dependent(k.sums, grid, dim3(k.threads), k.smem_sums, st, kargs);
+        // (one row block: the second pass made the mass)
+        if (rc == PA_OK && w.row_blocks > 1)
+            rc = launch_dependent(prefill_mass_finish(),
+                                  dim3(share_grid(units * (kMassFinishThreads / 32),
+                                                  kMassFinishThreads, 4, ds)),
+                                  dim3(kMassFinishThreads), 0, st, fargs);
+    }
+    return rc;
 }
 
 // Workspace of pa_evict: per (sequence, kv head) the holes and the slots that move into

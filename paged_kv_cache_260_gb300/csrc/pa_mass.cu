@@ -163,7 +163,8 @@ struct MassShape {
     static_assert(SMEM <= 227 * 1024, "one block per SM");
 };
 
-// A sequence's chunk: its first row of q, rows, length and row blocks (0: nothing to do).
+// A sequence's chunk: its first row of q, rows, length and the end of its row blocks that this
+// launch takes (0: nothing to do; up to block0: nothing in this launch).
 struct MassSeq {
     int L, c, qs, blocks;
 };
@@ -179,11 +180,11 @@ __device__ __forceinline__ MassSeq mass_seq(const PrefillMassParams &p, int s, i
         if (report)
             record_error(p.err, PA_DEVERR_SEQLEN_RANGE);
     } else if (x.c < 0 || x.c > x.L || x.qs < 0 || x.c > p.num_queries - x.qs ||
-               (x.c + TPB - 1) / TPB > p.row_blocks) {
+               (x.c + TPB - 1) / TPB > p.all_blocks) {
         if (report)
             record_error(p.err, PA_DEVERR_QUERY_RANGE);
     } else {
-        x.blocks = (x.c + TPB - 1) / TPB;
+        x.blocks = min((x.c + TPB - 1) / TPB, p.block0 + p.row_blocks);
     }
     return x;
 }
@@ -194,10 +195,11 @@ __device__ __forceinline__ int mass_tiles(const MassSeq &x, int b, int TPB)
     return (x.L - x.c + min((b + 1) * TPB, x.c) - 1) / kMassKeys + 1;
 }
 
-__device__ __forceinline__ int mass_tiles(const MassSeq &x, int TPB)
+// Those of the launch's row blocks.
+__device__ __forceinline__ int mass_tiles(const PrefillMassParams &p, const MassSeq &x, int TPB)
 {
     int n = 0;
-    for (int b = 0; b < x.blocks; ++b)
+    for (int b = p.block0; b < x.blocks; ++b)
         n += mass_tiles(x, b, TPB);
     return n;
 }
@@ -228,10 +230,10 @@ struct MassWalker {
             return;
         s = s0;
         x = mass_seq(p, s, TPB, false);
-        const int per = mass_tiles(x, TPB);
+        const int per = mass_tiles(p, x, TPB);
         h = (at - from) / per;
         first = from + h * per;
-        b = 0;
+        b = p.block0;
         while (first + mass_tiles(x, b, TPB) <= at)
             first += mass_tiles(x, b++, TPB);
         piece(TPB, at);
@@ -244,12 +246,12 @@ struct MassWalker {
         if (!valid)
             return;
         if (++b == x.blocks) {
-            b = 0;
+            b = p.block0;
             if (++h == p.num_kv_heads) {
                 h = 0;
                 do
                     x = mass_seq(p, ++s, TPB, false);
-                while (x.blocks == 0);
+                while (x.blocks <= p.block0);
             }
         }
         piece(TPB, first);
@@ -324,7 +326,7 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
     // ---- the block's share: the list's length, then the sequence its share starts in ----
     auto tiles_of = [&](int s, bool report) {
         const MassSeq x = mass_seq(p, s, TPB, report);
-        return Hkv * mass_tiles(x, TPB);
+        return Hkv * mass_tiles(p, x, TPB);
     };
     int carry = 0, mine = 0, before = 0;          // of this thread's last sequence
     auto scan_from = [&](int s0, bool report) {
@@ -548,7 +550,7 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
             const T *qg = static_cast<const T *>(p.q);
             const int tok = t0 + rr / G;
             const bool row_valid = rr < TPG * G && tok < w.x.c;
-            const int unit = (w.s * Hkv + w.h) * p.row_blocks + w.b;
+            const int unit = (w.s * Hkv + w.h) * p.row_blocks + w.b - p.block0;
             // a piece's statistics: [half of the key tiles][query tile][row]
             float2 *stats = p.stats + (size_t)unit * (2 * ROWS) + grp * Sh::BM + rr;
             float m = -INFINITY, l = 0.f;
@@ -650,7 +652,7 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
             }
             // pass 2: one row block of the chunk makes the whole mass, the second query tile's
             // threads adding the first one's sums; of several each leaves its sums
-            const bool alone = p.row_blocks == 1;
+            const bool alone = p.all_blocks == 1;
             float *sums = (alone ? p.mass + (size_t)(w.s * Hkv + w.h) * p.max_blocks * kBlockSize
                                  : p.sums + (size_t)(2 * unit + grp) * p.max_blocks * kBlockSize) + rr;
             // a key of the second query tile's threads that waits for the first one's sum: it is
@@ -1300,7 +1302,8 @@ __global__ void __launch_bounds__(kMassShortThreads) prefill_mass_short_kernel(c
     }
 }
 
-// Several row blocks: the sum over a sequence's query tiles, added to the mass.  Eight warps
+// Several row blocks: the sum over a sequence's query tiles of the launch, added to the mass (to
+// what the launches before made of it, from the second on).  Eight warps
 // (with two row blocks, four) share out the query tiles of 128 tokens of a (sequence, kv
 // head), four tokens a lane.  What bounds it is a warp's chain of loads: 14 runs of 1130
 // tokens, 34 row blocks, 9 us (a warp for all of the tiles 25); 64 runs to 5534 tokens, 2 row
@@ -1322,7 +1325,7 @@ prefill_mass_finish_kernel(const PrefillMassParams p)
         ragged_prefix<NTH>(sm, begin, n, [&](int s) {
             // what the passes skipped stays as it was
             const MassSeq x = mass_seq(p, s, kMassTiles * TPG, false);
-            return x.blocks ? (x.L + TOK - 1) / TOK : 0;
+            return x.blocks > p.block0 ? (x.L + TOK - 1) / TOK : 0;
         });
         const long long total = (long long)sm.pre[n] * Hkv;
         for (long long u0 = (long long)blockIdx.x * (NW / split); u0 < total;
@@ -1339,11 +1342,13 @@ prefill_mass_finish_kernel(const PrefillMassParams p)
             const float *from = p.sums + run * (kMassTiles * p.row_blocks) * T + t;
             float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
             // query tiles whose keys reach t (a unit's end where its last row's do)
-            const int TPB = kMassTiles * TPG, tiles = t < L ? (c + TPG - 1) / TPG : 0;
+            const int TPB = kMassTiles * TPG, k0 = kMassTiles * p.block0;
+            const int tiles = t < L ? min((c + TPG - 1) / TPG, k0 + kMassTiles * p.row_blocks) : 0;
 #pragma unroll 4
-            for (int k = max(0, (t - (L - c)) / TPB) * kMassTiles + warp % split; k < tiles;
+            for (int k = max(p.block0, (t - (L - c)) / TPB) * kMassTiles + warp % split; k < tiles;
                  k += split) {
-                const float4 x = __ldcg(reinterpret_cast<const float4 *>(from + (size_t)k * T));
+                const float4 x =
+                    __ldcg(reinterpret_cast<const float4 *>(from + (size_t)(k - k0) * T));
                 const int end = L - c + min((k / kMassTiles + 1) * TPB, c);
                 sum.x += x.x;                     // (t itself is reached by the first unit)
                 sum.y += t + 1 < end ? x.y : 0.f;
@@ -1359,7 +1364,7 @@ prefill_mass_finish_kernel(const PrefillMassParams p)
                 for (int w = 0; w < split; ++w)
                     all += reinterpret_cast<const float *>(part[warp / split * split + w])[j];
                 float *mass = p.mass + run * T + t0 + j;
-                *mass = add_mass(mass, p.decay, t0 + j >= L - c, all);
+                *mass = p.block0 ? *mass + all : add_mass(mass, p.decay, t0 + j >= L - c, all);
             }
             __syncthreads();
         }

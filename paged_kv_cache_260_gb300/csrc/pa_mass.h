@@ -31,12 +31,18 @@ struct PrefillMassParams {
     uint32_t *err;
     int num_seqs, num_heads, num_kv_heads, max_blocks, num_blocks;
     int num_queries;               // rows of q
-    int row_blocks;                // units of 2 x 128 (token, head) rows per (sequence, kv head)
+    // units of 2 x 128 (token, head) rows per (sequence, kv head): a launch takes row_blocks of
+    // them, from block0 on, of the longest chunk's all_blocks
+    int row_blocks, block0, all_blocks;
     // few rows: columns of the kept scores (in sums, [run][max_blocks * 16][columns]), the longest
     // chunk, the first kernel's warps; stats are [run + warp][kMassFewRows]
     int few_cols, few_tokens, few_warps;
     float scale_log2, decay;
 };
+
+// Scores or sums that a call keeps at a time: a gigabyte of workspace.  What would be more is
+// taken in parts (but for one sequence's or one row block's own).
+constexpr long long kMassKept = 1 << 28;
 
 constexpr int kMassRows = 128;     // (token, head) rows of one query tile
 constexpr int kMassTiles = 2;      // query tiles of a unit
@@ -63,7 +69,6 @@ constexpr int kMassShortThreads = 512;
 // faster: 32 runs of 128 keys 7.8 / 8.8, of 32 keys 7.4 / 6.9, 128 runs of 128 keys 9.7 / 8.8, 16
 // rows of 512 keys 13.6 / 10.3.
 constexpr int kMassFewRows = 16;
-constexpr long long kMassFewScores = 1 << 28;      // a gigabyte of workspace
 constexpr int kMassFewThreads = 128;
 
 struct MassKernels {

@@ -752,6 +752,36 @@ def test_prefill_mass_reports_bad_arguments(pa):
                        run(lens, [0, 40, 80], 40, 0, zero.cuda()))
 
 
+@pytest.mark.parametrize("lens,chunks,g,d,hkv,parts", [
+    ([300, 70, 900, 40], [150, 70, 5, 0], 128, 64, 1, 3),
+    ([700, 611, 65, 130], [600, 90, 65, 129], 16, 128, 2, 3),
+    ([90, 17, 1, 64], [85, 17, 1, 64], 128, 128, 1, 2)])
+@pytest.mark.parametrize("decay", [0.9, 0.0])
+def test_prefill_mass_in_parts(pa, lens, chunks, g, d, hkv, parts, decay):
+    # wide tables: the sums of so many row blocks are taken a gigabyte at a time
+    mb = 65536
+    tokens = 2 * (128 // g)
+    blocks = (max(chunks) + tokens - 1) // tokens
+    most = 2 ** 28 // (2 * len(lens) * hkv * 16 * mb)
+    assert (blocks + most - 1) // most == parts
+    chunk_case(pa, gen(70, g, d), lens, chunks, "bf16", d, hkv, g, decay, mb=mb)
+
+
+def test_prefill_mass_workspaces_are_bounded(pa):
+    size = pa.prefill_mass_workspace_size
+    # a whole prompt of 131072 tokens, and 8 chunks of 8192 in tables for 32768
+    for shape in ((1, 131072, 32, 8, 8192), (8, 8192, 32, 8, 2048)):
+        assert 0 < size(*shape) < 2 ** 30 + 2 ** 25
+    # that of longer chunks is no smaller
+    sizes = [size(4, c, 32, 8, 8192) for c in range(1, 3000, 7)]
+    assert sizes[1:] == sorted(sizes[1:]) and max(sizes) < 2 ** 30 + 2 ** 25
+    # one row block alone may be more
+    assert size(64, 65, 32, 8, 65536) > 2 ** 32
+    # what no call takes
+    assert size(2 ** 30, 8, 2 ** 21, 2 ** 20, 2 ** 10) == 0
+    assert size(2 ** 15, 8, 2 ** 4, 2 ** 4, 2 ** 12) == 0
+
+
 # ---------------------------------------------------------------------------
 # evict
 # ---------------------------------------------------------------------------

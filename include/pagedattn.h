@@ -582,7 +582,9 @@ int pa_sparse_decode(const struct pa_sparse_args *args);
  *   out, q, k_cache, v_cache, block_tables, seq_lens, max_blocks_per_seq, scale,
  *   mass [num_seqs][num_kv_heads][max_blocks_per_seq * 16] fp32, decay (finite);
  *   out may not be q.  The workspace holds the scores: 4 bytes for each query head
- *   and position of the tables.
+ *   (an odd group one more) and position of the tables, of as many sequences as four
+ *   gigabytes hold, but one at least: a larger batch is taken in parts, one after the other.
+ *   Shapes that the call refuses have size 0.
  * Errors as pa_decode.
  */
 size_t pa_decode_mass_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,

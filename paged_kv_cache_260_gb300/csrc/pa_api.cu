@@ -1630,20 +1630,28 @@ int pa_sparse_decode(const struct pa_sparse_args *args)
                        0, a.workspace, a.workspace_bytes, a.stream, x);
 }
 
-// Workspace of pa_decode_mass: the decode's own, the statistics, the scores.
+// Workspace of pa_decode_mass: the decode's own, the statistics, the scores, all of `most`
+// sequences at a time, as many as kMassDecodeKept holds the scores of.
 struct MassLayout {
-    size_t stat_off, score_off, total;
+    long long most;
+    size_t own, stat_off, score_off, total;
 };
 
-static MassLayout mass_layout(size_t decode_bytes, int num_seqs, int num_heads, int num_kv_heads,
-                              int max_blocks)
+static bool mass_layout(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int max_blocks,
+                        MassLayout *w)
 {
-    MassLayout w{};
-    w.stat_off = round_up(decode_bytes, 256);
-    w.score_off = w.stat_off + round_up(sizeof(float2) * (size_t)num_seqs * num_heads, 256);
-    w.total = w.score_off + sizeof(float) * (size_t)num_seqs * num_kv_heads * max_blocks *
-                                kBlockSize * score_cols(num_heads / num_kv_heads);
-    return w;
+    if (num_heads / num_kv_heads > kMaxGroup ||
+        (long long)num_seqs * num_kv_heads >= (1LL << 31) ||
+        (long long)num_seqs * num_kv_heads * max_blocks >= (1LL << 31))     // (as sparse_tables)
+        return false;
+    const long long scores =
+        (long long)num_kv_heads * max_blocks * kBlockSize * score_cols(num_heads / num_kv_heads);
+    w->most = std::max(1LL, std::min((long long)num_seqs, kMassDecodeKept / scores));
+    w->own = pa_decode_workspace_size((int)w->most, num_heads, num_kv_heads, head_dim, max_blocks, 0);
+    w->stat_off = round_up(w->own, 256);
+    w->score_off = w->stat_off + round_up(sizeof(float2) * (size_t)w->most * num_heads, 256);
+    w->total = w->score_off + sizeof(float) * (size_t)(w->most * scores);
+    return w->own > 0;
 }
 
 size_t pa_decode_mass_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
@@ -1652,9 +1660,9 @@ size_t pa_decode_mass_workspace_size(int num_seqs, int num_heads, int num_kv_hea
     if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads ||
         max_blocks_per_seq <= 0)
         return 0;
-    const size_t own = pa_decode_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim,
-                                                max_blocks_per_seq, 0);
-    return own ? mass_layout(own, num_seqs, num_heads, num_kv_heads, max_blocks_per_seq).total : 0;
+    MassLayout w{};
+    return mass_layout(num_seqs, num_heads, num_kv_heads, head_dim, max_blocks_per_seq, &w) ? w.total
+                                                                                            : 0;
 }
 
 int pa_decode_mass(const struct pa_sparse_args *args)
@@ -1675,42 +1683,53 @@ int pa_decode_mass(const struct pa_sparse_args *args)
     if (!all_aligned({a.mass, a.out, a.q, a.k_cache, a.v_cache}, 16) ||
         !all_aligned({a.block_tables, a.seq_lens}, 4) || a.out == a.q)
         return PA_ERR_INVALID_ARG;
-    const size_t own = pa_decode_workspace_size(a.num_seqs, a.num_heads, a.num_kv_heads, a.head_dim,
-                                                a.max_blocks_per_seq, 0);
-    const MassLayout w = mass_layout(own, a.num_seqs, a.num_heads, a.num_kv_heads,
-                                     a.max_blocks_per_seq);
-    if (!a.workspace || a.workspace_bytes < w.total || !aligned(a.workspace, 256))
-        return PA_ERR_WORKSPACE;
     DeviceState *ds;
     rc = device_state(&ds);
     if (rc != PA_OK)
         return rc;
+    MassLayout w{};
+    if (!mass_layout(a.num_seqs, a.num_heads, a.num_kv_heads, a.head_dim, a.max_blocks_per_seq, &w))
+        return PA_ERR_UNSUPPORTED;
+    if (!a.workspace || a.workspace_bytes < w.total || !aligned(a.workspace, 256))
+        return PA_ERR_WORKSPACE;
     char *ws = static_cast<char *>(a.workspace);
     DecodeExtra x;
     x.wide = true;
     x.stat = reinterpret_cast<float2 *>(ws + w.stat_off);
     x.scores = reinterpret_cast<float *>(ws + w.score_off);
-    rc = decode_impl(a.out, a.q, a.k_cache, a.v_cache, a.block_tables, a.seq_lens, a.num_seqs,
-                     a.num_heads, a.num_kv_heads, a.head_dim, a.block_size, a.max_blocks_per_seq,
-                     a.num_blocks, scale, a.dtype, 0, a.workspace, own, a.stream, x);
-    if (rc != PA_OK)
-        return rc;
-    DecodeMassParams p{};
-    p.mass = a.mass;
-    p.scores = x.scores;
-    p.stat = x.stat;
-    p.seq_lens = a.seq_lens;
-    p.num_seqs = a.num_seqs;
-    p.num_heads = a.num_heads;
-    p.num_kv_heads = a.num_kv_heads;
-    p.max_blocks = a.max_blocks_per_seq;
-    p.decay = decay;
-    // units of 128 tokens
-    const long long units = (long long)a.num_seqs * a.num_kv_heads * ((a.max_blocks_per_seq + 7) / 8);
-    void *kargs[] = {&p};
-    return launch_dependent(decode_mass_finish(),
-                            dim3(share_grid(units, kMassFinishThreads, 4, ds)),
-                            dim3(kMassFinishThreads), 0, static_cast<cudaStream_t>(a.stream), kargs);
+    // equal shares of the sequences
+    const long long parts = (a.num_seqs + w.most - 1) / w.most;
+    const long long share = (a.num_seqs + parts - 1) / parts;
+    for (long long first = 0; first < a.num_seqs && rc == PA_OK; first += share) {
+        const int n = (int)std::min(share, a.num_seqs - first);
+        const size_t rows = 2 * (size_t)first * a.num_heads * a.head_dim;
+        const int32_t *lens = a.seq_lens + first;
+        rc = decode_impl(static_cast<char *>(a.out) + rows, static_cast<const char *>(a.q) + rows,
+                         a.k_cache, a.v_cache, a.block_tables + first * a.max_blocks_per_seq, lens,
+                         n, a.num_heads, a.num_kv_heads, a.head_dim, a.block_size,
+                         a.max_blocks_per_seq, a.num_blocks, scale, a.dtype, 0, a.workspace, w.own,
+                         a.stream, x);
+        if (rc != PA_OK)
+            break;
+        DecodeMassParams p{};
+        p.mass = a.mass + first * a.num_kv_heads * a.max_blocks_per_seq * kBlockSize;
+        p.scores = x.scores;
+        p.stat = x.stat;
+        p.seq_lens = lens;
+        p.num_seqs = n;
+        p.num_heads = a.num_heads;
+        p.num_kv_heads = a.num_kv_heads;
+        p.max_blocks = a.max_blocks_per_seq;
+        p.decay = decay;
+        // units of 128 tokens
+        const long long units = (long long)n * a.num_kv_heads * ((a.max_blocks_per_seq + 7) / 8);
+        void *kargs[] = {&p};
+        rc = launch_dependent(decode_mass_finish(),
+                              dim3(share_grid(units, kMassFinishThreads, 4, ds)),
+                              dim3(kMassFinishThreads), 0, static_cast<cudaStream_t>(a.stream),
+                              kargs);
+    }
+    return rc;
 }
 
 // pa_prefill_mass's units of 2 x 128 rows, and its workspace: the statistics of the units'

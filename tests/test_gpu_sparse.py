@@ -457,6 +457,43 @@ def test_decode_mass_of_shared_blocks(pa):
     su.mass_close(m, *ref[2:])
 
 
+@pytest.mark.parametrize("dt,d,hkv,g,n,most", [("bf16", 128, 2, 16, 70, 32), ("f16", 64, 1, 5, 350, 170),
+                                               ("bf16", 64, 8, 4, 33, 32)])
+def test_decode_mass_in_parts(pa, dt, d, hkv, g, n, most):
+    # wide tables: the scores of so many sequences are taken four gigabytes at a time
+    mb, r, scale = 65536, gen(71, n), SCALE[d]
+    assert 2 ** 30 // (hkv * 16 * mb * (g + g % 2)) == most
+    lens = [(97 * i) % 300 for i in range(n)]
+    tables, nb = su.tables_for(r, lens)
+    k, v = (su.pool(r, nb, hkv, d, DT[dt], su.dead_slots(tables, lens, nb)) for _ in range(2))
+    q = (torch.randn(n, hkv * g, d, generator=r) * 2).to(DT[dt])
+    used = 16 * tables.shape[1]
+    mass = torch.rand(n, hkv, used, generator=r) * 5
+    ref = su.decode_mass(q, mass, k, v, tables, lens, scale, 0.9)
+    mm = torch.full((n, hkv, 16 * mb), 7.0, device="cuda")
+    mm[..., :used] = mass.cuda()
+    tt = torch.full((n, mb), -1, dtype=torch.int32, device="cuda")
+    tt[:, :tables.shape[1]] = tables.cuda()
+    qq, kk, vv, ll = cuda(q, k, v, lens)
+    out = torch.full_like(qq, math.nan)
+    pa.decode_mass(out, mm, qq, kk, vv, tt, ll, scale, decay=0.9)
+    check(pa)
+    su.close(out, *ref[:2], "out")
+    su.mass_close(mm[..., :used], *ref[2:], "mass")
+    assert bool((mm[..., used:] == 7.0).all())
+
+
+def test_decode_mass_workspaces_are_bounded(pa):
+    size = pa.decode_mass_workspace_size
+    assert 0 < size(512, 32, 8, 128, 8192) < 2 ** 32 + 2 ** 27
+    sizes = [size(n, 32, 8, 128, 8192) for n in range(1, 600)]
+    assert sizes == sorted(sizes) and sizes[-1] == sizes[260]
+    assert size(2, 16, 1, 64, 2 ** 24) > 2 ** 33         # one sequence alone may be more
+    # what no call takes
+    assert size(2, 17, 1, 64, 8) == 0 and size(2 ** 15, 2 ** 4, 2 ** 4, 64, 2 ** 12) == 0
+    assert size(2 ** 30, 2 ** 20, 2 ** 20, 64, 8) == 0
+
+
 # ---------------------------------------------------------------------------
 # prefill_mass
 # ---------------------------------------------------------------------------

@@ -63,7 +63,8 @@ enum pa_dtype { PA_DTYPE_F16 = 0, PA_DTYPE_BF16 = 1 };
 #define PA_DEVERR_TIMEOUT      0x10u /* a bounded wait on a copy expired */
 #define PA_DEVERR_APPEND_SLOT  0x20u /* decode_append: slot is not the last position's */
 #define PA_DEVERR_QUERY_RANGE  0x40u /* prefill: chunk < 0, > seq_len or > max_query_len;
-                                      * block_bounds: start outside [0, seq_len] */
+                                      * block_bounds: start outside [0, seq_len], or
+                                      * not -1 with seq_len 0 */
 #define PA_DEVERR_POSITION_RANGE 0x80u /* rotation: position >= max_position */
 
 /* PAGEDATTN_VERSION of the loaded library. */
@@ -522,12 +523,13 @@ struct pa_sparse_args {
  *     bounds[b][h][0][c] = min_t k[b][h][t][c],  bounds[b][h][1][c] = max_t k[b][h][t][c]
  * over the block's live tokens (all of them, also those before starts[s]).  Exact;
  * a NaN among the keys makes the channel's bounds NaN.  After a decode step starts is
- * seq_lens - 1, after a prompt chunk the chunk's first position; NULL is 0.
+ * seq_lens - 1 (-1 where a sequence has no token), after a prompt chunk the chunk's first
+ * position; NULL is 0.
  *
  *   bounds [num_blocks][num_kv_heads][2][head_dim] dtype, written; k_cache,
  *   block_tables, seq_lens, starts [num_seqs] int32 or NULL, max_blocks_per_seq
- * A start outside [0, seq_len] sets PA_DEVERR_QUERY_RANGE and counts as the
- * nearer end.  Lengths are clamped, bad table entries skipped.  A block that two
+ * A start outside [0, seq_len], but for the -1 of an empty sequence, sets
+ * PA_DEVERR_QUERY_RANGE and counts as the nearer end.  Lengths are clamped, bad table entries skipped.  A block that two
  * sequences hold to different lengths gets the bounds of one of them.
  */
 int pa_block_bounds(const struct pa_sparse_args *args);

@@ -661,7 +661,8 @@ def block_bounds(bounds, k_cache, block_tables, seq_lens, starts=None, stream=No
     starts[s] .. seq_lens[s] - 1 (all of a sequence's without starts).
 
     bounds [num_blocks, num_kv_heads, 2, head_dim] in the pool's type; starts int32
-    [num_seqs]: seq_lens - 1 after a decode step, a chunk's first position after it.
+    [num_seqs]: seq_lens - 1 after a decode step (-1 for a sequence without tokens), a
+    chunk's first position after it.
     """
     names = _hot()
     nb, hkv, bs, d = k_cache.shape

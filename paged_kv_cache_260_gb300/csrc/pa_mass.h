@@ -43,8 +43,9 @@ struct PrefillMassParams {
 // Sums or scores that pa_prefill_mass keeps at a time, a gigabyte of workspace, and scores that
 // pa_decode_mass does, four.  What would be more is taken in parts (but for one sequence's or
 // one row block's own).  A part of a chunk's row blocks is milliseconds long where the tables
-// are full; one of a decode costs 10 us: 128 sequences of the lognormal lengths to 4096 in tables for 131K tokens, 2.2 GB
-// in one part, 88.3 us in a graph, 98.2 in two; of eight times the lengths 647 and 669.
+// are full; one of a decode costs 10 us: 128 sequences of the lognormal lengths to 4096 in tables
+// for 131K tokens, 2.2 GB in one part, 88.3 us in a graph, 98.2 in two; of eight times the
+// lengths 647 and 669.
 constexpr long long kMassKept = 1 << 28, kMassDecodeKept = 1 << 30;
 
 constexpr int kMassRows = 128;     // (token, head) rows of one query tile

@@ -79,7 +79,8 @@ __global__ void __launch_bounds__(kBoundsThreads) block_bounds_kernel(const Boun
             const int L = checked_len(p.seq_lens, s, p.max_blocks, p.err);
             if (p.starts) {
                 const int b = __ldg(p.starts + s);
-                if (b < 0 || b > L)
+                // (the newest token of a sequence that has none is at -1)
+                if ((b < 0 && (L > 0 || b < -1)) || b > L)
                     record_error(p.err, PA_DEVERR_QUERY_RANGE);
                 if (b >= L)
                     return 0;

@@ -101,6 +101,26 @@ def test_bounds_report_bad_arguments(pa):
     assert torch.equal(bb.cpu(), su.bounds(b, k, tables, [40, 0, 0]))
 
 
+def test_bounds_after_a_step_of_a_padded_batch(pa):
+    # starts = seq_lens - 1, also of sequences without tokens
+    g = gen(72)
+    lens = [0, 40, 0, 1, 16, 0]
+    tables, nb = su.tables_for(g, lens)
+    k = su.pool(g, nb, 3, 64, torch.bfloat16)
+    old = su.pool(g, nb, 3, 64, torch.bfloat16)[:, :, :2].contiguous()
+    b, kk, tt, ll = cuda(old, k, tables, lens)
+    pa.block_bounds(b, kk, tt, ll, starts=ll - 1)
+    check(pa)
+    ref = su.bounds(old, k, tables, lens, [max(0, n - 1) for n in lens])
+    assert torch.equal(su.bits(b), su.bits(ref))
+    # other starts of empty sequences, and -1 of others, are none
+    for i, x in ((0, -2), (0, 1), (1, -1)):
+        starts = ll - 1
+        starts[i] = x
+        pa.block_bounds(b, kk, tt, ll, starts=starts)
+        check(pa, pa.DEVERR["QUERY_RANGE"])
+
+
 # ---------------------------------------------------------------------------
 # select_blocks
 # ---------------------------------------------------------------------------

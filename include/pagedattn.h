@@ -529,8 +529,10 @@ struct pa_sparse_args {
  *   bounds [num_blocks][num_kv_heads][2][head_dim] dtype, written; k_cache,
  *   block_tables, seq_lens, starts [num_seqs] int32 or NULL, max_blocks_per_seq
  * A start outside [0, seq_len], but for the -1 of an empty sequence, sets
- * PA_DEVERR_QUERY_RANGE and counts as the nearer end.  Lengths are clamped, bad table entries skipped.  A block that two
- * sequences hold to different lengths gets the bounds of one of them.
+ * PA_DEVERR_QUERY_RANGE and counts as the nearer end.  Lengths are clamped, bad table entries skipped.  A block that
+ * sequences of one call hold to different lengths, which copy-on-write never leaves, gets each
+ * minimum and each maximum from any of them: no bounds of the longer ones, for which
+ * pa_select_blocks may then leave out blocks that matter.
  */
 int pa_block_bounds(const struct pa_sparse_args *args);
 

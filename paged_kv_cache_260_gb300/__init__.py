@@ -662,7 +662,8 @@ def block_bounds(bounds, k_cache, block_tables, seq_lens, starts=None, stream=No
 
     bounds [num_blocks, num_kv_heads, 2, head_dim] in the pool's type; starts int32
     [num_seqs]: seq_lens - 1 after a decode step (-1 for a sequence without tokens), a
-    chunk's first position after it.
+    chunk's first position after it.  Sequences that share a block hold it to the same
+    length (what copy-on-write leaves): of several the bounds are none's in particular.
     """
     names = _hot()
     nb, hkv, bs, d = k_cache.shape

@@ -71,6 +71,29 @@ int pa_bm_fork(pa_block_manager *bm, int64_t parent, int64_t child);
 int pa_bm_append(pa_block_manager *bm, int64_t seq_id, int num_tokens, int64_t *slots,
                  int64_t *cow_pairs, int *num_cow);
 
+/*
+ * Make the blocks that hold a sequence's first num_tokens tokens (all of its blocks, if it has
+ * fewer) its own: each one that it shares is replaced by a fresh block, in the order of the
+ * table, and the pair (shared block, copy) goes to cow_pairs[2 i], [2 i + 1]; *num_cow receives
+ * their count.  The caller copies them with pa_copy_blocks before they are written.  If there
+ * are more than max_pairs, *num_cow says how many, and the call returns PA_ERR_INVALID_ARG and
+ * changes nothing; cow_pairs may be NULL where max_pairs is 0.
+ *
+ * This is what pa_evict asks for, with num_tokens the new length: it reads the whole sequence,
+ * but writes nothing past that.
+ */
+int pa_bm_own_blocks(pa_block_manager *bm, int64_t seq_id, int64_t num_tokens, int64_t *cow_pairs,
+                     int max_pairs, int *num_cow);
+
+/*
+ * Shorten a sequence to its first num_tokens tokens; one of at most so many stays as it is (as
+ * with pa_evict's new_lens).  The blocks past them lose one reference, those no longer
+ * referenced go back to the free list, and pa_bm_append goes on from the new length.  After an
+ * eviction: once pa_evict is enqueued, since what is given back may be handed out and written by
+ * later calls on its stream.
+ */
+int pa_bm_shorten(pa_block_manager *bm, int64_t seq_id, int64_t num_tokens);
+
 /* Drop a sequence: its blocks lose one reference and those no longer
  * referenced go back to the free list. */
 int pa_bm_free_sequence(pa_block_manager *bm, int64_t seq_id);

@@ -529,10 +529,11 @@ struct pa_sparse_args {
  *   bounds [num_blocks][num_kv_heads][2][head_dim] dtype, written; k_cache,
  *   block_tables, seq_lens, starts [num_seqs] int32 or NULL, max_blocks_per_seq
  * A start outside [0, seq_len], but for the -1 of an empty sequence, sets
- * PA_DEVERR_QUERY_RANGE and counts as the nearer end.  Lengths are clamped, bad table entries skipped.  A block that
- * sequences of one call hold to different lengths, which copy-on-write never leaves, gets each
- * minimum and each maximum from any of them: no bounds of the longer ones, for which
- * pa_select_blocks may then leave out blocks that matter.
+ * PA_DEVERR_QUERY_RANGE and counts as the nearer end.  Lengths are clamped, bad table
+ * entries skipped.  A block that sequences of one call hold to different lengths, which
+ * forks and appends never leave, gets each minimum and each maximum from any of them: no
+ * bounds of the longer ones, for which pa_select_blocks may then leave out blocks that
+ * matter.
  */
 int pa_block_bounds(const struct pa_sparse_args *args);
 
@@ -630,12 +631,14 @@ int pa_prefill_mass(const struct pa_sparse_args *args);
  * before it that dropped tokens leave, in ascending order.  (Attention of a later
  * token does not depend on the order of the keys before it; what was rotated into
  * a key stays with it.)  mass moves along.  Slots from B on are left as they were, as
- * are sequences of at most B tokens.  The caller shortens seq_lens to B, and may give
- * back the blocks past it; pa_block_bounds of the sequence are out of date.
+ * are sequences of at most B tokens.  The caller goes on with min(seq_len, B) tokens, and
+ * may give back the blocks past them (pa_bm_shorten); pa_block_bounds of the sequence are
+ * out of date.
  *   k_cache, v_cache, mass (written), block_tables, seq_lens, new_lens [num_seqs]
  *   int32, max_blocks_per_seq, keep_first >= 0, keep_last >= 0
- * The sequence's blocks must be its own (copy-on-write first).  A negative new_len, a
- * bad length or table entry leaves the sequence as it was.
+ * The blocks that hold the first B tokens must be the sequence's own (pa_bm_own_blocks and
+ * pa_copy_blocks first); those past them are only read.  A negative new_len, a bad length or
+ * table entry leaves the sequence as it was.
  */
 size_t pa_evict_workspace_size(int num_seqs, int num_kv_heads, int max_blocks_per_seq);
 int pa_evict(const struct pa_sparse_args *args);

@@ -663,7 +663,7 @@ def block_bounds(bounds, k_cache, block_tables, seq_lens, starts=None, stream=No
     bounds [num_blocks, num_kv_heads, 2, head_dim] in the pool's type; starts int32
     [num_seqs]: seq_lens - 1 after a decode step (-1 for a sequence without tokens), a
     chunk's first position after it.  Sequences that share a block hold it to the same
-    length (what copy-on-write leaves): of several the bounds are none's in particular.
+    length (as forks and appends leave it), else its bounds are none's in particular.
     """
     names = _hot()
     nb, hkv, bs, d = k_cache.shape
@@ -890,8 +890,9 @@ def evict(k_cache, v_cache, mass, block_tables, seq_lens, new_lens, keep_first=0
           workspace=None, stream=None):
     """pa_evict: every sequence longer than new_lens[s] is cut to that many tokens in place:
     each kv head keeps its first keep_first, its last keep_last and the heaviest of the rest
-    by mass, which moves along.  The caller shortens seq_lens to new_lens, gives back the
-    blocks past it and renews the bounds; the sequence's blocks must be its own."""
+    by mass, which moves along.  The caller goes on with min(seq_lens, new_lens), gives back the
+    blocks past that (BlockManager.shorten) and renews the bounds; the blocks that hold the
+    first new_lens[s] tokens must be the sequence's own (BlockManager.own_blocks)."""
     names = _hot()
     nb, hkv, bs, d = pool = k_cache.shape
     n = seq_lens.shape[0]

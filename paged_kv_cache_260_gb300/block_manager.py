@@ -38,6 +38,10 @@ def _lib():
         L.pa_bm_fork.argtypes = [vp, i64, i64]
         L.pa_bm_append.restype = i
         L.pa_bm_append.argtypes = [vp, i64, i, vp, vp, C.POINTER(C.c_int)]
+        L.pa_bm_own_blocks.restype = i
+        L.pa_bm_own_blocks.argtypes = [vp, i64, i64, vp, i, C.POINTER(C.c_int)]
+        L.pa_bm_shorten.restype = i
+        L.pa_bm_shorten.argtypes = [vp, i64, i64]
         L.pa_bm_free_sequence.restype = i
         L.pa_bm_free_sequence.argtypes = [vp, i64]
         L.pa_bm_block_table.restype = i
@@ -92,6 +96,20 @@ class BlockManager:
         _check("pa_bm_append", self._L.pa_bm_append(
             self._h, seq_id, num_tokens, slots.ctypes.data, pair.ctypes.data, C.byref(ncow)))
         return slots[:num_tokens], (tuple(int(x) for x in pair) if ncow.value else None)
+
+    def own_blocks(self, seq_id: int, num_tokens: int):
+        """Makes the blocks of the first num_tokens tokens the sequence's own: the copies to
+        make, int64 [pairs, 2], for copy_blocks (what evict asks for, with its new length)."""
+        most = min(self.num_blocks, -(-num_tokens // self.block_size)) if num_tokens > 0 else 0
+        pairs = np.empty((most, 2), dtype=np.int64)
+        n = C.c_int(0)
+        _check("pa_bm_own_blocks", self._L.pa_bm_own_blocks(
+            self._h, seq_id, num_tokens, pairs.ctypes.data, most, C.byref(n)))
+        return pairs[:n.value]
+
+    def shorten(self, seq_id: int, num_tokens: int):
+        """Gives back the blocks past the first num_tokens tokens; append goes on from there."""
+        _check("pa_bm_shorten", self._L.pa_bm_shorten(self._h, seq_id, num_tokens))
 
     def free(self, seq_id: int):
         _check("pa_bm_free_sequence", self._L.pa_bm_free_sequence(self._h, seq_id))

@@ -130,6 +130,58 @@ int pa_bm_append(pa_block_manager *bm, int64_t seq_id, int num_tokens, int64_t *
     return PA_OK;
 }
 
+int pa_bm_own_blocks(pa_block_manager *bm, int64_t seq_id, int64_t num_tokens, int64_t *cow_pairs,
+                     int max_pairs, int *num_cow)
+{
+    if (!bm || num_tokens < 0 || max_pairs < 0 || (max_pairs > 0 && !cow_pairs) || !num_cow)
+        return PA_ERR_INVALID_ARG;
+    auto it = bm->seqs.find(seq_id);
+    if (it == bm->seqs.end())
+        return PA_ERR_INVALID_ARG;
+    pa_block_manager::Seq &s = it->second;
+    const size_t end = num_tokens >= s.len
+                           ? s.blocks.size()
+                           : (size_t)((num_tokens + bm->block_size - 1) / bm->block_size);
+    int shared = 0;
+    for (size_t j = 0; j < end; ++j)
+        shared += bm->refs[s.blocks[j]] > 1;
+    *num_cow = shared;
+    if (shared > max_pairs)
+        return PA_ERR_INVALID_ARG;
+    if ((size_t)shared > bm->free_list.size())
+        return PA_ERR_OUT_OF_BLOCKS;
+    for (size_t j = 0; j < end; ++j) {
+        const int32_t src = s.blocks[j];
+        if (bm->refs[src] < 2)
+            continue;
+        s.blocks[j] = bm->take();
+        bm->drop(src);
+        *cow_pairs++ = src;
+        *cow_pairs++ = s.blocks[j];
+        ++bm->cow_copies;
+    }
+    return PA_OK;
+}
+
+int pa_bm_shorten(pa_block_manager *bm, int64_t seq_id, int64_t num_tokens)
+{
+    if (!bm || num_tokens < 0)
+        return PA_ERR_INVALID_ARG;
+    auto it = bm->seqs.find(seq_id);
+    if (it == bm->seqs.end())
+        return PA_ERR_INVALID_ARG;
+    pa_block_manager::Seq &s = it->second;
+    if (num_tokens >= s.len)
+        return PA_OK;
+    const size_t keep = (size_t)((num_tokens + bm->block_size - 1) / bm->block_size);
+    while (s.blocks.size() > keep) {     // the one taken last is handed out first again
+        bm->drop(s.blocks.back());
+        s.blocks.pop_back();
+    }
+    s.len = num_tokens;
+    return PA_OK;
+}
+
 int pa_bm_free_sequence(pa_block_manager *bm, int64_t seq_id)
 {
     if (!bm)

@@ -135,6 +135,130 @@ def test_no_leak_and_reference_invariant():
     assert st["shared_blocks"] == 0 and st["num_sequences"] == 0
 
 
+def test_a_shortened_sequence_goes_on_from_its_new_length():
+    bm = BlockManager(16)
+    bm.add_sequence(0)
+    bm.append(0, 70)                                        # blocks 0 to 4
+    bm.shorten(0, 40)
+    table, nb, ln = bm.block_table(0, 6)
+    assert table.tolist() == [0, 1, 2, -1, -1, -1] and nb == 3 and ln == 40
+    st = bm.stats()
+    assert st["free_blocks"] == 13 and st["releases"] == 2
+    slots, cow = bm.append(0, 10)                           # 8 more of block 2, then block 3 again
+    assert cow is None and slots.tolist() == [2 * 16 + 8 + i for i in range(8)] + [48, 49]
+    bm.shorten(0, 50)                                       # its own length, and more: as it was
+    bm.shorten(0, 2 ** 62)
+    assert bm.block_table(0, 6)[1:] == (4, 50)
+    bm.shorten(0, 48)                                       # on a block's border
+    assert bm.block_table(0, 6)[1:] == (3, 48) and bm.append(0, 1)[0][0] == 48
+    bm.shorten(0, 0)
+    assert bm.block_table(0, 6)[1:] == (0, 0) and bm.stats()["free_blocks"] == 16
+    assert bm.append(0, 1)[0][0] == 0
+
+
+def test_shortening_keeps_what_others_hold():
+    bm = BlockManager(16)
+    bm.add_sequence(0)
+    bm.append(0, 70)
+    bm.fork(0, 1)
+    bm.shorten(1, 20)
+    assert [bm.ref_count(b) for b in range(5)] == [2, 2, 1, 1, 1]
+    assert bm.stats()["free_blocks"] == 11 and bm.block_table(0, 5)[1:] == (5, 70)
+    slots, cow = bm.append(1, 1)                            # into the shared, partly held block
+    assert cow == (1, 5) and slots[0] == 5 * 16 + 4
+    bm.free(0)
+    bm.free(1)
+    assert bm.stats()["free_blocks"] == 16
+
+
+def test_own_blocks_copies_the_shared_ones_of_the_first_tokens():
+    bm = BlockManager(16)
+    bm.add_sequence(0)
+    bm.append(0, 70)                                        # blocks 0 to 4
+    assert bm.own_blocks(0, 70).shape == (0, 2)             # nothing is shared
+    bm.fork(0, 1)
+    assert bm.append(1, 1)[1] == (4, 5)                     # block 4 is not any more
+    pairs = bm.own_blocks(1, 33)                            # three blocks hold them
+    assert pairs.tolist() == [[0, 6], [1, 7], [2, 8]]
+    assert bm.block_table(1, 5)[0].tolist() == [6, 7, 8, 3, 5]
+    assert bm.block_table(0, 5)[0].tolist() == [0, 1, 2, 3, 4]
+    assert [bm.ref_count(b) for b in range(9)] == [1, 1, 1, 2, 1, 1, 1, 1, 1]
+    assert bm.stats()["cow_copies"] == 4
+    assert len(bm.own_blocks(1, 48)) == 0 and len(bm.own_blocks(1, 0)) == 0
+    assert bm.own_blocks(0, 1000).tolist() == [[3, 9]]      # more than it has: all of them
+    assert all(bm.ref_count(b) == 1 for b in range(10))
+
+
+def test_own_blocks_refused_changes_nothing():
+    import ctypes as C
+    bm = BlockManager(6)
+    bm.add_sequence(0)
+    bm.append(0, 64)
+    bm.fork(0, 1)
+    before = bm.stats()
+    with pytest.raises(PagedAttnError) as e:
+        bm.own_blocks(1, 64)                                # four copies, two free blocks
+    assert e.value.status == PA_ERR_OUT_OF_BLOCKS and bm.stats() == before
+    n, pairs = C.c_int(-1), np.zeros(4, np.int64)
+    assert bm._L.pa_bm_own_blocks(bm._h, 1, 40, pairs.ctypes.data, 2, C.byref(n)) == 1
+    assert n.value == 3 and bm.stats() == before            # room for two
+    assert bm._L.pa_bm_own_blocks(bm._h, 1, 40, None, 0, C.byref(n)) == 1 and n.value == 3
+    assert bm._L.pa_bm_own_blocks(bm._h, 1, 40, None, 2, C.byref(n)) == 1
+    assert bm._L.pa_bm_own_blocks(bm._h, 1, 40, pairs.ctypes.data, 2, None) == 1
+    for call in (lambda: bm.own_blocks(7, 3), lambda: bm.own_blocks(1, -1),
+                 lambda: bm.shorten(7, 3), lambda: bm.shorten(1, -1)):
+        with pytest.raises(PagedAttnError):
+            call()
+    assert bm.stats() == before and len(bm.own_blocks(1, 32)) == 2
+
+
+def test_no_leak_with_shortened_and_owned_sequences():
+    rng = np.random.default_rng(3)
+    bm = BlockManager(3000)
+    live = {}
+    for step in range(800):
+        op = int(rng.integers(6))
+        if op == 0 or not live:
+            bm.add_sequence(step)
+            live[step] = 0
+        elif op == 1:
+            parent = int(rng.choice(list(live)))
+            bm.fork(parent, 100000 + step)
+            live[100000 + step] = live[parent]
+        elif op == 2:
+            sid, n = int(rng.choice(list(live))), int(rng.integers(1, 60))
+            slots, _ = bm.append(sid, n)
+            table = bm.block_table(sid, 3000)[0]
+            assert slots.tolist() == [table[t // 16] * 16 + t % 16
+                                      for t in range(live[sid], live[sid] + n)]
+            live[sid] += n
+        elif op == 3:
+            sid = int(rng.choice(list(live)))
+            n = int(rng.integers(0, live[sid] + 5))
+            bm.shorten(sid, n)
+            live[sid] = min(live[sid], n)
+        elif op == 4:
+            sid = int(rng.choice(list(live)))
+            n = int(rng.integers(0, live[sid] + 5))
+            pairs = bm.own_blocks(sid, n)
+            table = bm.block_table(sid, 3000)[0]
+            own = -(-min(n, live[sid]) // 16)
+            assert all(bm.ref_count(int(b)) == 1 for b in table[:own])
+            assert set(pairs[:, 1].tolist()) <= set(table[:own].tolist())
+        else:
+            sid = int(rng.choice(list(live)))
+            bm.free(sid)
+            del live[sid]
+        assert [bm.block_table(s, 3000)[1:] for s in live] == [(-(-n // 16), n)
+                                                               for n in live.values()]
+        assert (sum(bm.ref_count(b) for b in range(3000)) == sum(-(-n // 16)
+                                                                 for n in live.values()))
+    for sid in live:
+        bm.free(sid)
+    st = bm.stats()
+    assert st["free_blocks"] == 3000 and st["allocations"] == st["releases"]
+
+
 def test_bad_calls():
     bm = BlockManager(8)
     bm.add_sequence(5)

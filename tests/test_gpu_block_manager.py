@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import oracle
+import sparse_util as su
 import synth
 from gpu_util import TOL, dev_bits, host_bits, max_err
 from paged_kv_cache_260_gb300.block_manager import BlockManager
@@ -76,3 +77,74 @@ def test_parallel_sampling_steps_with_the_block_manager(pa, prompt_lens, mode):
         bm.free(sid)
     st = bm.stats()
     assert st["free_blocks"] == NB and st["allocations"] == st["releases"]
+
+
+def test_evicted_sequences_go_on_with_the_block_manager(pa):
+    """Forked prompts are cut to their heaviest tokens and decoded on: the manager copies the
+    shared blocks first, takes back the blocks past the new ends and hands out slots from there."""
+    r = torch.Generator().manual_seed(11)
+    hq, hkv, d, nb, mb, scale, budget = 8, 2, 64, 64, 24, 0.125, 100
+
+    def rows(*shape):
+        return torch.randn(*shape, generator=r).half()
+
+    k, v = rows(nb, hkv, 16, d).cuda(), rows(nb, hkv, 16, d).cuda()
+    bm = BlockManager(nb)
+    for sid, length in ((0, 300), (2, 220)):
+        bm.add_sequence(sid)
+        slots, _ = bm.append(sid, length)
+        pa.reshape_and_cache(rows(length, hkv, d).cuda(), rows(length, hkv, d).cuda(), k, v,
+                             torch.from_numpy(slots).cuda())
+    bm.fork(0, 1)                                            # 0 stays whole
+    bm.fork(2, 3)
+    ids = [1, 2, 3]
+
+    def state():
+        t = np.stack([bm.block_table(s, mb)[0] for s in ids])
+        return torch.from_numpy(t), [bm.block_table(s, mb)[2] for s in ids]
+
+    def ints(x):
+        return torch.tensor(x, dtype=torch.int32).cuda()
+
+    whole = [su.rows_of(x.cpu(), torch.from_numpy(bm.block_table(0, mb)[0]), 300, h)
+             for x in (k, v) for h in range(hkv)]
+    tables, lens = state()
+    mass = torch.full((3, hkv, 16 * mb), np.nan).cuda()
+    q = rows(24, hq, d)
+    pa.prefill_mass(mass, q.cuda(), k, tables.cuda(), ints(lens), ints([0, 8, 16, 24]), 8, scale,
+                    decay=0.0)
+    for _ in range(2):
+        pairs = np.concatenate([bm.own_blocks(s, budget) for s in ids])
+        if len(pairs):
+            pa.copy_blocks(k, v, torch.from_numpy(pairs).cuda())
+        assert len(pairs) in (0, 14)                         # 7 blocks of 1 and of 2 or 3
+        tables, lens = state()
+        before = k.cpu(), v.cpu(), mass.cpu()
+        pa.evict(k, v, mass, tables.cuda(), ints(lens), ints([budget] * 3), keep_first=4,
+                 keep_last=16)
+        ref = su.evict(*before, tables, lens, [budget] * 3, 4, 16)
+        assert all(torch.equal(su.bits(x), su.bits(y)) for x, y in zip((k, v, mass), ref))
+        for s in ids:
+            bm.shorten(s, budget)
+        assert state()[1] == [budget] * 3
+        for step in range(20):
+            new = [bm.append(s, 1) for s in ids]
+            assert all(cow is None for _, cow in new)
+            slots = torch.from_numpy(np.concatenate([x for x, _ in new]))
+            pa.reshape_and_cache(rows(3, hkv, d).cuda(), rows(3, hkv, d).cuda(), k, v, slots.cuda())
+            tables, lens = state()
+            q, before = rows(3, hq, d), mass.cpu()
+            out, _ = pa.decode_mass(torch.empty_like(q).cuda(), mass, q.cuda(), k, v, tables.cuda(),
+                                    ints(lens), scale)
+            ref = su.decode_mass(q, before, k.cpu(), v.cpu(), tables, lens, scale, 1.0)
+            su.close(out, *ref[:2], "step")
+            su.mass_close(mass, *ref[2:], "step")
+        assert lens == [budget + 20] * 3
+    assert pa.get_device_error() == 0
+    # the sequence that was not cut has its tokens still
+    now = [su.rows_of(x.cpu(), torch.from_numpy(bm.block_table(0, mb)[0]), 300, h)
+           for x in (k, v) for h in range(hkv)]
+    assert all(torch.equal(x, y) for x, y in zip(whole, now))
+    for s in [0] + ids:
+        bm.free(s)
+    assert bm.stats()["free_blocks"] == nb

@@ -424,6 +424,9 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
                     cur = to_row(win, nxt);
                     nxt = fetch(win + step);
                 }
+                // (the bounded waits of pass 2 begin once pass 1, which they wait for too, has ended)
+                if (SUMS && it == NS)
+                    grid_dependency_wait();
                 bool ready = true;
                 if (lane == 0)
                     ready = !*abort_flag &&
@@ -464,6 +467,8 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
         int rows[Sh::NG] = {0, 0};                // units so far of each query tile
         int turn[Sh::NG] = {0, 0};                // key tiles so far of each query tile
         uint32_t used = 0, odd = 0;               // of each score buffer: used yet, parity
+        if (SUMS)                                 // the rows come after it
+            grid_dependency_wait();
         for (; ok && w.valid; w.next(p, TPB)) {
             const int ng = groups();
             for (int i = 0; ok && i < w.te - w.tb; ++i, ++it) {

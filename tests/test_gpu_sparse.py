@@ -332,6 +332,43 @@ def test_sparse_decode_past_the_end_holds_anything(pa):
     su.close(out, ref, tol)
 
 
+@pytest.mark.parametrize("dt,d,hkv,g,n,keep", [
+    ("f16", 64, 2, 1, 3, 5), ("bf16", 128, 8, 4, 4, 40), ("f16", 128, 1, 7, 5, 100),
+    ("bf16", 64, 3, 16, 2, 17), ("f16", 64, 8, 2, 300, 9), ("bf16", 128, 2, 9, 1, 300),
+    ("bf16", 64, 1, 9, 3, 700), ("f16", 128, 2, 16, 2, 500), ("bf16", 128, 1, 8, 1, 2000)])
+def test_sparse_decode_past_the_end_of_every_list(pa, dt, d, hkv, g, n, keep):
+    # every run's last tile is its own, and holds NaN and infinities past the run's tokens; so
+    # do the tiles that are named past it
+    r = gen(73, n, keep)
+    nb = 50
+    last = (n * hkv + hkv - 1) // hkv                  # blocks of last tiles, behind the others
+    k, v = (su.pool(r, nb + last + 1, hkv, d, DT[dt]) for _ in range(2))
+    held = torch.randint(0, 16 * keep + 1, (n, hkv), generator=r).int()
+    held[0, 0], held[-1, -1] = 1, 16 * keep - 7
+    tiles = random_tiles(r, n, hkv, keep, nb, held)
+    for i in range(n):
+        for h in range(hkv):
+            used = (int(held[i, h]) + 15) // 16
+            tiles[i, h, used:] = (nb + last) * hkv + h
+            if used:
+                tiles[i, h, used - 1] = nb * hkv + i * hkv + h
+    q = torch.randn(n, hkv * g, d, generator=r).to(DT[dt])
+    ref, tol = su.sparse_decode(q, k, v, tiles, held, SCALE[d])
+    kt, vt = (x.view(-1, 16, d) for x in (k, v))
+    for i in range(n):
+        for h in range(hkv):
+            m = int(held[i, h])
+            at = int(tiles[i, h, (m - 1) // 16]) if m else 0
+            if m % 16:
+                kt[at, m % 16:], vt[at, m % 16:] = ((math.nan, math.inf), (math.inf, math.nan),
+                                                    (-math.inf, math.nan))[(i + h) % 3]
+    k[nb + last], v[nb + last] = math.nan, math.nan
+    out = pa.sparse_decode(torch.full_like(q, math.nan).cuda(), *cuda(q, k, v, tiles, held),
+                           SCALE[d])
+    check(pa)
+    su.close(out, ref, tol)
+
+
 def test_sparse_decode_names_a_tile_twice(pa):
     r = gen(14)
     k, v = (su.pool(r, 4, 1, 64, torch.float16) for _ in range(2))

@@ -582,14 +582,16 @@ int pa_sparse_decode(const struct pa_sparse_args *args);
  *     mass[s][h][t] = decay * mass[s][h][t] + sum_g softmax_t(scale * q_g . k_t)
  * over the heads g of kv head h, for t < seq_lens[s].  The newest token, t =
  * seq_lens[s] - 1, has no weight from before: its old entry is not read, nor is
- * any with decay 0.  Entries past the length are left as they were.  fp32
- * throughout, no atomics.  Keys of live tokens must be finite.
+ * any with decay 0.  Entries past the length are left as they were.  Masses are
+ * fp32 throughout, no atomics.  Keys of live tokens must be finite.
  *   out, q, k_cache, v_cache, block_tables, seq_lens, max_blocks_per_seq, scale,
  *   mass [num_seqs][num_kv_heads][max_blocks_per_seq * 16] fp32, decay (finite);
- *   out may not be q.  The workspace holds the scores: 4 bytes for each query head
- *   (an odd group one more) and position of the tables, of as many sequences as four
- *   gigabytes hold, but one at least: a larger batch is taken in parts, one after the other.
- *   Shapes that the call refuses have size 0.
+ *   out may not be q.  A sequence's masses lie in its row of the batch and are as wide as
+ *   the tables: where a sequence gets another row, or the tables another width, the
+ *   caller copies them over (and a fork's from its parent's row).  The workspace holds the
+ *   scores: 4 bytes for each query head (an odd group one more) and position of the tables,
+ *   of as many sequences as four gigabytes hold, but one at least: a larger batch is taken
+ *   in parts, one after the other.  Shapes that the call refuses have size 0.
  * Errors as pa_decode.
  */
 size_t pa_decode_mass_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,

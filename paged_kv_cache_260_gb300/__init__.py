@@ -808,7 +808,8 @@ def decode_mass(out, mass, q, k_cache, v_cache, block_tables, seq_lens, scale, d
     for t < seq_lens[s]; the newest token starts without any.
 
     mass float32 [num_seqs, num_kv_heads, 16 * block_tables.shape[1]], rows in the order of
-    the tables'.
+    the tables'; when a sequence gets another row or the tables another width, the caller copies
+    its masses over.
     """
     names = _hot()
     n, hq, d = q.shape

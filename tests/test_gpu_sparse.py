@@ -1031,6 +1031,48 @@ def test_a_prompt_is_cut_and_decoded_on(pa):
     check(pa)
 
 
+def test_a_batch_goes_on_after_an_eviction(pa):
+    """The documented lines: sequences longer than new_lens are cut, the shorter one stays, each
+    gets a token and a step counts it; then the batch changes its rows and its tables' width."""
+    r = gen(74)
+    hq, hkv, d, scale = 8, 2, 64, 0.125
+    lens, nb, mb = [300, 40, 0, 100], 60, 20
+    tables = torch.full((4, mb), -1, dtype=torch.int32)
+    order = torch.randperm(nb, generator=r).int()
+    tables[0, :19], tables[1, :3], tables[2, :1], tables[3, :7] = (order[:19], order[19:22],
+                                                                   order[22:23], order[23:30])
+    k, v = (su.pool(r, nb, hkv, d, torch.float16) for _ in range(2))
+    mass = torch.full((4, hkv, 16 * mb), math.nan)
+    kk, vv, mm, tt, ll, new = cuda(k, v, mass, tables, lens, [100] * 4)
+    start = [0, 8, 12, 12, 20]
+    q = torch.randn(20, hq, d, generator=r).half()
+    pa.prefill_mass(mm, q.cuda(), kk, tt, ll, cuda(start)[0], 8, scale, decay=0.0)
+    su.mass_close(mm, *su.prefill_mass(q, mass, k, tables, lens, start, scale, 0.0))
+    before = mm.cpu()
+    pa.evict(kk, vv, mm, tt, ll, new, keep_first=4, keep_last=16)
+    ref = su.evict(k, v, before, tables, lens, [100] * 4, 4, 16)
+    assert all(torch.equal(su.bits(x), su.bits(y)) for x, y in zip((kk, vv, mm), ref))
+    ll = torch.minimum(ll, new)
+    for step in range(3):
+        where = tt.gather(1, (ll // 16).long()[:, None])[:, 0]
+        kn, vn, q = (torch.randn(4, x, d, generator=r).half() for x in (hkv, hkv, hq))
+        pa.reshape_and_cache(kn.cuda(), vn.cuda(), kk, vv, where.long() * 16 + ll % 16)
+        ll += 1
+        before = mm.cpu()
+        out, _ = pa.decode_mass(torch.empty_like(q).cuda(), mm, q.cuda(), kk, vv, tt, ll, scale)
+        ref = su.decode_mass(q, before, kk.cpu(), vv.cpu(), tt.cpu(), ll.tolist(), scale, 1.0)
+        su.close(out, *ref[:2])
+        su.mass_close(mm, *ref[2:])
+        if step == 0:                                  # other rows, wider tables
+            rows = torch.tensor([3, 0, 2, 1]).cuda()
+            wide = torch.full((4, hkv, 16 * (mb + 5)), math.nan, device="cuda")
+            wide[..., :16 * mb] = mm[rows]
+            mm, ll = wide, ll[rows].contiguous()
+            tt = torch.nn.functional.pad(tt[rows], (0, 5), value=-1).contiguous()
+    assert ll.tolist() == [103, 103, 3, 43]
+    check(pa)
+
+
 class Step:
     """The six calls on state of their own, with workspaces of their own."""
 

@@ -31,8 +31,10 @@ __device__ __forceinline__ uint32_t mass_key(float x)
 // One (sequence, kv head) per thread block, or per cluster of blocks that share out its
 // slots and its moves (CLUSTER).  The choice is a chain of passes over the keys in shared
 // memory, a barrier each (two to four digits of a histogram, ties, holes and movers); the moves
-// are bound by HBM where many rows move (128 x 4096 tokens to 2048: 1.1 GB read and written in
-// 140 us).  A batch of 128 that gives back one block, 47 rows a run, 11.5 us: half the choice.
+// are bound by HBM where many rows move (128 x 4096 tokens to 2048: 1.15 GB read and written in
+// 197 us, 5.8 TB/s).  A batch of 128 that gives back one block, 47 rows a run, 55 MB, 17.3 us: half
+// the choice.  (Here and below: K, V and masses renewed before each call and none of them in
+// L2; a second call on the same masses finds most of the heavy tokens moved.)
 template <int D, int NTH, bool CLUSTER>
 __global__ void __launch_bounds__(NTH) evict_kernel_t(const EvictParams p)
 {
@@ -250,12 +252,12 @@ constexpr int kEvictTable = 8192;                 // table entries a block holds
 // 256 threads a block, four of which an SM holds; where the runs leave SMs idle, or a run's
 // masses would take much of an SM's shared memory, a cluster of 2, 4 or 8 blocks shares one.
 // More than three short runs an SM: 128 threads, eight blocks an SM.  us in a graph, bf16, 8 heads x
-// 128, sequences x tokens -> kept.  128 / 256 threads: 128 x 1040 -> 1024 11.5 / 15.3, 128 x 2048
-// -> 2030 15.5 / 18.7, 128 x 2048 -> 1024 72.4 / 68.6, 32 x 1040 -> 1024 8.3 / 7.2.  1 / 2 / 4 / 8
-// blocks: 4 x 4096 -> 2048 23.0 / 18.5 / 15.0 / 16.7, 32 x 2048 -> 2030 8.3 / 12.4 / 21.8 / 42.3,
-// 16 x 8192 -> 8000 18.2 / 17.0 / 15.4 / 27.1, 8 x 32K -> 2048 77.5 / 46.2 / 31.3 / 26.2, 32 x 32K
-// -> 4096 222 / 157 / 150 / 141, 128 x 16K -> 2048 281 / 230 / 240 / 316, 64 x 8192 -> 2048
-// 103 / 106 / 115 / 150 (the bytes' time at HBM's rate 124: part of them stays in L2).
+// 128, sequences x tokens -> kept.  128 / 256 threads: 128 x 1040 -> 1024 17.3 / 22.0, 128 x 2048
+// -> 2030 27.5 / 32.0, 128 x 2048 -> 1024 113 / 107, 32 x 1040 -> 1024 12.7 / 12.5, 4 x 2000 -> 1024
+// 33.8 / 19.7.  1 / 2 / 4 / 8 blocks: 4 x 4096 -> 2048 34.0 / 24.2 / 22.2 / 20.9, 32 x 2048 -> 2030
+// 14.2 / 14.8 / 24.6 / 46.5, 16 x 8192 -> 8000 24.8 / 23.0 / 19.6 / 31.9, 8 x 32K -> 2048 96.2 /
+// 62.4 / 53.0 / 41.7, 32 x 32K -> 4096 297 / 220 / 224 / 210, 128 x 16K -> 2048 421 / 367 / 370 /
+// 413, 64 x 8192 -> 2048 158 / 162 / 170 / 198, 128 x 4096 -> 2048 200 / 209 / 227 / 303.
 EvictLaunch evict_launch(int head_dim, int num_runs, int max_blocks, int num_sms)
 {
     EvictLaunch e{};

@@ -32,8 +32,9 @@ __device__ __forceinline__ float add_mass(float *at, float decay, bool fresh, fl
 // After a decode: every token's weights from the kept scores.  A warp takes 128
 // tokens of a (sequence, kv head), four a lane a stride of 32 apart.  The batch-128
 // decode step, 32/8 heads: 19.2 MB in 8.4 us of the 88.1 that decode and accounting take in
-// a graph (the plain decode 77.7, leaving the scores 2): two or three runs a warp, each a
-// chain of length, statistics and scores.
+// a graph of one batch (the plain decode 77.7, leaving the scores 2; 92.5 and 78.2 where three
+// batches take turns and L2 keeps nothing): two or three runs a warp, each a chain of length,
+// statistics and scores.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kMassFinishThreads, 4)
 decode_mass_finish_kernel(const DecodeMassParams p)
@@ -832,7 +833,7 @@ prefill_mass_kernel(const PrefillMassParams p, const __grid_constant__ CUtensorM
 // its columns.  A lane keeps the maximum and sum of its own keys for each of its columns; a
 // warp's piece of a (sequence, kv head) leaves them in slot (run + warp), which no two pieces
 // share.  HBM bounds it: 4 rows over 8 sequences of 16K tokens, 8 kv heads x 128, 268 MB of keys
-// and 34 MB of scores in 46 us; the sum of the weights takes 10 more.
+// and 17 MB of scores in 46 us, 6.2 TB/s; the sum of the weights takes 11 more.
 // ---------------------------------------------------------------------------
 constexpr int kFewThreads = kMassFewThreads, kFewKeys = 32;
 
@@ -1127,7 +1128,8 @@ prefill_mass_few_finish_kernel(const PrefillMassParams p)
 // split between the warps, which exchange their rows' statistics; the warps' sums for a
 // key meet in shared memory.  What bounds it is one block's chain: lengths, table, rows,
 // then 1.0 us (64 channels) or 1.3 us (128) for every 32 keys of a warp and pass.  Two chunks
-// of 5 and 70 tokens, 8/2 heads x 64: 10.4 us in a graph, 14 by the passes and their sum.
+// of 5 and 70 tokens, 8/2 heads x 64, the long one over 70 keys 10.3 us in a graph (by the passes
+// and their sum 13.4), over 150 keys 17.9 (13.3).
 // ---------------------------------------------------------------------------
 template <typename T, int D>
 __global__ void __launch_bounds__(kMassShortThreads) prefill_mass_short_kernel(const PrefillMassParams p)
@@ -1310,8 +1312,8 @@ __global__ void __launch_bounds__(kMassShortThreads) prefill_mass_short_kernel(c
 // Several row blocks: the sum over a sequence's query tiles of the launch, added to the mass (to
 // what the launches before made of it, from the second on).  Eight warps
 // (with two row blocks, four) share out the query tiles of 128 tokens of a (sequence, kv
-// head), four tokens a lane.  What bounds it is a warp's chain of loads: 14 runs of 1130
-// tokens, 34 row blocks, 9 us (a warp for all of the tiles 25); 64 runs to 5534 tokens, 2 row
+// head), four tokens a lane.  What bounds it is a warp's chain of loads: 14 runs to
+// 1130 tokens, 34 row blocks, 9 us (a warp for all of the tiles 25); 64 runs to 5534 tokens, 2 row
 // blocks, 51 us in all with four warps, 54 with eight.
 __global__ void __launch_bounds__(kMassFinishThreads)
 prefill_mass_finish_kernel(const PrefillMassParams p)

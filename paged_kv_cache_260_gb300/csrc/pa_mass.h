@@ -59,8 +59,9 @@ constexpr int kMassKeys = 128;     // keys of a tile
 // heads of a group) and keys, 32 runs of 128 channels: 4 x 512 10.3 / 11.0, 64 x 128 9.1 / 10.1,
 // 128 x 128 13.4 / 10.1, 64 x 256 13.6 / 10.1, 512 x 128 24.1 / 15.8; 4 runs of 64 channels:
 // 16 x 64 6.1 / 9.1, 4 x 512 8.2 / 9.5, 64 x 128 7.0 / 9.4, 128 x 128 9.9 / 9.2, 256 x 64
-// 7.9 / 10.8, 280 x 128 16.8 / 14.1; chunks of 5 and 70 tokens of four heads with a table of
-// 160 keys: 10.4 / 14.
+// 7.9 / 10.8, 280 x 128 16.8 / 14.1.  The tables' width is all that the host knows of the keys:
+// chunks of 5 and of 70 tokens of four heads in tables of 160 keys, the long one over 70 keys
+// 10.3 / 13.4, over 150 17.9 / 13.3.
 constexpr int kMassShortKeys = 512;
 constexpr long long kMassShortWork = 1 << 20, kMassShortWorkOfBlocks = 3 << 20;
 constexpr int kMassShortThreads = 512;

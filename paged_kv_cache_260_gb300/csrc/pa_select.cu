@@ -176,8 +176,8 @@ __global__ void __launch_bounds__(kBoundsThreads) block_bounds_kernel(const Boun
 // The bounds are read once, 4 head_dim bytes a block and kv head.  With many runs HBM
 // bounds the scores and a block's choice comes after its own: 1024 runs to 16K tokens, 278 MB,
 // 70 us cold (60 % of the copy rate).  With few runs the scores of 4 x 32K to 131K tokens, 84
-// MB, take 16 us and the choice of 256 of 8192 blocks 9 more: a chain of passes over the scores
-// in shared memory, a barrier each.
+// MB, take 16 us from L2 and 20 from HBM, and the choice of 256 of 8192 blocks 9 more: a chain
+// of passes over the scores in shared memory, a barrier each.
 // ---------------------------------------------------------------------------
 constexpr int kDoubt = 256;                       // blocks in doubt that are ranked directly
 constexpr int kSelectNear = 16384;                // scores a block holds (64 KB)

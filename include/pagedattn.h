@@ -616,8 +616,9 @@ int pa_decode_mass(const struct pa_sparse_args *args);
  * Bad table entries read block 0.  A workspace of a longer max_query_len serves shorter
  * ones too (its own, where chunks have few rows, lets the keys be read only once).  It holds
  * 8 bytes for each 2 * (128 / group) tokens of a chunk and place of the tables of a kv head, of
- * as many of those as a gigabyte holds, but one at least: a longer chunk is taken in parts, one
- * after the other.  Shapes that the call refuses have size 0.
+ * as many of those as a gigabyte holds, but one at least: a longer max_query_len (as far as
+ * the tables reach) is taken in parts, one after the other, whether chunks have rows there or
+ * not.  Shapes that the call refuses have size 0.
  */
 size_t pa_prefill_mass_workspace_size(int num_seqs, int max_query_len, int num_heads,
                                       int num_kv_heads, int max_blocks_per_seq);

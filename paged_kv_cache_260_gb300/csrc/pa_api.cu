@@ -1738,8 +1738,10 @@ int pa_decode_mass(const struct pa_sparse_args *args)
 // as many as kMassKept holds, so that a longer chunk takes passes of its own for every
 // `most` of them.
 // Chunks of few rows keep their scores instead, with the statistics of the warps' pieces.
+// (A chunk fits its table, so max_query_len may be any bound: the row blocks that tables have
+// room for are `reach`.)
 struct PrefillMassPlan {
-    long long row_blocks, most;
+    long long row_blocks, reach, most;
     size_t sums_off, total;
     int few_cols, few_warps;       // the form for few rows, or 0
     size_t few_off, few_total;
@@ -1758,7 +1760,8 @@ static bool prefill_mass_plan(int num_seqs, int max_query_len, int num_heads, in
     if (runs >= (1LL << 31) || runs * max_blocks >= (1LL << 31))    // (as sparse_tables)
         return false;
     const long long keys = runs * max_blocks * kBlockSize;
-    w->most = std::max(1LL, std::min(w->row_blocks, kMassKept / (kMassTiles * keys)));
+    w->reach = std::min(w->row_blocks, ((long long)max_blocks * kBlockSize + tokens - 1) / tokens);
+    w->most = std::max(1LL, std::min(w->reach, kMassKept / (kMassTiles * keys)));
     if (rows <= kMassFewRows && num_seqs <= kRaggedSeqs &&
         keys * score_cols((int)rows) <= kMassKept) {
         w->few_cols = score_cols((int)rows);
@@ -1814,8 +1817,8 @@ int pa_prefill_mass(const struct pa_sparse_args *args)
                            a.max_blocks_per_seq, ds->num_sms, &w))
         return PA_ERR_INVALID_ARG;
     // equal shares of the row blocks
-    const long long parts = (w.row_blocks + w.most - 1) / w.most;
-    const long long share = (w.row_blocks + parts - 1) / parts;
+    const long long parts = (w.reach + w.most - 1) / w.most;
+    const long long share = (w.reach + parts - 1) / parts;
     auto tiles_of = [&](long long row_blocks) {
         return (long long)a.num_seqs * a.num_kv_heads * row_blocks *
                (((long long)a.max_blocks_per_seq * kBlockSize + kMassKeys - 1) / kMassKeys);
@@ -1886,9 +1889,9 @@ int pa_prefill_mass(const struct pa_sparse_args *args)
         return rc;
     void *kargs[] = {&p, &tmk};
     const long long units = (long long)a.num_seqs * a.num_kv_heads * ((a.max_blocks_per_seq + 7) / 8);
-    for (long long first = 0; first < w.row_blocks && rc == PA_OK; first += share) {
+    for (long long first = 0; first < w.reach && rc == PA_OK; first += share) {
         p.block0 = (int)first;
-        p.row_blocks = (int)std::min(share, w.row_blocks - first);
+        p.row_blocks = (int)std::min(share, w.reach - first);
         // A key tile a block while the second pass's blocks find SMs of their own beside the
         // first's, two of a unit's where they would not: 32 units of four tiles 13.1 us by one
         // each, 11.0 by two, units of one tile 9.8 and 15.0.

@@ -861,6 +861,17 @@ def test_prefill_mass_in_parts(pa, lens, chunks, g, d, hkv, parts, decay):
     chunk_case(pa, gen(70, g, d), lens, chunks, "bf16", d, hkv, g, decay, mb=mb)
 
 
+@pytest.mark.parametrize("g,d", [(4, 64), (16, 128)])
+def test_prefill_mass_with_a_far_bound_on_chunks(pa, g, d):
+    # no chunk is longer than the tables: a bound above that asks for nothing more
+    lens, chunks = [300, 960, 40, 0], [70, 500, 40, 0]
+    size = pa.prefill_mass_workspace_size
+    for hkv in (1, 3):
+        full = size(4, 960, hkv * g, hkv, 60)
+        assert 0 < full == size(4, 2000, hkv * g, hkv, 60) == size(4, 2 ** 31 - 1, hkv * g, hkv, 60)
+    chunk_case(pa, gen(75, g), lens, chunks, "f16", d, 2, g, 0.9, mb=60, longest=10 ** 6)
+
+
 def test_prefill_mass_workspaces_are_bounded(pa):
     size = pa.prefill_mass_workspace_size
     # a whole prompt of 131072 tokens, and 8 chunks of 8192 in tables for 32768
